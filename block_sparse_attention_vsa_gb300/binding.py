@@ -7,13 +7,16 @@ GPU the calls raise.
 
 Functions mirror the C entry points:
   vsa_fwd, vsa_fwd_gqa, vsa_fwd_split, vsa_fwd_from_mask, jenga_fwd, vsa_bwd, vsa_lut_to_bitmap,
-  vsa_bitmap_to_lut, vsa_fwd_from_host, vsa_device_status, vsa_workspace_bytes
+  vsa_bitmap_to_lut, vsa_fwd_from_host, vsa_device_status, vsa_workspace_bytes,
+  vsa_block_mean, vsa_select_blocks, and over an 8-bit cache (Cache8): vsa_cache_select,
+  vsa_cache_write, vsa_fwd_cache, vsa_cache_evict
 """
 from __future__ import annotations
 
 import ctypes
 import math
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -30,7 +33,9 @@ EXPORTS = ("vsa_fwd", "jenga_fwd", "vsa_workspace_bytes", "vsa_lut_to_bitmap",
            "vsa_bitmap_to_lut", "vsa_fwd_from_host", "vsa_device_status",
            "vsa_last_launch_count", "vsa_status_str", "vsa_fwd_noalloc", "vsa_fwd_gqa",
            "vsa_fwd_from_mask", "vsa_fwd_split", "vsa_split_workspace_bytes", "vsa_bwd",
-           "vsa_bwd_workspace_bytes", "vsa_set_wait_limit_ns", "vsa_set_stall_test")
+           "vsa_bwd_workspace_bytes", "vsa_set_wait_limit_ns", "vsa_set_stall_test",
+           "vsa_block_mean", "vsa_select_blocks", "vsa_cache_select", "vsa_cache_write",
+           "vsa_fwd_cache", "vsa_cache_workspace_bytes", "vsa_cache_evict")
 MAX_SPLITS = 64
 
 
@@ -96,6 +101,20 @@ def load(path: str = LIB_PATH):
     h.vsa_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]
     h.vsa_set_stall_test.restype = None
     h.vsa_set_stall_test.argtypes = [i32]
+    h.vsa_block_mean.restype = i32
+    h.vsa_block_mean.argtypes = [P, P, i32, i32, i32, i32, i32, P, P]
+    h.vsa_select_blocks.restype = i32
+    h.vsa_select_blocks.argtypes = [P, P, P] + [i32] * 10 + [P, P, P]
+    h.vsa_cache_select.restype = i32
+    h.vsa_cache_select.argtypes = [P, P, P, P] + [i32] * 10 + [P, P, P]
+    h.vsa_cache_write.restype = i32
+    h.vsa_cache_write.argtypes = [P] * 5 + [i32] * 7 + [P] * 6
+    h.vsa_cache_workspace_bytes.restype = sz
+    h.vsa_cache_workspace_bytes.argtypes = [i32] * 5
+    h.vsa_fwd_cache.restype = i32
+    h.vsa_fwd_cache.argtypes = [P] * 9 + [i32] * 8 + [f32, f32, P, P, P, P, sz, P]
+    h.vsa_cache_evict.restype = i32
+    h.vsa_cache_evict.argtypes = [P, P, P] + [i32] * 6 + [P] * 6
     _lib = h
     return h
 
@@ -455,3 +474,235 @@ def vsa_set_stall_test(enable: bool) -> None:
     """Timeout-path test hook: while on, every launch's MMA warp waits on a barrier nothing
     completes, so the launch reports VSA_ERR_DEVICE_TIMEOUT."""
     load().vsa_set_stall_test(1 if enable else 0)
+
+
+# --------------------------------------------------------- choosing blocks, the 8-bit cache
+def _same_device(first, **others):
+    """The device the call runs on: every tensor's, whichever device is current."""
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+    return torch.cuda.device(first.device)
+
+
+def _call(fn, device, *args, stream=None):
+    with device:
+        _check(fn, getattr(load(), fn)(*args, _stream(stream)))
+
+
+def _i32(t, name, shape):
+    _dev(t, name, torch.int32)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def vsa_block_mean(x, sizes=None, block=64, out=None, stream=None):
+    """Block means: x bf16 [B,H,S,128] -> bf16 [B,H,ceil(S/block),128], each the mean of the
+    first sizes[j] tokens of block j (sizes int32 [nb]; None = all there are)."""
+    _dev(x, "x", torch.bfloat16, 4)
+    B, H, S, D = x.shape
+    nb = -(-S // block) if block else 0
+    if sizes is not None:
+        _i32(sizes, "sizes", (nb,))
+    if out is None:
+        out = torch.empty((B, H, nb, D), dtype=torch.bfloat16, device=x.device)
+    elif _dev(out, "out", torch.bfloat16).shape != (B, H, nb, D):
+        raise ValueError("out must be [B,H,ceil(S/block),128]")
+    _call("vsa_block_mean", _same_device(x, sizes=sizes, out=out), _ptr(x), _ptr(sizes), B, H, S,
+          D, block, _ptr(out), stream=stream)
+    return out
+
+
+def vsa_select_blocks(q_mean, k_mean, topk, sizes=None, causal=False, n_first=0, n_near=0,
+                      stream=None):
+    """The LUT of the topk key blocks of highest q_mean . k_mean per query block: q_mean bf16
+    [B,Hq,nq,128], k_mean bf16 [B,Hkv,nk,128] -> (q2k_idx int32 [B,Hq,nq,topk] ascending,
+    -1 behind; q2k_num int32 [B,Hq,nq]).  sizes int32 [nk]: blocks of size 0 are not chosen;
+    causal: no block past the diagonal i + nk - nq; the first n_first blocks and those
+    nearer than n_near to the diagonal are always chosen."""
+    _dev(q_mean, "q_mean", torch.bfloat16, 4)
+    _dev(k_mean, "k_mean", torch.bfloat16, 4)
+    B, Hq, nq, D = q_mean.shape
+    Bk, Hkv, nk, Dk = k_mean.shape
+    if Bk != B or Dk != D:
+        raise ValueError("k_mean must be [B,Hkv,nk,D] with q_mean's B and D")
+    if sizes is not None:
+        _i32(sizes, "sizes", (nk,))
+    idx = torch.empty((B, Hq, nq, max(0, topk)), dtype=torch.int32, device=q_mean.device)
+    num = torch.empty((B, Hq, nq), dtype=torch.int32, device=q_mean.device)
+    _call("vsa_select_blocks", _same_device(q_mean, k_mean=k_mean, sizes=sizes), _ptr(q_mean),
+          _ptr(k_mean), _ptr(sizes), B, Hq, Hkv, nq, nk, D, topk, int(bool(causal)), n_first,
+          n_near, _ptr(idx), _ptr(num), stream=stream)
+    return idx, num
+
+
+class Cache8(NamedTuple):
+    """A pool of pages of the 8-bit key/value cache.  Page p holds `block` tokens of one
+    sequence and key/value head: value = code * scale, k_mean the mean of its keys."""
+    k: torch.Tensor        # float8_e4m3fn [pages, block, 128]
+    v: torch.Tensor        # float8_e4m3fn [pages, block, 128]
+    k_scale: torch.Tensor  # float32 [pages]
+    v_scale: torch.Tensor  # float32 [pages]
+    k_mean: Optional[torch.Tensor] = None  # bfloat16 [pages, 128]; needed to choose blocks
+
+
+def new_cache8(pages, block=64, device=None) -> Cache8:
+    """An empty pool."""
+    device = device or "cuda"
+    code = torch.zeros((2, pages, block, HEAD_DIM), dtype=torch.uint8, device=device)
+    code = code.view(torch.float8_e4m3fn)
+    scale = torch.zeros((2, pages), dtype=torch.float32, device=device)
+    mean = torch.zeros((pages, HEAD_DIM), dtype=torch.bfloat16, device=device)
+    return Cache8(code[0], code[1], scale[0], scale[1], mean)
+
+
+def _cache(cache, table, lens, B):
+    """(pages, block, Hkv, max_blocks) of a checked cache, table and lens."""
+    _dev(cache.k, "cache.k", torch.float8_e4m3fn, 3)
+    pages, block, D = cache.k.shape
+    if _dev(cache.v, "cache.v", torch.float8_e4m3fn).shape != cache.k.shape or D != HEAD_DIM:
+        raise ValueError("cache.k and cache.v must both be [pages,block,128]")
+    for name, t in (("k_scale", cache.k_scale), ("v_scale", cache.v_scale)):
+        if _dev(t, "cache." + name, torch.float32).shape != (pages,):
+            raise ValueError(f"cache.{name} must be [pages]")
+    if cache.k_mean is not None:
+        if _dev(cache.k_mean, "cache.k_mean", torch.bfloat16).shape != (pages, D):
+            raise ValueError("cache.k_mean must be [pages,128]")
+    _dev(table, "table", torch.int32, 3)
+    if table.shape[0] != B:
+        raise ValueError("table must be [B,Hkv,max_blocks]")
+    _i32(lens, "lens", (B,))
+    return pages, block, table.shape[1], table.shape[2]
+
+
+def _one_token(q):
+    _dev(q, "q", torch.bfloat16, 4)
+    if q.shape[2] != 1:
+        raise ValueError("q must be [B,Hq,1,128]: one token per sequence")
+    return q.shape[0], q.shape[1], q.shape[3]
+
+
+def vsa_cache_select(q, k_mean, table, lens, topk, block=64, n_first=0, n_near=1, stream=None):
+    """vsa_select_blocks for one token per sequence over a cache: q bf16 [B,Hq,1,128], k_mean
+    bf16 [pages,128] (Cache8.k_mean), table int32 [B,Hkv,max_blocks], lens int32 [B] ->
+    (idx int32 [B,Hkv,topk], num int32 [B,Hkv]), shared by the heads of a group (a block's
+    score is the largest of its heads')."""
+    B, Hq, D = _one_token(q)
+    _dev(k_mean, "k_mean", torch.bfloat16, 2)
+    _dev(table, "table", torch.int32, 3)
+    if table.shape[0] != B or k_mean.shape[1] != D:
+        raise ValueError("table must be [B,Hkv,max_blocks] and k_mean [pages,128]")
+    _i32(lens, "lens", (B,))
+    Hkv, max_blocks = table.shape[1:]
+    idx = torch.empty((B, Hkv, max(0, topk)), dtype=torch.int32, device=q.device)
+    num = torch.empty((B, Hkv), dtype=torch.int32, device=q.device)
+    _call("vsa_cache_select", _same_device(q, k_mean=k_mean, table=table, lens=lens), _ptr(q),
+          _ptr(k_mean), _ptr(table), _ptr(lens), B, Hq, Hkv, D, k_mean.shape[0], max_blocks,
+          block, topk, n_first, n_near, _ptr(idx), _ptr(num), stream=stream)
+    return idx, num
+
+
+def vsa_cache_write(cache, k, v, table, lens, n_new=None, stream=None):
+    """Tokens lens[b] .. of every sequence into its pages: k, v bf16 [B,Hkv,T,128], of which
+    sequence b writes the first n_new[b] (int32 [B]; None = T).  lens counts the tokens held
+    before; add n_new to it afterwards."""
+    _dev(k, "k", torch.bfloat16, 4)
+    _dev(v, "v", torch.bfloat16, 4)
+    B, Hkv, T, D = k.shape
+    pages, block, Ht, max_blocks = _cache(cache, table, lens, B)
+    if v.shape != k.shape or Ht != Hkv:
+        raise ValueError("k and v must be [B,Hkv,T,128] and table [B,Hkv,max_blocks]")
+    if n_new is not None:
+        _i32(n_new, "n_new", (B,))
+    _call("vsa_cache_write",
+          _same_device(k, v=v, table=table, lens=lens, n_new=n_new, cache_k=cache.k,
+                       cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale,
+                       k_mean=cache.k_mean),
+          _ptr(k), _ptr(v), _ptr(table), _ptr(lens), _ptr(n_new), B, Hkv, T, D, pages,
+          max_blocks, block, _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale),
+          _ptr(cache.v_scale), _ptr(cache.k_mean), stream=stream)
+
+
+def cache_workspace_bytes(B, Hq, Hkv, max_blocks, weights=False) -> int:
+    return int(load().vsa_cache_workspace_bytes(B, Hq, Hkv, max_blocks, int(bool(weights))))
+
+
+def new_cache_workspace(B, Hq, Hkv, max_blocks, weights=False, device=None) -> torch.Tensor:
+    """Workspace for vsa_fwd_cache (weights: with a weight tensor); each call leaves its
+    counters zero again."""
+    n = cache_workspace_bytes(B, Hq, Hkv, max_blocks, weights)
+    if n == 0:
+        raise ValueError("invalid cache shape")
+    return torch.zeros((n + 15) // 16 * 4, dtype=torch.int32, device=device or "cuda")
+
+
+def vsa_fwd_cache(q, cache, table, lens, idx=None, num=None, scale=None, out=None, lse=True,
+                  weight=None, keep=1.0, workspace=None, stream=None):
+    """Attention of one token per sequence over its 8-bit cache: q bf16 [B,Hq,1,128], table
+    int32 [B,Hkv,max_blocks], lens int32 [B]; over the blocks listed per key/value head (idx
+    int32 [B,Hkv,max_sel], num int32 [B,Hkv]) or all.  Returns (out, lse or None).  weight
+    (float32 [B,Hkv,max_blocks]) becomes keep * weight + the step's weight of each block.
+    The workspace is allocated if not given."""
+    B, Hq, D = _one_token(q)
+    pages, block, Hkv, max_blocks = _cache(cache, table, lens, B)
+    if (idx is None) != (num is None):
+        raise ValueError("idx and num go together")
+    max_sel = 0
+    if idx is not None:
+        _dev(idx, "idx", torch.int32, 3)
+        if idx.shape[:2] != (B, Hkv):
+            raise ValueError("idx must be [B,Hkv,max_sel]")
+        _i32(num, "num", (B, Hkv))
+        max_sel = idx.shape[2]
+    if weight is not None and _dev(weight, "weight", torch.float32).shape != table.shape:
+        raise ValueError("weight must be [B,Hkv,max_blocks]")
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    if out is None:
+        out = torch.empty_like(q)
+    elif _dev(out, "out", torch.bfloat16).shape != q.shape:
+        raise ValueError("out must have q's shape")
+    lse_t = _lse_arg(lse, (B, Hq, 1), q.device)
+    if lse_t is not None and lse_t.shape != (B, Hq, 1):
+        raise ValueError("lse must be [B,Hq,1]")
+    if workspace is None:
+        if Hkv < 1 or Hq < 1 or Hq % Hkv:
+            raise ValueError("Hq must be a multiple of table's Hkv")
+        workspace = new_cache_workspace(B, Hq, Hkv, max_blocks, weight is not None, q.device)
+    _call("vsa_fwd_cache",
+          _same_device(q, cache_k=cache.k, cache_v=cache.v, k_scale=cache.k_scale,
+                       v_scale=cache.v_scale, table=table, lens=lens, idx=idx, num=num, out=out,
+                       lse=lse_t, weight=weight, workspace=workspace),
+          _ptr(q), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale),
+          _ptr(table), _ptr(lens), _ptr(idx), _ptr(num), max_sel, B, Hq, Hkv, D, pages,
+          max_blocks, block, scale, float(keep), _ptr(out), _ptr(lse_t), _ptr(weight),
+          _ptr(workspace), workspace.numel() * workspace.element_size(), stream=stream)
+    return out, lse_t
+
+
+class Evicted(NamedTuple):
+    """What vsa_cache_evict leaves: the table, weights and lengths to go on with, and the
+    pages let go (freed[b, h, :n_freed[b]])."""
+    table: torch.Tensor
+    weight: torch.Tensor
+    lens: torch.Tensor
+    freed: torch.Tensor
+    n_freed: torch.Tensor
+
+
+def vsa_cache_evict(weight, table, lens, budget, block=64, n_first=0, n_last=1,
+                    stream=None) -> Evicted:
+    """Cut every sequence to at most `budget` blocks per key/value head: the first n_first
+    and last n_last stay, and of the rest those of the highest weight (float32
+    [B,Hkv,max_blocks], as vsa_fwd_cache accumulates it)."""
+    _dev(weight, "weight", torch.float32, 3)
+    B, Hkv, max_blocks = weight.shape
+    _i32(table, "table", weight.shape)
+    _i32(lens, "lens", (B,))
+    r = Evicted(torch.empty_like(table), torch.empty_like(weight), torch.empty_like(lens),
+                torch.empty_like(table), torch.empty_like(lens))
+    _call("vsa_cache_evict", _same_device(weight, table=table, lens=lens), _ptr(weight),
+          _ptr(table), _ptr(lens), B, Hkv, max_blocks, block, budget, n_first, n_last,
+          _ptr(r.table), _ptr(r.weight), _ptr(r.lens), _ptr(r.freed), _ptr(r.n_freed),
+          stream=stream)
+    return r

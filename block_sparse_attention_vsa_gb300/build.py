@@ -2,7 +2,8 @@
 
     python -m block_sparse_attention_vsa_gb300.build [--force]
 
-One translation unit, one -gencode (sm_103a), static CUDA runtime, no cmake.
+Two translation units compiled side by side, one -gencode (sm_103a), static CUDA runtime,
+no cmake.
 """
 from __future__ import annotations
 
@@ -15,14 +16,15 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libvsa_gb300.so")
-SOURCES = [os.path.join(CSRC, "vsa_api.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("vsa_fwd_kernel.cuh", "vsa_bwd_kernel.cuh",
-                                                "sm103_ptx.cuh")] + [
+SOURCES = [os.path.join(CSRC, f) for f in ("vsa_api.cu", "vsa_serve_api.cu")]
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in (
+    "vsa_fwd_kernel.cuh", "vsa_bwd_kernel.cuh", "vsa_select_kernel.cuh", "vsa_cache_kernel.cuh",
+    "sm103_ptx.cuh", "vsa_warp_ptx.cuh", "vsa_host.h")] + [
     os.path.join(ROOT, "include", "vsa.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-shared", "-Xcompiler", "-fPIC",
-         "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr"]
+         "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr", "--threads", "2"]
 
 
 def nvcc() -> str:

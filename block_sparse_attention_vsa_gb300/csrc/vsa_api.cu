@@ -14,6 +14,7 @@
 #include <mutex>
 
 #include "../../include/vsa.h"
+#include "vsa_host.h"
 #include "vsa_fwd_kernel.cuh"
 #include "vsa_bwd_kernel.cuh"
 
@@ -452,6 +453,22 @@ vsa_status host_pipe(HostPipe** out) {
 }
 
 }  // namespace
+
+namespace vsa {
+
+vsa_status host_device(int* ordinal, int* sm_count) {
+  DeviceInfo* d = nullptr;
+  const vsa_status st = device_info(&d);
+  if (st != VSA_OK) return st;
+  if (d->major != 10 || d->minor != 3) return VSA_ERR_UNSUPPORTED;
+  *ordinal = (int)(d - g_dev);
+  *sm_count = d->sm_count;
+  return VSA_OK;
+}
+
+void host_set_launches(int n) { t_last_launches = n; }
+
+}  // namespace vsa
 
 extern "C" {
 

@@ -297,6 +297,140 @@ VSA_API vsa_status vsa_fwd_from_host(const vsa_bf16 *h_q, const vsa_bf16 *h_k, c
                              int32_t *d_variable_block_sizes, vsa_bf16 *d_out, float *d_lse,
                              void *workspace, vsa_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Choosing the blocks, and serving single tokens from an 8-bit cache.
+ *
+ * vsa_block_mean and vsa_select_blocks make the (q2k_idx, q2k_num) that vsa_fwd,
+ * vsa_fwd_gqa, vsa_fwd_split and vsa_bwd take: one mean per block of q and of k, and for
+ * every query block the key blocks of the highest q_mean . k_mean.  (The choice has no
+ * gradient; that of the attention over the chosen blocks is vsa_bwd's.)
+ *
+ * The 8-bit cache holds a server's keys and values.  Its pool has `pages` pages; a page
+ * holds `block` (64 or 128) consecutive tokens of one sequence and key/value head:
+ *   k_cache, v_cache  [pages, block, D] e4m3 codes (uint8), 16-byte aligned
+ *   k_scale, v_scale  [pages] fp32: value = code * scale
+ *   k_mean            [pages, D] bf16: the mean of the page's keys as the cache holds them
+ * table[b, h, j] (int32 [B, Hkv, max_blocks]) is the page of tokens j*block .. of sequence
+ * b and key/value head h, lens[b] (int32 [B]) the tokens that sequence b holds, at most
+ * max_blocks * block.  A table entry outside [0, pages) names no page: nothing is written
+ * there, and its tokens are not attended or chosen.  Entries past a sequence's last block
+ * are not read.  A cache whose pages hold all heads together, [n, Hkv, block, D], is this
+ * one with pages = n * Hkv and table entries page * Hkv + h.
+ * A step of a server: vsa_cache_write the new tokens, add their number to lens,
+ * vsa_cache_select (or none: all blocks), vsa_fwd_cache, and now and then
+ * vsa_cache_evict.  max_blocks <= VSA_MAX_BLOCKS.
+ * ------------------------------------------------------------------------------------- */
+
+/* Block means: mean[b, h, j] = the mean of the first n_j tokens of block j of x, in fp32,
+ * rounded to bf16 once; 0 where n_j = 0.
+ *   x      [B, H, S, D] bf16, 16-byte aligned; S need not be a multiple of block.
+ *   sizes  [nb] int32, nb = ceil(S / block): n_j = sizes[j] clamped to [0, block] and to
+ *          the tokens there are; NULL = all of them.  Tokens past n_j are not read.
+ *   mean   [B, H, nb, D] bf16 output; must not overlap x or sizes. */
+VSA_API vsa_status vsa_block_mean(const vsa_bf16 *x, const int32_t *sizes, int B, int H, int S,
+                                  int D, int block, vsa_bf16 *mean, vsa_stream_t stream);
+
+/* The key blocks each query block attends.  For query head hq (key/value head
+ * hq / (Hq / Hkv)) and query block i, with d = i + nk - nq the key block on its diagonal:
+ * of the eligible blocks j, the min(topk, their number) of the highest
+ * q_mean[b, hq, i] . k_mean[b, hkv, j], ascending in q2k_idx with -1 behind, and their
+ * number in q2k_num.
+ *   eligible   sizes[j] > 0 (sizes [nk] int32, or NULL), with causal != 0 j <= d, and the
+ *              score is not NaN
+ *   forced     blocks j < n_first or |j - d| < n_near that are eligible but for the score
+ *              come before all others whatever their score (a NaN too)
+ * Scores are compared as real numbers -- where fp32 sums leave the order open they are
+ * computed again in fp64 -- and equal ones go to the lower index, so the choice does not
+ * depend on the order of a sum.  A row with nothing eligible gets a count of 0.
+ *   q_mean [B, Hq, nq, D], k_mean [B, Hkv, nk, D] bf16, 16-byte aligned; nk <=
+ *   VSA_MAX_BLOCKS; q2k_idx [B, Hq, nq, topk], q2k_num [B, Hq, nq] int32 outputs, which
+ *   must not overlap anything else.  topk >= 1 (it may exceed nk).
+ * Rows with more than 32 blocks inside the fp32 error band (blocks with equal means, say)
+ * take a slower exact path. */
+VSA_API vsa_status vsa_select_blocks(const vsa_bf16 *q_mean, const vsa_bf16 *k_mean,
+                                     const int32_t *sizes, int B, int Hq, int Hkv, int nq, int nk,
+                                     int D, int topk, int causal, int n_first, int n_near,
+                                     int32_t *q2k_idx, int32_t *q2k_num, vsa_stream_t stream);
+
+/* vsa_select_blocks for one token per sequence over the cache: for each sequence and
+ * key/value head, the blocks of the highest score, a block's score being the largest of
+ * q[b, hq] . k_mean[page] over the query heads of the group.  The diagonal is the
+ * sequence's last block (n_near = 1 forces it), n_first forces the first ones; ties,
+ * forced blocks and NaN as in vsa_select_blocks.
+ *   q [B, Hq, 1, D] bf16; idx [B, Hkv, topk], num [B, Hkv] int32 outputs, the listing that
+ *   vsa_fwd_cache takes. */
+VSA_API vsa_status vsa_cache_select(const vsa_bf16 *q, const vsa_bf16 *k_mean,
+                                    const int32_t *table, const int32_t *lens, int B, int Hq,
+                                    int Hkv, int D, int pages, int max_blocks, int block,
+                                    int topk, int n_first, int n_near, int32_t *idx, int32_t *num,
+                                    vsa_stream_t stream);
+
+/* Tokens lens[b] .. lens[b] + n_new[b] - 1 of every sequence into the cache.
+ *   k, v   [B, Hkv, T, D] bf16: row t is token lens[b] + t; rows from n_new[b] on (a padded
+ *          batch) are not read.  n_new int32 [B], clamped to [0, T], or NULL = T each.
+ *   lens   the tokens held before the call; it is not changed (add n_new to it after).
+ * A page's scale is the least power of two s >= 2^-100 with max |x| <= 448 s over its
+ * finite values so far, and a code the nearest e4m3 value of x / s (ties to even;
+ * infinities become +-448 s, NaN stays NaN).  When a new token raises a page's scale, the
+ * codes it holds move to the new one: exactly, but for what falls below the smallest
+ * subnormal.  Token by token or at once, a page ends the same up to that.  k_mean (or NULL)
+ * gets the mean of the page's keys as now held.  Page bytes of tokens not yet held stay as
+ * they are, tokens past max_blocks * block are dropped, and what a page held before its
+ * first token is ignored.  No two written pages may be the same.  Scales that were not
+ * made here must be powers of two. */
+VSA_API vsa_status vsa_cache_write(const vsa_bf16 *k, const vsa_bf16 *v, const int32_t *table,
+                                   const int32_t *lens, const int32_t *n_new, int B, int Hkv,
+                                   int T, int D, int pages, int max_blocks, int block,
+                                   uint8_t *k_cache, uint8_t *v_cache, float *k_scale,
+                                   float *v_scale, vsa_bf16 *k_mean, vsa_stream_t stream);
+
+/* Attention of one token per sequence over its cache (lens counts the token itself if it
+ * has been written): out and lse as vsa_fwd's, over the tokens of the listed blocks.
+ *   q, out  [B, Hq, 1, D] bf16; lse [B, Hq, 1] fp32 (base 2) or NULL.
+ *   idx     [B, Hkv, max_sel] int32, num [B, Hkv]: the blocks the whole group of a
+ *           key/value head attends (counts clamped to [0, max_sel], entries outside the
+ *           sequence skipped, a block named twice attended once), or both NULL: every
+ *           block.  k_scale, v_scale may be any finite numbers.
+ *   weight  [B, Hkv, max_blocks] fp32 or NULL: becomes keep * weight + w, w the sum of the
+ *           attention weights that the group's heads give the block's tokens (0 for a
+ *           block not attended).  keep = 1 accumulates, 0 records this step alone (what
+ *           was there is not read), between them the past fades.
+ *   workspace  at least vsa_cache_workspace_bytes(B, Hq, Hkv, max_blocks, weight != NULL)
+ *           bytes, 16-byte aligned, whose first 256 KB are zero before the first call;
+ *           each call leaves them zero.  It may serve calls of other shapes in turn, but
+ *           calls sharing it must not overlap on the GPU (give graphs that may run at the
+ *           same time one each).
+ * A sequence that attends nothing gets out = +0 and lse = VSA_LSE_EMPTY.  Results do not
+ * depend on timing: splits of a row are joined in their order.  One kernel.
+ * B * Hkv * (ceil(Hq / Hkv / 8) + 1) <= 65536. */
+VSA_API vsa_status vsa_fwd_cache(const vsa_bf16 *q, const uint8_t *k_cache,
+                                 const uint8_t *v_cache, const float *k_scale,
+                                 const float *v_scale, const int32_t *table, const int32_t *lens,
+                                 const int32_t *idx, const int32_t *num, int max_sel, int B,
+                                 int Hq, int Hkv, int D, int pages, int max_blocks, int block,
+                                 float scale, float keep, vsa_bf16 *out, float *lse,
+                                 float *weight, void *workspace, size_t workspace_bytes,
+                                 vsa_stream_t stream);
+
+/* Workspace bytes vsa_fwd_cache needs for this shape (0 for an invalid one). */
+VSA_API size_t vsa_cache_workspace_bytes(int B, int Hq, int Hkv, int max_blocks, int weight);
+
+/* Eviction: every sequence with n = ceil(len / block) > budget blocks is cut to budget, in
+ * each key/value head on its own: its first n_first and last n_last blocks stay, and of the
+ * others those of the highest weight (equal ones: the lower index; NaN counts as the
+ * lowest).  n_last >= 1 (the last block may be part full), n_first + n_last <= budget.
+ *   table_out, weight_out  [B, Hkv, max_blocks]: the entries that stay, in their order,
+ *           then -1 and 0.
+ *   lens_out, n_freed      [B]: the tokens still held, and the pages that went, per head.
+ *   freed   [B, Hkv, max_blocks]: the pages that went, -1 behind.
+ * The outputs overlap nothing: a server keeps two tables and swaps them.  Codes do not
+ * move. */
+VSA_API vsa_status vsa_cache_evict(const float *weight, const int32_t *table,
+                                   const int32_t *lens, int B, int Hkv, int max_blocks, int block,
+                                   int budget, int n_first, int n_last, int32_t *table_out,
+                                   float *weight_out, int32_t *lens_out, int32_t *freed,
+                                   int32_t *n_freed, vsa_stream_t stream);
+
 /* Synchronises `stream`, then reads and clears the device status word of the current
  * device: VSA_OK, or VSA_ERR_DEVICE_TIMEOUT if a kernel gave up on a wait since the
  * last call (`detail`, if not NULL, receives the recorded code). */
