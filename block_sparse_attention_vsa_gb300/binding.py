@@ -477,40 +477,61 @@ def vsa_set_stall_test(enable: bool) -> None:
 
 
 # --------------------------------------------------------- choosing blocks, the 8-bit cache
-def _same_device(first, **others):
-    """The device the call runs on: every tensor's, whichever device is current."""
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
-    return torch.cuda.device(first.device)
-
-
-def _call(fn, device, *args, stream=None):
-    with device:
-        _check(fn, getattr(load(), fn)(*args, _stream(stream)))
-
-
-def _i32(t, name, shape):
-    _dev(t, name, torch.int32)
+# These calls run for microseconds, so what is checked here is checked in one expression per
+# tensor; _explain says afterwards what was wrong.
+def _explain(name, t, dtype, shape, dev):
+    _dev(t, name, dtype, len(shape))
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t
+    raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+
+
+def _need(name, t, dtype, shape, dev):
+    """The address of a contiguous tensor of this type, shape and device."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _explain(name, t, dtype, shape, dev)
+
+
+def _maybe(name, t, dtype, shape, dev):
+    return None if t is None else _need(name, t, dtype, shape, dev)
+
+
+def _lead(name, t, dtype, ndim):
+    """(shape, device ordinal) of the tensor that the others of a call go by."""
+    _dev(t, name, dtype, ndim)
+    return t.shape, t.get_device()
+
+
+def _call(fn, dev, stream, *args):
+    """Call the library with the tensors' device current, on ``stream`` or that device's
+    current one."""
+    f = getattr(_lib or load(), fn)
+    if torch.cuda.current_device() == dev:
+        code = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
+                 else stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            code = f(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
+                     else stream.cuda_stream)
+    if code:
+        _check(fn, code)
 
 
 def vsa_block_mean(x, sizes=None, block=64, out=None, stream=None):
     """Block means: x bf16 [B,H,S,128] -> bf16 [B,H,ceil(S/block),128], each the mean of the
     first sizes[j] tokens of block j (sizes int32 [nb]; None = all there are)."""
-    _dev(x, "x", torch.bfloat16, 4)
-    B, H, S, D = x.shape
-    nb = -(-S // block) if block else 0
-    if sizes is not None:
-        _i32(sizes, "sizes", (nb,))
+    (B, H, S, D), dev = _lead("x", x, torch.bfloat16, 4)
+    nb = -(-S // block) if block > 0 else 0
+    sizes_p = _maybe("sizes", sizes, torch.int32, (nb,), dev)
     if out is None:
         out = torch.empty((B, H, nb, D), dtype=torch.bfloat16, device=x.device)
-    elif _dev(out, "out", torch.bfloat16).shape != (B, H, nb, D):
-        raise ValueError("out must be [B,H,ceil(S/block),128]")
-    _call("vsa_block_mean", _same_device(x, sizes=sizes, out=out), _ptr(x), _ptr(sizes), B, H, S,
-          D, block, _ptr(out), stream=stream)
+    out_p = _need("out", out, torch.bfloat16, (B, H, nb, D), dev)
+    _call("vsa_block_mean", dev, stream, x.data_ptr(), sizes_p, B, H, S, D, block, out_p)
     return out
 
 
@@ -521,19 +542,14 @@ def vsa_select_blocks(q_mean, k_mean, topk, sizes=None, causal=False, n_first=0,
     -1 behind; q2k_num int32 [B,Hq,nq]).  sizes int32 [nk]: blocks of size 0 are not chosen;
     causal: no block past the diagonal i + nk - nq; the first n_first blocks and those
     nearer than n_near to the diagonal are always chosen."""
-    _dev(q_mean, "q_mean", torch.bfloat16, 4)
-    _dev(k_mean, "k_mean", torch.bfloat16, 4)
-    B, Hq, nq, D = q_mean.shape
-    Bk, Hkv, nk, Dk = k_mean.shape
-    if Bk != B or Dk != D:
-        raise ValueError("k_mean must be [B,Hkv,nk,D] with q_mean's B and D")
-    if sizes is not None:
-        _i32(sizes, "sizes", (nk,))
+    (B, Hq, nq, D), dev = _lead("q_mean", q_mean, torch.bfloat16, 4)
+    (_, Hkv, nk, _), _ = _lead("k_mean", k_mean, torch.bfloat16, 4)
+    k_p = _need("k_mean", k_mean, torch.bfloat16, (B, Hkv, nk, D), dev)
+    sizes_p = _maybe("sizes", sizes, torch.int32, (nk,), dev)
     idx = torch.empty((B, Hq, nq, max(0, topk)), dtype=torch.int32, device=q_mean.device)
     num = torch.empty((B, Hq, nq), dtype=torch.int32, device=q_mean.device)
-    _call("vsa_select_blocks", _same_device(q_mean, k_mean=k_mean, sizes=sizes), _ptr(q_mean),
-          _ptr(k_mean), _ptr(sizes), B, Hq, Hkv, nq, nk, D, topk, int(bool(causal)), n_first,
-          n_near, _ptr(idx), _ptr(num), stream=stream)
+    _call("vsa_select_blocks", dev, stream, q_mean.data_ptr(), k_p, sizes_p, B, Hq, Hkv, nq, nk,
+          D, topk, 1 if causal else 0, n_first, n_near, idx.data_ptr(), num.data_ptr())
     return idx, num
 
 
@@ -557,30 +573,20 @@ def new_cache8(pages, block=64, device=None) -> Cache8:
     return Cache8(code[0], code[1], scale[0], scale[1], mean)
 
 
-def _cache(cache, table, lens, B):
-    """(pages, block, Hkv, max_blocks) of a checked cache, table and lens."""
-    _dev(cache.k, "cache.k", torch.float8_e4m3fn, 3)
-    pages, block, D = cache.k.shape
-    if _dev(cache.v, "cache.v", torch.float8_e4m3fn).shape != cache.k.shape or D != HEAD_DIM:
-        raise ValueError("cache.k and cache.v must both be [pages,block,128]")
-    for name, t in (("k_scale", cache.k_scale), ("v_scale", cache.v_scale)):
-        if _dev(t, "cache." + name, torch.float32).shape != (pages,):
-            raise ValueError(f"cache.{name} must be [pages]")
-    if cache.k_mean is not None:
-        if _dev(cache.k_mean, "cache.k_mean", torch.bfloat16).shape != (pages, D):
-            raise ValueError("cache.k_mean must be [pages,128]")
-    _dev(table, "table", torch.int32, 3)
-    if table.shape[0] != B:
-        raise ValueError("table must be [B,Hkv,max_blocks]")
-    _i32(lens, "lens", (B,))
-    return pages, block, table.shape[1], table.shape[2]
+def _cache(cache, dev):
+    """(pages, block, addresses of k, v, k_scale, v_scale) of a checked cache."""
+    k, v, ks, vs, _ = cache
+    (pages, block, _), _ = _lead("cache.k", k, torch.float8_e4m3fn, 3)
+    shape = (pages, block, HEAD_DIM)
+    return (pages, block, _need("cache.k", k, torch.float8_e4m3fn, shape, dev),
+            _need("cache.v", v, torch.float8_e4m3fn, shape, dev),
+            _need("cache.k_scale", ks, torch.float32, (pages,), dev),
+            _need("cache.v_scale", vs, torch.float32, (pages,), dev))
 
 
-def _one_token(q):
-    _dev(q, "q", torch.bfloat16, 4)
-    if q.shape[2] != 1:
-        raise ValueError("q must be [B,Hq,1,128]: one token per sequence")
-    return q.shape[0], q.shape[1], q.shape[3]
+def _table(table, B, dev):
+    (_, Hkv, max_blocks), _ = _lead("table", table, torch.int32, 3)
+    return Hkv, max_blocks, _need("table", table, torch.int32, (B, Hkv, max_blocks), dev)
 
 
 def vsa_cache_select(q, k_mean, table, lens, topk, block=64, n_first=0, n_near=1, stream=None):
@@ -588,18 +594,16 @@ def vsa_cache_select(q, k_mean, table, lens, topk, block=64, n_first=0, n_near=1
     bf16 [pages,128] (Cache8.k_mean), table int32 [B,Hkv,max_blocks], lens int32 [B] ->
     (idx int32 [B,Hkv,topk], num int32 [B,Hkv]), shared by the heads of a group (a block's
     score is the largest of its heads')."""
-    B, Hq, D = _one_token(q)
-    _dev(k_mean, "k_mean", torch.bfloat16, 2)
-    _dev(table, "table", torch.int32, 3)
-    if table.shape[0] != B or k_mean.shape[1] != D:
-        raise ValueError("table must be [B,Hkv,max_blocks] and k_mean [pages,128]")
-    _i32(lens, "lens", (B,))
-    Hkv, max_blocks = table.shape[1:]
+    (B, Hq, _, D), dev = _lead("q", q, torch.bfloat16, 4)
+    q_p = _need("q", q, torch.bfloat16, (B, Hq, 1, D), dev)
+    (pages, _), _ = _lead("k_mean", k_mean, torch.bfloat16, 2)
+    mean_p = _need("k_mean", k_mean, torch.bfloat16, (pages, D), dev)
+    Hkv, max_blocks, table_p = _table(table, B, dev)
+    lens_p = _need("lens", lens, torch.int32, (B,), dev)
     idx = torch.empty((B, Hkv, max(0, topk)), dtype=torch.int32, device=q.device)
     num = torch.empty((B, Hkv), dtype=torch.int32, device=q.device)
-    _call("vsa_cache_select", _same_device(q, k_mean=k_mean, table=table, lens=lens), _ptr(q),
-          _ptr(k_mean), _ptr(table), _ptr(lens), B, Hq, Hkv, D, k_mean.shape[0], max_blocks,
-          block, topk, n_first, n_near, _ptr(idx), _ptr(num), stream=stream)
+    _call("vsa_cache_select", dev, stream, q_p, mean_p, table_p, lens_p, B, Hq, Hkv, D, pages,
+          max_blocks, block, topk, n_first, n_near, idx.data_ptr(), num.data_ptr())
     return idx, num
 
 
@@ -607,21 +611,16 @@ def vsa_cache_write(cache, k, v, table, lens, n_new=None, stream=None):
     """Tokens lens[b] .. of every sequence into its pages: k, v bf16 [B,Hkv,T,128], of which
     sequence b writes the first n_new[b] (int32 [B]; None = T).  lens counts the tokens held
     before; add n_new to it afterwards."""
-    _dev(k, "k", torch.bfloat16, 4)
-    _dev(v, "v", torch.bfloat16, 4)
-    B, Hkv, T, D = k.shape
-    pages, block, Ht, max_blocks = _cache(cache, table, lens, B)
-    if v.shape != k.shape or Ht != Hkv:
-        raise ValueError("k and v must be [B,Hkv,T,128] and table [B,Hkv,max_blocks]")
-    if n_new is not None:
-        _i32(n_new, "n_new", (B,))
-    _call("vsa_cache_write",
-          _same_device(k, v=v, table=table, lens=lens, n_new=n_new, cache_k=cache.k,
-                       cache_v=cache.v, k_scale=cache.k_scale, v_scale=cache.v_scale,
-                       k_mean=cache.k_mean),
-          _ptr(k), _ptr(v), _ptr(table), _ptr(lens), _ptr(n_new), B, Hkv, T, D, pages,
-          max_blocks, block, _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale),
-          _ptr(cache.v_scale), _ptr(cache.k_mean), stream=stream)
+    (B, Hkv, T, D), dev = _lead("k", k, torch.bfloat16, 4)
+    v_p = _need("v", v, torch.bfloat16, (B, Hkv, T, D), dev)
+    pages, block, kc, vc, ks, vs = _cache(cache, dev)
+    mean_p = _maybe("cache.k_mean", cache[4], torch.bfloat16, (pages, HEAD_DIM), dev)
+    _, max_blocks, _ = _table(table, B, dev)
+    table_p = _need("table", table, torch.int32, (B, Hkv, max_blocks), dev)
+    lens_p = _need("lens", lens, torch.int32, (B,), dev)
+    new_p = _maybe("n_new", n_new, torch.int32, (B,), dev)
+    _call("vsa_cache_write", dev, stream, k.data_ptr(), v_p, table_p, lens_p, new_p, B, Hkv, T, D,
+          pages, max_blocks, block, kc, vc, ks, vs, mean_p)
 
 
 def cache_workspace_bytes(B, Hq, Hkv, max_blocks, weights=False) -> int:
@@ -644,40 +643,38 @@ def vsa_fwd_cache(q, cache, table, lens, idx=None, num=None, scale=None, out=Non
     int32 [B,Hkv,max_sel], num int32 [B,Hkv]) or all.  Returns (out, lse or None).  weight
     (float32 [B,Hkv,max_blocks]) becomes keep * weight + the step's weight of each block.
     The workspace is allocated if not given."""
-    B, Hq, D = _one_token(q)
-    pages, block, Hkv, max_blocks = _cache(cache, table, lens, B)
-    if (idx is None) != (num is None):
+    (B, Hq, _, D), dev = _lead("q", q, torch.bfloat16, 4)
+    q_p = _need("q", q, torch.bfloat16, (B, Hq, 1, D), dev)
+    pages, block, kc, vc, ks, vs = _cache(cache, dev)
+    Hkv, max_blocks, table_p = _table(table, B, dev)
+    lens_p = _need("lens", lens, torch.int32, (B,), dev)
+    max_sel, idx_p, num_p = 0, None, None
+    if idx is not None and num is not None:
+        (_, _, max_sel), _ = _lead("idx", idx, torch.int32, 3)
+        idx_p = _need("idx", idx, torch.int32, (B, Hkv, max_sel), dev)
+        num_p = _need("num", num, torch.int32, (B, Hkv), dev)
+    elif idx is not None or num is not None:
         raise ValueError("idx and num go together")
-    max_sel = 0
-    if idx is not None:
-        _dev(idx, "idx", torch.int32, 3)
-        if idx.shape[:2] != (B, Hkv):
-            raise ValueError("idx must be [B,Hkv,max_sel]")
-        _i32(num, "num", (B, Hkv))
-        max_sel = idx.shape[2]
-    if weight is not None and _dev(weight, "weight", torch.float32).shape != table.shape:
-        raise ValueError("weight must be [B,Hkv,max_blocks]")
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    weight_p = _maybe("weight", weight, torch.float32, (B, Hkv, max_blocks), dev)
     if out is None:
         out = torch.empty_like(q)
-    elif _dev(out, "out", torch.bfloat16).shape != q.shape:
-        raise ValueError("out must have q's shape")
-    lse_t = _lse_arg(lse, (B, Hq, 1), q.device)
-    if lse_t is not None and lse_t.shape != (B, Hq, 1):
-        raise ValueError("lse must be [B,Hq,1]")
+    out_p = _need("out", out, torch.bfloat16, (B, Hq, 1, D), dev)
+    if lse is True:
+        lse = torch.empty((B, Hq, 1), dtype=torch.float32, device=q.device)
+    elif lse is False:
+        lse = None
+    lse_p = _maybe("lse", lse, torch.float32, (B, Hq, 1), dev)
     if workspace is None:
         if Hkv < 1 or Hq < 1 or Hq % Hkv:
             raise ValueError("Hq must be a multiple of table's Hkv")
         workspace = new_cache_workspace(B, Hq, Hkv, max_blocks, weight is not None, q.device)
-    _call("vsa_fwd_cache",
-          _same_device(q, cache_k=cache.k, cache_v=cache.v, k_scale=cache.k_scale,
-                       v_scale=cache.v_scale, table=table, lens=lens, idx=idx, num=num, out=out,
-                       lse=lse_t, weight=weight, workspace=workspace),
-          _ptr(q), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale),
-          _ptr(table), _ptr(lens), _ptr(idx), _ptr(num), max_sel, B, Hq, Hkv, D, pages,
-          max_blocks, block, scale, float(keep), _ptr(out), _ptr(lse_t), _ptr(weight),
-          _ptr(workspace), workspace.numel() * workspace.element_size(), stream=stream)
-    return out, lse_t
+    elif not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
+    _call("vsa_fwd_cache", dev, stream, q_p, kc, vc, ks, vs, table_p, lens_p, idx_p, num_p,
+          max_sel, B, Hq, Hkv, D, pages, max_blocks, block,
+          1.0 / math.sqrt(D) if scale is None else float(scale), float(keep), out_p, lse_p,
+          weight_p, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return out, lse
 
 
 class Evicted(NamedTuple):
@@ -695,14 +692,13 @@ def vsa_cache_evict(weight, table, lens, budget, block=64, n_first=0, n_last=1,
     """Cut every sequence to at most `budget` blocks per key/value head: the first n_first
     and last n_last stay, and of the rest those of the highest weight (float32
     [B,Hkv,max_blocks], as vsa_fwd_cache accumulates it)."""
-    _dev(weight, "weight", torch.float32, 3)
-    B, Hkv, max_blocks = weight.shape
-    _i32(table, "table", weight.shape)
-    _i32(lens, "lens", (B,))
-    r = Evicted(torch.empty_like(table), torch.empty_like(weight), torch.empty_like(lens),
-                torch.empty_like(table), torch.empty_like(lens))
-    _call("vsa_cache_evict", _same_device(weight, table=table, lens=lens), _ptr(weight),
-          _ptr(table), _ptr(lens), B, Hkv, max_blocks, block, budget, n_first, n_last,
-          _ptr(r.table), _ptr(r.weight), _ptr(r.lens), _ptr(r.freed), _ptr(r.n_freed),
-          stream=stream)
-    return r
+    (B, Hkv, max_blocks), dev = _lead("weight", weight, torch.float32, 3)
+    table_p = _need("table", table, torch.int32, (B, Hkv, max_blocks), dev)
+    lens_p = _need("lens", lens, torch.int32, (B,), dev)
+    table_out, freed = torch.empty_like(table), torch.empty_like(table)
+    lens_out, n_freed = torch.empty_like(lens), torch.empty_like(lens)
+    weight_out = torch.empty_like(weight)
+    _call("vsa_cache_evict", dev, stream, weight.data_ptr(), table_p, lens_p, B, Hkv, max_blocks,
+          block, budget, n_first, n_last, table_out.data_ptr(), weight_out.data_ptr(),
+          lens_out.data_ptr(), freed.data_ptr(), n_freed.data_ptr())
+    return Evicted(table_out, weight_out, lens_out, freed, n_freed)

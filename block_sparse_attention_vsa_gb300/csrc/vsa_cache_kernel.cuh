@@ -187,11 +187,13 @@ struct CacheFwdArgs {
   uint16_t* out;           // [B, Hq, 1, 128]
   float* lse;              // [B, Hq, 1] or null
   float* weight;           // [B, Hkv, max_blocks] or null
-  unsigned int* counters;  // [B, Hkv, chunks + 1], zero before and after
-  float* part;             // [B, Hkv, chunks, splits][8 * 128 + 16]
+  unsigned int* counters;  // zero before and after
+  float* part;             // [2 pieces][8 * 128 + 16], then [pieces / 8 + 2] more
   float* lse_ws;           // [B, Hkv, group] (with weight)
   float2* mass;            // [B, Hkv, max_blocks, 8 * chunks] (with weight)
-  int Hkv, group, chunks, splits, pages, max_blocks, max_sel;
+  int rows;                // B * Hkv * chunks
+  int Hkv, group, chunks, pages, max_blocks, max_sel;
+  int pieces;              // the most there can be
   float scale_log2, keep;
 };
 
@@ -199,15 +201,44 @@ constexpr int kCacheWarps = 4;
 constexpr int kCacheStages = 3;
 constexpr int kCacheTile = 32;                           // tokens a stage
 constexpr int kCacheStageBytes = 2 * kCacheTile * 128;   // keys, then values
-constexpr int kCacheList = 512;                          // blocks a CTA walks at most
+constexpr int kCacheList = 256;                          // blocks listed at a time
 constexpr int kCachePartFloats = 8 * 128 + 16;           // O [8][128], m [8], l [8]
-constexpr int kCacheMinBlocks = 4;                       // blocks a split has at least
-constexpr size_t kCacheSmem = (size_t)kCacheWarps * kCacheStages * kCacheStageBytes;
+constexpr int kCacheResident = 2;                        // CTAs an SM holds
+constexpr int kCacheGrid = 152 * kCacheResident;
+constexpr int kCacheLate = 1024;                         // pieces handed out at run time, at most
+constexpr int kCacheLateTokens = 1024;                    // tokens in one, at least
+constexpr int kCacheLateShare = 8;                       // of the units: one in 8
+constexpr int kCacheFan = 16;                            // partial results joined at a time
+constexpr int kCacheRingBytes = kCacheWarps * kCacheStages * kCacheStageBytes;
+constexpr int kCacheJoinHeads = 4;                       // heads joined at a time
+constexpr size_t kCacheSmem =
+    (size_t)kCacheRingBytes + kCacheWarps * kCacheJoinHeads * 128 * sizeof(float);
+// counters: groups of a row's pieces, rows, the queue and its end, chunks of a head group
+constexpr int kCacheRowCounters = 4096, kCacheQueue = 8190, kCacheChunkCounters = 8192;
 
-// One CTA: one 8-head chunk of a (sequence, key/value head) and one contiguous range of
-// its listed blocks; a warp takes every fourth block of the range, alone: its own ring of
-// asynchronous copies (32 tokens a stage: 4 KB of keys, 4 KB of values, two stages in
-// flight while one is used), its own running maximum and sums, no barrier until the end.
+// A stretch of listed blocks of one row, up to kCacheList of them.
+struct CacheSeg {
+  int piece, row, row_units;
+  long long row_at;           // the row's first unit
+  int first, from, past, to;  // units of the row: the piece's part [first, to), this stretch
+  int len, held, cnt;         // tokens and blocks of the sequence, blocks in the list
+};
+
+// A row is an 8-head chunk of a (sequence, key/value head).  All rows' blocks form one
+// sequence of units, and the sequence is cut into pieces: one for each CTA (two per SM,
+// one wave) of equal size, and, where there is enough, a last part in small pieces that
+// CTAs fetch from a counter when they are through -- SMs differ in speed by a fifth, and
+// lengths do not matter to such a cut.  A piece may hold several rows and begin and end
+// inside one; a row spread over several pieces leaves a partial result in each, and the
+// last one to arrive joins them in order (beyond 32 in groups of 16, then the groups).
+// Rows whose listing holds duplicates or bad entries count by their stated number; the
+// places that are not there do nothing.
+//
+// Within a stretch of a row each warp works alone on every fourth block: its own ring of
+// asynchronous copies (32 tokens a stage: 4 KB of keys and of values), its own running
+// maximum and sums, no barrier until the row's end.  The next stretch's list is made
+// before this one's blocks are worked on, and the ring runs on into it, so that copies
+// are in flight while a row is joined and the next one set up.
 //
 // Codes become fp16 in registers (exact) and both products run on m16n8k16 tensor
 // products with the heads as the 8 columns:
@@ -223,430 +254,664 @@ constexpr size_t kCacheSmem = (size_t)kCacheWarps * kCacheStages * kCacheStageBy
 // The 8-bit values are the only large traffic; everything else is arranged so that they
 // arrive without a pause.
 template <int BLOCK, bool WEIGHT>
-__global__ void __launch_bounds__(kCacheWarps * 32, 2) cache_fwd_kernel(const CacheFwdArgs a) {
+__global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
+    cache_fwd_kernel(const CacheFwdArgs a) {
   constexpr int kThreads = kCacheWarps * 32;
   constexpr int kHalves = BLOCK / kCacheTile;
+  constexpr int N = kCacheStages;
   extern __shared__ __align__(128) uint8_t s_ring[];
-  __shared__ uint32_t s_bits[kMaxBlocks / 32];
-  __shared__ int s_page[kCacheList];
-  __shared__ float s_ks[kCacheList], s_vs[kCacheList];
-  __shared__ uint16_t s_blk[kCacheList];
-  __shared__ float s_qf[8];
+  float* const s_o = reinterpret_cast<float*>(s_ring + kCacheRingBytes);
+  __shared__ uint32_t s_bits[2][kMaxBlocks / 32];
+  __shared__ int s_page[2][kCacheList];
+  __shared__ uint16_t s_blk[2][kCacheList];
+  __shared__ float s_scale[kCacheWarps][N][2];
   __shared__ float s_m[kCacheWarps][8], s_l[kCacheWarps][8];
-  __shared__ int s_last;
-  __shared__ int s_n;
+  __shared__ long long s_scan[kCacheWarps];
+  __shared__ long long s_at;
+  __shared__ int s_row, s_next, s_last;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, i4 = lane & 3;
-  int u = blockIdx.x;
-  const int split = u % a.splits;
-  u /= a.splits;
-  const int chunk = u % a.chunks;
-  const long long bh = u / a.chunks;
-  const int b = (int)(bh / a.Hkv);
-  const int len = max(0, a.lens[b]);
-  const int held = (int)min(((long long)len + BLOCK - 1) / BLOCK, (long long)a.max_blocks);
-  const int32_t* table = a.table + bh * a.max_blocks;
 
-  // the row's blocks: all it holds, or the listed ones as a set, ascending
-  int n = held;
-  if (a.idx != nullptr) {
-    for (int i = tid; i < kMaxBlocks / 32; i += kThreads) s_bits[i] = 0;
-    __syncthreads();
-    const int cnt = min(max(0, a.num[bh]), a.max_sel);
-    const int32_t* idx = a.idx + bh * a.max_sel;
-    for (int i = tid; i < cnt; i += kThreads) {
-      const int e = idx[i];
-      if (e >= 0 && e < held) atomicOr(&s_bits[e >> 5], 1u << (e & 31));
-    }
-    __syncthreads();
-    if (warp == 0) {
-      const int c = __reduce_add_sync(0xffffffffu, __popc(s_bits[lane]) + __popc(s_bits[lane + 32]));
-      if (lane == 0) s_n = c;
-    }
-    __syncthreads();
-    n = s_n;
-  }
-  const int splits = max(1, min(a.splits, (n + kCacheMinBlocks - 1) / kCacheMinBlocks));
-  if (split >= splits) return;
-  const int lo = (int)((long long)n * split / splits);
-  const int cnt = (int)((long long)n * (split + 1) / splits) - lo;
-  // the range's list
-  if (a.idx == nullptr) {
-    for (int i = tid; i < cnt; i += kThreads) s_blk[i] = (uint16_t)(lo + i);
-  } else if (warp < 2) {
-    const uint32_t w = s_bits[lane + 32 * warp];
-    int at = __popc(w);
+  auto held_of = [&](int b) {
+    const long long len = max(0, a.lens[b]);
+    return (int)min((len + BLOCK - 1) / BLOCK, (long long)a.max_blocks);
+  };
+  // units of a row: its blocks as stated, 1 at least
+  auto units_of = [&](int row) {
+    const int bh = row / a.chunks;
+    int n = held_of(bh / a.Hkv);
+    if (a.idx != nullptr) n = min(n, min(a.num[bh], a.max_sel));
+    return max(1, n);
+  };
+
+  // ---- the pieces: `early` ones of equal size over the first units, then `late` ones of
+  // `size` units
+  const int per = (a.rows + kThreads - 1) / kThreads;
+  const int my0 = min(a.rows, tid * per), my1 = min(a.rows, my0 + per);
+  long long mine_before, mine_sum = 0, total = 0, early_units;
+  int early, late, size;
+  {
+    for (int r = my0; r < my1; ++r) mine_sum += units_of(r);
+    long long x = mine_sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, at, o);
-      if (lane >= o) at += y;
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
-    at -= __popc(w);
-    if (warp == 1) at += __reduce_add_sync(0xffffffffu, __popc(s_bits[lane]));
-    for (uint32_t r = w; r != 0; r &= r - 1, ++at)
-      if (at >= lo && at < lo + cnt)
-        s_blk[at - lo] = (uint16_t)((lane + 32 * warp) * 32 + __ffs(r) - 1);
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    mine_before = x - mine_sum;
+#pragma unroll
+    for (int w = 0; w < kCacheWarps; ++w) {
+      if (w < warp) mine_before += s_scan[w];
+      total += s_scan[w];
+    }
+    early = (int)max(1ll, min((long long)gridDim.x, total / 2));
+    constexpr int kLeast = kCacheLateTokens / BLOCK;
+    const long long part = total / kCacheLateShare;
+    size = (int)max((long long)kLeast, (part + kCacheLate - 1) / kCacheLate);
+    late = part >= 2ll * kLeast * early ? (int)(part / size) : 0;
+    early_units = total - (long long)late * size;
   }
-  __syncthreads();
-  for (int i = tid; i < cnt; i += kThreads) {
-    int page = table[s_blk[i]];
-    if (page < 0 || page >= a.pages) page = -1;
-    s_page[i] = page;
-    s_ks[i] = page >= 0 ? a.k_scale[page] : 0.0f;
-    s_vs[i] = page >= 0 ? a.v_scale[page] : 0.0f;
-  }
+  const int pieces = early + late;
+  auto begin_of = [&](int p) {
+    return p <= early ? early_units * p / early : early_units + (long long)(p - early) * size;
+  };
+  auto piece_of = [&](long long u) {
+    return u < early_units ? (int)(((u + 1) * early - 1) / early_units)
+                           : early + (int)((u - early_units) / size);
+  };
 
-  // q of this thread's head column g: columns 16 * (i4 + 4 j) + 0..15
-  const int heads = min(8, a.group - chunk * 8);
-  const long long head0 = bh * a.group + chunk * 8;
-  uint32_t qb[2][4][2];
-  {
-    uint4 w[2][2];
-    uint32_t amax = 0;
+  // ---- from one stretch to the next; false when there is none.  Uniform over the CTA.
+  auto enter_row = [&](CacheSeg& s, long long unit) {
+    s.row_units = units_of(s.row);
+    s.first = s.from = (int)(unit - s.row_at);
+    s.to = (int)(min(begin_of(s.piece + 1), s.row_at + s.row_units) - s.row_at);
+    s.past = min(s.to, s.from + kCacheList);
+  };
+  auto enter_piece = [&](CacheSeg& s, int piece) {
+    if (piece >= pieces) return false;
+    const long long lo = begin_of(piece);
+    __syncthreads();
+    if (mine_before <= lo && lo < mine_before + mine_sum) {
+      long long at = mine_before;
+      int r = my0;
+      for (;; ++r) {
+        const int n = units_of(r);
+        if (lo < at + n) break;
+        at += n;
+      }
+      s_row = r;
+      s_at = at;
+    }
+    __syncthreads();
+    s.piece = piece;
+    s.row = s_row;
+    s.row_at = s_at;
+    enter_row(s, lo);
+    return true;
+  };
+  auto advance = [&](CacheSeg& s) {
+    if (s.past < s.to) {  // more of the same row
+      s.from = s.past;
+      s.past = min(s.to, s.from + kCacheList);
+      return true;
+    }
+    const long long unit = s.row_at + s.to;
+    if (unit < begin_of(s.piece + 1)) {  // the piece's next row
+      s.row_at += s.row_units;
+      ++s.row;
+      enter_row(s, unit);
+      return true;
+    }
+    if (late == 0) return false;
+    __syncthreads();
+    if (tid == 0) s_next = early + (int)atomicAdd(a.counters + kCacheQueue, 1u);
+    __syncthreads();
+    return enter_piece(s, s_next);
+  };
+  // ---- a stretch's list of pages, in buffer `buf`
+  auto list = [&](CacheSeg& s, int buf) {
+    const long long bh = s.row / a.chunks;
+    s.len = max(0, a.lens[bh / a.Hkv]);
+    s.held = held_of((int)(bh / a.Hkv));
+    const int32_t* table = a.table + bh * a.max_blocks;
+    uint32_t* bits = s_bits[buf];
+    __syncthreads();  // the buffer's last user is through
+    if (a.idx == nullptr) {
+      s.cnt = min(s.past, s.held) - s.from;  // held may be 0, with one unit all the same
+      for (int i = tid; i < s.cnt; i += kThreads) {
+        const int page = table[s.from + i];
+        s_blk[buf][i] = (uint16_t)(s.from + i);
+        s_page[buf][i] = page >= 0 && page < a.pages ? page : -1;
+      }
+    } else {
+      const int listed = min(max(0, a.num[bh]), a.max_sel);
+      const int32_t* idx = a.idx + bh * a.max_sel;
+      const int idx0 = tid < a.max_sel ? idx[tid] : -1;
+      for (int i = tid; i < kMaxBlocks / 32; i += kThreads) bits[i] = 0;
+      __syncthreads();
+      if (tid < listed && idx0 >= 0 && idx0 < s.held)
+        atomicOr(&bits[idx0 >> 5], 1u << (idx0 & 31));
+      for (int i = tid + kThreads; i < listed; i += kThreads) {
+        const int e = idx[i];
+        if (e >= 0 && e < s.held) atomicOr(&bits[e >> 5], 1u << (e & 31));
+      }
+      __syncthreads();
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < kMaxBlocks / 1024; ++i)
+        n += __reduce_add_sync(0xffffffffu, __popc(bits[lane + 32 * i]));
+      s.cnt = max(0, min(s.past, n) - s.from);
+      if (warp < kMaxBlocks / 1024) {
+        const uint32_t w = bits[lane + 32 * warp];
+        int at = __popc(w);
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, at, x);
+          if (lane >= x) at += y;
+        }
+        at -= __popc(w);
+        for (int i = 0; i < warp; ++i)
+          at += __reduce_add_sync(0xffffffffu, __popc(bits[lane + 32 * i]));
+        for (uint32_t r = w; r != 0; r &= r - 1, ++at)
+          if (at >= s.from && at < s.from + s.cnt) {
+            const int e = (lane + 32 * warp) * 32 + __ffs(r) - 1, page = table[e];
+            s_blk[buf][at - s.from] = (uint16_t)e;
+            s_page[buf][at - s.from] = page >= 0 && page < a.pages ? page : -1;
+          }
+      }
+    }
+    __syncthreads();
+  };
+  // a stretch's stages for this warp: every fourth block, kHalves stages each
+  auto stages_of = [&](const CacheSeg& s) {
+    return s.cnt > warp ? (s.cnt - warp + kCacheWarps - 1) / kCacheWarps * kHalves : 0;
+  };
+  auto valid_of = [&](const CacheSeg& s, int buf, int entry, int half) {  // tokens that exist
+    const int left = s.len - (int)s_blk[buf][entry] * BLOCK - half * kCacheTile;
+    return s_page[buf][entry] < 0 ? 0 : max(0, min(kCacheTile, left));
+  };
+  // Copy stage st into a slot.  Keys: token r, chunk c at chunk c ^ 4 (r & 1); values:
+  // c ^ 2 ((r >> 1) & 3) -- each makes its own reads (below) touch all banks.
+  uint8_t* const ring = s_ring + warp * (N * kCacheStageBytes);
+  auto copy = [&](const CacheSeg& s, int buf, int st, int slot) {
+    const int entry = warp + (st / kHalves) * kCacheWarps, half = st % kHalves;
+    const int ok = valid_of(s, buf, entry, half);
+    if (ok > 0) {
+      const int page = s_page[buf][entry];
+      const uint32_t dst = smem_addr(ring + slot * kCacheStageBytes);
+      const long long off = ((long long)page * BLOCK + half * kCacheTile) * 128;
+      if (lane < 2)
+        cp_async4(smem_addr(&s_scale[warp][slot][lane]),
+                  (lane == 0 ? a.k_scale : a.v_scale) + page);
+      const int c = lane & 7;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + (lane >> 3);
+        const uint32_t nb = r < ok ? 16u : 0u;
+        cp_async16(dst + r * 128 + ((c ^ ((r & 1) << 2)) << 4),
+                   a.k_cache + off + (nb ? r * 128 + c * 16 : 0), nb);
+        cp_async16(dst + kCacheTile * 128 + r * 128 + ((c ^ (((r >> 1) & 3) << 1)) << 4),
+                   a.v_cache + off + (nb ? r * 128 + c * 16 : 0), nb);
+      }
+    }
+  };
+
+  CacheSeg cur, nxt;
+  int buf = 0, slot = 0;  // the list in use; the slot of the next stage to be used
+  bool more = (int)blockIdx.x < pieces && enter_piece(cur, blockIdx.x);
+  if (more) list(cur, 0);
+  int n_cur = more ? stages_of(cur) : 0;
+  // N groups of copies are always outstanding, some of them empty
+#pragma unroll
+  for (int st = 0; st < N; ++st) {
+    if (st < n_cur) copy(cur, 0, st, st);
+    cp_async_commit();
+  }
+  float o[8][4];
+  float m0, m1, l0, l1, mass0 = 0.0f, mass1 = 0.0f;
+
+  while (more) {
+    nxt = cur;
+    const bool follows = advance(nxt);
+    if (follows) list(nxt, buf ^ 1);
+    const int n_nxt = follows ? stages_of(nxt) : 0;
+    auto wrap = [&](int x) { return x >= N ? x - N : x; };
+    // the slots that this stretch is too short to fill
+    for (int st = n_cur; st < N; ++st) {
+      if (st - n_cur < n_nxt) copy(nxt, buf ^ 1, st - n_cur, wrap(slot + st));
+      cp_async_commit();
+    }
+
+    const int chunk = cur.row % a.chunks;
+    const long long bh = cur.row / a.chunks;
+    const int heads = min(8, a.group - chunk * 8);
+    const long long head0 = bh * a.group + chunk * 8;
+    const int32_t* table = a.table + bh * a.max_blocks;
+    // q of this thread's head column g: columns 16 * (i4 + 4 j) + 0..15
+    uint4 qw[2][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        w[j][p] = g < heads ? __ldg(reinterpret_cast<const uint4*>(a.q + (head0 + g) * 128) +
-                                    2 * (i4 + 4 * j) + p)
-                            : make_uint4(0, 0, 0, 0);
-        const uint32_t e[4] = {w[j][p].x, w[j][p].y, w[j][p].z, w[j][p].w};
+      for (int p = 0; p < 2; ++p)
+        qw[j][p] = g < heads ? __ldg(reinterpret_cast<const uint4*>(a.q + (head0 + g) * 128) +
+                                     2 * (i4 + 4 * j) + p)
+                             : make_uint4(0, 0, 0, 0);
+    uint32_t qb[2][4][2];
+    float qf0, qf1;  // what turns the products of heads 2 i4, 2 i4 + 1 into log2 units
+    {
+      uint32_t amax = 0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const uint32_t e[4] = {qw[j][p].x, qw[j][p].y, qw[j][p].z, qw[j][p].w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t p0 = e[x] & 0x7fffu, p1 = e[x] >> 16 & 0x7fffu;
+            if (p0 < 0x7f80u) amax = max(amax, p0);
+            if (p1 < 0x7f80u) amax = max(amax, p1);
+          }
+        }
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // the largest |q| lands in [2^7, 2^8)
+      const int e2 = max(-100, min(119, (int)(amax >> 7) - 127 - 7));
+      const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
+      const float f = __uint_as_float((uint32_t)(e2 + 127) << 23) * a.scale_log2;
+      qf0 = __shfl_sync(0xffffffffu, f, 8 * i4);
+      qf1 = __shfl_sync(0xffffffffu, f, 8 * i4 + 4);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const uint32_t p0 = e[x] & 0x7fffu, p1 = e[x] >> 16 & 0x7fffu;
-          if (p0 < 0x7f80u) amax = max(amax, p0);
-          if (p1 < 0x7f80u) amax = max(amax, p1);
+          const uint4 ww = qw[j][x >> 1];
+          const uint32_t e0 = (x & 1) ? ww.z : ww.x, e1 = (x & 1) ? ww.w : ww.y;
+          qb[j][x][0] = pack_f16x2(bf16_lo(e0) * down, bf16_hi(e0) * down);
+          qb[j][x][1] = pack_f16x2(bf16_lo(e1) * down, bf16_hi(e1) * down);
         }
-      }
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    // the largest |q| lands in [2^7, 2^8)
-    const int e2 = max(-100, min(119, (int)(amax >> 7) - 127 - 7));
-    const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
-    if (warp == 0 && i4 == 0) s_qf[g] = __uint_as_float((uint32_t)(e2 + 127) << 23) * a.scale_log2;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint4 ww = w[j][x >> 1];
-        const uint32_t e0 = (x & 1) ? ww.z : ww.x, e1 = (x & 1) ? ww.w : ww.y;
-        qb[j][x][0] = pack_f16x2(bf16_lo(e0) * down, bf16_hi(e0) * down);
-        qb[j][x][1] = pack_f16x2(bf16_lo(e1) * down, bf16_hi(e1) * down);
-      }
-  }
-  __syncthreads();
-  const float qf0 = s_qf[2 * i4], qf1 = s_qf[2 * i4 + 1];
-
-  float o[8][4] = {};
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-
-  // this warp's stages: block entries warp, warp + 4, ...; kHalves stages each
-  const int mine = cnt > warp ? (cnt - warp + kCacheWarps - 1) / kCacheWarps : 0;
-  const int n_stage = mine * kHalves;
-  uint8_t* ring = s_ring + warp * (kCacheStages * kCacheStageBytes);
-  auto valid_of = [&](int entry, int half) {  // tokens of the stage that exist
-    const long long left = (long long)len - (long long)s_blk[entry] * BLOCK - half * kCacheTile;
-    return s_page[entry] < 0 ? 0 : (int)max(0ll, min((long long)kCacheTile, left));
-  };
-  // Keys: token r, chunk c at chunk c ^ 4 (r & 1); values: c ^ 2 ((r >> 1) & 3) -- each
-  // makes its own reads (below) touch all banks.
-  auto issue = [&](int st) {
-    if (st < n_stage) {
-      const int entry = warp + (st / kHalves) * kCacheWarps, half = st % kHalves;
-      const int ok = valid_of(entry, half);
-      if (ok > 0) {
-        const uint32_t dst = smem_addr(ring + (st % kCacheStages) * kCacheStageBytes);
-        const long long off = ((long long)s_page[entry] * BLOCK + half * kCacheTile) * 128;
-        const int c = lane & 7;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = i * 4 + (lane >> 3);
-          const uint32_t nb = r < ok ? 16u : 0u;
-          cp_async16(dst + r * 128 + ((c ^ ((r & 1) << 2)) << 4),
-                     a.k_cache + off + (nb ? r * 128 + c * 16 : 0), nb);
-          cp_async16(dst + kCacheTile * 128 + r * 128 + ((c ^ (((r >> 1) & 3) << 1)) << 4),
-                     a.v_cache + off + (nb ? r * 128 + c * 16 : 0), nb);
-        }
-      }
     }
-    cp_async_commit();
-  };
+    if (cur.from == cur.first) {
 #pragma unroll
-  for (int st = 0; st < kCacheStages - 1; ++st) issue(st);
-  float mass0 = 0.0f, mass1 = 0.0f;
-  for (int st = 0; st < n_stage; ++st) {
-    cp_async_wait<kCacheStages - 2>();
-    __syncwarp();
-    issue(st + kCacheStages - 1);
-    const int entry = warp + (st / kHalves) * kCacheWarps, half = st % kHalves;
-    const int ok = valid_of(entry, half);
-    if (ok > 0) {
-      const uint8_t* kt = ring + (st % kCacheStages) * kCacheStageBytes;
-      const uint8_t* vt = kt + kCacheTile * 128;
-      const float f0 = qf0 * s_ks[entry], f1 = qf1 * s_ks[entry];
-      float s[2][4];
+      for (int t = 0; t < 8; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.0f;
+      m0 = m1 = -INFINITY;
+      l0 = l1 = 0.0f;
+    }
+
+    for (int st = 0; st < n_cur; ++st) {
+      cp_async_wait<N - 1>();
+      __syncwarp();
+      const int entry = warp + (st / kHalves) * kCacheWarps, half = st % kHalves;
+      const int ok = valid_of(cur, buf, entry, half);
+      if (ok > 0) {
+        const uint8_t* kt = ring + slot * kCacheStageBytes;
+        const uint8_t* vt = kt + kCacheTile * 128;
+        const float f0 = qf0 * s_scale[warp][slot][0], f1 = qf1 * s_scale[warp][slot][0];
+        const float vs = s_scale[warp][slot][1];
+        float s[2][4];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
-        const int ra = t * 16 + g, rb = ra + 8;
+        for (int t = 0; t < 2; ++t) {
+          s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
+          const int ra = t * 16 + g, rb = ra + 8;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int c = (i4 + 4 * j) ^ ((g & 1) << 2);
-          const uint4 xa = *reinterpret_cast<const uint4*>(kt + ra * 128 + c * 16);
-          const uint4 xb = *reinterpret_cast<const uint4*>(kt + rb * 128 + c * 16);
-          const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
+          for (int j = 0; j < 2; ++j) {
+            const int c = (i4 + 4 * j) ^ ((g & 1) << 2);
+            const uint4 xa = *reinterpret_cast<const uint4*>(kt + ra * 128 + c * 16);
+            const uint4 xb = *reinterpret_cast<const uint4*>(kt + rb * 128 + c * 16);
+            const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16x2(wa[x], a0, a2);
+              e4m3x4_to_f16x2(wb[x], a1, a3);
+              mma_f16(s[t], a0, a1, a2, a3, qb[j][x][0], qb[j][x][1]);
+            }
+          }
+        }
+        // scores in log2 units; tokens past the sequence's end are left out
+        float top0 = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const bool in = t * 16 + r * 8 + g < ok;
+            s[t][2 * r] = in ? s[t][2 * r] * f0 : -INFINITY;
+            s[t][2 * r + 1] = in ? s[t][2 * r + 1] * f1 : -INFINITY;
+            top0 = fmaxf(top0, s[t][2 * r]);
+            top1 = fmaxf(top1, s[t][2 * r + 1]);
+          }
+        if (__any_sync(0xffffffffu, top0 > m0 + 10.0f || top1 > m1 + 10.0f)) {
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) {
+            top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, x));
+            top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, x));
+          }
+          const float n0 = top0 > m0 + 10.0f ? top0 - 4.0f : m0;
+          const float n1 = top1 > m1 + 10.0f ? top1 - 4.0f : m1;
+          const float c0_ = n0 > m0 ? fast_exp2(m0 - n0) : 1.0f;
+          const float c1_ = n1 > m1 ? fast_exp2(m1 - n1) : 1.0f;
+          m0 = n0;
+          m1 = n1;
+          l0 *= c0_;
+          l1 *= c1_;
+          if (WEIGHT) {
+            mass0 *= c0_;
+            mass1 *= c1_;
+          }
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            o[t][0] *= c0_;
+            o[t][1] *= c1_;
+            o[t][2] *= c0_;
+            o[t][3] *= c1_;
+          }
+        }
+        const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
+        float acc[8][4] = {};
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float p0 = fast_exp2(s[t][0] - z0), p1 = fast_exp2(s[t][1] - z1);
+          const float p2 = fast_exp2(s[t][2] - z0), p3 = fast_exp2(s[t][3] - z1);
+          l0 += p0 + p2;
+          l1 += p1 + p3;
+          if (WEIGHT) {
+            mass0 += p0 + p2;
+            mass1 += p1 + p3;
+          }
+          const uint32_t b0 = transpose_8x8(pack_f16x2(p0, p1));
+          const uint32_t b1 = transpose_8x8(pack_f16x2(p2, p3));
+          // tokens 2 i4, 2 i4 + 1, and 8 further; columns 16 g .. 16 g + 15
+          uint32_t w[4][4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int r = t * 16 + 2 * i4 + (x & 1) + 8 * (x >> 1);
+            const uint4 y = *reinterpret_cast<const uint4*>(vt + r * 128 + ((g ^ (i4 << 1)) << 4));
+            w[x][0] = y.x;
+            w[x][1] = y.y;
+            w[x][2] = y.z;
+            w[x][3] = y.w;
+          }
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             uint32_t a0, a1, a2, a3;
-            e4m3x4_to_f16x2(wa[x], a0, a2);
-            e4m3x4_to_f16x2(wb[x], a1, a3);
-            mma_f16(s[t], a0, a1, a2, a3, qb[j][x][0], qb[j][x][1]);
+            e4m3x4_to_f16x2(__byte_perm(w[0][x], w[1][x], 0x5140), a0, a1);
+            e4m3x4_to_f16x2(__byte_perm(w[2][x], w[3][x], 0x5140), a2, a3);
+            mma_f16(acc[2 * x], a0, a1, a2, a3, b0, b1);
+            e4m3x4_to_f16x2(__byte_perm(w[0][x], w[1][x], 0x7362), a0, a1);
+            e4m3x4_to_f16x2(__byte_perm(w[2][x], w[3][x], 0x7362), a2, a3);
+            mma_f16(acc[2 * x + 1], a0, a1, a2, a3, b0, b1);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[t][x] = fmaf(acc[t][x], vs, o[t][x]);
+      }
+      if (WEIGHT && half == kHalves - 1) {
+        // the block's weight under the running maximum, per head
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          mass0 += __shfl_xor_sync(0xffffffffu, mass0, x);
+          mass1 += __shfl_xor_sync(0xffffffffu, mass1, x);
+        }
+        if (g == 0) {
+          float4* to = reinterpret_cast<float4*>(
+              a.mass + ((bh * a.max_blocks + s_blk[buf][entry]) * a.chunks + chunk) * 8 + 2 * i4);
+          *to = make_float4(mass0, m0, mass1, m1);
+        }
+        mass0 = mass1 = 0.0f;
+      }
+      __syncwarp();
+      const int ahead = st + N;  // the stage that takes the slot's place
+      if (ahead < n_cur)
+        copy(cur, buf, ahead, slot);
+      else if (ahead - n_cur < n_nxt)
+        copy(nxt, buf ^ 1, ahead - n_cur, slot);
+      cp_async_commit();
+      slot = wrap(slot + 1);
+    }
+
+    if (cur.past == cur.to) {  // the piece's part of the row ends here
+      // ---- join the warps, four heads at a time: thread e has head e / 32, columns
+      // 4 (e % 32)..; x counts the two rounds
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, x);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, x);
+      }
+      if (g == 0) {
+        s_m[warp][2 * i4] = m0;
+        s_m[warp][2 * i4 + 1] = m1;
+        s_l[warp][2 * i4] = l0;
+        s_l[warp][2 * i4 + 1] = l1;
+      }
+      __syncthreads();
+      auto joint_m = [&](int h) {
+        float m = s_m[0][h];
+#pragma unroll
+        for (int w = 1; w < kCacheWarps; ++w) m = fmaxf(m, s_m[w][h]);
+        return m;
+      };
+      const float t0 = joint_m(2 * i4), t1 = joint_m(2 * i4 + 1);
+      const float d0 = m0 == -INFINITY ? 0.0f : fast_exp2(m0 - t0);
+      const float d1 = m1 == -INFINITY ? 0.0f : fast_exp2(m1 - t1);
+      const int c4 = lane * 4;
+      float4 v[2];
+      float vm[2], vl[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (i4 >> 1 == x) {
+          float* to = s_o + (warp * kCacheJoinHeads + 2 * (i4 & 1)) * 128 + 16 * g;
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            *reinterpret_cast<float2*>(to + 2 * t) = make_float2(o[t][0] * d0, o[t][2] * d0);
+            *reinterpret_cast<float2*>(to + 128 + 2 * t) = make_float2(o[t][1] * d1, o[t][3] * d1);
+          }
+        }
+        __syncthreads();
+        const int h = 4 * x + warp;
+        v[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        vl[x] = 0.0f;
+        vm[x] = joint_m(h);
+#pragma unroll
+        for (int w = 0; w < kCacheWarps; ++w) {
+          const float4 y =
+              *reinterpret_cast<const float4*>(s_o + (w * kCacheJoinHeads + warp) * 128 + c4);
+          v[x].x += y.x;
+          v[x].y += y.y;
+          v[x].z += y.z;
+          v[x].w += y.w;
+          if (s_m[w][h] != -INFINITY) vl[x] += s_l[w][h] * fast_exp2(s_m[w][h] - vm[x]);
+        }
+        if (x == 0) __syncthreads();
+      }
+
+      // ---- join the row's pieces
+      const int piece0 = piece_of(cur.row_at);
+      const int piece1 = piece_of(cur.row_at + cur.row_units - 1);
+      auto leave = [&](float* p) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int h = 4 * x + warp;
+          *reinterpret_cast<float4*>(p + h * 128 + c4) = v[x];
+          if (lane == 0) {
+            p[1024 + h] = vm[x];
+            p[1032 + h] = vl[x];
+          }
+        }
+      };
+      // whether this CTA is the last of `of` to arrive at a counter, which it then clears;
+      // what the others wrote before they arrived is visible then
+      auto last_at = [&](unsigned int* counter, int of) {
+        __syncthreads();
+        if (tid == 0) {
+          __threadfence();
+          const bool last = atomicAdd(counter, 1u) == (unsigned)of - 1u;
+          if (last) *counter = 0;
+          __threadfence();
+          s_last = last;
+        }
+        __syncthreads();
+        return s_last != 0;
+      };
+      // A part's place: twice its piece, one more for a row's first part that does not open
+      // its piece (another row's last part does).
+      const int odd = begin_of(piece0) != cur.row_at ? 1 : 0;
+      auto place_of = [&](int p) { return 2 * p + (p == piece0 ? odd : 0); };
+      // `count` <= 32 partial results in order: the s-th at place(s)
+      auto join = [&](const float* base, auto place, int count) {
+        constexpr int kBatch = 8;
+        float w[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {  // a lane per source: its maximum and sum
+          float pm = -INFINITY, pl = 0.0f;
+          if (lane < count) {
+            const float* p = base + (long long)place(lane) * kCachePartFloats + 4 * x + warp;
+            pm = __ldcg(p + 1024);
+            pl = __ldcg(p + 1032);
+          }
+          float m = pm;
+#pragma unroll
+          for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+          w[x] = pm == -INFINITY ? 0.0f : fast_exp2(pm - m);
+          float l = pl * w[x];
+#pragma unroll
+          for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+          vm[x] = m;
+          vl[x] = l;
+          v[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        for (int s0 = 0; s0 < count; s0 += kBatch) {
+          float4 y[kBatch][2];
+#pragma unroll
+          for (int s = 0; s < kBatch; ++s)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              y[s][x] = s0 + s < count
+                            ? __ldcg(reinterpret_cast<const float4*>(
+                                  base + (long long)place(s0 + s) * kCachePartFloats +
+                                  (4 * x + warp) * 128 + c4))
+                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int s = 0; s < kBatch; ++s)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float c = __shfl_sync(0xffffffffu, w[x], (s0 + s) & 31);
+              v[x].x = fmaf(y[s][x].x, c, v[x].x);
+              v[x].y = fmaf(y[s][x].y, c, v[x].y);
+              v[x].z = fmaf(y[s][x].z, c, v[x].z);
+              v[x].w = fmaf(y[s][x].w, c, v[x].w);
+            }
+        }
+      };
+      const int sharers = piece1 - piece0 + 1;
+      bool finish = true;
+      if (sharers > 1) {
+        leave(a.part + (long long)place_of(cur.piece) * kCachePartFloats);
+        unsigned int* counter = a.counters + kCacheRowCounters + place_of(piece0);
+        if (sharers <= 2 * kCacheFan) {
+          finish = last_at(counter, sharers);
+          if (finish) join(a.part, [&](int s) { return place_of(piece0 + s); }, sharers);
+        } else {
+          const int group = (cur.piece - piece0) / kCacheFan, lead = piece0 + group * kCacheFan;
+          const int groups = (sharers + kCacheFan - 1) / kCacheFan;
+          const int count = min(kCacheFan, piece1 + 1 - lead);
+          float* wide = a.part + (long long)2 * a.pieces * kCachePartFloats;
+          // 16 pieces hold the leads of two rows at most: one's last group, another's first
+          auto group_place = [&](int s) {
+            return 2 * ((piece0 + s * kCacheFan) / kCacheFan) + (s == 0 ? 1 : 0);
+          };
+          finish = last_at(a.counters + place_of(lead), count);
+          if (finish) {
+            join(a.part, [&](int s) { return place_of(lead + s); }, count);
+            leave(wide + (long long)group_place(group) * kCachePartFloats);
+            finish = last_at(counter, groups);
+            // (more than 512 pieces in a row: 32 groups at a time)
+            if (finish) {
+              if (groups <= 32) {
+                join(wide, group_place, groups);
+              } else {
+                float4 av[2];
+                float am[2], al[2];
+                for (int s0 = 0; s0 < groups; s0 += 32) {
+                  join(wide, [&](int s) { return group_place(s0 + s); }, min(32, groups - s0));
+#pragma unroll
+                  for (int x = 0; x < 2; ++x) {
+                    if (s0 > 0) {
+                      const float m = fmaxf(am[x], vm[x]);
+                      const float ca = am[x] == -INFINITY ? 0.0f : fast_exp2(am[x] - m);
+                      const float cv = vm[x] == -INFINITY ? 0.0f : fast_exp2(vm[x] - m);
+                      v[x].x = av[x].x * ca + v[x].x * cv;
+                      v[x].y = av[x].y * ca + v[x].y * cv;
+                      v[x].z = av[x].z * ca + v[x].z * cv;
+                      v[x].w = av[x].w * ca + v[x].w * cv;
+                      vl[x] = al[x] * ca + vl[x] * cv;
+                      vm[x] = m;
+                    }
+                    av[x] = v[x];
+                    am[x] = vm[x];
+                    al[x] = vl[x];
+                  }
+                }
+              }
+            }
           }
         }
       }
-      // scores in log2 units; tokens past the sequence's end are left out
-      float top0 = -INFINITY, top1 = -INFINITY;
+      if (finish) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const bool in = t * 16 + r * 8 + g < ok;
-          s[t][2 * r] = in ? s[t][2 * r] * f0 : -INFINITY;
-          s[t][2 * r + 1] = in ? s[t][2 * r + 1] * f1 : -INFINITY;
-          top0 = fmaxf(top0, s[t][2 * r]);
-          top1 = fmaxf(top1, s[t][2 * r + 1]);
-        }
-      if (__any_sync(0xffffffffu, top0 > m0 + 10.0f || top1 > m1 + 10.0f)) {
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) {
-          top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, x));
-          top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, x));
-        }
-        const float n0 = top0 > m0 + 10.0f ? top0 - 4.0f : m0;
-        const float n1 = top1 > m1 + 10.0f ? top1 - 4.0f : m1;
-        const float c0 = n0 > m0 ? fast_exp2(m0 - n0) : 1.0f;
-        const float c1 = n1 > m1 ? fast_exp2(m1 - n1) : 1.0f;
-        m0 = n0;
-        m1 = n1;
-        l0 *= c0;
-        l1 *= c1;
-        if (WEIGHT) {
-          mass0 *= c0;
-          mass1 *= c1;
-        }
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          o[t][0] *= c0;
-          o[t][1] *= c1;
-          o[t][2] *= c0;
-          o[t][3] *= c1;
+        for (int x = 0; x < 2; ++x) {
+          const int h = 4 * x + warp;
+          if (h >= heads) continue;
+          const float l = vl[x], r = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+          uint2 w;
+          w.x = pack_bf16x2(v[x].x * r, v[x].y * r);
+          w.y = pack_bf16x2(v[x].z * r, v[x].w * r);
+          reinterpret_cast<uint2*>(a.out + (head0 + h) * 128)[lane] = w;
+          if (lane == 0) {
+            const float lse = l == 0.0f ? VSA_LSE_EMPTY : vm[x] + log2f(l);
+            if (a.lse != nullptr) a.lse[head0 + h] = lse;
+            if (WEIGHT) a.lse_ws[head0 + h] = lse;
+          }
         }
       }
-      const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
-      float acc[8][4] = {};
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const float p0 = fast_exp2(s[t][0] - z0), p1 = fast_exp2(s[t][1] - z1);
-        const float p2 = fast_exp2(s[t][2] - z0), p3 = fast_exp2(s[t][3] - z1);
-        l0 += p0 + p2;
-        l1 += p1 + p3;
-        if (WEIGHT) {
-          mass0 += p0 + p2;
-          mass1 += p1 + p3;
-        }
-        const uint32_t b0 = transpose_8x8(pack_f16x2(p0, p1));
-        const uint32_t b1 = transpose_8x8(pack_f16x2(p2, p3));
-        // tokens 2 i4, 2 i4 + 1, and 8 further; columns 16 g .. 16 g + 15
-        uint32_t w[4][4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int r = t * 16 + 2 * i4 + (x & 1) + 8 * (x >> 1);
-          const uint4 y = *reinterpret_cast<const uint4*>(vt + r * 128 + ((g ^ (i4 << 1)) << 4));
-          w[x][0] = y.x;
-          w[x][1] = y.y;
-          w[x][2] = y.z;
-          w[x][3] = y.w;
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_f16x2(__byte_perm(w[0][x], w[1][x], 0x5140), a0, a1);
-          e4m3x4_to_f16x2(__byte_perm(w[2][x], w[3][x], 0x5140), a2, a3);
-          mma_f16(acc[2 * x], a0, a1, a2, a3, b0, b1);
-          e4m3x4_to_f16x2(__byte_perm(w[0][x], w[1][x], 0x7362), a0, a1);
-          e4m3x4_to_f16x2(__byte_perm(w[2][x], w[3][x], 0x7362), a2, a3);
-          mma_f16(acc[2 * x + 1], a0, a1, a2, a3, b0, b1);
+      // the last chunk of the group adds each block's share of the weights
+      if (WEIGHT && finish && last_at(a.counters + kCacheChunkCounters + bh, a.chunks)) {
+        float* weight = a.weight + bh * a.max_blocks;
+        const uint32_t* bits = s_bits[buf];
+        for (int j = tid; j < a.max_blocks; j += kThreads) {
+          float w = a.keep == 0.0f ? 0.0f : a.keep * weight[j];
+          bool on = j < cur.held && (a.idx == nullptr || (bits[j >> 5] >> (j & 31) & 1u));
+          if (on) {
+            const int page = table[j];
+            on = page >= 0 && page < a.pages;
+          }
+          if (on) {
+            float share = 0.0f;
+            const float2* ms = a.mass + (bh * a.max_blocks + j) * a.chunks * 8;
+            for (int h = 0; h < a.group; ++h) {
+              const float2 y = __ldcg(ms + h);
+              const float z = __ldcg(a.lse_ws + bh * a.group + h);
+              if (y.x != 0.0f) share = fmaf(y.x, exp2f(y.y - z), share);
+            }
+            w += share;
+          }
+          weight[j] = w;
         }
       }
-      const float vs = s_vs[entry];
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) o[t][x] = fmaf(acc[t][x], vs, o[t][x]);
     }
-    if (WEIGHT && half == kHalves - 1) {
-      // the block's weight under the running maximum, per head
-#pragma unroll
-      for (int x = 4; x < 32; x <<= 1) {
-        mass0 += __shfl_xor_sync(0xffffffffu, mass0, x);
-        mass1 += __shfl_xor_sync(0xffffffffu, mass1, x);
-      }
-      if (g == 0) {
-        float4* to = reinterpret_cast<float4*>(
-            a.mass + ((bh * a.max_blocks + s_blk[entry]) * a.chunks + chunk) * 8 + 2 * i4);
-        *to = make_float4(mass0, m0, mass1, m1);
-      }
-      mass0 = mass1 = 0.0f;
-    }
-    __syncwarp();
-  }
-
-  // join the warps
-#pragma unroll
-  for (int x = 4; x < 32; x <<= 1) {
-    l0 += __shfl_xor_sync(0xffffffffu, l0, x);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, x);
-  }
-  if (g == 0) {
-    s_m[warp][2 * i4] = m0;
-    s_m[warp][2 * i4 + 1] = m1;
-    s_l[warp][2 * i4] = l0;
-    s_l[warp][2 * i4 + 1] = l1;
+    cur = nxt;
+    buf ^= 1;
+    n_cur = n_nxt;
+    more = follows;
   }
   cp_async_wait<0>();
-  __syncthreads();
-  float* s_o = reinterpret_cast<float*>(s_ring);  // [warp][8][128]
-  auto joint_m = [&](int h) {
-    float m = s_m[0][h];
-#pragma unroll
-    for (int w = 1; w < kCacheWarps; ++w) m = fmaxf(m, s_m[w][h]);
-    return m;
-  };
-  {
-    const float t0 = joint_m(2 * i4), t1 = joint_m(2 * i4 + 1);
-    const float c0 = m0 == -INFINITY ? 0.0f : fast_exp2(m0 - t0);
-    const float c1 = m1 == -INFINITY ? 0.0f : fast_exp2(m1 - t1);
-    float* to = s_o + warp * 1024;
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      *reinterpret_cast<float2*>(to + (2 * i4) * 128 + 16 * g + 2 * t) =
-          make_float2(o[t][0] * c0, o[t][2] * c0);
-      *reinterpret_cast<float2*>(to + (2 * i4 + 1) * 128 + 16 * g + 2 * t) =
-          make_float2(o[t][1] * c1, o[t][3] * c1);
-    }
-  }
-  __syncthreads();
-  const long long bc = bh * a.chunks + chunk;
-  // thread: head h, columns c4 .. c4+3
-  auto finish = [&](int h, int c4, float4 v, float m, float l) {
-    if (h >= heads) return;
-    const float r = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-    uint2 w;
-    w.x = pack_bf16x2(v.x * r, v.y * r);
-    w.y = pack_bf16x2(v.z * r, v.w * r);
-    reinterpret_cast<uint2*>(a.out + (head0 + h) * 128)[c4 >> 2] = w;
-    if (c4 == 0) {
-      const float lse = l == 0.0f ? VSA_LSE_EMPTY : m + log2f(l);
-      if (a.lse != nullptr) a.lse[head0 + h] = lse;
-      if (WEIGHT) a.lse_ws[head0 + h] = lse;
-    }
-  };
-  for (int e = tid; e < 256; e += kThreads) {
-    const int h = e >> 5, c4 = (e & 31) * 4;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float l = 0.0f;
-    const float m = joint_m(h);
-#pragma unroll
-    for (int w = 0; w < kCacheWarps; ++w) {
-      const float4 y = *reinterpret_cast<const float4*>(s_o + w * 1024 + h * 128 + c4);
-      v.x += y.x;
-      v.y += y.y;
-      v.z += y.z;
-      v.w += y.w;
-      if (s_m[w][h] != -INFINITY) l += s_l[w][h] * fast_exp2(s_m[w][h] - m);
-    }
-    if (splits == 1) {
-      finish(h, c4, v, m, l);
-    } else {
-      float* p = a.part + (bc * a.splits + split) * kCachePartFloats;
-      *reinterpret_cast<float4*>(p + h * 128 + c4) = v;
-      if (c4 == 0) {
-        p[1024 + h] = m;
-        p[1032 + h] = l;
-      }
-    }
-  }
-  if (splits > 1) {
-    // the last of the row's splits to arrive joins them, in their order
-    __threadfence();
-    __syncthreads();
-    unsigned int* counter = a.counters + bh * (a.chunks + 1) + chunk;
-    if (tid == 0) {
-      const bool last = atomicAdd(counter, 1u) == (unsigned)splits - 1u;
-      if (last) *counter = 0;
-      s_last = last;
-    }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    for (int e = tid; e < 256; e += kThreads) {
-      const int h = e >> 5, c4 = (e & 31) * 4;
-      const float* p = a.part + bc * a.splits * kCachePartFloats;
-      float m = -INFINITY;
-      for (int s = 0; s < splits; ++s) m = fmaxf(m, __ldcg(p + s * kCachePartFloats + 1024 + h));
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      float l = 0.0f;
-      for (int s = 0; s < splits; ++s) {
-        const float* ps = p + s * kCachePartFloats;
-        const float ms = __ldcg(ps + 1024 + h);
-        if (ms == -INFINITY) continue;
-        const float c = fast_exp2(ms - m);
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(ps + h * 128 + c4));
-        v.x = fmaf(y.x, c, v.x);
-        v.y = fmaf(y.y, c, v.y);
-        v.z = fmaf(y.z, c, v.z);
-        v.w = fmaf(y.w, c, v.w);
-        l = fmaf(__ldcg(ps + 1032 + h), c, l);
-      }
-      finish(h, c4, v, m, l);
-    }
-  }
-  if (WEIGHT) {
-    // the last chunk of the group adds each block's share of the weights
-    __threadfence();
-    __syncthreads();
-    if (a.chunks > 1) {
-      unsigned int* counter = a.counters + bh * (a.chunks + 1) + a.chunks;
-      if (tid == 0) {
-        const bool last = atomicAdd(counter, 1u) == (unsigned)a.chunks - 1u;
-        if (last) *counter = 0;
-        s_last = last;
-      }
-      __syncthreads();
-      if (!s_last) return;
-      __threadfence();
-    }
-    float* weight = a.weight + bh * a.max_blocks;
-    for (int j = tid; j < a.max_blocks; j += kThreads) {
-      float w = a.keep == 0.0f ? 0.0f : a.keep * weight[j];
-      bool on = j < held && (a.idx == nullptr || (s_bits[j >> 5] >> (j & 31) & 1u));
-      if (on) {
-        const int page = table[j];
-        on = page >= 0 && page < a.pages;
-      }
-      if (on) {
-        float share = 0.0f;
-        const float2* ms = a.mass + (bh * a.max_blocks + j) * a.chunks * 8;
-        for (int h = 0; h < a.group; ++h) {
-          const float2 y = __ldcg(ms + h);
-          const float z = __ldcg(a.lse_ws + bh * a.group + h);
-          if (y.x != 0.0f) share = fmaf(y.x, exp2f(y.y - z), share);
-        }
-        w += share;
-      }
-      weight[j] = w;
-    }
+  // the last CTA to end clears the queue
+  if (late > 0 && tid == 0 && atomicAdd(a.counters + kCacheQueue + 1, 1u) == gridDim.x - 1) {
+    a.counters[kCacheQueue] = 0;
+    a.counters[kCacheQueue + 1] = 0;
   }
 }
 

@@ -72,26 +72,19 @@ vsa_status launch_select(const SelectArgs& a, long long ctas, int dev, int slot,
 }
 
 template <int BLOCK, bool WEIGHT>
-vsa_status launch_cache_fwd(const CacheFwdArgs& a, long long ctas, int dev, cudaStream_t s) {
+vsa_status launch_cache_fwd(const CacheFwdArgs& a, int dev, cudaStream_t s) {
   auto kern = cache_fwd_kernel<BLOCK, WEIGHT>;
   const vsa_status st =
       smem_limit(kern, kCacheSmem, dev, kAttrFwd + (BLOCK == 128 ? 1 : 0) + (WEIGHT ? 2 : 0));
   if (st != VSA_OK) return st;
-  kern<<<(unsigned)ctas, kCacheWarps * 32, kCacheSmem, s>>>(a);
+  // one wave, two units a CTA at least; a multiple of the rows where there are fewer of
+  // them, so that rows of one length end where pieces do
+  const int n_max = a.idx != nullptr && a.max_sel < a.max_blocks ? a.max_sel : a.max_blocks;
+  const long long most = (long long)a.rows * n_max / 2;
+  int grid = most < 1 ? 1 : (most < kCacheGrid ? (int)most : kCacheGrid);
+  if (a.rows <= grid / 8) grid -= grid % a.rows;
+  kern<<<grid, kCacheWarps * 32, kCacheSmem, s>>>(a);
   return launched(1);
-}
-
-// Splits of a row's blocks: enough CTAs for about kCacheWaves rounds of two per SM, so
-// that rows of different lengths even out, but no more than give a split kCacheMinBlocks
-// blocks, and no fewer than keep a split's list within kCacheList.
-constexpr int kSms = 152, kCacheWaves = 3;
-int cache_splits(long long rows, int n_max) {
-  const long long want = ((long long)kSms * 2 * kCacheWaves + rows - 1) / (rows > 0 ? rows : 1);
-  const long long most = (n_max + kCacheMinBlocks - 1) / kCacheMinBlocks;
-  const long long least = (n_max + kCacheList - 1) / kCacheList;
-  long long s = want < most ? want : most;
-  s = s > least ? s : least;
-  return (int)(s < 1 ? 1 : s);
 }
 
 // Workspace: counters (at one place whatever the shape, so that a workspace may serve calls
@@ -99,17 +92,18 @@ int cache_splits(long long rows, int n_max) {
 constexpr long long kCacheCounters = 65536;
 struct CacheLayout {
   size_t part, lse, mass, total;
-  int chunks, splits;
+  int chunks, pieces;
 };
 CacheLayout cache_layout(long long B, long long Hq, long long Hkv, long long max_blocks,
                          bool weight) {
   auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
   CacheLayout l;
   l.chunks = (int)((Hq / Hkv + 7) / 8);
-  const long long rows = B * Hkv * l.chunks;
-  l.splits = cache_splits(rows, (int)max_blocks);
   l.part = (size_t)kCacheCounters * sizeof(unsigned int);
-  l.lse = l.part + up((size_t)(rows * l.splits) * kCachePartFloats * sizeof(float));
+  // pieces of the unit sequence: one a CTA, two units or more each, and the late ones
+  const long long most = B * Hkv * l.chunks * (max_blocks > 0 ? max_blocks : 1);
+  l.pieces = (int)(most < kCacheGrid ? most : kCacheGrid + kCacheLate);
+  l.lse = l.part + up((size_t)(2 * l.pieces + l.pieces / 8 + 2) * kCachePartFloats * sizeof(float));
   l.mass = l.lse + (weight ? up((size_t)(B * Hq) * sizeof(float)) : 0);
   l.total = l.mass +
             (weight ? (size_t)(B * Hkv * max_blocks * l.chunks) * 8 * sizeof(float2) : 0);
@@ -371,22 +365,19 @@ vsa_status vsa_fwd_cache(const vsa_bf16* q, const uint8_t* k_cache, const uint8_
   a.Hkv = Hkv;
   a.group = Hq / Hkv;
   a.chunks = l.chunks;
-  // a listed call may need fewer splits than the table's width allows for
-  const int n_max = idx && max_sel < max_blocks ? max_sel : max_blocks;
-  a.splits = cache_splits((long long)B * Hkv * l.chunks, n_max);
+  a.rows = (int)((long long)B * Hkv * l.chunks);
+  a.pieces = l.pieces;
   a.pages = pages;
   a.max_blocks = max_blocks;
   a.max_sel = max_sel;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.keep = keep;
-  const long long ctas = (long long)B * Hkv * l.chunks * a.splits;
-  if (ctas > INT_MAX) return VSA_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (weight)
-    return block == 64 ? launch_cache_fwd<64, true>(a, ctas, dev, s)
-                       : launch_cache_fwd<128, true>(a, ctas, dev, s);
-  return block == 64 ? launch_cache_fwd<64, false>(a, ctas, dev, s)
-                     : launch_cache_fwd<128, false>(a, ctas, dev, s);
+    return block == 64 ? launch_cache_fwd<64, true>(a, dev, s)
+                       : launch_cache_fwd<128, true>(a, dev, s);
+  return block == 64 ? launch_cache_fwd<64, false>(a, dev, s)
+                     : launch_cache_fwd<128, false>(a, dev, s);
 }
 
 vsa_status vsa_cache_evict(const float* weight, const int32_t* table, const int32_t* lens, int B,

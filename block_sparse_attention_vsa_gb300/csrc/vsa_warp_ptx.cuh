@@ -18,6 +18,12 @@ __device__ __forceinline__ void cp_async16(uint32_t dst_smem, const void* src, u
                "l"(static_cast<uint64_t>(__cvta_generic_to_global(src))), "r"(n_src)
                : "memory");
 }
+// 4 bytes global -> shared, asynchronously.
+__device__ __forceinline__ void cp_async4(uint32_t dst_smem, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst_smem),
+               "l"(static_cast<uint64_t>(__cvta_generic_to_global(src)))
+               : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
