@@ -11,6 +11,7 @@
 // tighter bound, then fp64, in which the products of bf16 values are exact).
 #pragma once
 
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include "vsa_warp_ptx.cuh"
@@ -100,6 +101,35 @@ struct KthScratch {
   int digit, rest;
 };
 
+// Which of 256 counted digits, from the largest down, holds the rest-th key, and which of
+// its keys that is: s.digit and s.rest.  One warp.
+__device__ __forceinline__ void digit_of(KthScratch& s, int rest, int lane) {
+  // lane l holds digits 255-8l down to 248-8l
+  unsigned int h[8], sum = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    h[e] = s.hist[255 - 8 * lane - e];
+    sum += h[e];
+  }
+  unsigned int upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  unsigned int before = upto - sum;
+  if (before < (unsigned)rest && upto >= (unsigned)rest) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (before < (unsigned)rest && before + h[e] >= (unsigned)rest) {
+        s.digit = 255 - 8 * lane - e;
+        s.rest = rest - (int)before;
+      }
+      before += h[e];
+    }
+  }
+}
+
 // The k-th largest of keys[0..n) (1 <= k <= n) and how many keys are larger: a radix
 // descent, 8 bits a pass.  Every thread of the CTA calls it and gets the same answer.
 template <typename K>
@@ -114,32 +144,7 @@ __device__ void kth_largest(const K* keys, int n, int k, KthScratch& s, K* thr, 
       if ((key & mask) == prefix) atomicAdd(&s.hist[(unsigned)(key >> shift) & 255u], 1u);
     }
     __syncthreads();
-    if (threadIdx.x < 32) {
-      // lane l holds digits 255-8l down to 248-8l
-      unsigned int h[8], sum = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        h[e] = s.hist[255 - 8 * (int)threadIdx.x - e];
-        sum += h[e];
-      }
-      unsigned int upto = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned int y = __shfl_up_sync(0xffffffffu, upto, o);
-        if ((int)threadIdx.x >= o) upto += y;
-      }
-      unsigned int before = upto - sum;
-      if (before < (unsigned)rest && upto >= (unsigned)rest) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (before < (unsigned)rest && before + h[e] >= (unsigned)rest) {
-            s.digit = 255 - 8 * (int)threadIdx.x - e;
-            s.rest = rest - (int)before;
-          }
-          before += h[e];
-        }
-      }
-    }
+    if (threadIdx.x < 32) digit_of(s, rest, threadIdx.x);
     __syncthreads();
     prefix |= (K)s.digit << shift;
     mask |= (K)255 << shift;
@@ -239,10 +244,57 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) {
 template <int NREG>
 __device__ __forceinline__ int count_ge(const uint32_t (&key)[NREG], uint16_t thr) {
   const __nv_bfloat162 t = as_bf162(bf16_pair(thr));
-  __nv_bfloat162 c = as_bf162(0);  // at most NREG <= 32 per half: exact
+  __nv_bfloat162 c = as_bf162(0), d = as_bf162(0);  // at most 16 each per half: exact
 #pragma unroll
-  for (int j = 0; j < NREG; ++j) c = __hadd2(c, __hge2(as_bf162(key[j]), t));
+  for (int j = 0; j < NREG; j += 2) {
+    c = __hadd2(c, __hge2(as_bf162(key[j]), t));
+    d = __hadd2(d, __hge2(as_bf162(key[j + 1]), t));
+  }
+  c = __hadd2(c, d);
   return __reduce_add_sync(0xffffffffu, (int)(__low2float(c) + __high2float(c)));
+}
+
+// Bit i of x to bit 2 i.
+__device__ __forceinline__ uint32_t spread16(uint32_t x) {
+  x = (x | x << 8) & 0x00ff00ffu;
+  x = (x | x << 4) & 0x0f0f0f0fu;
+  x = (x | x << 2) & 0x33333333u;
+  return (x | x << 1) & 0x55555555u;
+}
+
+// A lane's 2*NREG flags, ascending.
+template <int NREG>
+struct LaneSet {
+  static constexpr int kWords = (NREG + 15) / 16;
+  uint32_t w[kWords];
+  // from masks of pairs: bit j of the low half the even element of pair j, of the high
+  // half the odd one (16 pairs a word)
+  __device__ __forceinline__ void from_pairs(const uint32_t (&m)[kWords]) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = spread16(m[i] & 0xffffu) | spread16(m[i] >> 16) << 1;
+  }
+  __device__ __forceinline__ int count() const {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) n += __popc(w[i]);
+    return n;
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      for (uint32_t r = w[i]; r != 0; r &= r - 1) f(32 * i + __ffs(r) - 1, i, r & (0u - r));
+  }
+};
+
+__device__ __forceinline__ int warp_exclusive(int v, int lane) {
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x - v;
 }
 
 // One CTA: 32 query-block rows of one head against all nk <= 64*NREG key blocks.
@@ -251,13 +303,17 @@ __device__ __forceinline__ int count_ge(const uint32_t (&key)[NREG], uint16_t th
 //      fit where fp32 would not; the rounding only widens the band that is scored again).
 //      Operands are read 16 bytes a thread with the contraction index permuted the same
 //      way on both sides, so no shuffle or transposition is needed.
-//   2. a warp per row: 64*NREG keys in NREG registers of pairs; the k-th largest key by
-//      bisection over the 16-bit order; blocks surely above it are in, the others within
-//      the error bound are scored again.
+//   2. a warp per row, a lane with 2*NREG consecutive keys in NREG registers of pairs.
+//      The border is bracketed in the 16-bit order of the keys by counting, two keys an
+//      instruction: outwards from the last row's border, then by interpolation and halving
+//      in turn, until at most 4 keys lie between the brackets' ends.  Blocks surely above
+//      the bracket are in; those that the error bound leaves open are scored again.
 template <int NREG>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kSelThreads, NREG <= 24 ? 2 : 1)
+    select_kernel(const SelectArgs a) {
   extern __shared__ __align__(16) uint16_t s_key[];  // [32][stride]
   constexpr int kStride = select_stride(NREG);
+  __shared__ __align__(16) uint16_t s_q[kSelRows][128];
   __shared__ float s_q1[kSelRows];
   __shared__ uint32_t s_kmax[kSelThreads / 32];
   __shared__ unsigned int s_slow;
@@ -290,6 +346,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
       float s = 0.0f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        reinterpret_cast<uint4*>(s_q[g + 8 * r])[i4 + 4 * j] = qa[r][j];
         const uint32_t u[4] = {qa[r][j].x, qa[r][j].y, qa[r][j].z, qa[r][j].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) s += fabsf(bf16_lo(u[e])) + fabsf(bf16_hi(u[e]));
@@ -353,23 +410,31 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
   }
   __syncthreads();
   // what may not be chosen by any row
-  for (int e = tid; e < NREG * 64; e += kSelThreads)
-    if (e >= a.nk || (a.sizes != nullptr && a.sizes[e] <= 0))
+  int n_fair = 0;
+#pragma unroll
+  for (int e0 = 0; e0 < NREG * 64; e0 += kSelThreads) {
+    const int e = e0 + tid;
+    const bool fair = e < a.nk && (a.sizes == nullptr || a.sizes[e] > 0);
+    if (!fair)
       for (int r = 0; r < kSelRows; ++r) s_key[r * kStride + e] = 0x7fff;
-  __syncthreads();
+    n_fair += __syncthreads_count(fair);
+  }
 
   uint32_t kmax_bits = 0;
 #pragma unroll
   for (int w = 0; w < kSelThreads / 32; ++w) kmax_bits = max(kmax_bits, s_kmax[w]);
   const float kmax = __uint_as_float(kmax_bits);
-  const unsigned int lt = (1u << lane) - 1u;
+  constexpr uint32_t kLowest = 0x007fu, kHighest = 0xff80u;  // order of -inf and +inf
+  // where the border is looked for first: this far below the bound for values like normal
+  // ones, and at the last row's after that
+  uint32_t guess = 0, stride0 = 64;
 
   for (int r = warp; r < kSelRows; r += kSelThreads / 32) {
     const int row = row0 + r;
     if (row >= a.nq) break;
     if ((s_slow >> r) & 1u) continue;
-    const float q1 = s_q1[r], eps = kDotBound * q1 * kmax + kTiny;
-    if (!(q1 * kmax < kFinite)) {
+    const float q1 = s_q1[r], bound = q1 * kmax, eps = kDotBound * bound + kTiny;
+    if (!(bound < kFinite)) {
       if (lane == 0) atomicOr(&s_slow, 1u << r);
       continue;
     }
@@ -380,174 +445,189 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
     for (int e = max(0, d - a.n_near + 1) + lane; e < min(a.nk, d + a.n_near); e += 32)
       if (select_allowed(a, e, d)) krow[e] = 0x7f80;
     __syncwarp();
+    const int base = lane * 2 * NREG;
     uint32_t key[NREG];
 #pragma unroll
-    for (int j = 0; j < NREG; ++j) {
-      key[j] = reinterpret_cast<const uint32_t*>(krow)[j * 32 + lane];
-      if (a.causal) {
-        const int e = 2 * (j * 32 + lane);
-        if (e > d) key[j] |= 0x00007fffu;
-        if (e + 1 > d) key[j] |= 0x7fff0000u;
-      }
+    for (int j = 0; j < NREG; j += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(krow + base + 2 * j);
+      key[j] = v.x;
+      key[j + 1] = v.y;
+      key[j + 2] = v.z;
+      key[j + 3] = v.w;
     }
-    const int n_ok = count_ge<NREG>(key, 0xff80);  // all but the NaN keys
-    const int k = min(a.topk, n_ok);
-    uint32_t in_lo = 0, in_hi = 0, cand_lo = 0, cand_hi = 0;
-    int by_index = 0;  // candidates to take from the lowest index on
-    bool slow = false;
-    if (n_ok <= a.topk) {
+    int n_ok = n_fair;
+    if (a.causal) {
 #pragma unroll
       for (int j = 0; j < NREG; ++j) {
-        in_lo |= (uint32_t)((key[j] & 0x7fffu) <= 0x7f80u) << j;
-        in_hi |= (uint32_t)((key[j] >> 16 & 0x7fffu) <= 0x7f80u) << j;
+        if (base + 2 * j > d) key[j] |= 0x00007fffu;
+        if (base + 2 * j + 1 > d) key[j] |= 0x7fff0000u;
       }
+      n_ok = count_ge<NREG>(key, bf16_unorder(kLowest));
+    }
+    const int k = min(a.topk, n_ok);
+    uint32_t in_thr, cand_thr;  // in: key > in_thr, candidate: the others >= cand_thr
+    bool ties = false;          // candidates are equal: the lowest indices
+    if (n_ok <= a.topk) {
+      in_thr = cand_thr = bf16_unorder(kLowest);  // all, as candidates
     } else {
-      // largest t with count(>= t) >= k, over the order of bf16 values
-      uint32_t lo = 0x007fu, hi = 0xff81u;
-      while (hi - lo > 1) {
-        const uint32_t mid = (lo + hi) >> 1;
-        if (count_ge<NREG>(key, bf16_unorder(mid)) >= k) lo = mid; else hi = mid;
-      }
-      const float t = __uint_as_float((uint32_t)bf16_unorder(lo) << 16);
-      uint32_t in_thr, cand_thr;  // in: key > in_thr, candidate: the others >= cand_thr
-      bool ties = true;
-      if (isinf(t)) {
-        in_thr = cand_thr = 0x7f80u;  // more forced blocks than places
-      } else if (q1 == 0.0f || kmax == 0.0f) {
-        in_thr = cand_thr = (uint32_t)bf16_unorder(lo);  // every score is 0
+      uint32_t lo = kLowest, hi = kHighest;  // count(>= lo) >= k > count(>= hi)
+      int c_lo = n_ok, c_hi = 0;
+      if (a.n_first + 2 * a.n_near >= k) c_hi = count_ge<NREG>(key, bf16_unorder(kHighest));
+      if (c_hi >= k) {  // more forced blocks than places
+        in_thr = cand_thr = 0x7f80u;
+        ties = true;
       } else {
-        // bf16 rounding is off by at most 2^-9 of the value; s - bound(s) and s + bound(s)
-        // grow with s, so the true k-th score lies between those of t
-        ties = false;
-        const float c = 0.00196f;
-        const float up = t + c * fabsf(t) + 2.0f * eps, dn = t - c * fabsf(t) - 2.0f * eps;
-        in_thr = __bfloat16_as_ushort(__float2bfloat16_ru(up / (up > 0.0f ? 1.0f - c : 1.0f + c)));
-        cand_thr = __bfloat16_as_ushort(__float2bfloat16_rd(dn / (dn > 0.0f ? 1.0f + c : 1.0f - c)));
+        if (guess == 0) {
+          guess = (__float_as_uint(bound * 0.03125f) >> 16) | 0x8000u;
+          guess = max(guess, 0x8100u);
+        }
+        uint32_t at = guess, step = stride0;
+        bool halve = false;
+        while (hi - lo > 1 && c_lo - c_hi > 4) {
+          const int c = count_ge<NREG>(key, bf16_unorder(at));
+          if (c >= k) {
+            lo = at;
+            c_lo = c;
+          } else {
+            hi = at;
+            c_hi = c;
+          }
+          if (lo == kLowest) {
+            at = hi - lo > step ? hi - step : (lo + hi) >> 1;
+            step *= 4;
+          } else if (hi == kHighest) {
+            at = hi - lo > step ? lo + step : (lo + hi) >> 1;
+            step *= 4;
+          } else if (halve) {
+            at = (lo + hi) >> 1;
+            halve = false;
+          } else {
+            at = lo + (hi - lo) * (uint32_t)(c_lo - k) / (uint32_t)(c_lo - c_hi);
+            halve = true;
+          }
+          at = min(max(at, lo + 1), hi - 1);
+        }
+        guess = lo == kLowest ? 0 : lo;
+        stride0 = 8;
+        const float t = __uint_as_float((uint32_t)bf16_unorder(lo) << 16);
+        const float u = __uint_as_float((uint32_t)bf16_unorder(hi - 1) << 16);
+        if (q1 == 0.0f || kmax == 0.0f) {  // every score is 0
+          in_thr = 0x0000u;
+          cand_thr = 0x8000u;
+          ties = true;
+        } else {
+          // bf16 rounding is off by at most 2^-9 of the value; s - bound(s) and s + bound(s)
+          // grow with s, so the true k-th score lies between those of t and of u
+          const float c = 0.00196f;
+          const float up = u + c * fabsf(u) + 2.0f * eps, dn = t - c * fabsf(t) - 2.0f * eps;
+          in_thr = __bfloat16_as_ushort(
+              __float2bfloat16_ru(up / (up > 0.0f ? 1.0f - c : 1.0f + c)));
+          cand_thr = __bfloat16_as_ushort(
+              __float2bfloat16_rd(dn / (dn > 0.0f ? 1.0f + c : 1.0f - c)));
+          if (hi == kHighest || in_thr == 0x7f80u) in_thr = 0x7f7fu;  // the forced ones
+        }
       }
+    }
+    LaneSet<NREG> in, cand;
+    {
       const __nv_bfloat162 ti = as_bf162(bf16_pair((uint16_t)in_thr));
       const __nv_bfloat162 tc = as_bf162(bf16_pair((uint16_t)cand_thr));
+      uint32_t mi[LaneSet<NREG>::kWords] = {}, mc[LaneSet<NREG>::kWords] = {};
 #pragma unroll
       for (int j = 0; j < NREG; ++j) {
-        const uint32_t gi = __hgt2_mask(as_bf162(key[j]), ti);
-        const uint32_t gc = __hge2_mask(as_bf162(key[j]), tc) & ~gi;
-        in_lo |= (gi & 1u) << j;
-        in_hi |= (gi >> 31) << j;
-        cand_lo |= (gc & 1u) << j;
-        cand_hi |= (gc >> 31) << j;
+        mi[j / 16] |= __hgt2_mask(as_bf162(key[j]), ti) & (0x00010001u << (j & 15));
+        mc[j / 16] |= __hge2_mask(as_bf162(key[j]), tc) & (0x00010001u << (j & 15));
       }
-      const int n_in = __reduce_add_sync(0xffffffffu, __popc(in_lo) + __popc(in_hi));
-      const int n_cand = __reduce_add_sync(0xffffffffu, __popc(cand_lo) + __popc(cand_hi));
-      const int need = k - n_in;
-      if (n_cand == need) {
-        in_lo |= cand_lo;
-        in_hi |= cand_hi;
-        cand_lo = cand_hi = 0;
-      } else if (ties) {
-        by_index = need;
-      } else if (n_cand > 32) {
-        slow = true;
-      } else {
-        // gather the candidates' indices, one per lane
-        int at = 0;
 #pragma unroll
-        for (int j = 0; j < NREG; ++j) {
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            const bool c = ((p ? cand_hi : cand_lo) >> j) & 1u;
-            const unsigned int m = __ballot_sync(0xffffffffu, c);
-            if (c) s_cand[warp][at + __popc(m & lt)] = (uint16_t)(2 * (j * 32 + lane) + p);
-            at += __popc(m);
-          }
-        }
-        __syncwarp();
-        const int mine = lane < n_cand ? s_cand[warp][lane] : 0x7fffffff;
-        const uint2 qw = __ldg(reinterpret_cast<const uint2*>(qh + (long long)row * 128) + lane);
-        const float qf[4] = {bf16_lo(qw.x), bf16_hi(qw.x), bf16_lo(qw.y), bf16_hi(qw.y)};
-        // fp32 sums of 128 exact products: 4 in a lane, 5 levels across lanes
-        float sc = 0.0f;
-        for (int c = 0; c < n_cand; ++c) {
-          const uint2 kw = __ldg(
-              reinterpret_cast<const uint2*>(kh + (long long)s_cand[warp][c] * 128) + lane);
-          float s = qf[0] * bf16_lo(kw.x);
-          s = fmaf(qf[1], bf16_hi(kw.x), s);
-          s = fmaf(qf[2], bf16_lo(kw.y), s);
-          s = fmaf(qf[3], bf16_hi(kw.y), s);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          if (lane == c) sc = s;
-        }
-        int rank = 0;
-        for (int c = 0; c < n_cand; ++c) {
-          const float o = __shfl_sync(0xffffffffu, sc, c);
-          const int oi = __shfl_sync(0xffffffffu, mine, c);
-          rank += o > sc || (o == sc && oi < mine);
-        }
-        bool take = lane < n_cand && rank < need;
-        // 9 roundings of partial sums of at most sum |q||k|
-        const float tight = 2.0f * 9.5f * 5.9604645e-8f * q1 * kmax + kTiny;
-        float worst_in = take ? sc : INFINITY, best_out = lane < n_cand && !take ? sc : -INFINITY;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          worst_in = fminf(worst_in, __shfl_xor_sync(0xffffffffu, worst_in, o));
-          best_out = fmaxf(best_out, __shfl_xor_sync(0xffffffffu, best_out, o));
-        }
-        if (worst_in - best_out <= tight) {
-          double sd = 0.0;
-          for (int c = 0; c < n_cand; ++c) {
-            const uint2 kw = __ldg(
-                reinterpret_cast<const uint2*>(kh + (long long)s_cand[warp][c] * 128) + lane);
-            double s = (double)qf[0] * (double)bf16_lo(kw.x);
-            s = fma((double)qf[1], (double)bf16_hi(kw.x), s);
-            s = fma((double)qf[2], (double)bf16_lo(kw.y), s);
-            s = fma((double)qf[3], (double)bf16_hi(kw.y), s);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (lane == c) sd = s;
-          }
-          rank = 0;
-          for (int c = 0; c < n_cand; ++c) {
-            const double o = __shfl_sync(0xffffffffu, sd, c);
-            const int oi = __shfl_sync(0xffffffffu, mine, c);
-            rank += o > sd || (o == sd && oi < mine);
-          }
-          take = lane < n_cand && rank < need;
-        }
-        cand_lo = cand_hi = 0;
-        unsigned int taken = __ballot_sync(0xffffffffu, take);
-        while (taken != 0) {
-          const int e = s_cand[warp][__ffs(taken) - 1];
-          taken &= taken - 1;
-          if (((e >> 1) & 31) == lane) {
-            if (e & 1) in_hi |= 1u << (e >> 6); else in_lo |= 1u << (e >> 6);
-          }
-        }
-        __syncwarp();
-      }
+      for (int i = 0; i < LaneSet<NREG>::kWords; ++i) mc[i] &= ~mi[i];
+      in.from_pairs(mi);
+      cand.from_pairs(mc);
     }
-    if (slow) {
-      if (lane == 0) atomicOr(&s_slow, 1u << r);
-      continue;
+    const int my_cand = cand.count();
+    const int n_in = __reduce_add_sync(0xffffffffu, in.count());
+    const int n_cand = __reduce_add_sync(0xffffffffu, my_cand);
+    const int need = k - n_in;
+    if (n_cand == need) {
+#pragma unroll
+      for (int i = 0; i < LaneSet<NREG>::kWords; ++i) in.w[i] |= cand.w[i];
+    } else {
+      int at = warp_exclusive(my_cand, lane);
+      if (ties) {
+        cand.each([&](int, int i, uint32_t bit) {
+          if (at < need) in.w[i] |= bit;
+          ++at;
+        });
+      } else if (n_cand > 32) {
+        if (lane == 0) atomicOr(&s_slow, 1u << r);
+        continue;
+      } else {
+        // candidate c in lane c, ascending; scored 4 at a time, 8 lanes and 16 products each
+        const int at0 = at;
+        cand.each([&](int e, int, uint32_t) { s_cand[warp][at++] = (uint16_t)(base + e); });
+        __syncwarp();
+        const uint4* qp = reinterpret_cast<const uint4*>(s_q[r]) + (lane & 7);
+        auto score = [&](int c, auto zero) {
+          using T = decltype(zero);
+          const uint4* kp = reinterpret_cast<const uint4*>(kh + (long long)s_cand[warp][c] * 128) +
+                            (lane & 7);
+          T s = zero;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint4 kw = __ldg(kp + 8 * x), qw = qp[8 * x];
+            const uint32_t ku[4] = {kw.x, kw.y, kw.z, kw.w}, qu[4] = {qw.x, qw.y, qw.z, qw.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              s = fma((T)bf16_lo(qu[y]), (T)bf16_lo(ku[y]), s);
+              s = fma((T)bf16_hi(qu[y]), (T)bf16_hi(ku[y]), s);
+            }
+          }
+#pragma unroll
+          for (int x = 4; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+          return s;
+        };
+        auto rank_of = [&](auto zero) {
+          using T = decltype(zero);
+          T mine = zero;
+          for (int c0 = 0; c0 < n_cand; c0 += 4) {
+            const T s = score(min(c0 + (lane >> 3), n_cand - 1), zero);
+            const T t = __shfl_sync(0xffffffffu, s, (lane & 3) * 8);
+            if (lane >> 2 == c0 >> 2) mine = t;
+          }
+          int rank = 0;
+          for (int c = 0; c < n_cand; ++c) {
+            const T o = __shfl_sync(0xffffffffu, mine, c);
+            rank += o > mine || (o == mine && c < lane);
+          }
+          const bool take = lane < n_cand && rank < need;
+          // the gap at the border
+          T worst = take ? mine : (T)INFINITY, best = lane < n_cand && !take ? mine : (T)-INFINITY;
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) {
+            const T y = __shfl_xor_sync(0xffffffffu, worst, x);
+            worst = y < worst ? y : worst;
+            const T z = __shfl_xor_sync(0xffffffffu, best, x);
+            best = z > best ? z : best;
+          }
+          // 19 roundings of partial sums of at most sum |q||k|
+          const bool sure =
+              sizeof(T) == 8 || worst - best > (T)(2.0f * 19.5f * 5.9604645e-8f * bound + kTiny);
+          return (sure ? 0x100 : 0) | (take ? 1 : 0);
+        };
+        int got = rank_of(0.0f);
+        if (!(got & 0x100)) got = rank_of(0.0);
+        const unsigned int taken = __ballot_sync(0xffffffffu, got & 1);
+        at = at0;
+        cand.each([&](int, int i, uint32_t bit) {
+          if (taken >> at & 1u) in.w[i] |= bit;
+          ++at;
+        });
+        __syncwarp();
+      }
     }
     // ascending indices, -1 behind
     int32_t* out = a.idx + (bh * a.nq + row) * (long long)a.topk;
-    int at = 0, seen = 0;
-#pragma unroll
-    for (int j = 0; j < NREG; ++j) {
-      bool lo = (in_lo >> j) & 1u, hi = (in_hi >> j) & 1u;
-      if (by_index > 0) {
-        const bool cl = (cand_lo >> j) & 1u, ch = (cand_hi >> j) & 1u;
-        const unsigned int ml = __ballot_sync(0xffffffffu, cl), mh = __ballot_sync(0xffffffffu, ch);
-        const int before = seen + __popc(ml & lt) + __popc(mh & lt);
-        lo |= cl && before < by_index;
-        hi |= ch && before + cl < by_index;
-        seen += __popc(ml) + __popc(mh);
-      }
-      const unsigned int ml = __ballot_sync(0xffffffffu, lo), mh = __ballot_sync(0xffffffffu, hi);
-      const int pos = at + __popc(ml & lt) + __popc(mh & lt), e = 2 * (j * 32 + lane);
-      if (lo) out[pos] = e;
-      if (hi) out[pos + lo] = e + 1;
-      at += __popc(ml) + __popc(mh);
-    }
+    int at = warp_exclusive(in.count(), lane);
+    in.each([&](int e, int, uint32_t) { out[at++] = base + e; });
     for (int s = k + lane; s < a.topk; s += 32) out[s] = -1;
     if (lane == 0) a.num[bh * a.nq + row] = k;
   }
@@ -641,27 +721,40 @@ __device__ __forceinline__ uint64_t cache_score64(const uint16_t* q, int group,
   return nan ? 0 : order64(best);
 }
 
-// One CTA per (sequence, key/value head): scores of its n <= 2048 blocks on the tensor
-// cores (16 blocks x 8 query heads a tile, the pages' means gathered through the table),
-// the largest over the heads as an ordered 32-bit key in shared memory, then a radix
-// descent to the k-th; blocks inside the error band of it are scored again in fp64.
+// A cluster of CTAs per (sequence, key/value head), up to 2048 blocks: the CTAs score the
+// blocks between them on the tensor cores (16 blocks x 8 query heads a tile, the pages'
+// means gathered through the table) into the first CTA's shared memory, as ordered 32-bit
+// keys of the largest over the heads; the first CTA chooses.  The k-th key is found from
+// one histogram of 256 even steps of value and a ranking of the step it falls into (where
+// that holds too many, by radix descent); blocks inside the error band of it are scored
+// again in fp64.
 __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSelectArgs a) {
   __shared__ uint32_t s_key[kMaxBlocks];
   __shared__ uint64_t s_key64[kMaxBlocks];
   __shared__ uint16_t s_cand[kMaxBlocks];
   __shared__ KthScratch s_kth;
-  __shared__ uint32_t s_kmax[kSelThreads / 32], s_q1[kSelThreads / 32];
-  __shared__ int s_n_cand;
+  constexpr int kWarps = kSelThreads / 32, kMostCtas = 8;
+  __shared__ uint32_t s_kmax[kMostCtas * kWarps], s_q1[kWarps], s_lo[kWarps], s_hi[kWarps];
+  __shared__ uint32_t s_bad;
+  __shared__ int s_n_cand, s_ok, s_forced;
+  __shared__ uint32_t s_thr;
+  auto cluster = cooperative_groups::this_cluster();
+  const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, i4 = lane & 3;
-  const long long bh = blockIdx.x;
+  const long long bh = blockIdx.x / ctas;
   const int b = (int)(bh / a.Hkv);
-  int len = a.lens[b];
-  len = len < 0 ? 0 : len;
-  const int n = (int)min(((long long)len + a.block - 1) / a.block, (long long)a.max_blocks);
+  const long long len = max(0, a.lens[b]);
+  const int n = (int)min((len + a.block - 1) / a.block, (long long)a.max_blocks);
   const uint16_t* q = a.q + bh * a.group * 128;
   const int32_t* table = a.table + bh * a.max_blocks;
   int32_t* out = a.idx + bh * a.topk;
+  uint32_t* const first_key = cluster.map_shared_rank(s_key, 0);
+  uint32_t* const first_kmax = cluster.map_shared_rank(s_kmax, 0);
+  uint32_t* const first_bad = cluster.map_shared_rank(&s_bad, 0);
+
+  if (tid == 0) s_n_cand = s_ok = s_forced = s_bad = 0;
+  cluster.sync();  // the first CTA runs and has cleared s_bad
 
   auto emit = [&](auto* keys, auto thr, int n_eq, int k) {
     partition_ascending(
@@ -669,11 +762,12 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSe
     for (int s = k + tid; s < a.topk; s += kSelThreads) out[s] = -1;
     if (tid == 0) a.num[bh] = k;
   };
-  if (tid == 0) s_n_cand = 0;
+  auto forced = [&](int e) { return e < a.n_first || e > n - 1 - a.n_near; };
 
   bool bad = false;
   __nv_bfloat162 kmax2 = as_bf162(0);
   float q1max = 0.0f;
+  const int step = ctas * kWarps;
   for (int h0 = 0; h0 < a.group; h0 += 8) {
     uint4 qb[4];
     float q1 = 0.0f;
@@ -690,20 +784,28 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSe
     q1 += __shfl_xor_sync(0xffffffffu, q1, 2);
     q1max = fmaxf(q1max, q1);
     bad |= !(q1 < kFinite);
-    for (int t = warp; t * 16 < n; t += kSelThreads / 32) {
+    const bool c0 = h0 + 2 * i4 < a.group, c1 = h0 + 2 * i4 + 1 < a.group;
+    auto page_of = [&](int t, int r) {
+      const int e = t * 16 + g + 8 * r;
+      return e < n ? __ldg(table + e) : -1;
+    };
+    int page[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) page[r] = page_of(rank * kWarps + warp, r);
+    for (int t = rank * kWarps + warp; t * 16 < n; t += step) {
       float d[4] = {};
       uint4 ka[2][4];
       bool ok[2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int e = t * 16 + g + 8 * r;
-        const int page = e < n ? __ldg(table + e) : -1;
-        ok[r] = page >= 0 && page < a.pages;
+        ok[r] = page[r] >= 0 && page[r] < a.pages;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          ka[r][j] = ok[r] ? __ldg(reinterpret_cast<const uint4*>(a.k_mean + (long long)page * 128) +
+          ka[r][j] = ok[r] ? __ldg(reinterpret_cast<const uint4*>(a.k_mean +
+                                                                  (long long)page[r] * 128) +
                                    i4 + 4 * j)
                            : make_uint4(0, 0, 0, 0);
+        page[r] = page_of(t + step, r);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -717,7 +819,6 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSe
           kmax2 = __hmax2(kmax2, __habs2(as_bf162(ka[r][j].w)));
         }
       }
-      const bool c0 = h0 + 2 * i4 < a.group, c1 = h0 + 2 * i4 + 1 < a.group;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         float x = max_nan(c0 ? d[2 * r] : -INFINITY, c1 ? d[2 * r + 1] : -INFINITY);
@@ -726,8 +827,9 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSe
         const int e = t * 16 + g + 8 * r;
         if (i4 == 0 && e < n) {
           bad |= ok[r] && !(fabsf(x) < kFinite);
-          const uint32_t key = ok[r] ? order32(x) : 0u;
-          s_key[e] = h0 == 0 ? key : max(s_key[e], key);
+          uint32_t key = ok[r] ? order32(x) : 0u;
+          if (h0 > 0) key = max(key, first_key[e]);  // this thread's own, of the heads before
+          first_key[e] = key;
         }
       }
     }
@@ -737,34 +839,24 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSe
     const uint32_t mm = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
     const uint32_t qq = __reduce_max_sync(0xffffffffu, __float_as_uint(q1max));
     if (lane == 0) {
-      s_kmax[warp] = mm;
+      first_kmax[rank * kWarps + warp] = mm;
       s_q1[warp] = qq;
     }
+    if (bad) atomicOr(first_bad, 1u);
   }
-  const bool any_bad = __syncthreads_or(bad);
+  cluster.sync();
+  if (rank != 0) return;
+
   uint32_t km = 0, qm = 0;
+  for (int w = 0; w < ctas * kWarps; ++w) km = max(km, s_kmax[w]);
 #pragma unroll
-  for (int w = 0; w < kSelThreads / 32; ++w) {
-    km = max(km, s_kmax[w]);
-    qm = max(qm, s_q1[w]);
-  }
+  for (int w = 0; w < kWarps; ++w) qm = max(qm, s_q1[w]);
   const float sum_bound = __uint_as_float(qm) * __uint_as_float(km);
   const float eps = kDotBound * sum_bound + kTiny;
-  auto forced = [&](int e) { return e < a.n_first || e > n - 1 - a.n_near; };
-  int n_ok = 0;
-  for (int e0 = 0; e0 < n; e0 += kSelThreads) {
-    const int e = e0 + tid;
-    bool ok = false;
-    if (e < n) {
-      ok = s_key[e] != 0;
-      if (ok && forced(e)) s_key[e] = kForced32;
-    }
-    n_ok += __syncthreads_count(ok);
-  }
 
-  if (any_bad || !(sum_bound < kFinite)) {  // scores that overflow fp32, or are not numbers
-    n_ok = 0;
-    for (int e = warp; e < n; e += kSelThreads / 32) {
+  if (s_bad != 0 || !(sum_bound < kFinite)) {  // scores that overflow fp32, or are not numbers
+    int n_ok = 0;
+    for (int e = warp; e < n; e += kWarps) {
       uint64_t key = 0;
       const int page = __ldg(table + e);
       if (page >= 0 && page < a.pages)
@@ -782,27 +874,115 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSe
     emit(s_key64, thr, n_ok > a.topk ? k - larger : 0, k);
     return;
   }
-  const int k = min(a.topk, n_ok);
+  // mark the forced ones; count, and the least and largest of the others
+  {
+    int ok = 0, sure = 0;
+    uint32_t lo = kForced32, hi = 0;
+    for (int e = tid; e < n; e += kSelThreads) {
+      const uint32_t key = s_key[e];
+      if (key == 0) continue;
+      ++ok;
+      if (forced(e)) {
+        s_key[e] = kForced32;
+        ++sure;
+      } else {
+        lo = min(lo, key);
+        hi = max(hi, key);
+      }
+    }
+    ok = __reduce_add_sync(0xffffffffu, ok);
+    sure = __reduce_add_sync(0xffffffffu, sure);
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+      atomicAdd(&s_ok, ok);
+      atomicAdd(&s_forced, sure);
+      s_lo[warp] = lo;
+      s_hi[warp] = hi;
+    }
+  }
+  s_kth.hist[tid] = 0;
+  __syncthreads();
+  const int n_ok = s_ok, k = min(a.topk, n_ok);
   if (n_ok <= a.topk) {
     emit(s_key, 0u, 0, k);
     return;
   }
+  if (s_forced >= k) {  // more forced blocks than places
+    emit(s_key, kForced32 - 1, 0, k);
+    return;
+  }
+  uint32_t lo_key = kForced32, hi_key = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    lo_key = min(lo_key, s_lo[w]);
+    hi_key = max(hi_key, s_hi[w]);
+  }
+  // 256 even steps of value: the step of a key never falls as the key grows
+  const float low = unorder32(lo_key), span = unorder32(hi_key) - low;
+  const float per = span > 0.0f && span < kFinite ? 255.0f / span : 0.0f;
+  auto step_of = [&](uint32_t key) {
+    return min(255, (int)((unorder32(key) - low) * per));
+  };
+  for (int e = tid; e < n; e += kSelThreads) {
+    const uint32_t key = s_key[e];
+    if (key != 0 && key != kForced32) atomicAdd(&s_kth.hist[step_of(key)], 1u);
+  }
+  __syncthreads();
+  const int rest = k - s_forced;
+  if (warp == 0) digit_of(s_kth, rest, lane);
+  __syncthreads();
+  const int digit = s_kth.digit, within = s_kth.rest, members = (int)s_kth.hist[digit];
   uint32_t thr;
   int larger;
-  kth_largest<uint32_t>(s_key, n, k, s_kth, &thr, &larger);
-  if (thr == kForced32 || qm == 0 || km == 0) {
+  constexpr int kRanked = 128;
+  if (members <= kRanked && per < INFINITY) {
+    for (int e = tid; e < n; e += kSelThreads) {
+      const uint32_t key = s_key[e];
+      if (key != 0 && key != kForced32 && step_of(key) == digit)
+        s_cand[atomicAdd(&s_n_cand, 1)] = (uint16_t)e;
+    }
+    __syncthreads();
+    if (tid < members) {
+      const uint32_t mine = s_key[s_cand[tid]];
+      int gt = 0, ge = 0;
+      for (int o = 0; o < members; ++o) {
+        const uint32_t y = s_key[s_cand[o]];
+        gt += y > mine;
+        ge += y >= mine;
+      }
+      if (gt < within && within <= ge) {
+        s_thr = mine;
+        s_kth.rest = within - gt;
+      }
+    }
+    __syncthreads();
+    thr = s_thr;
+    larger = k - s_kth.rest;
+    if (tid == 0) s_n_cand = 0;
+  } else {
+    kth_largest<uint32_t>(s_key, n, k, s_kth, &thr, &larger);
+  }
+  if (qm == 0 || km == 0) {  // every score is 0
     emit(s_key, thr, k - larger, k);
     return;
   }
   const float t = unorder32(thr);
   const uint32_t hi = order32(__fadd_ru(t, 2.0f * eps)), lo = order32(__fadd_rd(t, -2.0f * eps));
-  int n_in = 0, n_cand = 0;
-  for (int e0 = 0; e0 < n; e0 += kSelThreads) {
-    const uint32_t key = e0 + tid < n ? s_key[e0 + tid] : 0u;
-    n_in += __syncthreads_count(key > hi);
-    n_cand += __syncthreads_count(key >= lo && key <= hi);
+  // above the band in the low half, inside it in the high half
+  unsigned int mine = 0;
+  for (int e = tid; e < n; e += kSelThreads) {
+    const uint32_t key = s_key[e];
+    mine += key > hi ? 1u : (key >= lo ? 0x10000u : 0u);
   }
-  const int need = k - n_in;
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  __syncthreads();
+  if (lane == 0) s_kth.warp_sum[warp] = mine;
+  __syncthreads();
+  unsigned int both = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) both += s_kth.warp_sum[w];
+  const int n_cand = (int)(both >> 16), need = k - (int)(both & 0xffffu);
   if (n_cand == need) {
     emit(s_key, lo - 1, 0, k);
     return;
@@ -810,7 +990,7 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSe
   for (int e = tid; e < n; e += kSelThreads)
     if (s_key[e] >= lo && s_key[e] <= hi) s_cand[atomicAdd(&s_n_cand, 1)] = (uint16_t)e;
   __syncthreads();
-  for (int c = warp; c < n_cand; c += kSelThreads / 32) {
+  for (int c = warp; c < n_cand; c += kWarps) {
     const uint64_t key = cache_score64(
         q, a.group, a.k_mean + (long long)__ldg(table + s_cand[c]) * 128, lane);
     if (lane == 0) s_key64[c] = key;
@@ -819,12 +999,12 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSe
   for (int e = tid; e < n; e += kSelThreads) s_key[e] = s_key[e] > hi ? 2u : 0u;
   __syncthreads();
   for (int c = tid; c < n_cand; c += kSelThreads) {
-    const uint64_t mine = s_key64[c];
+    const uint64_t own = s_key64[c];
     const int e = s_cand[c];
-    int rank = 0;
+    int place = 0;
     for (int o = 0; o < n_cand; ++o)
-      rank += s_key64[o] > mine || (s_key64[o] == mine && s_cand[o] < e);
-    if (rank < need) s_key[e] = 2u;
+      place += s_key64[o] > own || (s_key64[o] == own && s_cand[o] < e);
+    if (place < need) s_key[e] = 2u;
   }
   __syncthreads();
   emit(s_key, 1u, 0, k);

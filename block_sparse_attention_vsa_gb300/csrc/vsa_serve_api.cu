@@ -38,6 +38,8 @@ bool outputs_clear(const Range (&out)[NO], const Range (&in)[NI]) {
   return true;
 }
 
+constexpr int kSms = 152;
+
 std::mutex g_attr_mu;
 enum AttrSlot { kAttrSel8, kAttrSel16, kAttrSel24, kAttrSel32, kAttrFwd, kAttrSlots = kAttrFwd + 4 };
 bool g_attr[64][kAttrSlots];
@@ -238,7 +240,24 @@ vsa_status vsa_cache_select(const vsa_bf16* q, const vsa_bf16* k_mean, const int
   a.topk = topk;
   a.n_first = n_first < max_blocks ? n_first : max_blocks;
   a.n_near = n_near < max_blocks ? n_near : max_blocks;
-  cache_select_kernel<<<(unsigned)rows, kSelThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  // CTAs that share a row's blocks: 1 up to 256 blocks (two tiles a warp), else 4, or 8
+  // where that many fit the device at once
+  const int ctas = max_blocks <= 256 ? 1 : (rows * 8 <= 2 * kSms ? 8 : 4);
+  if (rows * ctas > INT_MAX) return VSA_ERR_UNSUPPORTED;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = ctas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(rows * ctas));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, cache_select_kernel, a) != cudaSuccess) {
+    cudaGetLastError();
+    return VSA_ERR_CUDA;
+  }
   return launched(1);
 }
 
