@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(BLOCK * 2)
 // ------------------------------------------------------------------ order and selection
 // Order-preserving whole numbers of finite fp32 / fp64 values (-0 counts as +0); 0 is kept
 // for "not eligible" and the largest for "chosen whatever its score".
+constexpr int kMaxBlocks = 2048;
 constexpr uint32_t kForced32 = 0xffffffffu;
 constexpr uint64_t kForced64 = ~0ull;
 __device__ __forceinline__ uint32_t order32(float f) {
@@ -93,11 +94,12 @@ __device__ __forceinline__ uint64_t order64(double f) {
   return (b >> 63) ? ~b : b | (1ull << 63);
 }
 
-constexpr int kSelThreads = 256;
+constexpr int kSelThreads = 256;  // of the kernels that choose within one row
 
+// The helpers below are called by every thread of a CTA of 256 or more.
 struct KthScratch {
   unsigned int hist[256];
-  unsigned int warp_sum[kSelThreads / 32];
+  unsigned int warp_sum[32];
   int digit, rest;
 };
 
@@ -137,9 +139,9 @@ __device__ void kth_largest(const K* keys, int n, int k, KthScratch& s, K* thr, 
   K prefix = 0, mask = 0;
   int rest = k;
   for (int shift = 8 * (int)sizeof(K) - 8; shift >= 0; shift -= 8) {
-    s.hist[threadIdx.x] = 0;
+    if (threadIdx.x < 256) s.hist[threadIdx.x] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kSelThreads) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
       const K key = keys[i];
       if ((key & mask) == prefix) atomicAdd(&s.hist[(unsigned)(key >> shift) & 255u], 1u);
     }
@@ -167,9 +169,7 @@ __device__ __forceinline__ unsigned int cta_exclusive(unsigned int v, KthScratch
   if (lane == 31) s.warp_sum[warp] = x;
   __syncthreads();
   unsigned int before = 0;
-#pragma unroll
-  for (int w = 0; w < kSelThreads / 32; ++w)
-    if (w < warp) before += s.warp_sum[w];
+  for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
   return before + x - v;
 }
 
@@ -178,7 +178,7 @@ __device__ __forceinline__ unsigned int cta_exclusive(unsigned int v, KthScratch
 template <typename K, typename F, typename R>
 __device__ void partition_ascending(const K* keys, int n, K thr, int n_eq, KthScratch& s,
                                     F chosen, R rest) {
-  const int per = (n + kSelThreads - 1) / kSelThreads;
+  const int per = (n + (int)blockDim.x - 1) / (int)blockDim.x;
   const int a = min(n, (int)threadIdx.x * per), e = min(n, a + per);
   unsigned int mine = 0;  // larger in the low half, equal in the high half
   for (int i = a; i < e; ++i) mine += keys[i] > thr ? 1u : (keys[i] == thr ? 0x10000u : 0u);
@@ -214,7 +214,7 @@ struct SelectArgs {
   int Hq, Hkv, group, nq, nk, topk, causal, n_first, n_near, tiles;
 };
 
-constexpr int kSelRows = 32;
+constexpr int kSelRows = 32, kSelRowThreads = 512;
 
 __host__ __device__ constexpr int select_stride(int nreg) { return nreg * 64 + 8; }
 __host__ __device__ constexpr size_t select_smem(int nreg) {
@@ -229,26 +229,32 @@ __device__ __forceinline__ bool select_forced(const SelectArgs& a, int e, int d)
   return e < a.n_first || (e > d - a.n_near && e < d + a.n_near);
 }
 
-__device__ __forceinline__ uint16_t bf16_unorder(uint32_t o) {
+// fp16 values in the order of 16-bit whole numbers.
+__device__ __forceinline__ uint16_t f16_unorder(uint32_t o) {
   return (uint16_t)((o & 0x8000u) ? o & 0x7fffu : ~o & 0xffffu);
 }
-__device__ __forceinline__ uint32_t bf16_pair(uint16_t b) { return (uint32_t)b << 16 | b; }
+__device__ __forceinline__ float f16_value(uint16_t b) {
+  return __half2float(__ushort_as_half(b));
+}
+__device__ __forceinline__ __half2 f16_pair(uint16_t b) {
+  return __half2half2(__ushort_as_half(b));
+}
+__device__ __forceinline__ __half2 as_half2(uint32_t w) {
+  return *reinterpret_cast<const __half2*>(&w);
+}
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) {
   return *reinterpret_cast<const __nv_bfloat162*>(&w);
-}
-__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) {
-  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // How many of the warp's 64*NREG keys are >= the threshold (NaN keys never count).
 template <int NREG>
 __device__ __forceinline__ int count_ge(const uint32_t (&key)[NREG], uint16_t thr) {
-  const __nv_bfloat162 t = as_bf162(bf16_pair(thr));
-  __nv_bfloat162 c = as_bf162(0), d = as_bf162(0);  // at most 16 each per half: exact
+  const __half2 t = f16_pair(thr);
+  __half2 c = as_half2(0), d = as_half2(0);
 #pragma unroll
   for (int j = 0; j < NREG; j += 2) {
-    c = __hadd2(c, __hge2(as_bf162(key[j]), t));
-    d = __hadd2(d, __hge2(as_bf162(key[j + 1]), t));
+    c = __hadd2(c, __hge2(as_half2(key[j]), t));
+    d = __hadd2(d, __hge2(as_half2(key[j + 1]), t));
   }
   c = __hadd2(c, d);
   return __reduce_add_sync(0xffffffffu, (int)(__low2float(c) + __high2float(c)));
@@ -298,26 +304,31 @@ __device__ __forceinline__ int warp_exclusive(int v, int lane) {
 }
 
 // One CTA: 32 query-block rows of one head against all nk <= 64*NREG key blocks.
-//   1. scores on the tensor cores: a warp holds the 32 rows' operands in registers and
-//      walks key tiles of 8; scores go to shared memory rounded to bf16 (32 x nk x 2 bytes
-//      fit where fp32 would not; the rounding only widens the band that is scored again).
-//      Operands are read 16 bytes a thread with the contraction index permuted the same
-//      way on both sides, so no shuffle or transposition is needed.
+//   1. scores on the tensor cores: a warp walks key tiles of 16 against the 32 rows, whose
+//      operands lie in shared memory; operands are read 16 bytes a thread with the
+//      contraction index permuted the same way on both sides, so no shuffle or
+//      transposition is needed.  Scores go to shared memory as fp16, times a power of two
+//      per row that brings them into its range (32 x nk x 2 bytes fit twice on an SM, fp32
+//      would not; the rounding only widens the band that is scored again).
 //   2. a warp per row, a lane with 2*NREG consecutive keys in NREG registers of pairs.
 //      The border is bracketed in the 16-bit order of the keys by counting, two keys an
 //      instruction: outwards from the last row's border, then by interpolation and halving
-//      in turn, until at most 4 keys lie between the brackets' ends.  Blocks surely above
+//      in turn, until at most 2 keys lie between the brackets' ends.  Blocks surely above
 //      the bracket are in; those that the error bound leaves open are scored again.
+// Both parts wait for latencies more than for any unit: 16 warps of 64 registers a CTA,
+// two CTAs on an SM.
 template <int NREG>
-__global__ void __launch_bounds__(kSelThreads, NREG <= 24 ? 2 : 1)
+__global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
     select_kernel(const SelectArgs a) {
   extern __shared__ __align__(16) uint16_t s_key[];  // [32][stride]
-  constexpr int kStride = select_stride(NREG);
-  __shared__ __align__(16) uint16_t s_q[kSelRows][128];
+  constexpr int kStride = select_stride(NREG), kWarps = kSelRowThreads / 32;
+  constexpr int kQStride = 160;  // 320 bytes: rows g and g + 1 in different halves of the banks
+  __shared__ __align__(16) uint16_t s_q[kSelRows][kQStride];
+  __shared__ uint32_t s_fair[kMaxBlocks / 32];
   __shared__ float s_q1[kSelRows];
-  __shared__ uint32_t s_kmax[kSelThreads / 32];
-  __shared__ unsigned int s_slow;
-  __shared__ uint16_t s_cand[kSelThreads / 32][32];
+  __shared__ uint32_t s_kmax[kWarps];
+  __shared__ unsigned int s_slow, s_sample;
+  __shared__ uint16_t s_cand[kWarps][32];
   __shared__ KthScratch s_kth;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, i4 = lane & 3;
@@ -327,123 +338,143 @@ __global__ void __launch_bounds__(kSelThreads, NREG <= 24 ? 2 : 1)
   const int hkv = (int)(bh - b * a.Hq) / a.group;
   const uint16_t* qh = a.q + (bh * a.nq) * 128;
   const uint16_t* kh = a.k + ((b * a.Hkv + hkv) * (long long)a.nk) * 128;
-  if (tid == 0) s_slow = 0;
-
-  // rows g, g+8, g+16, g+24; 16-byte chunks i4, i4+4, i4+8, i4+12
-  uint4 qa[4][4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int row = row0 + g + 8 * r;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      qa[r][j] = row < a.nq
-                     ? __ldg(reinterpret_cast<const uint4*>(qh + (long long)row * 128) + i4 + 4 * j)
-                     : make_uint4(0, 0, 0, 0);
-  }
-  if (warp == 0) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      float s = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        reinterpret_cast<uint4*>(s_q[g + 8 * r])[i4 + 4 * j] = qa[r][j];
-        const uint32_t u[4] = {qa[r][j].x, qa[r][j].y, qa[r][j].z, qa[r][j].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s += fabsf(bf16_lo(u[e])) + fabsf(bf16_hi(u[e]));
-      }
-      s += __shfl_xor_sync(0xffffffffu, s, 1);
-      s += __shfl_xor_sync(0xffffffffu, s, 2);
-      if (i4 == 0) s_q1[g + 8 * r] = s;
-    }
-  }
+  if (tid == 0) s_slow = s_sample = 0;
   __syncthreads();
+
+  auto abs_max = [](__nv_bfloat162 m, const uint4& v) {
+    m = __hmax2(m, __habs2(as_bf162(v.x)));
+    m = __hmax2(m, __habs2(as_bf162(v.y)));
+    m = __hmax2(m, __habs2(as_bf162(v.z)));
+    return __hmax2(m, __habs2(as_bf162(v.w)));
+  };
+  {  // the rows and their sums of |q|; the largest |k| of the first 32 blocks
+    const int r = tid >> 4, c = tid & 15;
+    const uint4 v = row0 + r < a.nq
+                        ? __ldg(reinterpret_cast<const uint4*>(qh + (long long)(row0 + r) * 128) + c)
+                        : make_uint4(0, 0, 0, 0);
+    const uint4 w = r < a.nk
+                        ? __ldg(reinterpret_cast<const uint4*>(kh + (long long)r * 128) + c)
+                        : make_uint4(0, 0, 0, 0);
+    reinterpret_cast<uint4*>(s_q[r])[c] = v;
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s += fabsf(bf16_lo(u[e])) + fabsf(bf16_hi(u[e]));
+#pragma unroll
+    for (int x = 8; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+    if (c == 0) s_q1[r] = s;
+    const __nv_bfloat162 m = abs_max(as_bf162(0), w);
+    const uint32_t mm = __reduce_max_sync(
+        0xffffffffu, __float_as_uint(fmaxf(__low2float(m), __high2float(m))));
+    if (lane == 0) atomicMax(&s_sample, mm);
+  }
+  // what may be chosen at all
+  int n_fair = 0;
+#pragma unroll
+  for (int e0 = 0; e0 < NREG * 64; e0 += kSelRowThreads) {
+    const int e = e0 + tid;
+    const bool fair = e < a.nk && (a.sizes == nullptr || a.sizes[e] > 0);
+    const unsigned int m = __ballot_sync(0xffffffffu, fair);
+    if (lane == 0 && e < NREG * 64) s_fair[e >> 5] = m;
+    n_fair += __syncthreads_count(fair);
+  }
+  // the power of two that brings a row's largest possible score, were the sampled |k| the
+  // largest, to 2^13
+  auto factor_of = [&](int r) {
+    const uint32_t e = __float_as_uint(s_q1[r] * __uint_as_float(s_sample)) >> 23 & 0xffu;
+    return __uint_as_float((uint32_t)(127 + min(100, max(-100, 127 + 13 - (int)e))) << 23);
+  };
 
   // scores
   {
-    const int nt = (a.nk + 7) / 8;
+    float f[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) f[r] = factor_of(g + 8 * r);
     __nv_bfloat162 kmax = as_bf162(0);
-    bool bad[4] = {false, false, false, false};
-    uint4 kb[4];
-    auto load = [&](int t) {
-      const int key = t * 8 + g;
+    unsigned int bad = 0;
+    for (int t = warp; t * 16 < a.nk; t += kWarps) {
+      uint4 kb[2][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        kb[j] = key < a.nk
-                    ? __ldg(reinterpret_cast<const uint4*>(kh + (long long)key * 128) + i4 + 4 * j)
-                    : make_uint4(0, 0, 0, 0);
-    };
-    if (warp < nt) load(warp);
-    for (int t = warp; t < nt; t += kSelThreads / 32) {
-      uint4 cur[4];
+      for (int x = 0; x < 2; ++x) {
+        const int key = t * 16 + 8 * x + g;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) cur[j] = kb[j];
-      if (t + kSelThreads / 32 < nt) load(t + kSelThreads / 32);
-      float d0[4] = {}, d1[4] = {};
+        for (int j = 0; j < 4; ++j)
+          kb[x][j] = key < a.nk ? __ldg(reinterpret_cast<const uint4*>(kh + (long long)key * 128) +
+                                        i4 + 4 * j)
+                                : make_uint4(0, 0, 0, 0);
+      }
+      float d[2][2][4] = {};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        mma_bf16(d0, qa[0][j].x, qa[1][j].x, qa[0][j].y, qa[1][j].y, cur[j].x, cur[j].y);
-        mma_bf16(d1, qa[2][j].x, qa[3][j].x, qa[2][j].y, qa[3][j].y, cur[j].x, cur[j].y);
-        mma_bf16(d0, qa[0][j].z, qa[1][j].z, qa[0][j].w, qa[1][j].w, cur[j].z, cur[j].w);
-        mma_bf16(d1, qa[2][j].z, qa[3][j].z, qa[2][j].w, qa[3][j].w, cur[j].z, cur[j].w);
-        kmax = __hmax2(kmax, __habs2(as_bf162(cur[j].x)));
-        kmax = __hmax2(kmax, __habs2(as_bf162(cur[j].y)));
-        kmax = __hmax2(kmax, __habs2(as_bf162(cur[j].z)));
-        kmax = __hmax2(kmax, __habs2(as_bf162(cur[j].w)));
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const uint4 qa = reinterpret_cast<const uint4*>(s_q[16 * m + g])[i4 + 4 * j];
+          const uint4 qb = reinterpret_cast<const uint4*>(s_q[16 * m + 8 + g])[i4 + 4 * j];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            mma_bf16(d[m][x], qa.x, qb.x, qa.y, qb.y, kb[x][j].x, kb[x][j].y);
+            mma_bf16(d[m][x], qa.z, qb.z, qa.w, qb.w, kb[x][j].z, kb[x][j].w);
+          }
+        }
+        kmax = abs_max(kmax, kb[0][j]);
+        kmax = abs_max(kmax, kb[1][j]);
       }
-      uint16_t* out = s_key + t * 8 + 2 * i4;
-      auto put = [&](int r, float x, float y) {
-        bad[r] |= !(fabsf(x) < kFinite) | !(fabsf(y) < kFinite);
-        *reinterpret_cast<uint32_t*>(out + (g + 8 * r) * kStride) =
-            as_u32(__floats2bfloat162_rn(x, y));
-      };
-      put(0, d0[0], d0[1]);
-      put(1, d0[2], d0[3]);
-      put(2, d1[0], d1[1]);
-      put(3, d1[2], d1[3]);
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = 16 * m + 8 * h + g;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float u = d[m][x][2 * h], v = d[m][x][2 * h + 1];
+            const float fu = u * f[2 * m + h], fv = v * f[2 * m + h];
+            if (!(fabsf(u) < kFinite && fabsf(v) < kFinite && fabsf(fu) < 65000.0f &&
+                  fabsf(fv) < 65000.0f))
+              bad |= 1u << (2 * m + h);
+            *reinterpret_cast<uint32_t*>(s_key + r * kStride + t * 16 + 8 * x + 2 * i4) =
+                pack_f16x2(fu, fv);
+          }
+        }
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      if (bad[r]) atomicOr(&s_slow, 1u << (g + 8 * r));
-    const float m = fmaxf(__low2float(kmax), __high2float(kmax));
-    const uint32_t mm = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+      if (bad >> r & 1u) atomicOr(&s_slow, 1u << (g + 8 * r));
+    const uint32_t mm = __reduce_max_sync(
+        0xffffffffu, __float_as_uint(fmaxf(__low2float(kmax), __high2float(kmax))));
     if (lane == 0) s_kmax[warp] = mm;
   }
   __syncthreads();
-  // what may not be chosen by any row
-  int n_fair = 0;
-#pragma unroll
-  for (int e0 = 0; e0 < NREG * 64; e0 += kSelThreads) {
-    const int e = e0 + tid;
-    const bool fair = e < a.nk && (a.sizes == nullptr || a.sizes[e] > 0);
-    if (!fair)
+  for (int e = tid; e < NREG * 64; e += kSelRowThreads)
+    if (!(s_fair[e >> 5] >> (e & 31) & 1u))
       for (int r = 0; r < kSelRows; ++r) s_key[r * kStride + e] = 0x7fff;
-    n_fair += __syncthreads_count(fair);
-  }
+  __syncthreads();
 
   uint32_t kmax_bits = 0;
 #pragma unroll
-  for (int w = 0; w < kSelThreads / 32; ++w) kmax_bits = max(kmax_bits, s_kmax[w]);
+  for (int w = 0; w < kWarps; ++w) kmax_bits = max(kmax_bits, s_kmax[w]);
   const float kmax = __uint_as_float(kmax_bits);
-  constexpr uint32_t kLowest = 0x007fu, kHighest = 0xff80u;  // order of -inf and +inf
-  // where the border is looked for first: this far below the bound for values like normal
-  // ones, and at the last row's after that
-  uint32_t guess = 0, stride0 = 64;
+  constexpr uint32_t kLowest = 0x03ffu, kHighest = 0xfc00u;  // order of -inf and +inf
+  // where the border is looked for first: 1/32 of the largest possible score, as of values
+  // like normal ones, and at the last row's after that
+  uint32_t guess = 0, stride0 = 256;
 
-  for (int r = warp; r < kSelRows; r += kSelThreads / 32) {
+  for (int r = warp; r < kSelRows; r += kWarps) {
     const int row = row0 + r;
     if (row >= a.nq) break;
     if ((s_slow >> r) & 1u) continue;
-    const float q1 = s_q1[r], bound = q1 * kmax, eps = kDotBound * bound + kTiny;
+    const float q1 = s_q1[r], bound = q1 * kmax;
     if (!(bound < kFinite)) {
       if (lane == 0) atomicOr(&s_slow, 1u << r);
       continue;
     }
+    const float f = factor_of(r);
     const int d = row + a.nk - a.nq;
     uint16_t* krow = s_key + r * kStride;
-    for (int e = lane; e < min(a.n_first, a.nk); e += 32)
-      if (select_allowed(a, e, d)) krow[e] = 0x7f80;
-    for (int e = max(0, d - a.n_near + 1) + lane; e < min(a.nk, d + a.n_near); e += 32)
-      if (select_allowed(a, e, d)) krow[e] = 0x7f80;
+    auto force = [&](int e) {
+      if ((s_fair[e >> 5] >> (e & 31) & 1u) && (!a.causal || e <= d)) krow[e] = 0x7c00;
+    };
+    for (int e = lane; e < a.n_first; e += 32) force(e);
+    for (int e = max(0, d - a.n_near + 1) + lane; e < min(a.nk, d + a.n_near); e += 32) force(e);
     __syncwarp();
     const int base = lane * 2 * NREG;
     uint32_t key[NREG];
@@ -462,29 +493,29 @@ __global__ void __launch_bounds__(kSelThreads, NREG <= 24 ? 2 : 1)
         if (base + 2 * j > d) key[j] |= 0x00007fffu;
         if (base + 2 * j + 1 > d) key[j] |= 0x7fff0000u;
       }
-      n_ok = count_ge<NREG>(key, bf16_unorder(kLowest));
+      n_ok = count_ge<NREG>(key, f16_unorder(kLowest));
     }
     const int k = min(a.topk, n_ok);
-    uint32_t in_thr, cand_thr;  // in: key > in_thr, candidate: the others >= cand_thr
+    uint16_t in_thr, cand_thr;  // in: key > in_thr, candidate: the others >= cand_thr
     bool ties = false;          // candidates are equal: the lowest indices
     if (n_ok <= a.topk) {
-      in_thr = cand_thr = bf16_unorder(kLowest);  // all, as candidates
+      in_thr = cand_thr = f16_unorder(kLowest);  // all are in
     } else {
       uint32_t lo = kLowest, hi = kHighest;  // count(>= lo) >= k > count(>= hi)
       int c_lo = n_ok, c_hi = 0;
-      if (a.n_first + 2 * a.n_near >= k) c_hi = count_ge<NREG>(key, bf16_unorder(kHighest));
+      if (a.n_first + 2 * a.n_near >= k) c_hi = count_ge<NREG>(key, f16_unorder(kHighest));
       if (c_hi >= k) {  // more forced blocks than places
-        in_thr = cand_thr = 0x7f80u;
+        in_thr = cand_thr = 0x7c00u;
         ties = true;
       } else {
         if (guess == 0) {
-          guess = (__float_as_uint(bound * 0.03125f) >> 16) | 0x8000u;
-          guess = max(guess, 0x8100u);
+          const float first = fminf(fmaxf(bound * f * 0.03125f, 1e-3f), 60000.0f);
+          guess = __half_as_ushort(__float2half_rn(first)) | 0x8000u;
         }
         uint32_t at = guess, step = stride0;
         bool halve = false;
-        while (hi - lo > 1 && c_lo - c_hi > 4) {
-          const int c = count_ge<NREG>(key, bf16_unorder(at));
+        while (hi - lo > 1 && c_lo - c_hi > 2) {
+          const int c = count_ge<NREG>(key, f16_unorder(at));
           if (c >= k) {
             lo = at;
             c_lo = c;
@@ -508,35 +539,33 @@ __global__ void __launch_bounds__(kSelThreads, NREG <= 24 ? 2 : 1)
           at = min(max(at, lo + 1), hi - 1);
         }
         guess = lo == kLowest ? 0 : lo;
-        stride0 = 8;
-        const float t = __uint_as_float((uint32_t)bf16_unorder(lo) << 16);
-        const float u = __uint_as_float((uint32_t)bf16_unorder(hi - 1) << 16);
+        stride0 = 64;
         if (q1 == 0.0f || kmax == 0.0f) {  // every score is 0
           in_thr = 0x0000u;
           cand_thr = 0x8000u;
           ties = true;
         } else {
-          // bf16 rounding is off by at most 2^-9 of the value; s - bound(s) and s + bound(s)
-          // grow with s, so the true k-th score lies between those of t and of u
-          const float c = 0.00196f;
+          // a key is off by half an fp16 step, 2^-11 of it or 2^-25, and what the fp32 sum
+          // was; s - bound(s) and s + bound(s) grow with s, so the true k-th score lies
+          // between those of the bracket's ends
+          const float c = 0.00049f;
+          const float eps = (kDotBound * bound + kTiny) * f + 3.1e-8f;
+          const float t = f16_value(f16_unorder(lo)), u = f16_value(f16_unorder(hi - 1));
           const float up = u + c * fabsf(u) + 2.0f * eps, dn = t - c * fabsf(t) - 2.0f * eps;
-          in_thr = __bfloat16_as_ushort(
-              __float2bfloat16_ru(up / (up > 0.0f ? 1.0f - c : 1.0f + c)));
-          cand_thr = __bfloat16_as_ushort(
-              __float2bfloat16_rd(dn / (dn > 0.0f ? 1.0f + c : 1.0f - c)));
-          if (hi == kHighest || in_thr == 0x7f80u) in_thr = 0x7f7fu;  // the forced ones
+          in_thr = __half_as_ushort(__float2half_ru(up / (up > 0.0f ? 1.0f - c : 1.0f + c)));
+          cand_thr = __half_as_ushort(__float2half_rd(dn / (dn > 0.0f ? 1.0f + c : 1.0f - c)));
+          if (hi == kHighest || in_thr == 0x7c00u) in_thr = 0x7bffu;  // the forced ones
         }
       }
     }
     LaneSet<NREG> in, cand;
     {
-      const __nv_bfloat162 ti = as_bf162(bf16_pair((uint16_t)in_thr));
-      const __nv_bfloat162 tc = as_bf162(bf16_pair((uint16_t)cand_thr));
+      const __half2 ti = f16_pair(in_thr), tc = f16_pair(cand_thr);
       uint32_t mi[LaneSet<NREG>::kWords] = {}, mc[LaneSet<NREG>::kWords] = {};
 #pragma unroll
       for (int j = 0; j < NREG; ++j) {
-        mi[j / 16] |= __hgt2_mask(as_bf162(key[j]), ti) & (0x00010001u << (j & 15));
-        mc[j / 16] |= __hge2_mask(as_bf162(key[j]), tc) & (0x00010001u << (j & 15));
+        mi[j / 16] |= __hgt2_mask(as_half2(key[j]), ti) & (0x00010001u << (j & 15));
+        mc[j / 16] |= __hge2_mask(as_half2(key[j]), tc) & (0x00010001u << (j & 15));
       }
 #pragma unroll
       for (int i = 0; i < LaneSet<NREG>::kWords; ++i) mc[i] &= ~mi[i];
@@ -593,22 +622,19 @@ __global__ void __launch_bounds__(kSelThreads, NREG <= 24 ? 2 : 1)
             const T t = __shfl_sync(0xffffffffu, s, (lane & 3) * 8);
             if (lane >> 2 == c0 >> 2) mine = t;
           }
+          // (need lies in [1, n_cand): the border has a block on either side)
           int rank = 0;
           for (int c = 0; c < n_cand; ++c) {
             const T o = __shfl_sync(0xffffffffu, mine, c);
             rank += o > mine || (o == mine && c < lane);
           }
           const bool take = lane < n_cand && rank < need;
-          // the gap at the border
-          T worst = take ? mine : (T)INFINITY, best = lane < n_cand && !take ? mine : (T)-INFINITY;
-#pragma unroll
-          for (int x = 16; x > 0; x >>= 1) {
-            const T y = __shfl_xor_sync(0xffffffffu, worst, x);
-            worst = y < worst ? y : worst;
-            const T z = __shfl_xor_sync(0xffffffffu, best, x);
-            best = z > best ? z : best;
-          }
-          // 19 roundings of partial sums of at most sum |q||k|
+          // the gap at the border: 19 roundings of partial sums of at most sum |q||k|
+          const T worst = __shfl_sync(
+              0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, take && rank == need - 1)) - 1);
+          const T best = __shfl_sync(
+              0xffffffffu, mine,
+              __ffs(__ballot_sync(0xffffffffu, lane < n_cand && rank == need)) - 1);
           const bool sure =
               sizeof(T) == 8 || worst - best > (T)(2.0f * 19.5f * 5.9604645e-8f * bound + kTiny);
           return (sure ? 0x100 : 0) | (take ? 1 : 0);
@@ -633,7 +659,7 @@ __global__ void __launch_bounds__(kSelThreads, NREG <= 24 ? 2 : 1)
   }
   __syncthreads();
 
-  // Rows whose fp32 scores overflow, or with more than 32 blocks inside the error band
+  // Rows whose scores overflow fp32 or fp16, or with more than 32 blocks inside the error band
   // (equal blocks, say): every score in fp64, one row at a time by the whole CTA.
   unsigned int slow = s_slow;
   uint64_t* key64 = reinterpret_cast<uint64_t*>(s_key);  // nk * 8 <= 32 * stride * 2 bytes
@@ -645,7 +671,7 @@ __global__ void __launch_bounds__(kSelThreads, NREG <= 24 ? 2 : 1)
     const int d = row + a.nk - a.nq;
     __syncthreads();
     int n_ok = 0;
-    for (int e0 = 0; e0 < a.nk; e0 += kSelThreads) {
+    for (int e0 = 0; e0 < a.nk; e0 += kSelRowThreads) {
       const int e = e0 + tid;
       uint64_t key = 0;
       if (e < a.nk && select_allowed(a, e, d)) {
@@ -675,7 +701,7 @@ __global__ void __launch_bounds__(kSelThreads, NREG <= 24 ? 2 : 1)
     partition_ascending<uint64_t>(
         key64, a.nk, thr, n_ok > a.topk ? k - larger : 0, s_kth, [&](int at, int e) { out[at] = e; },
         [](int, int) {});
-    for (int s = k + tid; s < a.topk; s += kSelThreads) out[s] = -1;
+    for (int s = k + tid; s < a.topk; s += kSelRowThreads) out[s] = -1;
     if (tid == 0) a.num[bh * a.nq + row] = k;
   }
 }
@@ -690,8 +716,6 @@ struct CacheSelectArgs {
   int32_t* num;            // [B, Hkv]
   int Hkv, group, pages, max_blocks, block, topk, n_first, n_near;
 };
-
-constexpr int kMaxBlocks = 2048;
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;

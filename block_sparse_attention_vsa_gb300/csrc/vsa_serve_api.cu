@@ -69,7 +69,7 @@ template <int NREG>
 vsa_status launch_select(const SelectArgs& a, long long ctas, int dev, int slot, cudaStream_t s) {
   const vsa_status st = smem_limit(select_kernel<NREG>, select_smem(NREG), dev, slot);
   if (st != VSA_OK) return st;
-  select_kernel<NREG><<<(unsigned)ctas, kSelThreads, select_smem(NREG), s>>>(a);
+  select_kernel<NREG><<<(unsigned)ctas, kSelRowThreads, select_smem(NREG), s>>>(a);
   return launched(1);
 }
 
