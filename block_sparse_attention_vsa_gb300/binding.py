@@ -46,11 +46,12 @@ class VsaError(RuntimeError):
 
 
 _lib = None
+_fast = None  # the short way (csrc/vsa_torch.cpp) to the calls that run for microseconds
 
 
 def load(path: str = LIB_PATH):
     """Load the library and declare its signatures (no CUDA call happens here)."""
-    global _lib
+    global _lib, _fast
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -115,6 +116,13 @@ def load(path: str = LIB_PATH):
     h.vsa_fwd_cache.argtypes = [P] * 9 + [i32] * 8 + [f32, f32, P, P, P, P, sz, P]
     h.vsa_cache_evict.restype = i32
     h.vsa_cache_evict.argtypes = [P, P, P] + [i32] * 6 + [P] * 6
+    try:
+        from . import _vsa_torch
+    except ImportError as e:
+        raise RuntimeError("_vsa_torch.so is missing or was built for another torch: build it "
+                           "with `python -m block_sparse_attention_vsa_gb300.build`") from e
+    _vsa_torch.bind(h._handle)
+    _fast = _vsa_torch
     _lib = h
     return h
 
@@ -477,8 +485,19 @@ def vsa_set_stall_test(enable: bool) -> None:
 
 
 # --------------------------------------------------------- choosing blocks, the 8-bit cache
-# These calls run for microseconds, so what is checked here is checked in one expression per
-# tensor; _explain says afterwards what was wrong.
+# These calls run for microseconds.  With the tensors on the current device and its current
+# stream they go the short way, one step of C++ that checks, allocates and calls; what that
+# does not take goes the long way below it, which serves the call or says what is wrong.
+def _short(fn, call, *args):
+    """The result of the short way, or None where the long way has to be taken."""
+    if _fast is None:
+        load()
+    r = getattr(_fast, call)(*args)
+    if r.__class__ is int:
+        _check(fn, r)
+    return r
+
+
 def _explain(name, t, dtype, shape, dev):
     _dev(t, name, dtype, len(shape))
     if tuple(t.shape) != tuple(shape):
@@ -525,6 +544,10 @@ def _call(fn, dev, stream, *args):
 def vsa_block_mean(x, sizes=None, block=64, out=None, stream=None):
     """Block means: x bf16 [B,H,S,128] -> bf16 [B,H,ceil(S/block),128], each the mean of the
     first sizes[j] tokens of block j (sizes int32 [nb]; None = all there are)."""
+    if stream is None:
+        r = _short("vsa_block_mean", "block_mean", x, sizes, block, out)
+        if r is not None:
+            return r[0]
     (B, H, S, D), dev = _lead("x", x, torch.bfloat16, 4)
     nb = -(-S // block) if block > 0 else 0
     sizes_p = _maybe("sizes", sizes, torch.int32, (nb,), dev)
@@ -542,6 +565,11 @@ def vsa_select_blocks(q_mean, k_mean, topk, sizes=None, causal=False, n_first=0,
     -1 behind; q2k_num int32 [B,Hq,nq]).  sizes int32 [nk]: blocks of size 0 are not chosen;
     causal: no block past the diagonal i + nk - nq; the first n_first blocks and those
     nearer than n_near to the diagonal are always chosen."""
+    if stream is None:
+        r = _short("vsa_select_blocks", "select_blocks", q_mean, k_mean, topk, sizes, causal,
+                   n_first, n_near)
+        if r is not None:
+            return r
     (B, Hq, nq, D), dev = _lead("q_mean", q_mean, torch.bfloat16, 4)
     (_, Hkv, nk, _), _ = _lead("k_mean", k_mean, torch.bfloat16, 4)
     k_p = _need("k_mean", k_mean, torch.bfloat16, (B, Hkv, nk, D), dev)
@@ -594,6 +622,11 @@ def vsa_cache_select(q, k_mean, table, lens, topk, block=64, n_first=0, n_near=1
     bf16 [pages,128] (Cache8.k_mean), table int32 [B,Hkv,max_blocks], lens int32 [B] ->
     (idx int32 [B,Hkv,topk], num int32 [B,Hkv]), shared by the heads of a group (a block's
     score is the largest of its heads')."""
+    if stream is None:
+        r = _short("vsa_cache_select", "cache_select", q, k_mean, table, lens, topk, block, n_first,
+                   n_near)
+        if r is not None:
+            return r
     (B, Hq, _, D), dev = _lead("q", q, torch.bfloat16, 4)
     q_p = _need("q", q, torch.bfloat16, (B, Hq, 1, D), dev)
     (pages, _), _ = _lead("k_mean", k_mean, torch.bfloat16, 2)
@@ -611,6 +644,9 @@ def vsa_cache_write(cache, k, v, table, lens, n_new=None, stream=None):
     """Tokens lens[b] .. of every sequence into its pages: k, v bf16 [B,Hkv,T,128], of which
     sequence b writes the first n_new[b] (int32 [B]; None = T).  lens counts the tokens held
     before; add n_new to it afterwards."""
+    if stream is None and _short("vsa_cache_write", "cache_write", cache, k, v, table, lens,
+                                 n_new) is not None:
+        return
     (B, Hkv, T, D), dev = _lead("k", k, torch.bfloat16, 4)
     v_p = _need("v", v, torch.bfloat16, (B, Hkv, T, D), dev)
     pages, block, kc, vc, ks, vs = _cache(cache, dev)
@@ -643,6 +679,11 @@ def vsa_fwd_cache(q, cache, table, lens, idx=None, num=None, scale=None, out=Non
     int32 [B,Hkv,max_sel], num int32 [B,Hkv]) or all.  Returns (out, lse or None).  weight
     (float32 [B,Hkv,max_blocks]) becomes keep * weight + the step's weight of each block.
     The workspace is allocated if not given."""
+    if stream is None and workspace is not None:
+        r = _short("vsa_fwd_cache", "fwd_cache", q, cache, table, lens, idx, num, scale, out, lse,
+                   weight, keep, workspace)
+        if r is not None:
+            return r
     (B, Hq, _, D), dev = _lead("q", q, torch.bfloat16, 4)
     q_p = _need("q", q, torch.bfloat16, (B, Hq, 1, D), dev)
     pages, block, kc, vc, ks, vs = _cache(cache, dev)
@@ -692,6 +733,11 @@ def vsa_cache_evict(weight, table, lens, budget, block=64, n_first=0, n_last=1,
     """Cut every sequence to at most `budget` blocks per key/value head: the first n_first
     and last n_last stay, and of the rest those of the highest weight (float32
     [B,Hkv,max_blocks], as vsa_fwd_cache accumulates it)."""
+    if stream is None:
+        r = _short("vsa_cache_evict", "cache_evict", weight, table, lens, budget, block, n_first,
+                   n_last)
+        if r is not None:
+            return Evicted._make(r)
     (B, Hkv, max_blocks), dev = _lead("weight", weight, torch.float32, 3)
     table_p = _need("table", table, torch.int32, (B, Hkv, max_blocks), dev)
     lens_p = _need("lens", lens, torch.int32, (B,), dev)

@@ -1,16 +1,19 @@
-"""Build libvsa_gb300.so (the CUDA kernels + C ABI) in-tree with nvcc for sm_103a.
+"""Build libvsa_gb300.so (the CUDA kernels + C ABI) in-tree with nvcc for sm_103a, and
+_vsa_torch.so (the short way from torch tensors to its microsecond calls) with g++.
 
     python -m block_sparse_attention_vsa_gb300.build [--force]
 
-Two translation units compiled side by side, one -gencode (sm_103a), static CUDA runtime,
+Three translation units compiled side by side, one -gencode (sm_103a), static CUDA runtime,
 no cmake.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +24,8 @@ DEPS = SOURCES + [os.path.join(CSRC, f) for f in (
     "vsa_fwd_kernel.cuh", "vsa_bwd_kernel.cuh", "vsa_select_kernel.cuh", "vsa_cache_kernel.cuh",
     "sm103_ptx.cuh", "vsa_warp_ptx.cuh", "vsa_host.h")] + [
     os.path.join(ROOT, "include", "vsa.h")]
+TORCH_LIB = os.path.join(PKG, "_vsa_torch.so")
+TORCH_SOURCE = os.path.join(CSRC, "vsa_torch.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-shared", "-Xcompiler", "-fPIC",
@@ -34,25 +39,46 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA 13 toolkit is required to build libvsa_gb300.so")
 
 
-def stale() -> bool:
-    if not os.path.exists(LIB):
+def stale(lib: str = LIB, deps=None) -> bool:
+    if not os.path.exists(lib):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(p) > t for p in DEPS if os.path.exists(p))
+    t = os.path.getmtime(lib)
+    return any(os.path.getmtime(p) > t for p in (deps or DEPS) if os.path.exists(p))
+
+
+def _torch_command(out: str):
+    """The g++ command for _vsa_torch.so, against the headers and libraries of the torch that
+    this Python imports (looked up without importing it)."""
+    torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    include = [os.path.join(torch_dir, "include"), sysconfig.get_paths()["include"],
+               os.path.join(cuda, "include")]
+    return (["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", TORCH_SOURCE]
+            + [x for d in include for x in ("-isystem", d)]
+            + ["-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+               "-ltorch_cuda", "-ltorch_python", "-ldl", "-o", out]), os.path.join(torch_dir, "version.py")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not stale():
-        return LIB
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [nvcc()] + ARCH + FLAGS + (["-Xptxas", "-v"] if verbose else []) + SOURCES + [
-        "-o", tmp, "-cudart", "static"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
-    if verbose:
-        sys.stderr.write(r.stdout + r.stderr)
-    os.replace(tmp, LIB)
+    jobs = []
+    if force or stale():
+        tmp = LIB + ".tmp%d" % os.getpid()
+        cmd = [nvcc()] + ARCH + FLAGS + (["-Xptxas", "-v"] if verbose else []) + SOURCES + [
+            "-o", tmp, "-cudart", "static"]
+        jobs.append((cmd, tmp, LIB))
+    tmp = TORCH_LIB + ".tmp%d" % os.getpid()
+    cmd, version = _torch_command(tmp)
+    if force or stale(TORCH_LIB, [TORCH_SOURCE, DEPS[-1], version]):
+        jobs.append((cmd, tmp, TORCH_LIB))
+    running = [subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+               for cmd, _, _ in jobs]
+    said = [p.communicate()[0] for p in running]
+    for p, text, (cmd, tmp, lib) in zip(running, said, jobs):
+        if p.returncode != 0:
+            raise RuntimeError("build failed:\n" + " ".join(cmd) + "\n" + text)
+        if verbose:
+            sys.stderr.write(text)
+        os.replace(tmp, lib)
     return LIB
 
 

@@ -685,3 +685,46 @@ def test_refusals():
         with pytest.raises(binding.VsaError):
             call()
     torch.cuda.synchronize()
+
+
+def test_short_and_long_way_agree():
+    """A call without a stream goes the short way through C++, one with the current stream the
+    long way through Python: the same results, and the same refusals (above)."""
+    g, table, lens, pages, state = cache_case(63, 2, 2, [300, 70], 64, spare=2)
+    cache, table, lens = to_cache(state), table.to(DEV), lens.to(DEV)
+    other = binding.Cache8(*(t.view(torch.uint8).clone().view(t.dtype) if i < 2 else t.clone()
+                             for i, t in enumerate(cache)))
+    x = randn((2, 2, 80, D), g).to(DEV)
+    q = randn((2, 4, 1, D), g).to(DEV)
+    sizes = i32([64, 11]).to(DEV)
+    now = torch.cuda.current_stream()
+    means = [binding.vsa_block_mean(x, sizes, stream=s) for s in (None, now)]
+    assert torch.equal(*means)
+    for a, b in zip(*(binding.vsa_select_blocks(m, m, 3, sizes=sizes, causal=True, n_near=1,
+                                                stream=s) for m, s in zip(means, (None, now)))):
+        assert torch.equal(a, b)
+    n_new = i32([80, 5]).to(DEV)
+    for c, s in ((cache, None), (other, now)):
+        binding.vsa_cache_write(c, x, x, table, lens, n_new, stream=s)
+    for a, b in zip(cache, other):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    lens = lens + n_new
+    picks = [binding.vsa_cache_select(q, cache.k_mean, table, lens, 3, n_first=1, stream=s)
+             for s in (None, now)]
+    ws = binding.new_cache_workspace(2, 4, 2, table.shape[2], True, DEV)
+    outs = []
+    for (idx, num), s in zip(picks, (None, now)):
+        weight = torch.ones(table.shape, device=DEV)
+        out = binding.vsa_fwd_cache(q, cache, table, lens, idx=idx, num=num, scale=0.1,
+                                    weight=weight, keep=0.5, workspace=ws, stream=s)
+        outs.append((idx, num) + out + (weight,) +
+                    tuple(binding.vsa_cache_evict(weight, table, lens, 4, n_first=1, stream=s)))
+    for a, b in zip(*outs):
+        assert a.dtype == b.dtype and torch.equal(a, b)
+    kept = binding.vsa_cache_evict(weight, table, lens, 4)
+    assert kept.n_freed.tolist() == [2, 0] and kept.lens.tolist() == [380 - 128, 75]
+    # outputs given are the ones returned
+    out, lse = torch.empty_like(q), torch.empty((2, 4, 1), device=DEV)
+    got = binding.vsa_fwd_cache(q, cache, table, lens, out=out, lse=lse, workspace=ws)
+    assert got[0] is out and got[1] is lse
+    assert binding.vsa_fwd_cache(q, cache, table, lens, lse=False, workspace=ws)[1] is None
