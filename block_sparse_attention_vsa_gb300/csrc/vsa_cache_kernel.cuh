@@ -46,6 +46,7 @@ __device__ __forceinline__ int cache_exponent(uint32_t amax_bits) {
 // codes out.
 template <int BLOCK>
 __global__ void __launch_bounds__(BLOCK * 2) cache_write_kernel(const CacheWriteArgs a) {
+  after_predecessor();
   constexpr int kThreads = BLOCK * 2, kRowsPerPass = kThreads / 16, kWarps = kThreads / 32;
   __shared__ uint32_t s_amax[kWarps];
   __shared__ float s_sum[kWarps][128];
@@ -256,6 +257,7 @@ struct CacheSeg {
 template <int BLOCK, bool WEIGHT>
 __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
     cache_fwd_kernel(const CacheFwdArgs a) {
+  after_predecessor();
   constexpr int kThreads = kCacheWarps * 32;
   constexpr int kHalves = BLOCK / kCacheTile;
   constexpr int N = kCacheStages;
@@ -932,6 +934,7 @@ struct CacheEvictArgs {
 // memory (sure ones above all, NaN below all), the budget-th largest by radix descent,
 // then one ascending walk that writes what stays and what goes.
 __global__ void __launch_bounds__(kSelThreads) cache_evict_kernel(const CacheEvictArgs a) {
+  after_predecessor();
   __shared__ uint32_t s_key[kMaxBlocks];
   __shared__ KthScratch s_kth;
   const int tid = threadIdx.x;

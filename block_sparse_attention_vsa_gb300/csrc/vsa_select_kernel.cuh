@@ -25,6 +25,7 @@ template <int BLOCK>
 __global__ void __launch_bounds__(BLOCK * 2)
     block_mean_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ sizes, int S,
                       int nb, uint16_t* __restrict__ mean) {
+  after_predecessor();
   constexpr int kThreads = BLOCK * 2, kRowsPerPass = kThreads / 16, kWarps = kThreads / 32;
   __shared__ float part[kWarps][128];
   const long long blk = blockIdx.x;
@@ -320,6 +321,7 @@ __device__ __forceinline__ int warp_exclusive(int v, int lane) {
 template <int NREG>
 __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
     select_kernel(const SelectArgs a) {
+  after_predecessor();
   extern __shared__ __align__(16) uint16_t s_key[];  // [32][stride]
   constexpr int kStride = select_stride(NREG), kWarps = kSelRowThreads / 32;
   constexpr int kQStride = 160;  // 320 bytes: rows g and g + 1 in different halves of the banks
@@ -753,6 +755,7 @@ __device__ __forceinline__ uint64_t cache_score64(const uint16_t* q, int group,
 // that holds too many, by radix descent); blocks inside the error band of it are scored
 // again in fp64.
 __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSelectArgs a) {
+  after_predecessor();
   __shared__ uint32_t s_key[kMaxBlocks];
   __shared__ uint64_t s_key64[kMaxBlocks];
   __shared__ uint16_t s_cand[kMaxBlocks];

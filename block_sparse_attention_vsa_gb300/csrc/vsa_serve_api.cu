@@ -57,9 +57,29 @@ vsa_status smem_limit(Kern kern, size_t bytes, int dev, int slot) {
   return VSA_OK;
 }
 
-vsa_status launched(int n) {
-  if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
-  host_set_launches(n);
+// One launch; the kernel may start up while its predecessor in the stream ends (each begins
+// with after_predecessor()).  `cluster` CTAs form a cluster.
+template <typename... P, typename... A>
+vsa_status launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                  int cluster, A... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kern, P(args)...) != cudaSuccess) {
+    cudaGetLastError();
+    return VSA_ERR_CUDA;
+  }
+  host_set_launches(1);
   return VSA_OK;
 }
 
@@ -69,8 +89,8 @@ template <int NREG>
 vsa_status launch_select(const SelectArgs& a, long long ctas, int dev, int slot, cudaStream_t s) {
   const vsa_status st = smem_limit(select_kernel<NREG>, select_smem(NREG), dev, slot);
   if (st != VSA_OK) return st;
-  select_kernel<NREG><<<(unsigned)ctas, kSelRowThreads, select_smem(NREG), s>>>(a);
-  return launched(1);
+  return launch(select_kernel<NREG>, dim3((unsigned)ctas), kSelRowThreads, select_smem(NREG), s, 0,
+                a);
 }
 
 template <int BLOCK, bool WEIGHT>
@@ -85,8 +105,7 @@ vsa_status launch_cache_fwd(const CacheFwdArgs& a, int dev, cudaStream_t s) {
   const long long most = (long long)a.rows * n_max / 2;
   int grid = most < 1 ? 1 : (most < kCacheGrid ? (int)most : kCacheGrid);
   if (a.rows <= grid / 8) grid -= grid % a.rows;
-  kern<<<grid, kCacheWarps * 32, kCacheSmem, s>>>(a);
-  return launched(1);
+  return launch(kern, dim3(grid), kCacheWarps * 32, kCacheSmem, s, 0, a);
 }
 
 // Workspace: counters (at one place whatever the shape, so that a workspace may serve calls
@@ -142,11 +161,8 @@ vsa_status vsa_block_mean(const vsa_bf16* x, const int32_t* sizes, int B, int H,
   const vsa_status st = host_device(&dev, &sms);
   if (st != VSA_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (block == 64)
-    block_mean_kernel<64><<<(unsigned)ctas, 128, 0, s>>>(x, sizes, S, (int)nb, mean);
-  else
-    block_mean_kernel<128><<<(unsigned)ctas, 256, 0, s>>>(x, sizes, S, (int)nb, mean);
-  return launched(1);
+  return launch(block == 64 ? block_mean_kernel<64> : block_mean_kernel<128>,
+                dim3((unsigned)ctas), block * 2, 0, s, 0, x, sizes, S, (int)nb, mean);
 }
 
 vsa_status vsa_select_blocks(const vsa_bf16* q_mean, const vsa_bf16* k_mean, const int32_t* sizes,
@@ -244,21 +260,8 @@ vsa_status vsa_cache_select(const vsa_bf16* q, const vsa_bf16* k_mean, const int
   // where that many fit the device at once
   const int ctas = max_blocks <= 256 ? 1 : (rows * 8 <= 2 * kSms ? 8 : 4);
   if (rows * ctas > INT_MAX) return VSA_ERR_UNSUPPORTED;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = ctas;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(rows * ctas));
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, cache_select_kernel, a) != cudaSuccess) {
-    cudaGetLastError();
-    return VSA_ERR_CUDA;
-  }
-  return launched(1);
+  return launch(cache_select_kernel, dim3((unsigned)(rows * ctas)), kSelThreads, 0,
+                reinterpret_cast<cudaStream_t>(stream), ctas, a);
 }
 
 vsa_status vsa_cache_write(const vsa_bf16* k, const vsa_bf16* v, const int32_t* table,
@@ -302,11 +305,8 @@ vsa_status vsa_cache_write(const vsa_bf16* k, const vsa_bf16* v, const int32_t* 
                          max_blocks};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const dim3 grid((unsigned)ctas, 2);
-  if (block == 64)
-    cache_write_kernel<64><<<grid, 128, 0, s>>>(a);
-  else
-    cache_write_kernel<128><<<grid, 256, 0, s>>>(a);
-  return launched(1);
+  return launch(block == 64 ? cache_write_kernel<64> : cache_write_kernel<128>, grid, block * 2, 0,
+                s, 0, a);
 }
 
 size_t vsa_cache_workspace_bytes(int B, int Hq, int Hkv, int max_blocks, int weight) {
@@ -429,8 +429,8 @@ vsa_status vsa_cache_evict(const float* weight, const int32_t* table, const int3
   if (st != VSA_OK) return st;
   const CacheEvictArgs a{weight,     table,    lens,  table_out, weight_out, lens_out, freed,
                          n_freed,    Hkv,      max_blocks, block, budget,    n_first,  n_last};
-  cache_evict_kernel<<<(unsigned)rows, kSelThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-  return launched(1);
+  return launch(cache_evict_kernel, dim3((unsigned)rows), kSelThreads, 0,
+                reinterpret_cast<cudaStream_t>(stream), 0, a);
 }
 
 }  // extern "C"

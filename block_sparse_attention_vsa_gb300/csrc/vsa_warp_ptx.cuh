@@ -11,6 +11,16 @@
 
 namespace vsa {
 
+// A kernel launched with programmatic serialization starts while its predecessor in the
+// stream still runs.  First thing in the kernel: wait until the predecessor has ended and
+// its writes are visible, and let the successor start likewise.  Nothing is read or
+// written before that, so the order of the stream's work is that of ordinary launches; what
+// overlaps is the start-up.
+__device__ __forceinline__ void after_predecessor() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // 16 bytes global -> shared, asynchronously; `n_src` of them are read (0 or 16), the
 // rest of the destination is filled with zeros.
 __device__ __forceinline__ void cp_async16(uint32_t dst_smem, const void* src, uint32_t n_src) {
