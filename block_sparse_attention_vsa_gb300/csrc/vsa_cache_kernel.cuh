@@ -931,39 +931,81 @@ struct CacheEvictArgs {
 };
 
 // One CTA per (sequence, key/value head): weights as ordered whole numbers in shared
-// memory (sure ones above all, NaN below all), the budget-th largest by radix descent,
-// then one ascending walk that writes what stays and what goes.
+// memory (sure ones above all, NaN below all) beside the table's row; the last of those
+// that stay is found between the least and the largest weight; then one ascending walk
+// orders what stays and what goes.  Bound by its barriers more than by its bytes.
 __global__ void __launch_bounds__(kSelThreads) cache_evict_kernel(const CacheEvictArgs a) {
   after_predecessor();
+  constexpr int kWarps = kSelThreads / 32;
   __shared__ uint32_t s_key[kMaxBlocks];
+  __shared__ float s_weight[kMaxBlocks];
+  __shared__ int32_t s_table[kMaxBlocks];
+  __shared__ uint16_t s_order[kMaxBlocks];
+  __shared__ __align__(16) uint32_t s_list[kRanked];
   __shared__ KthScratch s_kth;
-  const int tid = threadIdx.x;
+  __shared__ uint32_t s_lo[kWarps], s_hi[kWarps], s_thr;
+  __shared__ int s_sure[kWarps], s_members;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long bh = blockIdx.x, row = bh * a.max_blocks;
   const int b = (int)(bh / a.Hkv);
   const int len = max(0, a.lens[b]);
   const int n = (int)min(((long long)len + a.block - 1) / a.block, (long long)a.max_blocks);
   const int gone = max(0, n - a.budget), stay = n - gone;
+  uint32_t lo = kForced32, hi = 0;
+  int sure = 0;
   for (int e = tid; e < n; e += kSelThreads) {
     const float w = a.weight[row + e];
-    const bool sure = e < a.n_first || e >= n - a.n_last;
-    s_key[e] = sure ? kForced32 : (w != w ? 1u : order32(w));
+    s_weight[e] = w;
+    s_table[e] = a.table[row + e];
+    uint32_t key = w != w ? 1u : order32(w);
+    if (e < a.n_first || e >= n - a.n_last) {
+      key = kForced32;
+      ++sure;
+    } else {
+      lo = min(lo, key);
+      hi = max(hi, key);
+    }
+    s_key[e] = key;
   }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  sure = __reduce_add_sync(0xffffffffu, sure);
+  if (lane == 0) {
+    s_lo[warp] = lo;
+    s_hi[warp] = hi;
+    s_sure[warp] = sure;
+  }
+  if (tid == 0) s_members = 0;
   __syncthreads();
   uint32_t thr = 0;
   int larger = n;
-  if (gone > 0) kth_largest<uint32_t>(s_key, n, stay, s_kth, &thr, &larger);
-  partition_ascending<uint32_t>(
-      s_key, n, thr, stay - larger, s_kth,
-      [&](int at, int e) {
-        a.table_out[row + at] = a.table[row + e];
-        a.weight_out[row + at] = a.weight[row + e];
-      },
-      [&](int at, int e) { a.freed[row + at] = a.table[row + e]; });
-  for (int e = stay + tid; e < a.max_blocks; e += kSelThreads) {
-    a.table_out[row + e] = -1;
-    a.weight_out[row + e] = 0.0f;
+  if (gone > 0) {
+    sure = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      lo = min(lo, s_lo[w]);
+      hi = max(hi, s_hi[w]);
+      sure += s_sure[w];
+    }
+    if (stay > sure) {
+      kth_between(s_key, n, stay - sure, lo, hi, s_kth, s_list, &s_members, &s_thr, &thr, &larger);
+      larger += sure;
+    } else {  // only the sure ones stay (they are fewer than the budget or as many)
+      thr = kForced32 - 1;
+      larger = stay;
+    }
   }
-  for (int e = gone + tid; e < a.max_blocks; e += kSelThreads) a.freed[row + e] = -1;
+  // the order of those that stay, then of those that go, so that the writes run through
+  partition_ascending<uint32_t>(
+      s_key, n, thr, stay - larger, s_kth, [&](int at, int e) { s_order[at] = (uint16_t)e; },
+      [&](int at, int e) { s_order[stay + at] = (uint16_t)e; });
+  __syncthreads();
+  for (int at = tid; at < a.max_blocks; at += kSelThreads) {
+    const int e = at < stay ? s_order[at] : -1, f = at < gone ? s_order[stay + at] : -1;
+    a.table_out[row + at] = e >= 0 ? s_table[e] : -1;
+    a.weight_out[row + at] = e >= 0 ? s_weight[e] : 0.0f;
+    a.freed[row + at] = f >= 0 ? s_table[f] : -1;
+  }
   if (tid == 0 && bh % a.Hkv == 0) {
     a.lens_out[b] = len - gone * a.block;
     a.n_freed[b] = gone;

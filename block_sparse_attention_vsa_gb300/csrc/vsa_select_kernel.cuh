@@ -101,11 +101,11 @@ constexpr int kSelThreads = 256;  // of the kernels that choose within one row
 struct KthScratch {
   unsigned int hist[256];
   unsigned int warp_sum[32];
-  int digit, rest;
+  int digit, rest, count;
 };
 
 // Which of 256 counted digits, from the largest down, holds the rest-th key, and which of
-// its keys that is: s.digit and s.rest.  One warp.
+// its keys that is, of how many: s.digit, s.rest and s.count.  One warp.
 __device__ __forceinline__ void digit_of(KthScratch& s, int rest, int lane) {
   // lane l holds digits 255-8l down to 248-8l
   unsigned int h[8], sum = 0;
@@ -127,6 +127,7 @@ __device__ __forceinline__ void digit_of(KthScratch& s, int rest, int lane) {
       if (before < (unsigned)rest && before + h[e] >= (unsigned)rest) {
         s.digit = 255 - 8 * lane - e;
         s.rest = rest - (int)before;
+        s.count = (int)h[e];
       }
       before += h[e];
     }
@@ -154,6 +155,67 @@ __device__ void kth_largest(const K* keys, int n, int k, KthScratch& s, K* thr, 
     rest = s.rest;
   }
   *thr = prefix;
+  *larger = k - rest;
+}
+
+// The value of rank `within` (1 = largest) among members[0..count), count <= kRanked and
+// none of them 0: to *thr, and which of those equal to it that is to s.rest.  `members` is
+// 16-byte aligned with room for kRanked.
+constexpr int kRanked = 128;
+__device__ __forceinline__ void rank_members(uint32_t* members, int count, int within,
+                                             KthScratch& s, uint32_t* thr) {
+  if (threadIdx.x < 4 && count + (int)threadIdx.x < kRanked) members[count + threadIdx.x] = 0;
+  __syncthreads();
+  if ((int)threadIdx.x < count) {
+    const uint32_t mine = members[threadIdx.x];
+    int gt = 0, ge = 0;
+#pragma unroll 4
+    for (int o = 0; o < count; o += 4) {
+      const uint4 y = *reinterpret_cast<const uint4*>(members + o);
+      gt += (y.x > mine) + (y.y > mine) + (y.z > mine) + (y.w > mine);
+      ge += (y.x >= mine) + (y.y >= mine) + (y.z >= mine) + (y.w >= mine);
+    }
+    if (gt < within && within <= ge) {  // the same from every thread that gets here
+      *thr = mine;
+      s.rest = within - gt;
+    }
+  }
+  __syncthreads();
+}
+
+// kth_largest of the keys in [base, top], whose least and largest these are: 256 even steps between those,
+// then between the ends of the step that the k-th falls into, until that holds few enough
+// to rank.  *n_members is 0 before.
+__device__ __forceinline__ void kth_between(const uint32_t* keys, int n, int k, uint32_t base,
+                                            uint32_t top, KthScratch& s, uint32_t* members,
+                                            int* n_members, uint32_t* s_thr, uint32_t* thr,
+                                            int* larger) {
+  int bits = 32 - __clz(top - base), rest = k, count;
+  do {
+    const int shift = max(0, bits - 8);
+    if (threadIdx.x < 256) s.hist[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      const uint32_t key = keys[i], off = key - base;
+      if (key >= base && key <= top && (bits >= 32 || off >> bits == 0)) atomicAdd(&s.hist[off >> shift], 1u);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) digit_of(s, rest, threadIdx.x);
+    __syncthreads();
+    base += (uint32_t)s.digit << shift;
+    bits = shift;
+    rest = s.rest;
+    count = s.count;
+  } while (bits > 0 && count > kRanked);
+  if (bits > 0) {
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+      if (keys[i] >= base && keys[i] <= top && (keys[i] - base) >> bits == 0)
+        members[atomicAdd(n_members, 1)] = keys[i];
+    rank_members(members, count, rest, s, s_thr);
+    base = *s_thr;
+    rest = s.rest;
+  }
+  *thr = base;
   *larger = k - rest;
 }
 
@@ -655,8 +717,9 @@ __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
     // ascending indices, -1 behind
     int32_t* out = a.idx + (bh * a.nq + row) * (long long)a.topk;
     int at = warp_exclusive(in.count(), lane);
-    in.each([&](int e, int, uint32_t) { out[at++] = base + e; });
-    for (int s = k + lane; s < a.topk; s += 32) out[s] = -1;
+    in.each([&](int e, int, uint32_t) { krow[at++] = (uint16_t)(base + e); });  // keys are in registers
+    __syncwarp();
+    for (int s = lane; s < a.topk; s += 32) out[s] = s < k ? krow[s] : -1;
     if (lane == 0) a.num[bh * a.nq + row] = k;
   }
   __syncthreads();
@@ -726,25 +789,37 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 // The exact score of a block: the largest over the group's heads (NaN if any is), as an
-// ordered whole number.  One warp.
+// ordered whole number.  One warp, four heads at a time on 8 lanes each.
 __device__ __forceinline__ uint64_t cache_score64(const uint16_t* q, int group,
                                                   const uint16_t* mean, int lane) {
-  const uint2 kw = __ldg(reinterpret_cast<const uint2*>(mean) + lane);
-  const double k0 = bf16_lo(kw.x), k1 = bf16_hi(kw.x), k2 = bf16_lo(kw.y), k3 = bf16_hi(kw.y);
+  const uint4* kp = reinterpret_cast<const uint4*>(mean) + (lane & 7);
+  const uint4 kw[2] = {__ldg(kp), __ldg(kp + 8)};
   double best = -INFINITY;
   bool nan = false;
-  for (int h = 0; h < group; ++h) {
-    const uint2 qw = __ldg(reinterpret_cast<const uint2*>(q + (long long)h * 128) + lane);
-    double s = (double)bf16_lo(qw.x) * k0;
-    s = fma((double)bf16_hi(qw.x), k1, s);
-    s = fma((double)bf16_lo(qw.y), k2, s);
-    s = fma((double)bf16_hi(qw.y), k3, s);
+  for (int h0 = 0; h0 < group; h0 += 4) {
+    const int h = min(h0 + (lane >> 3), group - 1);
+    const uint4* qp = reinterpret_cast<const uint4*>(q + (long long)h * 128) + (lane & 7);
+    const uint4 qw[2] = {__ldg(qp), __ldg(qp + 8)};
+    double s = 0.0, t = 0.0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int x = 0; x < 2; ++x) {
+      const uint32_t ku[4] = {kw[x].x, kw[x].y, kw[x].z, kw[x].w};
+      const uint32_t qu[4] = {qw[x].x, qw[x].y, qw[x].z, qw[x].w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        s = fma((double)bf16_lo(qu[y]), (double)bf16_lo(ku[y]), s);
+        t = fma((double)bf16_hi(qu[y]), (double)bf16_hi(ku[y]), t);
+      }
+    }
+    s += t;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     nan |= s != s;
     best = fmax(best, s);
   }
-  return nan ? 0 : order64(best);
+  best = fmax(best, __shfl_xor_sync(0xffffffffu, best, 8));
+  best = fmax(best, __shfl_xor_sync(0xffffffffu, best, 16));
+  return __any_sync(0xffffffffu, nan) ? 0 : order64(best);
 }
 
 // A cluster of CTAs per (sequence, key/value head), up to 2048 blocks: the CTAs score the
@@ -765,6 +840,7 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSe
   __shared__ uint32_t s_bad;
   __shared__ int s_n_cand, s_ok, s_forced;
   __shared__ uint32_t s_thr;
+  __shared__ __align__(16) uint32_t s_members[kRanked];
   auto cluster = cooperative_groups::this_cluster();
   const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -959,31 +1035,16 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSe
   const int rest = k - s_forced;
   if (warp == 0) digit_of(s_kth, rest, lane);
   __syncthreads();
-  const int digit = s_kth.digit, within = s_kth.rest, members = (int)s_kth.hist[digit];
+  const int digit = s_kth.digit, within = s_kth.rest, members = s_kth.count;
   uint32_t thr;
   int larger;
-  constexpr int kRanked = 128;
   if (members <= kRanked && per < INFINITY) {
     for (int e = tid; e < n; e += kSelThreads) {
       const uint32_t key = s_key[e];
       if (key != 0 && key != kForced32 && step_of(key) == digit)
-        s_cand[atomicAdd(&s_n_cand, 1)] = (uint16_t)e;
+        s_members[atomicAdd(&s_n_cand, 1)] = key;
     }
-    __syncthreads();
-    if (tid < members) {
-      const uint32_t mine = s_key[s_cand[tid]];
-      int gt = 0, ge = 0;
-      for (int o = 0; o < members; ++o) {
-        const uint32_t y = s_key[s_cand[o]];
-        gt += y > mine;
-        ge += y >= mine;
-      }
-      if (gt < within && within <= ge) {
-        s_thr = mine;
-        s_kth.rest = within - gt;
-      }
-    }
-    __syncthreads();
+    rank_members(s_members, members, within, s_kth, &s_thr);
     thr = s_thr;
     larger = k - s_kth.rest;
     if (tid == 0) s_n_cand = 0;

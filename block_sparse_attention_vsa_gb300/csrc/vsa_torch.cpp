@@ -81,6 +81,23 @@ T* address(const at::Tensor& t) {
 at::Tensor empty(const at::Tensor& like, at::ScalarType type, Shape shape) {
   return at::detail::empty_cuda(at::IntArrayRef(shape), type, like.device(), std::nullopt);
 }
+// Consecutive parts of one allocation, each 256-byte aligned.
+struct Parts {
+  at::Tensor all;
+  int64_t at = 0;
+  static int64_t room(int64_t n) { return (n + 63) & ~int64_t{63}; }
+  Parts(const at::Tensor& like, at::ScalarType type, int64_t n) : all(empty(like, type, {n})) {}
+  at::Tensor part(Shape shape) {
+    int64_t n = 1;
+    for (const int64_t d : shape) n *= d;
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+        c10::Storage(all.storage()), all.key_set(), all.dtype());
+    t.unsafeGetTensorImpl()->set_storage_offset(at);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(at::IntArrayRef(shape));
+    at += room(n);
+    return t;
+  }
+};
 int to_int(int64_t v) {
   if (v < INT_MIN || v > INT_MAX) throw LongWay();
   return (int)v;
@@ -343,10 +360,12 @@ PyObject* cache_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t B = weight.size(0), Hkv = weight.size(1), blocks = weight.size(2);
     const int32_t* tp = need<int32_t>(a[1], kI32, {B, Hkv, blocks}, dev);
     const int32_t* lens = need<int32_t>(a[2], kI32, {B}, dev);
-    const at::Tensor table_out = empty(table, kI32, {B, Hkv, blocks});
+    // what goes on living together in one allocation, what is looked at once in another
+    Parts kept(table, kI32, Parts::room(B * Hkv * blocks) + B);
+    Parts went(table, kI32, Parts::room(B * Hkv * blocks) + B);
+    const at::Tensor table_out = kept.part({B, Hkv, blocks}), lens_out = kept.part({B});
+    const at::Tensor freed = went.part({B, Hkv, blocks}), n_freed = went.part({B});
     const at::Tensor weight_out = empty(weight, kF32, {B, Hkv, blocks});
-    const at::Tensor lens_out = empty(table, kI32, {B}), freed = empty(table, kI32, {B, Hkv, blocks});
-    const at::Tensor n_freed = empty(table, kI32, {B});
     const float* wp = address<float>(weight);
     float* wo = address<float>(weight_out);
     int32_t *to = address<int32_t>(table_out), *lo = address<int32_t>(lens_out);
