@@ -461,10 +461,27 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
     }
   };
 
+  // q of this thread's head column g: columns 16 * (i4 + 4 j) + 0..15
+  auto fetch_q = [&](const CacheSeg& s, uint4 (&qw)[2][2]) {
+    const int chunk = s.row % a.chunks;
+    const long long head = (long long)(s.row / a.chunks) * a.group + chunk * 8 + g;
+    const bool on = g < a.group - chunk * 8;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        qw[j][p] = on ? __ldg(reinterpret_cast<const uint4*>(a.q + head * 128) + 2 * (i4 + 4 * j) + p)
+                      : make_uint4(0, 0, 0, 0);
+  };
+
   CacheSeg cur, nxt;
+  uint4 qw[2][2];
   int buf = 0, slot = 0;  // the list in use; the slot of the next stage to be used
   bool more = (int)blockIdx.x < pieces && enter_piece(cur, blockIdx.x);
-  if (more) list(cur, 0);
+  if (more) {
+    fetch_q(cur, qw);
+    list(cur, 0);
+  }
   int n_cur = more ? stages_of(cur) : 0;
   // N groups of copies are always outstanding, some of them empty
 #pragma unroll
@@ -492,15 +509,6 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
     const int heads = min(8, a.group - chunk * 8);
     const long long head0 = bh * a.group + chunk * 8;
     const int32_t* table = a.table + bh * a.max_blocks;
-    // q of this thread's head column g: columns 16 * (i4 + 4 j) + 0..15
-    uint4 qw[2][2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-        qw[j][p] = g < heads ? __ldg(reinterpret_cast<const uint4*>(a.q + (head0 + g) * 128) +
-                                     2 * (i4 + 4 * j) + p)
-                             : make_uint4(0, 0, 0, 0);
     uint32_t qb[2][4][2];
     float qf0, qf1;  // what turns the products of heads 2 i4, 2 i4 + 1 into log2 units
     {
@@ -908,6 +916,7 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
     buf ^= 1;
     n_cur = n_nxt;
     more = follows;
+    if (more) fetch_q(cur, qw);
   }
   cp_async_wait<0>();
   // the last CTA to end clears the queue

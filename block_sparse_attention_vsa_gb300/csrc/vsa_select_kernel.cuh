@@ -788,38 +788,41 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-// The exact score of a block: the largest over the group's heads (NaN if any is), as an
-// ordered whole number.  One warp, four heads at a time on 8 lanes each.
-__device__ __forceinline__ uint64_t cache_score64(const uint16_t* q, int group,
-                                                  const uint16_t* mean, int lane) {
+// A block's score in T: the largest over the group's heads, NaN if any is.  One warp, four
+// heads at a time on 8 lanes each; every lane gets it.
+template <typename T>
+__device__ __forceinline__ T cache_score(const uint16_t* q, int group, const uint16_t* mean,
+                                         int lane) {
   const uint4* kp = reinterpret_cast<const uint4*>(mean) + (lane & 7);
   const uint4 kw[2] = {__ldg(kp), __ldg(kp + 8)};
-  double best = -INFINITY;
+  T best = (T)-INFINITY;
   bool nan = false;
   for (int h0 = 0; h0 < group; h0 += 4) {
     const int h = min(h0 + (lane >> 3), group - 1);
     const uint4* qp = reinterpret_cast<const uint4*>(q + (long long)h * 128) + (lane & 7);
     const uint4 qw[2] = {__ldg(qp), __ldg(qp + 8)};
-    double s = 0.0, t = 0.0;
+    T s = 0;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const uint32_t ku[4] = {kw[x].x, kw[x].y, kw[x].z, kw[x].w};
       const uint32_t qu[4] = {qw[x].x, qw[x].y, qw[x].z, qw[x].w};
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        s = fma((double)bf16_lo(qu[y]), (double)bf16_lo(ku[y]), s);
-        t = fma((double)bf16_hi(qu[y]), (double)bf16_hi(ku[y]), t);
+        s = fma((T)bf16_lo(qu[y]), (T)bf16_lo(ku[y]), s);
+        s = fma((T)bf16_hi(qu[y]), (T)bf16_hi(ku[y]), s);
       }
     }
-    s += t;
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     nan |= s != s;
-    best = fmax(best, s);
+    best = s > best ? s : best;
   }
-  best = fmax(best, __shfl_xor_sync(0xffffffffu, best, 8));
-  best = fmax(best, __shfl_xor_sync(0xffffffffu, best, 16));
-  return __any_sync(0xffffffffu, nan) ? 0 : order64(best);
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) {
+    const T y = __shfl_xor_sync(0xffffffffu, best, o);
+    best = y > best ? y : best;
+  }
+  return __any_sync(0xffffffffu, nan) ? (T)NAN : best;
 }
 
 // A cluster of CTAs per (sequence, key/value head), up to 2048 blocks: the CTAs score the
@@ -964,7 +967,8 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSe
       const int page = __ldg(table + e);
       if (page >= 0 && page < a.pages)
         key = forced(e) ? kForced64
-                        : cache_score64(q, a.group, a.k_mean + (long long)page * 128, lane);
+                        : order64(cache_score<double>(
+                              q, a.group, a.k_mean + (long long)page * 128, lane));
       if (lane == 0) s_key64[e] = key;
     }
     __syncthreads();
@@ -1078,23 +1082,32 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSe
   for (int e = tid; e < n; e += kSelThreads)
     if (s_key[e] >= lo && s_key[e] <= hi) s_cand[atomicAdd(&s_n_cand, 1)] = (uint16_t)e;
   __syncthreads();
-  for (int c = warp; c < n_cand; c += kWarps) {
-    const uint64_t key = cache_score64(
-        q, a.group, a.k_mean + (long long)__ldg(table + s_cand[c]) * 128, lane);
-    if (lane == 0) s_key64[c] = key;
-  }
-  __syncthreads();
   for (int e = tid; e < n; e += kSelThreads) s_key[e] = s_key[e] > hi ? 2u : 0u;
-  __syncthreads();
-  for (int c = tid; c < n_cand; c += kSelThreads) {
-    const uint64_t own = s_key64[c];
-    const int e = s_cand[c];
-    int place = 0;
-    for (int o = 0; o < n_cand; ++o)
-      place += s_key64[o] > own || (s_key64[o] == own && s_cand[o] < e);
-    if (place < need) s_key[e] = 2u;
+  // the candidates' scores from fp32 sums of 19 roundings at most, and from fp64 where the
+  // border's gap is not beyond those
+  auto mean_of = [&](int c) { return a.k_mean + (long long)__ldg(table + s_cand[c]) * 128; };
+  const float tight = 2.0f * 19.5f * 5.9604645e-8f * sum_bound + kTiny;
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int c = warp; c < n_cand; c += kWarps) {
+      const uint64_t key = pass == 0 ? order32(cache_score<float>(q, a.group, mean_of(c), lane))
+                                     : order64(cache_score<double>(q, a.group, mean_of(c), lane));
+      if (lane == 0) s_key64[c] = key;
+    }
+    __syncthreads();
+    for (int c = tid; c < n_cand; c += kSelThreads) {
+      const uint64_t own = s_key64[c];
+      const int e = s_cand[c];
+      int place = 0;
+      for (int o = 0; o < n_cand; ++o)
+        place += s_key64[o] > own || (s_key64[o] == own && s_cand[o] < e);
+      s_key[e] = place < need ? 2u : 0u;
+      if (place == need - 1) s_lo[0] = (uint32_t)own;
+      if (place == need) s_hi[0] = (uint32_t)own;
+    }
+    __syncthreads();
+    if (pass == 0 && unorder32(s_lo[0]) - unorder32(s_hi[0]) > tight) break;
+    __syncthreads();  // both ends are read before they are written again
   }
-  __syncthreads();
   emit(s_key, 1u, 0, k);
 }
 
