@@ -206,34 +206,33 @@ constexpr int kCacheList = 256;                          // blocks listed at a t
 constexpr int kCachePartFloats = 8 * 128 + 16;           // O [8][128], m [8], l [8]
 constexpr int kCacheResident = 2;                        // CTAs an SM holds
 constexpr int kCacheGrid = 152 * kCacheResident;
-constexpr int kCacheLate = 1024;                         // pieces handed out at run time, at most
-constexpr int kCacheLateTokens = 1024;                    // tokens in one, at least
-constexpr int kCacheLateShare = 8;                       // of the units: one in 8
+constexpr int kCacheRowCost = 12;                        // blocks' time that a row costs, at most
 constexpr int kCacheFan = 16;                            // partial results joined at a time
 constexpr int kCacheRingBytes = kCacheWarps * kCacheStages * kCacheStageBytes;
 constexpr int kCacheJoinHeads = 4;                       // heads joined at a time
 constexpr size_t kCacheSmem =
     (size_t)kCacheRingBytes + kCacheWarps * kCacheJoinHeads * 128 * sizeof(float);
-// counters: groups of a row's pieces, rows, the queue and its end, chunks of a head group
-constexpr int kCacheRowCounters = 4096, kCacheQueue = 8190, kCacheChunkCounters = 8192;
+// counters: groups of a row's pieces, rows, chunks of a head group
+constexpr int kCacheRowCounters = 1024, kCacheChunkCounters = 2048;
 
 // A stretch of listed blocks of one row, up to kCacheList of them.
 struct CacheSeg {
-  int piece, row, row_units;
+  int row, blocks;            // the row's blocks, as stated
   long long row_at;           // the row's first unit
-  int first, from, past, to;  // units of the row: the piece's part [first, to), this stretch
+  int first, from, past, to;  // blocks of the row: the piece's part [first, to), this stretch
   int len, held, cnt;         // tokens and blocks of the sequence, blocks in the list
 };
 
-// A row is an 8-head chunk of a (sequence, key/value head).  All rows' blocks form one
-// sequence of units, and the sequence is cut into pieces: one for each CTA (two per SM,
-// one wave) of equal size, and, where there is enough, a last part in small pieces that
-// CTAs fetch from a counter when they are through -- SMs differ in speed by a fifth, and
-// lengths do not matter to such a cut.  A piece may hold several rows and begin and end
-// inside one; a row spread over several pieces leaves a partial result in each, and the
-// last one to arrive joins them in order (beyond 32 in groups of 16, then the groups).
-// Rows whose listing holds duplicates or bad entries count by their stated number; the
-// places that are not there do nothing.
+// A row is an 8-head chunk of a (sequence, key/value head).  All rows form one sequence of
+// units, a row's being a few for what it costs whatever its length and one for each of its
+// blocks, and the sequence is cut into equal pieces, one for each CTA (two per SM, one
+// wave): whatever the lengths, every CTA does the same amount.  A piece may hold several
+// rows and begin and end inside one; a row spread over several pieces leaves a partial
+// result in each, and the last one to arrive joins them in order (beyond 32 in groups of
+// 16, then the groups).  Rows whose listing holds duplicates or bad entries count by their
+// stated number; the places that are not there do nothing.
+// (Pieces of a last part handed out at run time, to even out SMs that differ by a tenth,
+// made no call faster: 193 us with and without for 1.24 GB.)
 //
 // Within a stretch of a row each warp works alone on every fourth block: its own ring of
 // asynchronous copies (32 tokens a stage: 4 KB of keys and of values), its own running
@@ -270,7 +269,7 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
   __shared__ float s_m[kCacheWarps][8], s_l[kCacheWarps][8];
   __shared__ long long s_scan[kCacheWarps];
   __shared__ long long s_at;
-  __shared__ int s_row, s_next, s_last;
+  __shared__ int s_row, s_last;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, i4 = lane & 3;
@@ -279,22 +278,21 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
     const long long len = max(0, a.lens[b]);
     return (int)min((len + BLOCK - 1) / BLOCK, (long long)a.max_blocks);
   };
-  // units of a row: its blocks as stated, 1 at least
-  auto units_of = [&](int row) {
+  // a row's blocks as stated, 1 at least
+  auto blocks_of = [&](int row) {
     const int bh = row / a.chunks;
     int n = held_of(bh / a.Hkv);
     if (a.idx != nullptr) n = min(n, min(a.num[bh], a.max_sel));
     return max(1, n);
   };
 
-  // ---- the pieces: `early` ones of equal size over the first units, then `late` ones of
-  // `size` units
+  // ---- the pieces
   const int per = (a.rows + kThreads - 1) / kThreads;
   const int my0 = min(a.rows, tid * per), my1 = min(a.rows, my0 + per);
-  long long mine_before, mine_sum = 0, total = 0, early_units;
-  int early, late, size;
+  long long mine_before, mine_sum = 0, total = 0;
+  int pieces, cost;
   {
-    for (int r = my0; r < my1; ++r) mine_sum += units_of(r);
+    for (int r = my0; r < my1; ++r) mine_sum += blocks_of(r);
     long long x = mine_sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -309,50 +307,28 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
       if (w < warp) mine_before += s_scan[w];
       total += s_scan[w];
     }
-    early = (int)max(1ll, min((long long)gridDim.x, total / 2));
-    constexpr int kLeast = kCacheLateTokens / BLOCK;
-    const long long part = total / kCacheLateShare;
-    size = (int)max((long long)kLeast, (part + kCacheLate - 1) / kCacheLate);
-    late = part >= 2ll * kLeast * early ? (int)(part / size) : 0;
-    early_units = total - (long long)late * size;
+    pieces = (int)max(1ll, min((long long)gridDim.x, total / 2));
+    cost = (int)min((long long)kCacheRowCost, total / (8ll * pieces));
+    total += (long long)a.rows * cost;
+    mine_before += (long long)my0 * cost;
+    mine_sum += (long long)(my1 - my0) * cost;
   }
-  const int pieces = early + late;
-  auto begin_of = [&](int p) {
-    return p <= early ? early_units * p / early : early_units + (long long)(p - early) * size;
-  };
-  auto piece_of = [&](long long u) {
-    return u < early_units ? (int)(((u + 1) * early - 1) / early_units)
-                           : early + (int)((u - early_units) / size);
-  };
+  auto begin_of = [&](int p) { return total * p / pieces; };
+  auto piece_of = [&](long long u) { return (int)(((u + 1) * pieces - 1) / total); };
+  const int piece = blockIdx.x;
+  if (piece >= pieces) return;
+  const long long piece_from = begin_of(piece), piece_to = begin_of(piece + 1);
 
   // ---- from one stretch to the next; false when there is none.  Uniform over the CTA.
+  // The row's part that lies in the piece, from unit `unit` on (none where the piece ends
+  // among the units before the row's first block).
   auto enter_row = [&](CacheSeg& s, long long unit) {
-    s.row_units = units_of(s.row);
-    s.first = s.from = (int)(unit - s.row_at);
-    s.to = (int)(min(begin_of(s.piece + 1), s.row_at + s.row_units) - s.row_at);
+    s.blocks = blocks_of(s.row);
+    const long long at = s.row_at + cost;
+    s.first = s.from = (int)max(0ll, unit - at);
+    s.to = (int)max(0ll, min((long long)s.blocks, piece_to - at));
     s.past = min(s.to, s.from + kCacheList);
-  };
-  auto enter_piece = [&](CacheSeg& s, int piece) {
-    if (piece >= pieces) return false;
-    const long long lo = begin_of(piece);
-    __syncthreads();
-    if (mine_before <= lo && lo < mine_before + mine_sum) {
-      long long at = mine_before;
-      int r = my0;
-      for (;; ++r) {
-        const int n = units_of(r);
-        if (lo < at + n) break;
-        at += n;
-      }
-      s_row = r;
-      s_at = at;
-    }
-    __syncthreads();
-    s.piece = piece;
-    s.row = s_row;
-    s.row_at = s_at;
-    enter_row(s, lo);
-    return true;
+    return s.from < s.to;
   };
   auto advance = [&](CacheSeg& s) {
     if (s.past < s.to) {  // more of the same row
@@ -360,18 +336,10 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
       s.past = min(s.to, s.from + kCacheList);
       return true;
     }
-    const long long unit = s.row_at + s.to;
-    if (unit < begin_of(s.piece + 1)) {  // the piece's next row
-      s.row_at += s.row_units;
-      ++s.row;
-      enter_row(s, unit);
-      return true;
-    }
-    if (late == 0) return false;
-    __syncthreads();
-    if (tid == 0) s_next = early + (int)atomicAdd(a.counters + kCacheQueue, 1u);
-    __syncthreads();
-    return enter_piece(s, s_next);
+    s.row_at += cost + s.blocks;
+    if (s.row_at >= piece_to) return false;
+    ++s.row;
+    return enter_row(s, s.row_at);
   };
   // ---- a stretch's list of pages, in buffer `buf`
   auto list = [&](CacheSeg& s, int buf) {
@@ -477,7 +445,21 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
   CacheSeg cur, nxt;
   uint4 qw[2][2];
   int buf = 0, slot = 0;  // the list in use; the slot of the next stage to be used
-  bool more = (int)blockIdx.x < pieces && enter_piece(cur, blockIdx.x);
+  if (mine_before <= piece_from && piece_from < mine_before + mine_sum) {
+    long long at = mine_before;
+    int r = my0;
+    for (;; ++r) {
+      const int n = cost + blocks_of(r);
+      if (piece_from < at + n) break;
+      at += n;
+    }
+    s_row = r;
+    s_at = at;
+  }
+  __syncthreads();
+  cur.row = s_row;
+  cur.row_at = s_at;
+  bool more = enter_row(cur, piece_from);
   if (more) {
     fetch_q(cur, qw);
     list(cur, 0);
@@ -739,8 +721,8 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
       }
 
       // ---- join the row's pieces
-      const int piece0 = piece_of(cur.row_at);
-      const int piece1 = piece_of(cur.row_at + cur.row_units - 1);
+      const int piece0 = piece_of(cur.row_at + cost);
+      const int piece1 = piece_of(cur.row_at + cost + cur.blocks - 1);
       auto leave = [&](float* p) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -768,33 +750,13 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
       };
       // A part's place: twice its piece, one more for a row's first part that does not open
       // its piece (another row's last part does).
-      const int odd = begin_of(piece0) != cur.row_at ? 1 : 0;
+      const int odd = begin_of(piece0) != cur.row_at + cost ? 1 : 0;
       auto place_of = [&](int p) { return 2 * p + (p == piece0 ? odd : 0); };
       // `count` <= 32 partial results in order: the s-th at place(s)
       auto join = [&](const float* base, auto place, int count) {
         constexpr int kBatch = 8;
-        float w[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {  // a lane per source: its maximum and sum
-          float pm = -INFINITY, pl = 0.0f;
-          if (lane < count) {
-            const float* p = base + (long long)place(lane) * kCachePartFloats + 4 * x + warp;
-            pm = __ldcg(p + 1024);
-            pl = __ldcg(p + 1032);
-          }
-          float m = pm;
-#pragma unroll
-          for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-          w[x] = pm == -INFINITY ? 0.0f : fast_exp2(pm - m);
-          float l = pl * w[x];
-#pragma unroll
-          for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-          vm[x] = m;
-          vl[x] = l;
-          v[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
-        for (int s0 = 0; s0 < count; s0 += kBatch) {
-          float4 y[kBatch][2];
+        float4 y[kBatch][2];
+        auto fetch = [&](int s0) {
 #pragma unroll
           for (int s = 0; s < kBatch; ++s)
 #pragma unroll
@@ -804,6 +766,34 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
                                   base + (long long)place(s0 + s) * kCachePartFloats +
                                   (4 * x + warp) * 128 + c4))
                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        };
+        float pm[2], pl[2], w[2];  // a lane per source: its maximum, sum and weight
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          pm[x] = -INFINITY;
+          pl[x] = 0.0f;
+          if (lane < count) {
+            const float* p = base + (long long)place(lane) * kCachePartFloats + 4 * x + warp;
+            pm[x] = __ldcg(p + 1024);
+            pl[x] = __ldcg(p + 1032);
+          }
+        }
+        fetch(0);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float m = pm[x];
+#pragma unroll
+          for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+          w[x] = pm[x] == -INFINITY ? 0.0f : fast_exp2(pm[x] - m);
+          float l = pl[x] * w[x];
+#pragma unroll
+          for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+          vm[x] = m;
+          vl[x] = l;
+          v[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        for (int s0 = 0; s0 < count; s0 += kBatch) {
+          if (s0 > 0) fetch(s0);
 #pragma unroll
           for (int s = 0; s < kBatch; ++s)
 #pragma unroll
@@ -819,13 +809,13 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
       const int sharers = piece1 - piece0 + 1;
       bool finish = true;
       if (sharers > 1) {
-        leave(a.part + (long long)place_of(cur.piece) * kCachePartFloats);
+        leave(a.part + (long long)place_of(piece) * kCachePartFloats);
         unsigned int* counter = a.counters + kCacheRowCounters + place_of(piece0);
         if (sharers <= 2 * kCacheFan) {
           finish = last_at(counter, sharers);
           if (finish) join(a.part, [&](int s) { return place_of(piece0 + s); }, sharers);
         } else {
-          const int group = (cur.piece - piece0) / kCacheFan, lead = piece0 + group * kCacheFan;
+          const int group = (piece - piece0) / kCacheFan, lead = piece0 + group * kCacheFan;
           const int groups = (sharers + kCacheFan - 1) / kCacheFan;
           const int count = min(kCacheFan, piece1 + 1 - lead);
           float* wide = a.part + (long long)2 * a.pieces * kCachePartFloats;
@@ -838,35 +828,7 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
             join(a.part, [&](int s) { return place_of(lead + s); }, count);
             leave(wide + (long long)group_place(group) * kCachePartFloats);
             finish = last_at(counter, groups);
-            // (more than 512 pieces in a row: 32 groups at a time)
-            if (finish) {
-              if (groups <= 32) {
-                join(wide, group_place, groups);
-              } else {
-                float4 av[2];
-                float am[2], al[2];
-                for (int s0 = 0; s0 < groups; s0 += 32) {
-                  join(wide, [&](int s) { return group_place(s0 + s); }, min(32, groups - s0));
-#pragma unroll
-                  for (int x = 0; x < 2; ++x) {
-                    if (s0 > 0) {
-                      const float m = fmaxf(am[x], vm[x]);
-                      const float ca = am[x] == -INFINITY ? 0.0f : fast_exp2(am[x] - m);
-                      const float cv = vm[x] == -INFINITY ? 0.0f : fast_exp2(vm[x] - m);
-                      v[x].x = av[x].x * ca + v[x].x * cv;
-                      v[x].y = av[x].y * ca + v[x].y * cv;
-                      v[x].z = av[x].z * ca + v[x].z * cv;
-                      v[x].w = av[x].w * ca + v[x].w * cv;
-                      vl[x] = al[x] * ca + vl[x] * cv;
-                      vm[x] = m;
-                    }
-                    av[x] = v[x];
-                    am[x] = vm[x];
-                    al[x] = vl[x];
-                  }
-                }
-              }
-            }
+            if (finish) join(wide, group_place, groups);
           }
         }
       }
@@ -899,12 +861,25 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
             on = page >= 0 && page < a.pages;
           }
           if (on) {
+            // eight heads of a chunk at a time, in pairs of (sum, maximum)
             float share = 0.0f;
-            const float2* ms = a.mass + (bh * a.max_blocks + j) * a.chunks * 8;
-            for (int h = 0; h < a.group; ++h) {
-              const float2 y = __ldcg(ms + h);
-              const float z = __ldcg(a.lse_ws + bh * a.group + h);
-              if (y.x != 0.0f) share = fmaf(y.x, exp2f(y.y - z), share);
+            const float4* ms = reinterpret_cast<const float4*>(
+                a.mass + (bh * a.max_blocks + j) * a.chunks * 8);
+            for (int h = 0; h < a.group; h += 8) {
+              float4 y[4];
+              float z[8];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) y[x] = __ldcg(ms + h / 2 + x);
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                z[x] = h + x < a.group ? __ldcg(a.lse_ws + bh * a.group + h + x) : 0.0f;
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                if (y[x].x != 0.0f && h + 2 * x < a.group)
+                  share = fmaf(y[x].x, exp2f(y[x].y - z[2 * x]), share);
+                if (y[x].z != 0.0f && h + 2 * x + 1 < a.group)
+                  share = fmaf(y[x].z, exp2f(y[x].w - z[2 * x + 1]), share);
+              }
             }
             w += share;
           }
@@ -919,11 +894,6 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
     if (more) fetch_q(cur, qw);
   }
   cp_async_wait<0>();
-  // the last CTA to end clears the queue
-  if (late > 0 && tid == 0 && atomicAdd(a.counters + kCacheQueue + 1, 1u) == gridDim.x - 1) {
-    a.counters[kCacheQueue] = 0;
-    a.counters[kCacheQueue + 1] = 0;
-  }
 }
 
 // ------------------------------------------------------------------ eviction

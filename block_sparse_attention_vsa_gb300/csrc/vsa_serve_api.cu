@@ -121,9 +121,9 @@ CacheLayout cache_layout(long long B, long long Hq, long long Hkv, long long max
   CacheLayout l;
   l.chunks = (int)((Hq / Hkv + 7) / 8);
   l.part = (size_t)kCacheCounters * sizeof(unsigned int);
-  // pieces of the unit sequence: one a CTA, two units or more each, and the late ones
+  // pieces of the unit sequence: one a CTA, two blocks or more each
   const long long most = B * Hkv * l.chunks * (max_blocks > 0 ? max_blocks : 1);
-  l.pieces = (int)(most < kCacheGrid ? most : kCacheGrid + kCacheLate);
+  l.pieces = (int)(most < kCacheGrid ? most : kCacheGrid);
   l.lse = l.part + up((size_t)(2 * l.pieces + l.pieces / 8 + 2) * kCachePartFloats * sizeof(float));
   l.mass = l.lse + (weight ? up((size_t)(B * Hq) * sizeof(float)) : 0);
   l.total = l.mass +
