@@ -692,6 +692,8 @@ def vsa_fwd_cache(q, cache, table, lens, idx=None, num=None, scale=None, out=Non
     max_sel, idx_p, num_p = 0, None, None
     if idx is not None and num is not None:
         (_, _, max_sel), _ = _lead("idx", idx, torch.int32, 3)
+        if max_sel < 1:  # an empty tensor has no address: it would read as "all blocks"
+            raise ValueError("idx must have room for at least one block")
         idx_p = _need("idx", idx, torch.int32, (B, Hkv, max_sel), dev)
         num_p = _need("num", num, torch.int32, (B, Hkv), dev)
     elif idx is not None or num is not None:

@@ -62,14 +62,9 @@ __global__ void __launch_bounds__(BLOCK * 2) cache_write_kernel(const CacheWrite
   const int n_old = (int)max(0ll, min((long long)BLOCK, len - start));
   const int n_all = (int)min((long long)BLOCK, (long long)len + n - start);
   if (n_all <= n_old) return;
-  const int page = a.table[bh * a.max_blocks + j];
-  if (page < 0 || page >= a.pages) return;
   const bool values = blockIdx.y != 0;
   const int c = tid & 15, r0 = tid >> 4;
   const uint16_t* x = (values ? a.v : a.k) + bh * a.T * 128;  // row r of the page: start-len+r
-  uint8_t* codes = (values ? a.v_cache : a.k_cache) + (long long)page * BLOCK * 128;
-  float* scale = (values ? a.v_scale : a.k_scale) + page;
-
   uint4 w[8];
   uint32_t amax = 0;
 #pragma unroll
@@ -79,14 +74,32 @@ __global__ void __launch_bounds__(BLOCK * 2) cache_write_kernel(const CacheWrite
                ? __ldg(reinterpret_cast<const uint4*>(x + (start - len + r) * 128) + c)
                : make_uint4(0, 0, 0, 0);
   }
+  const int page = a.table[bh * a.max_blocks + j];
+  if (page < 0 || page >= a.pages) return;
+  uint8_t* codes = (values ? a.v_cache : a.k_cache) + (long long)page * BLOCK * 128;
+  float* scale = (values ? a.v_scale : a.k_scale) + page;
+  {  // the largest |x|: NaN does not count; where an infinity does, once more without those
+    __nv_bfloat162 m = as_bf162(0);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    for (int i = 0; i < 8; ++i) {
+      m = __hmax2(m, __habs2(as_bf162(w[i].x)));
+      m = __hmax2(m, __habs2(as_bf162(w[i].y)));
+      m = __hmax2(m, __habs2(as_bf162(w[i].z)));
+      m = __hmax2(m, __habs2(as_bf162(w[i].w)));
+    }
+    amax = __float_as_uint(fmaxf(__low2float(m), __high2float(m))) >> 16;
+    if (amax >= 0x7f80u) {
+      amax = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = u[e] & 0x7fffu, hi = u[e] >> 16 & 0x7fffu;
-      if (lo < 0x7f80u) amax = max(amax, lo);  // infinities saturate, NaN stays NaN
-      if (hi < 0x7f80u) amax = max(amax, hi);
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t lo = u[e] & 0x7fffu, hi = u[e] >> 16 & 0x7fffu;
+          if (lo < 0x7f80u) amax = max(amax, lo);
+          if (hi < 0x7f80u) amax = max(amax, hi);
+        }
+      }
     }
   }
   const float s_old = n_old > 0 ? *scale : 0.0f;
@@ -99,6 +112,7 @@ __global__ void __launch_bounds__(BLOCK * 2) cache_write_kernel(const CacheWrite
   float s = __uint_as_float((uint32_t)(e2 + 127) << 23);
   if (n_old > 0) s = fmaxf(s, s_old);
   const float inv = 1.0f / s, move = n_old > 0 ? s_old / s : 1.0f;
+  const uint64_t inv2 = f32x2(inv, inv);
   const bool moved = n_old > 0 && s != s_old;
   const bool mean = !values && a.k_mean != nullptr;
   float sum[8] = {};
@@ -112,7 +126,11 @@ __global__ void __launch_bounds__(BLOCK * 2) cache_write_kernel(const CacheWrite
       const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
       uint32_t h[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = f32x2_to_e4m3x2(bf16_lo(u[e]) * inv, bf16_hi(u[e]) * inv);
+      for (int e = 0; e < 4; ++e) {
+        float lo, hi;
+        split_f32x2(mul_f32x2(bf16x2_to_f32x2(u[e]), inv2), lo, hi);
+        h[e] = f32x2_to_e4m3x2(lo, hi);
+      }
       o = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
       *at = o;
     } else {
@@ -140,12 +158,8 @@ __global__ void __launch_bounds__(BLOCK * 2) cache_write_kernel(const CacheWrite
       for (int e = 0; e < 2; ++e) {
         uint32_t p, q;
         e4m3x4_to_f16x2(u[e], p, q);
-        const float2 fp = __half22float2(*reinterpret_cast<const __half2*>(&p));
-        const float2 fq = __half22float2(*reinterpret_cast<const __half2*>(&q));
-        sum[4 * e] += fp.x;
-        sum[4 * e + 1] += fp.y;
-        sum[4 * e + 2] += fq.x;
-        sum[4 * e + 3] += fq.y;
+        add_f16x2_to_f32(p, sum[4 * e], sum[4 * e + 1]);
+        add_f16x2_to_f32(q, sum[4 * e + 2], sum[4 * e + 3]);
       }
     }
   }
@@ -673,6 +687,9 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
         l0 += __shfl_xor_sync(0xffffffffu, l0, x);
         l1 += __shfl_xor_sync(0xffffffffu, l1, x);
       }
+      // weights that are not numbers leave the maximum where it was: never as if there were none
+      if (l0 != l0 && m0 == -INFINITY) m0 = 0.0f;
+      if (l1 != l1 && m1 == -INFINITY) m1 = 0.0f;
       if (g == 0) {
         s_m[warp][2 * i4] = m0;
         s_m[warp][2 * i4 + 1] = m1;

@@ -411,14 +411,14 @@ __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
     m = __hmax2(m, __habs2(as_bf162(v.z)));
     return __hmax2(m, __habs2(as_bf162(v.w)));
   };
-  {  // the rows and their sums of |q|; the largest |k| of the first 32 blocks
+  {  // the rows and their sums of |q|; the largest |k| of 32 blocks from all over
     const int r = tid >> 4, c = tid & 15;
     const uint4 v = row0 + r < a.nq
                         ? __ldg(reinterpret_cast<const uint4*>(qh + (long long)(row0 + r) * 128) + c)
                         : make_uint4(0, 0, 0, 0);
-    const uint4 w = r < a.nk
-                        ? __ldg(reinterpret_cast<const uint4*>(kh + (long long)r * 128) + c)
-                        : make_uint4(0, 0, 0, 0);
+    const uint4 w = a.nk > 0 ? __ldg(reinterpret_cast<const uint4*>(
+                                         kh + (long long)(r * a.nk / kSelRows) * 128) + c)
+                             : make_uint4(0, 0, 0, 0);
     reinterpret_cast<uint4*>(s_q[r])[c] = v;
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
     float s = 0.0f;

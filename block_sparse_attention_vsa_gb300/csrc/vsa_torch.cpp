@@ -305,6 +305,7 @@ PyObject* fwd_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int64_t width = 0;
     if (a[4] != Py_None) {
       width = lead(a[4], kI32, 3).size(2);
+      if (width < 1) throw LongWay();  // an empty tensor has no address: not "all blocks"
       idx = need<int32_t>(a[4], kI32, {B, Hkv, width}, dev);
       num = need<int32_t>(a[5], kI32, {B, Hkv}, dev);
     } else if (a[5] != Py_None) {

@@ -91,6 +91,15 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return d;
 }
 
+// acc_lo += fp16 value in bits 0..15 of w, acc_hi += fp16 value in bits 16..31 (fp32 adds of
+// the exact values, no unpacking)
+__device__ __forceinline__ void add_f16x2_to_f32(uint32_t w, float& acc_lo, float& acc_hi) {
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n add.rn.f32.f16 %0, lo, %0;\n"
+      " add.rn.f32.f16 %1, hi, %1;\n}"
+      : "+f"(acc_lo), "+f"(acc_hi)
+      : "r"(w));
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 

@@ -728,3 +728,52 @@ def test_short_and_long_way_agree():
     got = binding.vsa_fwd_cache(q, cache, table, lens, out=out, lse=lse, workspace=ws)
     assert got[0] is out and got[1] is lse
     assert binding.vsa_fwd_cache(q, cache, table, lens, lse=False, workspace=ws)[1] is None
+
+
+def test_an_empty_listing_is_refused_and_an_empty_row_is_empty():
+    g, table, lens, pages, state = cache_case(64, 2, 2, [300, 70], 64)
+    cache, table, lens = to_cache(state), table.to(DEV), lens.to(DEV)
+    q = randn((2, 4, 1, D), g).to(DEV)
+    ws = binding.new_cache_workspace(2, 4, 2, table.shape[2], False, DEV)
+    none = torch.zeros((2, 2, 0), dtype=torch.int32, device=DEV)
+    num = torch.zeros((2, 2), dtype=torch.int32, device=DEV)
+    for stream in (None, torch.cuda.current_stream()):
+        with pytest.raises(ValueError):
+            binding.vsa_fwd_cache(q, cache, table, lens, idx=none, num=num, workspace=ws,
+                                  stream=stream)
+    out, lse = binding.vsa_fwd_cache(q, cache, table, lens, idx=none.new_zeros((2, 2, 3)), num=num,
+                                     workspace=ws)
+    assert (out == 0).all() and (lse == ref.LSE_EMPTY).all()
+
+
+@pytest.mark.parametrize("tokens", [1, 64, 5000])
+def test_fwd_cache_nan_in_an_attended_token(tokens):
+    """A NaN among the attended keys or values makes the row NaN, never an empty one; other
+    sequences and heads do not see it."""
+    g, table, lens, pages, state = cache_case(65, 2, 2, [tokens, tokens], 64)
+    for t in "kv":
+        bad = {x: y.clone() for x, y in state.items()}
+        bad[t][int(table[0, 1, (tokens - 1) // 64]), (tokens - 1) % 64] = math.nan
+        q = randn((2, 4, 1, D), g)
+        weight = torch.zeros(table.shape, device=DEV)
+        out, lse = binding.vsa_fwd_cache(q.to(DEV), to_cache(bad), table.to(DEV), lens.to(DEV),
+                                         weight=weight)
+        assert out[0, 2:].isnan().all()
+        assert lse[0, 2:].isnan().all() == (t == "k")
+        clean = ref.attend(q, state, table, lens, 64)
+        keep = torch.ones(2, 4, 1, dtype=torch.bool)
+        keep[0, 2:] = False
+        ok, want = out.cpu().double()[keep], clean["out"][keep]
+        assert ok.isfinite().all() and (ok - want).abs().max() <= 2.0 ** -7 * clean["vmax"].max()
+
+
+def test_cache_write_without_means():
+    g, table, lens, pages, state = cache_case(66, 1, 2, [50], 64, spare=2)
+    k, v = randn((1, 2, 90, D), g), randn((1, 2, 90, D), g)
+    cache = to_cache(state)
+    for c in (cache._replace(k_mean=None),):
+        binding.vsa_cache_write(c, k.to(DEV), v.to(DEV), table.to(DEV), lens.to(DEV))
+    before = state["k_mean"].clone()
+    ref.cache_write(state, k, v, table, lens, None, 64)
+    check_cache(cache, state, mean=False)
+    assert torch.equal(cache.k_mean.cpu().double(), before)
