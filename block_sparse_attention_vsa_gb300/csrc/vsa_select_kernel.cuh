@@ -277,11 +277,11 @@ struct SelectArgs {
   int Hq, Hkv, group, nq, nk, topk, causal, n_first, n_near, tiles;
 };
 
-constexpr int kSelRows = 32, kSelRowThreads = 512;
+constexpr int kSelRowThreads = 512;
 
 __host__ __device__ constexpr int select_stride(int nreg) { return nreg * 64 + 8; }
-__host__ __device__ constexpr size_t select_smem(int nreg) {
-  return (size_t)kSelRows * select_stride(nreg) * 2;
+__host__ __device__ constexpr size_t select_smem(int nreg, int rows) {
+  return (size_t)rows * select_stride(nreg) * 2;
 }
 
 // Whether block e may be chosen by a row whose diagonal is d, and whether it must be.
@@ -366,8 +366,9 @@ __device__ __forceinline__ int warp_exclusive(int v, int lane) {
   return x - v;
 }
 
-// One CTA: 32 query-block rows of one head against all nk <= 64*NREG key blocks.
-//   1. scores on the tensor cores: a warp walks key tiles of 16 against the 32 rows, whose
+// One CTA: ROWS (32, or 16 where that leaves SMs idle) query-block rows of one head against
+// all nk <= 64*NREG key blocks.
+//   1. scores on the tensor cores: a warp walks key tiles of 16 against the rows, whose
 //      operands lie in shared memory; operands are read 16 bytes a thread with the
 //      contraction index permuted the same way on both sides, so no shuffle or
 //      transposition is needed.  Scores go to shared memory as fp16, times a power of two
@@ -375,21 +376,22 @@ __device__ __forceinline__ int warp_exclusive(int v, int lane) {
 //      would not; the rounding only widens the band that is scored again).
 //   2. a warp per row, a lane with 2*NREG consecutive keys in NREG registers of pairs.
 //      The border is bracketed in the 16-bit order of the keys by counting, two keys an
-//      instruction: outwards from the last row's border, then by interpolation and halving
-//      in turn, until at most 2 keys lie between the brackets' ends.  Blocks surely above
+//      instruction: outwards from where a normal distribution of the row's mean and mean
+//      deviation (of a third of its keys) has it, then by interpolation, aimed at either
+//      side of the border in turn, until at most 2 keys lie between the bracket's ends.  Blocks surely above
 //      the bracket are in; those that the error bound leaves open are scored again.
 // Both parts wait for latencies more than for any unit: 16 warps of 64 registers a CTA,
 // two CTAs on an SM.
-template <int NREG>
+template <int NREG, int ROWS>
 __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
     select_kernel(const SelectArgs a) {
   after_predecessor();
-  extern __shared__ __align__(16) uint16_t s_key[];  // [32][stride]
+  extern __shared__ __align__(16) uint16_t s_key[];  // [ROWS][stride]
   constexpr int kStride = select_stride(NREG), kWarps = kSelRowThreads / 32;
   constexpr int kQStride = 160;  // 320 bytes: rows g and g + 1 in different halves of the banks
-  __shared__ __align__(16) uint16_t s_q[kSelRows][kQStride];
+  __shared__ __align__(16) uint16_t s_q[ROWS][kQStride];
   __shared__ uint32_t s_fair[kMaxBlocks / 32];
-  __shared__ float s_q1[kSelRows];
+  __shared__ float s_q1[ROWS];
   __shared__ uint32_t s_kmax[kWarps];
   __shared__ unsigned int s_slow, s_sample;
   __shared__ uint16_t s_cand[kWarps][32];
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, i4 = lane & 3;
   const long long bh = blockIdx.x / a.tiles;  // b * Hq + hq
-  const int row0 = (int)(blockIdx.x - bh * a.tiles) * kSelRows;
+  const int row0 = (int)(blockIdx.x - bh * a.tiles) * ROWS;
   const long long b = bh / a.Hq;
   const int hkv = (int)(bh - b * a.Hq) / a.group;
   const uint16_t* qh = a.q + (bh * a.nq) * 128;
@@ -413,20 +415,20 @@ __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
   };
   {  // the rows and their sums of |q|; the largest |k| of 32 blocks from all over
     const int r = tid >> 4, c = tid & 15;
-    const uint4 v = row0 + r < a.nq
+    const uint4 v = r < ROWS && row0 + r < a.nq
                         ? __ldg(reinterpret_cast<const uint4*>(qh + (long long)(row0 + r) * 128) + c)
                         : make_uint4(0, 0, 0, 0);
     const uint4 w = a.nk > 0 ? __ldg(reinterpret_cast<const uint4*>(
-                                         kh + (long long)(r * a.nk / kSelRows) * 128) + c)
+                                         kh + (long long)(r * a.nk / 32) * 128) + c)
                              : make_uint4(0, 0, 0, 0);
-    reinterpret_cast<uint4*>(s_q[r])[c] = v;
+    if (r < ROWS) reinterpret_cast<uint4*>(s_q[r])[c] = v;
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
     float s = 0.0f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) s += fabsf(bf16_lo(u[e])) + fabsf(bf16_hi(u[e]));
 #pragma unroll
     for (int x = 8; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    if (c == 0) s_q1[r] = s;
+    if (c == 0 && r < ROWS) s_q1[r] = s;
     const __nv_bfloat162 m = abs_max(as_bf162(0), w);
     const uint32_t mm = __reduce_max_sync(
         0xffffffffu, __float_as_uint(fmaxf(__low2float(m), __high2float(m))));
@@ -451,9 +453,10 @@ __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
 
   // scores
   {
-    float f[4];
+    constexpr int kM = ROWS / 16;
+    float f[2 * kM];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) f[r] = factor_of(g + 8 * r);
+    for (int r = 0; r < 2 * kM; ++r) f[r] = factor_of(g + 8 * r);
     __nv_bfloat162 kmax = as_bf162(0);
     unsigned int bad = 0;
     for (int t = warp; t * 16 < a.nk; t += kWarps) {
@@ -467,11 +470,11 @@ __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
                                         i4 + 4 * j)
                                 : make_uint4(0, 0, 0, 0);
       }
-      float d[2][2][4] = {};
+      float d[kM][2][4] = {};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
+        for (int m = 0; m < kM; ++m) {
           const uint4 qa = reinterpret_cast<const uint4*>(s_q[16 * m + g])[i4 + 4 * j];
           const uint4 qb = reinterpret_cast<const uint4*>(s_q[16 * m + 8 + g])[i4 + 4 * j];
 #pragma unroll
@@ -484,7 +487,7 @@ __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
         kmax = abs_max(kmax, kb[1][j]);
       }
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < kM; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int r = 16 * m + 8 * h + g;
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
         }
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < 2 * kM; ++r)
       if (bad >> r & 1u) atomicOr(&s_slow, 1u << (g + 8 * r));
     const uint32_t mm = __reduce_max_sync(
         0xffffffffu, __float_as_uint(fmaxf(__low2float(kmax), __high2float(kmax))));
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
   __syncthreads();
   for (int e = tid; e < NREG * 64; e += kSelRowThreads)
     if (!(s_fair[e >> 5] >> (e & 31) & 1u))
-      for (int r = 0; r < kSelRows; ++r) s_key[r * kStride + e] = 0x7fff;
+      for (int r = 0; r < ROWS; ++r) s_key[r * kStride + e] = 0x7fff;
   __syncthreads();
 
   uint32_t kmax_bits = 0;
@@ -518,11 +521,8 @@ __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
   for (int w = 0; w < kWarps; ++w) kmax_bits = max(kmax_bits, s_kmax[w]);
   const float kmax = __uint_as_float(kmax_bits);
   constexpr uint32_t kLowest = 0x03ffu, kHighest = 0xfc00u;  // order of -inf and +inf
-  // where the border is looked for first: 1/32 of the largest possible score, as of values
-  // like normal ones, and at the last row's after that
-  uint32_t guess = 0, stride0 = 256;
 
-  for (int r = warp; r < kSelRows; r += kWarps) {
+  for (int r = warp; r < ROWS; r += kWarps) {
     const int row = row0 + r;
     if (row >= a.nq) break;
     if ((s_slow >> r) & 1u) continue;
@@ -572,38 +572,63 @@ __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
         in_thr = cand_thr = 0x7c00u;
         ties = true;
       } else {
-        if (guess == 0) {
-          const float first = fminf(fmaxf(bound * f * 0.03125f, 1e-3f), 60000.0f);
-          guess = __half_as_ushort(__float2half_rn(first)) | 0x8000u;
+        // of a third of the keys, the finite ones: mean and mean deviation from 0
+        __half2 sum2 = as_half2(0), dev2 = as_half2(0), num2 = as_half2(0);
+#pragma unroll
+        for (int j = 0; j < NREG; j += 3) {
+          const __half2 one = __float2half2_rn(1.0f), most = __float2half2_rn(65504.0f);
+          const uint32_t on = __hle2_mask(__habs2(as_half2(key[j])), most);
+          const __half2 x = as_half2(key[j] & on);
+          sum2 = __hadd2(sum2, x);
+          dev2 = __hadd2(dev2, __habs2(x));
+          num2 = __hadd2(num2, as_half2(*reinterpret_cast<const uint32_t*>(&one) & on));
         }
-        uint32_t at = guess, step = stride0;
-        bool halve = false;
+        float sum = __low2float(sum2) + __high2float(sum2);
+        float dev = __low2float(dev2) + __high2float(dev2);
+        float num = __low2float(num2) + __high2float(num2);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) {
+          sum += __shfl_xor_sync(0xffffffffu, sum, x);
+          dev += __shfl_xor_sync(0xffffffffu, dev, x);
+          num += __shfl_xor_sync(0xffffffffu, num, x);
+        }
+        num = fmaxf(num, 1.0f);
+        const float mean = sum / num, sigma = fmaxf(1.2533f * dev / num, fabsf(mean) * 0.01f);
+        const float z = normcdfinvf(1.0f - (float)k / (float)n_ok);
+        // keys lie this far apart around there
+        const float gap = sigma * 2.5066f * __expf(0.5f * z * z) / (float)n_ok;
+        float at_value = mean + z * sigma;
+        float reach = 2.0f;  // keys to go beyond the border by
+        if (!(fabsf(at_value) < 60000.0f && gap < 60000.0f)) at_value = 0.0f;
+        auto order_of = [&](float x) {
+          const uint32_t h = __half_as_ushort(__float2half_rn(x));
+          return (h & 0x8000u) ? ~h & 0xffffu : h | 0x8000u;
+        };
+        uint32_t at = min(max(order_of(at_value), kLowest + 1), kHighest - 1);
+        int tries = 0;
         while (hi - lo > 1 && c_lo - c_hi > 2) {
           const int c = count_ge<NREG>(key, f16_unorder(at));
-          if (c >= k) {
+          const bool above = c >= k;
+          if (above) {
             lo = at;
             c_lo = c;
           } else {
             hi = at;
             c_hi = c;
           }
-          if (lo == kLowest) {
-            at = hi - lo > step ? hi - step : (lo + hi) >> 1;
-            step *= 4;
-          } else if (hi == kHighest) {
-            at = hi - lo > step ? lo + step : (lo + hi) >> 1;
-            step *= 4;
-          } else if (halve) {
-            at = (lo + hi) >> 1;
-            halve = false;
-          } else {
-            at = lo + (hi - lo) * (uint32_t)(c_lo - k) / (uint32_t)(c_lo - c_hi);
-            halve = true;
+          const uint32_t half = (lo + hi) >> 1;
+          if (lo == kLowest || hi == kHighest) {  // out to the border and `reach` keys beyond
+            at_value += above ? ((float)(c - k) + reach) * gap : -((float)(k - c) + reach) * gap;
+            reach *= 4.0f;
+            at = ++tries < 6 && fabsf(at_value) < 65000.0f ? order_of(at_value) : half;
+          } else if (++tries > 8) {
+            at = half;
+          } else {  // half a key past the border, on the side that moved less
+            const float aim = (float)(c_lo - k) + (above ? 1.0f : 0.0f);
+            at = lo + (uint32_t)((float)(hi - lo) * aim / (float)(c_lo - c_hi));
           }
           at = min(max(at, lo + 1), hi - 1);
         }
-        guess = lo == kLowest ? 0 : lo;
-        stride0 = 64;
         if (q1 == 0.0f || kmax == 0.0f) {  // every score is 0
           in_thr = 0x0000u;
           cand_thr = 0x8000u;

@@ -41,7 +41,7 @@ bool outputs_clear(const Range (&out)[NO], const Range (&in)[NI]) {
 constexpr int kSms = 152;
 
 std::mutex g_attr_mu;
-enum AttrSlot { kAttrSel8, kAttrSel16, kAttrSel24, kAttrSel32, kAttrFwd, kAttrSlots = kAttrFwd + 4 };
+enum AttrSlot { kAttrSelect, kAttrFwd = kAttrSelect + 8, kAttrSlots = kAttrFwd + 4 };
 bool g_attr[64][kAttrSlots];
 
 // The dynamic shared-memory limit of a kernel, raised once per device.
@@ -85,12 +85,20 @@ vsa_status launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaS
 
 bool heads_ok(int Hq, int Hkv) { return Hkv >= 1 && Hq % Hkv == 0; }
 
-template <int NREG>
-vsa_status launch_select(const SelectArgs& a, long long ctas, int dev, int slot, cudaStream_t s) {
-  const vsa_status st = smem_limit(select_kernel<NREG>, select_smem(NREG), dev, slot);
+template <int NREG, int ROWS>
+vsa_status launch_select_rows(SelectArgs& a, long long heads, int dev, int slot, cudaStream_t s) {
+  a.tiles = (a.nq + ROWS - 1) / ROWS;
+  const vsa_status st =
+      smem_limit(select_kernel<NREG, ROWS>, select_smem(NREG, ROWS), dev, slot);
   if (st != VSA_OK) return st;
-  return launch(select_kernel<NREG>, dim3((unsigned)ctas), kSelRowThreads, select_smem(NREG), s, 0,
-                a);
+  return launch(select_kernel<NREG, ROWS>, dim3((unsigned)(heads * a.tiles)), kSelRowThreads,
+                select_smem(NREG, ROWS), s, 0, a);
+}
+// 32 rows a CTA, or 16 where the CTAs of 32 would not fill the SMs once.
+template <int NREG>
+vsa_status launch_select(SelectArgs& a, long long heads, int dev, int slot, cudaStream_t s) {
+  if (heads * ((a.nq + 31) / 32) > kSms) return launch_select_rows<NREG, 32>(a, heads, dev, slot, s);
+  return launch_select_rows<NREG, 16>(a, heads, dev, slot + 1, s);
 }
 
 template <int BLOCK, bool WEIGHT>
@@ -175,9 +183,8 @@ vsa_status vsa_select_blocks(const vsa_bf16* q_mean, const vsa_bf16* k_mean, con
   if (D != VSA_HEAD_DIM || nk > VSA_MAX_BLOCKS) return VSA_ERR_UNSUPPORTED;
   if (nq > (1 << 24) || topk > (1 << 24) || (long long)B * Hq > INT_MAX)
     return VSA_ERR_UNSUPPORTED;
-  const long long tiles = ((long long)nq + kSelRows - 1) / kSelRows;
-  const long long rows = (long long)B * Hq * nq, ctas = (long long)B * Hq * tiles;
-  if (ctas > INT_MAX) return VSA_ERR_UNSUPPORTED;
+  const long long heads = (long long)B * Hq, rows = heads * nq;
+  if (heads * (((long long)nq + 15) / 16) > INT_MAX) return VSA_ERR_UNSUPPORTED;
   if (rows == 0) return VSA_OK;
   if (!heads_ok(Hq, Hkv)) return VSA_ERR_INVALID_ARG;
   if (!q_mean || (nk > 0 && !k_mean) || !q2k_idx || !q2k_num || !host_aligned16(q_mean) ||
@@ -208,12 +215,11 @@ vsa_status vsa_select_blocks(const vsa_bf16* q_mean, const vsa_bf16* k_mean, con
   // no more than there are blocks on either side: e - n_near and the like stay in range
   a.n_first = n_first < nk ? n_first : nk;
   a.n_near = n_near < nk + nq ? n_near : nk + nq;
-  a.tiles = (int)tiles;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (nk <= 512) return launch_select<8>(a, ctas, dev, kAttrSel8, s);
-  if (nk <= 1024) return launch_select<16>(a, ctas, dev, kAttrSel16, s);
-  if (nk <= 1536) return launch_select<24>(a, ctas, dev, kAttrSel24, s);
-  return launch_select<32>(a, ctas, dev, kAttrSel32, s);
+  if (nk <= 512) return launch_select<8>(a, heads, dev, kAttrSelect, s);
+  if (nk <= 1024) return launch_select<16>(a, heads, dev, kAttrSelect + 2, s);
+  if (nk <= 1536) return launch_select<24>(a, heads, dev, kAttrSelect + 4, s);
+  return launch_select<32>(a, heads, dev, kAttrSelect + 6, s);
 }
 
 vsa_status vsa_cache_select(const vsa_bf16* q, const vsa_bf16* k_mean, const int32_t* table,
