@@ -1041,7 +1041,7 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSe
     return;
   }
   if (s_forced >= k) {  // more forced blocks than places
-    emit(s_key, kForced32 - 1, 0, k);
+    emit(s_key, kForced32, k, k);
     return;
   }
   uint32_t lo_key = kForced32, hi_key = 0;

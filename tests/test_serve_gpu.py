@@ -777,3 +777,13 @@ def test_cache_write_without_means():
     ref.cache_write(state, k, v, table, lens, None, 64)
     check_cache(cache, state, mean=False)
     assert torch.equal(cache.k_mean.cpu().double(), before)
+
+
+@pytest.mark.parametrize("topk,n_first,n_near", [(1, 2, 3), (3, 1, 3), (4, 3, 3), (2, 0, 40)])
+def test_cache_select_with_more_forced_blocks_than_places(topk, n_first, n_near):
+    """The lowest of the forced blocks are chosen, and nothing is written past a row's end."""
+    g, table, lens, pages, _ = cache_case(67, 3, 2, [700, 64, 5000], 64, codes=False)
+    q, mean = randn((3, 6, 1, D), g), randn((pages, D), g)
+    got = binding.vsa_cache_select(q.to(DEV), mean.to(DEV), table.to(DEV), lens.to(DEV), topk,
+                                   n_first=n_first, n_near=n_near)
+    same(got, ref.cache_select(q, mean, table, lens, topk, 64, n_first, n_near))
