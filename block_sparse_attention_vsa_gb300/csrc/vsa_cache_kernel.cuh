@@ -322,13 +322,18 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
       total += s_scan[w];
     }
     pieces = (int)max(1ll, min((long long)gridDim.x, total / 2));
-    cost = (int)min((long long)kCacheRowCost, total / (8ll * pieces));
+    // no more than an eighth of a piece
+    cost = total >= 8ll * kCacheRowCost * pieces ? kCacheRowCost : (int)((int)total / (8 * pieces));
     total += (long long)a.rows * cost;
     mine_before += (long long)my0 * cost;
     mine_sum += (long long)(my1 - my0) * cost;
   }
-  auto begin_of = [&](int p) { return total * p / pieces; };
-  auto piece_of = [&](long long u) { return (int)(((u + 1) * pieces - 1) / total); };
+  // (a 64-bit division takes a few hundred cycles, one of 32 bits some tens)
+  auto quotient = [](long long x, long long y) {
+    return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+  };
+  auto begin_of = [&](int p) { return quotient(total * p, pieces); };
+  auto piece_of = [&](long long u) { return (int)quotient((u + 1) * pieces - 1, total); };
   const int piece = blockIdx.x;
   if (piece >= pieces) return;
   const long long piece_from = begin_of(piece), piece_to = begin_of(piece + 1);
@@ -930,9 +935,10 @@ struct CacheEvictArgs {
 // memory (sure ones above all, NaN below all) beside the table's row; the last of those
 // that stay is found between the least and the largest weight; then one ascending walk
 // orders what stays and what goes.  Bound by its barriers more than by its bytes.
-__global__ void __launch_bounds__(kSelThreads) cache_evict_kernel(const CacheEvictArgs a) {
+constexpr int kEvictThreads = 512;
+__global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const CacheEvictArgs a) {
   after_predecessor();
-  constexpr int kWarps = kSelThreads / 32;
+  constexpr int kWarps = kEvictThreads / 32, kEach = kMaxBlocks / kEvictThreads;
   __shared__ uint32_t s_key[kMaxBlocks];
   __shared__ float s_weight[kMaxBlocks];
   __shared__ int32_t s_table[kMaxBlocks];
@@ -944,15 +950,27 @@ __global__ void __launch_bounds__(kSelThreads) cache_evict_kernel(const CacheEvi
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long bh = blockIdx.x, row = bh * a.max_blocks;
   const int b = (int)(bh / a.Hkv);
+  // the whole row, before its length is known
+  float weight[kEach];
+  int32_t page[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int e = tid + i * kEvictThreads;
+    weight[i] = e < a.max_blocks ? __ldg(a.weight + row + e) : 0.0f;
+    page[i] = e < a.max_blocks ? __ldg(a.table + row + e) : -1;
+  }
   const int len = max(0, a.lens[b]);
   const int n = (int)min(((long long)len + a.block - 1) / a.block, (long long)a.max_blocks);
   const int gone = max(0, n - a.budget), stay = n - gone;
   uint32_t lo = kForced32, hi = 0;
   int sure = 0;
-  for (int e = tid; e < n; e += kSelThreads) {
-    const float w = a.weight[row + e];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int e = tid + i * kEvictThreads;
+    if (e >= n) continue;
+    const float w = weight[i];
     s_weight[e] = w;
-    s_table[e] = a.table[row + e];
+    s_table[e] = page[i];
     uint32_t key = w != w ? 1u : order32(w);
     if (e < a.n_first || e >= n - a.n_last) {
       key = kForced32;
@@ -996,7 +1014,7 @@ __global__ void __launch_bounds__(kSelThreads) cache_evict_kernel(const CacheEvi
       s_key, n, thr, stay - larger, s_kth, [&](int at, int e) { s_order[at] = (uint16_t)e; },
       [&](int at, int e) { s_order[stay + at] = (uint16_t)e; });
   __syncthreads();
-  for (int at = tid; at < a.max_blocks; at += kSelThreads) {
+  for (int at = tid; at < a.max_blocks; at += kEvictThreads) {
     const int e = at < stay ? s_order[at] : -1, f = at < gone ? s_order[stay + at] : -1;
     a.table_out[row + at] = e >= 0 ? s_table[e] : -1;
     a.weight_out[row + at] = e >= 0 ? s_weight[e] : 0.0f;

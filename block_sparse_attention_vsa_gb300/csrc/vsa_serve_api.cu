@@ -435,7 +435,7 @@ vsa_status vsa_cache_evict(const float* weight, const int32_t* table, const int3
   if (st != VSA_OK) return st;
   const CacheEvictArgs a{weight,     table,    lens,  table_out, weight_out, lens_out, freed,
                          n_freed,    Hkv,      max_blocks, block, budget,    n_first,  n_last};
-  return launch(cache_evict_kernel, dim3((unsigned)rows), kSelThreads, 0,
+  return launch(cache_evict_kernel, dim3((unsigned)rows), kEvictThreads, 0,
                 reinterpret_cast<cudaStream_t>(stream), 0, a);
 }
 
