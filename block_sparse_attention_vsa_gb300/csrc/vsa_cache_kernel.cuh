@@ -935,7 +935,7 @@ struct CacheEvictArgs {
 // memory (sure ones above all, NaN below all) beside the table's row; the last of those
 // that stay is found between the least and the largest weight; then one ascending walk
 // orders what stays and what goes.  Bound by its barriers more than by its bytes.
-constexpr int kEvictThreads = 512;
+constexpr int kEvictThreads = 256;
 __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const CacheEvictArgs a) {
   after_predecessor();
   constexpr int kWarps = kEvictThreads / 32, kEach = kMaxBlocks / kEvictThreads;
