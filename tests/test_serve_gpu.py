@@ -441,6 +441,21 @@ def test_fwd_cache_does_not_read_past_the_sequence():
     check_attend(clean, out, lse)
 
 
+def test_fwd_cache_rows_of_nothing():
+    """Many rows a piece, every other one without a token: a warp may be at the next row's
+    end before another has read this one's statistics."""
+    lens = [(j * 7) % 130 if j % 2 == 0 else 0 for j in range(160)]
+    g, table, lens, pages, state = cache_case(41, 160, 8, lens, 64)
+    q = randn((160, 8, 1, D), g)
+    args = (q.to(DEV), to_cache(state), table.to(DEV), lens.to(DEV))
+    out, lse = binding.vsa_fwd_cache(*args)
+    check_attend(ref.attend(q, state, table, lens, 64), out, lse)
+    ws = binding.new_cache_workspace(160, 8, 8, table.shape[2])
+    for _ in range(20):
+        again = binding.vsa_fwd_cache(*args, workspace=ws)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
 def test_fwd_cache_shared_workspace_streams_and_graphs():
     """One workspace for two shapes in turn, a call on another stream, a captured call
     replayed on new contents: the same bits each time."""
