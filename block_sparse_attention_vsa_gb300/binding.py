@@ -488,6 +488,7 @@ def vsa_set_stall_test(enable: bool) -> None:
 # These calls run for microseconds.  With the tensors on the current device and its current
 # stream they go the short way, one step of C++ that checks, allocates and calls; what that
 # does not take goes the long way below it, which serves the call or says what is wrong.
+# What a call allocates belongs to the stream that it runs on.
 def _short(fn, call, *args):
     """The result of the short way, or None where the long way has to be taken."""
     if _fast is None:
@@ -552,7 +553,8 @@ def vsa_block_mean(x, sizes=None, block=64, out=None, stream=None):
     nb = -(-S // block) if block > 0 else 0
     sizes_p = _maybe("sizes", sizes, torch.int32, (nb,), dev)
     if out is None:
-        out = torch.empty((B, H, nb, D), dtype=torch.bfloat16, device=x.device)
+        with torch.cuda.stream(stream):
+            out = torch.empty((B, H, nb, D), dtype=torch.bfloat16, device=x.device)
     out_p = _need("out", out, torch.bfloat16, (B, H, nb, D), dev)
     _call("vsa_block_mean", dev, stream, x.data_ptr(), sizes_p, B, H, S, D, block, out_p)
     return out
@@ -574,8 +576,9 @@ def vsa_select_blocks(q_mean, k_mean, topk, sizes=None, causal=False, n_first=0,
     (_, Hkv, nk, _), _ = _lead("k_mean", k_mean, torch.bfloat16, 4)
     k_p = _need("k_mean", k_mean, torch.bfloat16, (B, Hkv, nk, D), dev)
     sizes_p = _maybe("sizes", sizes, torch.int32, (nk,), dev)
-    idx = torch.empty((B, Hq, nq, max(0, topk)), dtype=torch.int32, device=q_mean.device)
-    num = torch.empty((B, Hq, nq), dtype=torch.int32, device=q_mean.device)
+    with torch.cuda.stream(stream):
+        idx = torch.empty((B, Hq, nq, max(0, topk)), dtype=torch.int32, device=q_mean.device)
+        num = torch.empty((B, Hq, nq), dtype=torch.int32, device=q_mean.device)
     _call("vsa_select_blocks", dev, stream, q_mean.data_ptr(), k_p, sizes_p, B, Hq, Hkv, nq, nk,
           D, topk, 1 if causal else 0, n_first, n_near, idx.data_ptr(), num.data_ptr())
     return idx, num
@@ -633,8 +636,9 @@ def vsa_cache_select(q, k_mean, table, lens, topk, block=64, n_first=0, n_near=1
     mean_p = _need("k_mean", k_mean, torch.bfloat16, (pages, D), dev)
     Hkv, max_blocks, table_p = _table(table, B, dev)
     lens_p = _need("lens", lens, torch.int32, (B,), dev)
-    idx = torch.empty((B, Hkv, max(0, topk)), dtype=torch.int32, device=q.device)
-    num = torch.empty((B, Hkv), dtype=torch.int32, device=q.device)
+    with torch.cuda.stream(stream):
+        idx = torch.empty((B, Hkv, max(0, topk)), dtype=torch.int32, device=q.device)
+        num = torch.empty((B, Hkv), dtype=torch.int32, device=q.device)
     _call("vsa_cache_select", dev, stream, q_p, mean_p, table_p, lens_p, B, Hq, Hkv, D, pages,
           max_blocks, block, topk, n_first, n_near, idx.data_ptr(), num.data_ptr())
     return idx, num
@@ -700,17 +704,20 @@ def vsa_fwd_cache(q, cache, table, lens, idx=None, num=None, scale=None, out=Non
         raise ValueError("idx and num go together")
     weight_p = _maybe("weight", weight, torch.float32, (B, Hkv, max_blocks), dev)
     if out is None:
-        out = torch.empty_like(q)
+        with torch.cuda.stream(stream):
+            out = torch.empty_like(q)
     out_p = _need("out", out, torch.bfloat16, (B, Hq, 1, D), dev)
     if lse is True:
-        lse = torch.empty((B, Hq, 1), dtype=torch.float32, device=q.device)
+        with torch.cuda.stream(stream):
+            lse = torch.empty((B, Hq, 1), dtype=torch.float32, device=q.device)
     elif lse is False:
         lse = None
     lse_p = _maybe("lse", lse, torch.float32, (B, Hq, 1), dev)
     if workspace is None:
         if Hkv < 1 or Hq < 1 or Hq % Hkv:
             raise ValueError("Hq must be a multiple of table's Hkv")
-        workspace = new_cache_workspace(B, Hq, Hkv, max_blocks, weight is not None, q.device)
+        with torch.cuda.stream(stream):
+            workspace = new_cache_workspace(B, Hq, Hkv, max_blocks, weight is not None, q.device)
     elif not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
     _call("vsa_fwd_cache", dev, stream, q_p, kc, vc, ks, vs, table_p, lens_p, idx_p, num_p,
@@ -743,9 +750,10 @@ def vsa_cache_evict(weight, table, lens, budget, block=64, n_first=0, n_last=1,
     (B, Hkv, max_blocks), dev = _lead("weight", weight, torch.float32, 3)
     table_p = _need("table", table, torch.int32, (B, Hkv, max_blocks), dev)
     lens_p = _need("lens", lens, torch.int32, (B,), dev)
-    table_out, freed = torch.empty_like(table), torch.empty_like(table)
-    lens_out, n_freed = torch.empty_like(lens), torch.empty_like(lens)
-    weight_out = torch.empty_like(weight)
+    with torch.cuda.stream(stream):
+        table_out, freed = torch.empty_like(table), torch.empty_like(table)
+        lens_out, n_freed = torch.empty_like(lens), torch.empty_like(lens)
+        weight_out = torch.empty_like(weight)
     _call("vsa_cache_evict", dev, stream, weight.data_ptr(), table_p, lens_p, B, Hkv, max_blocks,
           block, budget, n_first, n_last, table_out.data_ptr(), weight_out.data_ptr(),
           lens_out.data_ptr(), freed.data_ptr(), n_freed.data_ptr())

@@ -456,6 +456,37 @@ def test_fwd_cache_rows_of_nothing():
         assert torch.equal(again[0], out) and torch.equal(again[1], lse)
 
 
+def test_calls_on_another_stream_while_the_current_one_is_busy():
+    """What a call with a stream allocates (a zeroed workspace among it) is ready on that
+    stream, not behind the current one's work."""
+    g, table, lens, pages, state = cache_case(42, 2, 2, [3000, 500], 64)
+    q = randn((2, 8, 1, D), g).to(DEV)
+    cache, table, lens = to_cache(state), table.to(DEV), lens.to(DEV)
+    weight = torch.rand(table.shape, generator=g).to(DEV)
+    x = randn((1, 2, 1000, D), g).to(DEV)
+
+    def calls(stream):
+        m = binding.vsa_block_mean(x, stream=stream)
+        return (m, *binding.vsa_select_blocks(m, m, 4, stream=stream),
+                *binding.vsa_cache_select(q, cache.k_mean, table, lens, 5, stream=stream),
+                *binding.vsa_fwd_cache(q, cache, table, lens, stream=stream),
+                *binding.vsa_cache_evict(weight, table, lens, 5, stream=stream))
+
+    want = calls(None)
+    busy = torch.ones(4096, 4096, device=DEV)
+    # blocks for the current stream's allocator to hand out, full of ones
+    filled = [torch.ones(1 << 18, dtype=torch.int32, device=DEV) for _ in range(8)]
+    torch.cuda.synchronize()
+    del filled
+    for _ in range(20):
+        busy = busy @ busy
+    side = torch.cuda.Stream()
+    got = calls(side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_fwd_cache_shared_workspace_streams_and_graphs():
     """One workspace for two shapes in turn, a call on another stream, a captured call
     replayed on new contents: the same bits each time."""
