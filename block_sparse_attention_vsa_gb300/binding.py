@@ -521,6 +521,14 @@ def _maybe(name, t, dtype, shape, dev):
     return None if t is None else _need(name, t, dtype, shape, dev)
 
 
+def _whole(name, v):
+    """v, if it is a whole number that the library's 32-bit arguments can hold (ctypes would
+    wrap it round in silence)."""
+    if not isinstance(v, int) or not -2**31 <= v < 2**31:
+        raise ValueError(f"{name} must be a 32-bit whole number, got {v!r}")
+    return v
+
+
 def _lead(name, t, dtype, ndim):
     """(shape, device ordinal) of the tensor that the others of a call go by."""
     _dev(t, name, dtype, ndim)
@@ -549,6 +557,7 @@ def vsa_block_mean(x, sizes=None, block=64, out=None, stream=None):
         r = _short("vsa_block_mean", "block_mean", x, sizes, block, out)
         if r is not None:
             return r[0]
+    _whole("block", block)
     (B, H, S, D), dev = _lead("x", x, torch.bfloat16, 4)
     nb = -(-S // block) if block > 0 else 0
     sizes_p = _maybe("sizes", sizes, torch.int32, (nb,), dev)
@@ -572,6 +581,9 @@ def vsa_select_blocks(q_mean, k_mean, topk, sizes=None, causal=False, n_first=0,
                    n_first, n_near)
         if r is not None:
             return r
+    _whole("topk", topk)
+    _whole("n_first", n_first)
+    _whole("n_near", n_near)
     (B, Hq, nq, D), dev = _lead("q_mean", q_mean, torch.bfloat16, 4)
     (_, Hkv, nk, _), _ = _lead("k_mean", k_mean, torch.bfloat16, 4)
     k_p = _need("k_mean", k_mean, torch.bfloat16, (B, Hkv, nk, D), dev)
@@ -630,6 +642,10 @@ def vsa_cache_select(q, k_mean, table, lens, topk, block=64, n_first=0, n_near=1
                    n_near)
         if r is not None:
             return r
+    _whole("topk", topk)
+    _whole("block", block)
+    _whole("n_first", n_first)
+    _whole("n_near", n_near)
     (B, Hq, _, D), dev = _lead("q", q, torch.bfloat16, 4)
     q_p = _need("q", q, torch.bfloat16, (B, Hq, 1, D), dev)
     (pages, _), _ = _lead("k_mean", k_mean, torch.bfloat16, 2)
@@ -664,6 +680,8 @@ def vsa_cache_write(cache, k, v, table, lens, n_new=None, stream=None):
 
 
 def cache_workspace_bytes(B, Hq, Hkv, max_blocks, weights=False) -> int:
+    for name, v in (("B", B), ("Hq", Hq), ("Hkv", Hkv), ("max_blocks", max_blocks)):
+        _whole(name, v)
     return int(load().vsa_cache_workspace_bytes(B, Hq, Hkv, max_blocks, int(bool(weights))))
 
 
@@ -747,6 +765,10 @@ def vsa_cache_evict(weight, table, lens, budget, block=64, n_first=0, n_last=1,
                    n_last)
         if r is not None:
             return Evicted._make(r)
+    _whole("budget", budget)
+    _whole("block", block)
+    _whole("n_first", n_first)
+    _whole("n_last", n_last)
     (B, Hkv, max_blocks), dev = _lead("weight", weight, torch.float32, 3)
     table_p = _need("table", table, torch.int32, (B, Hkv, max_blocks), dev)
     lens_p = _need("lens", lens, torch.int32, (B,), dev)

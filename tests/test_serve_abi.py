@@ -165,6 +165,24 @@ def test_cache_evict_checks(lib, kw, code):
 
 
 # ------------------------------------------------------------------ the plain forms' pins
+@pytest.mark.parametrize("big", [2**31, 2**32 + 64, -2**31 - 1, 1.5])
+def test_arguments_beyond_32_bits(lib, big):
+    """The binding refuses what a 32-bit argument would wrap round."""
+    x, t = torch.zeros(1, 1, 1, 128, dtype=torch.bfloat16), torch.zeros(1, 1, 1, dtype=torch.int32)
+    calls = [(binding.vsa_block_mean, (x,), {"block": big})]
+    calls += [(binding.vsa_select_blocks, (x, x), {"topk": 1, name: big})
+              for name in ("topk", "n_first", "n_near")]
+    calls += [(binding.vsa_cache_select, (x, x[0, 0], t, t[0, 0]), {"topk": 1, name: big})
+              for name in ("topk", "block", "n_first", "n_near")]
+    calls += [(binding.vsa_cache_evict, (t.float(), t, t[0, 0]), {"budget": 1, name: big})
+              for name in ("budget", "block", "n_first", "n_last")]
+    calls += [(binding.cache_workspace_bytes, tuple(big if i == at else 1 for i in range(4)), {})
+              for at in range(4)]
+    for call, args, names in calls:
+        with pytest.raises(ValueError, match="32-bit"):
+            call(*args, **names)
+
+
 def test_plain_e4m3_values():
     x = torch.tensor([0.0, 1.0, 17.0, 18.0, 19.0, 447.0, 500.0, math.inf, -math.inf, 2.0 ** -9,
                       2.0 ** -10, 3 * 2.0 ** -10, 1.0625, 1.1875, -0.3])
