@@ -94,10 +94,12 @@ vsa_status launch_select_rows(SelectArgs& a, long long heads, int dev, int slot,
   return launch(select_kernel<NREG, ROWS>, dim3((unsigned)(heads * a.tiles)), kSelRowThreads,
                 select_smem(NREG, ROWS), s, 0, a);
 }
-// 32 rows a CTA, or 16 where the CTAs of 32 would not fill the SMs once.
+// 32 rows a CTA, or 16 where the CTAs of 32 would hardly fill the SMs once: 256 x 256 blocks
+// of 12 / 20 / 32 heads took 14.6 / 19.8 / 20.7 us with 32 rows, 13.1 / 17.8 / 23.4 with 16.
 template <int NREG>
 vsa_status launch_select(SelectArgs& a, long long heads, int dev, int slot, cudaStream_t s) {
-  if (heads * ((a.nq + 31) / 32) > kSms) return launch_select_rows<NREG, 32>(a, heads, dev, slot, s);
+  if (heads * ((a.nq + 31) / 32) > kSms + kSms / 8)
+    return launch_select_rows<NREG, 32>(a, heads, dev, slot, s);
   return launch_select_rows<NREG, 16>(a, heads, dev, slot + 1, s);
 }
 
@@ -262,9 +264,10 @@ vsa_status vsa_cache_select(const vsa_bf16* q, const vsa_bf16* k_mean, const int
   a.topk = topk;
   a.n_first = n_first < max_blocks ? n_first : max_blocks;
   a.n_near = n_near < max_blocks ? n_near : max_blocks;
-  // CTAs that share a row's blocks: 1 up to 256 blocks (two tiles a warp), else 4, or 8
-  // where that many fit the device at once
-  const int ctas = max_blocks <= 256 ? 1 : (rows * 8 <= 2 * kSms ? 8 : 4);
+  // CTAs that share a row's blocks: 1 up to 256 blocks (128 rows of 128 blocks: 9.0 us with
+  // one, 11.1 with four), else 4 (32 rows of 1,536: 17.2 with one, 11.4 with four, 12.1 with
+  // eight), or 8 for few rows (8 rows of 1,536: 10.4 with four, 9.9 with eight)
+  const int ctas = max_blocks <= 256 ? 1 : (rows * 8 <= kSms ? 8 : 4);
   if (rows * ctas > INT_MAX) return VSA_ERR_UNSUPPORTED;
   return launch(cache_select_kernel, dim3((unsigned)(rows * ctas)), kSelThreads, 0,
                 reinterpret_cast<cudaStream_t>(stream), ctas, a);
