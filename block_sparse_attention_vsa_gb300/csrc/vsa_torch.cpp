@@ -81,17 +81,17 @@ T* address(const at::Tensor& t) {
 at::Tensor empty(const at::Tensor& like, at::ScalarType type, Shape shape) {
   return at::detail::empty_cuda(at::IntArrayRef(shape), type, like.device(), std::nullopt);
 }
-// Consecutive parts of one allocation, each 256-byte aligned.
+// Consecutive parts of one allocation of 4-byte elements, each 256-byte aligned.
 struct Parts {
   at::Tensor all;
   int64_t at = 0;
   static int64_t room(int64_t n) { return (n + 63) & ~int64_t{63}; }
-  Parts(const at::Tensor& like, at::ScalarType type, int64_t n) : all(empty(like, type, {n})) {}
-  at::Tensor part(Shape shape) {
+  Parts(const at::Tensor& like, int64_t n) : all(empty(like, at::kInt, {n})) {}
+  at::Tensor part(at::ScalarType type, Shape shape) {
     int64_t n = 1;
     for (const int64_t d : shape) n *= d;
     at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
-        c10::Storage(all.storage()), all.key_set(), all.dtype());
+        c10::Storage(all.storage()), all.key_set(), c10::scalarTypeToTypeMeta(type));
     t.unsafeGetTensorImpl()->set_storage_offset(at);
     t.unsafeGetTensorImpl()->set_sizes_contiguous(at::IntArrayRef(shape));
     at += room(n);
@@ -362,11 +362,11 @@ PyObject* cache_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* tp = need<int32_t>(a[1], kI32, {B, Hkv, blocks}, dev);
     const int32_t* lens = need<int32_t>(a[2], kI32, {B}, dev);
     // what goes on living together in one allocation, what is looked at once in another
-    Parts kept(table, kI32, Parts::room(B * Hkv * blocks) + B);
-    Parts went(table, kI32, Parts::room(B * Hkv * blocks) + B);
-    const at::Tensor table_out = kept.part({B, Hkv, blocks}), lens_out = kept.part({B});
-    const at::Tensor freed = went.part({B, Hkv, blocks}), n_freed = went.part({B});
-    const at::Tensor weight_out = empty(weight, kF32, {B, Hkv, blocks});
+    const int64_t cells = Parts::room(B * Hkv * blocks);
+    Parts kept(table, 2 * cells + B), went(table, cells + B);
+    const at::Tensor table_out = kept.part(kI32, {B, Hkv, blocks}),
+                     weight_out = kept.part(kF32, {B, Hkv, blocks}), lens_out = kept.part(kI32, {B});
+    const at::Tensor freed = went.part(kI32, {B, Hkv, blocks}), n_freed = went.part(kI32, {B});
     const float* wp = address<float>(weight);
     float* wo = address<float>(weight_out);
     int32_t *to = address<int32_t>(table_out), *lo = address<int32_t>(lens_out);
