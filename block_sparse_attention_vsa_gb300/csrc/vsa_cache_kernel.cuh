@@ -270,14 +270,21 @@ struct CacheSeg {
 // The 8-bit values are the only large traffic; everything else is arranged so that they
 // arrive without a pause.  Measured: 1.24 GB (8 sequences of up to 98,304 tokens, 64 heads
 // on 8) in 194 us, 6.4 TB/s, which is what DRAM gives to pages in random order; 0.6 GB of 32
-// ragged sequences with weights in 107 us; 50 MB of one sequence's chosen blocks in 19.8
-// us, of which about 5 lie before the first stage and 5 behind the last, mostly a chain of
+// ragged sequences with weights in 106 us; 50 MB of one sequence's chosen blocks in 19.5
+// us (19.9 and 107.5 without the prefetch), of which about 5 lie before the first stage and 5 behind the last, mostly a chain of
 // dependent loads and the join.  (Three CTAs an SM of shorter ranges: 207 us and more; one
 // range a row on the hardware's scheduler: 210 us; a fifth warp for the lists: 205 us, it
 // costs the others registers.)
 template <int BLOCK, bool WEIGHT>
 __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
     cache_fwd_kernel(const CacheFwdArgs a) {
+  {  // the row that this piece begins in, were the rows equal
+    const long long bh = (long long)blockIdx.x * a.rows / gridDim.x / a.chunks;
+    prefetch_l2(a.table + bh * a.max_blocks, (size_t)a.max_blocks * 4, threadIdx.x, blockDim.x);
+    if (a.idx != nullptr)
+      prefetch_l2(a.idx + bh * a.max_sel, (size_t)a.max_sel * 4, threadIdx.x, blockDim.x);
+    prefetch_l2(a.q + bh * a.group * 128, (size_t)a.group * 256, threadIdx.x, blockDim.x);
+  }
   after_predecessor();
   constexpr int kThreads = kCacheWarps * 32;
   constexpr int kHalves = BLOCK / kCacheTile;
@@ -949,6 +956,10 @@ struct CacheEvictArgs {
 // one sequence of 255 blocks and 8 heads, 9.6 us for 64 of up to 1,536 (12 MB).
 constexpr int kEvictThreads = 256;
 __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const CacheEvictArgs a) {
+  prefetch_l2(a.weight + (long long)blockIdx.x * a.max_blocks, (size_t)a.max_blocks * 4,
+              threadIdx.x, kEvictThreads);
+  prefetch_l2(a.table + (long long)blockIdx.x * a.max_blocks, (size_t)a.max_blocks * 4,
+              threadIdx.x, kEvictThreads);
   after_predecessor();
   constexpr int kWarps = kEvictThreads / 32, kEach = kMaxBlocks / kEvictThreads;
   __shared__ uint32_t s_key[kMaxBlocks];

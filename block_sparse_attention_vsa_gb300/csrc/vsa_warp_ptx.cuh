@@ -15,10 +15,17 @@ namespace vsa {
 // stream still runs.  First thing in the kernel: wait until the predecessor has ended and
 // its writes are visible, and let the successor start likewise.  Nothing is read or
 // written before that, so the order of the stream's work is that of ordinary launches; what
-// overlaps is the start-up.
+// overlaps is the start-up, in which lines that the kernel will read may be fetched into L2
+// (where all SMs' writes meet: a line fetched early is never stale).
 __device__ __forceinline__ void after_predecessor() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// `bytes` from `p` on into L2, a line a thread.
+__device__ __forceinline__ void prefetch_l2(const void* p, size_t bytes, int tid, int threads) {
+  for (size_t at = (size_t)tid * 128; at < bytes; at += (size_t)threads * 128)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) + at));
 }
 
 // 16 bytes global -> shared, asynchronously; `n_src` of them are read (0 or 16), the

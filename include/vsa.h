@@ -314,7 +314,7 @@ VSA_API vsa_status vsa_fwd_from_host(const vsa_bf16 *h_q, const vsa_bf16 *h_k, c
  * b and key/value head h, lens[b] (int32 [B]) the tokens that sequence b holds, at most
  * max_blocks * block.  A table entry outside [0, pages) names no page: nothing is written
  * there, and its tokens are not attended or chosen.  Entries past a sequence's last block
- * are not read.  A cache whose pages hold all heads together, [n, Hkv, block, D], is this
+ * are ignored.  A cache whose pages hold all heads together, [n, Hkv, block, D], is this
  * one with pages = n * Hkv and table entries page * Hkv + h.
  * A step of a server: vsa_cache_write the new tokens, add their number to lens,
  * vsa_cache_select (or none: all blocks), vsa_fwd_cache, and now and then
