@@ -271,8 +271,8 @@ struct CacheSeg {
 // arrive without a pause.  Measured: 1.24 GB (8 sequences of up to 98,304 tokens, 64 heads
 // on 8) in 194 us, 6.4 TB/s, which is what DRAM gives to pages in random order; 0.6 GB of 32
 // ragged sequences with weights in 106 us; 50 MB of one sequence's chosen blocks in 19.5
-// us (19.9 and 107.5 without the prefetch), of which about 5 lie before the first stage and 5 behind the last, mostly a chain of
-// dependent loads and the join.  (Three CTAs an SM of shorter ranges: 207 us and more; one
+// us, of which about 5 lie before the first stage and 5 behind the last, mostly a chain of
+// dependent loads and the join (107.5 and 19.9 us without the tables fetched early).  (Three CTAs an SM of shorter ranges: 207 us and more; one
 // range a row on the hardware's scheduler: 210 us; a fifth warp for the lists: 205 us, it
 // costs the others registers.)
 template <int BLOCK, bool WEIGHT>
@@ -282,7 +282,8 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
     const long long bh = (long long)blockIdx.x * a.rows / gridDim.x / a.chunks;
     prefetch_l2(a.table + bh * a.max_blocks, (size_t)a.max_blocks * 4, threadIdx.x, blockDim.x);
     if (a.idx != nullptr)
-      prefetch_l2(a.idx + bh * a.max_sel, (size_t)a.max_sel * 4, threadIdx.x, blockDim.x);
+      prefetch_l2(a.idx + bh * a.max_sel, (size_t)min(a.max_sel, a.max_blocks) * 4, threadIdx.x,
+                  blockDim.x);
     prefetch_l2(a.q + bh * a.group * 128, (size_t)a.group * 256, threadIdx.x, blockDim.x);
   }
   after_predecessor();
