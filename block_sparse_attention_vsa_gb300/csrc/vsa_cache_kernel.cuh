@@ -272,9 +272,9 @@ struct CacheSeg {
 // on 8) in 194 us, 6.4 TB/s, which is what DRAM gives to pages in random order; 0.6 GB of 32
 // ragged sequences with weights in 106 us; 50 MB of one sequence's chosen blocks in 19.5
 // us, of which about 5 lie before the first stage and 5 behind the last, mostly a chain of
-// dependent loads and the join (107.5 and 19.9 us without the tables fetched early).  (Three CTAs an SM of shorter ranges: 207 us and more; one
-// range a row on the hardware's scheduler: 210 us; a fifth warp for the lists: 205 us, it
-// costs the others registers.)
+// dependent loads and the join (107.5 and 19.9 us without the tables fetched early).
+// (Three CTAs an SM of shorter ranges: 207 us and more; one range a row on the hardware's
+// scheduler: 210 us; a fifth warp for the lists: 205 us, it costs the others registers.)
 template <int BLOCK, bool WEIGHT>
 __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
     cache_fwd_kernel(const CacheFwdArgs a) {
