@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(BLOCK * 2) cache_write_kernel(const CacheWrite
   for (int i = 0; i < 8; ++i) {
     const int r = r0 + i * kRowsPerPass;
     w[i] = r >= n_old && r < n_all
-               ? __ldg(reinterpret_cast<const uint4*>(x + (start - len + r) * 128) + c)
+               ? read_global(reinterpret_cast<const uint4*>(x + (start - len + r) * 128) + c)
                : make_uint4(0, 0, 0, 0);
   }
   const int page = a.table[bh * a.max_blocks + j];
@@ -475,7 +475,8 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int p = 0; p < 2; ++p)
-        qw[j][p] = on ? __ldg(reinterpret_cast<const uint4*>(a.q + head * 128) + 2 * (i4 + 4 * j) + p)
+        qw[j][p] = on ? read_global(reinterpret_cast<const uint4*>(a.q + head * 128) +
+                                    2 * (i4 + 4 * j) + p)
                       : make_uint4(0, 0, 0, 0);
   };
 
@@ -954,7 +955,7 @@ struct CacheEvictArgs {
 // memory (sure ones above all, NaN below all) beside the table's row; the last of those
 // that stay is found between the least and the largest weight; then one ascending walk
 // orders what stays and what goes.  Bound by its barriers more than by its bytes: 3.2 us for
-// one sequence of 255 blocks and 8 heads, 9.6 us for 64 of up to 1,536 (12 MB).
+// one sequence of 255 blocks and 8 heads, 8.5 us for 64 of up to 1,536 (12 MB).
 constexpr int kEvictThreads = 256;
 __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const CacheEvictArgs a) {
   prefetch_l2(a.weight + (long long)blockIdx.x * a.max_blocks, (size_t)a.max_blocks * 4,
@@ -980,8 +981,8 @@ __global__ void __launch_bounds__(kEvictThreads) cache_evict_kernel(const CacheE
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int e = tid + i * kEvictThreads;
-    weight[i] = e < a.max_blocks ? __ldg(a.weight + row + e) : 0.0f;
-    page[i] = e < a.max_blocks ? __ldg(a.table + row + e) : -1;
+    weight[i] = e < a.max_blocks ? read_global(a.weight + row + e) : 0.0f;
+    page[i] = e < a.max_blocks ? read_global(a.table + row + e) : -1;
   }
   const int len = max(0, a.lens[b]);
   const int n = (int)min(((long long)len + a.block - 1) / a.block, (long long)a.max_blocks);

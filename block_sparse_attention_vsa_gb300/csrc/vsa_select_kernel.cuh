@@ -25,8 +25,7 @@ namespace vsa {
 // of 98,304 tokens, 9.3 us (5.5 TB/s) for 12 of 16,384.
 template <int BLOCK>
 __global__ void __launch_bounds__(BLOCK * 2)
-    block_mean_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ sizes, int S,
-                      int nb, uint16_t* __restrict__ mean) {
+    block_mean_kernel(const uint16_t* x, const int32_t* sizes, int S, int nb, uint16_t* mean) {
   after_predecessor();
   constexpr int kThreads = BLOCK * 2, kRowsPerPass = kThreads / 16, kWarps = kThreads / 32;
   __shared__ float part[kWarps][128];
@@ -45,7 +44,7 @@ __global__ void __launch_bounds__(BLOCK * 2)
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = r0 + i * kRowsPerPass;
-    w[i] = r < n ? __ldg(src + r * 16) : make_uint4(0, 0, 0, 0);
+    w[i] = r < n ? read_global(src + r * 16) : make_uint4(0, 0, 0, 0);
   }
   float a[8] = {};
 #pragma unroll
@@ -422,12 +421,14 @@ __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
   };
   {  // the rows and their sums of |q|; the largest |k| of 32 blocks from all over
     const int r = tid >> 4, c = tid & 15;
-    const uint4 v = r < ROWS && row0 + r < a.nq
-                        ? __ldg(reinterpret_cast<const uint4*>(qh + (long long)(row0 + r) * 128) + c)
-                        : make_uint4(0, 0, 0, 0);
-    const uint4 w = a.nk > 0 ? __ldg(reinterpret_cast<const uint4*>(
-                                         kh + (long long)(r * a.nk / 32) * 128) + c)
-                             : make_uint4(0, 0, 0, 0);
+    const uint4 v =
+        r < ROWS && row0 + r < a.nq
+            ? read_global(reinterpret_cast<const uint4*>(qh + (long long)(row0 + r) * 128) + c)
+            : make_uint4(0, 0, 0, 0);
+    const uint4 w =
+        a.nk > 0 ? read_global(reinterpret_cast<const uint4*>(
+                                   kh + (long long)(r * a.nk / 32) * 128) + c)
+                 : make_uint4(0, 0, 0, 0);
     if (r < ROWS) reinterpret_cast<uint4*>(s_q[r])[c] = v;
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
     float s = 0.0f;
@@ -473,9 +474,10 @@ __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
         const int key = t * 16 + 8 * x + g;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          kb[x][j] = key < a.nk ? __ldg(reinterpret_cast<const uint4*>(kh + (long long)key * 128) +
-                                        i4 + 4 * j)
-                                : make_uint4(0, 0, 0, 0);
+          kb[x][j] = key < a.nk
+                         ? read_global(reinterpret_cast<const uint4*>(kh + (long long)key * 128) +
+                                       i4 + 4 * j)
+                         : make_uint4(0, 0, 0, 0);
       }
       float d[kM][2][4] = {};
 #pragma unroll
@@ -698,7 +700,7 @@ __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
           T s = zero;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const uint4 kw = __ldg(kp + 8 * x), qw = qp[8 * x];
+            const uint4 kw = read_global(kp + 8 * x), qw = qp[8 * x];
             const uint32_t ku[4] = {kw.x, kw.y, kw.z, kw.w}, qu[4] = {qw.x, qw.y, qw.z, qw.w};
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
@@ -780,7 +782,7 @@ __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
           double s = 0.0;
 #pragma unroll 8
           for (int c = 0; c < 64; ++c) {
-            const uint32_t qw = __ldg(qp + c), kw = __ldg(kp + c);
+            const uint32_t qw = read_global(qp + c), kw = read_global(kp + c);
             s = fma((double)bf16_lo(qw), (double)bf16_lo(kw), s);
             s = fma((double)bf16_hi(qw), (double)bf16_hi(kw), s);
           }
@@ -796,7 +798,8 @@ __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
     if (n_ok > a.topk) kth_largest<uint64_t>(key64, a.nk, k, s_kth, &thr, &larger);
     int32_t* out = a.idx + (bh * a.nq + row) * (long long)a.topk;
     partition_ascending<uint64_t>(
-        key64, a.nk, thr, n_ok > a.topk ? k - larger : 0, s_kth, [&](int at, int e) { out[at] = e; },
+        key64, a.nk, thr, n_ok > a.topk ? k - larger : 0, s_kth,
+        [&](int at, int e) { out[at] = e; },
         [](int, int) {});
     for (int s = k + tid; s < a.topk; s += kSelRowThreads) out[s] = -1;
     if (tid == 0) a.num[bh * a.nq + row] = k;
@@ -826,13 +829,13 @@ template <typename T>
 __device__ __forceinline__ T cache_score(const uint16_t* q, int group, const uint16_t* mean,
                                          int lane) {
   const uint4* kp = reinterpret_cast<const uint4*>(mean) + (lane & 7);
-  const uint4 kw[2] = {__ldg(kp), __ldg(kp + 8)};
+  const uint4 kw[2] = {read_global(kp), read_global(kp + 8)};
   T best = (T)-INFINITY;
   bool nan = false;
   for (int h0 = 0; h0 < group; h0 += 4) {
     const int h = min(h0 + (lane >> 3), group - 1);
     const uint4* qp = reinterpret_cast<const uint4*>(q + (long long)h * 128) + (lane & 7);
-    const uint4 qw[2] = {__ldg(qp), __ldg(qp + 8)};
+    const uint4 qw[2] = {read_global(qp), read_global(qp + 8)};
     T s = 0;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -864,7 +867,7 @@ __device__ __forceinline__ T cache_score(const uint16_t* q, int group, const uin
 // one histogram of 256 even steps of value and a ranking of the step it falls into (where
 // that holds too many, by radix descent); blocks inside the error band of it are scored
 // again, in fp32 and where that leaves the order open in fp64.  Bound by latencies one
-// after another (table, means, two cluster barriers, the histogram's barriers): 16.5 us for
+// after another (table, means, two cluster barriers, the histogram's barriers): 15.8 us for
 // 128 rows of up to 1,536 blocks (ragged, 26 MB), where one CTA a row and a radix descent
 // took 32.6 us.
 __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSelectArgs a) {
@@ -895,7 +898,7 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSe
   uint32_t* const first_bad = cluster.map_shared_rank(&s_bad, 0);
 
   if (tid == 0) s_n_cand = s_ok = s_forced = s_bad = 0;
-  cluster.sync();  // the first CTA runs and has cleared s_bad
+  cluster.barrier_arrive();
 
   auto emit = [&](auto* keys, auto thr, int n_eq, int k) {
     partition_ascending(
@@ -909,14 +912,52 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSe
   __nv_bfloat162 kmax2 = as_bf162(0);
   float q1max = 0.0f;
   const int step = ctas * kWarps;
+  uint4 qb[4];
+  auto heads_from = [&](int h0) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      qb[j] = h0 + g < a.group
+                  ? read_global(reinterpret_cast<const uint4*>(q + (long long)(h0 + g) * 128) +
+                                i4 + 4 * j)
+                  : make_uint4(0, 0, 0, 0);
+  };
+  auto page_of = [&](int t, int r) {
+    const int e = t * 16 + g + 8 * r;
+    return e < n ? read_global(table + e) : -1;
+  };
+  int page[2];
+  uint4 ka[2][4];
+  bool ok[2];
+  auto means_at = [&]() {  // of page[]
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      ok[r] = page[r] >= 0 && page[r] < a.pages;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        ka[r][j] = ok[r] ? read_global(reinterpret_cast<const uint4*>(
+                                           a.k_mean + (long long)page[r] * 128) +
+                                       i4 + 4 * j)
+                         : make_uint4(0, 0, 0, 0);
+    }
+  };
+  // the first tile is fetched while the cluster's CTAs start: only the first CTA's shared
+  // memory has to wait for that (15.8 us; 17.1 with the means behind the barrier, 18.6 with
+  // all three there)
+#pragma unroll
+  for (int r = 0; r < 2; ++r) page[r] = page_of(rank * kWarps + warp, r);
+  heads_from(0);
+  means_at();
+  bool fetched = true;
+  cluster.barrier_wait();  // the first CTA runs and has cleared s_bad
   for (int h0 = 0; h0 < a.group; h0 += 8) {
-    uint4 qb[4];
+    if (h0 > 0) {
+      heads_from(h0);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) page[r] = page_of(rank * kWarps + warp, r);
+    }
     float q1 = 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      qb[j] = h0 + g < a.group
-                  ? __ldg(reinterpret_cast<const uint4*>(q + (long long)(h0 + g) * 128) + i4 + 4 * j)
-                  : make_uint4(0, 0, 0, 0);
       const uint32_t u[4] = {qb[j].x, qb[j].y, qb[j].z, qb[j].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) q1 += fabsf(bf16_lo(u[e])) + fabsf(bf16_hi(u[e]));
@@ -926,28 +967,12 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSe
     q1max = fmaxf(q1max, q1);
     bad |= !(q1 < kFinite);
     const bool c0 = h0 + 2 * i4 < a.group, c1 = h0 + 2 * i4 + 1 < a.group;
-    auto page_of = [&](int t, int r) {
-      const int e = t * 16 + g + 8 * r;
-      return e < n ? __ldg(table + e) : -1;
-    };
-    int page[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) page[r] = page_of(rank * kWarps + warp, r);
     for (int t = rank * kWarps + warp; t * 16 < n; t += step) {
       float d[4] = {};
-      uint4 ka[2][4];
-      bool ok[2];
+      if (!fetched) means_at();
+      fetched = false;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        ok[r] = page[r] >= 0 && page[r] < a.pages;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          ka[r][j] = ok[r] ? __ldg(reinterpret_cast<const uint4*>(a.k_mean +
-                                                                  (long long)page[r] * 128) +
-                                   i4 + 4 * j)
-                           : make_uint4(0, 0, 0, 0);
-        page[r] = page_of(t + step, r);
-      }
+      for (int r = 0; r < 2; ++r) page[r] = page_of(t + step, r);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         mma_bf16(d, ka[0][j].x, ka[1][j].x, ka[0][j].y, ka[1][j].y, qb[j].x, qb[j].y);
@@ -999,7 +1024,7 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSe
     int n_ok = 0;
     for (int e = warp; e < n; e += kWarps) {
       uint64_t key = 0;
-      const int page = __ldg(table + e);
+      const int page = read_global(table + e);
       if (page >= 0 && page < a.pages)
         key = forced(e) ? kForced64
                         : order64(cache_score<double>(
@@ -1120,7 +1145,7 @@ __global__ void __launch_bounds__(kSelThreads) cache_select_kernel(const CacheSe
   for (int e = tid; e < n; e += kSelThreads) s_key[e] = s_key[e] > hi ? 2u : 0u;
   // the candidates' scores from fp32 sums of 19 roundings at most, and from fp64 where the
   // border's gap is not beyond those
-  auto mean_of = [&](int c) { return a.k_mean + (long long)__ldg(table + s_cand[c]) * 128; };
+  auto mean_of = [&](int c) { return a.k_mean + (long long)read_global(table + s_cand[c]) * 128; };
   const float tight = 2.0f * 19.5f * 5.9604645e-8f * sum_bound + kTiny;
   for (int pass = 0; pass < 2; ++pass) {
     for (int c = warp; c < n_cand; c += kWarps) {

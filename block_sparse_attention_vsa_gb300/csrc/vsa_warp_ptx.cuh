@@ -22,6 +22,16 @@ __device__ __forceinline__ void after_predecessor() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// What a call reads may be what its predecessor in the stream writes, and this kernel's life
+// begins before that one's ends: not memory that is read-only for as long as the kernel
+// lives, which the non-coherent path (__ldg, const __restrict__ parameters) asks for and
+// which lets the compiler move a load above the wait.  These kernels read by ordinary loads,
+// which stay behind the wait's memory clobber.
+template <typename T>
+__device__ __forceinline__ T read_global(const T* p) {
+  return *p;
+}
+
 // `bytes` from `p` on into L2, a line a thread.
 __device__ __forceinline__ void prefetch_l2(const void* p, size_t bytes, int tid, int threads) {
   for (size_t at = (size_t)tid * 128; at < bytes; at += (size_t)threads * 128)
