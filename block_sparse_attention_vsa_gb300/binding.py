@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import warnings
 from typing import NamedTuple, Optional
 
 import torch
@@ -46,7 +47,9 @@ class VsaError(RuntimeError):
 
 
 _lib = None
-_fast = None  # the short way (csrc/vsa_torch.cpp) to the calls that run for microseconds
+# the short way (csrc/vsa_torch.cpp) to the calls that run for microseconds; None before load,
+# False where it cannot be had
+_fast = None
 
 
 def load(path: str = LIB_PATH):
@@ -116,15 +119,22 @@ def load(path: str = LIB_PATH):
     h.vsa_fwd_cache.argtypes = [P] * 9 + [i32] * 8 + [f32, f32, P, P, P, P, sz, P]
     h.vsa_cache_evict.restype = i32
     h.vsa_cache_evict.argtypes = [P, P, P] + [i32] * 6 + [P] * 6
+    _fast = _load_fast(h)
+    _lib = h
+    return h
+
+
+def _load_fast(h):
+    """The short way, or False where it cannot be had: every call has a long way without it."""
     try:
         from . import _vsa_torch
     except ImportError as e:
-        raise RuntimeError("_vsa_torch.so is missing or was built for another torch: build it "
-                           "with `python -m block_sparse_attention_vsa_gb300.build`") from e
+        warnings.warn(f"_vsa_torch.so is missing or does not fit this torch ({e}): calls on small "
+                      "tensors take longer on the host.  Build it with `python -m "
+                      "block_sparse_attention_vsa_gb300.build`", RuntimeWarning, stacklevel=3)
+        return False
     _vsa_torch.bind(h._handle)
-    _fast = _vsa_torch
-    _lib = h
-    return h
+    return _vsa_torch
 
 
 def _check(fn: str, code: int):
@@ -493,6 +503,8 @@ def _short(fn, call, *args):
     """The result of the short way, or None where the long way has to be taken."""
     if _fast is None:
         load()
+    if not _fast:
+        return None
     r = getattr(_fast, call)(*args)
     if r.__class__ is int:
         _check(fn, r)
