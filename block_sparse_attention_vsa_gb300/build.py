@@ -46,30 +46,37 @@ def stale(lib: str = LIB, deps=None) -> bool:
     return any(os.path.getmtime(p) > t for p in (deps or DEPS) if os.path.exists(p))
 
 
-def _torch_command(out: str):
-    """The g++ command for _vsa_torch.so, against the headers and libraries of the torch that
-    this Python imports (looked up without importing it)."""
-    torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+def _torch_dir():
+    """The directory of the torch that this Python imports (looked up without importing it),
+    or None: the library itself builds without one."""
+    spec = importlib.util.find_spec("torch")
+    return list(spec.submodule_search_locations)[0] if spec else None
+
+
+def _torch_command(torch_dir: str, out: str):
+    """The g++ command for _vsa_torch.so, against that torch's headers and libraries."""
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     include = [os.path.join(torch_dir, "include"), sysconfig.get_paths()["include"],
                os.path.join(cuda, "include")]
     return (["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", TORCH_SOURCE]
             + [x for d in include for x in ("-isystem", d)]
             + ["-L" + os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
-               "-ltorch_cuda", "-ltorch_python", "-ldl", "-o", out]), os.path.join(torch_dir, "version.py")
+               "-ltorch_cuda", "-ltorch_python", "-ldl", "-o", out])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Build what is older than its sources.  Compilers are looked for only then."""
     jobs = []
     if force or stale():
         tmp = LIB + ".tmp%d" % os.getpid()
         cmd = [nvcc()] + ARCH + FLAGS + (["-Xptxas", "-v"] if verbose else []) + SOURCES + [
             "-o", tmp, "-cudart", "static"]
         jobs.append((cmd, tmp, LIB))
-    tmp = TORCH_LIB + ".tmp%d" % os.getpid()
-    cmd, version = _torch_command(tmp)
-    if force or stale(TORCH_LIB, [TORCH_SOURCE, DEPS[-1], version]):
-        jobs.append((cmd, tmp, TORCH_LIB))
+    torch_dir = _torch_dir()
+    if torch_dir and (force or stale(TORCH_LIB, [TORCH_SOURCE, DEPS[-1],
+                                                 os.path.join(torch_dir, "version.py")])):
+        tmp = TORCH_LIB + ".tmp%d" % os.getpid()
+        jobs.append((_torch_command(torch_dir, tmp), tmp, TORCH_LIB))
     running = [subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
                for cmd, _, _ in jobs]
     said = [p.communicate()[0] for p in running]
