@@ -14,6 +14,7 @@ Functions mirror the C entry points:
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 import warnings
@@ -126,15 +127,19 @@ def load(path: str = LIB_PATH):
 
 def _load_fast(h):
     """The short way, or False where it cannot be had: every call has a long way without it."""
+    from .build import torch_lib
+    path = torch_lib(torch.__version__)
     try:
-        from . import _vsa_torch
+        spec = importlib.util.spec_from_file_location(f"{__package__}._vsa_torch", path)
+        fast = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(fast)
     except ImportError as e:
-        warnings.warn(f"_vsa_torch.so is missing or does not fit this torch ({e}): calls on small "
-                      "tensors take longer on the host.  Build it with `python -m "
+        warnings.warn(f"{path} is missing or does not load ({e}): calls on small tensors take "
+                      "longer on the host.  Build it with `python -m "
                       "block_sparse_attention_vsa_gb300.build`", RuntimeWarning, stacklevel=3)
         return False
-    _vsa_torch.bind(h._handle)
-    return _vsa_torch
+    fast.bind(h._handle)
+    return fast
 
 
 def _check(fn: str, code: int):

@@ -1,5 +1,6 @@
 """Build libvsa_gb300.so (the CUDA kernels + C ABI) in-tree with nvcc for sm_103a, and
-_vsa_torch.so (the short way from torch tensors to its microsecond calls) with g++.
+_vsa_torch_<torch>_<python>.so (the short way from torch tensors to its microsecond calls)
+with g++.
 
     python -m block_sparse_attention_vsa_gb300.build [--force]
 
@@ -10,6 +11,7 @@ from __future__ import annotations
 
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -24,7 +26,6 @@ DEPS = SOURCES + [os.path.join(CSRC, f) for f in (
     "vsa_fwd_kernel.cuh", "vsa_bwd_kernel.cuh", "vsa_select_kernel.cuh", "vsa_cache_kernel.cuh",
     "sm103_ptx.cuh", "vsa_warp_ptx.cuh", "vsa_host.h")] + [
     os.path.join(ROOT, "include", "vsa.h")]
-TORCH_LIB = os.path.join(PKG, "_vsa_torch.so")
 TORCH_SOURCE = os.path.join(CSRC, "vsa_torch.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -53,8 +54,15 @@ def _torch_dir():
     return list(spec.submodule_search_locations)[0] if spec else None
 
 
+def torch_lib(version: str) -> str:
+    """The extension's file for this version of torch and this Python.  It is compiled against
+    the layout of torch's own objects, so each pair has a file of its own."""
+    tag = re.sub(r"[^0-9A-Za-z]+", "_", f"{version} {sysconfig.get_config_var('SOABI')}")
+    return os.path.join(PKG, f"_vsa_torch_{tag}.so")
+
+
 def _torch_command(torch_dir: str, out: str):
-    """The g++ command for _vsa_torch.so, against that torch's headers and libraries."""
+    """The g++ command for the extension, against that torch's headers and libraries."""
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     include = [os.path.join(torch_dir, "include"), sysconfig.get_paths()["include"],
                os.path.join(cuda, "include")]
@@ -73,10 +81,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
             "-o", tmp, "-cudart", "static"]
         jobs.append((cmd, tmp, LIB))
     torch_dir = _torch_dir()
-    if torch_dir and (force or stale(TORCH_LIB, [TORCH_SOURCE, DEPS[-1],
-                                                 os.path.join(torch_dir, "version.py")])):
-        tmp = TORCH_LIB + ".tmp%d" % os.getpid()
-        jobs.append((_torch_command(torch_dir, tmp), tmp, TORCH_LIB))
+    if torch_dir:
+        version = os.path.join(torch_dir, "version.py")
+        with open(version) as f:
+            said = re.search(r"^__version__ *= *['\"](.+?)['\"]", f.read(), re.M)
+        lib = torch_lib(said.group(1))
+        if force or stale(lib, [TORCH_SOURCE, DEPS[-1], version]):
+            tmp = lib + ".tmp%d" % os.getpid()
+            jobs.append((_torch_command(torch_dir, tmp), tmp, lib))
     running = [subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
                for cmd, _, _ in jobs]
     said = [p.communicate()[0] for p in running]
