@@ -1,5 +1,6 @@
 """The short way from torch tensors (the extension built beside the library) only saves host
 time: without it every entry point still loads and serves."""
+import io
 import os
 import subprocess
 import sys
@@ -49,7 +50,8 @@ def test_calls_without_the_short_way(monkeypatch):
     def bf16(*shape):
         return torch.randn(shape, generator=g).to(torch.bfloat16).to(DEV)
 
-    x, q, k, v = bf16(1, 2, 500, 128), bf16(1, 4, 1, 128), bf16(1, 2, 300, 128), bf16(1, 2, 300, 128)
+    x, q = bf16(1, 2, 500, 128), bf16(1, 4, 1, 128)
+    k, v = bf16(1, 2, 300, 128), bf16(1, 2, 300, 128)
     table = torch.arange(12, dtype=torch.int32, device=DEV).view(1, 2, 6)
     none = torch.zeros(1, dtype=torch.int32, device=DEV)
     lens = none + 300
@@ -64,10 +66,35 @@ def test_calls_without_the_short_way(monkeypatch):
         out = binding.vsa_fwd_cache(q, cache, table, lens, idx=idx, num=num, weight=weight,
                                     workspace=ws)
         return (m, *binding.vsa_select_blocks(m, m, 3), idx, num, *out, weight,
-                *(t.view(torch.uint8) for t in cache), *binding.vsa_cache_evict(weight, table, lens, 3))
+                *(t.view(torch.uint8) for t in cache),
+                *binding.vsa_cache_evict(weight, table, lens, 3))
 
     binding.load()
     short = calls()
     monkeypatch.setattr(binding, "_fast", False)
     for a, b in zip(calls(), short):
         assert a.dtype == b.dtype and torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_evicted_tensors_stand_alone():
+    """What an eviction returns can be saved together, and what is kept does not hold
+    the memory of the rest."""
+    libbuild.build()
+    g = torch.Generator().manual_seed(6)
+    weight = torch.rand((2, 3, 10), generator=g).to(DEV)
+    table = torch.arange(60, dtype=torch.int32, device=DEV).view(2, 3, 10)
+    lens = torch.tensor([640, 100], dtype=torch.int32, device=DEV)
+    for stream in (None, torch.cuda.current_stream()):  # the short way, the long way
+        got = binding.vsa_cache_evict(weight, table, lens, 4, stream=stream)
+        kept = io.BytesIO()
+        torch.save(got._asdict(), kept)
+        kept.seek(0)
+        for name, t in torch.load(kept).items():
+            assert torch.equal(t, getattr(got, name))
+        # at most one number a sequence more
+        for t in (got.table, got.weight, got.freed):
+            assert t.untyped_storage().nbytes() <= t.numel() * t.element_size() + 2 * 4
+        apart = {t.untyped_storage().data_ptr() for t in (got.table, got.weight, got.freed)}
+        assert len(apart) == 3
+        assert got.lens.untyped_storage().data_ptr() != got.freed.untyped_storage().data_ptr()
