@@ -5,10 +5,12 @@
 //   select_kernel        LUT rows: the topk key blocks j of highest q_mean_i . k_mean_j
 //   cache_select_kernel  the same for one token per sequence over the pages of a cache
 //
-// The choice is that of the real numbers, ties to the lowest index: scores are first
-// computed on the tensor cores with fp32 sums, and only where the error bound of that
-// arithmetic leaves the border open are the blocks near it scored again (fp32 with a
-// tighter bound, then fp64, in which the products of bf16 values are exact).
+// The choice is that of fp64 sums, ties to the lowest index: scores are first computed on the
+// tensor cores with fp32 sums, and only where the error bound of that arithmetic leaves the
+// border open are the blocks near it scored again (fp32 with a tighter bound, then fp64, in
+// which the products of bf16 values are exact, and their sum while they differ by less than
+// 2^30 in size: 16 bits of a product and 7 of 128 terms fit 53).  The fp64 sum has one order
+// everywhere, that of 8 lanes with 16 products each.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -384,7 +386,7 @@ __device__ __forceinline__ int warp_exclusive(int v, int lane) {
 //      Blocks surely above the bracket are in; those that the error bound leaves open are
 //      scored again.
 // Both parts wait for latencies more than for any unit: 16 warps of 64 registers a CTA,
-// two CTAs on an SM.  24 heads of 1,536 x 1,536 blocks: 147 us, of which the scores are
+// two CTAs on an SM.  24 heads of 1,536 x 1,536 blocks: 149 us, of which the scores are
 // about 64 (the L1 and shared memory's data path: 6 KB read for 16 keys x 32 rows), the
 // border 33, the blocks scored again 18, masks and output 17.  With the scores in bf16, 8
 // warps and 128 registers, and a bisection of all 16 bits it was 267 us.
@@ -777,14 +779,29 @@ __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
         if (select_forced(a, e, d)) {
           key = kForced64;
         } else {
-          const uint32_t* qp = reinterpret_cast<const uint32_t*>(qh + (long long)row * 128);
-          const uint32_t* kp = reinterpret_cast<const uint32_t*>(kh + (long long)e * 128);
-          double s = 0.0;
-#pragma unroll 8
-          for (int c = 0; c < 64; ++c) {
-            const uint32_t qw = read_global(qp + c), kw = read_global(kp + c);
-            s = fma((double)bf16_lo(qw), (double)bf16_lo(kw), s);
-            s = fma((double)bf16_hi(qw), (double)bf16_hi(kw), s);
+          const uint4* qp = reinterpret_cast<const uint4*>(qh + (long long)row * 128);
+          const uint4* kp = reinterpret_cast<const uint4*>(kh + (long long)e * 128);
+          // summed in the order of the 8 lanes that score a candidate above, so that equal rows
+          // have equal scores on either path where the sum is not exact
+          double s = 0.0, one = 0.0, two = 0.0, four = 0.0;
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            const int l = (i & 1) << 2 | (i & 2) | i >> 2;
+            s = 0.0;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint4 qw = read_global(qp + l + 8 * x), kw = read_global(kp + l + 8 * x);
+              const uint32_t qu[4] = {qw.x, qw.y, qw.z, qw.w}, ku[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                s = fma((double)bf16_lo(qu[y]), (double)bf16_lo(ku[y]), s);
+                s = fma((double)bf16_hi(qu[y]), (double)bf16_hi(ku[y]), s);
+              }
+            }
+            // lanes 0 and 4 and so on in pairs, pairs in fours, fours
+            if (i & 1) s += one; else one = s;
+            if ((i & 3) == 3) s += two; else if (i & 1) two = s;
+            if (i == 7) s += four; else if (i == 3) four = s;
           }
           key = order64(s);
         }

@@ -339,9 +339,12 @@ VSA_API vsa_status vsa_block_mean(const vsa_bf16 *x, const int32_t *sizes, int B
  *              score is not NaN
  *   forced     blocks j < n_first or |j - d| < n_near that are eligible but for the score
  *              come before all others whatever their score (a NaN too)
- * Scores are compared as real numbers -- where fp32 sums leave the order open they are
- * computed again in fp64 -- and equal ones go to the lower index, so the choice does not
- * depend on the order of a sum.  A row with nothing eligible gets a count of 0.
+ * Scores are compared by their fp64 sums, and equal ones go to the lower index; fp32 sums
+ * serve where their error bound leaves no doubt.  Products of bf16 values are exact in fp64,
+ * and so is their sum while the products of a score differ by less than 2^30 in size: the
+ * order is then that of the real numbers.  Beyond that the sum, always taken in the same
+ * order, is off by at most 2^-48 of sum |q||k|.  A row with nothing eligible gets a count
+ * of 0.
  *   q_mean [B, Hq, nq, D], k_mean [B, Hkv, nk, D] bf16, 16-byte aligned; nk <=
  *   VSA_MAX_BLOCKS; q2k_idx [B, Hq, nq, topk], q2k_num [B, Hq, nq] int32 outputs, which
  *   must not overlap anything else.  topk >= 1 (it may exceed nk).
