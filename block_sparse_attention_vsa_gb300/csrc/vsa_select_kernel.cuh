@@ -761,7 +761,9 @@ __global__ void __launch_bounds__(kSelRowThreads, NREG <= 24 ? 2 : 1)
   __syncthreads();
 
   // Rows whose scores overflow fp32 or fp16, or with more than 32 blocks inside the error
-  // band (equal blocks, say): every score in fp64, one row at a time by the whole CTA.
+  // band (equal blocks, or means with a large common part): every score in fp64, one row at a
+  // time by the whole CTA.  With every row here 43 ms for 24 heads of 1,536 x 1,536 blocks
+  // (14.5 GFLOP, 0.34 TFLOP/s), 0.94 ms for 12 heads of 256 x 256.
   unsigned int slow = s_slow;
   uint64_t* key64 = reinterpret_cast<uint64_t*>(s_key);  // nk * 8 <= 32 * stride * 2 bytes
   while (slow != 0) {

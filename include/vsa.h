@@ -348,8 +348,12 @@ VSA_API vsa_status vsa_block_mean(const vsa_bf16 *x, const int32_t *sizes, int B
  *   q_mean [B, Hq, nq, D], k_mean [B, Hkv, nk, D] bf16, 16-byte aligned; nk <=
  *   VSA_MAX_BLOCKS; q2k_idx [B, Hq, nq, topk], q2k_num [B, Hq, nq] int32 outputs, which
  *   must not overlap anything else.  topk >= 1 (it may exceed nk).
- * Rows with more than 32 blocks inside the fp32 error band (blocks with equal means, say)
- * take a slower exact path. */
+ * Rows with more than 32 blocks inside the fp32 error band -- blocks with equal means, or
+ * means whose common part is large against what tells them apart -- take a far slower path,
+ * on which every score of the row is an fp64 sum: with every row on it 43 ms instead of 0.15
+ * for 24 heads of 1,536 x 1,536 blocks, 0.94 ms instead of 0.013 for 12 heads of 256 x 256.
+ * A part that all key means share changes no order: with it taken off them beforehand the
+ * rows stay on the fast path. */
 VSA_API vsa_status vsa_select_blocks(const vsa_bf16 *q_mean, const vsa_bf16 *k_mean,
                                      const int32_t *sizes, int B, int Hq, int Hkv, int nq, int nk,
                                      int D, int topk, int causal, int n_first, int n_near,
