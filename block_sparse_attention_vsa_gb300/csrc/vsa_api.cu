@@ -456,13 +456,12 @@ vsa_status host_pipe(HostPipe** out) {
 
 namespace vsa {
 
-vsa_status host_device(int* ordinal, int* sm_count) {
+vsa_status host_device(int* ordinal) {
   DeviceInfo* d = nullptr;
   const vsa_status st = device_info(&d);
   if (st != VSA_OK) return st;
   if (d->major != 10 || d->minor != 3) return VSA_ERR_UNSUPPORTED;
   *ordinal = (int)(d - g_dev);
-  *sm_count = d->sm_count;
   return VSA_OK;
 }
 

@@ -8,9 +8,8 @@
 
 namespace vsa {
 
-// The current device's ordinal (0..63) and SM count; VSA_ERR_UNSUPPORTED if it is not
-// an sm_103 device.
-vsa_status host_device(int* ordinal, int* sm_count);
+// The current device's ordinal (0..63); VSA_ERR_UNSUPPORTED if it is not an sm_103 device.
+vsa_status host_device(int* ordinal);
 
 // What vsa_last_launch_count() reports for this thread.
 void host_set_launches(int n);
