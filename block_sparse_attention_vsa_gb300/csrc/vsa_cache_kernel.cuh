@@ -40,9 +40,11 @@ __device__ __forceinline__ int cache_exponent(uint32_t amax_bits) {
 }
 
 // One CTA per touched page and tensor (blockIdx.y: 0 keys, 1 values); a thread holds 8
-// columns of 8 rows.  The scale is a power of two, so dividing by it and moving held codes
-// to a larger one are exact but for codes that fall below the smallest subnormal, and a
-// page written token by token ends as one written at once.  Bound by the bytes, bf16 in and
+// columns of 8 rows.  The scale is a power of two, so dividing by it is exact, and so is
+// moving held codes to a larger one while they stay normal (2^-6 or more); those that become
+// subnormal are rounded to a multiple of 2^-9 at each move, each move halving the errors of
+// those before: one step in all.  Up to that a page written token by token ends as one
+// written at once.  Bound by the bytes, bf16 in and
 // codes out, once the arithmetic is packed: 31 us and 6.4 TB/s for two prompts of about
 // 12,700 tokens and 8 heads (36 us with 16-bit values taken apart one by one), 3.7 us for one
 // token of 32 sequences.

@@ -379,9 +379,12 @@ VSA_API vsa_status vsa_cache_select(const vsa_bf16 *q, const vsa_bf16 *k_mean,
  * A page's scale is the least power of two s >= 2^-100 with max |x| <= 448 s over its
  * finite values so far, and a code the nearest e4m3 value of x / s (ties to even;
  * infinities become +-448 s, NaN stays NaN).  When a new token raises a page's scale, the
- * codes it holds move to the new one: exactly, but for what falls below the smallest
- * subnormal.  Token by token or at once, a page ends the same up to that.  k_mean (or NULL)
- * gets the mean of the page's keys as now held.  Page bytes of tokens not yet held stay as
+ * codes it holds move to the new one: exactly while they stay normal (2^-6 or more); a code
+ * that becomes subnormal is rounded to a multiple of 2^-9 at each move.  So a page written
+ * token by token ends as one written at once, but for codes up to 2^-6, which may be one
+ * step of 2^-9 apart (and the mean, which is that of the codes held), and for infinities,
+ * which count as 448 times the scale of their time.  k_mean (or NULL) gets the mean of the
+ * page's keys as now held.  Page bytes of tokens not yet held stay as
  * they are, tokens past max_blocks * block are dropped, and what a page held before its
  * first token is ignored.  No two written pages may be the same.  Scales that were not
  * made here must be powers of two. */
