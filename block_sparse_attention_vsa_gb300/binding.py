@@ -776,7 +776,9 @@ def vsa_cache_evict(weight, table, lens, budget, block=64, n_first=0, n_last=1,
                     stream=None) -> Evicted:
     """Cut every sequence to at most `budget` blocks per key/value head: the first n_first
     and last n_last stay, and of the rest those of the highest weight (float32
-    [B,Hkv,max_blocks], as vsa_fwd_cache accumulates it)."""
+    [B,Hkv,max_blocks], as vsa_fwd_cache accumulates it).  Behind the entries that stay the
+    new table holds -1: pages mapped ahead in `table` have to be mapped again, or freed ones
+    in their place, before a write opens the next block."""
     if stream is None:
         r = _short("vsa_cache_evict", "cache_evict", weight, table, lens, budget, block, n_first,
                    n_last)

@@ -433,6 +433,10 @@ VSA_API size_t vsa_cache_workspace_bytes(int B, int Hq, int Hkv, int max_blocks,
  *           then -1 and 0.
  *   lens_out, n_freed      [B]: the tokens still held, and the pages that went, per head.
  *   freed   [B, Hkv, max_blocks]: the pages that went, -1 behind.
+ * Pages mapped ahead of a sequence's last block (table entries from n on) are in neither
+ * table_out nor freed: the caller still has them, in `table`, and has to map them, or freed
+ * ones, behind the new last block before vsa_cache_write opens one there -- where no page is
+ * mapped it drops the token.  This holds for sequences that lost nothing too.
  * The outputs overlap nothing: a server keeps two tables and swaps them.  Codes do not
  * move. */
 VSA_API vsa_status vsa_cache_evict(const float *weight, const int32_t *table,

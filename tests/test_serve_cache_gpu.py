@@ -69,3 +69,58 @@ def test_an_infinity_counts_by_the_scale_of_its_time():
     binding.vsa_cache_write(cache, x[:, :, 1:].contiguous(), x[:, :, 1:].contiguous(), table,
                             i32([1]))
     assert cache.k[0, 0, 0].double().item() * cache.k_scale[0].item() == 448.0 * s
+
+
+def grown(kept, table, block):
+    """The table to go on with: what stays, the pages that went, those mapped ahead."""
+    j = torch.arange(table.shape[2], device=table.device)
+    held, n_freed = ((kept.lens + block - 1) // block)[:, None, None], kept.n_freed[:, None, None]
+    back = kept.freed.gather(2, (j - held).clamp(min=0).expand(table.shape))
+    return torch.where(j < held, kept.table, torch.where(j < held + n_freed, back, table))
+
+
+@pytest.mark.parametrize("block", [64, 128])
+def test_pages_mapped_ahead_through_an_eviction(block):
+    """Sequences that lose nothing, some blocks, and hold nothing; all with pages mapped ahead.
+    Mapped again, every page is there once, and the tokens after land where they should;
+    without it the ones that open a block are dropped."""
+    g = torch.Generator().manual_seed(block)
+    B, H, mb = 3, 2, 12
+    held = [2 * block, 7 * block, 0]
+    table = torch.randperm(B * H * mb, generator=g).to(torch.int32).view(B, H, mb)
+
+    def bf16(T):
+        return torch.randn((B, H, T, D), generator=g).to(torch.bfloat16)
+
+    state = {t: torch.zeros(B * H * mb, block, D).double() for t in "kv"}
+    state.update({t: torch.zeros(B * H * mb).double() for t in ("k_scale", "v_scale")})
+    state["k_mean"] = torch.zeros(B * H * mb, D).double()
+    cache = binding.new_cache8(B * H * mb, block, DEV)
+    k, v, zero, n = bf16(7 * block), bf16(7 * block), torch.zeros(B, dtype=torch.int32), i32(held)
+    binding.vsa_cache_write(cache, k.to(DEV), v.to(DEV), table.to(DEV), zero.to(DEV), n)
+    ref.cache_write(state, k, v, table, zero, n.cpu(), block)
+    weight = torch.rand((B, H, mb), generator=g)
+    kept = binding.vsa_cache_evict(weight.to(DEV), table.to(DEV), n, 4, block=block, n_last=1)
+    want = ref.evict(weight, table, n.cpu(), 4, block, 0, 1)
+    assert kept.n_freed.tolist() == [0, 3, 0] and kept.lens.tolist() == [2 * block, 4 * block, 0]
+    # (nothing behind what stays)
+    for b, at in enumerate((2, 4, 0)):
+        assert (kept.table[b, :, at:] == -1).all()
+    new = grown(kept, table.to(DEV), block)
+    assert new.dtype == torch.int32
+    assert torch.equal(new.flatten(1).sort(-1).values, table.to(DEV).flatten(1).sort(-1).values)
+    assert torch.equal(new[:, :, :4].cpu()[1], want[0][1, :, :4])
+    k, v = bf16(block + 9), bf16(block + 9)
+    lost = [t.clone() for t in (cache.k.view(torch.uint8), cache.k_scale)]
+    binding.vsa_cache_write(cache, k.to(DEV), v.to(DEV), kept.table, kept.lens)
+    assert torch.equal(cache.k.view(torch.uint8), lost[0]) and torch.equal(cache.k_scale, lost[1])
+    binding.vsa_cache_write(cache, k.to(DEV), v.to(DEV), new, kept.lens)
+    ref.cache_write(state, k, v, new.cpu(), kept.lens.cpu(), None, block)
+    for t in "kv":
+        assert torch.equal(getattr(cache, t).cpu().double(), state[t])
+        assert torch.equal(getattr(cache, t + "_scale").cpu().double(), state[t + "_scale"])
+    # attention over the new tokens' blocks finds them
+    q, lens = torch.randn((B, 4, 1, D), generator=g).to(torch.bfloat16), kept.lens + block + 9
+    from test_serve_gpu import check_attend
+    out, lse = binding.vsa_fwd_cache(q.to(DEV), cache, new, lens)
+    check_attend(ref.attend(q, state, new.cpu(), lens.cpu(), block), out, lse)
