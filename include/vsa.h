@@ -400,7 +400,9 @@ VSA_API vsa_status vsa_cache_write(const vsa_bf16 *k, const vsa_bf16 *v, const i
  *   idx     [B, Hkv, max_sel] int32, num [B, Hkv]: the blocks the whole group of a
  *           key/value head attends (counts clamped to [0, max_sel], entries outside the
  *           sequence skipped, a block named twice attended once), or both NULL: every
- *           block.  k_scale, v_scale may be any finite numbers.
+ *           block.  k_scale, v_scale may be any numbers of up to 2^80 in magnitude (and
+ *           scale * |q| up to 2^40): products and sums are taken in fp32, whose range
+ *           larger ones can leave although the result would not.
  *   weight  [B, Hkv, max_blocks] fp32 or NULL: becomes keep * weight + w, w the sum of the
  *           attention weights that the group's heads give the block's tokens (0 for a
  *           block not attended).  keep = 1 accumulates, 0 records this step alone (what

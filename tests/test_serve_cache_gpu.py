@@ -124,3 +124,19 @@ def test_pages_mapped_ahead_through_an_eviction(block):
     from test_serve_gpu import check_attend
     out, lse = binding.vsa_fwd_cache(q.to(DEV), cache, new, lens)
     check_attend(ref.attend(q, state, new.cpu(), lens.cpu(), block), out, lse)
+
+
+@pytest.mark.parametrize("key,value,query", [(80, 80, -80), (-80, -40, 40), (0, 80, 0),
+                                             (80, 0, -100)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_attention_at_the_ends_of_the_scales_range(key, value, query, sign):
+    """Scales of 2^+-80 and of either sign, with queries that bring the scores back to size."""
+    from test_serve_gpu import cache_case, check_attend, to_cache
+    g, table, lens, pages, state = cache_case(81, 2, 2, [700, 70], 64)
+    state["k_scale"] = state["k_scale"] * sign * 2.0 ** key
+    state["v_scale"] = state["v_scale"] * sign * 2.0 ** value
+    q = (torch.randn((2, 8, 1, D), generator=g).double() * 2.0 ** query).to(torch.bfloat16)
+    weight = torch.zeros(table.shape, device=DEV)
+    out, lse = binding.vsa_fwd_cache(q.to(DEV), to_cache(state), table.to(DEV), lens.to(DEV),
+                                     weight=weight)
+    check_attend(ref.attend(q, state, table, lens, 64), out, lse, weight)
