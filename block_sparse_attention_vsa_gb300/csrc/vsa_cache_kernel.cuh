@@ -271,8 +271,8 @@ struct CacheSeg {
 //
 // The 8-bit values are the only large traffic; everything else is arranged so that they
 // arrive without a pause.  Measured: 1.24 GB (8 sequences of up to 98,304 tokens, 64 heads
-// on 8) in 194 us, 6.4 TB/s, which is what DRAM gives to pages in random order; 0.6 GB of 32
-// ragged sequences with weights in 106 us; 50 MB of one sequence's chosen blocks in 19.5
+// on 8) in 193 us, 6.4 TB/s, which is what DRAM gives to pages in random order; 0.6 GB of 32
+// ragged sequences with weights in 107 us; 50 MB of one sequence's chosen blocks in 19.5
 // us, of which about 5 lie before the first stage and 5 behind the last, mostly a chain of
 // dependent loads and the join (107.5 and 19.9 us without the tables fetched early).
 // (Three CTAs an SM of shorter ranges: 207 us and more; one range a row on the hardware's
