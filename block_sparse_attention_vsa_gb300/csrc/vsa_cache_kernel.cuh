@@ -227,6 +227,7 @@ constexpr int kCacheGrid = 152 * kCacheResident;
 constexpr int kCacheRowCost = 12;                        // blocks' time that a row costs, at most
 constexpr int kCacheFan = 16;                            // partial results joined at a time
 constexpr int kCacheRingBytes = kCacheWarps * kCacheStages * kCacheStageBytes;
+constexpr float kNoWeight = -3.4028234663852886e38f;     // the maximum of scores of -infinity
 constexpr int kCacheJoinHeads = 4;                       // heads joined at a time
 constexpr size_t kCacheSmem =
     (size_t)kCacheRingBytes + kCacheWarps * kCacheJoinHeads * 128 * sizeof(float);
@@ -513,6 +514,7 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
   }
   float o[8][4];
   float m0, m1, l0, l1, mass0 = 0.0f, mass1 = 0.0f;
+  bool any = false;  // whether this warp has attended a token of the row
 
   while (more) {
     nxt = cur;
@@ -570,6 +572,7 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
       for (int t = 0; t < 8; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.0f;
       m0 = m1 = -INFINITY;
       l0 = l1 = 0.0f;
+      any = false;
     }
 
     for (int st = 0; st < n_cur; ++st) {
@@ -578,6 +581,7 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
       const int entry = warp + (st / kHalves) * kCacheWarps, half = st % kHalves;
       const int ok = valid_of(cur, buf, entry, half);
       if (ok > 0) {
+        any = true;
         const uint8_t* kt = ring + slot * kCacheStageBytes;
         const uint8_t* vt = kt + kCacheTile * 128;
         const float f0 = qf0 * s_scale[warp][slot][0], f1 = qf1 * s_scale[warp][slot][0];
@@ -713,9 +717,10 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
         l0 += __shfl_xor_sync(0xffffffffu, l0, x);
         l1 += __shfl_xor_sync(0xffffffffu, l1, x);
       }
-      // weights that are not numbers leave the maximum where it was: never as if there were none
-      if (l0 != l0 && m0 == -INFINITY) m0 = 0.0f;
-      if (l1 != l1 && m1 == -INFINITY) m1 = 0.0f;
+      // weights that are not numbers, and scores that are all -infinity, leave the maximum where
+      // it was: never as if there were none
+      if (any && m0 == -INFINITY) m0 = l0 != l0 ? 0.0f : kNoWeight;
+      if (any && m1 == -INFINITY) m1 = l1 != l1 ? 0.0f : kNoWeight;
       if (g == 0) {
         s_m[buf][warp][2 * i4] = m0;
         s_m[buf][warp][2 * i4 + 1] = m1;
@@ -881,7 +886,9 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
         for (int x = 0; x < 2; ++x) {
           const int h = 4 * x + warp;
           if (h >= heads) continue;
-          const float l = vl[x], r = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+          // (tokens, but no weight among them: 0 / 0)
+          const float l = vl[x] == 0.0f && vm[x] != -INFINITY ? NAN : vl[x];
+          const float r = l > 0.0f || l != l ? 1.0f / l : 0.0f;
           uint2 w;
           w.x = pack_bf16x2(v[x].x * r, v[x].y * r);
           w.y = pack_bf16x2(v[x].z * r, v[x].w * r);
@@ -919,9 +926,10 @@ __global__ void __launch_bounds__(kCacheWarps * 32, kCacheResident)
                 z[x] = h + x < a.group ? __ldcg(a.lse_ws + bh * a.group + h + x) : 0.0f;
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
-                if (y[x].x != 0.0f && h + 2 * x < a.group)
+                // (a head whose weights are not numbers makes the share none, be its sum 0)
+                if ((y[x].x != 0.0f || z[2 * x] != z[2 * x]) && h + 2 * x < a.group)
                   share = fmaf(y[x].x, exp2f(y[x].y - z[2 * x]), share);
-                if (y[x].z != 0.0f && h + 2 * x + 1 < a.group)
+                if ((y[x].z != 0.0f || z[2 * x + 1] != z[2 * x + 1]) && h + 2 * x + 1 < a.group)
                   share = fmaf(y[x].z, exp2f(y[x].w - z[2 * x + 1]), share);
               }
             }

@@ -412,7 +412,9 @@ VSA_API vsa_status vsa_cache_write(const vsa_bf16 *k, const vsa_bf16 *v, const i
  *           each call leaves them zero.  It may serve calls of other shapes in turn, but
  *           calls sharing it must not overlap on the GPU (give graphs that may run at the
  *           same time one each).
- * A sequence that attends nothing gets out = +0 and lse = VSA_LSE_EMPTY.  Results do not
+ * A sequence that attends nothing gets out = +0 and lse = VSA_LSE_EMPTY; a head that attends
+ * tokens whose weights are no numbers (a NaN among the scores, or all of them -infinity) gets
+ * NaN in out, lse and the weights.  Results do not
  * depend on timing: splits of a row are joined in their order.  One kernel.
  * B * Hkv * (ceil(Hq / Hkv / 8) + 1) <= 65536. */
 VSA_API vsa_status vsa_fwd_cache(const vsa_bf16 *q, const uint8_t *k_cache,

@@ -140,3 +140,38 @@ def test_attention_at_the_ends_of_the_scales_range(key, value, query, sign):
     out, lse = binding.vsa_fwd_cache(q.to(DEV), to_cache(state), table.to(DEV), lens.to(DEV),
                                      weight=weight)
     check_attend(ref.attend(q, state, table, lens, 64), out, lse, weight)
+
+
+@pytest.mark.parametrize("tokens", [1, 64, 5000])
+@pytest.mark.parametrize("block", [64, 128])
+def test_scores_of_minus_infinity_are_not_an_empty_row(tokens, block):
+    """A query head whose every score is -infinity (an infinite element against keys of one
+    sign) attends tokens: the softmax is not a number, and that shows.  Heads beside it, and a
+    sequence that holds nothing, are as ever."""
+    from test_serve_gpu import cache_case, check_attend, to_cache
+    g, table, lens, pages, state = cache_case(82, 3, 2, [tokens, tokens, 0], block)
+    state["k"][..., 5] = state["k"][..., 5].abs().clamp(min=1.0)
+    q = torch.randn((3, 8, 1, D), generator=g).to(torch.bfloat16)
+    clean = ref.attend(q, state, table, lens, block)
+    bad = q.clone()
+    bad[0, 2, 0, 5] = -math.inf
+    weight = torch.zeros(table.shape, device=DEV)
+    out, lse = binding.vsa_fwd_cache(bad.to(DEV), to_cache(state), table.to(DEV), lens.to(DEV),
+                                     weight=weight)
+    assert out[0, 2].isnan().all() and lse[0, 2].isnan().all()
+    assert weight[0, 0, :-(-tokens // block)].isnan().all()
+    out, lse, weight = out.cpu(), lse.cpu(), weight.cpu()
+    out[0, 2], lse[0, 2] = clean["out"][0, 2].to(torch.bfloat16), clean["lse"][0, 2].float()
+    weight[0, 0] = clean["weight"][0, 0].float()
+    check_attend(clean, out, lse, weight)
+    # weights of nothing in some of the row's parts are nothing: one finite score is enough
+    bad[0, 2, 0, 5] = -3e38
+    far = dict(state, k=state["k"].clone())
+    far["k"][int(table[0, 0, (tokens - 1) // block]), (tokens - 1) % block, 5] = 0.0
+    out, lse = binding.vsa_fwd_cache(bad.to(DEV), to_cache(far), table.to(DEV), lens.to(DEV),
+                                     scale=1.0)
+    last = far["v"][int(table[0, 0, (tokens - 1) // block]), (tokens - 1) % block]
+    want = last * state["v_scale"][int(table[0, 0, (tokens - 1) // block])]
+    # one weight of 1, all others 0: the value, rounded once
+    assert ((out[0, 2, 0].cpu().double() - want).abs() <= 2.0 ** -8 * want.abs()).all()
+    assert lse[0, 2].isfinite().all()
