@@ -37,7 +37,7 @@ EXPORTS = ("vsa_fwd", "jenga_fwd", "vsa_workspace_bytes", "vsa_lut_to_bitmap",
            "vsa_fwd_from_mask", "vsa_fwd_split", "vsa_split_workspace_bytes", "vsa_bwd",
            "vsa_bwd_workspace_bytes", "vsa_set_wait_limit_ns", "vsa_set_stall_test",
            "vsa_block_mean", "vsa_select_blocks", "vsa_cache_select", "vsa_cache_write",
-           "vsa_fwd_cache", "vsa_cache_workspace_bytes", "vsa_cache_evict")
+           "vsa_fwd_cache", "vsa_cache_workspace_bytes", "vsa_cache_evict", "vsa_fwd_prompt")
 MAX_SPLITS = 64
 
 
@@ -120,6 +120,8 @@ def load(path: str = LIB_PATH):
     h.vsa_fwd_cache.argtypes = [P] * 9 + [i32] * 8 + [f32, f32, P, P, P, P, sz, P]
     h.vsa_cache_evict.restype = i32
     h.vsa_cache_evict.argtypes = [P, P, P] + [i32] * 6 + [P] * 6
+    h.vsa_fwd_prompt.restype = i32
+    h.vsa_fwd_prompt.argtypes = [P] * 6 + [i32] * 8 + [f32, P, P, P]
     _fast = _load_fast(h)
     _lib = h
     return h
@@ -799,3 +801,94 @@ def vsa_cache_evict(weight, table, lens, budget, block=64, n_first=0, n_last=1,
           block, budget, n_first, n_last, table_out.data_ptr(), weight_out.data_ptr(),
           lens_out.data_ptr(), freed.data_ptr(), n_freed.data_ptr())
     return Evicted(table_out, weight_out, lens_out, freed, n_freed)
+
+
+# ------------------------------------------------------------- attention over whole prompts
+def _rows(name, t, dtype, ndim, dev=None, shape=None):
+    """A tensor of rows: any strides, but the last axis' elements lie side by side."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must be {ndim}-D, got {t.dim()}-D")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel():
+        raise ValueError(f"{name}'s last axis must have stride 1")
+    return t
+
+
+class _Prompt:
+    """The checked shape of a call over whole prompts: packed [tokens, heads, 128] with starts
+    [B + 1], or a padded batch [B, heads, S, 128] with lengths [B]."""
+
+    def __init__(self, q, k, v, q_seq, k_seq):
+        if not isinstance(q, torch.Tensor):
+            raise TypeError("q must be a torch.Tensor")
+        self.packed = q.dim() == 3
+        ndim = 3 if self.packed else 4
+        _rows("q", q, torch.bfloat16, ndim)
+        self.dev = q.get_device()
+        _rows("k", k, torch.bfloat16, ndim, self.dev)
+        _rows("v", v, torch.bfloat16, ndim, self.dev, k.shape)
+        if self.packed:
+            self.Sq, self.Hq, self.D = q.shape
+            self.Sk, self.Hkv, _ = k.shape
+            if q_seq is None:
+                raise ValueError("packed sequences need their starts, q_seq")
+            k_seq = q_seq if k_seq is None else k_seq
+            self.B = _lead("q_seq", q_seq, torch.int32, 1)[0][0] - 1
+            if self.B < 0:
+                raise ValueError("q_seq must hold the start of every sequence and the end")
+            n = self.B + 1
+        else:
+            self.B, self.Hq, self.Sq, self.D = q.shape
+            Bk, self.Hkv, self.Sk, _ = k.shape
+            if Bk != self.B:
+                raise ValueError(f"k must hold {self.B} sequences, got {Bk}")
+            n = self.B
+        if k.shape[-1] != self.D:
+            raise ValueError(f"k must have heads of {self.D}, got {k.shape[-1]}")
+        self.q_seq = _maybe("q_seq", q_seq, torch.int32, (n,), self.dev)
+        self.k_seq = _maybe("k_seq", k_seq, torch.int32, (n,), self.dev)
+        self.lse = (self.Hq, self.Sq) if self.packed else (self.B, self.Hq, self.Sq)
+
+    def sizes(self):
+        return (self.q_seq, self.k_seq, int(self.packed), self.B, self.Hq, self.Hkv, self.Sq,
+                self.Sk, self.D)
+
+    def strides(self, *tensors):
+        """(batch, head, token) strides of each, as the library takes them."""
+        r = []
+        for t in tensors:
+            s = t.stride()
+            r += [0, s[1], s[0]] if self.packed else s[:3]
+        return (ctypes.c_int64 * len(r))(*r)
+
+
+def vsa_fwd_prompt(q, k, v, q_seq=None, k_seq=None, causal=True, scale=None, out=None, lse=True,
+                   stream=None):
+    """Attention over whole prompts.  Packed: q bf16 [tokens,Hq,128], k, v [tokens,Hkv,128],
+    q_seq, k_seq int32 [B+1] the starts of the sequences and the end (k_seq None: q_seq); rows
+    of no sequence are not written.  Padded: q [B,Hq,Sq,128], k, v [B,Hkv,Sk,128], q_seq,
+    k_seq int32 [B] the sequences' lengths (None: all rows); rows behind a length get 0.  Any
+    strides but the last.  causal: the last query is at the last key, query i attends keys up
+    to i + nk - nq.  Returns (out, lse or None), lse float32 (base 2) [Hq,tokens] or
+    [B,Hq,Sq]."""
+    p = _Prompt(q, k, v, q_seq, k_seq)
+    with torch.cuda.stream(stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is True:
+            lse = torch.empty(p.lse, dtype=torch.float32, device=q.device)
+    _rows("out", out, torch.bfloat16, q.dim(), p.dev, q.shape)
+    lse_p = _maybe("lse", None if lse is False else lse, torch.float32, p.lse, p.dev)
+    _call("vsa_fwd_prompt", p.dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          p.strides(q, k, v, out), *p.sizes(), 1 if causal else 0,
+          1.0 / math.sqrt(p.D) if scale is None else float(scale), out.data_ptr(), lse_p)
+    return out, None if lse is False else lse

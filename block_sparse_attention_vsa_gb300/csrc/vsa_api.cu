@@ -467,6 +467,12 @@ vsa_status host_device(int* ordinal) {
 
 void host_set_launches(int n) { t_last_launches = n; }
 
+unsigned int* host_status_word() { return status_word(); }
+
+unsigned long long host_wait_ns(unsigned long long full) { return launch_wait_ns(full); }
+
+int host_stall() { return g_stall.load(); }
+
 }  // namespace vsa
 
 extern "C" {

@@ -11,6 +11,12 @@ namespace vsa {
 // The current device's ordinal (0..63); VSA_ERR_UNSUPPORTED if it is not an sm_103 device.
 vsa_status host_device(int* ordinal);
 
+// The device status word (null if it cannot be had), and the timeout-path test hooks: the limit
+// of a kernel's waits that are not drains, given its full limit, and the stall switch.
+unsigned int* host_status_word();
+unsigned long long host_wait_ns(unsigned long long full);
+int host_stall();
+
 // What vsa_last_launch_count() reports for this thread.
 void host_set_launches(int n);
 

@@ -1,0 +1,236 @@
+// vsa_prompt_api.cu -- the C ABI of the attention over whole prompts and its gradient
+// (declared in include/vsa.h): host-side argument checks, TMA tensor maps and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+#include <utility>
+
+#include "../../include/vsa.h"
+#include "vsa_host.h"
+#include "vsa_prompt_fwd_kernel.cuh"
+
+using namespace vsa;
+
+namespace {
+
+constexpr int kSms = 152;  // of a GB300, which host_device() asks for
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// A bf16 tensor [batch, heads, tokens, 128] with strides in elements.
+struct View {
+  const void* p;
+  long long nb, nh, nt;
+  long long sb, sh, st;
+  bool empty() const { return nb == 0 || nh == 0 || nt == 0; }
+  long long last() const {  // elements from the first to behind the last one
+    return (nb - 1) * sb + (nh - 1) * sh + (nt - 1) * st + VSA_HEAD_DIM;
+  }
+};
+
+View view(const void* p, const int64_t* s, long long nb, long long nh, long long nt) {
+  View v{p, nb, nh, nt, s[0], s[1], s[2]};
+  // the stride of an axis of one is free: any valid one serves
+  if (nb == 1) v.sb = VSA_HEAD_DIM;
+  if (nh == 1) v.sh = VSA_HEAD_DIM;
+  if (nt == 1) v.st = VSA_HEAD_DIM;
+  return v;
+}
+
+// Address and strides: 16-byte steps, rows that do not overlap, what a tensor map can hold.
+bool view_ok(const View& v) {
+  if (v.empty()) return true;
+  if (!v.p || !host_aligned16(v.p)) return false;
+  for (long long s : {v.sb, v.sh, v.st})
+    if (s < VSA_HEAD_DIM || s % 8 != 0 || s >= (1ll << 38)) return false;
+  return true;
+}
+
+// Whether two tensors share memory.  Ranges that meet may still be parts of one larger tensor:
+// slices of the heads of one token (or of one batch's heads) repeat with the same stride and
+// lie apart inside it.
+bool views_meet(const View& x, const View& y) {
+  if (x.empty() || y.empty()) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  if (a >= b + 2 * (uintptr_t)y.last() || b >= a + 2 * (uintptr_t)x.last()) return false;
+  // modulo a period, an axis whose stride is a multiple of it adds nothing, and the others span
+  // an interval: two intervals that lie apart inside one period never share an element
+  auto span = [](const View& v, long long period) {
+    long long n = VSA_HEAD_DIM;
+    for (const auto& e : {std::pair<long long, long long>(v.nb, v.sb), {v.nh, v.sh}, {v.nt, v.st}})
+      if (e.first > 1 && e.second % period != 0) n += (e.first - 1) * e.second;
+    return n;
+  };
+  for (long long period : {x.sb, x.sh, x.st}) {
+    const long long nx = span(x, period), ny = span(y, period);
+    const long long apart = ((long long)(b - a) / 2 % period + period) % period;  // y behind x
+    if (apart >= nx && apart + ny <= period) return false;
+  }
+  return true;
+}
+
+// Tiles of `heads` heads times `tokens` tokens, 64 of the 128 columns at a time.
+bool make_map(CUtensorMap* m, const View& v, int tokens, int heads) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[4] = {VSA_HEAD_DIM, (cuuint64_t)v.nt, (cuuint64_t)v.nh, (cuuint64_t)v.nb};
+  cuuint64_t strides[3] = {(cuuint64_t)v.st * 2, (cuuint64_t)v.sh * 2, (cuuint64_t)v.sb * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)tokens, (cuuint32_t)heads, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(v.p), dims, strides, box,
+            es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+std::mutex g_attr_mu;
+constexpr int kKernels = 1;
+struct KernelInfo {
+  bool ready;
+  int regs;
+} g_kernel[64][kKernels];
+
+// Dynamic shared memory and the register pool that the kernel's re-balancing draws on.
+template <typename Kern>
+vsa_status prepare(Kern kern, int dev, int slot, uint32_t smem, int threads, uint32_t pool) {
+  std::lock_guard<std::mutex> lk(g_attr_mu);
+  KernelInfo& k = g_kernel[dev][slot];
+  if (!k.ready) {
+    cudaFuncAttributes fa;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+            cudaSuccess ||
+        cudaFuncGetAttributes(&fa, kern) != cudaSuccess) {
+      cudaGetLastError();
+      return VSA_ERR_CUDA;
+    }
+    k.regs = fa.numRegs;
+    k.ready = true;
+  }
+  return (long long)k.regs * threads < (long long)pool ? VSA_ERR_UNSUPPORTED : VSA_OK;
+}
+
+// What both directions check: sizes, heads, types of sequence arrays.
+struct Shape {
+  const int32_t *q_seq, *k_seq;
+  int packed, B, Hq, Hkv, Sq, Sk, D, causal;
+  float scale;
+};
+vsa_status check_shape(const Shape& p) {
+  if (p.B < 0 || p.Hq < 0 || p.Hkv < 0 || p.Sq < 0 || p.Sk < 0) return VSA_ERR_INVALID_ARG;
+  if (p.D != VSA_HEAD_DIM) return VSA_ERR_UNSUPPORTED;
+  if (!(p.scale > 0.0f) || !std::isfinite(p.scale)) return VSA_ERR_INVALID_ARG;
+  if (p.Hq > 0 && (p.Hkv < 1 || p.Hq % p.Hkv != 0)) return VSA_ERR_INVALID_ARG;
+  if (!host_aligned4(p.q_seq) || !host_aligned4(p.k_seq)) return VSA_ERR_INVALID_ARG;
+  if (p.packed && p.B > 0 && (!p.q_seq || !p.k_seq)) return VSA_ERR_INVALID_ARG;
+  // row coordinates, and with 128 rows behind them, stay below 2^31
+  const long long most = INT_MAX - 1024;
+  if (p.Sq > most || p.Sk > most) return VSA_ERR_UNSUPPORTED;
+  return VSA_OK;
+}
+prompt::SeqArgs seq_args(const Shape& p) {
+  return prompt::SeqArgs{p.q_seq, p.k_seq, p.packed ? 1 : 0, p.B, p.Sq, p.Sk, p.causal ? 1 : 0};
+}
+
+// Heads that share a tile: the largest power of two, 16 at most, that divides a group.  A
+// packed tile costs no more than one of a single head, and fills up where tokens are few.
+int pack_log(int group) {
+  int l = 0;
+  while (l < 4 && (group >> l) % 2 == 0) ++l;
+  return l;
+}
+
+bool meets(const View& x, const void* p, long long bytes) {
+  if (x.empty() || !p || bytes <= 0) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(p);
+  return a < b + (uintptr_t)bytes && b < a + 2 * (uintptr_t)x.last();
+}
+
+long long seq_bytes(const Shape& p, const int32_t* s) {
+  return s ? ((long long)p.B + (p.packed ? 1 : 0)) * 4 : 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+vsa_status vsa_fwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* v,
+                          const int64_t* strides, const int32_t* q_seq, const int32_t* k_seq,
+                          int packed, int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal,
+                          float scale, vsa_bf16* out, float* lse, vsa_stream_t stream) {
+  host_set_launches(0);
+  const Shape p{q_seq, k_seq, packed, B, Hq, Hkv, Sq, Sk, D, causal, scale};
+  vsa_status st = check_shape(p);
+  if (st != VSA_OK) return st;
+  if (B == 0 || Hq == 0 || Sq == 0) return VSA_OK;
+  if (!strides) return VSA_ERR_INVALID_ARG;
+  const long long nb = packed ? 1 : B;
+  const View vq = view(q, strides, nb, Hq, Sq), vk = view(k, strides + 3, nb, Hkv, Sk),
+             vv = view(v, strides + 6, nb, Hkv, Sk), vo = view(out, strides + 9, nb, Hq, Sq);
+  for (const View* x : {&vq, &vk, &vv, &vo})
+    if (!view_ok(*x)) return VSA_ERR_INVALID_ARG;
+  if (!host_aligned4(lse)) return VSA_ERR_INVALID_ARG;
+  const long long lse_bytes = lse ? nb * Hq * Sq * 4 : 0;
+  for (const View* x : {&vq, &vk, &vv})
+    if (views_meet(vo, *x) || meets(*x, lse, lse_bytes)) return VSA_ERR_INVALID_ARG;
+  if (meets(vo, lse, lse_bytes) || meets(vo, q_seq, seq_bytes(p, q_seq)) ||
+      meets(vo, k_seq, seq_bytes(p, k_seq)))
+    return VSA_ERR_INVALID_ARG;
+
+  prompt::FwdArgs a{};
+  a.seq = seq_args(p);
+  a.out = out;
+  a.lse = lse;
+  a.out_b = vo.sb;
+  a.out_h = vo.sh;
+  a.out_t = vo.st;
+  a.Hq = Hq;
+  a.group = Hq / Hkv;
+  a.pack = pack_log(a.group);
+  a.n_packs = Hq >> a.pack;
+  const long long slots = prompt::tile_slots(packed, B, Sq, 256 >> a.pack);
+  if (slots * a.n_packs > INT_MAX - 2 * kSms) return VSA_ERR_UNSUPPORTED;
+  a.n_slots = (int)slots;
+  a.n_items = (int)(slots * a.n_packs);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.wait_ns = host_wait_ns(prompt::kWaitLimitNs);
+  a.stall = host_stall();
+
+  int dev = 0;
+  st = host_device(&dev);
+  if (st != VSA_OK) return st;
+  a.status = host_status_word();
+  if (a.status == nullptr) return VSA_ERR_CUDA;
+  st = prepare(prompt::fwd::prompt_fwd_kernel, dev, 0, prompt::fwd::kSmemBytes,
+               prompt::fwd::kThreads, prompt::fwd::kRegPoolNeeded);
+  if (st != VSA_OK) return st;
+  CUtensorMap tq, tk, tv;
+  // without keys nothing is fetched through their maps, which only have to encode
+  if (!make_map(&tq, vq, 128 >> a.pack, 1 << a.pack) || !make_map(&tk, vk.empty() ? vq : vk, 128, 1) ||
+      !make_map(&tv, vv.empty() ? vq : vv, 128, 1))
+    return VSA_ERR_CUDA;
+  const int grid = a.n_items < kSms ? a.n_items : kSms;
+  prompt::fwd::prompt_fwd_kernel<<<grid, prompt::fwd::kThreads, prompt::fwd::kSmemBytes,
+                                   reinterpret_cast<cudaStream_t>(stream)>>>(tq, tk, tv, a);
+  if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
+  host_set_launches(1);
+  return VSA_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,149 @@
+// vsa_prompt_common.cuh -- what the forward and the backward of the attention over whole
+// prompts share: where the sequences lie, how query tiles are numbered, bounded waits.
+//
+// Sequences are packed one behind the other along the token axis (their starts in a device
+// array) or lie in a padded batch (their lengths in one); neither is known to the host.
+// A query tile is 128 rows, the M of one tcgen05 MMA: `heads` = 2^pack query heads that share
+// a key/value head, times 128 / heads consecutive tokens, row = head * tokens + token.  A
+// short sequence, or one token of it, then still fills a tile with the heads of its group.
+//
+// Tile slots.  With T tokens a tile (or item), sequence b owns the slots from
+// A_b = floor(start_b / T) + b on (packed), or b * ceil(S / T) (padded).  For packed sequences
+// ceil(len_b / T) <= A_{b+1} - A_b, as len_b = start_{b+1} - start_b, so slots never meet,
+// there are floor(S / T) + B of them, and a slot's sequence is found from the starts alone by
+// a search; slots that hold no token are passed over.
+#pragma once
+
+#include <cuda.h>
+
+#include <cstdint>
+
+#include "sm103_ptx.cuh"
+
+namespace vsa {
+namespace prompt {
+
+constexpr uint64_t kWaitLimitNs = 1000000000ull;  // one second per wait
+constexpr unsigned kErrTimeout = 0x100u;          // | code of the wait that gave up
+constexpr uint32_t kTile = 128 * 128 * 2;         // 128 rows of Q, K, V or dO
+constexpr float kLseEmpty = -3.402823466e+38f;
+
+struct SeqArgs {
+  const int32_t *q_seq, *k_seq;  // packed: starts [B + 1]; padded: lengths [B] or null
+  int packed, B, Sq, Sk;         // rows of the token axis
+  int causal;
+};
+
+struct Seq {
+  int z, q0, nq, k0, nk;  // batch coordinate, first row and number of queries / keys
+};
+
+__device__ __forceinline__ int clampi(int x, int lo, int hi) {
+  return x < lo ? lo : (x > hi ? hi : x);
+}
+
+// Whatever the arrays hold, the rows lie inside the tensors.
+__device__ __forceinline__ Seq load_seq(const SeqArgs& a, int b) {
+  Seq s;
+  if (a.packed) {
+    s.z = 0;
+    s.q0 = clampi(__ldg(a.q_seq + b), 0, a.Sq);
+    s.nq = clampi(__ldg(a.q_seq + b + 1), s.q0, a.Sq) - s.q0;
+    s.k0 = clampi(__ldg(a.k_seq + b), 0, a.Sk);
+    s.nk = clampi(__ldg(a.k_seq + b + 1), s.k0, a.Sk) - s.k0;
+  } else {
+    s.z = b;
+    s.q0 = s.k0 = 0;
+    s.nq = a.q_seq ? clampi(__ldg(a.q_seq + b), 0, a.Sq) : a.Sq;
+    s.nk = a.k_seq ? clampi(__ldg(a.k_seq + b), 0, a.Sk) : a.Sk;
+  }
+  return s;
+}
+
+__host__ __device__ inline long long tile_slots(int packed, long long B, long long S, int T) {
+  return packed ? S / T + B : B * ((S + T - 1) / T);
+}
+
+// The packed sequence that owns a slot, by a whole warp: 32 candidates a step.
+// `seq` holds starts, S bounds them; *tile is the slot's place in the sequence (it can lie
+// outside of it).
+__device__ __forceinline__ int find_slot(const int32_t* seq, int B, int S, int T, int slot,
+                                         int* tile) {
+  const int lane = (int)lane_id();
+  int lo = 0, n = B;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int i = lane * step;
+    bool below = false;
+    if (i < n) below = clampi(__ldg(seq + lo + i), 0, S) / T + lo + i <= slot;
+    const uint32_t votes = __ballot_sync(0xffffffffu, below);
+    const int at = votes ? 31 - __clz((int)votes) : 0;
+    lo += at * step;
+    n = n - at * step < step ? n - at * step : step;
+  }
+  *tile = slot - (clampi(__ldg(seq + lo), 0, S) / T + lo);
+  return lo;
+}
+
+// Bounded wait on an mbarrier phase: gives up after `limit_ns`, recording `code` in the status
+// word and raising the abort flag, or as soon as another role has raised the flag -- unless
+// `drain`, for copies and MMAs in flight, which always runs to the full limit.
+struct WaitCtx {
+  int* abort_flag;
+  unsigned int* status;
+  unsigned long long limit_ns;
+};
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const WaitCtx& w,
+                                     unsigned code, bool drain = false) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t limit = drain ? kWaitLimitNs : w.limit_ns;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (!drain && *reinterpret_cast<volatile int*>(w.abort_flag)) return false;
+    if (global_timer_ns() - t0 > limit) {
+      *reinterpret_cast<volatile int*>(w.abort_flag) = 1;
+      atomicCAS(w.status, 0u, kErrTimeout | code);
+      return false;
+    }
+  }
+}
+// The same by every lane of a warp that goes on to warp-collective instructions: it goes on
+// only if every lane saw the phase complete, so an abort cannot split it.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const WaitCtx& w,
+                                          unsigned code) {
+  const bool ok = wait(bar, parity, w, code);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// Box of a 4-D view (d, token, head, batch) -> shared; what lies outside the tensor reads 0.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+// A 128-row tile as two halves of 64 columns (128-byte rows, 128-byte swizzle).
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar,
+                                          int token, int head, int z) {
+  tma_load_4d(dst, map, bar, 0, token, head, z);
+  tma_load_4d(dst + kTile / 2, map, bar, 64, token, head, z);
+}
+
+// Rows [n, 128) of a tile to zero, by one warp (the rows' bytes are the same under the
+// swizzle, which moves 16-byte pieces inside a row only), ordered before later MMAs.
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int n) {
+  const int lane = (int)lane_id();
+  for (int i = n * 8 + lane; i < 128 * 8; i += 32) {
+    reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
+    reinterpret_cast<uint4*>(tile + kTile / 2)[i] = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+}  // namespace prompt
+}  // namespace vsa

@@ -1,0 +1,541 @@
+// vsa_prompt_fwd_kernel.cuh -- attention over whole prompts: every query of a sequence against
+// the sequence's keys, causal or not, grouped heads, ragged lengths.
+//
+//   out_i = sum_j p_ij v_j,  p_ij = 2^(c q_i.k_j - lse_i),  c = scale log2 e,
+//   lse_i = log2 sum_j 2^(c q_i.k_j)  over j < nk, with causal j <= i + nk - nq
+//
+// computed in one pass over the keys: with a reference m that follows the running maximum (it
+// may lag by up to 2^32, in log2 units 32, so that the accumulator is rarely rescaled),
+// P = 2^(S - m) is rounded to bf16 for the product with V, and out = O / l with l the sum of
+// the rounded weights (so that the weights applied add up to one), lse = m + log2 of the sum
+// of the fp32 weights.  S, O, m and the sums are fp32.
+//
+// An item is two query tiles of 128 rows (neighbours in the sequence) that share every K and V
+// tile: an SS product of 128 x 128 x 128 takes the tensor core 512 cycles and reads 64 KB of
+// shared memory, as much as that gives in 512 cycles, so what the two tiles share is what
+// keeps the copies' writes affordable.  A warpgroup per query tile works on its scores while
+// the tensor core works for the other one.
+//
+// One persistent CTA per SM, 12 warps:
+//   warps 0-3, 4-7  softmax warpgroups of query tile 0 and 1 (thread = query row)
+//   warp 8          TMA: Q tiles, and K, V alternating through a ring of 5 stages
+//   warp 9          MMA issuer (one lane): QK_0(0), QK_1(0), then per key tile j and query
+//                   tile t: PV_t(j), QK_t(j + 1).  MMAs of one thread run in order, so
+//                   QK_t(j + 1) may overwrite P_t(j), and S_t(j + 1) complete says that
+//                   O_t holds tile j.
+//   warp 10         decodes items, one ahead
+//   warp 11         zeroes the rows of a V tile behind the sequence's last key: their weight
+//                   is 0, but 0 times what lies there (another sequence, padding) may be NaN
+// TMEM (512 columns): S_0, S_1 (P over the first 64 columns of S), O_0, O_1.
+#pragma once
+
+#include "vsa_prompt_common.cuh"
+
+namespace vsa {
+namespace prompt {
+
+struct FwdArgs {
+  SeqArgs seq;
+  uint16_t* out;
+  float* lse;  // [Hq, Sq] or [B, Hq, Sq], or null
+  long long out_b, out_h, out_t;  // strides in elements
+  unsigned int* status;
+  int Hq, group, pack;  // query heads a key/value head; log2 of the heads in a tile
+  int n_packs, n_slots;  // head packs, item slots
+  int n_items;
+  float scale_log2;
+  unsigned long long wait_ns;
+  int stall;
+};
+
+namespace fwd {
+
+constexpr int kThreads = 384;
+constexpr int kStages = 5;
+constexpr uint32_t kOffQ = 0;  // [2]
+constexpr uint32_t kOffKV = 2 * kTile;
+constexpr uint32_t kOffCtl = kOffKV + kStages * kTile;
+constexpr uint32_t kSmemBytes = kOffCtl + 1024 + 1024;  // + alignment slack
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+constexpr uint32_t kSoftmaxRegs = 216, kOtherRegs = 56;
+constexpr uint32_t kRegPoolNeeded = 256 * kSoftmaxRegs + 128 * kOtherRegs;
+constexpr float kRescale = 32.0f;
+constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
+
+struct Item {
+  int head0, kv_head, z;  // first query head of the pack, key/value head, batch coordinate
+  int tok, q0, nq;        // first token, first row and number of queries of the sequence
+  int k0, nk;
+  int n[2];               // key tiles of the two query tiles
+  int go;
+};
+
+struct Ctl {
+  uint64_t item_full[2], item_empty[2];
+  uint64_t q_full[2], q_empty[2];  // per query tile
+  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t s_full[2];      // S_t is in TMEM (and O_t holds the tile before)
+  uint64_t p_full[4];      // [2 t + h]: half h of P_t is in TMEM
+  uint64_t o_full[2], o_empty[2];
+  uint64_t v_dirty, v_clean;  // the mailbox of warp 11
+  uint64_t drain, never;
+  Item item[2];
+  int dirty_stage;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(Ctl) <= 1024, "control block");
+
+// Items in the order of their size for one sequence: the last tokens first, heads inside.
+__device__ __forceinline__ bool decode(const FwdArgs& a, int id, Item& it) {
+  const int T = 256 >> a.pack, half = 128 >> a.pack;
+  const int slot = id / a.n_packs;
+  const int hp = id - slot * a.n_packs;
+  int b, tile;
+  if (a.seq.packed) {
+    b = find_slot(a.seq.q_seq, a.seq.B, a.seq.Sq, T, a.n_slots - 1 - slot, &tile);
+  } else {
+    const int per = (a.seq.Sq + T - 1) / T;
+    tile = slot / a.seq.B;
+    b = slot - tile * a.seq.B;
+    tile = per - 1 - tile;
+  }
+  const Seq s = load_seq(a.seq, b);
+  it.z = s.z;
+  it.q0 = s.q0;
+  it.nq = s.nq;
+  it.k0 = s.k0;
+  it.nk = s.nk;
+  it.tok = tile * T;
+  it.head0 = hp << a.pack;
+  it.kv_head = it.head0 / a.group;
+  it.go = 1;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int t0 = it.tok + t * half;
+    const int last = (t0 + half < s.nq ? t0 + half : s.nq) - 1;  // its last query
+    int keys = s.nk;
+    if (a.seq.causal) keys = clampi(last + 1 + s.nk - s.nq, 0, s.nk);
+    it.n[t] = t0 < s.nq ? (keys + 127) / 128 : 0;
+  }
+  return a.seq.packed ? tile >= 0 && it.tok < s.nq : true;
+}
+
+__device__ __forceinline__ void sched_role(const FwdArgs& a, Ctl* ctl, const WaitCtx& w) {
+  uint32_t n = 0;
+  for (int id = (int)blockIdx.x;; id += (int)gridDim.x) {
+    Item it;
+    it.go = 0;
+    if (id < a.n_items && !decode(a, id, it)) continue;
+    const uint32_t buf = n & 1;
+    if (n >= 2 && !wait_warp(&ctl->item_empty[buf], ((n >> 1) + 1) & 1, w, 0x01)) return;
+    if (lane_id() == 0) {
+      ctl->item[buf] = it;
+      mbar_arrive(&ctl->item_full[buf]);
+    }
+    __syncwarp();
+    ++n;
+    if (!it.go) return;
+  }
+}
+
+__device__ __forceinline__ void tma_role(const FwdArgs& a, uint8_t* smem, Ctl* ctl,
+                                         const WaitCtx& w, const CUtensorMap* tq,
+                                         const CUtensorMap* tk, const CUtensorMap* tv) {
+  uint32_t L = 0, nq[2] = {0, 0};
+  bool ok = true;
+  for (uint32_t i = 0; ok; ++i) {
+    const uint32_t buf = i & 1;
+    if (!wait(&ctl->item_full[buf], (i >> 1) & 1, w, 0x02)) break;
+    const Item it = ctl->item[buf];
+    mbar_arrive(&ctl->item_empty[buf]);
+    if (!it.go) break;
+    const int n = it.n[0] > it.n[1] ? it.n[0] : it.n[1];
+    const int half = 128 >> a.pack;
+    auto put = [&](const CUtensorMap* map, int j) {
+      const uint32_t st = L % kStages;
+      if (L >= (uint32_t)kStages && !wait(&ctl->kv_empty[st], ((L / kStages) + 1) & 1, w, 0x03))
+        return false;
+      mbar_arrive_expect_tx(&ctl->kv_full[st], kTile);
+      load_tile(smem + kOffKV + st * kTile, map, &ctl->kv_full[st], it.k0 + 128 * j, it.kv_head,
+                it.z);
+      ++L;
+      return true;
+    };
+    auto put_q = [&](int t) {
+      if (it.n[t] == 0) return true;
+      uint32_t& c = t ? nq[1] : nq[0];
+      if (c > 0 && !wait(&ctl->q_empty[t], (c - 1) & 1, w, 0x04)) return false;
+      mbar_arrive_expect_tx(&ctl->q_full[t], kTile);
+      load_tile(smem + kOffQ + t * kTile, tq, &ctl->q_full[t], it.q0 + it.tok + t * half,
+                it.head0, it.z);
+      ++c;
+      return true;
+    };
+    // K of the first tile ahead of Q: its stage is free long before the Q buffers are
+    for (int j = 0; j < n && ok; ++j) {
+      ok = put(tk, j);
+      if (ok && j == 0) ok = put_q(0) && put_q(1);
+      if (ok) ok = put(tv, j);
+    }
+  }
+  // every copy issued has landed before the CTA exits
+  for (uint32_t s = 0; s < (uint32_t)kStages; ++s) {
+    const uint32_t fills = L > s ? (L - s + kStages - 1) / kStages : 0;
+    if (fills) wait(&ctl->kv_full[s], (fills - 1) & 1, w, 0x05, true);
+  }
+  if (nq[0]) wait(&ctl->q_full[0], (nq[0] - 1) & 1, w, 0x06, true);
+  if (nq[1]) wait(&ctl->q_full[1], (nq[1] - 1) & 1, w, 0x06, true);
+}
+
+__device__ __forceinline__ void mma_role(const FwdArgs& a, uint8_t* smem, Ctl* ctl,
+                                         const WaitCtx& w, uint32_t tmem) {
+  constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
+  constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, false, true);
+  uint32_t L = 0;          // ring position of the item's K tile 0
+  uint32_t items0 = 0, items1 = 0, p0 = 0, p1 = 0;  // per query tile: items, key tiles so far
+  uint32_t cleaned = 0;
+  if (a.stall) {  // test hook: a barrier that nothing completes
+    wait(&ctl->never, 0, w, 0x1f);
+  } else {
+    for (uint32_t i = 0;; ++i) {
+      const uint32_t buf = i & 1;
+      if (!wait(&ctl->item_full[buf], (i >> 1) & 1, w, 0x07)) break;
+      const int n0 = ctl->item[buf].n[0], n1 = ctl->item[buf].n[1];
+      const int nk = ctl->item[buf].nk;
+      const int go = ctl->item[buf].go;
+      mbar_arrive(&ctl->item_empty[buf]);
+      if (!go) break;
+      const int n = n0 > n1 ? n0 : n1;
+      if (n == 0) continue;
+      bool ok = true;
+      auto landed = [&](uint32_t pos) {
+        return wait(&ctl->kv_full[pos % kStages], (pos / kStages) & 1, w, 0x08);
+      };
+      // S_t = Q_t K_j^T
+      auto qk = [&](int t, int j) {
+        const uint32_t st = (L + 2 * j) % kStages;
+        const uint64_t qd = smem_desc_sw128(smem_addr(smem + kOffQ + t * kTile), 16, 1024);
+        const uint64_t kd = smem_desc_sw128(smem_addr(smem + kOffKV + st * kTile), 16, 1024);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint64_t off = ((k >> 2) * (kTile / 2) + (k & 3) * 32) >> 4;
+          mma_ss(tmem + kColS + 128 * t, qd + off, kd + off, kIdescS, k > 0);
+        }
+        mma_commit(&ctl->s_full[t]);
+      };
+      for (int t = 0; t < 2 && ok; ++t) {
+        if ((t ? n1 : n0) == 0) continue;
+        ok = wait(&ctl->q_full[t], (t ? items1 : items0) & 1, w, 0x09) && landed(L);
+        if (!ok) break;
+        tc_fence_after();
+        qk(t, 0);
+        if ((t ? n1 : n0) == 1) mma_commit(&ctl->q_empty[t]);
+      }
+      if (ok) mma_commit(&ctl->kv_empty[L % kStages]);
+      for (int j = 0; j < n && ok; ++j) {
+        const uint32_t vpos = L + 2 * j + 1, vst = vpos % kStages;
+        if (!landed(vpos)) {
+          ok = false;
+          break;
+        }
+        const bool part = nk - 128 * j < 128;  // keys behind the last: their V rows to zero
+        if (part) {
+          ctl->dirty_stage = (int)vst;
+          mbar_arrive(&ctl->v_dirty);
+        }
+        const bool more_k = j + 1 < n;
+#pragma unroll 1
+        for (int t = 0; t < 2 && ok; ++t) {
+          const int nt = t ? n1 : n0;
+          if (j < nt) {
+            const uint32_t pc = t ? p1 : p0;
+            if (j == 0 && (t ? items1 : items0) > 0 &&
+                !wait(&ctl->o_empty[t], ((t ? items1 : items0) - 1) & 1, w, 0x0a)) {
+              ok = false;
+              break;
+            }
+            const uint64_t vd =
+                smem_desc_sw128(smem_addr(smem + kOffKV + vst * kTile), kTile / 2, 1024);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (!wait(&ctl->p_full[2 * t + h], pc & 1, w, 0x0b)) {
+                ok = false;
+                break;
+              }
+              if (h == 0 && part && t == (n0 > j ? 0 : 1)) {
+                if (!wait(&ctl->v_clean, cleaned & 1, w, 0x0c)) {
+                  ok = false;
+                  break;
+                }
+                ++cleaned;
+              }
+              tc_fence_after();
+#pragma unroll
+              for (int k = 4 * h; k < 4 * h + 4; ++k)
+                mma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * k,
+                       vd + ((k * 2048) >> 4), kIdescPV, (j > 0 || k > 0) ? 1u : 0u);
+            }
+            if (!ok) break;
+            if (t) ++p1; else ++p0;
+            if (j + 1 == nt) mma_commit(&ctl->o_full[t]);
+          }
+          // V_j is free behind the last tile's product
+          if (t == (n1 > j ? 1 : 0)) mma_commit(&ctl->kv_empty[vst]);
+          if (j + 1 < nt) {
+            if (!landed(L + 2 * j + 2)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            qk(t, j + 1);
+            if (j + 2 == nt) mma_commit(&ctl->q_empty[t]);
+          }
+          if (more_k && t == (n1 > j + 1 ? 1 : 0)) mma_commit(&ctl->kv_empty[(L + 2 * j + 2) % kStages]);
+        }
+      }
+      if (!ok) break;
+      if (n0 > 0) ++items0;
+      if (n1 > 0) ++items1;
+      L += 2 * n;
+    }
+  }
+  // every MMA issued has completed before TMEM can be released
+  mma_commit(&ctl->drain);
+  wait(&ctl->drain, 0, w, 0x0d, true);
+}
+
+__device__ __forceinline__ void clean_role(uint8_t* smem, Ctl* ctl, const WaitCtx& w) {
+  uint32_t n_dirty = 0;
+  for (uint32_t i = 0;; ++i) {
+    const uint32_t buf = i & 1;
+    if (!wait_warp(&ctl->item_full[buf], (i >> 1) & 1, w, 0x13)) return;
+    const int n0 = ctl->item[buf].n[0], n1 = ctl->item[buf].n[1];
+    const int nk = ctl->item[buf].nk, go = ctl->item[buf].go;
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(&ctl->item_empty[buf]);
+    if (!go) return;
+    if (128 * (n0 > n1 ? n0 : n1) <= nk) continue;  // every tile of the item is full
+    if (!wait_warp(&ctl->v_dirty, n_dirty & 1, w, 0x14)) return;
+    ++n_dirty;
+    zero_rows(smem + kOffKV + ctl->dirty_stage * kTile, nk & 127);
+    if (lane_id() == 0) mbar_arrive(&ctl->v_clean);
+    __syncwarp();
+  }
+}
+
+__device__ __forceinline__ void softmax_role(const FwdArgs& a, Ctl* ctl, const WaitCtx& w,
+                                             uint32_t tmem, int t) {
+  const int row = (int)(threadIdx.x & 127);
+  const uint32_t lanes = (uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16;
+  const uint32_t tS = tmem + lanes + kColS + 128 * t, tO = tmem + lanes + kColO + 128 * t;
+  const float sl2 = a.scale_log2;
+  uint32_t done = 0, tiles = 0;  // items with keys, key tiles so far
+  const int half = 128 >> a.pack;
+  for (uint32_t i = 0;; ++i) {
+    const uint32_t buf = i & 1;
+    if (!wait_warp(&ctl->item_full[buf], (i >> 1) & 1, w, 0x10)) break;
+    const Item it = ctl->item[buf];
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(&ctl->item_empty[buf]);
+    if (!it.go) break;
+    const int n = it.n[t];
+    const int tok = it.tok + t * half + (row & (half - 1));
+    const int head = it.head0 + (row >> (7 - a.pack));
+    // keys this row attends
+    int lim = it.nk;
+    if (a.seq.causal) lim = clampi(tok + 1 + it.nk - it.nq, 0, it.nk);
+    if (tok >= it.nq) lim = 0;
+    float m = -INFINITY, l_exact = 0.0f, l_round = 0.0f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j, ++tiles) {
+      if (!wait_warp(&ctl->s_full[t], tiles & 1, w, 0x11)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t r[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        tmem_ld_32x32b_x32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&r[32 * c]));
+      tmem_wait_ld();
+      float s[128];
+#pragma unroll
+      for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(r[c]);
+      const int left = lim - 128 * j;
+      if (__any_sync(0xffffffffu, left < 128)) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c >= left) s[c] = -INFINITY;
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int c = 4; c + 1 < 128; c += 8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + 2 * e + 1 < 128) mx[e] = fmax3(mx[e], s[c + 2 * e], s[c + 2 * e + 1]);
+      }
+      const float top = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sl2;
+      float alpha = 1.0f;
+      if (top > m + kRescale) {
+        if (m != -INFINITY) alpha = fast_exp2(m - top);
+        m = top;
+      }
+      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+        // S_t(j) complete: so is the product that O_t held last
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(tO + 32 * c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          tmem_st_32x32b_x32(tO + 32 * c, o);
+        }
+      }
+      const float neg = m == -INFINITY ? 0.0f : -m;
+      const uint64_t c2 = f32x2(sl2, sl2), neg2 = f32x2(neg, neg);
+      uint64_t acc_e[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+      float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int c = 64 * h + 2 * e;
+          float y0, y1;
+          split_f32x2(fma_f32x2(f32x2(s[c], s[c + 1]), c2, neg2), y0, y1);
+          const float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
+          acc_e[e & 1] = add_f32x2(acc_e[e & 1], f32x2(e0, e1));
+          pk[e] = pack_bf16x2(e0, e1);
+          if (e & 1)
+            add_bf16x2_to_f32(pk[e], r2, r3);
+          else
+            add_bf16x2_to_f32(pk[e], r0, r1);
+        }
+        tmem_st_32x32b_x32(tS + 32 * h, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane_id() == 0) mbar_arrive(&ctl->p_full[2 * t + h]);
+      }
+      float e0, e1, e2, e3;
+      split_f32x2(acc_e[0], e0, e1);
+      split_f32x2(acc_e[1], e2, e3);
+      l_exact = l_exact * alpha + ((e0 + e1) + (e2 + e3));
+      l_round = l_round * alpha + ((r0 + r1) + (r2 + r3));
+    }
+    if (!ok) break;
+    // a row that attends nothing gets +0 and the sentinel; scores that are no numbers, or all
+    // -infinity, give NaN
+    const bool some = lim > 0;
+    const float inv = some ? 1.0f / l_round : 0.0f;
+    const bool write = tok < (a.seq.packed ? it.nq : a.seq.Sq);
+    uint16_t* dst = a.out + it.z * a.out_b + head * a.out_h + (long long)(it.q0 + tok) * a.out_t;
+    if (n > 0) {
+      if (!wait_warp(&ctl->o_full[t], done & 1, w, 0x12)) break;
+      ++done;
+      tc_fence_after();
+    }
+    if (write && a.lse != nullptr)
+      a.lse[((long long)it.z * a.Hq + head) * a.seq.Sq + it.q0 + tok] =
+          some ? (l_exact > 0.0f ? m + log2f(l_exact) : __int_as_float(0x7fffffff)) : kLseEmpty;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[32];
+      if (n > 0) {
+        tmem_ld_32x32b_x32(tO + 32 * c, o);
+        tmem_wait_ld();
+      }
+      if (c == 3 && n > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane_id() == 0) mbar_arrive(&ctl->o_empty[t]);
+      }
+      if (!write) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t x[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          x[y] = some && n > 0 ? pack_bf16x2(__uint_as_float(o[8 * e + 2 * y]) * inv,
+                                             __uint_as_float(o[8 * e + 2 * y + 1]) * inv)
+                               : 0u;
+        reinterpret_cast<uint4*>(dst + 32 * c)[e] = make_uint4(x[0], x[1], x[2], x[3]);
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                      const __grid_constant__ CUtensorMap tv, const FwdArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + kOffCtl);
+  const uint32_t warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->item_full[i], 1);
+      mbar_init(&ctl->item_empty[i], 11);  // TMA, MMA, 8 softmax warps, warp 11
+      mbar_init(&ctl->q_full[i], 1);
+      mbar_init(&ctl->q_empty[i], 1);
+      mbar_init(&ctl->s_full[i], 1);
+      mbar_init(&ctl->p_full[2 * i], 4);
+      mbar_init(&ctl->p_full[2 * i + 1], 4);
+      mbar_init(&ctl->o_full[i], 1);
+      mbar_init(&ctl->o_empty[i], 4);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&ctl->kv_full[i], 1);
+      mbar_init(&ctl->kv_empty[i], 1);
+    }
+    mbar_init(&ctl->v_dirty, 1);
+    mbar_init(&ctl->v_clean, 1);
+    mbar_init(&ctl->drain, 1);
+    mbar_init(&ctl->never, 1);
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8 && lane_id() == 0) {
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+  }
+  if (warp == 9) {
+    tmem_alloc(&ctl->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  const WaitCtx w{&ctl->abort_flag, a.status, a.wait_ns};
+
+  if (warp < 8) {
+    regs_increase<kSoftmaxRegs>();
+    softmax_role(a, ctl, w, tmem, (int)(warp >> 2));
+  } else {
+    regs_decrease<kOtherRegs>();
+    if (warp == 8) {
+      if (lane_id() == 0) tma_role(a, smem, ctl, w, &tq, &tk, &tv);
+      __syncwarp();
+    } else if (warp == 9) {
+      if (lane_id() == 0) mma_role(a, smem, ctl, w, tmem);
+      __syncwarp();
+    } else if (warp == 10) {
+      sched_role(a, ctl, w);
+    } else {
+      clean_role(smem, ctl, w);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, kTmemCols);
+}
+
+}  // namespace fwd
+}  // namespace prompt
+}  // namespace vsa

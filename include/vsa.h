@@ -449,6 +449,46 @@ VSA_API vsa_status vsa_cache_evict(const float *weight, const int32_t *table,
                                    float *weight_out, int32_t *lens_out, int32_t *freed,
                                    int32_t *n_freed, vsa_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Attention over whole prompts: every query of a sequence against that sequence's keys, for
+ * the prompt that fills a cache and for layers without a choice of blocks.
+ *
+ * Sequences.  The host does not know their lengths; int32 device arrays do.
+ *   packed != 0  the sequences lie one behind the other along the token axis (the tensors have
+ *                no batch axis): q_seq [B + 1] holds the first row of each and, last, the end;
+ *                k_seq the same for keys and values.  Starts ascend from 0 or more; rows of no
+ *                sequence are neither read into a result nor written.
+ *   packed == 0  a padded batch: sequence b is rows 0 .. q_seq[b] - 1 of batch b (k_seq for
+ *                keys); q_seq [B], k_seq [B], or NULL = all Sq (Sk) rows.  Rows behind a length
+ *                are written: 0, and VSA_LSE_EMPTY in lse.
+ *   Starts and lengths outside the tensor are clamped to it.
+ * Masks.  Sequence b has nq queries and nk keys.  Query i attends the keys j < nk, and with
+ * causal != 0 those with j <= i + nk - nq: the last query stands at the last key, keys in
+ * front of the queries are a past that is held already, and with nk < nq the first queries
+ * attend nothing.  What a tensor holds in rows of no sequence reaches no result; inside a
+ * sequence, keys are expected to be finite: a NaN or infinity in v reaches all rows of the
+ * query tiles that walk over it, masked or not.
+ * Tensors.  bf16 [batch, heads, tokens, 128] with strides in elements, `strides` a host array
+ * of (batch, head, token) for each tensor in the order of the arguments: 128 or more,
+ * multiples of 8, addresses 16-byte aligned; the stride of an axis of length 1 is free.  So
+ * slices of a fused projection's output go in as they are, and outputs may be slices of one
+ * buffer.  Outputs must not share elements with inputs or with one another.
+ * ------------------------------------------------------------------------------------- */
+
+/* Forward.
+ *   q, out  [B or 1, Hq, Sq, D];  k, v  [B or 1, Hkv, Sk, D];  Hq a multiple of Hkv, query head
+ *           hq reads key/value head hq / (Hq / Hkv).
+ *   strides int64 [12]: (batch, head, token) of q, k, v, out.
+ *   scale   natural-exp softmax scale (finite, > 0).
+ *   lse     [Hq, Sq] (packed) or [B, Hq, Sq] fp32, base 2, contiguous, or NULL.
+ * A row that attends nothing gets out = +0 and lse = VSA_LSE_EMPTY; one whose scores are no
+ * numbers, or all -infinity, gets NaN.  Needs no workspace.  One kernel. */
+VSA_API vsa_status vsa_fwd_prompt(const vsa_bf16 *q, const vsa_bf16 *k, const vsa_bf16 *v,
+                                  const int64_t *strides, const int32_t *q_seq,
+                                  const int32_t *k_seq, int packed, int B, int Hq, int Hkv, int Sq,
+                                  int Sk, int D, int causal, float scale, vsa_bf16 *out,
+                                  float *lse, vsa_stream_t stream);
+
 /* Synchronises `stream`, then reads and clears the device status word of the current
  * device: VSA_OK, or VSA_ERR_DEVICE_TIMEOUT if a kernel gave up on a wait since the
  * last call (`detail`, if not NULL, receives the recorded code). */
