@@ -37,7 +37,8 @@ EXPORTS = ("vsa_fwd", "jenga_fwd", "vsa_workspace_bytes", "vsa_lut_to_bitmap",
            "vsa_fwd_from_mask", "vsa_fwd_split", "vsa_split_workspace_bytes", "vsa_bwd",
            "vsa_bwd_workspace_bytes", "vsa_set_wait_limit_ns", "vsa_set_stall_test",
            "vsa_block_mean", "vsa_select_blocks", "vsa_cache_select", "vsa_cache_write",
-           "vsa_fwd_cache", "vsa_cache_workspace_bytes", "vsa_cache_evict", "vsa_fwd_prompt")
+           "vsa_fwd_cache", "vsa_cache_workspace_bytes", "vsa_cache_evict", "vsa_fwd_prompt",
+           "vsa_bwd_prompt", "vsa_bwd_prompt_workspace_bytes")
 MAX_SPLITS = 64
 
 
@@ -122,6 +123,10 @@ def load(path: str = LIB_PATH):
     h.vsa_cache_evict.argtypes = [P, P, P] + [i32] * 6 + [P] * 6
     h.vsa_fwd_prompt.restype = i32
     h.vsa_fwd_prompt.argtypes = [P] * 6 + [i32] * 8 + [f32, P, P, P]
+    h.vsa_bwd_prompt_workspace_bytes.restype = sz
+    h.vsa_bwd_prompt_workspace_bytes.argtypes = [i32] * 5
+    h.vsa_bwd_prompt.restype = i32
+    h.vsa_bwd_prompt.argtypes = [P] * 9 + [i32] * 8 + [f32, P, P, P, P, sz, P]
     _fast = _load_fast(h)
     _lib = h
     return h
@@ -892,3 +897,38 @@ def vsa_fwd_prompt(q, k, v, q_seq=None, k_seq=None, causal=True, scale=None, out
           p.strides(q, k, v, out), *p.sizes(), 1 if causal else 0,
           1.0 / math.sqrt(p.D) if scale is None else float(scale), out.data_ptr(), lse_p)
     return out, None if lse is False else lse
+
+
+def vsa_bwd_prompt(q, k, v, out, dout, lse, q_seq=None, k_seq=None, causal=True, scale=None,
+                   dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Gradient of vsa_fwd_prompt: dq, dk, dv for an upstream gradient dout, given the forward's
+    out and lse; the rest as given to the forward.  dq, dk, dv may be given, as slices of one
+    buffer for instance.  The workspace (uint8, bwd_prompt_workspace_bytes) is allocated if
+    not given."""
+    p = _Prompt(q, k, v, q_seq, k_seq)
+    ndim = q.dim()
+    _rows("out", out, torch.bfloat16, ndim, p.dev, q.shape)
+    _rows("dout", dout, torch.bfloat16, ndim, p.dev, q.shape)
+    lse_p = _need("lse", lse, torch.float32, p.lse, p.dev)
+    with torch.cuda.stream(stream):
+        dq, dk, dv = (torch.empty(x.shape, dtype=x.dtype, device=x.device) if d is None else d
+                      for x, d in ((q, dq), (k, dk), (v, dv)))
+        if workspace is None:
+            n = bwd_prompt_workspace_bytes(p.packed, p.B, p.Hq, p.Hkv, p.Sq)
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    for name, d, x in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        _rows(name, d, torch.bfloat16, ndim, p.dev, x.shape)
+    if not workspace.is_contiguous() or workspace.get_device() != p.dev:
+        raise ValueError(f"workspace must be contiguous and on cuda:{p.dev}")
+    _call("vsa_bwd_prompt", p.dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          out.data_ptr(), dout.data_ptr(), lse_p, p.strides(q, k, v, out, dout, dq, dk, dv),
+          *p.sizes(), 1 if causal else 0, 1.0 / math.sqrt(p.D) if scale is None else float(scale),
+          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    return dq, dk, dv
+
+
+def bwd_prompt_workspace_bytes(packed, B, Hq, Hkv, Sq) -> int:
+    for name, n in (("B", B), ("Hq", Hq), ("Hkv", Hkv), ("Sq", Sq)):
+        _whole(name, n)
+    return int(load().vsa_bwd_prompt_workspace_bytes(1 if packed else 0, B, Hq, Hkv, Sq))

@@ -24,7 +24,7 @@ LIB = os.path.join(PKG, "libvsa_gb300.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("vsa_api.cu", "vsa_serve_api.cu", "vsa_prompt_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in (
     "vsa_fwd_kernel.cuh", "vsa_bwd_kernel.cuh", "vsa_select_kernel.cuh", "vsa_cache_kernel.cuh",
-    "vsa_prompt_common.cuh", "vsa_prompt_fwd_kernel.cuh",
+    "vsa_prompt_common.cuh", "vsa_prompt_fwd_kernel.cuh", "vsa_prompt_bwd_kernel.cuh",
     "sm103_ptx.cuh", "vsa_warp_ptx.cuh", "vsa_host.h")] + [
     os.path.join(ROOT, "include", "vsa.h")]
 TORCH_SOURCE = os.path.join(CSRC, "vsa_torch.cpp")

@@ -12,6 +12,7 @@
 
 #include "../../include/vsa.h"
 #include "vsa_host.h"
+#include "vsa_prompt_bwd_kernel.cuh"
 #include "vsa_prompt_fwd_kernel.cuh"
 
 using namespace vsa;
@@ -101,7 +102,7 @@ bool make_map(CUtensorMap* m, const View& v, int tokens, int heads) {
 }
 
 std::mutex g_attr_mu;
-constexpr int kKernels = 1;
+constexpr int kKernels = 3;
 struct KernelInfo {
   bool ready;
   int regs;
@@ -230,6 +231,127 @@ vsa_status vsa_fwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
                                    reinterpret_cast<cudaStream_t>(stream)>>>(tq, tk, tv, a);
   if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
   host_set_launches(1);
+  return VSA_OK;
+}
+
+size_t vsa_bwd_prompt_workspace_bytes(int packed, int B, int Hq, int Hkv, int Sq) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Sq < 0) return 0;
+  const int pack = pack_log(Hq / Hkv);
+  return (size_t)(prompt::tile_slots(packed, B, Sq, 128 >> pack) * (Hq >> pack)) * 1024;
+}
+
+vsa_status vsa_bwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* v,
+                          const vsa_bf16* out, const vsa_bf16* dout, const float* lse,
+                          const int64_t* strides, const int32_t* q_seq, const int32_t* k_seq,
+                          int packed, int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal,
+                          float scale, vsa_bf16* dq, vsa_bf16* dk, vsa_bf16* dv, void* workspace,
+                          size_t workspace_bytes, vsa_stream_t stream) {
+  host_set_launches(0);
+  const Shape p{q_seq, k_seq, packed, B, Hq, Hkv, Sq, Sk, D, causal, scale};
+  vsa_status st = check_shape(p);
+  if (st != VSA_OK) return st;
+  if (B == 0 || Hq == 0 || (Sq == 0 && Sk == 0)) return VSA_OK;
+  if (!strides) return VSA_ERR_INVALID_ARG;
+  const long long nb = packed ? 1 : B;
+  const View vq = view(q, strides, nb, Hq, Sq), vk = view(k, strides + 3, nb, Hkv, Sk),
+             vv = view(v, strides + 6, nb, Hkv, Sk), vo = view(out, strides + 9, nb, Hq, Sq),
+             vg = view(dout, strides + 12, nb, Hq, Sq), wq = view(dq, strides + 15, nb, Hq, Sq),
+             wk = view(dk, strides + 18, nb, Hkv, Sk), wv = view(dv, strides + 21, nb, Hkv, Sk);
+  const View* in[5] = {&vq, &vk, &vv, &vo, &vg};
+  const View* res[3] = {&wq, &wk, &wv};
+  for (const View* x : in)
+    if (!view_ok(*x)) return VSA_ERR_INVALID_ARG;
+  for (const View* x : res)
+    if (!view_ok(*x)) return VSA_ERR_INVALID_ARG;
+  const size_t need = vsa_bwd_prompt_workspace_bytes(packed, B, Hq, Hkv, Sq);
+  const long long lse_bytes = nb * Hq * Sq * 4;
+  if (Sq > 0 && (!lse || !host_aligned4(lse) || !workspace || workspace_bytes < need ||
+                 !host_aligned16(workspace)))
+    return VSA_ERR_INVALID_ARG;
+  for (const View* y : res) {
+    for (const View* x : in)
+      if (views_meet(*y, *x)) return VSA_ERR_INVALID_ARG;
+    for (const View* x : res)
+      if (x != y && views_meet(*y, *x)) return VSA_ERR_INVALID_ARG;
+    if (meets(*y, lse, lse_bytes) || meets(*y, workspace, (long long)need) ||
+        meets(*y, q_seq, seq_bytes(p, q_seq)) || meets(*y, k_seq, seq_bytes(p, k_seq)))
+      return VSA_ERR_INVALID_ARG;
+  }
+  for (const View* x : in)
+    if (meets(*x, workspace, (long long)need)) return VSA_ERR_INVALID_ARG;
+
+  prompt::bwd::Args a{};
+  a.seq = seq_args(p);
+  a.stats = static_cast<const float*>(workspace);
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.group = Hq / Hkv;
+  a.pack = pack_log(a.group);
+  a.n_packs = Hq >> a.pack;
+  const long long tslots = prompt::tile_slots(packed, B, Sq, 128 >> a.pack),
+                  kslots = prompt::tile_slots(packed, B, Sk, 128);
+  if (tslots * a.n_packs > INT_MAX || kslots * Hkv > INT_MAX) return VSA_ERR_UNSUPPORTED;
+  a.n_tslots = (int)tslots;
+  a.n_kslots = (int)kslots;
+  a.scale = scale;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.wait_ns = host_wait_ns(prompt::kWaitLimitNs);
+  a.stall = host_stall();
+
+  int dev = 0;
+  st = host_device(&dev);
+  if (st != VSA_OK) return st;
+  a.status = host_status_word();
+  if (a.status == nullptr) return VSA_ERR_CUDA;
+  namespace pb = prompt::bwd;
+  st = prepare(pb::dkv::prompt_dkv_kernel, dev, 1, pb::dkv::kSmemBytes, pb::kThreads,
+               pb::kRegPoolNeeded);
+  if (st != VSA_OK) return st;
+  st = prepare(pb::dq::prompt_dq_kernel, dev, 2, pb::dq::kSmemBytes, pb::kThreads,
+               pb::kRegPoolNeeded);
+  if (st != VSA_OK) return st;
+  CUtensorMap tq, tg, tk, tv;
+  // what is empty is not fetched: its map only has to encode
+  const View &mq = vq.empty() ? vk : vq, &mg = vg.empty() ? vk : vg, &mk = vk.empty() ? vq : vk,
+             &mv = vv.empty() ? vq : vv;
+  if (!make_map(&tq, mq, 128 >> a.pack, 1 << a.pack) ||
+      !make_map(&tg, mg, 128 >> a.pack, 1 << a.pack) || !make_map(&tk, mk, 128, 1) ||
+      !make_map(&tv, mv, 128, 1))
+    return VSA_ERR_CUDA;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int launches = 0;
+  if (tslots > 0 && Sq > 0) {
+    const pb::PrepArgs pa{a.seq, out, dout, lse, static_cast<float*>(workspace),
+                          vo.sb, vo.sh, vo.st, vg.sb, vg.sh, vg.st,
+                          Hq, a.pack, a.n_packs, a.n_tslots};
+    pb::prompt_prep_kernel<<<(unsigned)(tslots * a.n_packs), 256, 0, s>>>(pa);
+    ++launches;
+  }
+  if (Sk > 0) {
+    a.d0 = dk;
+    a.d0_b = wk.sb;
+    a.d0_h = wk.sh;
+    a.d0_t = wk.st;
+    a.d1 = dv;
+    a.d1_b = wv.sb;
+    a.d1_h = wv.sh;
+    a.d1_t = wv.st;
+    pb::dkv::prompt_dkv_kernel<<<(unsigned)(kslots * Hkv), pb::kThreads, pb::dkv::kSmemBytes, s>>>(
+        tq, tg, tk, tv, a);
+    ++launches;
+  }
+  if (Sq > 0) {
+    a.d0 = dq;
+    a.d0_b = wq.sb;
+    a.d0_h = wq.sh;
+    a.d0_t = wq.st;
+    a.d1 = nullptr;
+    pb::dq::prompt_dq_kernel<<<(unsigned)(tslots * a.n_packs), pb::kThreads, pb::dq::kSmemBytes,
+                               s>>>(tq, tg, tk, tv, a);
+    ++launches;
+  }
+  if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
+  host_set_launches(launches);
   return VSA_OK;
 }
 

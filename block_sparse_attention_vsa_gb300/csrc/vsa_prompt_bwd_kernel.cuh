@@ -1,0 +1,774 @@
+// vsa_prompt_bwd_kernel.cuh -- gradient of the attention over whole prompts.
+//
+// With p_ij = 2^(c q_i.k_j - lse_i) over the attended pairs (c = scale log2 e), D_i = dout_i .
+// out_i and ds_ij = p_ij (dout_i . v_j - D_i):
+//   dv_j = sum_i p_ij dout_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j,
+// dk and dv summed over the query heads of a key/value head.
+//
+// Three kernels, without atomics, so results do not depend on timing:
+//   prompt_prep_kernel  per query row -lse (-infinity where a row attends nothing, or behind a
+//                       sequence's end, so that every p of the row is 0) and -D, in the order
+//                       of the query tiles.
+//   prompt_dkv_kernel   a CTA per key tile of 128 keys and key/value head: K and V stay in
+//                       shared memory, dK and dV add up in TMEM while it walks the query
+//                       tiles that see the keys.  Per step, transposed (lanes = keys):
+//                         S^T = K Q^T, dP^T = V dO^T           (SS, both K-major)
+//                         P^T = 2^(c S^T - lse), dS^T = P^T (dP^T - D)  -> bf16 over S^T, dP^T
+//                         dV += P^T dO, dK += dS^T Q           (TS, A from TMEM)
+//   prompt_dq_kernel    a CTA per query tile: Q and dO stay, dQ adds up in TMEM while it
+//                       walks the key tiles: S = Q K^T, dP = dO V^T, dS, dQ += dS K.
+// That is seven products where one kernel with atomic sums of dQ takes five, but those sums
+// are 64 KB of L2 reductions a step, and their order would be anyone's.  P and dS are rounded
+// to bf16 for the products, everything else is fp32.
+//
+// A step's products take 512 tensor cycles each (128 x 128 x 128).  Order of issue, one lane:
+//   dkv  dV_g, S_{g+1}, dK_g, dP_{g+1}: P_{g+1} may take as long as dK_g and dP_{g+1}, dS_{g+1}
+//        as long as dV_{g+1} and S_{g+2}.  S_{g+1} overwrites P_g, dP_{g+1} overwrites dS_g.
+//   dq   S_{g+1}, dP_{g+1}, dQ_g, with two buffers of dP / dS.
+//
+// 12 warps: 0-7 gradient warps (thread = lane of the tile, warpgroup w = columns 64 w ..),
+// 8 TMA, 9 MMA issuer (one lane), 11 hands landed tiles on to the MMA warp and zeroes rows
+// that are not the sequence's first: they get weight 0, but 0 times what lies there (another
+// sequence, padding) may be NaN.
+#pragma once
+
+#include "vsa_prompt_common.cuh"
+
+namespace vsa {
+namespace prompt {
+namespace bwd {
+
+constexpr int kThreads = 384;
+constexpr uint32_t kGradRegs = 216, kOtherRegs = 56;
+constexpr uint32_t kRegPoolNeeded = 256 * kGradRegs + 128 * kOtherRegs;
+constexpr uint32_t kTmemCols = 512;
+
+struct Args {
+  SeqArgs seq;
+  const float* stats;  // [n_packs][n_tslots][-lse | -D][128]
+  uint16_t *d0, *d1;   // dkv: dk, dv; dq: dq, null
+  long long d0_b, d0_h, d0_t, d1_b, d1_h, d1_t;  // strides in elements
+  unsigned int* status;
+  int Hq, Hkv, group, pack, n_packs, n_tslots;  // query tiles of 128 >> pack tokens
+  int n_kslots;                                 // key tiles of 128 tokens
+  float scale, scale_log2;
+  unsigned long long wait_ns;
+  int stall;
+};
+
+// the slot of a sequence's query tile (as tile_slots numbers them)
+__device__ __forceinline__ long long query_slot(const Args& a, int b, int q0, int tile) {
+  const int T = 128 >> a.pack;
+  return a.seq.packed ? (long long)(q0 / T) + b + tile
+                      : (long long)b * ((a.seq.Sq + T - 1) / T) + tile;
+}
+
+// -------------------------------------------------------------------------------- prep
+// One CTA per query tile, half a warp a row (8 of the 128 elements a lane).
+struct PrepArgs {
+  SeqArgs seq;
+  const uint16_t *out, *dout;
+  const float* lse;
+  float* stats;
+  long long o_b, o_h, o_t, g_b, g_h, g_t;
+  int Hq, pack, n_packs, n_tslots;
+};
+__global__ void __launch_bounds__(256) prompt_prep_kernel(const PrepArgs a) {
+  const int slot = (int)(blockIdx.x / (unsigned)a.n_packs);
+  const int hp = (int)(blockIdx.x - (unsigned)slot * (unsigned)a.n_packs);
+  const int T = 128 >> a.pack;
+  int b, tile;
+  if (a.seq.packed) {
+    b = find_slot(a.seq.q_seq, a.seq.B, a.seq.Sq, T, slot, &tile);
+  } else {
+    const int per = (a.seq.Sq + T - 1) / T;
+    b = slot / per;
+    tile = slot - b * per;
+  }
+  const Seq s = load_seq(a.seq, b);
+  if (tile < 0 || tile * T >= s.nq) return;  // no step reads this tile
+  const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+  float* stats = a.stats + ((long long)hp * a.n_tslots + slot) * 256;
+  float acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 16 * warp + 2 * i + (lane >> 4);
+    const int tok = tile * T + (r & (T - 1)), head = (hp << a.pack) + (r >> (7 - a.pack));
+    acc[i] = 0.0f;
+    if (tok < s.nq) {
+      const long long row = s.q0 + tok;
+      const uint4 o = __ldg(reinterpret_cast<const uint4*>(a.out + s.z * a.o_b + head * a.o_h +
+                                                           row * a.o_t) + (lane & 15));
+      const uint4 g = __ldg(reinterpret_cast<const uint4*>(a.dout + s.z * a.g_b + head * a.g_h +
+                                                           row * a.g_t) + (lane & 15));
+      const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, gw[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[i] = fmaf(__uint_as_float(ow[e] << 16), __uint_as_float(gw[e] << 16), acc[i]);
+        acc[i] = fmaf(__uint_as_float(ow[e] & 0xFFFF0000u), __uint_as_float(gw[e] & 0xFFFF0000u),
+                      acc[i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int x = 8; x > 0; x >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], x);
+    const int r = 16 * warp + 2 * i + (lane >> 4);
+    const int tok = tile * T + (r & (T - 1)), head = (hp << a.pack) + (r >> (7 - a.pack));
+    if ((lane & 15) == 0) {
+      float l = -INFINITY;
+      if (tok < s.nq) {
+        const float x = __ldg(a.lse + ((long long)s.z * a.Hq + head) * a.seq.Sq + s.q0 + tok);
+        if (!(x <= -3.0e38f)) l = -x;
+      }
+      stats[r] = l;
+      stats[128 + r] = tok < s.nq ? -acc[i] : 0.0f;
+    }
+  }
+}
+
+// --------------------------------------------------------------------------- dK and dV
+namespace dkv {
+
+constexpr int kQStages = 3, kGStages = 2;
+constexpr uint32_t kOffK = 0, kOffV = kTile, kOffQ = 2 * kTile;
+constexpr uint32_t kOffG = kOffQ + kQStages * kTile;
+constexpr uint32_t kOffStats = kOffG + kGStages * kTile;  // [kGStages] -lse[128], -D[128]
+constexpr uint32_t kOffCtl = kOffStats + kGStages * 1024;
+constexpr uint32_t kSmemBytes = kOffCtl + 1024;  // (no room for slack: the base is aligned)
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+constexpr uint32_t kColS = 0, kColDP = 128, kColDV = 256, kColDK = 384;
+
+struct Ctl {
+  uint64_t kv_full;
+  uint64_t q_full[kQStages], q_ready[kQStages], q_empty[kQStages];
+  uint64_t g_full[kGStages], g_ready[kGStages], g_empty[kGStages];
+  uint64_t s_full, dp_full, p_full, ds_full, acc_full, drain, never;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(Ctl) <= 1024, "control block");
+
+// A CTA's work: key tile `tile` of sequence b, and the query tiles that see it.
+struct Work {
+  Seq s;
+  int b, tile, hk;
+  int first, n_tok;   // first query tile and their number, for each head pack
+  int hp0, steps;     // first head pack; all steps
+  int nk;             // keys of the tile
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_dkv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tg,
+                      const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                      const Args a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_addr(smem) & 1023u) {  // the swizzle goes by address bits
+    atomicCAS(a.status, 0u, kErrTimeout | 0xffu);
+    return;
+  }
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + kOffCtl);
+  const int warp = (int)(threadIdx.x >> 5);
+  const uint32_t lane = lane_id();
+  const int T = 128 >> a.pack;
+
+  Work k;
+  {
+    const int slot = (int)(blockIdx.x / (unsigned)a.Hkv);
+    k.hk = (int)(blockIdx.x - (unsigned)slot * (unsigned)a.Hkv);
+    // the first keys are seen by the most queries: they come first
+    if (a.seq.packed) {
+      k.b = find_slot(a.seq.k_seq, a.seq.B, a.seq.Sk, 128, slot, &k.tile);
+    } else {
+      k.tile = slot / a.seq.B;
+      k.b = slot - k.tile * a.seq.B;
+    }
+    k.s = load_seq(a.seq, k.b);
+    const int rows = a.seq.packed ? k.s.nk : a.seq.Sk;  // rows that are written
+    if (k.tile < 0 || 128 * k.tile >= rows) return;
+    k.nk = clampi(k.s.nk - 128 * k.tile, 0, 128);
+    int first = 0;
+    if (a.seq.causal) first = clampi(128 * k.tile - (k.s.nk - k.s.nq), 0, k.s.nq);
+    k.first = first / T;
+    k.n_tok = k.nk > 0 && first < k.s.nq ? (k.s.nq + T - 1) / T - k.first : 0;
+    k.hp0 = (k.hk * a.group) >> a.pack;
+    k.steps = k.n_tok * (a.group >> a.pack);
+  }
+  const int off = k.s.nk - k.s.nq;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&ctl->kv_full, 1);
+    for (int i = 0; i < kQStages; ++i) {
+      mbar_init(&ctl->q_full[i], 1);
+      mbar_init(&ctl->q_ready[i], 1);
+      mbar_init(&ctl->q_empty[i], 1);
+    }
+    for (int i = 0; i < kGStages; ++i) {
+      mbar_init(&ctl->g_full[i], 1);
+      mbar_init(&ctl->g_ready[i], 1);
+      mbar_init(&ctl->g_empty[i], 9);  // dV done; the gradient warps have read -D
+    }
+    mbar_init(&ctl->s_full, 1);
+    mbar_init(&ctl->dp_full, 1);
+    mbar_init(&ctl->p_full, 8);
+    mbar_init(&ctl->ds_full, 8);
+    mbar_init(&ctl->acc_full, 1);
+    mbar_init(&ctl->drain, 1);
+    mbar_init(&ctl->never, 1);
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tg);
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+  }
+  if (warp == 9) {
+    tmem_alloc(&ctl->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  const WaitCtx w{&ctl->abort_flag, a.status, a.wait_ns};
+
+  if (warp < 8) {
+    regs_increase<kGradRegs>();
+    const int wg = warp >> 2;
+    const int r = (warp & 3) * 32 + (int)lane;  // key of the tile
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + kColS + 64 * wg, tDP = tmem + lanes + kColDP + 64 * wg;
+    const uint64_t c2 = f32x2(a.scale_log2, a.scale_log2);
+    bool ok = true;
+    int ti = k.first;
+    for (int g = 0; g < k.steps; ++g) {
+      const int st = g & 1;
+      const float* nlse = reinterpret_cast<const float*>(smem + kOffStats + st * 1024) + 64 * wg;
+      const float* nD = nlse + 128;
+      if (!wait_warp(&ctl->g_full[st], (g >> 1) & 1, w, 0x20) ||
+          !wait_warp(&ctl->s_full, g & 1, w, 0x21)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t x[64];
+      tmem_ld_32x32b_x32(tS, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+      tmem_ld_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+      tmem_wait_ld();
+      float p[64];
+#pragma unroll
+      for (int c = 0; c < 64; c += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(nlse + c);
+        float y0, y1, y2, y3;
+        split_f32x2(fma_f32x2(f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), c2,
+                              f32x2(l.x, l.y)), y0, y1);
+        split_f32x2(fma_f32x2(f32x2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), c2,
+                              f32x2(l.z, l.w)), y2, y3);
+        p[c] = fast_exp2(y0);
+        p[c + 1] = fast_exp2(y1);
+        p[c + 2] = fast_exp2(y2);
+        p[c + 3] = fast_exp2(y3);
+      }
+      // causal: query token t sees this key from t = 128 tile + r - off on
+      if (a.seq.causal && 128 * k.tile + 127 > ti * T + off) {
+        const int from = 128 * k.tile + r - off - ti * T;
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (((64 * wg + c) & (T - 1)) < from) p[c] = 0.0f;
+      }
+      uint32_t pk[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
+      tmem_st_32x32b_x32(tS, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->p_full);
+      if (!wait_warp(&ctl->dp_full, g & 1, w, 0x22)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      tmem_ld_32x32b_x32(tDP, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+      tmem_ld_32x32b_x32(tDP + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 64; c += 4) {
+        const float4 d = *reinterpret_cast<const float4*>(nD + c);
+        float y0, y1, y2, y3;
+        split_f32x2(mul_f32x2(f32x2(p[c], p[c + 1]),
+                              add_f32x2(f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
+                                        f32x2(d.x, d.y))), y0, y1);
+        split_f32x2(mul_f32x2(f32x2(p[c + 2], p[c + 3]),
+                              add_f32x2(f32x2(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])),
+                                        f32x2(d.z, d.w))), y2, y3);
+        pk[c / 2] = pack_bf16x2(y0, y1);
+        pk[c / 2 + 1] = pack_bf16x2(y2, y3);
+      }
+      tmem_st_32x32b_x32(tDP, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ctl->ds_full);
+        mbar_arrive(&ctl->g_empty[st]);
+      }
+      if (++ti == k.first + k.n_tok) ti = k.first;
+    }
+    // dV (warpgroup 0) and dK (warpgroup 1)
+    if (k.steps > 0 && ok) ok = wait_warp(&ctl->acc_full, 0, w, 0x23);
+    if (ok) {
+      tc_fence_after();
+      const long long row = k.s.k0 + 128 * k.tile + r;
+      const bool write = a.seq.packed ? r < k.nk : 128 * k.tile + r < a.seq.Sk;
+      uint16_t* dst = wg ? a.d0 + k.s.z * a.d0_b + k.hk * a.d0_h + row * a.d0_t
+                         : a.d1 + k.s.z * a.d1_b + k.hk * a.d1_h + row * a.d1_t;
+      const float f = wg ? a.scale : 1.0f;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32];
+        if (k.steps > 0) {
+          tmem_ld_32x32b_x32(tmem + lanes + (wg ? kColDK : kColDV) + 32 * c, x);
+          tmem_wait_ld();
+        }
+        if (!write) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            y[i] = k.steps > 0 && r < k.nk
+                       ? pack_bf16x2(__uint_as_float(x[8 * e + 2 * i]) * f,
+                                     __uint_as_float(x[8 * e + 2 * i + 1]) * f)
+                       : 0u;
+          reinterpret_cast<uint4*>(dst + 32 * c)[e] = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+      }
+    }
+  } else {
+    regs_decrease<kOtherRegs>();
+    if (warp == 8) {
+      if (lane == 0 && k.steps > 0) {
+        mbar_arrive_expect_tx(&ctl->kv_full, 2 * kTile);
+        load_tile(smem + kOffK, &tk, &ctl->kv_full, k.s.k0 + 128 * k.tile, k.hk, k.s.z);
+        load_tile(smem + kOffV, &tv, &ctl->kv_full, k.s.k0 + 128 * k.tile, k.hk, k.s.z);
+        int ti = k.first, hp = k.hp0, g = 0;
+        const long long slot0 = query_slot(a, k.b, k.s.q0, 0);
+        for (; g < k.steps; ++g) {
+          const int qs = g % kQStages, gs = g % kGStages;
+          if (g >= kQStages && !wait(&ctl->q_empty[qs], (g / kQStages + 1) & 1, w, 0x24)) break;
+          mbar_arrive_expect_tx(&ctl->q_full[qs], kTile);
+          load_tile(smem + kOffQ + qs * kTile, &tq, &ctl->q_full[qs], k.s.q0 + ti * T,
+                    hp << a.pack, k.s.z);
+          if (g >= kGStages && !wait(&ctl->g_empty[gs], (g / kGStages + 1) & 1, w, 0x25)) {
+            wait(&ctl->q_full[qs], (g / kQStages) & 1, w, 0x26, true);  // this one has no pair
+            break;
+          }
+          mbar_arrive_expect_tx(&ctl->g_full[gs], kTile + 1024);
+          load_tile(smem + kOffG + gs * kTile, &tg, &ctl->g_full[gs], k.s.q0 + ti * T,
+                    hp << a.pack, k.s.z);
+          bulk_load(smem + kOffStats + gs * 1024,
+                    a.stats + ((long long)hp * a.n_tslots + slot0 + ti) * 256, 1024,
+                    &ctl->g_full[gs]);
+          if (++ti == k.first + k.n_tok) {
+            ti = k.first;
+            ++hp;
+          }
+        }
+        // every copy issued has landed before the CTA exits
+        wait(&ctl->kv_full, 0, w, 0x27, true);
+        for (int i = 0; i < kQStages; ++i) {
+          const int fills = g > i ? (g - i + kQStages - 1) / kQStages : 0;
+          if (fills) wait(&ctl->q_full[i], (fills - 1) & 1, w, 0x28, true);
+        }
+        for (int i = 0; i < kGStages; ++i) {
+          const int fills = g > i ? (g - i + kGStages - 1) / kGStages : 0;
+          if (fills) wait(&ctl->g_full[i], (fills - 1) & 1, w, 0x29, true);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 9) {
+      if (lane == 0 && k.steps > 0) {
+        constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
+        constexpr uint32_t kIdescG = idesc_bf16_f32(128, 128, false, true);
+        auto operand = [&](uint32_t at, uint32_t lbo) {
+          return smem_desc_sw128(smem_addr(smem + at), lbo, 1024);
+        };
+        const uint64_t kd = operand(kOffK, 16), vd = operand(kOffV, 16);
+        auto ss = [&](uint32_t d, uint64_t ad, uint64_t bd) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint64_t o = ((i >> 2) * (kTile / 2) + (i & 3) * 32) >> 4;
+            mma_ss(tmem + d, ad + o, bd + o, kIdescS, i > 0);
+          }
+        };
+        // += A B with A's columns as the gradient warps leave them
+        auto ts = [&](uint32_t d, uint32_t col, uint64_t bd, bool first) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            mma_ts(tmem + d, tmem + col + 64 * (i >> 2) + 8 * (i & 3), bd + ((i * 2048) >> 4),
+                   kIdescG, (!first || i > 0) ? 1u : 0u);
+        };
+        auto q_at = [&](int g) { return kOffQ + (uint32_t)(g % kQStages) * kTile; };
+        auto g_at = [&](int g) { return kOffG + (uint32_t)(g % kGStages) * kTile; };
+        auto q_in = [&](int g) {
+          return wait(&ctl->q_ready[g % kQStages], (g / kQStages) & 1, w, 0x2a);
+        };
+        auto g_in = [&](int g) {
+          return wait(&ctl->g_ready[g % kGStages], (g / kGStages) & 1, w, 0x2b);
+        };
+        bool ok = a.stall ? wait(&ctl->never, 0, w, 0x3f) : wait(&ctl->kv_full, 0, w, 0x2c);
+        ok = ok && q_in(0);
+        if (ok) {
+          tc_fence_after();
+          ss(kColS, kd, operand(q_at(0), 16));
+          mma_commit(&ctl->s_full);
+          ok = g_in(0);
+        }
+        if (ok) {
+          tc_fence_after();
+          ss(kColDP, vd, operand(g_at(0), 16));
+          mma_commit(&ctl->dp_full);
+        }
+        for (int g = 0; g < k.steps && ok; ++g) {
+          const bool more = g + 1 < k.steps;
+          if (!wait(&ctl->p_full, g & 1, w, 0x2d)) break;
+          tc_fence_after();
+          ts(kColDV, kColS, operand(g_at(g), kTile / 2), g == 0);
+          mma_commit(&ctl->g_empty[g % kGStages]);
+          if (more) {
+            if (!q_in(g + 1)) break;
+            tc_fence_after();
+            ss(kColS, kd, operand(q_at(g + 1), 16));
+            mma_commit(&ctl->s_full);
+          }
+          if (!wait(&ctl->ds_full, g & 1, w, 0x2e)) break;
+          tc_fence_after();
+          ts(kColDK, kColDP, operand(q_at(g), kTile / 2), g == 0);
+          mma_commit(&ctl->q_empty[g % kQStages]);
+          if (more) {
+            if (!g_in(g + 1)) break;
+            tc_fence_after();
+            ss(kColDP, vd, operand(g_at(g + 1), 16));
+            mma_commit(&ctl->dp_full);
+          } else {
+            mma_commit(&ctl->acc_full);
+          }
+        }
+        mma_commit(&ctl->drain);
+        wait(&ctl->drain, 0, w, 0x2f, true);
+      }
+      __syncwarp();
+    } else if (warp == 11) {
+      int ti = k.first;
+      for (int g = 0; g < k.steps; ++g) {
+        const int qs = g % kQStages, gs = g % kGStages;
+        const int valid = k.s.nq - ti * T;  // tokens of the tile
+        if (!wait_warp(&ctl->q_full[qs], (g / kQStages) & 1, w, 0x30)) break;
+        if (valid < T) zero_tokens(smem + kOffQ + qs * kTile, valid, T);
+        if (lane == 0) mbar_arrive(&ctl->q_ready[qs]);
+        if (!wait_warp(&ctl->g_full[gs], (g / kGStages) & 1, w, 0x31)) break;
+        if (valid < T) zero_tokens(smem + kOffG + gs * kTile, valid, T);
+        if (lane == 0) mbar_arrive(&ctl->g_ready[gs]);
+        if (++ti == k.first + k.n_tok) ti = k.first;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, kTmemCols);
+}
+
+}  // namespace dkv
+
+// ---------------------------------------------------------------------------------- dQ
+namespace dq {
+
+constexpr int kKStages = 3, kVStages = 2;
+constexpr uint32_t kOffQ = 0, kOffG = kTile, kOffK = 2 * kTile;
+constexpr uint32_t kOffV = kOffK + kKStages * kTile;
+constexpr uint32_t kOffCtl = kOffV + kVStages * kTile;
+constexpr uint32_t kSmemBytes = kOffCtl + 1024;  // (the base is aligned)
+static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 384;  // dP twice
+
+struct Ctl {
+  uint64_t q_full;
+  uint64_t k_full[kKStages], k_ready[kKStages], k_empty[kKStages];
+  uint64_t v_full[kVStages], v_empty[kVStages];
+  uint64_t s_full, s_empty, dp_full[2], ds_full[2], acc_full, drain, never;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(Ctl) <= 1024, "control block");
+
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tg,
+                     const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                     const Args a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_addr(smem) & 1023u) {  // the swizzle goes by address bits
+    atomicCAS(a.status, 0u, kErrTimeout | 0xffu);
+    return;
+  }
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + kOffCtl);
+  const int warp = (int)(threadIdx.x >> 5);
+  const uint32_t lane = lane_id();
+  const int T = 128 >> a.pack;
+
+  // the last tokens see the most keys: they come first
+  const int rank = (int)(blockIdx.x / (unsigned)a.n_packs);
+  const int hp = (int)(blockIdx.x - (unsigned)rank * (unsigned)a.n_packs);
+  int b, tile;
+  if (a.seq.packed) {
+    b = find_slot(a.seq.q_seq, a.seq.B, a.seq.Sq, T, a.n_tslots - 1 - rank, &tile);
+  } else {
+    tile = (a.seq.Sq + T - 1) / T - 1 - rank / a.seq.B;
+    b = rank % a.seq.B;
+  }
+  const Seq s = load_seq(a.seq, b);
+  if (tile < 0 || tile * T >= (a.seq.packed ? s.nq : a.seq.Sq)) return;
+  const int off = s.nk - s.nq;
+  const int tok0 = tile * T, head0 = hp << a.pack, hk = head0 / a.group;
+  int keys = tok0 < s.nq ? s.nk : 0;
+  if (a.seq.causal) keys = clampi((tok0 + T < s.nq ? tok0 + T : s.nq) + off, 0, keys);
+  const int steps = (keys + 127) / 128;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&ctl->q_full, 1);
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(&ctl->k_full[i], 1);
+      mbar_init(&ctl->k_ready[i], 1);
+      mbar_init(&ctl->k_empty[i], 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(&ctl->v_full[i], 1);
+      mbar_init(&ctl->v_empty[i], 1);
+      mbar_init(&ctl->dp_full[i], 1);
+      mbar_init(&ctl->ds_full[i], 8);
+    }
+    mbar_init(&ctl->s_full, 1);
+    mbar_init(&ctl->s_empty, 8);
+    mbar_init(&ctl->acc_full, 1);
+    mbar_init(&ctl->drain, 1);
+    mbar_init(&ctl->never, 1);
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tg);
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+  }
+  if (warp == 9) {
+    tmem_alloc(&ctl->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  const WaitCtx w{&ctl->abort_flag, a.status, a.wait_ns};
+
+  if (warp < 8) {
+    regs_increase<kGradRegs>();
+    const int wg = warp >> 2;
+    const int r = (warp & 3) * 32 + (int)lane;  // row of the tile
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + kColS + 64 * wg, tDP = tmem + lanes + kColDP + 64 * wg;
+    const int tok = tok0 + (r & (T - 1)), head = head0 + (r >> (7 - a.pack));
+    float nlse = -INFINITY, nD = 0.0f;
+    if (steps > 0) {
+      const float* st =
+          a.stats + ((long long)hp * a.n_tslots + query_slot(a, b, s.q0, tile)) * 256;
+      nlse = __ldg(st + r);
+      nD = __ldg(st + 128 + r);
+    }
+    int lim = s.nk;  // keys this row attends
+    if (a.seq.causal) lim = clampi(tok + 1 + off, 0, s.nk);
+    const uint64_t c2 = f32x2(a.scale_log2, a.scale_log2), l2 = f32x2(nlse, nlse),
+                   d2 = f32x2(nD, nD);
+    bool ok = true;
+    for (int g = 0; g < steps; ++g) {
+      if (!wait_warp(&ctl->s_full, g & 1, w, 0x40)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t x[64];
+      tmem_ld_32x32b_x32(tS, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+      tmem_ld_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->s_empty);
+      float p[64];
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        float y0, y1;
+        split_f32x2(fma_f32x2(f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), c2, l2),
+                    y0, y1);
+        p[c] = fast_exp2(y0);
+        p[c + 1] = fast_exp2(y1);
+      }
+      if (!wait_warp(&ctl->dp_full[g & 1], (g >> 1) & 1, w, 0x41)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t t = tDP + 128 * (g & 1);
+      tmem_ld_32x32b_x32(t, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+      tmem_ld_32x32b_x32(t + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+      tmem_wait_ld();
+      const int left = lim - 128 * g - 64 * wg;
+      const bool part = __any_sync(0xffffffffu, left < 64);
+      uint32_t pk[32];
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        float y0, y1;
+        split_f32x2(mul_f32x2(f32x2(p[c], p[c + 1]),
+                              add_f32x2(f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
+                                        d2)), y0, y1);
+        if (part) {
+          if (c >= left) y0 = 0.0f;
+          if (c + 1 >= left) y1 = 0.0f;
+        }
+        pk[c / 2] = pack_bf16x2(y0, y1);
+      }
+      tmem_st_32x32b_x32(t, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->ds_full[g & 1]);
+    }
+    if (steps > 0 && ok) ok = wait_warp(&ctl->acc_full, 0, w, 0x42);
+    if (ok) {
+      tc_fence_after();
+      const bool write = tok < (a.seq.packed ? s.nq : a.seq.Sq);
+      const bool some = steps > 0 && tok < s.nq;
+      uint16_t* dst =
+          a.d0 + s.z * a.d0_b + head * a.d0_h + (long long)(s.q0 + tok) * a.d0_t + 64 * wg;
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        uint32_t x[32];
+        if (steps > 0) {
+          tmem_ld_32x32b_x32(tmem + lanes + kColDQ + 64 * wg + 32 * c, x);
+          tmem_wait_ld();
+        }
+        if (!write) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            y[i] = some ? pack_bf16x2(__uint_as_float(x[8 * e + 2 * i]) * a.scale,
+                                      __uint_as_float(x[8 * e + 2 * i + 1]) * a.scale)
+                        : 0u;
+          reinterpret_cast<uint4*>(dst + 32 * c)[e] = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+      }
+    }
+  } else {
+    regs_decrease<kOtherRegs>();
+    if (warp == 8) {
+      if (lane == 0 && steps > 0) {
+        mbar_arrive_expect_tx(&ctl->q_full, 2 * kTile);
+        load_tile(smem + kOffQ, &tq, &ctl->q_full, s.q0 + tok0, head0, s.z);
+        load_tile(smem + kOffG, &tg, &ctl->q_full, s.q0 + tok0, head0, s.z);
+        int g = 0;
+        for (; g < steps; ++g) {
+          const int ks = g % kKStages, vs = g % kVStages;
+          if (g >= kKStages && !wait(&ctl->k_empty[ks], (g / kKStages + 1) & 1, w, 0x43)) break;
+          mbar_arrive_expect_tx(&ctl->k_full[ks], kTile);
+          load_tile(smem + kOffK + ks * kTile, &tk, &ctl->k_full[ks], s.k0 + 128 * g, hk, s.z);
+          if (g >= kVStages && !wait(&ctl->v_empty[vs], (g / kVStages + 1) & 1, w, 0x44)) {
+            wait(&ctl->k_full[ks], (g / kKStages) & 1, w, 0x45, true);  // this one has no pair
+            break;
+          }
+          mbar_arrive_expect_tx(&ctl->v_full[vs], kTile);
+          load_tile(smem + kOffV + vs * kTile, &tv, &ctl->v_full[vs], s.k0 + 128 * g, hk, s.z);
+        }
+        wait(&ctl->q_full, 0, w, 0x46, true);
+        for (int i = 0; i < kKStages; ++i) {
+          const int fills = g > i ? (g - i + kKStages - 1) / kKStages : 0;
+          if (fills) wait(&ctl->k_full[i], (fills - 1) & 1, w, 0x47, true);
+        }
+        for (int i = 0; i < kVStages; ++i) {
+          const int fills = g > i ? (g - i + kVStages - 1) / kVStages : 0;
+          if (fills) wait(&ctl->v_full[i], (fills - 1) & 1, w, 0x48, true);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 9) {
+      if (lane == 0 && steps > 0) {
+        constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
+        constexpr uint32_t kIdescG = idesc_bf16_f32(128, 128, false, true);
+        auto operand = [&](uint32_t at, uint32_t lbo) {
+          return smem_desc_sw128(smem_addr(smem + at), lbo, 1024);
+        };
+        const uint64_t qd = operand(kOffQ, 16), gd = operand(kOffG, 16);
+        auto ss = [&](uint32_t d, uint64_t ad, uint64_t bd) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint64_t o = ((i >> 2) * (kTile / 2) + (i & 3) * 32) >> 4;
+            mma_ss(tmem + d, ad + o, bd + o, kIdescS, i > 0);
+          }
+        };
+        // S and dP of step g
+        auto scores = [&](int g) {
+          const int ks = g % kKStages, vs = g % kVStages;
+          if (!wait(&ctl->k_ready[ks], (g / kKStages) & 1, w, 0x49)) return false;
+          if (g > 0 && !wait(&ctl->s_empty, (g - 1) & 1, w, 0x4a)) return false;
+          tc_fence_after();
+          ss(kColS, qd, operand(kOffK + ks * kTile, 16));
+          mma_commit(&ctl->s_full);
+          if (!wait(&ctl->v_full[vs], (g / kVStages) & 1, w, 0x4b)) return false;
+          tc_fence_after();
+          ss(kColDP + 128 * (g & 1), gd, operand(kOffV + vs * kTile, 16));
+          mma_commit(&ctl->dp_full[g & 1]);
+          mma_commit(&ctl->v_empty[vs]);
+          return true;
+        };
+        bool ok = a.stall ? wait(&ctl->never, 0, w, 0x5f) : wait(&ctl->q_full, 0, w, 0x4c);
+        ok = ok && scores(0);
+        for (int g = 0; g < steps && ok; ++g) {
+          if (g + 1 < steps && !scores(g + 1)) break;
+          if (!wait(&ctl->ds_full[g & 1], (g >> 1) & 1, w, 0x4d)) break;
+          tc_fence_after();
+          const uint64_t kd = operand(kOffK + (g % kKStages) * kTile, kTile / 2);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            mma_ts(tmem + kColDQ, tmem + kColDP + 128 * (g & 1) + 64 * (i >> 2) + 8 * (i & 3),
+                   kd + ((i * 2048) >> 4), kIdescG, (g > 0 || i > 0) ? 1u : 0u);
+          mma_commit(&ctl->k_empty[g % kKStages]);
+          if (g + 1 == steps) mma_commit(&ctl->acc_full);
+        }
+        mma_commit(&ctl->drain);
+        wait(&ctl->drain, 0, w, 0x4e, true);
+      }
+      __syncwarp();
+    } else if (warp == 11) {
+      for (int g = 0; g < steps; ++g) {
+        const int ks = g % kKStages;
+        if (!wait_warp(&ctl->k_full[ks], (g / kKStages) & 1, w, 0x4f)) break;
+        if (s.nk - 128 * g < 128) zero_rows(smem + kOffK + ks * kTile, s.nk - 128 * g);
+        if (lane == 0) mbar_arrive(&ctl->k_ready[ks]);
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, kTmemCols);
+}
+
+}  // namespace dq
+}  // namespace bwd
+}  // namespace prompt
+}  // namespace vsa

@@ -489,6 +489,29 @@ VSA_API vsa_status vsa_fwd_prompt(const vsa_bf16 *q, const vsa_bf16 *k, const vs
                                   int Sk, int D, int causal, float scale, vsa_bf16 *out,
                                   float *lse, vsa_stream_t stream);
 
+/* Gradient: dq, dk, dv of vsa_fwd_prompt for an upstream gradient dout.  With p, lse of the
+ * forward, D_i = dout_i . out_i and ds_ij = p_ij (dout_i . v_j - D_i):
+ *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i,
+ * dk and dv summed over the query heads of a key/value head.  Rows that attend nothing get
+ * dq = 0, keys that nothing attends dk = dv = 0; rows of no sequence as in the forward (packed:
+ * not written; padded: 0).
+ *   q, k, v, q_seq, k_seq, sizes, causal, scale: as given to the forward; out, lse what it
+ *           returned; dout as out.
+ *   strides int64 [24]: (batch, head, token) of q, k, v, out, dout, dq, dk, dv.
+ *   workspace  vsa_bwd_prompt_workspace_bytes() bytes, 16-byte aligned, no initialisation
+ *           needed; calls sharing it must not overlap on the GPU.
+ * No atomics: results do not depend on timing.  Three kernels. */
+VSA_API vsa_status vsa_bwd_prompt(const vsa_bf16 *q, const vsa_bf16 *k, const vsa_bf16 *v,
+                                  const vsa_bf16 *out, const vsa_bf16 *dout, const float *lse,
+                                  const int64_t *strides, const int32_t *q_seq,
+                                  const int32_t *k_seq, int packed, int B, int Hq, int Hkv, int Sq,
+                                  int Sk, int D, int causal, float scale, vsa_bf16 *dq,
+                                  vsa_bf16 *dk, vsa_bf16 *dv, void *workspace,
+                                  size_t workspace_bytes, vsa_stream_t stream);
+
+/* Workspace bytes vsa_bwd_prompt needs for this shape (0 for an invalid one). */
+VSA_API size_t vsa_bwd_prompt_workspace_bytes(int packed, int B, int Hq, int Hkv, int Sq);
+
 /* Synchronises `stream`, then reads and clears the device status word of the current
  * device: VSA_OK, or VSA_ERR_DEVICE_TIMEOUT if a kernel gave up on a wait since the
  * last call (`detail`, if not NULL, receives the recorded code). */
