@@ -9,7 +9,9 @@ Functions mirror the C entry points:
   vsa_fwd, vsa_fwd_gqa, vsa_fwd_split, vsa_fwd_from_mask, jenga_fwd, vsa_bwd, vsa_lut_to_bitmap,
   vsa_bitmap_to_lut, vsa_fwd_from_host, vsa_device_status, vsa_workspace_bytes,
   vsa_block_mean, vsa_select_blocks, and over an 8-bit cache (Cache8): vsa_cache_select,
-  vsa_cache_write, vsa_fwd_cache, vsa_cache_evict
+  vsa_cache_write, vsa_fwd_cache, vsa_cache_evict; over the pool of its pages (Pages):
+  vsa_pages_reserve, vsa_pages_free, vsa_cache_fork, vsa_cache_compact; over whole prompts:
+  vsa_fwd_prompt, vsa_bwd_prompt
 """
 from __future__ import annotations
 
@@ -38,7 +40,8 @@ EXPORTS = ("vsa_fwd", "jenga_fwd", "vsa_workspace_bytes", "vsa_lut_to_bitmap",
            "vsa_bwd_workspace_bytes", "vsa_set_wait_limit_ns", "vsa_set_stall_test",
            "vsa_block_mean", "vsa_select_blocks", "vsa_cache_select", "vsa_cache_write",
            "vsa_fwd_cache", "vsa_cache_workspace_bytes", "vsa_cache_evict", "vsa_fwd_prompt",
-           "vsa_bwd_prompt", "vsa_bwd_prompt_workspace_bytes")
+           "vsa_bwd_prompt", "vsa_bwd_prompt_workspace_bytes", "vsa_pages_free",
+           "vsa_pages_reserve", "vsa_cache_fork", "vsa_cache_compact")
 MAX_SPLITS = 64
 
 
@@ -127,6 +130,14 @@ def load(path: str = LIB_PATH):
     h.vsa_bwd_prompt_workspace_bytes.argtypes = [i32] * 5
     h.vsa_bwd_prompt.restype = i32
     h.vsa_bwd_prompt.argtypes = [P] * 9 + [i32] * 8 + [f32, P, P, P, P, sz, P]
+    h.vsa_pages_free.restype = i32
+    h.vsa_pages_free.argtypes = [P, P] + [i32] * 5 + [P] * 3
+    h.vsa_pages_reserve.restype = i32
+    h.vsa_pages_reserve.argtypes = [P, P, P] + [i32] * 5 + [P] * 4
+    h.vsa_cache_fork.restype = i32
+    h.vsa_cache_fork.argtypes = [P, P, P] + [i32] * 7 + [P] * 11
+    h.vsa_cache_compact.restype = i32
+    h.vsa_cache_compact.argtypes = [P] + [i32] * 6 + [P] * 10
     _fast = _load_fast(h)
     _lib = h
     return h
@@ -808,6 +819,120 @@ def vsa_cache_evict(weight, table, lens, budget, block=64, n_first=0, n_last=1,
     return Evicted(table_out, weight_out, lens_out, freed, n_freed)
 
 
+class Pages(NamedTuple):
+    """The state of a pool of pages: the table entries that name each, and the bitmap of those
+    that none names (bit p % 32 of word p // 32)."""
+    refs: torch.Tensor  # int32 [pages]
+    free: torch.Tensor  # int32 [ceil(pages / 32)]
+
+
+def new_pages(pages, device=None) -> Pages:
+    """The state of an empty pool."""
+    device = device or "cuda"
+    return Pages(torch.zeros(pages, dtype=torch.int32, device=device),
+                 torch.full(((pages + 31) // 32,), -1, dtype=torch.int32, device=device))
+
+
+def _pool(pool, dev, pages=None):
+    """(pages, addresses of refs and free) of a checked pool."""
+    refs, free = pool
+    if pages is None:
+        pages = _lead("pool.refs", refs, torch.int32, 1)[0][0]
+    return (pages, _need("pool.refs", refs, torch.int32, (pages,), dev),
+            _need("pool.free", free, torch.int32, ((pages + 31) // 32,), dev))
+
+
+def vsa_pages_free(pool, table, lens=None, block=64, stream=None):
+    """Let pages go: entries of table (int32 [B,Hkv,max_blocks]) from block ceil(lens[b] / block)
+    on -- lens None: all of them -- become -1, and their pages lose a reference each.  Takes
+    Evicted.freed as well as tables."""
+    if stream is None and _short("vsa_pages_free", "pages_free", pool, table, lens,
+                                 block) is not None:
+        return
+    _whole("block", block)
+    (B, Hkv, max_blocks), dev = _lead("table", table, torch.int32, 3)
+    lens_p = _maybe("lens", lens, torch.int32, (B,), dev)
+    pages, refs_p, free_p = _pool(pool, dev)
+    _call("vsa_pages_free", dev, stream, table.data_ptr(), lens_p, B, Hkv, max_blocks, block,
+          pages, refs_p, free_p)
+
+
+def vsa_pages_reserve(pool, table, lens, n_new=None, block=64, stream=None):
+    """Map pages for the tokens lens[b] .. lens[b] + n_new[b] - 1 (n_new int32 [B]; None: one
+    token each) wherever table (int32 [B,Hkv,max_blocks], changed in place) names none.  Returns
+    lacking int32 [B], the pages that the pool did not have."""
+    if stream is None:
+        r = _short("vsa_pages_reserve", "pages_reserve", pool, table, lens, n_new, block)
+        if r is not None:
+            return r[0]
+    _whole("block", block)
+    (B, Hkv, max_blocks), dev = _lead("table", table, torch.int32, 3)
+    lens_p = _need("lens", lens, torch.int32, (B,), dev)
+    new_p = _maybe("n_new", n_new, torch.int32, (B,), dev)
+    pages, refs_p, free_p = _pool(pool, dev)
+    with torch.cuda.stream(stream):
+        lacking = torch.empty(B, dtype=torch.int32, device=table.device)
+    _call("vsa_pages_reserve", dev, stream, table.data_ptr(), lens_p, new_p, B, Hkv, max_blocks,
+          block, pages, refs_p, free_p, lacking.data_ptr())
+    return lacking
+
+
+class Forked(NamedTuple):
+    """What vsa_cache_fork makes: the children's table and lengths, and the pages that the pool
+    did not have for each."""
+    table: torch.Tensor
+    lens: torch.Tensor
+    lacking: torch.Tensor
+
+
+def vsa_cache_fork(cache, pool, table, lens, parent, table_out=None, stream=None) -> Forked:
+    """Children of the sequences that the cache holds: child i goes on from sequence parent[i]
+    (int32 [N]).  Full blocks are shared, a part-full last one is copied to a page of its own.
+    table_out (int32 [N,Hkv,max_blocks]) is written if given: it must name no page that has not
+    been let go."""
+    if stream is None:
+        r = _short("vsa_cache_fork", "cache_fork", cache, pool, table, lens, parent, table_out)
+        if r is not None:
+            return Forked._make(r)
+    (B, Hkv, max_blocks), dev = _lead("table", table, torch.int32, 3)
+    lens_p = _need("lens", lens, torch.int32, (B,), dev)
+    (N,), _ = _lead("parent", parent, torch.int32, 1)
+    parent_p = _need("parent", parent, torch.int32, (N,), dev)
+    pages, block, kc, vc, ks, vs = _cache(cache, dev)
+    mean_p = _maybe("cache.k_mean", cache[4], torch.bfloat16, (pages, HEAD_DIM), dev)
+    _, refs_p, free_p = _pool(pool, dev, pages)
+    with torch.cuda.stream(stream):
+        if table_out is None:
+            table_out = torch.empty((N, Hkv, max_blocks), dtype=torch.int32, device=table.device)
+        out = torch.empty((2, N), dtype=torch.int32, device=table.device)
+    out_p = _need("table_out", table_out, torch.int32, (N, Hkv, max_blocks), dev)
+    _call("vsa_cache_fork", dev, stream, table.data_ptr(), lens_p, parent_p, B, N, Hkv, HEAD_DIM,
+          max_blocks, block, pages, kc, vc, ks, vs, mean_p, refs_p, free_p, out_p,
+          out[0].data_ptr(), out[1].data_ptr())
+    return Forked(table_out, out[0], out[1])
+
+
+def vsa_cache_compact(cache, pool, table, stream=None):
+    """Close the pool up: the pages in use become its first ones, and table (int32
+    [B,Hkv,max_blocks]) follows.  Returns (to int32 [pages], where each page in use is now, -1
+    for free ones; n_used int32 [1])."""
+    if stream is None:
+        r = _short("vsa_cache_compact", "cache_compact", cache, pool, table)
+        if r is not None:
+            return r
+    (B, Hkv, max_blocks), dev = _lead("table", table, torch.int32, 3)
+    table_p = _need("table", table, torch.int32, (B, Hkv, max_blocks), dev)
+    pages, block, kc, vc, ks, vs = _cache(cache, dev)
+    mean_p = _maybe("cache.k_mean", cache[4], torch.bfloat16, (pages, HEAD_DIM), dev)
+    _, refs_p, free_p = _pool(pool, dev, pages)
+    with torch.cuda.stream(stream):
+        to = torch.empty(pages, dtype=torch.int32, device=table.device)
+        n_used = torch.empty(1, dtype=torch.int32, device=table.device)
+    _call("vsa_cache_compact", dev, stream, table_p, B, Hkv, HEAD_DIM, max_blocks, block, pages,
+          kc, vc, ks, vs, mean_p, refs_p, free_p, to.data_ptr(), n_used.data_ptr())
+    return to, n_used
+
+
 # ------------------------------------------------------------- attention over whole prompts
 def _rows(name, t, dtype, ndim, dev=None, shape=None):
     """A tensor of rows: any strides, but the last axis' elements lie side by side."""
@@ -885,6 +1010,10 @@ def vsa_fwd_prompt(q, k, v, q_seq=None, k_seq=None, causal=True, scale=None, out
     strides but the last.  causal: the last query is at the last key, query i attends keys up
     to i + nk - nq.  Returns (out, lse or None), lse float32 (base 2) [Hq,tokens] or
     [B,Hq,Sq]."""
+    if stream is None:
+        r = _short("vsa_fwd_prompt", "fwd_prompt", q, k, v, q_seq, k_seq, causal, scale, out, lse)
+        if r is not None:
+            return r
     p = _Prompt(q, k, v, q_seq, k_seq)
     with torch.cuda.stream(stream):
         if out is None:
@@ -905,6 +1034,11 @@ def vsa_bwd_prompt(q, k, v, out, dout, lse, q_seq=None, k_seq=None, causal=True,
     out and lse; the rest as given to the forward.  dq, dk, dv may be given, as slices of one
     buffer for instance.  The workspace (uint8, bwd_prompt_workspace_bytes) is allocated if
     not given."""
+    if stream is None:
+        r = _short("vsa_bwd_prompt", "bwd_prompt", q, k, v, out, dout, lse, q_seq, k_seq, causal,
+                   scale, dq, dk, dv, workspace)
+        if r is not None:
+            return r
     p = _Prompt(q, k, v, q_seq, k_seq)
     ndim = q.dim()
     _rows("out", out, torch.bfloat16, ndim, p.dev, q.shape)

@@ -4,7 +4,7 @@ with g++.
 
     python -m block_sparse_attention_vsa_gb300.build [--force]
 
-Four translation units compiled side by side, one -gencode (sm_103a), static CUDA runtime,
+Five translation units compiled side by side, one -gencode (sm_103a), static CUDA runtime,
 no cmake.
 """
 from __future__ import annotations
@@ -21,17 +21,18 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libvsa_gb300.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("vsa_api.cu", "vsa_serve_api.cu", "vsa_prompt_api.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("vsa_api.cu", "vsa_serve_api.cu", "vsa_prompt_api.cu",
+                                              "vsa_pages_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in (
     "vsa_fwd_kernel.cuh", "vsa_bwd_kernel.cuh", "vsa_select_kernel.cuh", "vsa_cache_kernel.cuh",
-    "vsa_prompt_common.cuh", "vsa_prompt_fwd_kernel.cuh", "vsa_prompt_bwd_kernel.cuh",
-    "sm103_ptx.cuh", "vsa_warp_ptx.cuh", "vsa_host.h")] + [
+    "vsa_prompt_common.cuh", "vsa_prompt_fwd_kernel.cuh", "vsa_prompt_bwd_kernel.cuh", "vsa_pages_kernel.cuh",
+    "sm103_ptx.cuh", "vsa_warp_ptx.cuh", "vsa_host.h", "vsa_launch.h")] + [
     os.path.join(ROOT, "include", "vsa.h")]
 TORCH_SOURCE = os.path.join(CSRC, "vsa_torch.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-shared", "-Xcompiler", "-fPIC",
-         "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr", "--threads", "4"]
+         "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr", "--threads", "5"]
 
 
 def nvcc() -> str:

@@ -1,0 +1,484 @@
+// vsa_pages_kernel.cuh -- the pages of the 8-bit cache: mapping them ahead of a write, letting
+// them go, forking sequences that share them, and closing up a pool.
+//
+// A pool's state is refs[p], the table entries that name page p, and a bitmap of the pages that
+// none names.  Taking always the lowest free page makes every outcome unique: counts change by
+// integer atomics, whose order does not matter, and the r-th page asked for is the r-th set bit
+// of the bitmap, found by counting.  A whole pool's bitmap is small (a pool of 100,000 pages:
+// 12.5 KB), so every CTA of one cluster counts all of it for itself, and only the rows of the
+// tables are divided among them.
+//
+// Launched with programmatic serialization, like the other serving kernels: everything is read
+// by ordinary loads behind the wait for the predecessor.
+#pragma once
+
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "vsa_warp_ptx.cuh"
+
+namespace vsa {
+
+constexpr int kPagesThreads = 1024;  // of a CTA that counts
+constexpr int kPagesCluster = 8;
+constexpr int kPagesWarps = kPagesCluster * (kPagesThreads / 32);
+
+struct Pool {
+  int32_t* refs;
+  uint32_t* free;
+  int pages;
+};
+
+__device__ __forceinline__ bool is_page(int p, int pages) { return p >= 0 && p < pages; }
+
+// Blocks that `tokens` tokens fill or begin, max_blocks at most.
+__device__ __forceinline__ int blocks_of(long long tokens, int block, int max_blocks) {
+  const long long n = tokens <= 0 ? 0 : (tokens + block - 1) / block;
+  return n < max_blocks ? (int)n : max_blocks;
+}
+
+// The word w of the bitmap; bits past the pool count as not free.
+__device__ __forceinline__ uint32_t free_word(const Pool& p, long long w) {
+  const uint32_t x = read_global(p.free + w);
+  const long long left = p.pages - w * 32;
+  return left >= 32 ? x : x & ((1u << left) - 1u);
+}
+
+// The position of the n-th (from 0) set bit; there is one.
+__device__ __forceinline__ int nth_bit(uint32_t x, int n) {
+  int at = 0;
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    const int c = __popc(x & ((1u << s) - 1u));
+    if (n >= c) {
+      n -= c;
+      x >>= s;
+      at += s;
+    }
+  }
+  return at;
+}
+
+// Sum over the CTA's threads before this one; *total of all.  s_warp [33] is scratch.
+__device__ __forceinline__ int block_before(int x, int* s_warp, int* total) {
+  const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
+  int sum = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += y;
+  }
+  if (lane == 31) s_warp[warp] = sum;
+  __syncthreads();
+  if (warp == 0) {
+    const int n = (int)blockDim.x >> 5;
+    const int t = lane < n ? s_warp[lane] : 0;
+    int run = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += y;
+    }
+    s_warp[lane] = run - t;
+    if (lane == 31) s_warp[32] = run;
+  }
+  __syncthreads();
+  const int before = s_warp[warp] + sum - x;
+  *total = s_warp[32];
+  __syncthreads();
+  return before;
+}
+
+// Free pages counted: thread t of the CTA has the words [t * per, (t + 1) * per), and
+// before[t] free pages come before them (before[kPagesThreads]: all).
+struct FreeCount {
+  int* before;
+  long long words;
+  int per, total;
+};
+__device__ __forceinline__ FreeCount count_free(const Pool& p, int* s_before, int* s_warp) {
+  FreeCount f;
+  f.before = s_before;
+  f.words = ((long long)p.pages + 31) / 32;
+  f.per = (int)((f.words + kPagesThreads - 1) / kPagesThreads);
+  const long long w0 = (long long)threadIdx.x * f.per;
+  int n = 0;
+  for (int i = 0; i < f.per; ++i)
+    if (w0 + i < f.words) n += __popc(free_word(p, w0 + i));
+  s_before[threadIdx.x] = block_before(n, s_warp, &f.total);
+  if (threadIdx.x == 0) s_before[kPagesThreads] = f.total;
+  __syncthreads();
+  return f;
+}
+// The r-th free page; -1 where there are not as many.
+__device__ __forceinline__ int nth_free(const Pool& p, const FreeCount& f, int r) {
+  int lo = 0;
+#pragma unroll
+  for (int s = kPagesThreads / 2; s > 0; s >>= 1)
+    if (f.before[lo + s] <= r) lo += s;
+  int left = r - f.before[lo];
+  for (long long w = (long long)lo * f.per; w < f.words; ++w) {
+    const uint32_t x = free_word(p, w);
+    const int n = __popc(x);
+    if (left < n) return (int)(w * 32) + nth_bit(x, left);
+    left -= n;
+  }
+  return -1;
+}
+// The first n free pages are free no more (by all CTAs of the cluster, a share each, once
+// every one has read the bitmap for the last time).
+__device__ __forceinline__ void clear_first(const Pool& p, const FreeCount& f, int n, int rank) {
+  if ((int)(threadIdx.x % kPagesCluster) != rank) return;
+  int left = n - f.before[threadIdx.x];
+  const long long w0 = (long long)threadIdx.x * f.per;
+  for (int i = 0; i < f.per && left > 0; ++i) {
+    if (w0 + i >= f.words) return;
+    uint32_t x = free_word(p, w0 + i);
+    const int c = __popc(x);
+    if (c == 0) continue;
+    if (left >= c) {
+      x = 0;
+    } else {
+      for (int k = 0; k < left; ++k) x &= x - 1;
+    }
+    left -= c;
+    p.free[w0 + i] = x;
+  }
+}
+
+// ------------------------------------------------------------------------------- free
+struct FreeArgs {
+  Pool pool;
+  int32_t* table;
+  const int32_t* lens;  // or null: every entry goes
+  unsigned entries;
+  int Hkv, max_blocks, block;
+};
+// One reference less for every entry behind its sequence's last block, which becomes -1.  A
+// page given up more often than it was taken stays at 0.
+__global__ void __launch_bounds__(256) pages_free_kernel(const FreeArgs a) {
+  after_predecessor();
+  for (unsigned e = blockIdx.x * 256 + threadIdx.x; e < a.entries; e += gridDim.x * 256) {
+    if (a.lens != nullptr) {
+      const unsigned row = e / (unsigned)a.max_blocks;
+      const int j = (int)(e - row * (unsigned)a.max_blocks);
+      if (j < blocks_of(read_global(a.lens + row / (unsigned)a.Hkv), a.block, a.max_blocks))
+        continue;
+    }
+    const int p = read_global(a.table + e);
+    if (p == -1) continue;
+    a.table[e] = -1;
+    if (!is_page(p, a.pool.pages)) continue;
+    const int had = atomicSub(a.pool.refs + p, 1);
+    if (had == 1)
+      atomicOr(a.pool.free + (p >> 5), 1u << (p & 31));
+    else if (had <= 0)
+      atomicAdd(a.pool.refs + p, 1);
+  }
+}
+
+// ---------------------------------------------------------------------------- reserve
+struct ReserveArgs {
+  Pool pool;
+  int32_t* table;
+  const int32_t *lens, *n_new;  // n_new or null: one token each
+  int32_t* lacking;
+  int B, Hkv, max_blocks, block;
+};
+// What the cluster shares: the pages that each CTA asks for.
+struct PagesShared {
+  int before[kPagesThreads + 1];
+  int warp[33];
+  int asked;
+};
+// Pages asked for by the CTAs before this one; *all of them.  (One cluster barrier.)
+__device__ __forceinline__ int cluster_before(PagesShared& s, int asked, int* all) {
+  auto cluster = cooperative_groups::this_cluster();
+  if (threadIdx.x == 0) s.asked = asked;
+  cluster.sync();
+  const int rank = (int)cluster.block_rank();
+  int before = 0, sum = 0;
+#pragma unroll
+  for (int c = 0; c < kPagesCluster; ++c) {
+    const int n = *cluster.map_shared_rank(&s.asked, c);
+    if (c < rank) before += n;
+    sum += n;
+  }
+  *all = sum;
+  return before;
+}
+
+__global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesThreads)
+    pages_reserve_kernel(const ReserveArgs a) {
+  __shared__ PagesShared s;
+  auto cluster = cooperative_groups::this_cluster();
+  const int rank = (int)cluster.block_rank();
+  const int lane = (int)threadIdx.x & 31, warp = rank * (kPagesThreads / 32) + ((int)threadIdx.x >> 5);
+  const long long rows = (long long)a.B * a.Hkv;
+  const long long r0 = rows * warp / kPagesWarps, r1 = rows * (warp + 1) / kPagesWarps;
+  after_predecessor();
+  for (int b = rank * kPagesThreads + (int)threadIdx.x; b < a.B; b += kPagesCluster * kPagesThreads)
+    a.lacking[b] = 0;
+  // blocks [first, last) of a row hold tokens to come
+  auto range = [&](long long row, int* first, int* last) {
+    const int b = (int)(row / a.Hkv);
+    const long long len = read_global(a.lens + b) > 0 ? read_global(a.lens + b) : 0;
+    long long more = 1;
+    if (a.n_new != nullptr) more = read_global(a.n_new + b) > 0 ? read_global(a.n_new + b) : 0;
+    *first = (int)(len / a.block < a.max_blocks ? len / a.block : a.max_blocks);
+    *last = blocks_of(len + more, a.block, a.max_blocks);
+    return b;
+  };
+  auto wanted = [&](long long row, int j, int last) {
+    return j < last && !is_page(read_global(a.table + row * a.max_blocks + j), a.pool.pages);
+  };
+  int asked = 0;
+  for (long long row = r0; row < r1; ++row) {
+    int first, last;
+    range(row, &first, &last);
+    for (int j = first; j < last; j += 32)
+      asked += __popc(__ballot_sync(0xffffffffu, wanted(row, j + lane, last)));
+  }
+  const FreeCount f = count_free(a.pool, s.before, s.warp);
+  int in_cta, all;
+  int at = block_before(lane == 0 ? asked : 0, s.warp, &in_cta);
+  at = __shfl_sync(0xffffffffu, at, 0);
+  at += cluster_before(s, in_cta, &all);
+  if (asked > 0)
+    for (long long row = r0; row < r1; ++row) {
+      int first, last;
+      const int b = range(row, &first, &last);
+      for (int j = first; j < last; j += 32) {
+        const bool want = wanted(row, j + lane, last);
+        const uint32_t votes = __ballot_sync(0xffffffffu, want);
+        const int r = at + __popc(votes & ((1u << lane) - 1u));
+        at += __popc(votes);
+        int p = -1;
+        if (want) {
+          if (r < f.total) p = nth_free(a.pool, f, r);
+          if (p >= 0) a.pool.refs[p] = 1;
+          a.table[row * a.max_blocks + j + lane] = p;
+        }
+        const uint32_t none = __ballot_sync(0xffffffffu, want && p < 0);
+        if (none && lane == 0) atomicAdd(a.lacking + b, __popc(none));
+      }
+    }
+  cluster.sync();
+  clear_first(a.pool, f, all, rank);
+}
+
+// ------------------------------------------------------------------------------- fork
+struct CachePtrs {
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
+  uint16_t* k_mean;  // or null
+};
+struct ForkArgs {
+  Pool pool;
+  CachePtrs cache;
+  const int32_t *table, *lens, *parent;
+  int32_t *table_out, *lens_out, *lacking;
+  int B, N, Hkv, max_blocks, block;
+};
+// A child's parent and tokens (none for a parent that is not there).
+__device__ __forceinline__ int fork_parent(const ForkArgs& a, int i, int* tokens) {
+  const int p = read_global(a.parent + i);
+  if (p < 0 || p >= a.B) {
+    *tokens = 0;
+    return -1;
+  }
+  const long long most = (long long)a.max_blocks * a.block, n = read_global(a.lens + p);
+  *tokens = n < 0 ? 0 : (int)(n < most ? n : most);
+  return p;
+}
+// Pages for the part-full blocks of the children: entry `tokens / block` of their rows.
+__global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesThreads)
+    pages_fork_kernel(const ForkArgs a) {
+  __shared__ PagesShared s;
+  auto cluster = cooperative_groups::this_cluster();
+  const int rank = (int)cluster.block_rank();
+  const int lane = (int)threadIdx.x & 31, warp = rank * (kPagesThreads / 32) + ((int)threadIdx.x >> 5);
+  const long long rows = (long long)a.N * a.Hkv;
+  const long long r0 = rows * warp / kPagesWarps, r1 = rows * (warp + 1) / kPagesWarps;
+  after_predecessor();
+  for (int i = rank * kPagesThreads + (int)threadIdx.x; i < a.N; i += kPagesCluster * kPagesThreads) {
+    int n;
+    fork_parent(a, i, &n);
+    a.lens_out[i] = n;
+    a.lacking[i] = 0;
+  }
+  auto wanted = [&](long long row, int* full) {
+    if (row >= r1) return false;
+    const int i = (int)(row / a.Hkv), h = (int)(row - (long long)i * a.Hkv);
+    int n;
+    const int p = fork_parent(a, i, &n);
+    *full = n / a.block;
+    return n % a.block != 0 &&
+           is_page(read_global(a.table + ((long long)p * a.Hkv + h) * a.max_blocks + *full),
+                   a.pool.pages);
+  };
+  int asked = 0;
+  for (long long row = r0; row < r1; row += 32) {
+    int full;
+    asked += __popc(__ballot_sync(0xffffffffu, wanted(row + lane, &full)));
+  }
+  const FreeCount f = count_free(a.pool, s.before, s.warp);
+  int in_cta, all;
+  int at = block_before(lane == 0 ? asked : 0, s.warp, &in_cta);
+  at = __shfl_sync(0xffffffffu, at, 0);
+  at += cluster_before(s, in_cta, &all);
+  for (long long row = r0; row < r1; row += 32) {
+    int full = 0;
+    const bool want = wanted(row + lane, &full);
+    const uint32_t votes = __ballot_sync(0xffffffffu, want);
+    const int r = at + __popc(votes & ((1u << lane) - 1u));
+    at += __popc(votes);
+    if (want) {
+      const int p = r < f.total ? nth_free(a.pool, f, r) : -1;
+      if (p >= 0)
+        a.pool.refs[p] = 1;
+      else
+        atomicAdd(a.lacking + (row + lane) / a.Hkv, 1);
+      a.table_out[(row + lane) * a.max_blocks + full] = p;
+    }
+  }
+  cluster.sync();
+  clear_first(a.pool, f, all, rank);
+}
+
+// `tokens` tokens of page src to page dst, with the page's scales and mean, by a CTA.
+__device__ __forceinline__ void copy_page(const CachePtrs& c, int block, int src, int dst,
+                                          int tokens) {
+  const int n = tokens * 8;  // pieces of 16 bytes in the keys, and as many in the values
+  const long long s = (long long)src * block * 8, d = (long long)dst * block * 8;
+  const uint4* k = reinterpret_cast<const uint4*>(c.k) + s;
+  const uint4* v = reinterpret_cast<const uint4*>(c.v) + s;
+  uint4* ko = reinterpret_cast<uint4*>(c.k) + d;
+  uint4* vo = reinterpret_cast<uint4*>(c.v) + d;
+  for (int i = (int)threadIdx.x; i < n; i += 2 * (int)blockDim.x) {
+    const int i2 = i + (int)blockDim.x;
+    const bool two = i2 < n;
+    const uint4 k1 = k[i], v1 = v[i];
+    uint4 k2, v2;
+    if (two) {
+      k2 = k[i2];
+      v2 = v[i2];
+    }
+    ko[i] = k1;
+    vo[i] = v1;
+    if (two) {
+      ko[i2] = k2;
+      vo[i2] = v2;
+    }
+  }
+  if (threadIdx.x < 16 && c.k_mean != nullptr)
+    reinterpret_cast<uint4*>(c.k_mean)[(long long)dst * 16 + threadIdx.x] =
+        reinterpret_cast<const uint4*>(c.k_mean)[(long long)src * 16 + threadIdx.x];
+  if (threadIdx.x == 32) c.k_scale[dst] = c.k_scale[src];
+  if (threadIdx.x == 33) c.v_scale[dst] = c.v_scale[src];
+}
+
+// A CTA a row: the entries of full blocks, each with a reference more, -1 behind, and what the
+// part-full block holds.
+__global__ void __launch_bounds__(256) cache_fork_kernel(const ForkArgs a) {
+  const long long row = blockIdx.x;
+  const int i = (int)(row / a.Hkv), h = (int)(row - (long long)i * a.Hkv);
+  after_predecessor();
+  int n;
+  const int p = fork_parent(a, i, &n);
+  const int full = n / a.block;
+  const bool part = n % a.block != 0;
+  const int32_t* from = a.table + ((long long)(p < 0 ? 0 : p) * a.Hkv + h) * a.max_blocks;
+  int32_t* to = a.table_out + row * a.max_blocks;
+  int src = -1, dst = -1;
+  if (part) {
+    src = read_global(from + full);
+    if (is_page(src, a.pool.pages)) dst = read_global(to + full);
+  }
+  for (int j = (int)threadIdx.x; j < a.max_blocks; j += 256) {
+    if (j == full && dst >= 0) continue;
+    int page = -1;
+    if (j < full) {
+      page = read_global(from + j);
+      if (is_page(page, a.pool.pages))
+        atomicAdd(a.pool.refs + page, 1);
+      else
+        page = -1;
+    }
+    to[j] = page;
+  }
+  if (dst >= 0) copy_page(a.cache, a.block, src, dst, n % a.block);
+}
+
+// ---------------------------------------------------------------------------- compact
+struct CompactArgs {
+  Pool pool;
+  CachePtrs cache;
+  int32_t *table, *to, *n_used;
+  long long entries;
+  int block;
+};
+// With U pages in use: where each goes.  Those below U stay, the r-th in use from U on goes to
+// the r-th free one (there are as many below U).
+__global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesThreads)
+    pages_compact_kernel(const CompactArgs a) {
+  __shared__ PagesShared s;
+  const int rank = (int)cooperative_groups::this_cluster().block_rank();
+  after_predecessor();
+  const FreeCount f = count_free(a.pool, s.before, s.warp);
+  const int used = a.pool.pages - f.total;
+  // free pages before page p
+  auto free_before = [&](int p) {
+    const long long w = p >> 5, t = w / f.per;
+    int n = f.before[t];
+    for (long long i = t * f.per; i < w; ++i) n += __popc(free_word(a.pool, i));
+    return n + __popc(free_word(a.pool, w) & ((1u << (p & 31)) - 1u));
+  };
+  // pages in use below U (U itself may be the pool's end)
+  const int below = used < a.pool.pages ? used - free_before(used) : used;
+  for (long long q = rank * kPagesThreads + (int)threadIdx.x; q < a.pool.pages;
+       q += kPagesCluster * kPagesThreads) {
+    const int p = (int)q;
+    int to = -1;
+    if (!((free_word(a.pool, p >> 5) >> (p & 31)) & 1u))
+      to = p < used ? p : nth_free(a.pool, f, p - free_before(p) - below);
+    a.to[p] = to;
+  }
+  if (rank == 0 && threadIdx.x == 0) *a.n_used = used;
+}
+// The moves, the counts, the bitmap and the table.
+__global__ void __launch_bounds__(256) cache_compact_kernel(const CompactArgs a) {
+  after_predecessor();
+  const int used = read_global(a.n_used);
+  const long long id = (long long)blockIdx.x * 256 + threadIdx.x, all = (long long)gridDim.x * 256;
+  for (long long e = id; e < a.entries; e += all) {
+    const int p = read_global(a.table + e);
+    if (is_page(p, a.pool.pages)) {
+      const int to = read_global(a.to + p);
+      if (to != p) a.table[e] = to;
+    }
+  }
+  for (long long w = id; w < ((long long)a.pool.pages + 31) / 32; w += all) {
+    const long long first = w * 32;
+    uint32_t x = 0xffffffffu;
+    if (first + 32 <= used)
+      x = 0;
+    else if (first < used)
+      x <<= used - first;
+    if (first + 32 > a.pool.pages) x &= (1u << (a.pool.pages - first)) - 1u;
+    a.pool.free[w] = x;
+  }
+  for (long long p = used + (long long)blockIdx.x; p < a.pool.pages; p += gridDim.x) {
+    const int to = read_global(a.to + p);
+    if (to < 0) continue;
+    copy_page(a.cache, a.block, (int)p, to, a.block);
+    if (threadIdx.x == 64) {
+      a.pool.refs[to] = a.pool.refs[p];
+      a.pool.refs[p] = 0;
+    }
+  }
+}
+
+}  // namespace vsa

@@ -1,5 +1,6 @@
 // vsa_torch.cpp -- the short way from torch tensors to the library's calls that run for
-// microseconds (block means, the choice of blocks, the 8-bit cache): argument checks,
+// microseconds (block means, the choice of blocks, the 8-bit cache and its pages, attention
+// over prompts): argument checks,
 // output allocation and the call in one step of C++.
 //
 // Every function returns its result, or the library's status as an int where that is not
@@ -32,6 +33,13 @@ struct Entry {
   decltype(&vsa_cache_write) cache_write;
   decltype(&vsa_fwd_cache) fwd_cache;
   decltype(&vsa_cache_evict) cache_evict;
+  decltype(&vsa_pages_free) pages_free;
+  decltype(&vsa_pages_reserve) pages_reserve;
+  decltype(&vsa_cache_fork) cache_fork;
+  decltype(&vsa_cache_compact) cache_compact;
+  decltype(&vsa_fwd_prompt) fwd_prompt;
+  decltype(&vsa_bwd_prompt) bwd_prompt;
+  decltype(&vsa_bwd_prompt_workspace_bytes) bwd_prompt_workspace_bytes;
 } lib;
 
 // Thrown where the long way has to be taken.
@@ -382,6 +390,266 @@ PyObject* cache_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A Pages tuple.
+struct PagesState {
+  int64_t pages;
+  int32_t* refs;
+  uint32_t* free;
+  PagesState(PyObject* o, const Device& dev) {
+    if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 2) throw LongWay();
+    pages = lead(PyTuple_GET_ITEM(o, 0), kI32, 1).size(0);
+    refs = need<int32_t>(PyTuple_GET_ITEM(o, 0), kI32, {pages}, dev);
+    free = need<uint32_t>(PyTuple_GET_ITEM(o, 1), kI32, {(pages + 31) / 32}, dev);
+  }
+};
+
+// (pool, table, lens, block)
+PyObject* pages_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return run(n, 4, [&]() -> PyObject* {
+    const at::Tensor& table = lead(a[1], kI32, 3);
+    const Device dev(table);
+    const PagesState p(a[0], dev);
+    const int block = whole(a[3]), B = to_int(table.size(0)), Hkv = to_int(table.size(1)),
+              blocks = to_int(table.size(2)), pages = to_int(p.pages);
+    const int32_t* lens = maybe<int32_t>(a[2], kI32, {B}, dev);
+    int32_t* tp = address<int32_t>(table);
+    const vsa_stream_t stream = dev.stream();
+    const vsa_status st = unlocked([&] {
+      return lib.pages_free(tp, lens, B, Hkv, blocks, block, pages, p.refs, p.free, stream);
+    });
+    if (st != VSA_OK) return PyLong_FromLong(st);
+    return tuple({});
+  });
+}
+
+// (pool, table, lens, n_new, block)
+PyObject* pages_reserve(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return run(n, 5, [&]() -> PyObject* {
+    const at::Tensor& table = lead(a[1], kI32, 3);
+    const Device dev(table);
+    const PagesState p(a[0], dev);
+    const int block = whole(a[4]), B = to_int(table.size(0)), Hkv = to_int(table.size(1)),
+              blocks = to_int(table.size(2)), pages = to_int(p.pages);
+    const int32_t* lens = need<int32_t>(a[2], kI32, {B}, dev);
+    const int32_t* n_new = maybe<int32_t>(a[3], kI32, {B}, dev);
+    const at::Tensor lacking = empty(table, kI32, {B});
+    int32_t *tp = address<int32_t>(table), *lp = address<int32_t>(lacking);
+    const vsa_stream_t stream = dev.stream();
+    const vsa_status st = unlocked([&] {
+      return lib.pages_reserve(tp, lens, n_new, B, Hkv, blocks, block, pages, p.refs, p.free, lp,
+                               stream);
+    });
+    if (st != VSA_OK) return PyLong_FromLong(st);
+    return tuple({THPVariable_Wrap(lacking)});
+  });
+}
+
+// (cache, pool, table, lens, parent, table_out)
+PyObject* cache_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return run(n, 6, [&]() -> PyObject* {
+    const at::Tensor& table = lead(a[2], kI32, 3);
+    const Device dev(table);
+    const Cache c(a[0], dev);
+    const PagesState p(a[1], dev);
+    if (p.pages != c.pages) throw LongWay();
+    vsa_bf16* mean = maybe<vsa_bf16>(c.k_mean, kBf16, {c.pages, VSA_HEAD_DIM}, dev);
+    const int64_t N = lead(a[4], kI32, 1).size(0);
+    const int v[6] = {to_int(table.size(0)), to_int(N),       to_int(table.size(1)),
+                      to_int(table.size(2)), to_int(c.block), to_int(c.pages)};
+    const int32_t* lens = need<int32_t>(a[3], kI32, {v[0]}, dev);
+    const int32_t* parent = need<int32_t>(a[4], kI32, {N}, dev);
+    at::Tensor made;
+    int32_t* to;
+    if (a[5] == Py_None) {
+      made = empty(table, kI32, {N, v[2], v[3]});
+      to = address<int32_t>(made);
+    } else {
+      to = need<int32_t>(a[5], kI32, {N, v[2], v[3]}, dev);
+    }
+    Parts parts(table, 2 * N);
+    const at::Tensor lens_out = parts.part({N}), lacking = parts.part({N});
+    int32_t *lo = address<int32_t>(lens_out), *mo = address<int32_t>(lacking);
+    const int32_t* tp = address<int32_t>(table);
+    const vsa_stream_t stream = dev.stream();
+    const vsa_status st = unlocked([&] {
+      return lib.cache_fork(tp, lens, parent, v[0], v[1], v[2], VSA_HEAD_DIM, v[3], v[4], v[5],
+                            c.k, c.v, c.k_scale, c.v_scale, mean, p.refs, p.free, to, lo, mo,
+                            stream);
+    });
+    if (st != VSA_OK) return PyLong_FromLong(st);
+    return tuple({a[5] == Py_None ? THPVariable_Wrap(made) : same(a[5]),
+                  THPVariable_Wrap(lens_out), THPVariable_Wrap(lacking)});
+  });
+}
+
+// (cache, pool, table)
+PyObject* cache_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return run(n, 3, [&]() -> PyObject* {
+    const at::Tensor& table = lead(a[2], kI32, 3);
+    const Device dev(table);
+    const Cache c(a[0], dev);
+    const PagesState p(a[1], dev);
+    if (p.pages != c.pages) throw LongWay();
+    vsa_bf16* mean = maybe<vsa_bf16>(c.k_mean, kBf16, {c.pages, VSA_HEAD_DIM}, dev);
+    const int v[5] = {to_int(table.size(0)), to_int(table.size(1)), to_int(table.size(2)),
+                      to_int(c.block), to_int(c.pages)};
+    const at::Tensor to = empty(table, kI32, {c.pages}), n_used = empty(table, kI32, {1});
+    int32_t *tp = address<int32_t>(table), *op = address<int32_t>(to),
+            *np = address<int32_t>(n_used);
+    const vsa_stream_t stream = dev.stream();
+    const vsa_status st = unlocked([&] {
+      return lib.cache_compact(tp, v[0], v[1], VSA_HEAD_DIM, v[2], v[3], v[4], c.k, c.v, c.k_scale,
+                               c.v_scale, mean, p.refs, p.free, op, np, stream);
+    });
+    if (st != VSA_OK) return PyLong_FromLong(st);
+    return tuple({THPVariable_Wrap(to), THPVariable_Wrap(n_used)});
+  });
+}
+
+// A bf16 tensor of rows: any strides, but its last axis lies in one piece.
+const at::Tensor& rows(PyObject* o, int64_t dims, const Device* dev = nullptr,
+                       const at::Tensor* like = nullptr) {
+  const at::Tensor& t = tensor(o);
+  if (t.scalar_type() != kBf16 || t.dim() != dims || !t.is_cuda() ||
+      (dev != nullptr && t.get_device() != dev->index) ||
+      (like != nullptr && t.sizes() != like->sizes()) || t.size(dims - 1) != VSA_HEAD_DIM ||
+      t.stride(dims - 1) != 1)
+    throw LongWay();
+  return t;
+}
+// The checked shape of a call over prompts (as the binding's _Prompt).
+struct Prompt {
+  const at::Tensor &q, &k, &v;
+  Device dev;
+  bool packed;
+  int64_t B, Hq, Hkv, Sq, Sk;
+  const int32_t *q_seq, *k_seq;
+  Prompt(PyObject* qo, PyObject* ko, PyObject* vo, PyObject* qs, PyObject* ks)
+      : q(tensor(qo)), k(tensor(ko)), v(tensor(vo)), dev(q), packed(q.dim() == 3) {
+    const int64_t dims = packed ? 3 : 4;
+    rows(qo, dims, &dev);
+    rows(ko, dims, &dev);
+    rows(vo, dims, &dev, &k);
+    int64_t n;
+    if (packed) {
+      Sq = q.size(0), Hq = q.size(1), Sk = k.size(0), Hkv = k.size(1);
+      n = lead(qs, kI32, 1).size(0);
+      B = n - 1;
+      if (B < 0) throw LongWay();
+      if (ks == Py_None) ks = qs;
+    } else {
+      B = q.size(0), Hq = q.size(1), Sq = q.size(2), Hkv = k.size(1), Sk = k.size(2);
+      if (k.size(0) != B) throw LongWay();
+      n = B;
+    }
+    q_seq = maybe<int32_t>(qs, kI32, {n}, dev);
+    k_seq = maybe<int32_t>(ks, kI32, {n}, dev);
+    for (int64_t x : {B, Hq, Hkv, Sq, Sk}) to_int(x);
+  }
+  // (batch, head, token) strides
+  void strides(const at::Tensor& t, int64_t* s) const {
+    s[0] = packed ? 0 : t.stride(0);
+    s[1] = t.stride(1);
+    s[2] = packed ? t.stride(0) : t.stride(2);
+  }
+  at::Tensor empty_like(const at::Tensor& t) const {
+    return at::detail::empty_cuda(t.sizes(), kBf16, t.device(), std::nullopt);
+  }
+  at::Tensor empty_lse() const {
+    return packed ? empty(q, kF32, {Hq, Sq}) : empty(q, kF32, {B, Hq, Sq});
+  }
+  float* lse(PyObject* o) const {
+    return packed ? need<float>(o, kF32, {Hq, Sq}, dev) : need<float>(o, kF32, {B, Hq, Sq}, dev);
+  }
+};
+
+// (q, k, v, q_seq, k_seq, causal, scale, out, lse)
+PyObject* fwd_prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return run(n, 9, [&]() -> PyObject* {
+    const Prompt p(a[0], a[1], a[2], a[3], a[4]);
+    const bool causal = truth(a[5]);
+    const float scale =
+        a[6] == Py_None ? (float)(1.0 / std::sqrt((double)VSA_HEAD_DIM)) : real(a[6]);
+    const at::Tensor out =
+        a[7] == Py_None ? p.empty_like(p.q) : rows(a[7], p.q.dim(), &p.dev, &p.q);
+    at::Tensor lse;
+    float* lp = nullptr;
+    PyObject* lse_given = nullptr;
+    if (a[8] == Py_True) {
+      lse = p.empty_lse();
+      lp = address<float>(lse);
+    } else if (a[8] == Py_None || a[8] == Py_False) {
+      lse_given = Py_None;
+    } else {
+      lp = p.lse(a[8]);
+      lse_given = a[8];
+    }
+    int64_t s[12];
+    p.strides(p.q, s);
+    p.strides(p.k, s + 3);
+    p.strides(p.v, s + 6);
+    p.strides(out, s + 9);
+    const vsa_bf16 *qp = address<vsa_bf16>(p.q), *kp = address<vsa_bf16>(p.k),
+                   *vp = address<vsa_bf16>(p.v);
+    vsa_bf16* op = address<vsa_bf16>(out);
+    const vsa_stream_t stream = p.dev.stream();
+    const vsa_status st = unlocked([&] {
+      return lib.fwd_prompt(qp, kp, vp, s, p.q_seq, p.k_seq, p.packed, (int)p.B, (int)p.Hq,
+                            (int)p.Hkv, (int)p.Sq, (int)p.Sk, VSA_HEAD_DIM, causal, scale, op, lp,
+                            stream);
+    });
+    if (st != VSA_OK) return PyLong_FromLong(st);
+    return tuple({a[7] == Py_None ? THPVariable_Wrap(out) : same(a[7]),
+                  lse_given != nullptr ? same(lse_given) : THPVariable_Wrap(lse)});
+  });
+}
+
+// (q, k, v, out, dout, lse, q_seq, k_seq, causal, scale, dq, dk, dv, workspace)
+PyObject* bwd_prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return run(n, 14, [&]() -> PyObject* {
+    const Prompt p(a[0], a[1], a[2], a[6], a[7]);
+    const int64_t dims = p.q.dim();
+    const at::Tensor &out = rows(a[3], dims, &p.dev, &p.q), &dout = rows(a[4], dims, &p.dev, &p.q);
+    const float* lp = p.lse(a[5]);
+    const bool causal = truth(a[8]);
+    const float scale =
+        a[9] == Py_None ? (float)(1.0 / std::sqrt((double)VSA_HEAD_DIM)) : real(a[9]);
+    const at::Tensor* like[3] = {&p.q, &p.k, &p.v};
+    at::Tensor d[3];
+    for (int i = 0; i < 3; ++i)
+      d[i] = a[10 + i] == Py_None ? p.empty_like(*like[i]) : rows(a[10 + i], dims, &p.dev, like[i]);
+    at::Tensor ws;
+    if (a[13] == Py_None) {
+      const size_t bytes = lib.bwd_prompt_workspace_bytes(p.packed, (int)p.B, (int)p.Hq,
+                                                          (int)p.Hkv, (int)p.Sq);
+      ws = empty(p.q, at::kByte, {(int64_t)bytes});
+    } else {
+      ws = tensor(a[13]);
+      if (!ws.is_cuda() || ws.get_device() != p.dev.index || !ws.is_contiguous()) throw LongWay();
+    }
+    int64_t s[24];
+    const at::Tensor* all[8] = {&p.q, &p.k, &p.v, &out, &dout, &d[0], &d[1], &d[2]};
+    for (int i = 0; i < 8; ++i) p.strides(*all[i], s + 3 * i);
+    const vsa_bf16* in[5];
+    vsa_bf16* res[3];
+    for (int i = 0; i < 5; ++i) in[i] = address<vsa_bf16>(*all[i]);
+    for (int i = 0; i < 3; ++i) res[i] = address<vsa_bf16>(d[i]);
+    void* wp = ws.data_ptr();
+    const size_t bytes = ws.nbytes();
+    const vsa_stream_t stream = p.dev.stream();
+    const vsa_status st = unlocked([&] {
+      return lib.bwd_prompt(in[0], in[1], in[2], in[3], in[4], lp, s, p.q_seq, p.k_seq, p.packed,
+                            (int)p.B, (int)p.Hq, (int)p.Hkv, (int)p.Sq, (int)p.Sk, VSA_HEAD_DIM,
+                            causal, scale, res[0], res[1], res[2], wp, bytes, stream);
+    });
+    if (st != VSA_OK) return PyLong_FromLong(st);
+    PyObject* o[3];
+    for (int i = 0; i < 3; ++i)
+      o[i] = a[10 + i] == Py_None ? THPVariable_Wrap(d[i]) : same(a[10 + i]);
+    return tuple({o[0], o[1], o[2]});
+  });
+}
+
 // bind(handle): takes the entry points from an open handle of the library.
 PyObject* bind(PyObject*, PyObject* arg) {
   void* h = PyLong_AsVoidPtr(arg);
@@ -392,7 +660,13 @@ PyObject* bind(PyObject*, PyObject* arg) {
   };
   if (!find(lib.block_mean, "vsa_block_mean") || !find(lib.select_blocks, "vsa_select_blocks") ||
       !find(lib.cache_select, "vsa_cache_select") || !find(lib.cache_write, "vsa_cache_write") ||
-      !find(lib.fwd_cache, "vsa_fwd_cache") || !find(lib.cache_evict, "vsa_cache_evict")) {
+      !find(lib.fwd_cache, "vsa_fwd_cache") || !find(lib.cache_evict, "vsa_cache_evict") ||
+      !find(lib.pages_free, "vsa_pages_free") ||
+      !find(lib.pages_reserve, "vsa_pages_reserve") ||
+      !find(lib.cache_fork, "vsa_cache_fork") ||
+      !find(lib.cache_compact, "vsa_cache_compact") ||
+      !find(lib.fwd_prompt, "vsa_fwd_prompt") || !find(lib.bwd_prompt, "vsa_bwd_prompt") ||
+      !find(lib.bwd_prompt_workspace_bytes, "vsa_bwd_prompt_workspace_bytes")) {
     PyErr_SetString(PyExc_RuntimeError, "the library lacks an entry point");
     return nullptr;
   }
@@ -407,6 +681,12 @@ PyMethodDef methods[] = {VSA_FAST(block_mean),
                          VSA_FAST(cache_write),
                          VSA_FAST(fwd_cache),
                          VSA_FAST(cache_evict),
+                         VSA_FAST(pages_free),
+                         VSA_FAST(pages_reserve),
+                         VSA_FAST(cache_fork),
+                         VSA_FAST(cache_compact),
+                         VSA_FAST(fwd_prompt),
+                         VSA_FAST(bwd_prompt),
                          {"bind", bind, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_vsa_torch", nullptr, -1, methods,

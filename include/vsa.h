@@ -450,6 +450,66 @@ VSA_API vsa_status vsa_cache_evict(const float *weight, const int32_t *table,
                                    int32_t *n_freed, vsa_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
+ * The pages of the 8-bit cache: which are free, and who shares them.
+ *
+ * A pool's state is refs [pages] int32, the number of table entries that name a page, and
+ * free_bits [ceil(pages / 32)] uint32, bit p % 32 of word p / 32 set where refs[p] is 0 (bits
+ * past the pool are ignored).  An empty pool has refs 0 and all bits set.  Pages are taken
+ * lowest first, in the order of the entries (b, h, j) that ask for them, so every outcome is
+ * unique.  Calls on one pool must not overlap on the GPU.  A page that several sequences name
+ * is one that none of them writes: vsa_cache_fork shares full blocks only, and a write goes
+ * behind those.  B * Hkv * max_blocks (and N * Hkv * max_blocks) < 2^31.
+ * ------------------------------------------------------------------------------------- */
+
+/* Lets pages go: every entry of table [B, Hkv, max_blocks] from block ceil(lens[b] / block) on
+ * (lens NULL: every entry) becomes -1, and the page that it named loses a reference; without
+ * any left it is free.  With lens, that takes back what was mapped ahead (after rejected
+ * tokens, say, lens having been set back); without, it ends sequences, or takes what
+ * vsa_cache_evict put in `freed`.  Entries that name no page become -1; references below 0 do
+ * not arise.  One kernel. */
+VSA_API vsa_status vsa_pages_free(int32_t *table, const int32_t *lens, int B, int Hkv,
+                                  int max_blocks, int block, int pages, int32_t *refs,
+                                  uint32_t *free_bits, vsa_stream_t stream);
+
+/* Maps pages ahead of a write: blocks lens[b] / block .. ceil((lens[b] + n_new[b]) / block) - 1
+ * (n_new NULL: one token each; at most max_blocks) that have no page in the table get one.
+ *   lacking [B] output: the pages that the pool could not give sequence b, all its heads
+ *           together; their entries are -1 (a write drops those tokens).
+ * One kernel. */
+VSA_API vsa_status vsa_pages_reserve(int32_t *table, const int32_t *lens, const int32_t *n_new,
+                                     int B, int Hkv, int max_blocks, int block, int pages,
+                                     int32_t *refs, uint32_t *free_bits, int32_t *lacking,
+                                     vsa_stream_t stream);
+
+/* N children of sequences that the cache holds (samples of one prompt, beams): child i goes on
+ * from sequence parent[i] (int32 [N]; one that is not in [0, B) leaves the child empty).
+ *   table_out [N, Hkv, max_blocks]: full blocks name the parent's pages, each with a reference
+ *           more; a part-full last block gets a page of its own, with what the parent's holds
+ *           (its tokens' codes, scales and mean); -1 behind.
+ *   lens_out [N]: the parent's length.  lacking [N]: pages that the pool could not give; their
+ *           entries are -1, and such a child is to be let go or forked anew.
+ *   Outputs overlap nothing else.  The parents stay: vsa_pages_free(table) ends them.
+ * Two kernels. */
+VSA_API vsa_status vsa_cache_fork(const int32_t *table, const int32_t *lens, const int32_t *parent,
+                                  int B, int N, int Hkv, int D, int max_blocks, int block,
+                                  int pages, uint8_t *k_cache, uint8_t *v_cache, float *k_scale,
+                                  float *v_scale, vsa_bf16 *k_mean, int32_t *refs,
+                                  uint32_t *free_bits, int32_t *table_out, int32_t *lens_out,
+                                  int32_t *lacking, vsa_stream_t stream);
+
+/* Closes a pool up: with U pages in use, those from U on move to the free ones below U, in
+ * order, whole (codes, scales, mean, count), and the table's entries follow.
+ *   to     [pages] output: where each page in use is now, -1 for free ones; entries of other
+ *          tables on the pool are to be replaced by to[entry].
+ *   n_used [1] output: U.  Pages from U on are free: the pool can be cut, or saved, there.
+ * k_mean may be NULL.  Two kernels. */
+VSA_API vsa_status vsa_cache_compact(int32_t *table, int B, int Hkv, int D, int max_blocks,
+                                     int block, int pages, uint8_t *k_cache, uint8_t *v_cache,
+                                     float *k_scale, float *v_scale, vsa_bf16 *k_mean,
+                                     int32_t *refs, uint32_t *free_bits, int32_t *to,
+                                     int32_t *n_used, vsa_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
  * Attention over whole prompts: every query of a sequence against that sequence's keys, for
  * the prompt that fills a cache and for layers without a choice of blocks.
  *
