@@ -166,6 +166,14 @@ bool meets(const View& x, const void* p, long long bytes) {
 long long seq_bytes(const Shape& p, const int32_t* s) {
   return s ? ((long long)p.B + (p.packed ? 1 : 0)) * 4 : 0;
 }
+// Whether a contiguous output shares memory with the sequences' starts or lengths.
+bool meets_seq(const Shape& p, const void* x, long long bytes) {
+  auto apart = [&](const void* y, long long n) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    return !x || !y || a + (uintptr_t)bytes <= b || b + (uintptr_t)n <= a;
+  };
+  return !apart(p.q_seq, seq_bytes(p, p.q_seq)) || !apart(p.k_seq, seq_bytes(p, p.k_seq));
+}
 
 }  // namespace
 
@@ -191,7 +199,7 @@ vsa_status vsa_fwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
   for (const View* x : {&vq, &vk, &vv})
     if (views_meet(vo, *x) || meets(*x, lse, lse_bytes)) return VSA_ERR_INVALID_ARG;
   if (meets(vo, lse, lse_bytes) || meets(vo, q_seq, seq_bytes(p, q_seq)) ||
-      meets(vo, k_seq, seq_bytes(p, k_seq)))
+      meets(vo, k_seq, seq_bytes(p, k_seq)) || meets_seq(p, lse, lse_bytes))
     return VSA_ERR_INVALID_ARG;
 
   prompt::FwdArgs a{};
@@ -279,10 +287,14 @@ vsa_status vsa_bwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
   }
   for (const View* x : in)
     if (meets(*x, workspace, (long long)need)) return VSA_ERR_INVALID_ARG;
+  const uintptr_t w0 = reinterpret_cast<uintptr_t>(workspace), l0 = reinterpret_cast<uintptr_t>(lse);
+  if (Sq > 0 && ((w0 < l0 + (uintptr_t)lse_bytes && l0 < w0 + need) ||
+                 meets_seq(p, workspace, (long long)need)))
+    return VSA_ERR_INVALID_ARG;
 
   prompt::bwd::Args a{};
   a.seq = seq_args(p);
-  a.stats = static_cast<const float*>(workspace);
+  a.stats = static_cast<float*>(workspace);
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.group = Hq / Hkv;
@@ -327,6 +339,15 @@ vsa_status vsa_bwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
     pb::prompt_prep_kernel<<<(unsigned)(tslots * a.n_packs), 256, 0, s>>>(pa);
     ++launches;
   }
+  if (Sq > 0) {
+    a.d0 = dq;
+    a.d0_b = wq.sb;
+    a.d0_h = wq.sh;
+    a.d0_t = wq.st;
+    pb::dq::prompt_dq_kernel<<<(unsigned)(tslots * a.n_packs), pb::kThreads, pb::dq::kSmemBytes,
+                               s>>>(tq, tg, tk, tv, a);
+    ++launches;
+  }
   if (Sk > 0) {
     a.d0 = dk;
     a.d0_b = wk.sb;
@@ -338,16 +359,6 @@ vsa_status vsa_bwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
     a.d1_t = wv.st;
     pb::dkv::prompt_dkv_kernel<<<(unsigned)(kslots * Hkv), pb::kThreads, pb::dkv::kSmemBytes, s>>>(
         tq, tg, tk, tv, a);
-    ++launches;
-  }
-  if (Sq > 0) {
-    a.d0 = dq;
-    a.d0_b = wq.sb;
-    a.d0_h = wq.sh;
-    a.d0_t = wq.st;
-    a.d1 = nullptr;
-    pb::dq::prompt_dq_kernel<<<(unsigned)(tslots * a.n_packs), pb::kThreads, pb::dq::kSmemBytes,
-                               s>>>(tq, tg, tk, tv, a);
     ++launches;
   }
   if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;

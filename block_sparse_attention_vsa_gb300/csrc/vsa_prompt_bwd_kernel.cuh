@@ -9,14 +9,19 @@
 //   prompt_prep_kernel  per query row -lse (-infinity where a row attends nothing, or behind a
 //                       sequence's end, so that every p of the row is 0) and -D, in the order
 //                       of the query tiles.
+//   prompt_dq_kernel    a CTA per query tile: Q and dO stay, dQ adds up in TMEM while it
+//                       walks the key tiles: S = Q K^T, dP = dO V^T, dS, dQ += dS K.
+//                       out is rounded to bf16, and D with it; but a row's dS add up to 0, so
+//                       what they come to is that error: it is taken off D for the next
+//                       kernel, and here off the dS of rows of one key tile, where out is
+//                       large (elsewhere it is the mean of many v).  12 heads of up to 411
+//                       tokens: dk off by 0.0024 (relative, in norm) instead of 0.0025.
 //   prompt_dkv_kernel   a CTA per key tile of 128 keys and key/value head: K and V stay in
 //                       shared memory, dK and dV add up in TMEM while it walks the query
 //                       tiles that see the keys.  Per step, transposed (lanes = keys):
 //                         S^T = K Q^T, dP^T = V dO^T           (SS, both K-major)
 //                         P^T = 2^(c S^T - lse), dS^T = P^T (dP^T - D)  -> bf16 over S^T, dP^T
 //                         dV += P^T dO, dK += dS^T Q           (TS, A from TMEM)
-//   prompt_dq_kernel    a CTA per query tile: Q and dO stay, dQ adds up in TMEM while it
-//                       walks the key tiles: S = Q K^T, dP = dO V^T, dS, dQ += dS K.
 // That is seven products where one kernel with atomic sums of dQ takes five, but those sums
 // are 64 KB of L2 reductions a step, and their order would be anyone's.  P and dS are rounded
 // to bf16 for the products, everything else is fp32.
@@ -45,7 +50,7 @@ constexpr uint32_t kTmemCols = 512;
 
 struct Args {
   SeqArgs seq;
-  const float* stats;  // [n_packs][n_tslots][-lse | -D][128]
+  float* stats;  // [n_packs][n_tslots][-lse | -D][128]
   uint16_t *d0, *d1;   // dkv: dk, dv; dq: dq, null
   long long d0_b, d0_h, d0_t, d1_b, d1_h, d1_t;  // strides in elements
   unsigned int* status;
@@ -491,7 +496,8 @@ namespace dq {
 constexpr int kKStages = 3, kVStages = 2;
 constexpr uint32_t kOffQ = 0, kOffG = kTile, kOffK = 2 * kTile;
 constexpr uint32_t kOffV = kOffK + kKStages * kTile;
-constexpr uint32_t kOffCtl = kOffV + kVStages * kTile;
+constexpr uint32_t kOffXch = kOffV + kVStages * kTile;  // the rows' sums of dS, a warpgroup each
+constexpr uint32_t kOffCtl = kOffXch + 1024;
 constexpr uint32_t kSmemBytes = kOffCtl + 1024;  // (the base is aligned)
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 384;  // dP twice
@@ -500,7 +506,7 @@ struct Ctl {
   uint64_t q_full;
   uint64_t k_full[kKStages], k_ready[kKStages], k_empty[kKStages];
   uint64_t v_full[kVStages], v_empty[kVStages];
-  uint64_t s_full, s_empty, dp_full[2], ds_full[2], acc_full, drain, never;
+  uint64_t s_full, s_empty, dp_full[2], ds_full[2], x_full[4], acc_full, drain, never;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -553,6 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&ctl->s_full, 1);
     mbar_init(&ctl->s_empty, 8);
+    for (int i = 0; i < 4; ++i) mbar_init(&ctl->x_full[i], 2);
     mbar_init(&ctl->acc_full, 1);
     mbar_init(&ctl->drain, 1);
     mbar_init(&ctl->never, 1);
@@ -583,12 +590,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + lanes + kColS + 64 * wg, tDP = tmem + lanes + kColDP + 64 * wg;
     const int tok = tok0 + (r & (T - 1)), head = head0 + (r >> (7 - a.pack));
     float nlse = -INFINITY, nD = 0.0f;
+    float* st = a.stats + ((long long)hp * a.n_tslots + query_slot(a, b, s.q0, tile)) * 256;
     if (steps > 0) {
-      const float* st =
-          a.stats + ((long long)hp * a.n_tslots + query_slot(a, b, s.q0, tile)) * 256;
-      nlse = __ldg(st + r);
-      nD = __ldg(st + 128 + r);
+      nlse = st[r];
+      nD = st[128 + r];
     }
+    float* xch = reinterpret_cast<float*>(smem + kOffXch);  // [2][128]
+    uint64_t sum2 = f32x2(0.0f, 0.0f);                      // of the row's dS
+    // with the warp that has the rows' other columns (once)
+    auto exchange = [&](float x) {
+      xch[128 * wg + r] = x;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->x_full[warp & 3]);
+      return wait_warp(&ctl->x_full[warp & 3], 0, w, 0x50);
+    };
     int lim = s.nk;  // keys this row attends
     if (a.seq.causal) lim = clampi(tok + 1 + off, 0, s.nk);
     const uint64_t c2 = f32x2(a.scale_log2, a.scale_log2), l2 = f32x2(nlse, nlse),
@@ -626,19 +641,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld_32x32b_x32(t + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
       tmem_wait_ld();
       const int left = lim - 128 * g - 64 * wg;
-      const bool part = __any_sync(0xffffffffu, left < 64);
+      if (__any_sync(0xffffffffu, left < 64)) {
+        // a masked pair: p = 0, and dP, where v may be no number, likewise
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (c >= left) {
+            p[c] = 0.0f;
+            x[c] = 0u;
+          }
+      }
       uint32_t pk[32];
 #pragma unroll
       for (int c = 0; c < 64; c += 2) {
+        const uint64_t ds = mul_f32x2(
+            f32x2(p[c], p[c + 1]),
+            add_f32x2(f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), d2));
+        sum2 = add_f32x2(sum2, ds);
         float y0, y1;
-        split_f32x2(mul_f32x2(f32x2(p[c], p[c + 1]),
-                              add_f32x2(f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])),
-                                        d2)), y0, y1);
-        if (part) {
-          if (c >= left) y0 = 0.0f;
-          if (c + 1 >= left) y1 = 0.0f;
-        }
+        split_f32x2(ds, y0, y1);
         pk[c / 2] = pack_bf16x2(y0, y1);
+        x[c] = __float_as_uint(y0);
+        x[c + 1] = __float_as_uint(y1);
+      }
+      if (steps == 1) {
+        // the row is here as a whole: take off what its dS, which add up to 0, come to
+        float lo, hi;
+        split_f32x2(sum2, lo, hi);
+        if (!exchange(lo + hi)) {
+          ok = false;
+          break;
+        }
+        const float rest = lo + hi + xch[128 * (wg ^ 1) + r];
+#pragma unroll
+        for (int c = 0; c < 64; c += 2)
+          pk[c / 2] = pack_bf16x2(fmaf(-p[c], rest, __uint_as_float(x[c])),
+                                  fmaf(-p[c + 1], rest, __uint_as_float(x[c + 1])));
       }
       tmem_st_32x32b_x32(t, pk);
       tmem_wait_st();
@@ -646,6 +683,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->ds_full[g & 1]);
     }
+    if (steps > 1 && ok) {
+      float lo, hi;
+      split_f32x2(sum2, lo, hi);
+      ok = exchange(lo + hi);
+    }
+    // D for the dkv kernel: sum_j p_ij (dout_i . v_j), without the rounding of out
+    if (steps > 0 && ok && wg == 0 && tok < s.nq)
+      st[128 + r] = nD - (xch[r] + xch[128 + r]);
     if (steps > 0 && ok) ok = wait_warp(&ctl->acc_full, 0, w, 0x42);
     if (ok) {
       tc_fence_after();
