@@ -227,6 +227,49 @@ __device__ __forceinline__ void warp_mma_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// Eight of them along K = 128, elected once: A and B of K-major tiles of two 64-column halves
+// `half` bytes apart (32 bytes a step inside a half).
+__device__ __forceinline__ void warp_mma8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t half) {
+  const uint64_t h = half >> 4;
+  asm volatile(
+      "{\n .reg .pred p, t, f;\n .reg .b64 a, b, c, d;\n elect.sync _|p, 0xffffffff;\n"
+      " setp.eq.u32 t, 0, 0;\n setp.ne.u32 f, 0, 0;\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n"
+      " add.u64 a, %1, 2;\n add.u64 b, %2, 2;\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u64 a, %1, 4;\n add.u64 b, %2, 4;\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u64 a, %1, 6;\n add.u64 b, %2, 6;\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u64 c, %1, %4;\n add.u64 d, %2, %4;\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], c, d, %3, t;\n"
+      " add.u64 a, c, 2;\n add.u64 b, d, 2;\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u64 a, c, 4;\n add.u64 b, d, 4;\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u64 a, c, 6;\n add.u64 b, d, 6;\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "l"(h)
+      : "memory");
+}
+// Four along K = 64 with A in TMEM (8 columns a step) and B MN-major (16 rows of 128 bytes, 2 KB,
+// a step); the first adds to what D holds only if `accumulate`.
+__device__ __forceinline__ void warp_mma4_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q, t;\n .reg .b64 b;\n .reg .b32 a;\n elect.sync _|p, 0xffffffff;\n"
+      " setp.ne.b32 q, %4, 0;\n setp.eq.u32 t, 0, 0;\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n"
+      " add.u32 a, %1, 8;\n add.u64 b, %2, 128;\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.u32 a, %1, 16;\n add.u64 b, %2, 256;\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
+      " add.u32 a, %1, 24;\n add.u64 b, %2, 384;\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 __device__ __forceinline__ void warp_mma_commit(uint64_t* bar) {
   asm volatile(
       "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n"

@@ -18,14 +18,16 @@
 //
 // One persistent CTA per SM, 12 warps:
 //   warps 0-3, 4-7  softmax warpgroups of query tile 0 and 1 (thread = query row)
-//   warp 8          TMA: Q tiles, and K, V alternating through a ring of 5 stages
-//   warp 9          MMA issuer (one lane): QK_0(0), QK_1(0), then per key tile j and query
-//                   tile t: PV_t(j), QK_t(j + 1).  MMAs of one thread run in order, so
-//                   QK_t(j + 1) may overwrite P_t(j), and S_t(j + 1) complete says that
-//                   O_t holds tile j.
-//   warp 10         decodes items, one ahead
-//   warp 11         zeroes the rows of a V tile behind the sequence's last key: their weight
-//                   is 0, but 0 times what lies there (another sequence, padding) may be NaN
+//   warp 8          decodes items and copies: Q tiles, and K, V alternating through a ring
+//   warp 9          MMA issuer: S_0(0), S_1(0), then per key tile j and query tile t: O_t +=
+//                   P_t(j) V_j, S_t(j + 1).  MMAs of one thread run in order, so S_t(j + 1)
+//                   may overwrite P_t(j), and S_t(j + 1) complete says that O_t holds tile j.
+//                   The order keeps the two softmax warpgroups half a period apart (with an
+//                   issuer each they fell into step, and the tensor core idled meanwhile).
+//                   The warp runs converged and elect.sync picks the lane that issues.
+//   warp 11         hands landed tiles on to the MMA warps, and zeroes the rows of a V tile
+//                   behind the sequence's last key: their weight is 0, but 0 times what lies
+//                   there (another sequence, padding) may be NaN
 // TMEM (512 columns): S_0, S_1 (P over the first 64 columns of S), O_0, O_1.
 #pragma once
 
@@ -66,21 +68,19 @@ struct Item {
   int head0, kv_head, z;  // first query head of the pack, key/value head, batch coordinate
   int tok, q0, nq;        // first token, first row and number of queries of the sequence
   int k0, nk;
-  int n[2];               // key tiles of the two query tiles
+  int n0, n1;             // key tiles of the two query tiles
   int go;
 };
 
 struct Ctl {
   uint64_t item_full[2], item_empty[2];
   uint64_t q_full[2], q_empty[2];  // per query tile
-  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t kv_full[kStages], ready[kStages], kv_empty[kStages];
   uint64_t s_full[2];      // S_t is in TMEM (and O_t holds the tile before)
   uint64_t p_full[4];      // [2 t + h]: half h of P_t is in TMEM
   uint64_t o_full[2], o_empty[2];
-  uint64_t v_dirty, v_clean;  // the mailbox of warp 11
   uint64_t drain, never;
   Item item[2];
-  int dirty_stage;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -110,217 +110,217 @@ __device__ __forceinline__ bool decode(const FwdArgs& a, int id, Item& it) {
   it.head0 = hp << a.pack;
   it.kv_head = it.head0 / a.group;
   it.go = 1;
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int t0 = it.tok + t * half;
+  auto key_tiles = [&](int t0) {
     const int last = (t0 + half < s.nq ? t0 + half : s.nq) - 1;  // its last query
     int keys = s.nk;
     if (a.seq.causal) keys = clampi(last + 1 + s.nk - s.nq, 0, s.nk);
-    it.n[t] = t0 < s.nq ? (keys + 127) / 128 : 0;
-  }
+    return t0 < s.nq ? (keys + 127) / 128 : 0;
+  };
+  it.n0 = key_tiles(it.tok);
+  it.n1 = key_tiles(it.tok + half);
   return a.seq.packed ? tile >= 0 && it.tok < s.nq : true;
 }
 
-__device__ __forceinline__ void sched_role(const FwdArgs& a, Ctl* ctl, const WaitCtx& w) {
-  uint32_t n = 0;
-  for (int id = (int)blockIdx.x;; id += (int)gridDim.x) {
-    Item it;
-    it.go = 0;
-    if (id < a.n_items && !decode(a, id, it)) continue;
-    const uint32_t buf = n & 1;
-    if (n >= 2 && !wait_warp(&ctl->item_empty[buf], ((n >> 1) + 1) & 1, w, 0x01)) return;
-    if (lane_id() == 0) {
+// The CTA's n-th item that holds something, from slot `id` on (by a whole warp).
+__device__ __forceinline__ Item next_item(const FwdArgs& a, int& id) {
+  Item it;
+  for (; id < a.n_items; id += (int)gridDim.x)
+    if (decode(a, id, it)) {
+      id += (int)gridDim.x;
+      return it;
+    }
+  it.go = 0;
+  return it;
+}
+
+__device__ __forceinline__ void load_role(const FwdArgs& a, uint8_t* smem, Ctl* ctl,
+                                          const WaitCtx& w, const CUtensorMap* tq,
+                                          const CUtensorMap* tk, const CUtensorMap* tv) {
+  const bool leader = lane_id() == 0;
+  uint32_t st = 0, ph = 0, fills = 0, nq0 = 0, nq1 = 0;  // ring position; loads of Q tiles
+  int id = (int)blockIdx.x;
+  const int half = 128 >> a.pack;
+  bool ok = true;
+  Item it = next_item(a, id);
+  for (uint32_t i = 0;; ++i) {
+    const uint32_t buf = i & 1;
+    if (i >= 2 && !wait_warp(&ctl->item_empty[buf], ((i >> 1) + 1) & 1, w, 0x01)) break;
+    if (leader) {
       ctl->item[buf] = it;
       mbar_arrive(&ctl->item_full[buf]);
     }
-    __syncwarp();
-    ++n;
-    if (!it.go) return;
-  }
-}
-
-__device__ __forceinline__ void tma_role(const FwdArgs& a, uint8_t* smem, Ctl* ctl,
-                                         const WaitCtx& w, const CUtensorMap* tq,
-                                         const CUtensorMap* tk, const CUtensorMap* tv) {
-  uint32_t L = 0, nq[2] = {0, 0};
-  bool ok = true;
-  for (uint32_t i = 0; ok; ++i) {
-    const uint32_t buf = i & 1;
-    if (!wait(&ctl->item_full[buf], (i >> 1) & 1, w, 0x02)) break;
-    const Item it = ctl->item[buf];
-    mbar_arrive(&ctl->item_empty[buf]);
     if (!it.go) break;
-    const int n = it.n[0] > it.n[1] ? it.n[0] : it.n[1];
-    const int half = 128 >> a.pack;
+    const Item cur = it;
+    const int n = cur.n0 > cur.n1 ? cur.n0 : cur.n1;
     auto put = [&](const CUtensorMap* map, int j) {
-      const uint32_t st = L % kStages;
-      if (L >= (uint32_t)kStages && !wait(&ctl->kv_empty[st], ((L / kStages) + 1) & 1, w, 0x03))
-        return false;
-      mbar_arrive_expect_tx(&ctl->kv_full[st], kTile);
-      load_tile(smem + kOffKV + st * kTile, map, &ctl->kv_full[st], it.k0 + 128 * j, it.kv_head,
-                it.z);
-      ++L;
+      if (fills >= (uint32_t)kStages && !wait_warp(&ctl->kv_empty[st], ph ^ 1, w, 0x03)) return false;
+      if (leader) {
+        mbar_arrive_expect_tx(&ctl->kv_full[st], kTile);
+        load_tile(smem + kOffKV + st * kTile, map, &ctl->kv_full[st], cur.k0 + 128 * j,
+                  cur.kv_head, cur.z);
+      }
+      ++fills;
+      if (++st == kStages) st = 0, ph ^= 1;
       return true;
     };
-    auto put_q = [&](int t) {
-      if (it.n[t] == 0) return true;
-      uint32_t& c = t ? nq[1] : nq[0];
-      if (c > 0 && !wait(&ctl->q_empty[t], (c - 1) & 1, w, 0x04)) return false;
-      mbar_arrive_expect_tx(&ctl->q_full[t], kTile);
-      load_tile(smem + kOffQ + t * kTile, tq, &ctl->q_full[t], it.q0 + it.tok + t * half,
-                it.head0, it.z);
-      ++c;
+    auto put_q = [&](int t, uint32_t& count) {
+      if (count > 0 && !wait_warp(&ctl->q_empty[t], (count - 1) & 1, w, 0x04)) return false;
+      if (leader) {
+        mbar_arrive_expect_tx(&ctl->q_full[t], kTile);
+        load_tile(smem + kOffQ + t * kTile, tq, &ctl->q_full[t], cur.q0 + cur.tok + t * half,
+                  cur.head0, cur.z);
+      }
+      ++count;
       return true;
     };
     // K of the first tile ahead of Q: its stage is free long before the Q buffers are
-    for (int j = 0; j < n && ok; ++j) {
-      ok = put(tk, j);
-      if (ok && j == 0) ok = put_q(0) && put_q(1);
-      if (ok) ok = put(tv, j);
+    if (n > 0) {
+      ok = put(tk, 0);
+      if (ok && cur.n0 > 0) ok = put_q(0, nq0);
+      if (ok && cur.n1 > 0) ok = put_q(1, nq1);
+      if (ok) ok = put(tv, 0);
     }
+    it = next_item(a, id);
+    for (int j = 1; j < n && ok; ++j) ok = put(tk, j) && put(tv, j);
+    if (!ok) break;
   }
   // every copy issued has landed before the CTA exits
   for (uint32_t s = 0; s < (uint32_t)kStages; ++s) {
-    const uint32_t fills = L > s ? (L - s + kStages - 1) / kStages : 0;
-    if (fills) wait(&ctl->kv_full[s], (fills - 1) & 1, w, 0x05, true);
+    const uint32_t f = fills > s ? (fills - s + kStages - 1) / kStages : 0;
+    if (f) wait(&ctl->kv_full[s], (f - 1) & 1, w, 0x05, true);
   }
-  if (nq[0]) wait(&ctl->q_full[0], (nq[0] - 1) & 1, w, 0x06, true);
-  if (nq[1]) wait(&ctl->q_full[1], (nq[1] - 1) & 1, w, 0x06, true);
+  if (nq0) wait(&ctl->q_full[0], (nq0 - 1) & 1, w, 0x06, true);
+  if (nq1) wait(&ctl->q_full[1], (nq1 - 1) & 1, w, 0x06, true);
 }
 
 __device__ __forceinline__ void mma_role(const FwdArgs& a, uint8_t* smem, Ctl* ctl,
                                          const WaitCtx& w, uint32_t tmem) {
   constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
   constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, false, true);
-  uint32_t L = 0;          // ring position of the item's K tile 0
+  const uint64_t qd = smem_desc_sw128(smem_addr(smem + kOffQ), 16, 1024);
+  const uint64_t kd = smem_desc_sw128(smem_addr(smem + kOffKV), 16, 1024);
+  const uint64_t vd = smem_desc_sw128(smem_addr(smem + kOffKV), kTile / 2, 1024);
+  uint32_t st = 0, ph = 0;                          // ring position
   uint32_t items0 = 0, items1 = 0, p0 = 0, p1 = 0;  // per query tile: items, key tiles so far
-  uint32_t cleaned = 0;
   if (a.stall) {  // test hook: a barrier that nothing completes
-    wait(&ctl->never, 0, w, 0x1f);
+    wait_warp(&ctl->never, 0, w, 0x1f);
   } else {
     for (uint32_t i = 0;; ++i) {
       const uint32_t buf = i & 1;
-      if (!wait(&ctl->item_full[buf], (i >> 1) & 1, w, 0x07)) break;
-      const int n0 = ctl->item[buf].n[0], n1 = ctl->item[buf].n[1];
-      const int nk = ctl->item[buf].nk;
-      const int go = ctl->item[buf].go;
-      mbar_arrive(&ctl->item_empty[buf]);
+      if (!wait_warp(&ctl->item_full[buf], (i >> 1) & 1, w, 0x07)) break;
+      const int n0 = ctl->item[buf].n0, n1 = ctl->item[buf].n1, go = ctl->item[buf].go;
+      __syncwarp();
+      if (lane_id() == 0) mbar_arrive(&ctl->item_empty[buf]);
       if (!go) break;
       const int n = n0 > n1 ? n0 : n1;
       if (n == 0) continue;
-      bool ok = true;
-      auto landed = [&](uint32_t pos) {
-        return wait(&ctl->kv_full[pos % kStages], (pos / kStages) & 1, w, 0x08);
+      auto next = [&] {
+        if (++st == kStages) st = 0, ph ^= 1;
       };
-      // S_t = Q_t K_j^T
-      auto qk = [&](int t, int j) {
-        const uint32_t st = (L + 2 * j) % kStages;
-        const uint64_t qd = smem_desc_sw128(smem_addr(smem + kOffQ + t * kTile), 16, 1024);
-        const uint64_t kd = smem_desc_sw128(smem_addr(smem + kOffKV + st * kTile), 16, 1024);
+      auto qk = [&](int t, uint32_t stage, bool last) {
+        warp_mma8_ss(tmem + kColS + 128 * t, qd + t * (kTile >> 4), kd + stage * (kTile >> 4),
+                     kIdescS, kTile / 2);
+        warp_mma_commit(&ctl->s_full[t]);
+        if (last) warp_mma_commit(&ctl->q_empty[t]);
+      };
+      // O_t += P_t V_j, a half of the keys at a time
+      auto pv = [&](int t, uint32_t stage, uint32_t phase, int j) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint64_t off = ((k >> 2) * (kTile / 2) + (k & 3) * 32) >> 4;
-          mma_ss(tmem + kColS + 128 * t, qd + off, kd + off, kIdescS, k > 0);
+        for (int h = 0; h < 2; ++h) {
+          if (!wait_warp(&ctl->p_full[2 * t + h], phase, w, 0x0b)) return false;
+          tc_fence_after();
+          warp_mma4_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 32 * h,
+                       vd + stage * (kTile >> 4) + 512 * h, kIdescPV, (j > 0 || h > 0) ? 1u : 0u);
         }
-        mma_commit(&ctl->s_full[t]);
+        return true;
       };
-      for (int t = 0; t < 2 && ok; ++t) {
-        if ((t ? n1 : n0) == 0) continue;
-        ok = wait(&ctl->q_full[t], (t ? items1 : items0) & 1, w, 0x09) && landed(L);
-        if (!ok) break;
-        tc_fence_after();
-        qk(t, 0);
-        if ((t ? n1 : n0) == 1) mma_commit(&ctl->q_empty[t]);
+      // S(0) of both
+      bool ok = wait_warp(&ctl->ready[st], ph, w, 0x08);
+      if (ok && n0 > 0) {
+        ok = wait_warp(&ctl->q_full[0], items0 & 1, w, 0x09);
+        if (ok) {
+          tc_fence_after();
+          qk(0, st, n0 == 1);
+        }
       }
-      if (ok) mma_commit(&ctl->kv_empty[L % kStages]);
-      for (int j = 0; j < n && ok; ++j) {
-        const uint32_t vpos = L + 2 * j + 1, vst = vpos % kStages;
-        if (!landed(vpos)) {
+      if (ok && n1 > 0) {
+        ok = wait_warp(&ctl->q_full[1], items1 & 1, w, 0x09);
+        if (ok) {
+          tc_fence_after();
+          qk(1, st, n1 == 1);
+        }
+      }
+      if (!ok) break;
+      warp_mma_commit(&ctl->kv_empty[st]);
+      next();
+      for (int j = 0; j < n; ++j) {
+        const uint32_t vst = st;
+        if (!wait_warp(&ctl->ready[vst], ph, w, 0x0e)) {
           ok = false;
           break;
         }
-        const bool part = nk - 128 * j < 128;  // keys behind the last: their V rows to zero
-        if (part) {
-          ctl->dirty_stage = (int)vst;
-          mbar_arrive(&ctl->v_dirty);
+        next();
+        const uint32_t kst = st, kph = ph;
+        const bool more = j + 1 < n;
+        if (more) next();
+        // an item's first product overwrites O: the one before has been read
+        if (j < n0) {
+          ok = (j > 0 || items0 == 0 || wait_warp(&ctl->o_empty[0], (items0 - 1) & 1, w, 0x0a)) &&
+               pv(0, vst, p0 & 1, j);
+          if (!ok) break;
+          ++p0;
+          if (j + 1 == n0) warp_mma_commit(&ctl->o_full[0]);
         }
-        const bool more_k = j + 1 < n;
-#pragma unroll 1
-        for (int t = 0; t < 2 && ok; ++t) {
-          const int nt = t ? n1 : n0;
-          if (j < nt) {
-            const uint32_t pc = t ? p1 : p0;
-            if (j == 0 && (t ? items1 : items0) > 0 &&
-                !wait(&ctl->o_empty[t], ((t ? items1 : items0) - 1) & 1, w, 0x0a)) {
-              ok = false;
-              break;
-            }
-            const uint64_t vd =
-                smem_desc_sw128(smem_addr(smem + kOffKV + vst * kTile), kTile / 2, 1024);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (!wait(&ctl->p_full[2 * t + h], pc & 1, w, 0x0b)) {
-                ok = false;
-                break;
-              }
-              if (h == 0 && part && t == (n0 > j ? 0 : 1)) {
-                if (!wait(&ctl->v_clean, cleaned & 1, w, 0x0c)) {
-                  ok = false;
-                  break;
-                }
-                ++cleaned;
-              }
-              tc_fence_after();
-#pragma unroll
-              for (int k = 4 * h; k < 4 * h + 4; ++k)
-                mma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * k,
-                       vd + ((k * 2048) >> 4), kIdescPV, (j > 0 || k > 0) ? 1u : 0u);
-            }
-            if (!ok) break;
-            if (t) ++p1; else ++p0;
-            if (j + 1 == nt) mma_commit(&ctl->o_full[t]);
-          }
-          // V_j is free behind the last tile's product
-          if (t == (n1 > j ? 1 : 0)) mma_commit(&ctl->kv_empty[vst]);
-          if (j + 1 < nt) {
-            if (!landed(L + 2 * j + 2)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            qk(t, j + 1);
-            if (j + 2 == nt) mma_commit(&ctl->q_empty[t]);
-          }
-          if (more_k && t == (n1 > j + 1 ? 1 : 0)) mma_commit(&ctl->kv_empty[(L + 2 * j + 2) % kStages]);
+        if (j >= n1) warp_mma_commit(&ctl->kv_empty[vst]);
+        if (more && !wait_warp(&ctl->ready[kst], kph, w, 0x08)) {
+          ok = false;
+          break;
         }
+        if (j + 1 < n0) {
+          tc_fence_after();
+          qk(0, kst, j + 2 == n0);
+        }
+        if (j < n1) {
+          ok = (j > 0 || items1 == 0 || wait_warp(&ctl->o_empty[1], (items1 - 1) & 1, w, 0x0a)) &&
+               pv(1, vst, p1 & 1, j);
+          if (!ok) break;
+          ++p1;
+          warp_mma_commit(&ctl->kv_empty[vst]);
+          if (j + 1 == n1) warp_mma_commit(&ctl->o_full[1]);
+        }
+        if (j + 1 < n1) qk(1, kst, j + 2 == n1);
+        if (more) warp_mma_commit(&ctl->kv_empty[kst]);
       }
       if (!ok) break;
       if (n0 > 0) ++items0;
       if (n1 > 0) ++items1;
-      L += 2 * n;
     }
   }
   // every MMA issued has completed before TMEM can be released
-  mma_commit(&ctl->drain);
+  warp_mma_commit(&ctl->drain);
   wait(&ctl->drain, 0, w, 0x0d, true);
+  __syncwarp();
 }
 
+// Hands landed tiles on to the MMA warps.
 __device__ __forceinline__ void clean_role(uint8_t* smem, Ctl* ctl, const WaitCtx& w) {
-  uint32_t n_dirty = 0;
+  uint32_t st = 0, ph = 0;
   for (uint32_t i = 0;; ++i) {
     const uint32_t buf = i & 1;
     if (!wait_warp(&ctl->item_full[buf], (i >> 1) & 1, w, 0x13)) return;
-    const int n0 = ctl->item[buf].n[0], n1 = ctl->item[buf].n[1];
+    const int n0 = ctl->item[buf].n0, n1 = ctl->item[buf].n1;
     const int nk = ctl->item[buf].nk, go = ctl->item[buf].go;
     __syncwarp();
     if (lane_id() == 0) mbar_arrive(&ctl->item_empty[buf]);
     if (!go) return;
-    if (128 * (n0 > n1 ? n0 : n1) <= nk) continue;  // every tile of the item is full
-    if (!wait_warp(&ctl->v_dirty, n_dirty & 1, w, 0x14)) return;
-    ++n_dirty;
-    zero_rows(smem + kOffKV + ctl->dirty_stage * kTile, nk & 127);
-    if (lane_id() == 0) mbar_arrive(&ctl->v_clean);
-    __syncwarp();
+    const int n = n0 > n1 ? n0 : n1;
+    for (int x = 0; x < 2 * n; ++x) {
+      if (!wait_warp(&ctl->kv_full[st], ph, w, 0x14)) return;
+      const int rows = nk - 128 * (x >> 1);
+      if ((x & 1) && rows < 128) zero_rows(smem + kOffKV + st * kTile, rows);
+      if (lane_id() == 0) mbar_arrive(&ctl->ready[st]);
+      if (++st == kStages) st = 0, ph ^= 1;
+    }
   }
 }
 
@@ -339,7 +339,7 @@ __device__ __forceinline__ void softmax_role(const FwdArgs& a, Ctl* ctl, const W
     __syncwarp();
     if (lane_id() == 0) mbar_arrive(&ctl->item_empty[buf]);
     if (!it.go) break;
-    const int n = it.n[t];
+    const int n = t ? it.n1 : it.n0;
     const int tok = it.tok + t * half + (row & (half - 1));
     const int head = it.head0 + (row >> (7 - a.pack));
     // keys this row attends
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->item_full[i], 1);
-      mbar_init(&ctl->item_empty[i], 11);  // TMA, MMA, 8 softmax warps, warp 11
+      mbar_init(&ctl->item_empty[i], 10);  // the MMA warp, 8 softmax warps, warp 11
       mbar_init(&ctl->q_full[i], 1);
       mbar_init(&ctl->q_empty[i], 1);
       mbar_init(&ctl->s_full[i], 1);
@@ -489,10 +489,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&ctl->kv_full[i], 1);
+      mbar_init(&ctl->ready[i], 1);
       mbar_init(&ctl->kv_empty[i], 1);
     }
-    mbar_init(&ctl->v_dirty, 1);
-    mbar_init(&ctl->v_clean, 1);
     mbar_init(&ctl->drain, 1);
     mbar_init(&ctl->never, 1);
     ctl->abort_flag = 0;
@@ -518,17 +517,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     softmax_role(a, ctl, w, tmem, (int)(warp >> 2));
   } else {
     regs_decrease<kOtherRegs>();
-    if (warp == 8) {
-      if (lane_id() == 0) tma_role(a, smem, ctl, w, &tq, &tk, &tv);
-      __syncwarp();
-    } else if (warp == 9) {
-      if (lane_id() == 0) mma_role(a, smem, ctl, w, tmem);
-      __syncwarp();
-    } else if (warp == 10) {
-      sched_role(a, ctl, w);
-    } else {
+    if (warp == 8)
+      load_role(a, smem, ctl, w, &tq, &tk, &tv);
+    else if (warp == 9)
+      mma_role(a, smem, ctl, w, tmem);
+    else if (warp == 11)
       clean_role(smem, ctl, w);
-    }
   }
   tc_fence_before();
   __syncthreads();
