@@ -79,7 +79,8 @@ struct Ctl {
   uint64_t s_full[2];      // S_t is in TMEM (and O_t holds the tile before)
   uint64_t p_full[4];      // [2 t + h]: half h of P_t is in TMEM
   uint64_t o_full[2], o_empty[2];
-  uint64_t drain, never;
+  uint64_t turn[2];        // of the MMA warps
+  uint64_t drain[2], never;
   Item item[2];
   uint32_t tmem_base;
   int abort_flag;
@@ -193,15 +194,34 @@ __device__ __forceinline__ void load_role(const FwdArgs& a, uint8_t* smem, Ctl* 
   if (nq1) wait(&ctl->q_full[1], (nq1 - 1) & 1, w, 0x06, true);
 }
 
+// Query tile t's products.  A unit is O += P(j) V_j and S(j + 1); units of the two tiles
+// alternate, a warp passing the turn on when it has issued one.
 __device__ __forceinline__ void mma_role(const FwdArgs& a, uint8_t* smem, Ctl* ctl,
-                                         const WaitCtx& w, uint32_t tmem) {
+                                         const WaitCtx& w, uint32_t tmem, int t) {
   constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
   constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, false, true);
-  const uint64_t qd = smem_desc_sw128(smem_addr(smem + kOffQ), 16, 1024);
+  const uint64_t qd = smem_desc_sw128(smem_addr(smem + kOffQ + t * kTile), 16, 1024);
   const uint64_t kd = smem_desc_sw128(smem_addr(smem + kOffKV), 16, 1024);
   const uint64_t vd = smem_desc_sw128(smem_addr(smem + kOffKV), kTile / 2, 1024);
-  uint32_t st = 0, ph = 0;                          // ring position
-  uint32_t items0 = 0, items1 = 0, p0 = 0, p1 = 0;  // per query tile: items, key tiles so far
+  const uint32_t tS = tmem + kColS + 128 * t, tO = tmem + kColO + 128 * t;
+  const bool leader = lane_id() == 0;
+  uint32_t st = 0, ph = 0;        // ring position
+  uint32_t items = 0, tiles = 0;  // with keys for this query tile; its key tiles so far
+  uint32_t turns = 0;
+  auto take = [&] {
+    // tile 0 has the first turn
+    const bool mine = (t == 0 && turns == 0) ||
+                      wait_warp(&ctl->turn[t], (t == 0 ? turns - 1 : turns) & 1, w, 0x0c);
+    ++turns;
+    return mine;
+  };
+  auto pass = [&] {
+    if (leader) mbar_arrive(&ctl->turn[t ^ 1]);
+  };
+  auto qk = [&] {
+    warp_mma8_ss(tS, qd, kd + st * (kTile >> 4), kIdescS, kTile / 2);
+    warp_mma_commit(&ctl->s_full[t]);
+  };
   if (a.stall) {  // test hook: a barrier that nothing completes
     wait_warp(&ctl->never, 0, w, 0x1f);
   } else {
@@ -210,95 +230,78 @@ __device__ __forceinline__ void mma_role(const FwdArgs& a, uint8_t* smem, Ctl* c
       if (!wait_warp(&ctl->item_full[buf], (i >> 1) & 1, w, 0x07)) break;
       const int n0 = ctl->item[buf].n0, n1 = ctl->item[buf].n1, go = ctl->item[buf].go;
       __syncwarp();
-      if (lane_id() == 0) mbar_arrive(&ctl->item_empty[buf]);
+      if (leader) mbar_arrive(&ctl->item_empty[buf]);
       if (!go) break;
-      const int n = n0 > n1 ? n0 : n1;
+      const int n = n0 > n1 ? n0 : n1, nt = t ? n1 : n0;
       if (n == 0) continue;
-      auto next = [&] {
-        if (++st == kStages) st = 0, ph ^= 1;
-      };
-      auto qk = [&](int t, uint32_t stage, bool last) {
-        warp_mma8_ss(tmem + kColS + 128 * t, qd + t * (kTile >> 4), kd + stage * (kTile >> 4),
-                     kIdescS, kTile / 2);
-        warp_mma_commit(&ctl->s_full[t]);
-        if (last) warp_mma_commit(&ctl->q_empty[t]);
-      };
-      // O_t += P_t V_j, a half of the keys at a time
-      auto pv = [&](int t, uint32_t stage, uint32_t phase, int j) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!wait_warp(&ctl->p_full[2 * t + h], phase, w, 0x0b)) return false;
-          tc_fence_after();
-          warp_mma4_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 32 * h,
-                       vd + stage * (kTile >> 4) + 512 * h, kIdescPV, (j > 0 || h > 0) ? 1u : 0u);
-        }
-        return true;
-      };
-      // S(0) of both
-      bool ok = wait_warp(&ctl->ready[st], ph, w, 0x08);
-      if (ok && n0 > 0) {
-        ok = wait_warp(&ctl->q_full[0], items0 & 1, w, 0x09);
-        if (ok) {
-          tc_fence_after();
-          qk(0, st, n0 == 1);
-        }
-      }
-      if (ok && n1 > 0) {
-        ok = wait_warp(&ctl->q_full[1], items1 & 1, w, 0x09);
-        if (ok) {
-          tc_fence_after();
-          qk(1, st, n1 == 1);
-        }
-      }
+      bool ok = wait_warp(&ctl->ready[st], ph, w, 0x08) &&
+                (nt == 0 || wait_warp(&ctl->q_full[t], items & 1, w, 0x09)) && take();
       if (!ok) break;
-      warp_mma_commit(&ctl->kv_empty[st]);
-      next();
+      if (nt > 0) {
+        tc_fence_after();
+        qk();
+      }
+      pass();
+      if (nt > 0) {
+        warp_mma_commit(&ctl->kv_empty[st]);
+        if (nt == 1) warp_mma_commit(&ctl->q_empty[t]);
+      } else if (leader) {
+        mbar_arrive(&ctl->kv_empty[st]);
+      }
+      if (++st == kStages) st = 0, ph ^= 1;
       for (int j = 0; j < n; ++j) {
+        // V_j has landed, the first half of P(j) is there, and (an item's first product
+        // overwrites O) what O held has been read
+        ok = wait_warp(&ctl->ready[st], ph, w, 0x0e) &&
+             (j >= nt || wait_warp(&ctl->p_full[2 * t], tiles & 1, w, 0x0b)) &&
+             (j > 0 || nt == 0 || items == 0 ||
+              wait_warp(&ctl->o_empty[t], (items - 1) & 1, w, 0x0a)) &&
+             take();
+        if (!ok) break;
         const uint32_t vst = st;
-        if (!wait_warp(&ctl->ready[vst], ph, w, 0x0e)) {
-          ok = false;
-          break;
-        }
-        next();
-        const uint32_t kst = st, kph = ph;
-        const bool more = j + 1 < n;
-        if (more) next();
-        // an item's first product overwrites O: the one before has been read
-        if (j < n0) {
-          ok = (j > 0 || items0 == 0 || wait_warp(&ctl->o_empty[0], (items0 - 1) & 1, w, 0x0a)) &&
-               pv(0, vst, p0 & 1, j);
-          if (!ok) break;
-          ++p0;
-          if (j + 1 == n0) warp_mma_commit(&ctl->o_full[0]);
-        }
-        if (j >= n1) warp_mma_commit(&ctl->kv_empty[vst]);
-        if (more && !wait_warp(&ctl->ready[kst], kph, w, 0x08)) {
-          ok = false;
-          break;
-        }
-        if (j + 1 < n0) {
+        if (j < nt) {
           tc_fence_after();
-          qk(0, kst, j + 2 == n0);
-        }
-        if (j < n1) {
-          ok = (j > 0 || items1 == 0 || wait_warp(&ctl->o_empty[1], (items1 - 1) & 1, w, 0x0a)) &&
-               pv(1, vst, p1 & 1, j);
+          warp_mma4_ts(tO, tS, vd + st * (kTile >> 4), kIdescPV, j > 0 ? 1u : 0u);
+          ok = wait_warp(&ctl->p_full[2 * t + 1], tiles & 1, w, 0x0b);
           if (!ok) break;
-          ++p1;
-          warp_mma_commit(&ctl->kv_empty[vst]);
-          if (j + 1 == n1) warp_mma_commit(&ctl->o_full[1]);
+          tc_fence_after();
+          warp_mma4_ts(tO, tS + 32, vd + st * (kTile >> 4) + 512, kIdescPV, 1u);
+          ++tiles;
         }
-        if (j + 1 < n1) qk(1, kst, j + 2 == n1);
-        if (more) warp_mma_commit(&ctl->kv_empty[kst]);
+        if (++st == kStages) st = 0, ph ^= 1;
+        if (j + 1 < n) {
+          ok = wait_warp(&ctl->ready[st], ph, w, 0x08);
+          if (!ok) break;
+          if (j + 1 < nt) {
+            tc_fence_after();
+            qk();
+          }
+        }
+        pass();
+        // (the commits also cover the other product of the unit, issued since)
+        if (j < nt) {
+          warp_mma_commit(&ctl->kv_empty[vst]);
+          if (j + 1 == nt) warp_mma_commit(&ctl->o_full[t]);
+        } else if (leader) {
+          mbar_arrive(&ctl->kv_empty[vst]);
+        }
+        if (j + 1 < n) {
+          if (j + 1 < nt) {
+            warp_mma_commit(&ctl->kv_empty[st]);
+            if (j + 2 == nt) warp_mma_commit(&ctl->q_empty[t]);
+          } else if (leader) {
+            mbar_arrive(&ctl->kv_empty[st]);
+          }
+          if (++st == kStages) st = 0, ph ^= 1;
+        }
       }
       if (!ok) break;
-      if (n0 > 0) ++items0;
-      if (n1 > 0) ++items1;
+      if (nt > 0) ++items;
     }
   }
   // every MMA issued has completed before TMEM can be released
-  warp_mma_commit(&ctl->drain);
-  wait(&ctl->drain, 0, w, 0x0d, true);
+  warp_mma_commit(&ctl->drain[t]);
+  wait(&ctl->drain[t], 0, w, 0x0d, true);
   __syncwarp();
 }
 
@@ -478,7 +481,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->item_full[i], 1);
-      mbar_init(&ctl->item_empty[i], 10);  // the MMA warp, 8 softmax warps, warp 11
+      mbar_init(&ctl->item_empty[i], 11);  // 2 MMA and 8 softmax warps, warp 11
+      mbar_init(&ctl->turn[i], 1);
+      mbar_init(&ctl->drain[i], 1);
       mbar_init(&ctl->q_full[i], 1);
       mbar_init(&ctl->q_empty[i], 1);
       mbar_init(&ctl->s_full[i], 1);
@@ -490,9 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&ctl->kv_full[i], 1);
       mbar_init(&ctl->ready[i], 1);
-      mbar_init(&ctl->kv_empty[i], 1);
+      mbar_init(&ctl->kv_empty[i], 2);  // both MMA warps
     }
-    mbar_init(&ctl->drain, 1);
     mbar_init(&ctl->never, 1);
     ctl->abort_flag = 0;
     fence_mbar_init();
@@ -519,9 +523,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_decrease<kOtherRegs>();
     if (warp == 8)
       load_role(a, smem, ctl, w, &tq, &tk, &tv);
-    else if (warp == 9)
-      mma_role(a, smem, ctl, w, tmem);
-    else if (warp == 11)
+    else if (warp < 11)
+      mma_role(a, smem, ctl, w, tmem, (int)warp - 9);
+    else
       clean_role(smem, ctl, w);
   }
   tc_fence_before();
