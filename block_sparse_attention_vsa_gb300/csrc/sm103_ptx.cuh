@@ -63,6 +63,18 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same, suspended for up to about `ns` nanoseconds while the phase is not complete.
+__device__ __forceinline__ bool mbar_sleep_wait(uint64_t* bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
+
 // Non-blocking probe of a phase (try_wait may suspend the thread for a while).
 __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -185,6 +197,13 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// The words of the shared-memory matrix descriptor of smem_desc_sw128 (below) for 8-row groups
+// 1 KB apart: the high one is a constant.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+
 // D[tmem] (+)= A[smem desc] * B[smem desc]; kind::f16 (bf16 inputs, fp32 accumulate).
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                        uint32_t idesc, uint32_t accumulate) {
@@ -228,46 +247,51 @@ __device__ __forceinline__ void warp_mma_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 // Eight of them along K = 128, elected once: A and B of K-major tiles of two 64-column halves
-// `half` bytes apart (32 bytes a step inside a half).
-__device__ __forceinline__ void warp_mma8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+// of `half` bytes (32 bytes a step inside a half).  Descriptors are given by their low words,
+// the high ones being the same.
+__device__ __forceinline__ void warp_mma8_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
                                              uint32_t idesc, uint32_t half) {
-  const uint64_t h = half >> 4;
   asm volatile(
-      "{\n .reg .pred p, t, f;\n .reg .b64 a, b, c, d;\n elect.sync _|p, 0xffffffff;\n"
-      " setp.eq.u32 t, 0, 0;\n setp.ne.u32 f, 0, 0;\n"
-      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n"
-      " add.u64 a, %1, 2;\n add.u64 b, %2, 2;\n"
+      "{\n .reg .pred p, t, f;\n .reg .b64 a, b;\n .reg .b32 x, y, u, v;\n"
+      " elect.sync _|p, 0xffffffff;\n setp.eq.u32 t, 0, 0;\n setp.ne.u32 f, 0, 0;\n"
+      " add.u32 u, %1, %5;\n add.u32 v, %2, %5;\n"
+      " add.u32 x, %1, 0;\n add.u32 y, %2, 0;\n mov.b64 a, {x, %4};\n mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, f;\n"
+      " add.u32 x, %1, 2;\n add.u32 y, %2, 2;\n mov.b64 a, {x, %4};\n mov.b64 b, {y, %4};\n"
       " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
-      " add.u64 a, %1, 4;\n add.u64 b, %2, 4;\n"
+      " add.u32 x, %1, 4;\n add.u32 y, %2, 4;\n mov.b64 a, {x, %4};\n mov.b64 b, {y, %4};\n"
       " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
-      " add.u64 a, %1, 6;\n add.u64 b, %2, 6;\n"
+      " add.u32 x, %1, 6;\n add.u32 y, %2, 6;\n mov.b64 a, {x, %4};\n mov.b64 b, {y, %4};\n"
       " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
-      " add.u64 c, %1, %4;\n add.u64 d, %2, %4;\n"
-      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], c, d, %3, t;\n"
-      " add.u64 a, c, 2;\n add.u64 b, d, 2;\n"
+      " add.u32 x, u, 0;\n add.u32 y, v, 0;\n mov.b64 a, {x, %4};\n mov.b64 b, {y, %4};\n"
       " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
-      " add.u64 a, c, 4;\n add.u64 b, d, 4;\n"
+      " add.u32 x, u, 2;\n add.u32 y, v, 2;\n mov.b64 a, {x, %4};\n mov.b64 b, {y, %4};\n"
       " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
-      " add.u64 a, c, 6;\n add.u64 b, d, 6;\n"
-      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "l"(h)
+      " add.u32 x, u, 4;\n add.u32 y, v, 4;\n mov.b64 a, {x, %4};\n mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      " add.u32 x, u, 6;\n add.u32 y, v, 6;\n mov.b64 a, {x, %4};\n mov.b64 b, {y, %4};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n"
+      "}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kDescHigh), "r"(half >> 4)
       : "memory");
 }
 // Four along K = 64 with A in TMEM (8 columns a step) and B MN-major (16 rows of 128 bytes, 2 KB,
 // a step); the first adds to what D holds only if `accumulate`.
-__device__ __forceinline__ void warp_mma4_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+__device__ __forceinline__ void warp_mma4_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
                                              uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p, q, t;\n .reg .b64 b;\n .reg .b32 a;\n elect.sync _|p, 0xffffffff;\n"
+      "{\n .reg .pred p, q, t;\n .reg .b64 b;\n .reg .b32 x, y;\n elect.sync _|p, 0xffffffff;\n"
       " setp.ne.b32 q, %4, 0;\n setp.eq.u32 t, 0, 0;\n"
-      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n"
-      " add.u32 a, %1, 8;\n add.u64 b, %2, 128;\n"
-      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
-      " add.u32 a, %1, 16;\n add.u64 b, %2, 256;\n"
-      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n"
-      " add.u32 a, %1, 24;\n add.u64 b, %2, 384;\n"
-      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      " add.u32 x, %1, 0;\n add.u32 y, %2, 0;\n mov.b64 b, {y, %5};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, q;\n"
+      " add.u32 x, %1, 8;\n add.u32 y, %2, 128;\n mov.b64 b, {y, %5};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n"
+      " add.u32 x, %1, 16;\n add.u32 y, %2, 256;\n mov.b64 b, {y, %5};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n"
+      " add.u32 x, %1, 24;\n add.u32 y, %2, 384;\n mov.b64 b, {y, %5};\n"
+      " @p tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, t;\n"
+      "}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
       : "memory");
 }
 __device__ __forceinline__ void warp_mma_commit(uint64_t* bar) {

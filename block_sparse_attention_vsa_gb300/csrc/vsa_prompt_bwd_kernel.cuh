@@ -149,7 +149,7 @@ struct Ctl {
   uint64_t kv_full;
   uint64_t q_full[kQStages], q_ready[kQStages], q_empty[kQStages];
   uint64_t g_full[kGStages], g_ready[kGStages], g_empty[kGStages];
-  uint64_t s_full, dp_full, p_full, ds_full, acc_full, drain, never;
+  uint64_t s_full, dp_full, p_full, ds_full, acc_full, turn[2], drain[2], never;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -218,8 +218,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&ctl->dp_full, 1);
     mbar_init(&ctl->p_full, 8);
     mbar_init(&ctl->ds_full, 8);
-    mbar_init(&ctl->acc_full, 1);
-    mbar_init(&ctl->drain, 1);
+    mbar_init(&ctl->acc_full, 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->turn[i], 1);
+      mbar_init(&ctl->drain[i], 1);
+    }
     mbar_init(&ctl->never, 1);
     ctl->abort_flag = 0;
     fence_mbar_init();
@@ -395,76 +398,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-    } else if (warp == 9) {
-      if (lane == 0 && k.steps > 0) {
+    } else if (warp == 9 || warp == 10) {
+      // warp 9: dV_g, S_{g+1}; warp 10: dK_g, dP_{g+1}; a unit each in turn
+      if (k.steps > 0) {
         constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
         constexpr uint32_t kIdescG = idesc_bf16_f32(128, 128, false, true);
-        auto operand = [&](uint32_t at, uint32_t lbo) {
-          return smem_desc_sw128(smem_addr(smem + at), lbo, 1024);
-        };
-        const uint64_t kd = operand(kOffK, 16), vd = operand(kOffV, 16);
-        auto ss = [&](uint32_t d, uint64_t ad, uint64_t bd) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint64_t o = ((i >> 2) * (kTile / 2) + (i & 3) * 32) >> 4;
-            mma_ss(tmem + d, ad + o, bd + o, kIdescS, i > 0);
-          }
-        };
-        // += A B with A's columns as the gradient warps leave them
-        auto ts = [&](uint32_t d, uint32_t col, uint64_t bd, bool first) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            mma_ts(tmem + d, tmem + col + 64 * (i >> 2) + 8 * (i & 3), bd + ((i * 2048) >> 4),
-                   kIdescG, (!first || i > 0) ? 1u : 0u);
-        };
-        auto q_at = [&](int g) { return kOffQ + (uint32_t)(g % kQStages) * kTile; };
-        auto g_at = [&](int g) { return kOffG + (uint32_t)(g % kGStages) * kTile; };
+        const int x = warp - 9;
+        const uint32_t sa = smem_addr(smem);
+        // A of the scores (K or V), the ring that both of the warp's products read
+        const uint32_t ad = desc_low(sa + (x ? kOffV : kOffK), 16);
+        const uint32_t b_k = desc_low(sa + (x ? kOffG : kOffQ), 16);          // K-major
+        const uint32_t b_mn = desc_low(sa + (x ? kOffQ : kOffG), kTile / 2);  // MN-major
+        const uint32_t col = x ? kColDP : kColS, acc = x ? kColDK : kColDV;
+        uint64_t* const full = x ? &ctl->dp_full : &ctl->s_full;
+        uint64_t* const ready = x ? &ctl->ds_full : &ctl->p_full;
         auto q_in = [&](int g) {
-          return wait(&ctl->q_ready[g % kQStages], (g / kQStages) & 1, w, 0x2a);
+          return wait_warp(&ctl->q_ready[g % kQStages], (g / kQStages) & 1, w, 0x2a);
         };
         auto g_in = [&](int g) {
-          return wait(&ctl->g_ready[g % kGStages], (g / kGStages) & 1, w, 0x2b);
+          return wait_warp(&ctl->g_ready[g % kGStages], (g / kGStages) & 1, w, 0x2b);
         };
-        bool ok = a.stall ? wait(&ctl->never, 0, w, 0x3f) : wait(&ctl->kv_full, 0, w, 0x2c);
-        ok = ok && q_in(0);
-        if (ok) {
+        // S^T or dP^T of step g
+        auto scores = [&](int g) {
+          const uint32_t st = x ? (uint32_t)(g % kGStages) : (uint32_t)(g % kQStages);
           tc_fence_after();
-          ss(kColS, kd, operand(q_at(0), 16));
-          mma_commit(&ctl->s_full);
-          ok = g_in(0);
-        }
-        if (ok) {
-          tc_fence_after();
-          ss(kColDP, vd, operand(g_at(0), 16));
-          mma_commit(&ctl->dp_full);
-        }
+          warp_mma8_ss(tmem + col, ad, b_k + st * (kTile >> 4), kIdescS, kTile / 2);
+          warp_mma_commit(full);
+        };
+        bool ok = a.stall ? wait_warp(&ctl->never, 0, w, 0x3f)
+                          : wait_warp(&ctl->kv_full, 0, w, 0x2c) && (x ? g_in(0) : q_in(0));
+        if (ok) scores(0);
         for (int g = 0; g < k.steps && ok; ++g) {
           const bool more = g + 1 < k.steps;
-          if (!wait(&ctl->p_full, g & 1, w, 0x2d)) break;
+          ok = (!more || (x ? g_in(g + 1) : q_in(g + 1))) && wait_warp(ready, g & 1, w, 0x2d) &&
+               ((x == 0 && g == 0) || wait_warp(&ctl->turn[x], (x ? g : g - 1) & 1, w, 0x32));
+          if (!ok) break;
+          const uint32_t st = x ? (uint32_t)(g % kQStages) : (uint32_t)(g % kGStages);
           tc_fence_after();
-          ts(kColDV, kColS, operand(g_at(g), kTile / 2), g == 0);
-          mma_commit(&ctl->g_empty[g % kGStages]);
-          if (more) {
-            if (!q_in(g + 1)) break;
-            tc_fence_after();
-            ss(kColS, kd, operand(q_at(g + 1), 16));
-            mma_commit(&ctl->s_full);
-          }
-          if (!wait(&ctl->ds_full, g & 1, w, 0x2e)) break;
-          tc_fence_after();
-          ts(kColDK, kColDP, operand(q_at(g), kTile / 2), g == 0);
-          mma_commit(&ctl->q_empty[g % kQStages]);
-          if (more) {
-            if (!g_in(g + 1)) break;
-            tc_fence_after();
-            ss(kColDP, vd, operand(g_at(g + 1), 16));
-            mma_commit(&ctl->dp_full);
-          } else {
-            mma_commit(&ctl->acc_full);
-          }
+          warp_mma4_ts(tmem + acc, tmem + col, b_mn + st * (kTile >> 4), kIdescG, g > 0 ? 1u : 0u);
+          warp_mma4_ts(tmem + acc, tmem + col + 64, b_mn + st * (kTile >> 4) + 512, kIdescG, 1u);
+          if (more) scores(g + 1);
+          if (lane == 0) mbar_arrive(&ctl->turn[x ^ 1]);
+          // (the commit also covers the next scores, issued since)
+          warp_mma_commit(x ? &ctl->q_empty[st] : &ctl->g_empty[st]);
+          if (!more) warp_mma_commit(&ctl->acc_full);
         }
-        mma_commit(&ctl->drain);
-        wait(&ctl->drain, 0, w, 0x2f, true);
+        warp_mma_commit(&ctl->drain[x]);
+        wait(&ctl->drain[x], 0, w, 0x2f, true);
       }
       __syncwarp();
     } else if (warp == 11) {
@@ -506,7 +486,8 @@ struct Ctl {
   uint64_t q_full;
   uint64_t k_full[kKStages], k_ready[kKStages], k_empty[kKStages];
   uint64_t v_full[kVStages], v_empty[kVStages];
-  uint64_t s_full, s_empty, dp_full[2], ds_full[2], x_full[4], acc_full, drain, never;
+  uint64_t s_full, s_empty, dp_full[2], ds_full[2], ds_empty[2], x_full[4], acc_full, drain[2];
+  uint64_t never;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -556,12 +537,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->v_empty[i], 1);
       mbar_init(&ctl->dp_full[i], 1);
       mbar_init(&ctl->ds_full[i], 8);
+      mbar_init(&ctl->ds_empty[i], 1);
+      mbar_init(&ctl->drain[i], 1);
     }
     mbar_init(&ctl->s_full, 1);
     mbar_init(&ctl->s_empty, 8);
     for (int i = 0; i < 4; ++i) mbar_init(&ctl->x_full[i], 2);
     mbar_init(&ctl->acc_full, 1);
-    mbar_init(&ctl->drain, 1);
     mbar_init(&ctl->never, 1);
     ctl->abort_flag = 0;
     fence_mbar_init();
@@ -750,51 +732,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp == 9) {
-      if (lane == 0 && steps > 0) {
+      // S_g, dP_g
+      if (steps > 0) {
         constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
-        constexpr uint32_t kIdescG = idesc_bf16_f32(128, 128, false, true);
-        auto operand = [&](uint32_t at, uint32_t lbo) {
-          return smem_desc_sw128(smem_addr(smem + at), lbo, 1024);
-        };
-        const uint64_t qd = operand(kOffQ, 16), gd = operand(kOffG, 16);
-        auto ss = [&](uint32_t d, uint64_t ad, uint64_t bd) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint64_t o = ((i >> 2) * (kTile / 2) + (i & 3) * 32) >> 4;
-            mma_ss(tmem + d, ad + o, bd + o, kIdescS, i > 0);
-          }
-        };
-        // S and dP of step g
-        auto scores = [&](int g) {
-          const int ks = g % kKStages, vs = g % kVStages;
-          if (!wait(&ctl->k_ready[ks], (g / kKStages) & 1, w, 0x49)) return false;
-          if (g > 0 && !wait(&ctl->s_empty, (g - 1) & 1, w, 0x4a)) return false;
-          tc_fence_after();
-          ss(kColS, qd, operand(kOffK + ks * kTile, 16));
-          mma_commit(&ctl->s_full);
-          if (!wait(&ctl->v_full[vs], (g / kVStages) & 1, w, 0x4b)) return false;
-          tc_fence_after();
-          ss(kColDP + 128 * (g & 1), gd, operand(kOffV + vs * kTile, 16));
-          mma_commit(&ctl->dp_full[g & 1]);
-          mma_commit(&ctl->v_empty[vs]);
-          return true;
-        };
-        bool ok = a.stall ? wait(&ctl->never, 0, w, 0x5f) : wait(&ctl->q_full, 0, w, 0x4c);
-        ok = ok && scores(0);
+        const uint32_t sa = smem_addr(smem);
+        const uint32_t qd = desc_low(sa + kOffQ, 16), gd = desc_low(sa + kOffG, 16),
+                       kd = desc_low(sa + kOffK, 16), vd = desc_low(sa + kOffV, 16);
+        bool ok = a.stall ? wait_warp(&ctl->never, 0, w, 0x5f)
+                          : wait_warp(&ctl->q_full, 0, w, 0x4c);
         for (int g = 0; g < steps && ok; ++g) {
-          if (g + 1 < steps && !scores(g + 1)) break;
-          if (!wait(&ctl->ds_full[g & 1], (g >> 1) & 1, w, 0x4d)) break;
+          const uint32_t ks = (uint32_t)(g % kKStages), vs = (uint32_t)(g % kVStages);
+          ok = wait_warp(&ctl->k_ready[ks], (g / kKStages) & 1, w, 0x49) &&
+               (g == 0 || wait_warp(&ctl->s_empty, (g - 1) & 1, w, 0x4a));
+          if (!ok) break;
           tc_fence_after();
-          const uint64_t kd = operand(kOffK + (g % kKStages) * kTile, kTile / 2);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            mma_ts(tmem + kColDQ, tmem + kColDP + 128 * (g & 1) + 64 * (i >> 2) + 8 * (i & 3),
-                   kd + ((i * 2048) >> 4), kIdescG, (g > 0 || i > 0) ? 1u : 0u);
-          mma_commit(&ctl->k_empty[g % kKStages]);
-          if (g + 1 == steps) mma_commit(&ctl->acc_full);
+          warp_mma8_ss(tmem + kColS, qd, kd + ks * (kTile >> 4), kIdescS, kTile / 2);
+          warp_mma_commit(&ctl->s_full);
+          // the buffer's dS (of step g - 2) has been read
+          ok = wait_warp(&ctl->v_full[vs], (g / kVStages) & 1, w, 0x4b) &&
+               (g < 2 || wait_warp(&ctl->ds_empty[g & 1], ((g - 2) >> 1) & 1, w, 0x51));
+          if (!ok) break;
+          tc_fence_after();
+          warp_mma8_ss(tmem + kColDP + 128 * (g & 1), gd, vd + vs * (kTile >> 4), kIdescS, kTile / 2);
+          warp_mma_commit(&ctl->dp_full[g & 1]);
+          warp_mma_commit(&ctl->v_empty[vs]);
         }
-        mma_commit(&ctl->drain);
-        wait(&ctl->drain, 0, w, 0x4e, true);
+        warp_mma_commit(&ctl->drain[0]);
+        wait(&ctl->drain[0], 0, w, 0x4e, true);
+      }
+      __syncwarp();
+    } else if (warp == 10) {
+      // dQ += dS_g K
+      if (steps > 0) {
+        constexpr uint32_t kIdescG = idesc_bf16_f32(128, 128, false, true);
+        const uint32_t kd = desc_low(smem_addr(smem) + kOffK, kTile / 2);
+        for (int g = 0; g < steps; ++g) {
+          const uint32_t ks = (uint32_t)(g % kKStages);
+          if (!wait_warp(&ctl->ds_full[g & 1], (g >> 1) & 1, w, 0x4d)) break;
+          tc_fence_after();
+          const uint32_t t = tmem + kColDP + 128 * (g & 1);
+          warp_mma4_ts(tmem + kColDQ, t, kd + ks * (kTile >> 4), kIdescG, g > 0 ? 1u : 0u);
+          warp_mma4_ts(tmem + kColDQ, t + 64, kd + ks * (kTile >> 4) + 512, kIdescG, 1u);
+          warp_mma_commit(&ctl->ds_empty[g & 1]);
+          warp_mma_commit(&ctl->k_empty[ks]);
+          if (g + 1 == steps) warp_mma_commit(&ctl->acc_full);
+        }
+        warp_mma_commit(&ctl->drain[1]);
+        wait(&ctl->drain[1], 0, w, 0x4e, true);
       }
       __syncwarp();
     } else if (warp == 11) {

@@ -25,6 +25,7 @@ namespace prompt {
 
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // one second per wait
 constexpr unsigned kErrTimeout = 0x100u;          // | code of the wait that gave up
+constexpr uint32_t kSleepNs = 20000;              // a waiting thread looks up this often
 constexpr uint32_t kTile = 128 * 128 * 2;         // 128 rows of Q, K, V or dO
 constexpr float kLseEmpty = -3.402823466e+38f;
 
@@ -99,7 +100,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const WaitC
   const uint64_t limit = drain ? kWaitLimitNs : w.limit_ns;
   const uint64_t t0 = global_timer_ns();
   while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_sleep_wait(bar, parity, kSleepNs)) return true;
     if (!drain && *reinterpret_cast<volatile int*>(w.abort_flag)) return false;
     if (global_timer_ns() - t0 > limit) {
       *reinterpret_cast<volatile int*>(w.abort_flag) = 1;

@@ -200,9 +200,9 @@ __device__ __forceinline__ void mma_role(const FwdArgs& a, uint8_t* smem, Ctl* c
                                          const WaitCtx& w, uint32_t tmem, int t) {
   constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
   constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, false, true);
-  const uint64_t qd = smem_desc_sw128(smem_addr(smem + kOffQ + t * kTile), 16, 1024);
-  const uint64_t kd = smem_desc_sw128(smem_addr(smem + kOffKV), 16, 1024);
-  const uint64_t vd = smem_desc_sw128(smem_addr(smem + kOffKV), kTile / 2, 1024);
+  const uint32_t qd = desc_low(smem_addr(smem + kOffQ + t * kTile), 16);
+  const uint32_t kd = desc_low(smem_addr(smem + kOffKV), 16);
+  const uint32_t vd = desc_low(smem_addr(smem + kOffKV), kTile / 2);
   const uint32_t tS = tmem + kColS + 128 * t, tO = tmem + kColO + 128 * t;
   const bool leader = lane_id() == 0;
   uint32_t st = 0, ph = 0;        // ring position
