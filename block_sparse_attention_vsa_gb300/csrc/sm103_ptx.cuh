@@ -169,6 +169,31 @@ __device__ __forceinline__ uint64_t policy_evict_first() {
   return p;
 }
 
+// ---------------------------------------------------------------- cluster launch control
+// Asks for a CTA of the grid that has not been launched yet, to do its work in its place: the
+// answer (16 bytes, aligned) arrives like a copy, counted on `bar` in bytes.  One request at a
+// time, and none after one that came back empty.
+__device__ __forceinline__ void try_cancel(void* answer, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128"
+      " [%0], [%1];" ::"r"(smem_addr(answer)),
+      "r"(smem_addr(bar))
+      : "memory");
+}
+// The x index of the CTA that the answer holds, or -1.
+__device__ __forceinline__ int canceled_cta(const void* answer) {
+  int x;
+  asm volatile(
+      "{\n .reg .b128 r;\n .reg .pred p;\n .reg .b32 a, b, c, d;\n ld.shared.b128 r, [%1];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n mov.b32 a, 0xffffffff;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {a, b, c, d}, r;\n"
+      " mov.b32 %0, a;\n}"
+      : "=r"(x)
+      : "r"(smem_addr(answer))
+      : "memory");
+  return x;
+}
+
 // ---------------------------------------------------------------- tcgen05 / TMEM
 // Allocation is a warp-wide operation; the TMEM base address is written to shared memory.
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {

@@ -19,8 +19,6 @@ using namespace vsa;
 
 namespace {
 
-constexpr int kSms = 152;  // of a GB300, which host_device() asks for
-
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -214,7 +212,7 @@ vsa_status vsa_fwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
   a.pack = pack_log(a.group);
   a.n_packs = Hq >> a.pack;
   const long long slots = prompt::tile_slots(packed, B, Sq, 256 >> a.pack);
-  if (slots * a.n_packs > INT_MAX - 2 * kSms) return VSA_ERR_UNSUPPORTED;
+  if (slots * a.n_packs > INT_MAX) return VSA_ERR_UNSUPPORTED;
   a.n_slots = (int)slots;
   a.n_items = (int)(slots * a.n_packs);
   a.scale_log2 = scale * 1.4426950408889634f;
@@ -234,8 +232,7 @@ vsa_status vsa_fwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
   if (!make_map(&tq, vq, 128 >> a.pack, 1 << a.pack) || !make_map(&tk, vk.empty() ? vq : vk, 128, 1) ||
       !make_map(&tv, vv.empty() ? vq : vv, 128, 1))
     return VSA_ERR_CUDA;
-  const int grid = a.n_items < kSms ? a.n_items : kSms;
-  prompt::fwd::prompt_fwd_kernel<<<grid, prompt::fwd::kThreads, prompt::fwd::kSmemBytes,
+  prompt::fwd::prompt_fwd_kernel<<<(unsigned)a.n_items, prompt::fwd::kThreads, prompt::fwd::kSmemBytes,
                                    reinterpret_cast<cudaStream_t>(stream)>>>(tq, tk, tv, a);
   if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
   host_set_launches(1);

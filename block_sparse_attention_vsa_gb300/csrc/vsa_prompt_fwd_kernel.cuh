@@ -6,9 +6,11 @@
 //
 // computed in one pass over the keys: with a reference m that follows the running maximum (it
 // may lag by up to 2^32, in log2 units 32, so that the accumulator is rarely rescaled),
-// P = 2^(S - m) is rounded to bf16 for the product with V, and out = O / l with l the sum of
-// the rounded weights (so that the weights applied add up to one), lse = m + log2 of the sum
-// of the fp32 weights.  S, O, m and the sums are fp32.
+// P = 2^(S - m) is rounded to bf16 for the product with V, out = O / l and lse = m + log2 l
+// with l the sum of the fp32 weights.  (A sum of the rounded ones as well, for out, takes a
+// quarter of the loop's instructions -- 1492 TFLOP/s instead of 1647 -- and gains nothing
+// where many keys count: out is off by 0.0023 of its norm either way, 0.0017 of it from its own
+// rounding.)  S, O, m and l are fp32.
 //
 // An item is two query tiles of 128 rows (neighbours in the sequence) that share every K and V
 // tile: an SS product of 128 x 128 x 128 takes the tensor core 512 cycles and reads 64 KB of
@@ -16,7 +18,8 @@
 // keeps the copies' writes affordable.  A warpgroup per query tile works on its scores while
 // the tensor core works for the other one.
 //
-// One persistent CTA per SM, 12 warps:
+// A CTA per item is launched, and one that has done its own takes over those not launched yet
+// (cluster launch control), so a CTA per SM stays and work is handed out as it is done.  12 warps:
 //   warps 0-3, 4-7  softmax warpgroups of query tile 0 and 1 (thread = query row)
 //   warp 8          decodes items and copies: Q tiles, and K, V alternating through a ring
 //   warp 9          MMA issuer: S_0(0), S_1(0), then per key tile j and query tile t: O_t +=
@@ -81,6 +84,8 @@ struct Ctl {
   uint64_t o_full[2], o_empty[2];
   uint64_t turn[2];        // of the MMA warps
   uint64_t drain[2], never;
+  alignas(16) uint8_t next[16];  // the answer to a request for work
+  uint64_t next_full;
   Item item[2];
   uint32_t tmem_base;
   int abort_flag;
@@ -122,28 +127,60 @@ __device__ __forceinline__ bool decode(const FwdArgs& a, int id, Item& it) {
   return a.seq.packed ? tile >= 0 && it.tok < s.nq : true;
 }
 
-// The CTA's n-th item that holds something, from slot `id` on (by a whole warp).
-__device__ __forceinline__ Item next_item(const FwdArgs& a, int& id) {
-  Item it;
-  for (; id < a.n_items; id += (int)gridDim.x)
-    if (decode(a, id, it)) {
-      id += (int)gridDim.x;
-      return it;
+// The items of a CTA (by a whole warp): its own, and then those of CTAs not yet launched, in
+// the order of their indices, each asked for while the one before is worked on.
+struct Items {
+  const FwdArgs& a;
+  Ctl* ctl;
+  const WaitCtx& w;
+  uint32_t asked = 0;
+  bool first = true, pending = false;
+
+  __device__ __forceinline__ void ask() {
+    if (lane_id() == 0) {
+      fence_proxy_async_smem();  // the last answer has been read
+      mbar_arrive_expect_tx(&ctl->next_full, 16);
+      try_cancel(ctl->next, &ctl->next_full);
     }
-  it.go = 0;
-  return it;
-}
+    __syncwarp();
+    pending = true;
+  }
+  // false: a wait has run out
+  __device__ __forceinline__ bool next(Item& it) {
+    it.go = 0;
+    if (first) {
+      first = false;
+      ask();
+      if (decode(a, (int)blockIdx.x, it)) return true;
+    }
+    while (pending) {
+      if (!wait_warp(&ctl->next_full, asked & 1, w, 0x15)) return false;
+      ++asked;
+      pending = false;
+      const int id = canceled_cta(ctl->next);
+      __syncwarp();
+      if (id < 0) break;
+      ask();
+      if (decode(a, id, it)) return true;
+    }
+    it.go = 0;
+    return true;
+  }
+  __device__ __forceinline__ void drain() {
+    if (pending) wait(&ctl->next_full, asked & 1, w, 0x16, true);
+  }
+};
 
 __device__ __forceinline__ void load_role(const FwdArgs& a, uint8_t* smem, Ctl* ctl,
                                           const WaitCtx& w, const CUtensorMap* tq,
                                           const CUtensorMap* tk, const CUtensorMap* tv) {
   const bool leader = lane_id() == 0;
   uint32_t st = 0, ph = 0, fills = 0, nq0 = 0, nq1 = 0;  // ring position; loads of Q tiles
-  int id = (int)blockIdx.x;
   const int half = 128 >> a.pack;
-  bool ok = true;
-  Item it = next_item(a, id);
-  for (uint32_t i = 0;; ++i) {
+  Items items{a, ctl, w};
+  Item it;
+  bool ok = items.next(it);
+  for (uint32_t i = 0; ok; ++i) {
     const uint32_t buf = i & 1;
     if (i >= 2 && !wait_warp(&ctl->item_empty[buf], ((i >> 1) + 1) & 1, w, 0x01)) break;
     if (leader) {
@@ -181,10 +218,10 @@ __device__ __forceinline__ void load_role(const FwdArgs& a, uint8_t* smem, Ctl* 
       if (ok && cur.n1 > 0) ok = put_q(1, nq1);
       if (ok) ok = put(tv, 0);
     }
-    it = next_item(a, id);
+    ok = ok && items.next(it);
     for (int j = 1; j < n && ok; ++j) ok = put(tk, j) && put(tv, j);
-    if (!ok) break;
   }
+  items.drain();
   // every copy issued has landed before the CTA exits
   for (uint32_t s = 0; s < (uint32_t)kStages; ++s) {
     const uint32_t f = fills > s ? (fills - s + kStages - 1) / kStages : 0;
@@ -349,7 +386,7 @@ __device__ __forceinline__ void softmax_role(const FwdArgs& a, Ctl* ctl, const W
     int lim = it.nk;
     if (a.seq.causal) lim = clampi(tok + 1 + it.nk - it.nq, 0, it.nk);
     if (tok >= it.nq) lim = 0;
-    float m = -INFINITY, l_exact = 0.0f, l_round = 0.0f;
+    float m = -INFINITY, l = 0.0f;
     bool ok = true;
     for (int j = 0; j < n; ++j, ++tiles) {
       if (!wait_warp(&ctl->s_full[t], tiles & 1, w, 0x11)) {
@@ -399,7 +436,6 @@ __device__ __forceinline__ void softmax_role(const FwdArgs& a, Ctl* ctl, const W
       const float neg = m == -INFINITY ? 0.0f : -m;
       const uint64_t c2 = f32x2(sl2, sl2), neg2 = f32x2(neg, neg);
       uint64_t acc_e[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
-      float r0 = 0.f, r1 = 0.f, r2 = 0.f, r3 = 0.f;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t pk[32];
@@ -411,10 +447,6 @@ __device__ __forceinline__ void softmax_role(const FwdArgs& a, Ctl* ctl, const W
           const float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
           acc_e[e & 1] = add_f32x2(acc_e[e & 1], f32x2(e0, e1));
           pk[e] = pack_bf16x2(e0, e1);
-          if (e & 1)
-            add_bf16x2_to_f32(pk[e], r2, r3);
-          else
-            add_bf16x2_to_f32(pk[e], r0, r1);
         }
         tmem_st_32x32b_x32(tS + 32 * h, pk);
         tmem_wait_st();
@@ -425,14 +457,13 @@ __device__ __forceinline__ void softmax_role(const FwdArgs& a, Ctl* ctl, const W
       float e0, e1, e2, e3;
       split_f32x2(acc_e[0], e0, e1);
       split_f32x2(acc_e[1], e2, e3);
-      l_exact = l_exact * alpha + ((e0 + e1) + (e2 + e3));
-      l_round = l_round * alpha + ((r0 + r1) + (r2 + r3));
+      l = l * alpha + ((e0 + e1) + (e2 + e3));
     }
     if (!ok) break;
     // a row that attends nothing gets +0 and the sentinel; scores that are no numbers, or all
     // -infinity, give NaN
     const bool some = lim > 0;
-    const float inv = some ? 1.0f / l_round : 0.0f;
+    const float inv = some ? 1.0f / l : 0.0f;
     const bool write = tok < (a.seq.packed ? it.nq : a.seq.Sq);
     uint16_t* dst = a.out + it.z * a.out_b + head * a.out_h + (long long)(it.q0 + tok) * a.out_t;
     if (n > 0) {
@@ -442,7 +473,7 @@ __device__ __forceinline__ void softmax_role(const FwdArgs& a, Ctl* ctl, const W
     }
     if (write && a.lse != nullptr)
       a.lse[((long long)it.z * a.Hq + head) * a.seq.Sq + it.q0 + tok] =
-          some ? (l_exact > 0.0f ? m + log2f(l_exact) : __int_as_float(0x7fffffff)) : kLseEmpty;
+          some ? (l > 0.0f ? m + log2f(l) : __int_as_float(0x7fffffff)) : kLseEmpty;
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       uint32_t o[32];
@@ -498,6 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->kv_empty[i], 2);  // both MMA warps
     }
     mbar_init(&ctl->never, 1);
+    mbar_init(&ctl->next_full, 1);
     ctl->abort_flag = 0;
     fence_mbar_init();
   }
