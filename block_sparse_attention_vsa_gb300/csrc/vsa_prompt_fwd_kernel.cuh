@@ -56,10 +56,11 @@ struct FwdArgs {
 namespace fwd {
 
 constexpr int kThreads = 384;
-constexpr int kStages = 5;
+constexpr int kStages = 4;
 constexpr uint32_t kOffQ = 0;  // [2]
 constexpr uint32_t kOffKV = 2 * kTile;
-constexpr uint32_t kOffCtl = kOffKV + kStages * kTile;
+constexpr uint32_t kOffOut = kOffKV + kStages * kTile;  // 32 rows of 32 columns a softmax warp
+constexpr uint32_t kOffCtl = kOffOut + 8 * 2048;
 constexpr uint32_t kSmemBytes = kOffCtl + 1024 + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 constexpr uint32_t kSoftmaxRegs = 216, kOtherRegs = 56;
@@ -86,7 +87,7 @@ struct Ctl {
   uint64_t drain[2], never;
   alignas(16) uint8_t next[16];  // the answer to a request for work
   uint64_t next_full;
-  Item item[2];
+  Item own, item[2];
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -134,7 +135,7 @@ struct Items {
   Ctl* ctl;
   const WaitCtx& w;
   uint32_t asked = 0;
-  bool first = true, pending = false;
+  bool pending = false;
 
   __device__ __forceinline__ void ask() {
     if (lane_id() == 0) {
@@ -147,12 +148,6 @@ struct Items {
   }
   // false: a wait has run out
   __device__ __forceinline__ bool next(Item& it) {
-    it.go = 0;
-    if (first) {
-      first = false;
-      ask();
-      if (decode(a, (int)blockIdx.x, it)) return true;
-    }
     while (pending) {
       if (!wait_warp(&ctl->next_full, asked & 1, w, 0x15)) return false;
       ++asked;
@@ -178,8 +173,9 @@ __device__ __forceinline__ void load_role(const FwdArgs& a, uint8_t* smem, Ctl* 
   uint32_t st = 0, ph = 0, fills = 0, nq0 = 0, nq1 = 0;  // ring position; loads of Q tiles
   const int half = 128 >> a.pack;
   Items items{a, ctl, w};
-  Item it;
-  bool ok = items.next(it);
+  items.ask();
+  Item it = ctl->own;
+  bool ok = it.go || items.next(it);
   for (uint32_t i = 0; ok; ++i) {
     const uint32_t buf = i & 1;
     if (i >= 2 && !wait_warp(&ctl->item_empty[buf], ((i >> 1) + 1) & 1, w, 0x01)) break;
@@ -364,8 +360,8 @@ __device__ __forceinline__ void clean_role(uint8_t* smem, Ctl* ctl, const WaitCt
   }
 }
 
-__device__ __forceinline__ void softmax_role(const FwdArgs& a, Ctl* ctl, const WaitCtx& w,
-                                             uint32_t tmem, int t) {
+__device__ __forceinline__ void softmax_role(const FwdArgs& a, uint8_t* smem, Ctl* ctl,
+                                             const WaitCtx& w, uint32_t tmem, int t) {
   const int row = (int)(threadIdx.x & 127);
   const uint32_t lanes = (uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16;
   const uint32_t tS = tmem + lanes + kColS + 128 * t, tO = tmem + lanes + kColO + 128 * t;
@@ -375,17 +371,16 @@ __device__ __forceinline__ void softmax_role(const FwdArgs& a, Ctl* ctl, const W
   for (uint32_t i = 0;; ++i) {
     const uint32_t buf = i & 1;
     if (!wait_warp(&ctl->item_full[buf], (i >> 1) & 1, w, 0x10)) break;
-    const Item it = ctl->item[buf];
-    __syncwarp();
-    if (lane_id() == 0) mbar_arrive(&ctl->item_empty[buf]);
-    if (!it.go) break;
-    const int n = t ? it.n1 : it.n0;
-    const int tok = it.tok + t * half + (row & (half - 1));
-    const int head = it.head0 + (row >> (7 - a.pack));
-    // keys this row attends
-    int lim = it.nk;
-    if (a.seq.causal) lim = clampi(tok + 1 + it.nk - it.nq, 0, it.nk);
-    if (tok >= it.nq) lim = 0;
+    // (what only the end needs is read again there: registers are short in the loop)
+    if (!ctl->item[buf].go) break;
+    const int n = t ? ctl->item[buf].n1 : ctl->item[buf].n0;
+    int lim;  // keys this row attends
+    {
+      const int nq = ctl->item[buf].nq, nk = ctl->item[buf].nk;
+      const int tok = ctl->item[buf].tok + t * half + (row & (half - 1));
+      lim = a.seq.causal ? clampi(tok + 1 + nk - nq, 0, nk) : nk;
+      if (tok >= nq) lim = 0;
+    }
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
     for (int j = 0; j < n; ++j, ++tiles) {
@@ -464,39 +459,62 @@ __device__ __forceinline__ void softmax_role(const FwdArgs& a, Ctl* ctl, const W
     // -infinity, give NaN
     const bool some = lim > 0;
     const float inv = some ? 1.0f / l : 0.0f;
-    const bool write = tok < (a.seq.packed ? it.nq : a.seq.Sq);
-    uint16_t* dst = a.out + it.z * a.out_b + head * a.out_h + (long long)(it.q0 + tok) * a.out_t;
     if (n > 0) {
       if (!wait_warp(&ctl->o_full[t], done & 1, w, 0x12)) break;
       ++done;
       tc_fence_after();
     }
-    if (write && a.lse != nullptr)
+    const Item it = ctl->item[buf];
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive(&ctl->item_empty[buf]);
+    const int n_rows = a.seq.packed ? it.nq : a.seq.Sq;  // tokens that are written
+    const int tok = it.tok + t * half + (row & (half - 1));
+    const int head = it.head0 + (row >> (7 - a.pack));
+    if (tok < n_rows && a.lse != nullptr)
       a.lse[((long long)it.z * a.Hq + head) * a.seq.Sq + it.q0 + tok] =
           some ? (l > 0.0f ? m + log2f(l) : __int_as_float(0x7fffffff)) : kLseEmpty;
+    // 32 columns at a time through shared memory, so that a warp's store is 8 rows of 64 bytes,
+    // not 32 of 16 (which took 6,000 cycles an item)
+    uint8_t* stage = smem + kOffOut + (threadIdx.x >> 5) * 2048;
+    const uint32_t lane = lane_id();
+    const int r0 = (int)(threadIdx.x & 96);  // the warp's first row of the tile
+    uint16_t* base = a.out + it.z * a.out_b + (long long)(it.q0 + it.tok + t * half) * a.out_t;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int h = 0; h < 4; ++h) {
       uint32_t o[32];
       if (n > 0) {
-        tmem_ld_32x32b_x32(tO + 32 * c, o);
+        tmem_ld_32x32b_x32(tO + 32 * h, o);
         tmem_wait_ld();
+        if (h == 3) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->o_empty[t]);
+        }
       }
-      if (c == 3 && n > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane_id() == 0) mbar_arrive(&ctl->o_empty[t]);
-      }
-      if (!write) continue;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int c = 0; c < 4; ++c) {
         uint32_t x[4];
 #pragma unroll
         for (int y = 0; y < 4; ++y)
-          x[y] = some && n > 0 ? pack_bf16x2(__uint_as_float(o[8 * e + 2 * y]) * inv,
-                                             __uint_as_float(o[8 * e + 2 * y + 1]) * inv)
+          x[y] = some && n > 0 ? pack_bf16x2(__uint_as_float(o[8 * c + 2 * y]) * inv,
+                                             __uint_as_float(o[8 * c + 2 * y + 1]) * inv)
                                : 0u;
-        reinterpret_cast<uint4*>(dst + 32 * c)[e] = make_uint4(x[0], x[1], x[2], x[3]);
+        // (pieces of 16 bytes, turned by the row so that eight rows' meet all banks)
+        *reinterpret_cast<uint4*>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16)) =
+            make_uint4(x[0], x[1], x[2], x[3]);
       }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t rr = 8 * i + (lane >> 2), c = lane & 3;
+        const uint4 x =
+            *reinterpret_cast<const uint4*>(stage + rr * 64 + ((c ^ ((rr >> 1) & 3)) * 16));
+        const int row = r0 + (int)rr, off = row & (half - 1);
+        if (it.tok + t * half + off < n_rows)
+          *reinterpret_cast<uint4*>(base + (it.head0 + (row >> (7 - a.pack))) * a.out_h +
+                                    (long long)off * a.out_t + 32 * h + 8 * c) = x;
+      }
+      __syncwarp();
     }
   }
 }
@@ -542,6 +560,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&ctl->tmem_base, kTmemCols);
     tmem_relinquish();
   }
+  if (warp == 8) {  // the CTA's own item is looked up while the others get ready
+    Item it;
+    const bool holds = decode(a, (int)blockIdx.x, it);
+    it.go = holds ? 1 : 0;
+    if (lane_id() == 0) ctl->own = it;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -550,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 8) {
     regs_increase<kSoftmaxRegs>();
-    softmax_role(a, ctl, w, tmem, (int)(warp >> 2));
+    softmax_role(a, smem, ctl, w, tmem, (int)(warp >> 2));
   } else {
     regs_decrease<kOtherRegs>();
     if (warp == 8)
