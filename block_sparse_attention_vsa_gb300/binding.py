@@ -40,6 +40,7 @@ EXPORTS = ("vsa_fwd", "jenga_fwd", "vsa_workspace_bytes", "vsa_lut_to_bitmap",
            "vsa_bwd_workspace_bytes", "vsa_set_wait_limit_ns", "vsa_set_stall_test",
            "vsa_block_mean", "vsa_select_blocks", "vsa_cache_select", "vsa_cache_write",
            "vsa_fwd_cache", "vsa_cache_workspace_bytes", "vsa_cache_evict", "vsa_fwd_prompt",
+           "vsa_fwd_prompt_workspace_bytes",
            "vsa_bwd_prompt", "vsa_bwd_prompt_workspace_bytes", "vsa_pages_free",
            "vsa_pages_reserve", "vsa_cache_fork", "vsa_cache_compact")
 MAX_SPLITS = 64
@@ -125,7 +126,9 @@ def load(path: str = LIB_PATH):
     h.vsa_cache_evict.restype = i32
     h.vsa_cache_evict.argtypes = [P, P, P] + [i32] * 6 + [P] * 6
     h.vsa_fwd_prompt.restype = i32
-    h.vsa_fwd_prompt.argtypes = [P] * 6 + [i32] * 8 + [f32, P, P, P]
+    h.vsa_fwd_prompt.argtypes = [P] * 6 + [i32] * 8 + [f32, P, P, P, sz, P]
+    h.vsa_fwd_prompt_workspace_bytes.restype = sz
+    h.vsa_fwd_prompt_workspace_bytes.argtypes = [i32] * 6
     h.vsa_bwd_prompt_workspace_bytes.restype = sz
     h.vsa_bwd_prompt_workspace_bytes.argtypes = [i32] * 5
     h.vsa_bwd_prompt.restype = i32
@@ -1002,16 +1005,18 @@ class _Prompt:
 
 
 def vsa_fwd_prompt(q, k, v, q_seq=None, k_seq=None, causal=True, scale=None, out=None, lse=True,
-                   stream=None):
+                   workspace=None, stream=None):
     """Attention over whole prompts.  Packed: q bf16 [tokens,Hq,128], k, v [tokens,Hkv,128],
     q_seq, k_seq int32 [B+1] the starts of the sequences and the end (k_seq None: q_seq); rows
     of no sequence are not written.  Padded: q [B,Hq,Sq,128], k, v [B,Hkv,Sk,128], q_seq,
     k_seq int32 [B] the sequences' lengths (None: all rows); rows behind a length get 0.  Any
     strides but the last.  causal: the last query is at the last key, query i attends keys up
-    to i + nk - nq.  Returns (out, lse or None), lse float32 (base 2) [Hq,tokens] or
-    [B,Hq,Sq]."""
+    to i + nk - nq.  workspace (uint8, fwd_prompt_workspace_bytes): where the keys of few
+    queries are cut into ranges; allocated if not given, False: they are not cut.  Returns (out,
+    lse or None), lse float32 (base 2) [Hq,tokens] or [B,Hq,Sq]."""
     if stream is None:
-        r = _short("vsa_fwd_prompt", "fwd_prompt", q, k, v, q_seq, k_seq, causal, scale, out, lse)
+        r = _short("vsa_fwd_prompt", "fwd_prompt", q, k, v, q_seq, k_seq, causal, scale, out, lse,
+                   workspace)
         if r is not None:
             return r
     p = _Prompt(q, k, v, q_seq, k_seq)
@@ -1020,12 +1025,26 @@ def vsa_fwd_prompt(q, k, v, q_seq=None, k_seq=None, causal=True, scale=None, out
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if lse is True:
             lse = torch.empty(p.lse, dtype=torch.float32, device=q.device)
+        if workspace is None:
+            n = fwd_prompt_workspace_bytes(p.packed, p.B, p.Hq, p.Hkv, p.Sq, p.Sk)
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else False
+    if workspace is not False and (not workspace.is_contiguous()
+                                   or workspace.get_device() != p.dev):
+        raise ValueError(f"workspace must be contiguous and on cuda:{p.dev}")
     _rows("out", out, torch.bfloat16, q.dim(), p.dev, q.shape)
     lse_p = _maybe("lse", None if lse is False else lse, torch.float32, p.lse, p.dev)
     _call("vsa_fwd_prompt", p.dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           p.strides(q, k, v, out), *p.sizes(), 1 if causal else 0,
-          1.0 / math.sqrt(p.D) if scale is None else float(scale), out.data_ptr(), lse_p)
+          1.0 / math.sqrt(p.D) if scale is None else float(scale), out.data_ptr(), lse_p,
+          None if workspace is False else workspace.data_ptr(),
+          0 if workspace is False else workspace.numel() * workspace.element_size())
     return out, None if lse is False else lse
+
+
+def fwd_prompt_workspace_bytes(packed, B, Hq, Hkv, Sq, Sk) -> int:
+    for name, n in (("B", B), ("Hq", Hq), ("Hkv", Hkv), ("Sq", Sq), ("Sk", Sk)):
+        _whole(name, n)
+    return int(load().vsa_fwd_prompt_workspace_bytes(1 if packed else 0, B, Hq, Hkv, Sq, Sk))
 
 
 def vsa_bwd_prompt(q, k, v, out, dout, lse, q_seq=None, k_seq=None, causal=True, scale=None,

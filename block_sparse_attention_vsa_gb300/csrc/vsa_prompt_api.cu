@@ -155,6 +155,24 @@ int pack_log(int group) {
   return l;
 }
 
+constexpr int kSms = 152;     // of a GB300, which host_device() asks for
+constexpr int kMaxSplits = 32;  // a lane each where they are joined
+
+// Into how many ranges the forward cuts an item's keys: as many as fill the SMs once, of four
+// key tiles or more, and none where the items fill them (they are taken up as SMs come free).
+// One token of 12 heads against 16,384 keys takes 36 us cut and 228 whole, 40 tokens of 2 x 12
+// heads against 4,000 keys 28 and 62; in ranges of two tiles 64 tokens of 8 heads against 512
+// keys take 19 us, whole 15.
+int key_splits(long long items, long long Sk) {
+  const long long fill = items > 0 ? kSms / items : 1, most = (Sk + 127) / 128 / 4;
+  const long long n = fill < most ? fill : most;
+  return n < 2 ? 1 : (n < kMaxSplits ? (int)n : kMaxSplits);
+}
+long long fwd_items(int packed, long long B, int Hq, int Hkv, long long Sq) {
+  const int pack = pack_log(Hq / Hkv);
+  return prompt::tile_slots(packed, B, Sq, 256 >> pack) * (Hq >> pack);
+}
+
 bool meets(const View& x, const void* p, long long bytes) {
   if (x.empty() || !p || bytes <= 0) return false;
   const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(p);
@@ -177,10 +195,18 @@ bool meets_seq(const Shape& p, const void* x, long long bytes) {
 
 extern "C" {
 
+size_t vsa_fwd_prompt_workspace_bytes(int packed, int B, int Hq, int Hkv, int Sq, int Sk) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Sq < 1 || Sk < 0) return 0;
+  const long long items = fwd_items(packed, B, Hq, Hkv, Sq);
+  const int n = key_splits(items, Sk);
+  return n > 1 ? (size_t)(items * n) * prompt::fwd::kPartFloats * sizeof(float) : 0;
+}
+
 vsa_status vsa_fwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* v,
                           const int64_t* strides, const int32_t* q_seq, const int32_t* k_seq,
                           int packed, int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal,
-                          float scale, vsa_bf16* out, float* lse, vsa_stream_t stream) {
+                          float scale, vsa_bf16* out, float* lse, void* workspace,
+                          size_t workspace_bytes, vsa_stream_t stream) {
   host_set_launches(0);
   const Shape p{q_seq, k_seq, packed, B, Hq, Hkv, Sq, Sk, D, causal, scale};
   vsa_status st = check_shape(p);
@@ -215,6 +241,20 @@ vsa_status vsa_fwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
   if (slots * a.n_packs > INT_MAX) return VSA_ERR_UNSUPPORTED;
   a.n_slots = (int)slots;
   a.n_items = (int)(slots * a.n_packs);
+  a.splits = 1;
+  if (workspace != nullptr) {
+    const size_t need = vsa_fwd_prompt_workspace_bytes(packed, B, Hq, Hkv, Sq, Sk);
+    if (!host_aligned16(workspace) || workspace_bytes < need) return VSA_ERR_INVALID_ARG;
+    const long long n = (long long)need;
+    for (const View* x : {&vq, &vk, &vv, &vo})
+      if (meets(*x, workspace, n)) return VSA_ERR_INVALID_ARG;
+    const uintptr_t w0 = reinterpret_cast<uintptr_t>(workspace), l0 = reinterpret_cast<uintptr_t>(lse);
+    if (meets_seq(p, workspace, n) ||
+        (lse && w0 < l0 + (uintptr_t)lse_bytes && l0 < w0 + (uintptr_t)n))
+      return VSA_ERR_INVALID_ARG;
+    a.splits = key_splits(a.n_items, Sk);
+    a.part = static_cast<float*>(workspace);
+  }
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_ns = host_wait_ns(prompt::kWaitLimitNs);
   a.stall = host_stall();
@@ -232,10 +272,13 @@ vsa_status vsa_fwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
   if (!make_map(&tq, vq, 128 >> a.pack, 1 << a.pack) || !make_map(&tk, vk.empty() ? vq : vk, 128, 1) ||
       !make_map(&tv, vv.empty() ? vq : vv, 128, 1))
     return VSA_ERR_CUDA;
-  prompt::fwd::prompt_fwd_kernel<<<(unsigned)a.n_items, prompt::fwd::kThreads, prompt::fwd::kSmemBytes,
-                                   reinterpret_cast<cudaStream_t>(stream)>>>(tq, tk, tv, a);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  prompt::fwd::prompt_fwd_kernel<<<(unsigned)(a.n_items * a.splits), prompt::fwd::kThreads,
+                                   prompt::fwd::kSmemBytes, s>>>(tq, tk, tv, a);
+  if (a.splits > 1)
+    prompt::fwd::prompt_join_kernel<<<(unsigned)(a.n_items * 32), 256, 0, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
-  host_set_launches(1);
+  host_set_launches(a.splits > 1 ? 2 : 1);
   return VSA_OK;
 }
 

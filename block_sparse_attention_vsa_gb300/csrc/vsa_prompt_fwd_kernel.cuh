@@ -48,6 +48,8 @@ struct FwdArgs {
   int Hq, group, pack;  // query heads a key/value head; log2 of the heads in a tile
   int n_packs, n_slots;  // head packs, item slots
   int n_items;
+  int splits;       // ranges of an item's key tiles, a unit of work each
+  float* part;      // [n_items * splits] partial results, if there are several
   float scale_log2;
   unsigned long long wait_ns;
   int stall;
@@ -73,8 +75,11 @@ struct Item {
   int tok, q0, nq;        // first token, first row and number of queries of the sequence
   int k0, nk;
   int n0, n1;             // key tiles of the two query tiles
+  int unit;
   int go;
 };
+// A unit's partial result: O [256][128] relative to the row's m, then m [256] and l [256].
+constexpr int kPartFloats = 256 * 128 + 512;
 
 struct Ctl {
   uint64_t item_full[2], item_empty[2];
@@ -94,7 +99,7 @@ struct Ctl {
 static_assert(sizeof(Ctl) <= 1024, "control block");
 
 // Items in the order of their size for one sequence: the last tokens first, heads inside.
-__device__ __forceinline__ bool decode(const FwdArgs& a, int id, Item& it) {
+__device__ __forceinline__ bool decode_item(const FwdArgs& a, int id, Item& it) {
   const int T = 256 >> a.pack, half = 128 >> a.pack;
   const int slot = id / a.n_packs;
   const int hp = id - slot * a.n_packs;
@@ -126,6 +131,22 @@ __device__ __forceinline__ bool decode(const FwdArgs& a, int id, Item& it) {
   it.n0 = key_tiles(it.tok);
   it.n1 = key_tiles(it.tok + half);
   return a.seq.packed ? tile >= 0 && it.tok < s.nq : true;
+}
+// A unit: an item, or a range of its key tiles -- the item of a sequence whose keys begin with
+// the range's first (a query attends keys up to its distance from the end, so nothing else
+// changes).
+__device__ __forceinline__ bool decode(const FwdArgs& a, int id, Item& it) {
+  it.unit = id;
+  if (a.splits == 1) return decode_item(a, id, it);
+  const int item = id / a.splits, s = id - item * a.splits;
+  if (!decode_item(a, item, it)) return false;
+  const int n = it.n0 > it.n1 ? it.n0 : it.n1;
+  const int lo = (int)((long long)n * s / a.splits), hi = (int)((long long)n * (s + 1) / a.splits);
+  it.k0 += 128 * lo;
+  it.nk = it.nk > 128 * lo ? it.nk - 128 * lo : 0;
+  it.n0 = clampi(it.n0 - lo, 0, hi - lo);
+  it.n1 = clampi(it.n1 - lo, 0, hi - lo);
+  return true;
 }
 
 // The items of a CTA (by a whole warp): its own, and then those of CTAs not yet launched, in
@@ -467,6 +488,28 @@ __device__ __forceinline__ void softmax_role(const FwdArgs& a, uint8_t* smem, Ct
     const Item it = ctl->item[buf];
     __syncwarp();
     if (lane_id() == 0) mbar_arrive(&ctl->item_empty[buf]);
+    if (a.splits > 1) {
+      float* part = a.part + (long long)it.unit * kPartFloats;
+      const int at = 128 * t + row;
+      part[256 * 128 + at] = m;
+      part[256 * 128 + 256 + at] = l;
+#pragma unroll 1
+      for (int c = 0; c < 4 && n > 0; ++c) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(tO + 32 * c, o);
+        tmem_wait_ld();
+        if (c == 3) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane_id() == 0) mbar_arrive(&ctl->o_empty[t]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          reinterpret_cast<uint4*>(part + at * 128 + 32 * c)[e] =
+              make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+      }
+      continue;
+    }
     const int n_rows = a.seq.packed ? it.nq : a.seq.Sq;  // tokens that are written
     const int tok = it.tok + t * half + (row & (half - 1));
     const int head = it.head0 + (row >> (7 - a.pack));
@@ -588,6 +631,56 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the ranges of split items, a warp a row: with M = max m_s and c_s = 2^(m_s - M), out =
+// sum c_s O_s / sum c_s l_s and lse = M + log2 sum c_s l_s, in the order of the ranges.
+__global__ void __launch_bounds__(256) prompt_join_kernel(const FwdArgs a) {
+  const int item = (int)(blockIdx.x >> 5);
+  const int at = (int)((blockIdx.x & 31) * 8 + (threadIdx.x >> 5)), t = at >> 7, row = at & 127;
+  const int lane = (int)lane_id();
+  Item it;
+  if (!decode_item(a, item, it)) return;
+  const int half = 128 >> a.pack;
+  const int tok = it.tok + t * half + (row & (half - 1));
+  const int head = it.head0 + (row >> (7 - a.pack));
+  if (tok >= (a.seq.packed ? it.nq : a.seq.Sq)) return;
+  int lim = a.seq.causal ? clampi(tok + 1 + it.nk - it.nq, 0, it.nk) : it.nk;
+  if (tok >= it.nq) lim = 0;
+  const float* part = a.part + (long long)item * a.splits * kPartFloats;
+  float m = -INFINITY, l = 0.0f;
+  if (lane < a.splits) {
+    m = part[(long long)lane * kPartFloats + 256 * 128 + at];
+    l = part[(long long)lane * kPartFloats + 256 * 128 + 256 + at];
+  }
+  float top = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  // (a range that the row attends nothing of has l = 0, and its O may not have been written; a
+  // sum that is no number stays one)
+  const float c = l != l ? 1.0f : (l == 0.0f ? 0.0f : fast_exp2(m - top));
+  float sum = 0.0f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < a.splits; ++s) {
+    const float cs = __shfl_sync(0xffffffffu, c, s), ls = __shfl_sync(0xffffffffu, l, s);
+    if (cs == 0.0f) continue;
+    const float4 o = reinterpret_cast<const float4*>(part + (long long)s * kPartFloats +
+                                                     at * 128)[lane];
+    sum = fmaf(cs, ls, sum);
+    acc.x = fmaf(cs, o.x, acc.x);
+    acc.y = fmaf(cs, o.y, acc.y);
+    acc.z = fmaf(cs, o.z, acc.z);
+    acc.w = fmaf(cs, o.w, acc.w);
+  }
+  const bool some = lim > 0;
+  const float inv = 1.0f / sum;
+  uint2 x = make_uint2(0u, 0u);
+  if (some) x = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  reinterpret_cast<uint2*>(a.out + it.z * a.out_b + head * a.out_h +
+                           (long long)(it.q0 + tok) * a.out_t)[lane] = x;
+  if (lane == 0 && a.lse != nullptr)
+    a.lse[((long long)it.z * a.Hq + head) * a.seq.Sq + it.q0 + tok] =
+        some ? (sum > 0.0f ? top + log2f(sum) : __int_as_float(0x7fffffff)) : kLseEmpty;
 }
 
 }  // namespace fwd

@@ -38,6 +38,7 @@ struct Entry {
   decltype(&vsa_cache_fork) cache_fork;
   decltype(&vsa_cache_compact) cache_compact;
   decltype(&vsa_fwd_prompt) fwd_prompt;
+  decltype(&vsa_fwd_prompt_workspace_bytes) fwd_prompt_workspace_bytes;
   decltype(&vsa_bwd_prompt) bwd_prompt;
   decltype(&vsa_bwd_prompt_workspace_bytes) bwd_prompt_workspace_bytes;
 } lib;
@@ -563,9 +564,9 @@ struct Prompt {
   }
 };
 
-// (q, k, v, q_seq, k_seq, causal, scale, out, lse)
+// (q, k, v, q_seq, k_seq, causal, scale, out, lse, workspace)
 PyObject* fwd_prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return run(n, 9, [&]() -> PyObject* {
+  return run(n, 10, [&]() -> PyObject* {
     const Prompt p(a[0], a[1], a[2], a[3], a[4]);
     const bool causal = truth(a[5]);
     const float scale =
@@ -584,6 +585,19 @@ PyObject* fwd_prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
       lp = p.lse(a[8]);
       lse_given = a[8];
     }
+    at::Tensor ws;
+    void* wp = nullptr;
+    size_t bytes = 0;
+    if (a[9] == Py_None) {
+      bytes = lib.fwd_prompt_workspace_bytes(p.packed, (int)p.B, (int)p.Hq, (int)p.Hkv, (int)p.Sq,
+                                             (int)p.Sk);
+      if (bytes > 0) ws = empty(p.q, at::kByte, {(int64_t)bytes});
+    } else if (a[9] != Py_False) {
+      ws = tensor(a[9]);
+      if (!ws.is_cuda() || ws.get_device() != p.dev.index || !ws.is_contiguous()) throw LongWay();
+      bytes = ws.nbytes();
+    }
+    if (ws.defined()) wp = ws.data_ptr();
     int64_t s[12];
     p.strides(p.q, s);
     p.strides(p.k, s + 3);
@@ -596,7 +610,7 @@ PyObject* fwd_prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const vsa_status st = unlocked([&] {
       return lib.fwd_prompt(qp, kp, vp, s, p.q_seq, p.k_seq, p.packed, (int)p.B, (int)p.Hq,
                             (int)p.Hkv, (int)p.Sq, (int)p.Sk, VSA_HEAD_DIM, causal, scale, op, lp,
-                            stream);
+                            wp, bytes, stream);
     });
     if (st != VSA_OK) return PyLong_FromLong(st);
     return tuple({a[7] == Py_None ? THPVariable_Wrap(out) : same(a[7]),
@@ -666,6 +680,7 @@ PyObject* bind(PyObject*, PyObject* arg) {
       !find(lib.cache_fork, "vsa_cache_fork") ||
       !find(lib.cache_compact, "vsa_cache_compact") ||
       !find(lib.fwd_prompt, "vsa_fwd_prompt") || !find(lib.bwd_prompt, "vsa_bwd_prompt") ||
+      !find(lib.fwd_prompt_workspace_bytes, "vsa_fwd_prompt_workspace_bytes") ||
       !find(lib.bwd_prompt_workspace_bytes, "vsa_bwd_prompt_workspace_bytes")) {
     PyErr_SetString(PyExc_RuntimeError, "the library lacks an entry point");
     return nullptr;

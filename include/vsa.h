@@ -541,13 +541,23 @@ VSA_API vsa_status vsa_cache_compact(int32_t *table, int B, int Hkv, int D, int 
  *   strides int64 [12]: (batch, head, token) of q, k, v, out.
  *   scale   natural-exp softmax scale (finite, > 0).
  *   lse     [Hq, Sq] (packed) or [B, Hq, Sq] fp32, base 2, contiguous, or NULL.
+ *   workspace  vsa_fwd_prompt_workspace_bytes() bytes or more, 16-byte aligned, no
+ *           initialisation needed; calls sharing it must not overlap on the GPU.  Where there
+ *           are too few queries to keep the GPU busy, the keys are cut into ranges whose
+ *           results meet there.  NULL: they are not cut (slower for few queries against many
+ *           keys, and other roundings).
  * A row that attends nothing gets out = +0 and lse = VSA_LSE_EMPTY; one whose scores are no
- * numbers, or all -infinity, gets NaN.  Needs no workspace.  One kernel. */
+ * numbers, or all -infinity, gets NaN.  Results do not depend on timing.  One kernel, or two
+ * where keys are cut. */
 VSA_API vsa_status vsa_fwd_prompt(const vsa_bf16 *q, const vsa_bf16 *k, const vsa_bf16 *v,
                                   const int64_t *strides, const int32_t *q_seq,
                                   const int32_t *k_seq, int packed, int B, int Hq, int Hkv, int Sq,
                                   int Sk, int D, int causal, float scale, vsa_bf16 *out,
-                                  float *lse, vsa_stream_t stream);
+                                  float *lse, void *workspace, size_t workspace_bytes,
+                                  vsa_stream_t stream);
+
+/* Workspace bytes vsa_fwd_prompt cuts keys with: 0 where it does not (or for an invalid shape). */
+VSA_API size_t vsa_fwd_prompt_workspace_bytes(int packed, int B, int Hq, int Hkv, int Sq, int Sk);
 
 /* Gradient: dq, dk, dv of vsa_fwd_prompt for an upstream gradient dout.  With p, lse of the
  * forward, D_i = dout_i . out_i and ds_ij = p_ij (dout_i . v_j - D_i):

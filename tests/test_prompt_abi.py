@@ -39,11 +39,12 @@ def strides(values):
 def fwd(lib, **kw):
     a = dict(q=64 * MB, k=96 * MB, v=128 * MB, s=rows(4) + 2 * rows(2) + rows(4), qs=1 * MB,
              ks=2 * MB, packed=1, B=2, Hq=4, Hkv=2, Sq=200, Sk=300, D=D, causal=1, scale=0.1,
-             out=160 * MB, lse=3 * MB)
+             out=160 * MB, lse=3 * MB, ws=0, n=0)
     a.update(kw)
     return lib.vsa_fwd_prompt(p(a["q"]), p(a["k"]), p(a["v"]), strides(a["s"]), p(a["qs"]),
                               p(a["ks"]), a["packed"], a["B"], a["Hq"], a["Hkv"], a["Sq"], a["Sk"],
-                              a["D"], a["causal"], a["scale"], p(a["out"]), p(a["lse"]), None)
+                              a["D"], a["causal"], a["scale"], p(a["out"]), p(a["lse"]), p(a["ws"]),
+                              a["n"], None)
 
 
 def with_strides(i, values, base=rows(4) + 2 * rows(2) + rows(4)):
@@ -66,7 +67,10 @@ def with_strides(i, values, base=rows(4) + 2 * rows(2) + rows(4)):
     (dict(out=64 * MB), INVALID), (dict(out=96 * MB), INVALID), (dict(out=128 * MB + 256), INVALID),
     (dict(lse=160 * MB), INVALID), (dict(lse=1 * MB), INVALID), (dict(lse=64 * MB), INVALID), (dict(out=1 * MB), INVALID),
     (dict(Sq=(1 << 31) - 1), UNSUPPORTED), (dict(B=0), OK), (dict(Sq=0), OK), (dict(Hq=0), OK),
-    (dict(packed=0, k=0), INVALID),
+    (dict(packed=0, k=0), INVALID), (dict(ws=4 * MB, n=1000, Sk=5000), INVALID),
+    (dict(ws=4 * MB + 8, n=1 << 30), INVALID), (dict(ws=64 * MB, n=1 << 30, Sk=5000), INVALID),
+    (dict(ws=4 * MB, n=1 << 30, Sk=5000, lse=4 * MB + 64), INVALID),
+    (dict(ws=4 * MB, n=1 << 30, Sk=5000, qs=4 * MB + 64), INVALID),
 ])
 def test_fwd_prompt_checks(lib, kw, code):
     assert fwd(lib, **kw) == code
@@ -118,6 +122,17 @@ def bwd(lib, **kw):
 ])
 def test_bwd_prompt_checks(lib, kw, code):
     assert bwd(lib, **kw) == code
+
+
+def test_fwd_prompt_workspace(lib):
+    f = lib.vsa_fwd_prompt_workspace_bytes
+    unit = (256 * 128 + 512) * 4
+    # 2 heads of 128 tokens an item: (200 // 128 + 2) * 2 items, 25 of 152 SMs each; 20 key tiles, 4 a range
+    assert f(1, 2, 4, 2, 200, 2500) == 6 * 5 * unit
+    assert f(1, 2, 4, 2, 200, 1000) == 6 * 2 * unit
+    assert f(1, 2, 4, 2, 200, 800) == 0 and f(1, 2, 4, 2, 20000, 20000) == 0
+    assert f(0, 1, 1, 1, 1, 1 << 20) == 32 * unit
+    assert f(1, 2, 5, 2, 200, 2500) == 0 and f(1, 0, 4, 2, 200, 2500) == 0
 
 
 def test_bwd_prompt_workspace(lib):

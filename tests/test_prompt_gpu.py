@@ -180,15 +180,15 @@ def test_layouts_agree():
         assert torch.equal(t, want[n]), n
     # padded, as views of [B, S, H, D], into views of one buffer
     v4 = [x[:, :, s].transpose(1, 2) for s in sl]
+    want = both(*(t.contiguous() for t in v4), dout.transpose(1, 2).contiguous())
     z = torch.empty_like(x)
     z4 = [z[:, :, s].transpose(1, 2) for s in sl]
     o4, l4 = binding.vsa_fwd_prompt(*v4)
     binding.vsa_bwd_prompt(*v4, o4, dout.transpose(1, 2), l4, dq=z4[0], dk=z4[1], dv=z4[2])
     ok()
-    assert torch.equal(o4.transpose(1, 2).flatten(0, 1), want["out"])
-    assert torch.equal(l4.transpose(0, 1).flatten(1), want["lse"])
+    assert torch.equal(o4, want["out"]) and torch.equal(l4, want["lse"])
     for t, n in zip(z4, ("dq", "dk", "dv")):
-        assert torch.equal(t.transpose(1, 2).flatten(0, 1), want[n]), n
+        assert torch.equal(t, want[n]), n
 
 
 @pytest.mark.parametrize("mul", [0.0, 4.0, 20.0], ids=["flat", "peaky", "one-hot"])
@@ -256,6 +256,42 @@ def test_long_sequences_by_rows():
                                 v[a:a + i + 1, h // 2].double(), True, 1.0 / math.sqrt(D))
                 assert ((out[a + i, h].double() - r["out"][0]).abs() <= b["out"][0]).all()
                 assert (lse[h, a + i].double() - r["lse"][0]).abs() <= b["lse"][0]
+
+
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("nq,nk,Hq,Hkv", [([1], [5000], 1, 1), ([3, 1], [2000, 129], 8, 2),
+                                          ([70], [4100], 4, 4), ([300], [40], 2, 2),
+                                          ([2, 5, 0], [1700, 0, 300], 6, 1)], ids=str)
+def test_few_queries_against_many_keys(nq, nk, Hq, Hkv, causal):
+    """Keys cut into ranges: within the bounds, and near the uncut result."""
+    g = gen(sum(nk))
+    q, k, v = randn((sum(nq), Hq, D), g), randn((sum(nk), Hkv, D), g), randn((sum(nk), Hkv, D), g)
+    aq, ak = i32(starts(nq)), i32(starts(nk))
+    assert binding.fwd_prompt_workspace_bytes(True, len(nq), Hq, Hkv, sum(nq), sum(nk)) > 0 \
+        or nk == [40]
+    out, lse = binding.vsa_fwd_prompt(q, k, v, aq, ak, causal=causal)
+    ok()
+    x = [t.transpose(0, 1) for t in (q, k, v)]
+    want, bound = ref.attend(*x, nq, nk, starts(nq), starts(nk), causal)
+    hold(dict(out=out.transpose(0, 1), lse=lse), want, bound)
+    whole, l2 = binding.vsa_fwd_prompt(q, k, v, aq, ak, causal=causal, workspace=False)
+    ok()
+    hold(dict(out=whole.transpose(0, 1), lse=l2), want, bound)
+
+
+def test_few_queries_scores_that_are_no_numbers():
+    g = gen(26)
+    q, k, v = randn((3, 1, D), g), randn((3000, 1, D), g), randn((3000, 1, D), g)
+    k[100] = math.nan                  # every query sees it
+    out, lse = binding.vsa_fwd_prompt(q, k, v, i32([0, 3]), i32([0, 3000]))
+    assert out.isnan().all() and lse.isnan().all()
+    k[100] = 0.0
+    k[:, :, 0] = 1.0
+    q[1], q[1, 0, 0] = 0.0, -math.inf  # all of one row's scores are -infinity
+    out, lse = binding.vsa_fwd_prompt(q, k, v, i32([0, 3]), i32([0, 3000]))
+    ok()
+    assert out[1].isnan().all() and lse[0, 1].isnan()
+    assert out[[0, 2]].isfinite().all() and lse[0, [0, 2]].isfinite().all()
 
 
 def test_results_do_not_depend_on_timing():
