@@ -18,6 +18,10 @@ constexpr int kSms = 152;  // of a GB300, which host_device() asks for
 
 bool block_ok(int block) { return block == 64 || block == 128; }
 
+// CTAs that divide so many table entries among them, one cluster: one where its barriers would
+// take longer than the entries.
+int pages_ctas(long long entries) { return entries <= (1 << 17) ? 1 : kPagesCluster; }
+
 size_t words(int pages) { return ((size_t)pages + 31) / 32; }
 
 // The cache's buffers as ranges.
@@ -93,8 +97,9 @@ vsa_status vsa_pages_reserve(int32_t* table, const int32_t* lens, const int32_t*
   if (st != VSA_OK) return st;
   const ReserveArgs a{{refs, free_bits, pages}, table, lens, n_new, lacking, B, Hkv, max_blocks,
                       block};
-  return launch(pages_reserve_kernel, dim3(kPagesCluster), kPagesThreads, 0,
-                reinterpret_cast<cudaStream_t>(stream), 0, a);
+  const int ctas = pages_ctas(entries);
+  return launch(pages_reserve_kernel, dim3(ctas), kPagesThreads, 0,
+                reinterpret_cast<cudaStream_t>(stream), ctas, a);
 }
 
 vsa_status vsa_cache_fork(const int32_t* table, const int32_t* lens, const int32_t* parent, int B,
@@ -137,7 +142,8 @@ vsa_status vsa_cache_fork(const int32_t* table, const int32_t* lens, const int32
                    table, lens, parent, table_out, lens_out, lacking, B, N, Hkv,
                    max_blocks, block};
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  st = launch(pages_fork_kernel, dim3(kPagesCluster), kPagesThreads, 0, s, 0, a);
+  const int ctas = pages_ctas(32 * rows);  // (a row's look-ups and its page: some 32 entries)
+  st = launch(pages_fork_kernel, dim3(ctas), kPagesThreads, 0, s, ctas, a);
   if (st != VSA_OK || entries == 0) return st;
   st = launch(cache_fork_kernel, dim3((unsigned)rows), 256, 0, s, 0, a);
   if (st == VSA_OK) host_set_launches(2);
@@ -175,11 +181,13 @@ vsa_status vsa_cache_compact(int32_t* table, int B, int Hkv, int D, int max_bloc
   const CompactArgs a{{refs, free_bits, pages}, {k_cache, v_cache, k_scale, v_scale, k_mean},
                       table, to, n_used, entries, block};
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  st = launch(pages_compact_kernel, dim3(kPagesCluster), kPagesThreads, 0, s, 0, a);
+  // a CTA a thousand pages, one wave at most
+  const int ctas = pages < kSms * kPagesThreads ? (pages + kPagesThreads - 1) / kPagesThreads : kSms;
+  st = launch(pages_compact_kernel, dim3(ctas < 1 ? 1 : ctas), kPagesThreads, 0, s, 0, a);
   if (st != VSA_OK || (pages == 0 && entries == 0)) return st;
-  long long ctas = (entries + 255) / 256;
-  if (pages > ctas) ctas = pages;
-  st = launch(cache_compact_kernel, dim3((unsigned)(ctas < 8 * kSms ? ctas : 8 * kSms)), 256, 0, s,
+  long long most = (entries + 255) / 256;
+  if (pages > most) most = pages;
+  st = launch(cache_compact_kernel, dim3((unsigned)(most < 8 * kSms ? most : 8 * kSms)), 256, 0, s,
               0, a);
   if (st == VSA_OK) host_set_launches(2);
   return st;

@@ -5,8 +5,9 @@
 // none names.  Taking always the lowest free page makes every outcome unique: counts change by
 // integer atomics, whose order does not matter, and the r-th page asked for is the r-th set bit
 // of the bitmap, found by counting.  A whole pool's bitmap is small (a pool of 100,000 pages:
-// 12.5 KB), so every CTA of one cluster counts all of it for itself, and only the rows of the
-// tables are divided among them.
+// 12.5 KB), so every CTA counts all of it for itself, and only the rows of the tables (or the
+// pages) are divided among them.  Where the bitmap is changed as well the CTAs are one cluster,
+// whose barrier tells that all have read it.
 //
 // Launched with programmatic serialization, like the other serving kernels: everything is read
 // by ordinary loads behind the wait for the predecessor.
@@ -23,7 +24,8 @@ namespace vsa {
 
 constexpr int kPagesThreads = 1024;  // of a CTA that counts
 constexpr int kPagesCluster = 8;
-constexpr int kPagesWarps = kPagesCluster * (kPagesThreads / 32);
+constexpr int kEntries = 8;  // table entries a lane has under way at a time
+constexpr int kFew = 4;      // blocks of a row that one lane looks after
 
 struct Pool {
   int32_t* refs;
@@ -105,6 +107,7 @@ __device__ __forceinline__ FreeCount count_free(const Pool& p, int* s_before, in
   f.per = (int)((f.words + kPagesThreads - 1) / kPagesThreads);
   const long long w0 = (long long)threadIdx.x * f.per;
   int n = 0;
+#pragma unroll 4
   for (int i = 0; i < f.per; ++i)
     if (w0 + i < f.words) n += __popc(free_word(p, w0 + i));
   s_before[threadIdx.x] = block_before(n, s_warp, &f.total);
@@ -127,10 +130,69 @@ __device__ __forceinline__ int nth_free(const Pool& p, const FreeCount& f, int r
   }
   return -1;
 }
+// Consecutive free pages for a warp: 32 words of the bitmap, one a lane.
+struct FreeWindow {
+  const Pool& p;
+  const FreeCount& f;
+  long long w0 = 0;   // first word
+  uint32_t word = 0;
+  int base = 0, upto = 0;  // free pages before the window; before it and up to the lane's word
+  int end = 0;             // before it and in it
+
+  __device__ __forceinline__ void load() {
+    const long long w = w0 + (int)(threadIdx.x & 31);
+    word = w < f.words ? free_word(p, w) : 0u;
+    upto = __popc(word);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if ((int)(threadIdx.x & 31) >= o) upto += y;
+    }
+    upto += base;
+    end = __shfl_sync(0xffffffffu, upto, 31);
+  }
+  // places the window on the r-th free page's thread
+  __device__ __forceinline__ void seek(int r) {
+    int lo = 0;
+#pragma unroll
+    for (int s = kPagesThreads / 2; s > 0; s >>= 1)
+      if (f.before[lo + s] <= r) lo += s;
+    w0 = (long long)lo * f.per;
+    base = f.before[lo];
+    load();
+  }
+  // The r-th free page for the lanes that want one (ranks ascend with the lane and from call
+  // to call); -1 where there are not as many.
+  __device__ __forceinline__ int get(bool want, int r) {
+    int page = -1;
+    bool open = want && r < f.total;
+    while (true) {
+      const bool here = open && r < end;
+      // the word that holds it: the first whose count passes r
+      int at = 0;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1)
+        if (__shfl_sync(0xffffffffu, upto, at + s - 1) <= r) at += s;
+      at &= 31;
+      const uint32_t x = __shfl_sync(0xffffffffu, word, at);
+      const int before = __shfl_sync(0xffffffffu, upto, at) - __popc(x);
+      if (here) {
+        page = (int)((w0 + at) * 32) + nth_bit(x, r - before);
+        open = false;
+      }
+      if (!__any_sync(0xffffffffu, open) || w0 + 32 >= f.words) return page;
+      w0 += 32;
+      base = end;
+      load();
+    }
+  }
+};
+
 // The first n free pages are free no more (by all CTAs of the cluster, a share each, once
 // every one has read the bitmap for the last time).
-__device__ __forceinline__ void clear_first(const Pool& p, const FreeCount& f, int n, int rank) {
-  if ((int)(threadIdx.x % kPagesCluster) != rank) return;
+__device__ __forceinline__ void clear_first(const Pool& p, const FreeCount& f, int n, int rank,
+                                            int ctas) {
+  if ((int)threadIdx.x % ctas != rank) return;
   int left = n - f.before[threadIdx.x];
   const long long w0 = (long long)threadIdx.x * f.per;
   for (int i = 0; i < f.per && left > 0; ++i) {
@@ -193,15 +255,16 @@ struct PagesShared {
   int warp[33];
   int asked;
 };
-// Pages asked for by the CTAs before this one; *all of them.  (One cluster barrier.)
+// Pages asked for by the CTAs before this one; *all of them.  (A barrier of a cluster of several.)
 __device__ __forceinline__ int cluster_before(PagesShared& s, int asked, int* all) {
   auto cluster = cooperative_groups::this_cluster();
+  *all = asked;
+  if (cluster.num_blocks() == 1) return 0;
   if (threadIdx.x == 0) s.asked = asked;
   cluster.sync();
   const int rank = (int)cluster.block_rank();
   int before = 0, sum = 0;
-#pragma unroll
-  for (int c = 0; c < kPagesCluster; ++c) {
+  for (int c = 0; c < (int)cluster.num_blocks(); ++c) {
     const int n = *cluster.map_shared_rank(&s.asked, c);
     if (c < rank) before += n;
     sum += n;
@@ -210,63 +273,163 @@ __device__ __forceinline__ int cluster_before(PagesShared& s, int asked, int* al
   return before;
 }
 
-__global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesThreads)
-    pages_reserve_kernel(const ReserveArgs a) {
+// The rows are divided among the cluster's warps in order.  A warp looks up 32 rows' ranges at a
+// time, a lane each; short ranges (a token each) stay with the lane, of long ones (a prompt) the
+// warp takes one after another, several entries a lane under way.
+__global__ void __launch_bounds__(kPagesThreads) pages_reserve_kernel(const ReserveArgs a) {
   __shared__ PagesShared s;
   auto cluster = cooperative_groups::this_cluster();
-  const int rank = (int)cluster.block_rank();
-  const int lane = (int)threadIdx.x & 31, warp = rank * (kPagesThreads / 32) + ((int)threadIdx.x >> 5);
-  const long long rows = (long long)a.B * a.Hkv;
-  const long long r0 = rows * warp / kPagesWarps, r1 = rows * (warp + 1) / kPagesWarps;
+  const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+  const int lane = (int)threadIdx.x & 31;
+  const unsigned warps = ctas * (kPagesThreads / 32),
+                 warp = rank * (kPagesThreads / 32) + (threadIdx.x >> 5);
+  // few rows are cut into parts, so that all warps have some
+  const unsigned heads = a.Hkv, whole = a.B * heads;
+  const unsigned parts = 2 * warps > whole && a.max_blocks > 32 ? 2 * warps / whole : 1;
+  const unsigned rows = whole * parts;
+  const unsigned r0 = (unsigned)((unsigned long long)rows * warp / warps),
+                 r1 = (unsigned)((unsigned long long)rows * (warp + 1) / warps);
   after_predecessor();
-  for (int b = rank * kPagesThreads + (int)threadIdx.x; b < a.B; b += kPagesCluster * kPagesThreads)
+  for (int b = rank * kPagesThreads + (int)threadIdx.x; b < a.B; b += ctas * kPagesThreads)
     a.lacking[b] = 0;
-  // blocks [first, last) of a row hold tokens to come
-  auto range = [&](long long row, int* first, int* last) {
-    const int b = (int)(row / a.Hkv);
-    const long long len = read_global(a.lens + b) > 0 ? read_global(a.lens + b) : 0;
-    long long more = 1;
-    if (a.n_new != nullptr) more = read_global(a.n_new + b) > 0 ? read_global(a.n_new + b) : 0;
-    *first = (int)(len / a.block < a.max_blocks ? len / a.block : a.max_blocks);
-    *last = blocks_of(len + more, a.block, a.max_blocks);
-    return b;
+  struct Range {
+    int first, last, b;  // blocks [first, last) of the part hold tokens to come
+    int32_t* row;
   };
-  auto wanted = [&](long long row, int j, int last) {
-    return j < last && !is_page(read_global(a.table + row * a.max_blocks + j), a.pool.pages);
+  auto range = [&](unsigned part) {
+    Range x{0, 0, 0, a.table};
+    if (part >= r1) return x;
+    const unsigned row = part / parts;
+    x.b = (int)(row / heads);
+    x.row = a.table + (size_t)row * a.max_blocks;
+    const int held = read_global(a.lens + x.b);
+    const int more = a.n_new != nullptr ? read_global(a.n_new + x.b) : 1;
+    const long long len = held > 0 ? held : 0;
+    // (blocks are of 64 or 128 tokens)
+    const int shift = a.block == 64 ? 6 : 7;
+    x.first = (int)(len >> shift) < a.max_blocks ? (int)(len >> shift) : a.max_blocks;
+    const long long end = (len + (more > 0 ? more : 0) + a.block - 1) >> shift;
+    x.last = end < a.max_blocks ? (int)end : a.max_blocks;
+    if (parts > 1) {
+      const unsigned n = x.last - x.first, q = part - row * parts;
+      x.last = x.first + (int)((unsigned long long)n * (q + 1) / parts);
+      x.first += (int)((unsigned long long)n * q / parts);
+    }
+    return x;
+  };
+  auto of_lane = [&](const Range& x, int k) {
+    Range y;
+    y.first = __shfl_sync(0xffffffffu, x.first, k);
+    y.last = __shfl_sync(0xffffffffu, x.last, k);
+    y.b = __shfl_sync(0xffffffffu, x.b, k);
+    y.row = reinterpret_cast<int32_t*>(
+        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x.row), k));
+    return y;
+  };
+  // the lane's entries j, j + 32, .. that want a page (of a range that is not empty)
+  auto batch = [&](const Range& x, int j, bool (&want)[kEntries]) {
+    int v[kEntries];
+#pragma unroll
+    for (int i = 0; i < kEntries; ++i)
+      v[i] = read_global(x.row + (j + 32 * i < x.last ? j + 32 * i : x.first));
+#pragma unroll
+    for (int i = 0; i < kEntries; ++i)
+      want[i] = j + 32 * i < x.last && !is_page(v[i], a.pool.pages);
+  };
+  // a short range, as a mask
+  auto few = [&](const Range& x) {
+    uint32_t mask = 0;
+    if (x.first < x.last) {
+      int v[kFew];
+#pragma unroll
+      for (int i = 0; i < kFew; ++i)
+        v[i] = read_global(x.row + (x.first + i < x.last ? x.first + i : x.first));
+#pragma unroll
+      for (int i = 0; i < kFew; ++i)
+        mask |= x.first + i < x.last && !is_page(v[i], a.pool.pages) ? 1u << i : 0u;
+    }
+    return mask;
   };
   int asked = 0;
-  for (long long row = r0; row < r1; ++row) {
-    int first, last;
-    range(row, &first, &last);
-    for (int j = first; j < last; j += 32)
-      asked += __popc(__ballot_sync(0xffffffffu, wanted(row, j + lane, last)));
+  Range x{0, 0, 0, a.table};
+  uint32_t mask = 0;
+  for (unsigned rb = r0; rb < r1; rb += 32) {
+    x = range(rb + lane);
+    if (__all_sync(0xffffffffu, x.last - x.first <= kFew)) {
+      mask = few(x);
+      asked += (int)__reduce_add_sync(0xffffffffu, (unsigned)__popc(mask));
+      continue;
+    }
+    for (unsigned k = 0; k < 32 && rb + k < r1; ++k) {
+      const Range y = of_lane(x, (int)k);
+      for (int j = y.first + lane; j - lane < y.last; j += 32 * kEntries) {
+        bool want[kEntries];
+        batch(y, j, want);
+#pragma unroll
+        for (int i = 0; i < kEntries; ++i) asked += __popc(__ballot_sync(0xffffffffu, want[i]));
+      }
+    }
   }
   const FreeCount f = count_free(a.pool, s.before, s.warp);
   int in_cta, all;
   int at = block_before(lane == 0 ? asked : 0, s.warp, &in_cta);
   at = __shfl_sync(0xffffffffu, at, 0);
   at += cluster_before(s, in_cta, &all);
-  if (asked > 0)
-    for (long long row = r0; row < r1; ++row) {
-      int first, last;
-      const int b = range(row, &first, &last);
-      for (int j = first; j < last; j += 32) {
-        const bool want = wanted(row, j + lane, last);
-        const uint32_t votes = __ballot_sync(0xffffffffu, want);
-        const int r = at + __popc(votes & ((1u << lane) - 1u));
-        at += __popc(votes);
-        int p = -1;
-        if (want) {
-          if (r < f.total) p = nth_free(a.pool, f, r);
-          if (p >= 0) a.pool.refs[p] = 1;
-          a.table[row * a.max_blocks + j + lane] = p;
+  if (asked > 0) {
+    FreeWindow window{a.pool, f};
+    for (unsigned rb = r0; rb < r1; rb += 32) {
+      if (r1 - r0 > 32) x = range(rb + lane);
+      if (__all_sync(0xffffffffu, x.last - x.first <= kFew)) {
+        if (r1 - r0 > 32) mask = few(x);
+        int r = __popc(mask), none = 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, r, o);
+          if (lane >= o) r += y;
         }
-        const uint32_t none = __ballot_sync(0xffffffffu, want && p < 0);
-        if (none && lane == 0) atomicAdd(a.lacking + b, __popc(none));
+        const int sum = __shfl_sync(0xffffffffu, r, 31);
+        r += at - __popc(mask);
+        at += sum;
+        for (; mask; mask &= mask - 1) {
+          const int p = r < f.total ? nth_free(a.pool, f, r) : -1;
+          ++r;
+          if (p >= 0)
+            a.pool.refs[p] = 1;
+          else
+            ++none;
+          x.row[x.first + __ffs((int)mask) - 1] = p;
+        }
+        if (none) atomicAdd(a.lacking + x.b, none);
+        continue;
+      }
+      window.seek(at);
+      for (unsigned k = 0; k < 32 && rb + k < r1; ++k) {
+        const Range y = of_lane(x, (int)k);
+        for (int j = y.first + lane; j - lane < y.last; j += 32 * kEntries) {
+          bool want[kEntries];
+          batch(y, j, want);
+#pragma unroll
+          for (int i = 0; i < kEntries; ++i) {
+            const uint32_t votes = __ballot_sync(0xffffffffu, want[i]);
+            if (votes == 0) continue;
+            const int p = window.get(want[i], at + __popc(votes & ((1u << lane) - 1u)));
+            at += __popc(votes);
+            if (want[i]) {
+              if (p >= 0) a.pool.refs[p] = 1;
+              y.row[j + 32 * i] = p;
+            }
+            const uint32_t none = __ballot_sync(0xffffffffu, want[i] && p < 0);
+            if (none && lane == 0) atomicAdd(a.lacking + y.b, __popc(none));
+          }
+        }
       }
     }
-  cluster.sync();
-  clear_first(a.pool, f, all, rank);
+  }
+  if (ctas > 1)
+    cluster.sync();
+  else
+    __syncthreads();
+  clear_first(a.pool, f, all, rank, ctas);
 }
 
 // ------------------------------------------------------------------------------- fork
@@ -294,24 +457,26 @@ __device__ __forceinline__ int fork_parent(const ForkArgs& a, int i, int* tokens
   return p;
 }
 // Pages for the part-full blocks of the children: entry `tokens / block` of their rows.
-__global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesThreads)
-    pages_fork_kernel(const ForkArgs a) {
+__global__ void __launch_bounds__(kPagesThreads) pages_fork_kernel(const ForkArgs a) {
   __shared__ PagesShared s;
   auto cluster = cooperative_groups::this_cluster();
-  const int rank = (int)cluster.block_rank();
-  const int lane = (int)threadIdx.x & 31, warp = rank * (kPagesThreads / 32) + ((int)threadIdx.x >> 5);
-  const long long rows = (long long)a.N * a.Hkv;
-  const long long r0 = rows * warp / kPagesWarps, r1 = rows * (warp + 1) / kPagesWarps;
+  const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+  const int lane = (int)threadIdx.x & 31;
+  const unsigned warps = ctas * (kPagesThreads / 32),
+                 warp = rank * (kPagesThreads / 32) + (threadIdx.x >> 5);
+  const unsigned heads = a.Hkv, rows = a.N * heads;
+  const unsigned r0 = (unsigned)((unsigned long long)rows * warp / warps),
+                 r1 = (unsigned)((unsigned long long)rows * (warp + 1) / warps);
   after_predecessor();
-  for (int i = rank * kPagesThreads + (int)threadIdx.x; i < a.N; i += kPagesCluster * kPagesThreads) {
+  for (int i = rank * kPagesThreads + (int)threadIdx.x; i < a.N; i += ctas * kPagesThreads) {
     int n;
     fork_parent(a, i, &n);
     a.lens_out[i] = n;
     a.lacking[i] = 0;
   }
-  auto wanted = [&](long long row, int* full) {
+  auto wanted = [&](unsigned row, int* full) {
     if (row >= r1) return false;
-    const int i = (int)(row / a.Hkv), h = (int)(row - (long long)i * a.Hkv);
+    const int i = (int)(row / heads), h = (int)(row - i * heads);
     int n;
     const int p = fork_parent(a, i, &n);
     *full = n / a.block;
@@ -319,19 +484,19 @@ __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesTh
            is_page(read_global(a.table + ((long long)p * a.Hkv + h) * a.max_blocks + *full),
                    a.pool.pages);
   };
-  int asked = 0;
-  for (long long row = r0; row < r1; row += 32) {
-    int full;
-    asked += __popc(__ballot_sync(0xffffffffu, wanted(row + lane, &full)));
+  int asked = 0, full = 0;
+  bool want = false;
+  for (unsigned row = r0; row < r1; row += 32) {
+    want = wanted(row + lane, &full);
+    asked += __popc(__ballot_sync(0xffffffffu, want));
   }
   const FreeCount f = count_free(a.pool, s.before, s.warp);
   int in_cta, all;
   int at = block_before(lane == 0 ? asked : 0, s.warp, &in_cta);
   at = __shfl_sync(0xffffffffu, at, 0);
   at += cluster_before(s, in_cta, &all);
-  for (long long row = r0; row < r1; row += 32) {
-    int full = 0;
-    const bool want = wanted(row + lane, &full);
+  for (unsigned row = r0; row < r1; row += 32) {
+    if (r1 - r0 > 32) want = wanted(row + lane, &full);
     const uint32_t votes = __ballot_sync(0xffffffffu, want);
     const int r = at + __popc(votes & ((1u << lane) - 1u));
     at += __popc(votes);
@@ -340,12 +505,15 @@ __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesTh
       if (p >= 0)
         a.pool.refs[p] = 1;
       else
-        atomicAdd(a.lacking + (row + lane) / a.Hkv, 1);
-      a.table_out[(row + lane) * a.max_blocks + full] = p;
+        atomicAdd(a.lacking + (row + lane) / heads, 1);
+      a.table_out[(size_t)(row + lane) * a.max_blocks + full] = p;
     }
   }
-  cluster.sync();
-  clear_first(a.pool, f, all, rank);
+  if (ctas > 1)
+    cluster.sync();
+  else
+    __syncthreads();
+  clear_first(a.pool, f, all, rank, ctas);
 }
 
 // `tokens` tokens of page src to page dst, with the page's scales and mean, by a CTA.
@@ -422,10 +590,8 @@ struct CompactArgs {
 };
 // With U pages in use: where each goes.  Those below U stay, the r-th in use from U on goes to
 // the r-th free one (there are as many below U).
-__global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesThreads)
-    pages_compact_kernel(const CompactArgs a) {
+__global__ void __launch_bounds__(kPagesThreads) pages_compact_kernel(const CompactArgs a) {
   __shared__ PagesShared s;
-  const int rank = (int)cooperative_groups::this_cluster().block_rank();
   after_predecessor();
   const FreeCount f = count_free(a.pool, s.before, s.warp);
   const int used = a.pool.pages - f.total;
@@ -438,15 +604,15 @@ __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesTh
   };
   // pages in use below U (U itself may be the pool's end)
   const int below = used < a.pool.pages ? used - free_before(used) : used;
-  for (long long q = rank * kPagesThreads + (int)threadIdx.x; q < a.pool.pages;
-       q += kPagesCluster * kPagesThreads) {
+  for (long long q = (long long)blockIdx.x * kPagesThreads + threadIdx.x; q < a.pool.pages;
+       q += (long long)gridDim.x * kPagesThreads) {
     const int p = (int)q;
     int to = -1;
     if (!((free_word(a.pool, p >> 5) >> (p & 31)) & 1u))
       to = p < used ? p : nth_free(a.pool, f, p - free_before(p) - below);
     a.to[p] = to;
   }
-  if (rank == 0 && threadIdx.x == 0) *a.n_used = used;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.n_used = used;
 }
 // The moves, the counts, the bitmap and the table.
 __global__ void __launch_bounds__(256) cache_compact_kernel(const CompactArgs a) {
