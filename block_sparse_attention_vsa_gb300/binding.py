@@ -130,7 +130,7 @@ def load(path: str = LIB_PATH):
     h.vsa_fwd_prompt_workspace_bytes.restype = sz
     h.vsa_fwd_prompt_workspace_bytes.argtypes = [i32] * 6
     h.vsa_bwd_prompt_workspace_bytes.restype = sz
-    h.vsa_bwd_prompt_workspace_bytes.argtypes = [i32] * 5
+    h.vsa_bwd_prompt_workspace_bytes.argtypes = [i32] * 6
     h.vsa_bwd_prompt.restype = i32
     h.vsa_bwd_prompt.argtypes = [P] * 9 + [i32] * 8 + [f32, P, P, P, P, sz, P]
     h.vsa_pages_free.restype = i32
@@ -1067,7 +1067,7 @@ def vsa_bwd_prompt(q, k, v, out, dout, lse, q_seq=None, k_seq=None, causal=True,
         dq, dk, dv = (torch.empty(x.shape, dtype=x.dtype, device=x.device) if d is None else d
                       for x, d in ((q, dq), (k, dk), (v, dv)))
         if workspace is None:
-            n = bwd_prompt_workspace_bytes(p.packed, p.B, p.Hq, p.Hkv, p.Sq)
+            n = bwd_prompt_workspace_bytes(p.packed, p.B, p.Hq, p.Hkv, p.Sq, p.Sk)
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     for name, d, x in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         _rows(name, d, torch.bfloat16, ndim, p.dev, x.shape)
@@ -1081,7 +1081,7 @@ def vsa_bwd_prompt(q, k, v, out, dout, lse, q_seq=None, k_seq=None, causal=True,
     return dq, dk, dv
 
 
-def bwd_prompt_workspace_bytes(packed, B, Hq, Hkv, Sq) -> int:
-    for name, n in (("B", B), ("Hq", Hq), ("Hkv", Hkv), ("Sq", Sq)):
+def bwd_prompt_workspace_bytes(packed, B, Hq, Hkv, Sq, Sk) -> int:
+    for name, n in (("B", B), ("Hq", Hq), ("Hkv", Hkv), ("Sq", Sq), ("Sk", Sk)):
         _whole(name, n)
-    return int(load().vsa_bwd_prompt_workspace_bytes(1 if packed else 0, B, Hq, Hkv, Sq))
+    return int(load().vsa_bwd_prompt_workspace_bytes(1 if packed else 0, B, Hq, Hkv, Sq, Sk))

@@ -12,6 +12,7 @@
 
 #include "../../include/vsa.h"
 #include "vsa_host.h"
+#include "vsa_launch.h"
 #include "vsa_prompt_bwd_kernel.cuh"
 #include "vsa_prompt_fwd_kernel.cuh"
 
@@ -173,6 +174,32 @@ long long fwd_items(int packed, long long B, int Hq, int Hkv, long long Sq) {
   return prompt::tile_slots(packed, B, Sq, 256 >> pack) * (Hq >> pack);
 }
 
+// Backward: the tiles of both kernels, into how many ranges their steps are cut, and the
+// workspace: the rows' statistics, and behind them the ranges' results (of one kernel at a time).
+// dq's ranges are chosen as the forward's, dkv's likewise among its steps, one a query tile and
+// head pack of its group.
+struct BwdLayout {
+  long long q_tiles, k_tiles;
+  int q_splits, k_splits;
+  size_t part, total;
+};
+BwdLayout bwd_layout(int packed, long long B, int Hq, int Hkv, long long Sq, long long Sk) {
+  const int pack = pack_log(Hq / Hkv);
+  BwdLayout l;
+  l.q_tiles = prompt::tile_slots(packed, B, Sq, 128 >> pack) * (Hq >> pack);
+  l.k_tiles = prompt::tile_slots(packed, B, Sk, 128) * Hkv;
+  l.q_splits = key_splits(l.q_tiles, Sk);
+  l.k_splits = key_splits(l.k_tiles, Sq * (Hq / Hkv));
+  l.part = (size_t)l.q_tiles * 1024;
+  const size_t dq = l.q_splits > 1 ? (size_t)(l.q_tiles * l.q_splits) *
+                                         prompt::bwd::dq::kPartFloats * sizeof(float)
+                                   : 0;
+  const size_t dkv = l.k_splits > 1 ? (size_t)(l.k_tiles * l.k_splits) * 2 * 128 * 128 * sizeof(float)
+                                    : 0;
+  l.total = l.part + (dq > dkv ? dq : dkv);
+  return l;
+}
+
 bool meets(const View& x, const void* p, long long bytes) {
   if (x.empty() || !p || bytes <= 0) return false;
   const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(p);
@@ -282,10 +309,9 @@ vsa_status vsa_fwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
   return VSA_OK;
 }
 
-size_t vsa_bwd_prompt_workspace_bytes(int packed, int B, int Hq, int Hkv, int Sq) {
-  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Sq < 0) return 0;
-  const int pack = pack_log(Hq / Hkv);
-  return (size_t)(prompt::tile_slots(packed, B, Sq, 128 >> pack) * (Hq >> pack)) * 1024;
+size_t vsa_bwd_prompt_workspace_bytes(int packed, int B, int Hq, int Hkv, int Sq, int Sk) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Sq < 0 || Sk < 0) return 0;
+  return bwd_layout(packed, B, Hq, Hkv, Sq, Sk).total;
 }
 
 vsa_status vsa_bwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* v,
@@ -311,7 +337,8 @@ vsa_status vsa_bwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
     if (!view_ok(*x)) return VSA_ERR_INVALID_ARG;
   for (const View* x : res)
     if (!view_ok(*x)) return VSA_ERR_INVALID_ARG;
-  const size_t need = vsa_bwd_prompt_workspace_bytes(packed, B, Hq, Hkv, Sq);
+  const BwdLayout l = bwd_layout(packed, B, Hq, Hkv, Sq, Sk);
+  const size_t need = l.total;
   const long long lse_bytes = nb * Hq * Sq * 4;
   if (Sq > 0 && (!lse || !host_aligned4(lse) || !workspace || workspace_bytes < need ||
                  !host_aligned16(workspace)))
@@ -340,11 +367,9 @@ vsa_status vsa_bwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
   a.group = Hq / Hkv;
   a.pack = pack_log(a.group);
   a.n_packs = Hq >> a.pack;
-  const long long tslots = prompt::tile_slots(packed, B, Sq, 128 >> a.pack),
-                  kslots = prompt::tile_slots(packed, B, Sk, 128);
-  if (tslots * a.n_packs > INT_MAX || kslots * Hkv > INT_MAX) return VSA_ERR_UNSUPPORTED;
-  a.n_tslots = (int)tslots;
-  a.n_kslots = (int)kslots;
+  if (l.q_tiles > INT_MAX || l.k_tiles > INT_MAX) return VSA_ERR_UNSUPPORTED;
+  a.n_tslots = (int)(l.q_tiles / a.n_packs);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + l.part);
   a.scale = scale;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_ns = host_wait_ns(prompt::kWaitLimitNs);
@@ -372,21 +397,27 @@ vsa_status vsa_bwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
     return VSA_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int launches = 0;
-  if (tslots > 0 && Sq > 0) {
+  // each starts up while the one before ends; dkv takes the D that dq leaves
+  if (Sq > 0) {
     const pb::PrepArgs pa{a.seq, out, dout, lse, static_cast<float*>(workspace),
                           vo.sb, vo.sh, vo.st, vg.sb, vg.sh, vg.st,
                           Hq, a.pack, a.n_packs, a.n_tslots};
-    pb::prompt_prep_kernel<<<(unsigned)(tslots * a.n_packs), 256, 0, s>>>(pa);
-    ++launches;
-  }
-  if (Sq > 0) {
+    st = launch(pb::prompt_prep_kernel, dim3((unsigned)l.q_tiles), 256, 0, s, 0, pa);
+    if (st != VSA_OK) return st;
     a.d0 = dq;
     a.d0_b = wq.sb;
     a.d0_h = wq.sh;
     a.d0_t = wq.st;
-    pb::dq::prompt_dq_kernel<<<(unsigned)(tslots * a.n_packs), pb::kThreads, pb::dq::kSmemBytes,
-                               s>>>(tq, tg, tk, tv, a);
-    ++launches;
+    a.splits = l.q_splits;
+    st = launch(pb::dq::prompt_dq_kernel, dim3((unsigned)(l.q_tiles * a.splits)), pb::kThreads,
+                pb::dq::kSmemBytes, s, 0, tq, tg, tk, tv, a);
+    if (st != VSA_OK) return st;
+    launches += 2;
+    if (a.splits > 1) {
+      st = launch(pb::dq::prompt_dq_join_kernel, dim3((unsigned)(l.q_tiles * 16)), 256, 0, s, 0, a);
+      if (st != VSA_OK) return st;
+      ++launches;
+    }
   }
   if (Sk > 0) {
     a.d0 = dk;
@@ -397,11 +428,17 @@ vsa_status vsa_bwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
     a.d1_b = wv.sb;
     a.d1_h = wv.sh;
     a.d1_t = wv.st;
-    pb::dkv::prompt_dkv_kernel<<<(unsigned)(kslots * Hkv), pb::kThreads, pb::dkv::kSmemBytes, s>>>(
-        tq, tg, tk, tv, a);
+    a.splits = Sq > 0 ? l.k_splits : 1;
+    st = launch(pb::dkv::prompt_dkv_kernel, dim3((unsigned)(l.k_tiles * a.splits)), pb::kThreads,
+                pb::dkv::kSmemBytes, s, 0, tq, tg, tk, tv, a);
+    if (st != VSA_OK) return st;
     ++launches;
+    if (a.splits > 1) {
+      st = launch(pb::dkv::prompt_dkv_join_kernel, dim3((unsigned)(l.k_tiles * 32)), 256, 0, s, 0, a);
+      if (st != VSA_OK) return st;
+      ++launches;
+    }
   }
-  if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
   host_set_launches(launches);
   return VSA_OK;
 }

@@ -51,6 +51,8 @@ constexpr uint32_t kTmemCols = 512;
 struct Args {
   SeqArgs seq;
   float* stats;  // [n_packs][n_tslots][-lse | -D][128]
+  int splits;    // ranges of a tile's steps, a CTA each
+  float* part;   // their partial results, if there are several
   uint16_t *d0, *d1;   // dkv: dk, dv; dq: dq, null
   long long d0_b, d0_h, d0_t, d1_b, d1_h, d1_t;  // strides in elements
   unsigned int* status;
@@ -79,6 +81,7 @@ struct PrepArgs {
   int Hq, pack, n_packs, n_tslots;
 };
 __global__ void __launch_bounds__(256) prompt_prep_kernel(const PrepArgs a) {
+  after_predecessor();
   const int slot = (int)(blockIdx.x / (unsigned)a.n_packs);
   const int hp = (int)(blockIdx.x - (unsigned)slot * (unsigned)a.n_packs);
   const int T = 128 >> a.pack;
@@ -102,9 +105,9 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(const PrepArgs a) {
     acc[i] = 0.0f;
     if (tok < s.nq) {
       const long long row = s.q0 + tok;
-      const uint4 o = __ldg(reinterpret_cast<const uint4*>(a.out + s.z * a.o_b + head * a.o_h +
+      const uint4 o = read_global(reinterpret_cast<const uint4*>(a.out + s.z * a.o_b + head * a.o_h +
                                                            row * a.o_t) + (lane & 15));
-      const uint4 g = __ldg(reinterpret_cast<const uint4*>(a.dout + s.z * a.g_b + head * a.g_h +
+      const uint4 g = read_global(reinterpret_cast<const uint4*>(a.dout + s.z * a.g_b + head * a.g_h +
                                                            row * a.g_t) + (lane & 15));
       const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, gw[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
@@ -124,7 +127,7 @@ __global__ void __launch_bounds__(256) prompt_prep_kernel(const PrepArgs a) {
     if ((lane & 15) == 0) {
       float l = -INFINITY;
       if (tok < s.nq) {
-        const float x = __ldg(a.lse + ((long long)s.z * a.Hq + head) * a.seq.Sq + s.q0 + tok);
+        const float x = read_global(a.lse + ((long long)s.z * a.Hq + head) * a.seq.Sq + s.q0 + tok);
         if (!(x <= -3.0e38f)) l = -x;
       }
       stats[r] = l;
@@ -160,8 +163,10 @@ struct Work {
   Seq s;
   int b, tile, hk;
   int first, n_tok;   // first query tile and their number, for each head pack
-  int hp0, steps;     // first head pack; all steps
+  int hp0;            // first head pack
+  int step0, steps;   // first step of the CTA's range, and their number
   int nk;             // keys of the tile
+  bool there;
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -177,30 +182,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = (int)(threadIdx.x >> 5);
   const uint32_t lane = lane_id();
   const int T = 128 >> a.pack;
-
-  Work k;
-  {
-    const int slot = (int)(blockIdx.x / (unsigned)a.Hkv);
-    k.hk = (int)(blockIdx.x - (unsigned)slot * (unsigned)a.Hkv);
-    // the first keys are seen by the most queries: they come first
-    if (a.seq.packed) {
-      k.b = find_slot(a.seq.k_seq, a.seq.B, a.seq.Sk, 128, slot, &k.tile);
-    } else {
-      k.tile = slot / a.seq.B;
-      k.b = slot - k.tile * a.seq.B;
-    }
-    k.s = load_seq(a.seq, k.b);
-    const int rows = a.seq.packed ? k.s.nk : a.seq.Sk;  // rows that are written
-    if (k.tile < 0 || 128 * k.tile >= rows) return;
-    k.nk = clampi(k.s.nk - 128 * k.tile, 0, 128);
-    int first = 0;
-    if (a.seq.causal) first = clampi(128 * k.tile - (k.s.nk - k.s.nq), 0, k.s.nq);
-    k.first = first / T;
-    k.n_tok = k.nk > 0 && first < k.s.nq ? (k.s.nq + T - 1) / T - k.first : 0;
-    k.hp0 = (k.hk * a.group) >> a.pack;
-    k.steps = k.n_tok * (a.group >> a.pack);
-  }
-  const int off = k.s.nk - k.s.nq;
 
   if (threadIdx.x == 0) {
     mbar_init(&ctl->kv_full, 1);
@@ -242,6 +223,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   const WaitCtx w{&ctl->abort_flag, a.status, a.wait_ns};
+  // (what comes before may run while the predecessor ends)
+  after_predecessor();
+  Work k;
+  const unsigned item = blockIdx.x / (unsigned)a.splits, split = blockIdx.x - item * a.splits;
+  {
+    const int slot = (int)(item / (unsigned)a.Hkv);
+    k.hk = (int)(item - (unsigned)slot * (unsigned)a.Hkv);
+    // the first keys are seen by the most queries: they come first
+    if (a.seq.packed) {
+      k.b = find_slot(a.seq.k_seq, a.seq.B, a.seq.Sk, 128, slot, &k.tile);
+    } else {
+      k.tile = slot / a.seq.B;
+      k.b = slot - k.tile * a.seq.B;
+    }
+    k.s = load_seq(a.seq, k.b);
+    const int rows = a.seq.packed ? k.s.nk : a.seq.Sk;  // rows that are written
+    k.there = k.tile >= 0 && 128 * k.tile < rows;
+    k.nk = clampi(k.s.nk - 128 * k.tile, 0, 128);
+    int first = 0;
+    if (a.seq.causal) first = clampi(128 * k.tile - (k.s.nk - k.s.nq), 0, k.s.nq);
+    k.first = first / T;
+    k.n_tok = k.nk > 0 && first < k.s.nq ? (k.s.nq + T - 1) / T - k.first : 0;
+    if (!k.there) k.n_tok = 0;
+    k.hp0 = (k.hk * a.group) >> a.pack;
+    const long long all = (long long)k.n_tok * (a.group >> a.pack);
+    k.step0 = (int)(all * split / a.splits);
+    k.steps = (int)(all * (split + 1) / a.splits) - k.step0;
+  }
+  const int off = k.s.nk - k.s.nq;
 
   if (warp < 8) {
     regs_increase<kGradRegs>();
@@ -251,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + lanes + kColS + 64 * wg, tDP = tmem + lanes + kColDP + 64 * wg;
     const uint64_t c2 = f32x2(a.scale_log2, a.scale_log2);
     bool ok = true;
-    int ti = k.first;
+    int ti = k.n_tok ? k.first + k.step0 % k.n_tok : 0;
     for (int g = 0; g < k.steps; ++g) {
       const int st = g & 1;
       const float* nlse = reinterpret_cast<const float*>(smem + kOffStats + st * 1024) + 64 * wg;
@@ -328,13 +338,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // dV (warpgroup 0) and dK (warpgroup 1)
     if (k.steps > 0 && ok) ok = wait_warp(&ctl->acc_full, 0, w, 0x23);
-    if (ok) {
+    if (ok && k.there) {
       tc_fence_after();
-      const long long row = k.s.k0 + 128 * k.tile + r;
-      const bool write = a.seq.packed ? r < k.nk : 128 * k.tile + r < a.seq.Sk;
-      uint16_t* dst = wg ? a.d0 + k.s.z * a.d0_b + k.hk * a.d0_h + row * a.d0_t
-                         : a.d1 + k.s.z * a.d1_b + k.hk * a.d1_h + row * a.d1_t;
+      const int rows = a.seq.packed ? k.nk : a.seq.Sk - 128 * k.tile;  // that are written
+      uint16_t* base = (wg ? a.d0 + k.s.z * a.d0_b + k.hk * a.d0_h
+                           : a.d1 + k.s.z * a.d1_b + k.hk * a.d1_h) +
+                       (k.s.k0 + 128ll * k.tile) * (wg ? a.d0_t : a.d1_t);
+      const long long stride = wg ? a.d0_t : a.d1_t;
       const float f = wg ? a.scale : 1.0f;
+      float* part = a.part + ((long long)blockIdx.x * 2 + (wg ? 0 : 1)) * (128 * 128) + r * 128;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t x[32];
@@ -342,17 +354,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_32x32b_x32(tmem + lanes + (wg ? kColDK : kColDV) + 32 * c, x);
           tmem_wait_ld();
         }
-        if (!write) continue;
+        if (a.splits == 1) {
+          // (the Q stages are free by now)
+          store_columns(smem + kOffQ + warp * 2048, x, f, k.steps > 0 && r < k.nk, [&](int i) {
+            const int rr = (warp & 3) * 32 + i;
+            return rr < rows ? base + rr * stride + 32 * c : nullptr;
+          });
+        } else if (k.steps > 0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t y[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            y[i] = k.steps > 0 && r < k.nk
-                       ? pack_bf16x2(__uint_as_float(x[8 * e + 2 * i]) * f,
-                                     __uint_as_float(x[8 * e + 2 * i + 1]) * f)
-                       : 0u;
-          reinterpret_cast<uint4*>(dst + 32 * c)[e] = make_uint4(y[0], y[1], y[2], y[3]);
+          for (int e = 0; e < 8; ++e)
+            reinterpret_cast<uint4*>(part + 32 * c)[e] =
+                make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
         }
       }
     }
@@ -363,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx(&ctl->kv_full, 2 * kTile);
         load_tile(smem + kOffK, &tk, &ctl->kv_full, k.s.k0 + 128 * k.tile, k.hk, k.s.z);
         load_tile(smem + kOffV, &tv, &ctl->kv_full, k.s.k0 + 128 * k.tile, k.hk, k.s.z);
-        int ti = k.first, hp = k.hp0, g = 0;
+        int ti = k.first + k.step0 % k.n_tok, hp = k.hp0 + k.step0 / k.n_tok, g = 0;
         const long long slot0 = query_slot(a, k.b, k.s.q0, 0);
         for (; g < k.steps; ++g) {
           const int qs = g % kQStages, gs = g % kGStages;
@@ -448,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp == 11) {
-      int ti = k.first;
+      int ti = k.n_tok ? k.first + k.step0 % k.n_tok : 0;
       for (int g = 0; g < k.steps; ++g) {
         const int qs = g % kQStages, gs = g % kGStages;
         const int valid = k.s.nq - ti * T;  // tokens of the tile
@@ -468,6 +480,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) tmem_dealloc(tmem, kTmemCols);
 }
 
+// Adds up the ranges of a tile's steps, in their order: a warp a row, dk and dv.
+__global__ void __launch_bounds__(256) prompt_dkv_join_kernel(const Args a) {
+  after_predecessor();
+  const unsigned item = blockIdx.x >> 5;
+  const int at = (int)((blockIdx.x & 31) * 8 + (threadIdx.x >> 5)), r = at & 127;
+  const int lane = (int)lane_id();
+  const int slot = (int)(item / (unsigned)a.Hkv), hk = (int)(item - (unsigned)slot * a.Hkv);
+  int b, tile;
+  if (a.seq.packed) {
+    b = find_slot(a.seq.k_seq, a.seq.B, a.seq.Sk, 128, slot, &tile);
+  } else {
+    tile = slot / a.seq.B;
+    b = slot - tile * a.seq.B;
+  }
+  const Seq s = load_seq(a.seq, b);
+  if (tile < 0 || 128ll * tile + r >= (a.seq.packed ? s.nk : a.seq.Sk)) return;
+  const int T = 128 >> a.pack;
+  int first = 0;
+  if (a.seq.causal) first = clampi(128 * tile - (s.nk - s.nq), 0, s.nq);
+  const int n_tok = first < s.nq && 128 * tile + r < s.nk ? (s.nq + T - 1) / T - first / T : 0;
+  const long long all = (long long)n_tok * (a.group >> a.pack);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < a.splits; ++i) {
+    if (all * (i + 1) / a.splits == all * i / a.splits) continue;  // a range of nothing
+    const float4 x = reinterpret_cast<const float4*>(
+        a.part + (((long long)item * a.splits + i) * 2 + (at >> 7)) * (128 * 128) + r * 128)[lane];
+    acc.x += x.x;
+    acc.y += x.y;
+    acc.z += x.z;
+    acc.w += x.w;
+  }
+  const float f = at < 128 ? a.scale : 1.0f;
+  const long long row = s.k0 + 128ll * tile + r;
+  uint16_t* dst = at < 128 ? a.d0 + s.z * a.d0_b + hk * a.d0_h + row * a.d0_t
+                           : a.d1 + s.z * a.d1_b + hk * a.d1_h + row * a.d1_t;
+  reinterpret_cast<uint2*>(dst)[lane] =
+      make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+}
+
 }  // namespace dkv
 
 // ---------------------------------------------------------------------------------- dQ
@@ -481,6 +532,7 @@ constexpr uint32_t kOffCtl = kOffXch + 1024;
 constexpr uint32_t kSmemBytes = kOffCtl + 1024;  // (the base is aligned)
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 384;  // dP twice
+constexpr int kPartFloats = 128 * 128 + 128;  // of a range: dQ and the rows' sums of dS
 
 struct Ctl {
   uint64_t q_full;
@@ -506,24 +558,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = (int)(threadIdx.x >> 5);
   const uint32_t lane = lane_id();
   const int T = 128 >> a.pack;
-
-  // the last tokens see the most keys: they come first
-  const int rank = (int)(blockIdx.x / (unsigned)a.n_packs);
-  const int hp = (int)(blockIdx.x - (unsigned)rank * (unsigned)a.n_packs);
-  int b, tile;
-  if (a.seq.packed) {
-    b = find_slot(a.seq.q_seq, a.seq.B, a.seq.Sq, T, a.n_tslots - 1 - rank, &tile);
-  } else {
-    tile = (a.seq.Sq + T - 1) / T - 1 - rank / a.seq.B;
-    b = rank % a.seq.B;
-  }
-  const Seq s = load_seq(a.seq, b);
-  if (tile < 0 || tile * T >= (a.seq.packed ? s.nq : a.seq.Sq)) return;
-  const int off = s.nk - s.nq;
-  const int tok0 = tile * T, head0 = hp << a.pack, hk = head0 / a.group;
-  int keys = tok0 < s.nq ? s.nk : 0;
-  if (a.seq.causal) keys = clampi((tok0 + T < s.nq ? tok0 + T : s.nq) + off, 0, keys);
-  const int steps = (keys + 127) / 128;
 
   if (threadIdx.x == 0) {
     mbar_init(&ctl->q_full, 1);
@@ -563,6 +597,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   const WaitCtx w{&ctl->abort_flag, a.status, a.wait_ns};
+  // the last tokens see the most keys: they come first
+  after_predecessor();
+  const unsigned item = blockIdx.x / (unsigned)a.splits, split = blockIdx.x - item * a.splits;
+  const int rank = (int)(item / (unsigned)a.n_packs);
+  const int hp = (int)(item - (unsigned)rank * (unsigned)a.n_packs);
+  int b, tile;
+  if (a.seq.packed) {
+    b = find_slot(a.seq.q_seq, a.seq.B, a.seq.Sq, T, a.n_tslots - 1 - rank, &tile);
+  } else {
+    tile = (a.seq.Sq + T - 1) / T - 1 - rank / a.seq.B;
+    b = rank % a.seq.B;
+  }
+  const Seq s = load_seq(a.seq, b);
+  const bool there = tile >= 0 && tile * T < (a.seq.packed ? s.nq : a.seq.Sq);
+  const int off = s.nk - s.nq;
+  const int tok0 = tile * T, head0 = hp << a.pack, hk = head0 / a.group;
+  int keys = there && tok0 < s.nq ? s.nk : 0;
+  if (a.seq.causal) keys = clampi((tok0 + T < s.nq ? tok0 + T : s.nq) + off, 0, keys);
+  const int all_steps = (keys + 127) / 128;
+  const int step0 = (int)((long long)all_steps * split / a.splits);
+  const int steps = (int)((long long)all_steps * (split + 1) / a.splits) - step0;
+  const int k_first = s.k0 + 128 * step0, nk = s.nk - 128 * step0;  // of the CTA's range
+
 
   if (warp < 8) {
     regs_increase<kGradRegs>();
@@ -570,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = (warp & 3) * 32 + (int)lane;  // row of the tile
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + kColS + 64 * wg, tDP = tmem + lanes + kColDP + 64 * wg;
-    const int tok = tok0 + (r & (T - 1)), head = head0 + (r >> (7 - a.pack));
+    const int tok = tok0 + (r & (T - 1));
     float nlse = -INFINITY, nD = 0.0f;
     float* st = a.stats + ((long long)hp * a.n_tslots + query_slot(a, b, s.q0, tile)) * 256;
     if (steps > 0) {
@@ -586,8 +643,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&ctl->x_full[warp & 3]);
       return wait_warp(&ctl->x_full[warp & 3], 0, w, 0x50);
     };
-    int lim = s.nk;  // keys this row attends
+    int lim = s.nk;  // keys this row attends, counted from the range's first
     if (a.seq.causal) lim = clampi(tok + 1 + off, 0, s.nk);
+    lim -= 128 * step0;
     const uint64_t c2 = f32x2(a.scale_log2, a.scale_log2), l2 = f32x2(nlse, nlse),
                    d2 = f32x2(nD, nD);
     bool ok = true;
@@ -645,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         x[c] = __float_as_uint(y0);
         x[c + 1] = __float_as_uint(y1);
       }
-      if (steps == 1) {
+      if (all_steps == 1) {
         // the row is here as a whole: take off what its dS, which add up to 0, come to
         float lo, hi;
         split_f32x2(sum2, lo, hi);
@@ -665,21 +723,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->ds_full[g & 1]);
     }
-    if (steps > 1 && ok) {
+    if (all_steps > 1 && steps > 0 && ok) {
       float lo, hi;
       split_f32x2(sum2, lo, hi);
       ok = exchange(lo + hi);
     }
     // D for the dkv kernel: sum_j p_ij (dout_i . v_j), without the rounding of out
-    if (steps > 0 && ok && wg == 0 && tok < s.nq)
-      st[128 + r] = nD - (xch[r] + xch[128 + r]);
+    float* part = a.part + (long long)blockIdx.x * kPartFloats;
+    if (steps > 0 && ok && wg == 0 && tok < s.nq) {
+      if (a.splits == 1)
+        st[128 + r] = nD - (xch[r] + xch[128 + r]);
+      else
+        part[128 * 128 + r] = xch[r] + xch[128 + r];
+    }
     if (steps > 0 && ok) ok = wait_warp(&ctl->acc_full, 0, w, 0x42);
-    if (ok) {
+    if (ok && there) {
       tc_fence_after();
-      const bool write = tok < (a.seq.packed ? s.nq : a.seq.Sq);
-      const bool some = steps > 0 && tok < s.nq;
-      uint16_t* dst =
-          a.d0 + s.z * a.d0_b + head * a.d0_h + (long long)(s.q0 + tok) * a.d0_t + 64 * wg;
+      const int rows = a.seq.packed ? s.nq : a.seq.Sq;  // tokens that are written
+      uint16_t* base =
+          a.d0 + s.z * a.d0_b + (long long)(s.q0 + tok0) * a.d0_t + head0 * a.d0_h + 64 * wg;
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
         uint32_t x[32];
@@ -687,16 +749,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_32x32b_x32(tmem + lanes + kColDQ + 64 * wg + 32 * c, x);
           tmem_wait_ld();
         }
-        if (!write) continue;
+        if (a.splits == 1) {
+          // (the K stages are free by now)
+          store_columns(smem + kOffK + warp * 2048, x, a.scale, steps > 0 && tok < s.nq,
+                        [&](int i) {
+                          const int rr = (warp & 3) * 32 + i, t = rr & (T - 1);
+                          return tok0 + t < rows ? base + (rr >> (7 - a.pack)) * a.d0_h +
+                                                       t * a.d0_t + 32 * c
+                                                 : nullptr;
+                        });
+        } else if (steps > 0) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t y[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            y[i] = some ? pack_bf16x2(__uint_as_float(x[8 * e + 2 * i]) * a.scale,
-                                      __uint_as_float(x[8 * e + 2 * i + 1]) * a.scale)
-                        : 0u;
-          reinterpret_cast<uint4*>(dst + 32 * c)[e] = make_uint4(y[0], y[1], y[2], y[3]);
+          for (int e = 0; e < 8; ++e)
+            reinterpret_cast<uint4*>(part + r * 128 + 64 * wg + 32 * c)[e] =
+                make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
         }
       }
     }
@@ -712,13 +778,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int ks = g % kKStages, vs = g % kVStages;
           if (g >= kKStages && !wait(&ctl->k_empty[ks], (g / kKStages + 1) & 1, w, 0x43)) break;
           mbar_arrive_expect_tx(&ctl->k_full[ks], kTile);
-          load_tile(smem + kOffK + ks * kTile, &tk, &ctl->k_full[ks], s.k0 + 128 * g, hk, s.z);
+          load_tile(smem + kOffK + ks * kTile, &tk, &ctl->k_full[ks], k_first + 128 * g, hk, s.z);
           if (g >= kVStages && !wait(&ctl->v_empty[vs], (g / kVStages + 1) & 1, w, 0x44)) {
             wait(&ctl->k_full[ks], (g / kKStages) & 1, w, 0x45, true);  // this one has no pair
             break;
           }
           mbar_arrive_expect_tx(&ctl->v_full[vs], kTile);
-          load_tile(smem + kOffV + vs * kTile, &tv, &ctl->v_full[vs], s.k0 + 128 * g, hk, s.z);
+          load_tile(smem + kOffV + vs * kTile, &tv, &ctl->v_full[vs], k_first + 128 * g, hk, s.z);
         }
         wait(&ctl->q_full, 0, w, 0x46, true);
         for (int i = 0; i < kKStages; ++i) {
@@ -785,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int g = 0; g < steps; ++g) {
         const int ks = g % kKStages;
         if (!wait_warp(&ctl->k_full[ks], (g / kKStages) & 1, w, 0x4f)) break;
-        if (s.nk - 128 * g < 128) zero_rows(smem + kOffK + ks * kTile, s.nk - 128 * g);
+        if (nk - 128 * g < 128) zero_rows(smem + kOffK + ks * kTile, nk - 128 * g);
         if (lane == 0) mbar_arrive(&ctl->k_ready[ks]);
         __syncwarp();
       }
@@ -795,6 +861,47 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Adds up the ranges of a tile's key tiles, in their order: a warp a row.
+__global__ void __launch_bounds__(256) prompt_dq_join_kernel(const Args a) {
+  after_predecessor();
+  const unsigned item = blockIdx.x >> 4;
+  const int r = (int)((blockIdx.x & 15) * 8 + (threadIdx.x >> 5)), lane = (int)lane_id();
+  const int T = 128 >> a.pack;
+  const int rank = (int)(item / (unsigned)a.n_packs),
+            hp = (int)(item - (unsigned)rank * (unsigned)a.n_packs);
+  int b, tile;
+  if (a.seq.packed) {
+    b = find_slot(a.seq.q_seq, a.seq.B, a.seq.Sq, T, a.n_tslots - 1 - rank, &tile);
+  } else {
+    tile = (a.seq.Sq + T - 1) / T - 1 - rank / a.seq.B;
+    b = rank % a.seq.B;
+  }
+  const Seq s = load_seq(a.seq, b);
+  const int tok0 = tile * T, tok = tok0 + (r & (T - 1)), head = (hp << a.pack) + (r >> (7 - a.pack));
+  if (tile < 0 || tok >= (a.seq.packed ? s.nq : a.seq.Sq)) return;
+  int keys = tok0 < s.nq ? s.nk : 0;
+  if (a.seq.causal) keys = clampi((tok0 + T < s.nq ? tok0 + T : s.nq) + s.nk - s.nq, 0, keys);
+  const int steps = (keys + 127) / 128;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float rest = 0.0f;
+  for (int i = 0; i < a.splits && tok < s.nq; ++i) {
+    if ((long long)steps * (i + 1) / a.splits == (long long)steps * i / a.splits) continue;
+    const float* part = a.part + ((long long)item * a.splits + i) * kPartFloats;
+    const float4 x = reinterpret_cast<const float4*>(part + r * 128)[lane];
+    acc.x += x.x;
+    acc.y += x.y;
+    acc.z += x.z;
+    acc.w += x.w;
+    rest += part[128 * 128 + r];
+  }
+  reinterpret_cast<uint2*>(a.d0 + s.z * a.d0_b + head * a.d0_h +
+                           (long long)(s.q0 + tok) * a.d0_t)[lane] =
+      make_uint2(pack_bf16x2(acc.x * a.scale, acc.y * a.scale),
+                 pack_bf16x2(acc.z * a.scale, acc.w * a.scale));
+  if (lane == 0 && tok < s.nq && steps > 0)
+    a.stats[((long long)hp * a.n_tslots + query_slot(a, b, s.q0, tile)) * 256 + 128 + r] -= rest;
 }
 
 }  // namespace dq

@@ -19,6 +19,7 @@
 #include <cstdint>
 
 #include "sm103_ptx.cuh"
+#include "vsa_warp_ptx.cuh"
 
 namespace vsa {
 namespace prompt {
@@ -48,15 +49,15 @@ __device__ __forceinline__ Seq load_seq(const SeqArgs& a, int b) {
   Seq s;
   if (a.packed) {
     s.z = 0;
-    s.q0 = clampi(__ldg(a.q_seq + b), 0, a.Sq);
-    s.nq = clampi(__ldg(a.q_seq + b + 1), s.q0, a.Sq) - s.q0;
-    s.k0 = clampi(__ldg(a.k_seq + b), 0, a.Sk);
-    s.nk = clampi(__ldg(a.k_seq + b + 1), s.k0, a.Sk) - s.k0;
+    s.q0 = clampi(read_global(a.q_seq + b), 0, a.Sq);
+    s.nq = clampi(read_global(a.q_seq + b + 1), s.q0, a.Sq) - s.q0;
+    s.k0 = clampi(read_global(a.k_seq + b), 0, a.Sk);
+    s.nk = clampi(read_global(a.k_seq + b + 1), s.k0, a.Sk) - s.k0;
   } else {
     s.z = b;
     s.q0 = s.k0 = 0;
-    s.nq = a.q_seq ? clampi(__ldg(a.q_seq + b), 0, a.Sq) : a.Sq;
-    s.nk = a.k_seq ? clampi(__ldg(a.k_seq + b), 0, a.Sk) : a.Sk;
+    s.nq = a.q_seq ? clampi(read_global(a.q_seq + b), 0, a.Sq) : a.Sq;
+    s.nk = a.k_seq ? clampi(read_global(a.k_seq + b), 0, a.Sk) : a.Sk;
   }
   return s;
 }
@@ -76,13 +77,13 @@ __device__ __forceinline__ int find_slot(const int32_t* seq, int B, int S, int T
     const int step = (n + 31) / 32;
     const int i = lane * step;
     bool below = false;
-    if (i < n) below = clampi(__ldg(seq + lo + i), 0, S) / T + lo + i <= slot;
+    if (i < n) below = clampi(read_global(seq + lo + i), 0, S) / T + lo + i <= slot;
     const uint32_t votes = __ballot_sync(0xffffffffu, below);
     const int at = votes ? 31 - __clz((int)votes) : 0;
     lo += at * step;
     n = n - at * step < step ? n - at * step : step;
   }
-  *tile = slot - (clampi(__ldg(seq + lo), 0, S) / T + lo);
+  *tile = slot - (clampi(read_global(seq + lo), 0, S) / T + lo);
   return lo;
 }
 
@@ -155,6 +156,36 @@ __device__ __forceinline__ void zero_tokens(uint8_t* tile, int n, int T) {
       reinterpret_cast<uint4*>(tile + kTile / 2)[i] = make_uint4(0, 0, 0, 0);
     }
   fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// 32 columns of a warp's 32 rows, fp32 in registers (a row a lane), times f to bf16 in global
+// memory, through 2 KB of shared memory, so that a store is 8 rows of 64 bytes and not 32 of 16
+// (the forward's results took 6,000 cycles an item that way).  `to` gives where a row's columns
+// go, or null.  (Pieces of 16 bytes are turned by the row so that eight rows' meet all banks.)
+template <class To>
+__device__ __forceinline__ void store_columns(uint8_t* stage, const uint32_t (&x)[32], float f,
+                                              bool some, To to) {
+  const uint32_t lane = lane_id();
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      y[i] = some ? pack_bf16x2(__uint_as_float(x[8 * c + 2 * i]) * f,
+                                __uint_as_float(x[8 * c + 2 * i + 1]) * f)
+                  : 0u;
+    *reinterpret_cast<uint4*>(stage + lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16)) =
+        make_uint4(y[0], y[1], y[2], y[3]);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t r = 8 * i + (lane >> 2), c = lane & 3;
+    const uint4 y = *reinterpret_cast<const uint4*>(stage + r * 64 + ((c ^ ((r >> 1) & 3)) * 16));
+    uint16_t* dst = to((int)r);
+    if (dst != nullptr) *reinterpret_cast<uint4*>(dst + 8 * c) = y;
+  }
   __syncwarp();
 }
 

@@ -635,7 +635,7 @@ PyObject* bwd_prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor ws;
     if (a[13] == Py_None) {
       const size_t bytes = lib.bwd_prompt_workspace_bytes(p.packed, (int)p.B, (int)p.Hq,
-                                                          (int)p.Hkv, (int)p.Sq);
+                                                          (int)p.Hkv, (int)p.Sq, (int)p.Sk);
       ws = empty(p.q, at::kByte, {(int64_t)bytes});
     } else {
       ws = tensor(a[13]);

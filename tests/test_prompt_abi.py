@@ -138,9 +138,14 @@ def test_fwd_prompt_workspace(lib):
 def test_bwd_prompt_workspace(lib):
     f = lib.vsa_bwd_prompt_workspace_bytes
     # a tile of 128 rows -- 2 heads of 64 tokens -- 1 KB each; 200 // 64 + 2 tiles a pair of heads
-    assert f(1, 2, 4, 2, 200) == 5 * 2 * 1024
-    assert f(0, 2, 4, 2, 200) == 2 * 4 * 2 * 1024
-    assert f(1, 2, 5, 2, 200) == 0 and f(1, 0, 4, 2, 200) == 0 and f(1, 2, 4, 0, 200) == 0
+    assert f(1, 2, 4, 2, 200, 200) == 5 * 2 * 1024
+    assert f(0, 2, 4, 2, 200, 200) == 2 * 4 * 2 * 1024
+    # dq of 10 tiles in 5 ranges of 4 key tiles; (dk, dv) of 20 in one
+    assert f(1, 2, 4, 2, 200, 2600) == 10 * 1024 + 10 * 5 * (128 * 128 + 128) * 4
+    # (dk, dv) of 8 tiles -- 300 // 128 + 2 for 2 heads -- in 9 ranges of its 40 steps
+    assert f(1, 2, 32, 2, 300, 300) == (37 + 2) * 2 * 1024 + 8 * 9 * 2 * 128 * 128 * 4
+    assert f(1, 2, 5, 2, 200, 200) == 0 and f(1, 0, 4, 2, 200, 200) == 0
+    assert f(1, 2, 4, 0, 200, 200) == 0
 
 
 def free(lib, **kw):

@@ -279,6 +279,29 @@ def test_few_queries_against_many_keys(nq, nk, Hq, Hkv, causal):
     hold(dict(out=whole.transpose(0, 1), lse=l2), want, bound)
 
 
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("nq,nk,Hq,Hkv", [([3], [2500], 2, 1), ([70, 1], [1500, 600], 4, 2),
+                                          ([600], [600], 8, 1), ([300, 41], [300, 41], 24, 1),
+                                          ([1100], [90], 6, 1), ([500, 0, 2], [1100, 700, 0], 16, 1)],
+                         ids=str)
+def test_gradients_of_few_tiles(nq, nk, Hq, Hkv, causal):
+    """dq over ranges of keys, (dk, dv) over ranges of queries and heads."""
+    check_packed(nq, nk, Hq, Hkv, causal, sum(nq) * 3 + Hq)
+
+
+def test_gradients_of_few_tiles_padded():
+    g = gen(27)
+    q, dout = randn((2, 16, 400, D), g), randn((2, 16, 400, D), g)
+    k, v = randn((2, 1, 900, D), g), randn((2, 1, 900, D), g)
+    nq, nk = [400, 37], [900, 130]
+    got = both(q, k, v, dout, q_seq=i32(nq), k_seq=i32(nk))
+    for b in range(2):
+        one = {n: t[b] for n, t in got.items()}
+        hold(one, *ref.attend(q[b], k[b], v[b], [nq[b]], [nk[b]], [0], [0], True, None, dout[b]))
+        for n, rows in (("out", nq), ("dq", nq), ("dk", nk), ("dv", nk)):
+            assert (one[n][:, rows[b]:] == 0).all(), n
+
+
 def test_few_queries_scores_that_are_no_numbers():
     g = gen(26)
     q, k, v = randn((3, 1, D), g), randn((3000, 1, D), g), randn((3000, 1, D), g)
