@@ -159,15 +159,24 @@ int pack_log(int group) {
 constexpr int kSms = 152;     // of a GB300, which host_device() asks for
 constexpr int kMaxSplits = 32;  // a lane each where they are joined
 
-// Into how many ranges the forward cuts an item's keys: as many as fill the SMs once, of four
-// key tiles or more, and none where the items fill them (they are taken up as SMs come free).
-// One token of 12 heads against 16,384 keys takes 36 us cut and 228 whole, 40 tokens of 2 x 12
-// heads against 4,000 keys 28 and 62; in ranges of two tiles 64 tokens of 8 heads against 512
-// keys take 19 us, whole 15.
-int key_splits(long long items, long long Sk) {
-  const long long fill = items > 0 ? kSms / items : 1, most = (Sk + 127) / 128 / 4;
+// Into how many ranges of `least` tiles or more the tiles of so many items are cut: as many as
+// give each SM `each` of them.
+int splits(long long items, long long tiles, int each, int least) {
+  const long long fill = items > 0 ? (long long)kSms * each / items : 1, most = tiles / least;
   const long long n = fill < most ? fill : most;
   return n < 2 ? 1 : (n < kMaxSplits ? (int)n : kMaxSplits);
+}
+// Keys of the forward and of dq: ranges of eight tiles, one an SM.  One token of 12 heads against
+// 16,384 keys takes 36 us cut and 228 whole; with two an SM 46, 2,048 tokens of 12 heads 44
+// where one an SM (whole) takes 33; in ranges of four tiles 300 tokens of 8 heads against 1,000
+// keys take 23, whole 21.
+int key_splits(long long items, long long Sk) { return splits(items, (Sk + 127) / 128, 1, 8); }
+// Steps of (dk, dv): likewise, and two an SM where ranges keep 32 steps, which evens out what
+// causal tiles differ by (8,192 tokens, 12 heads on 2: 501 us of the whole gradient, 751 with
+// one an SM).
+int step_splits(long long items, long long steps) {
+  const int a = splits(items, steps, 1, 8), b = splits(items, steps, 2, 32);
+  return a > b ? a : b;
 }
 long long fwd_items(int packed, long long B, int Hq, int Hkv, long long Sq) {
   const int pack = pack_log(Hq / Hkv);
@@ -189,7 +198,7 @@ BwdLayout bwd_layout(int packed, long long B, int Hq, int Hkv, long long Sq, lon
   l.q_tiles = prompt::tile_slots(packed, B, Sq, 128 >> pack) * (Hq >> pack);
   l.k_tiles = prompt::tile_slots(packed, B, Sk, 128) * Hkv;
   l.q_splits = key_splits(l.q_tiles, Sk);
-  l.k_splits = key_splits(l.k_tiles, Sq * (Hq / Hkv));
+  l.k_splits = step_splits(l.k_tiles, (Sq * (Hq / Hkv) + 127) / 128);
   l.part = (size_t)l.q_tiles * 1024;
   const size_t dq = l.q_splits > 1 ? (size_t)(l.q_tiles * l.q_splits) *
                                          prompt::bwd::dq::kPartFloats * sizeof(float)

@@ -127,10 +127,11 @@ def test_bwd_prompt_checks(lib, kw, code):
 def test_fwd_prompt_workspace(lib):
     f = lib.vsa_fwd_prompt_workspace_bytes
     unit = (256 * 128 + 512) * 4
-    # 2 heads of 128 tokens an item: (200 // 128 + 2) * 2 items, 25 of 152 SMs each; 20 key tiles, 4 a range
-    assert f(1, 2, 4, 2, 200, 2500) == 6 * 5 * unit
-    assert f(1, 2, 4, 2, 200, 1000) == 6 * 2 * unit
-    assert f(1, 2, 4, 2, 200, 800) == 0 and f(1, 2, 4, 2, 20000, 20000) == 0
+    # 2 heads of 128 tokens an item: (200 // 128 + 2) * 2 items, 25 of 152 SMs each; 40 key
+    # tiles, 8 a range
+    assert f(1, 2, 4, 2, 200, 5000) == 6 * 5 * unit
+    assert f(1, 2, 4, 2, 200, 2048) == 6 * 2 * unit
+    assert f(1, 2, 4, 2, 200, 1900) == 0 and f(1, 2, 4, 2, 20000, 20000) == 0
     assert f(0, 1, 1, 1, 1, 1 << 20) == 32 * unit
     assert f(1, 2, 5, 2, 200, 2500) == 0 and f(1, 0, 4, 2, 200, 2500) == 0
 
@@ -140,10 +141,12 @@ def test_bwd_prompt_workspace(lib):
     # a tile of 128 rows -- 2 heads of 64 tokens -- 1 KB each; 200 // 64 + 2 tiles a pair of heads
     assert f(1, 2, 4, 2, 200, 200) == 5 * 2 * 1024
     assert f(0, 2, 4, 2, 200, 200) == 2 * 4 * 2 * 1024
-    # dq of 10 tiles in 5 ranges of 4 key tiles; (dk, dv) of 20 in one
-    assert f(1, 2, 4, 2, 200, 2600) == 10 * 1024 + 10 * 5 * (128 * 128 + 128) * 4
-    # (dk, dv) of 8 tiles -- 300 // 128 + 2 for 2 heads -- in 9 ranges of its 40 steps
-    assert f(1, 2, 32, 2, 300, 300) == (37 + 2) * 2 * 1024 + 8 * 9 * 2 * 128 * 128 * 4
+    # dq of 10 tiles in 5 ranges of 8 key tiles; (dk, dv) of 82 in one
+    assert f(1, 2, 4, 2, 200, 5120) == 10 * 1024 + 10 * 5 * (128 * 128 + 128) * 4
+    # (dk, dv) of 8 tiles -- 300 // 128 + 2 for 2 heads -- in 4 ranges of its 38 steps
+    assert f(1, 2, 32, 2, 300, 300) == (37 + 2) * 2 * 1024 + 8 * 4 * 2 * 128 * 128 * 4
+    # of 130 tiles in 2 ranges of its 384 steps (tiles of 2 heads and 64 tokens)
+    assert f(1, 1, 12, 2, 8192, 8192) == 129 * 6 * 1024 + 130 * 2 * 2 * 128 * 128 * 4
     assert f(1, 2, 5, 2, 200, 200) == 0 and f(1, 0, 4, 2, 200, 200) == 0
     assert f(1, 2, 4, 0, 200, 200) == 0
 

@@ -259,9 +259,9 @@ def test_long_sequences_by_rows():
 
 
 @pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
-@pytest.mark.parametrize("nq,nk,Hq,Hkv", [([1], [5000], 1, 1), ([3, 1], [2000, 129], 8, 2),
+@pytest.mark.parametrize("nq,nk,Hq,Hkv", [([1], [5000], 1, 1), ([3, 1], [4000, 129], 8, 2),
                                           ([70], [4100], 4, 4), ([300], [40], 2, 2),
-                                          ([2, 5, 0], [1700, 0, 300], 6, 1)], ids=str)
+                                          ([2, 5, 0], [3700, 0, 300], 6, 1)], ids=str)
 def test_few_queries_against_many_keys(nq, nk, Hq, Hkv, causal):
     """Keys cut into ranges: within the bounds, and near the uncut result."""
     g = gen(sum(nk))
@@ -280,9 +280,9 @@ def test_few_queries_against_many_keys(nq, nk, Hq, Hkv, causal):
 
 
 @pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
-@pytest.mark.parametrize("nq,nk,Hq,Hkv", [([3], [2500], 2, 1), ([70, 1], [1500, 600], 4, 2),
+@pytest.mark.parametrize("nq,nk,Hq,Hkv", [([3], [2500], 2, 1), ([70, 1], [2500, 600], 4, 2),
                                           ([600], [600], 8, 1), ([300, 41], [300, 41], 24, 1),
-                                          ([1100], [90], 6, 1), ([500, 0, 2], [1100, 700, 0], 16, 1)],
+                                          ([1100], [90], 6, 1), ([500, 0, 2], [2100, 700, 0], 16, 1)],
                          ids=str)
 def test_gradients_of_few_tiles(nq, nk, Hq, Hkv, causal):
     """dq over ranges of keys, (dk, dv) over ranges of queries and heads."""
@@ -292,8 +292,8 @@ def test_gradients_of_few_tiles(nq, nk, Hq, Hkv, causal):
 def test_gradients_of_few_tiles_padded():
     g = gen(27)
     q, dout = randn((2, 16, 400, D), g), randn((2, 16, 400, D), g)
-    k, v = randn((2, 1, 900, D), g), randn((2, 1, 900, D), g)
-    nq, nk = [400, 37], [900, 130]
+    k, v = randn((2, 1, 2100, D), g), randn((2, 1, 2100, D), g)
+    nq, nk = [400, 37], [2100, 130]
     got = both(q, k, v, dout, q_seq=i32(nq), k_seq=i32(nk))
     for b in range(2):
         one = {n: t[b] for n, t in got.items()}
