@@ -309,11 +309,11 @@ vsa_status vsa_fwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
       !make_map(&tv, vv.empty() ? vq : vv, 128, 1))
     return VSA_ERR_CUDA;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  prompt::fwd::prompt_fwd_kernel<<<(unsigned)(a.n_items * a.splits), prompt::fwd::kThreads,
-                                   prompt::fwd::kSmemBytes, s>>>(tq, tk, tv, a);
-  if (a.splits > 1)
-    prompt::fwd::prompt_join_kernel<<<(unsigned)(a.n_items * 32), 256, 0, s>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return VSA_ERR_CUDA;
+  st = launch(prompt::fwd::prompt_fwd_kernel, dim3((unsigned)(a.n_items * a.splits)),
+              prompt::fwd::kThreads, prompt::fwd::kSmemBytes, s, 0, tq, tk, tv, a);
+  if (st == VSA_OK && a.splits > 1)
+    st = launch(prompt::fwd::prompt_join_kernel, dim3((unsigned)(a.n_items * 32)), 256, 0, s, 0, a);
+  if (st != VSA_OK) return st;
   host_set_launches(a.splits > 1 ? 2 : 1);
   return VSA_OK;
 }

@@ -603,6 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&ctl->tmem_base, kTmemCols);
     tmem_relinquish();
   }
+  // What comes before runs while the predecessor in the stream ends.  (A successor may not start
+  // up likewise: CTAs of this grid that are taken over are never launched.)
+  wait_predecessor();
   if (warp == 8) {  // the CTA's own item is looked up while the others get ready
     Item it;
     const bool holds = decode(a, (int)blockIdx.x, it);
@@ -636,6 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the ranges of split items, a warp a row: with M = max m_s and c_s = 2^(m_s - M), out =
 // sum c_s O_s / sum c_s l_s and lse = M + log2 sum c_s l_s, in the order of the ranges.
 __global__ void __launch_bounds__(256) prompt_join_kernel(const FwdArgs a) {
+  after_predecessor();
   const int item = (int)(blockIdx.x >> 5);
   const int at = (int)((blockIdx.x & 31) * 8 + (threadIdx.x >> 5)), t = at >> 7, row = at & 127;
   const int lane = (int)lane_id();

@@ -22,6 +22,11 @@ __device__ __forceinline__ void after_predecessor() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// The same for a kernel whose successor starts up only when it has ended.
+__device__ __forceinline__ void wait_predecessor() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // What a call reads may be what its predecessor in the stream writes, and this kernel's life
 // begins before that one's ends: not memory that is read-only for as long as the kernel
 // lives, which the non-coherent path (__ldg, const __restrict__ parameters) asks for and

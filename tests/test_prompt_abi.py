@@ -3,6 +3,8 @@ calls get the documented status before the GPU is touched (no GPU needed); and t
 forms the GPU tests compare with, pinned to torch's autograd and to hand-made pools."""
 import ctypes
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -229,6 +231,21 @@ def compact(lib, **kw):
 ])
 def test_cache_compact_checks(lib, kw, code):
     assert compact(lib, **kw) == code
+
+
+@pytest.mark.parametrize("name", ["vsa_prompt_common.cuh", "vsa_prompt_fwd_kernel.cuh",
+                                  "vsa_prompt_bwd_kernel.cuh", "vsa_pages_kernel.cuh"])
+def test_no_read_only_loads_in_kernels_that_start_early(name):
+    """They start up while their predecessor ends: what it may have written is read by ordinary
+    loads behind the wait for it."""
+    with open(os.path.join(libbuild.CSRC, name)) as f:
+        code = re.sub(r"//.*", "", f.read())
+    for word in ("__ldg", "__restrict__", "ld.global.nc", ".nc."):
+        assert word not in code, word
+    for body in code.split("__global__")[1:]:
+        wait = min(x for x in (body.find("after_predecessor();"), body.find("wait_predecessor();"))
+                   if x >= 0)
+        assert "read_global" not in body[:wait] and "load_seq" not in body[:wait]
 
 
 # ------------------------------------------------------------------- the plain forms' pins
