@@ -408,11 +408,15 @@ vsa_status vsa_bwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
   int launches = 0;
   // each starts up while the one before ends; dkv takes the D that dq leaves
   if (Sq > 0) {
-    const pb::PrepArgs pa{a.seq, out, dout, lse, static_cast<float*>(workspace),
-                          vo.sb, vo.sh, vo.st, vg.sb, vg.sh, vg.st,
-                          Hq, a.pack, a.n_packs, a.n_tslots};
-    st = launch(pb::prompt_prep_kernel, dim3((unsigned)l.q_tiles), 256, 0, s, 0, pa);
-    if (st != VSA_OK) return st;
+    a.out = out;
+    a.dout = dout;
+    a.lse = lse;
+    a.o_b = vo.sb;
+    a.o_h = vo.sh;
+    a.o_t = vo.st;
+    a.g_b = vg.sb;
+    a.g_h = vg.sh;
+    a.g_t = vg.st;
     a.d0 = dq;
     a.d0_b = wq.sb;
     a.d0_h = wq.sh;
@@ -421,7 +425,7 @@ vsa_status vsa_bwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
     st = launch(pb::dq::prompt_dq_kernel, dim3((unsigned)(l.q_tiles * a.splits)), pb::kThreads,
                 pb::dq::kSmemBytes, s, 0, tq, tg, tk, tv, a);
     if (st != VSA_OK) return st;
-    launches += 2;
+    ++launches;
     if (a.splits > 1) {
       st = launch(pb::dq::prompt_dq_join_kernel, dim3((unsigned)(l.q_tiles * 16)), 256, 0, s, 0, a);
       if (st != VSA_OK) return st;

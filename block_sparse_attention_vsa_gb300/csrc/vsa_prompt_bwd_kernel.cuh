@@ -5,12 +5,11 @@
 //   dv_j = sum_i p_ij dout_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j,
 // dk and dv summed over the query heads of a key/value head.
 //
-// Three kernels, without atomics, so results do not depend on timing:
-//   prompt_prep_kernel  per query row -lse (-infinity where a row attends nothing, or behind a
-//                       sequence's end, so that every p of the row is 0) and -D, in the order
-//                       of the query tiles.
+// Two kernels, without atomics, so results do not depend on timing:
 //   prompt_dq_kernel    a CTA per query tile: Q and dO stay, dQ adds up in TMEM while it
-//                       walks the key tiles: S = Q K^T, dP = dO V^T, dS, dQ += dS K.
+//                       walks the key tiles: S = Q K^T, dP = dO V^T, dS, dQ += dS K.  It sets
+//                       out with the rows' D and leaves -lse and -D for the other kernel, in
+//                       the order of the query tiles.
 //                       out is rounded to bf16, and D with it; but a row's dS add up to 0, so
 //                       what they come to is that error: it is taken off D for the next
 //                       kernel, and here off the dS of rows of one key tile, where out is
@@ -30,6 +29,9 @@
 //   dkv  dV_g, S_{g+1}, dK_g, dP_{g+1}: P_{g+1} may take as long as dK_g and dP_{g+1}, dS_{g+1}
 //        as long as dV_{g+1} and S_{g+2}.  S_{g+1} overwrites P_g, dP_{g+1} overwrites dS_g.
 //   dq   S_{g+1}, dP_{g+1}, dQ_g, with two buffers of dP / dS.
+//
+// Where there are fewer tiles than SMs the steps of each are cut into ranges, a CTA each, and a
+// kernel more adds up what they leave, in order.
 //
 // 12 warps: 0-7 gradient warps (thread = lane of the tile, warpgroup w = columns 64 w ..),
 // 8 TMA, 9 MMA issuer (one lane), 11 hands landed tiles on to the MMA warp and zeroes rows
@@ -55,6 +57,9 @@ struct Args {
   float* part;   // their partial results, if there are several
   uint16_t *d0, *d1;   // dkv: dk, dv; dq: dq, null
   long long d0_b, d0_h, d0_t, d1_b, d1_h, d1_t;  // strides in elements
+  const uint16_t *out, *dout;  // read row by row by dq
+  const float* lse;
+  long long o_b, o_h, o_t, g_b, g_h, g_t;
   unsigned int* status;
   int Hq, Hkv, group, pack, n_packs, n_tslots;  // query tiles of 128 >> pack tokens
   int n_kslots;                                 // key tiles of 128 tokens
@@ -68,72 +73,6 @@ __device__ __forceinline__ long long query_slot(const Args& a, int b, int q0, in
   const int T = 128 >> a.pack;
   return a.seq.packed ? (long long)(q0 / T) + b + tile
                       : (long long)b * ((a.seq.Sq + T - 1) / T) + tile;
-}
-
-// -------------------------------------------------------------------------------- prep
-// One CTA per query tile, half a warp a row (8 of the 128 elements a lane).
-struct PrepArgs {
-  SeqArgs seq;
-  const uint16_t *out, *dout;
-  const float* lse;
-  float* stats;
-  long long o_b, o_h, o_t, g_b, g_h, g_t;
-  int Hq, pack, n_packs, n_tslots;
-};
-__global__ void __launch_bounds__(256) prompt_prep_kernel(const PrepArgs a) {
-  after_predecessor();
-  const int slot = (int)(blockIdx.x / (unsigned)a.n_packs);
-  const int hp = (int)(blockIdx.x - (unsigned)slot * (unsigned)a.n_packs);
-  const int T = 128 >> a.pack;
-  int b, tile;
-  if (a.seq.packed) {
-    b = find_slot(a.seq.q_seq, a.seq.B, a.seq.Sq, T, slot, &tile);
-  } else {
-    const int per = (a.seq.Sq + T - 1) / T;
-    b = slot / per;
-    tile = slot - b * per;
-  }
-  const Seq s = load_seq(a.seq, b);
-  if (tile < 0 || tile * T >= s.nq) return;  // no step reads this tile
-  const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
-  float* stats = a.stats + ((long long)hp * a.n_tslots + slot) * 256;
-  float acc[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = 16 * warp + 2 * i + (lane >> 4);
-    const int tok = tile * T + (r & (T - 1)), head = (hp << a.pack) + (r >> (7 - a.pack));
-    acc[i] = 0.0f;
-    if (tok < s.nq) {
-      const long long row = s.q0 + tok;
-      const uint4 o = read_global(reinterpret_cast<const uint4*>(a.out + s.z * a.o_b + head * a.o_h +
-                                                           row * a.o_t) + (lane & 15));
-      const uint4 g = read_global(reinterpret_cast<const uint4*>(a.dout + s.z * a.g_b + head * a.g_h +
-                                                           row * a.g_t) + (lane & 15));
-      const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, gw[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        acc[i] = fmaf(__uint_as_float(ow[e] << 16), __uint_as_float(gw[e] << 16), acc[i]);
-        acc[i] = fmaf(__uint_as_float(ow[e] & 0xFFFF0000u), __uint_as_float(gw[e] & 0xFFFF0000u),
-                      acc[i]);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-#pragma unroll
-    for (int x = 8; x > 0; x >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], x);
-    const int r = 16 * warp + 2 * i + (lane >> 4);
-    const int tok = tile * T + (r & (T - 1)), head = (hp << a.pack) + (r >> (7 - a.pack));
-    if ((lane & 15) == 0) {
-      float l = -INFINITY;
-      if (tok < s.nq) {
-        const float x = read_global(a.lse + ((long long)s.z * a.Hq + head) * a.seq.Sq + s.q0 + tok);
-        if (!(x <= -3.0e38f)) l = -x;
-      }
-      stats[r] = l;
-      stats[128 + r] = tok < s.nq ? -acc[i] : 0.0f;
-    }
-  }
 }
 
 // --------------------------------------------------------------------------- dK and dV
@@ -527,8 +466,8 @@ namespace dq {
 constexpr int kKStages = 3, kVStages = 2;
 constexpr uint32_t kOffQ = 0, kOffG = kTile, kOffK = 2 * kTile;
 constexpr uint32_t kOffV = kOffK + kKStages * kTile;
-constexpr uint32_t kOffXch = kOffV + kVStages * kTile;  // the rows' sums of dS, a warpgroup each
-constexpr uint32_t kOffCtl = kOffXch + 1024;
+constexpr uint32_t kOffXch = kOffV + kVStages * kTile;  // a row's sums, of a warpgroup each
+constexpr uint32_t kOffCtl = kOffXch + 2048;
 constexpr uint32_t kSmemBytes = kOffCtl + 1024;  // (the base is aligned)
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 384;  // dP twice
@@ -628,28 +567,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + kColS + 64 * wg, tDP = tmem + lanes + kColDP + 64 * wg;
     const int tok = tok0 + (r & (T - 1));
-    float nlse = -INFINITY, nD = 0.0f;
     float* st = a.stats + ((long long)hp * a.n_tslots + query_slot(a, b, s.q0, tile)) * 256;
-    if (steps > 0) {
-      nlse = st[r];
-      nD = st[128 + r];
-    }
-    float* xch = reinterpret_cast<float*>(smem + kOffXch);  // [2][128]
+    float* xch = reinterpret_cast<float*>(smem + kOffXch);  // [2][2][128]
     uint64_t sum2 = f32x2(0.0f, 0.0f);                      // of the row's dS
-    // with the warp that has the rows' other columns (once)
-    auto exchange = [&](float x) {
-      xch[128 * wg + r] = x;
+    // with the warp that has the rows' other columns, twice: -D, then the sums of dS
+    auto exchange = [&](int n, float x) {
+      xch[256 * n + 128 * wg + r] = x;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->x_full[warp & 3]);
-      return wait_warp(&ctl->x_full[warp & 3], 0, w, 0x50);
+      return wait_warp(&ctl->x_full[warp & 3], n, w, 0x50);
     };
+    // the row's -lse (-infinity where it attends nothing, or is none of the sequence's, so that
+    // every p of it is 0) and -D = -sum_d dout out, this warpgroup's half of the columns
+    const bool in = there && tok < s.nq;
+    float nlse = -INFINITY, part_d = 0.0f;
+    if (in) {
+      const int head = head0 + (r >> (7 - a.pack));
+      const long long row = s.q0 + tok;
+      const uint4* o = reinterpret_cast<const uint4*>(a.out + s.z * a.o_b + head * a.o_h +
+                                                      row * a.o_t + 64 * wg);
+      const uint4* g = reinterpret_cast<const uint4*>(a.dout + s.z * a.g_b + head * a.g_h +
+                                                      row * a.g_t + 64 * wg);
+      const float l = read_global(a.lse + ((long long)s.z * a.Hq + head) * a.seq.Sq + row);
+      if (!(l <= -3.0e38f)) nlse = -l;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = read_global(o + 4 * h + i);
+          y[i] = read_global(g + 4 * h + i);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t ow[4] = {x[i].x, x[i].y, x[i].z, x[i].w},
+                         gw[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            part_d = fmaf(bf16_lo(ow[e]), bf16_lo(gw[e]), part_d);
+            part_d = fmaf(bf16_hi(ow[e]), bf16_hi(gw[e]), part_d);
+          }
+        }
+      }
+    }
+    bool ok = exchange(0, part_d);
+    const float nD = -(part_d + xch[128 * (wg ^ 1) + r]);
+    if (wg == 0 && split == 0 && there) {
+      st[r] = nlse;
+      st[128 + r] = in ? nD : 0.0f;
+    }
     int lim = s.nk;  // keys this row attends, counted from the range's first
     if (a.seq.causal) lim = clampi(tok + 1 + off, 0, s.nk);
     lim -= 128 * step0;
     const uint64_t c2 = f32x2(a.scale_log2, a.scale_log2), l2 = f32x2(nlse, nlse),
                    d2 = f32x2(nD, nD);
-    bool ok = true;
-    for (int g = 0; g < steps; ++g) {
+    for (int g = 0; g < steps && ok; ++g) {
       if (!wait_warp(&ctl->s_full, g & 1, w, 0x40)) {
         ok = false;
         break;
@@ -707,11 +679,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the row is here as a whole: take off what its dS, which add up to 0, come to
         float lo, hi;
         split_f32x2(sum2, lo, hi);
-        if (!exchange(lo + hi)) {
+        if (!exchange(1, lo + hi)) {
           ok = false;
           break;
         }
-        const float rest = lo + hi + xch[128 * (wg ^ 1) + r];
+        const float rest = lo + hi + xch[256 + 128 * (wg ^ 1) + r];
 #pragma unroll
         for (int c = 0; c < 64; c += 2)
           pk[c / 2] = pack_bf16x2(fmaf(-p[c], rest, __uint_as_float(x[c])),
@@ -726,15 +698,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (all_steps > 1 && steps > 0 && ok) {
       float lo, hi;
       split_f32x2(sum2, lo, hi);
-      ok = exchange(lo + hi);
+      ok = exchange(1, lo + hi);
     }
     // D for the dkv kernel: sum_j p_ij (dout_i . v_j), without the rounding of out
     float* part = a.part + (long long)blockIdx.x * kPartFloats;
-    if (steps > 0 && ok && wg == 0 && tok < s.nq) {
+    if (steps > 0 && ok && wg == 0 && in) {
+      const float rest = xch[256 + r] + xch[384 + r];
       if (a.splits == 1)
-        st[128 + r] = nD - (xch[r] + xch[128 + r]);
+        st[128 + r] = nD - rest;
       else
-        part[128 * 128 + r] = xch[r] + xch[128 + r];
+        part[128 * 128 + r] = rest;
     }
     if (steps > 0 && ok) ok = wait_warp(&ctl->acc_full, 0, w, 0x42);
     if (ok && there) {

@@ -570,7 +570,7 @@ VSA_API size_t vsa_fwd_prompt_workspace_bytes(int packed, int B, int Hq, int Hkv
  *   strides int64 [24]: (batch, head, token) of q, k, v, out, dout, dq, dk, dv.
  *   workspace  vsa_bwd_prompt_workspace_bytes() bytes, 16-byte aligned, no initialisation
  *           needed; calls sharing it must not overlap on the GPU.
- * No atomics: results do not depend on timing.  Three kernels, and one more for each of dq and
+ * No atomics: results do not depend on timing.  Two kernels, and one more for each of dq and
  * (dk, dv) where there are too few tiles of them to keep the GPU busy. */
 VSA_API vsa_status vsa_bwd_prompt(const vsa_bf16 *q, const vsa_bf16 *k, const vsa_bf16 *v,
                                   const vsa_bf16 *out, const vsa_bf16 *dout, const float *lse,

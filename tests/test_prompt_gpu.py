@@ -431,7 +431,7 @@ def test_launches_and_no_lse():
     o2, l2 = binding.vsa_fwd_prompt(q, k, v, i32([0, 64]), lse=False)
     assert l2 is None and torch.equal(out, o2)
     binding.vsa_bwd_prompt(q, k, v, out, out, lse, i32([0, 64]))
-    assert binding.vsa_last_launch_count() == 3
+    assert binding.vsa_last_launch_count() == 2
     empty = q[:0]
     o3, _ = binding.vsa_fwd_prompt(empty, k, v, i32([0, 0]), i32([0, 64]))
     assert o3.shape == (0, 2, D)
