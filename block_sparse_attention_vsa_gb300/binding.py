@@ -984,6 +984,10 @@ class _Prompt:
             Bk, self.Hkv, self.Sk, _ = k.shape
             if Bk != self.B:
                 raise ValueError(f"k must hold {self.B} sequences, got {Bk}")
+            if q_seq is not None and k_seq is None:
+                if self.Sk != self.Sq:
+                    raise ValueError("k_seq is needed: keys are padded to another length")
+                k_seq = q_seq
             n = self.B
         if k.shape[-1] != self.D:
             raise ValueError(f"k must have heads of {self.D}, got {k.shape[-1]}")
@@ -1007,10 +1011,10 @@ class _Prompt:
 def vsa_fwd_prompt(q, k, v, q_seq=None, k_seq=None, causal=True, scale=None, out=None, lse=True,
                    workspace=None, stream=None):
     """Attention over whole prompts.  Packed: q bf16 [tokens,Hq,128], k, v [tokens,Hkv,128],
-    q_seq, k_seq int32 [B+1] the starts of the sequences and the end (k_seq None: q_seq); rows
-    of no sequence are not written.  Padded: q [B,Hq,Sq,128], k, v [B,Hkv,Sk,128], q_seq,
-    k_seq int32 [B] the sequences' lengths (None: all rows); rows behind a length get 0.  Any
-    strides but the last.  causal: the last query is at the last key, query i attends keys up
+    q_seq, k_seq int32 [B+1] the starts of the sequences and the end; rows of no sequence are
+    not written.  Padded: q [B,Hq,Sq,128], k, v [B,Hkv,Sk,128], q_seq, k_seq int32 [B] the
+    sequences' lengths (q_seq None: all rows); rows behind a length get 0.  k_seq None: as
+    q_seq.  Any strides but the last.  causal: the last query is at the last key, query i attends keys up
     to i + nk - nq.  workspace (uint8, fwd_prompt_workspace_bytes): where the keys of few
     queries are cut into ranges; allocated if not given, False: they are not cut.  Returns (out,
     lse or None), lse float32 (base 2) [Hq,tokens] or [B,Hq,Sq]."""

@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_reserve_kernel(const Rese
                  warp = rank * (kPagesThreads / 32) + (threadIdx.x >> 5);
   // few rows are cut into parts, so that all warps have some
   const unsigned heads = a.Hkv, whole = a.B * heads;
-  const unsigned parts = 2 * warps > whole && a.max_blocks > 32 ? 2 * warps / whole : 1;
+  const unsigned parts = whole > 0 && 2 * warps > whole && a.max_blocks > 32 ? 2 * warps / whole : 1;
   const unsigned rows = whole * parts;
   const unsigned r0 = (unsigned)((unsigned long long)rows * warp / warps),
                  r1 = (unsigned)((unsigned long long)rows * (warp + 1) / warps);

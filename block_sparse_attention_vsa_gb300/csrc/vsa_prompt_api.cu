@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -60,6 +61,20 @@ bool view_ok(const View& v) {
   if (!v.p || !host_aligned16(v.p)) return false;
   for (long long s : {v.sb, v.sh, v.st})
     if (s < VSA_HEAD_DIM || s % 8 != 0 || s >= (1ll << 38)) return false;
+  return true;
+}
+
+// Whether the rows of a result lie apart: every stride spans what the smaller ones reach.
+bool rows_apart(const View& v) {
+  if (v.empty()) return true;
+  std::pair<long long, long long> d[3] = {{v.sb, v.nb}, {v.sh, v.nh}, {v.st, v.nt}};
+  std::sort(d, d + 3);
+  long long reach = VSA_HEAD_DIM;
+  for (const auto& e : d) {
+    if (e.second <= 1) continue;
+    if (e.first < reach) return false;
+    reach += (e.second - 1) * e.first;
+  }
   return true;
 }
 
@@ -254,7 +269,7 @@ vsa_status vsa_fwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
              vv = view(v, strides + 6, nb, Hkv, Sk), vo = view(out, strides + 9, nb, Hq, Sq);
   for (const View* x : {&vq, &vk, &vv, &vo})
     if (!view_ok(*x)) return VSA_ERR_INVALID_ARG;
-  if (!host_aligned4(lse)) return VSA_ERR_INVALID_ARG;
+  if (!rows_apart(vo) || !host_aligned4(lse)) return VSA_ERR_INVALID_ARG;
   const long long lse_bytes = lse ? nb * Hq * Sq * 4 : 0;
   for (const View* x : {&vq, &vk, &vv})
     if (views_meet(vo, *x) || meets(*x, lse, lse_bytes)) return VSA_ERR_INVALID_ARG;
@@ -345,7 +360,7 @@ vsa_status vsa_bwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
   for (const View* x : in)
     if (!view_ok(*x)) return VSA_ERR_INVALID_ARG;
   for (const View* x : res)
-    if (!view_ok(*x)) return VSA_ERR_INVALID_ARG;
+    if (!view_ok(*x) || !rows_apart(*x)) return VSA_ERR_INVALID_ARG;
   const BwdLayout l = bwd_layout(packed, B, Hq, Hkv, Sq, Sk);
   const size_t need = l.total;
   const long long lse_bytes = nb * Hq * Sq * 4;

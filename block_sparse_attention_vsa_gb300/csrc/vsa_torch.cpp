@@ -542,6 +542,10 @@ struct Prompt {
       B = q.size(0), Hq = q.size(1), Sq = q.size(2), Hkv = k.size(1), Sk = k.size(2);
       if (k.size(0) != B) throw LongWay();
       n = B;
+      if (qs != Py_None && ks == Py_None) {
+        if (Sk != Sq) throw LongWay();
+        ks = qs;
+      }
     }
     q_seq = maybe<int32_t>(qs, kI32, {n}, dev);
     k_seq = maybe<int32_t>(ks, kI32, {n}, dev);

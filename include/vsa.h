@@ -527,12 +527,14 @@ VSA_API vsa_status vsa_cache_compact(int32_t *table, int B, int Hkv, int D, int 
  * front of the queries are a past that is held already, and with nk < nq the first queries
  * attend nothing.  What a tensor holds in rows of no sequence reaches no result; inside a
  * sequence, keys are expected to be finite: a NaN or infinity in v reaches all rows of the
- * query tiles that walk over it, masked or not.
+ * query tiles that walk over it, masked or not.  (v of up to 2^60 in magnitude: weights are
+ * taken relative to a maximum that may lag behind by 2^32.)
  * Tensors.  bf16 [batch, heads, tokens, 128] with strides in elements, `strides` a host array
  * of (batch, head, token) for each tensor in the order of the arguments: 128 or more,
  * multiples of 8, addresses 16-byte aligned; the stride of an axis of length 1 is free.  So
  * slices of a fused projection's output go in as they are, and outputs may be slices of one
- * buffer.  Outputs must not share elements with inputs or with one another.
+ * buffer.  Outputs must not share elements with inputs or with one another.  (Broadcast
+ * tensors, with a stride of 0, are refused: copy them first.)
  * ------------------------------------------------------------------------------------- */
 
 /* Forward.

@@ -65,6 +65,8 @@ def with_strides(i, values, base=rows(4) + 2 * rows(2) + rows(4)):
     (dict(s=with_strides(1, [0, D, 0])), INVALID),            # broadcast
     (dict(s=with_strides(2, [0, 64, 256])), INVALID),         # rows that overlap
     (dict(s=with_strides(3, [0, D, -4 * D])), INVALID),
+    (dict(s=with_strides(3, [0, D, 2 * D])), INVALID),        # a result over itself
+    (dict(s=with_strides(3, [0, 150 * D, D])), INVALID),
     (dict(s=with_strides(0, [0, 1 << 39, 4 * D])), INVALID),  # more than a copy's stride holds
     (dict(out=64 * MB), INVALID), (dict(out=96 * MB), INVALID), (dict(out=128 * MB + 256), INVALID),
     (dict(lse=160 * MB), INVALID), (dict(lse=1 * MB), INVALID), (dict(lse=64 * MB), INVALID), (dict(out=1 * MB), INVALID),

@@ -441,6 +441,49 @@ def test_launches_and_no_lse():
     assert (dk == 0).all() and (dv == 0).all()
 
 
+@pytest.mark.parametrize("shape", [(1, 2, 300, 300), (2, 8, 40, 2500)], ids=str)
+def test_a_wait_that_runs_out_is_reported(shape):
+    """The test hook holds the MMA warps on a barrier that nothing completes: every role ends, the
+    status says so, and the next calls are right again."""
+    B, H, Sq, Sk = shape
+    g = gen(28)
+    q, k, v = randn((B, H, Sq, D), g), randn((B, 1, Sk, D), g), randn((B, 1, Sk, D), g)
+    want, lse = binding.vsa_fwd_prompt(q, k, v)
+    grads = binding.vsa_bwd_prompt(q, k, v, want, q, lse)
+    ok()
+    try:
+        binding.vsa_set_wait_limit_ns(2_000_000)
+        binding.vsa_set_stall_test(True)
+        binding.vsa_fwd_prompt(q, k, v)
+        code, detail = binding.vsa_device_status()
+        assert code == binding.VSA_ERR_DEVICE_TIMEOUT and detail & 0x100
+        binding.vsa_bwd_prompt(q, k, v, want, q, lse)
+        code, detail = binding.vsa_device_status()
+        assert code == binding.VSA_ERR_DEVICE_TIMEOUT and detail & 0x100
+    finally:
+        binding.vsa_set_stall_test(False)
+        binding.vsa_set_wait_limit_ns(0)
+    out, l2 = binding.vsa_fwd_prompt(q, k, v)
+    again = binding.vsa_bwd_prompt(q, k, v, out, q, l2)
+    ok()
+    assert torch.equal(out, want) and torch.equal(l2, lse)
+    for x, y in zip(again, grads):
+        assert torch.equal(x, y)
+
+
+def test_keys_are_as_long_as_queries_unless_said_otherwise():
+    g = gen(29)
+    q, k, v = randn((2, 2, 90, D), g), randn((2, 1, 90, D), g), randn((2, 1, 90, D), g)
+    n = i32([50, 90])
+    for causal in (True, False):
+        a, la = binding.vsa_fwd_prompt(q, k, v, n, causal=causal)
+        b, lb = binding.vsa_fwd_prompt(q, k, v, n, n, causal=causal)
+        assert torch.equal(a, b) and torch.equal(la, lb)
+    with pytest.raises(ValueError):
+        binding.vsa_fwd_prompt(q, k[:, :, :80], v[:, :, :80], n)
+    ok()
+
+
 def test_refusals():
     g = gen(24)
     q, k, v = (randn((64, h, D), g) for h in (4, 2, 2))
@@ -466,6 +509,8 @@ def test_refusals():
     d = torch.empty((64, 4, D), dtype=torch.bfloat16, device=DEV)
     with pytest.raises(binding.VsaError):  # two gradients that share rows
         binding.vsa_bwd_prompt(q, k, v, out, out, lse, seq, dq=d, dk=d[:, 1:3])
+    with pytest.raises(binding.VsaError):  # a result whose own rows overlap
+        fwd(q, k, v, seq, out=d.as_strided((64, 4, D), (D, D, 1)))
     ok()
 
 
