@@ -1,6 +1,7 @@
 """GB300-native (sm_103a) block-sparse attention: VSA look-up tables and Jenga block
-bitmaps, forward and backward; the choice of the blocks by their means; and the serving of
-single tokens from an 8-bit key/value cache, with eviction from it.
+bitmaps, forward and backward; the choice of the blocks by their means; attention over
+whole prompts, forward and backward; and the serving of single tokens from an 8-bit key/value
+cache, with eviction from it and the pages it lies in.
 
 The computation runs in hand-written CUDA kernels behind a C ABI
 (``include/vsa.h``, built into ``libvsa_gb300.so``); :mod:`.binding` is the thin

@@ -14,7 +14,7 @@
 //                       what they come to is that error: it is taken off D for the next
 //                       kernel, and here off the dS of rows of one key tile, where out is
 //                       large (elsewhere it is the mean of many v).  12 heads of up to 411
-//                       tokens: dk off by 0.0024 (relative, in norm) instead of 0.0025.
+//                       tokens: dk and dq off by 0.0024 (relative, in norm), not 0.0025.
 //   prompt_dkv_kernel   a CTA per key tile of 128 keys and key/value head: K and V stay in
 //                       shared memory, dK and dV add up in TMEM while it walks the query
 //                       tiles that see the keys.  Per step, transposed (lanes = keys):
@@ -25,18 +25,25 @@
 // are 64 KB of L2 reductions a step, and their order would be anyone's.  P and dS are rounded
 // to bf16 for the products, everything else is fp32.
 //
-// A step's products take 512 tensor cycles each (128 x 128 x 128).  Order of issue, one lane:
-//   dkv  dV_g, S_{g+1}, dK_g, dP_{g+1}: P_{g+1} may take as long as dK_g and dP_{g+1}, dS_{g+1}
-//        as long as dV_{g+1} and S_{g+2}.  S_{g+1} overwrites P_g, dP_{g+1} overwrites dS_g.
-//   dq   S_{g+1}, dP_{g+1}, dQ_g, with two buffers of dP / dS.
+// A step's products take 512 tensor cycles each (128 x 128 x 128), issued by two warps that run
+// converged (elect.sync picks the lane: one lane issuing for itself took 60 cycles and more a
+// product's sixteenth, and the kernels ran at 0.78 of what they do):
+//   dkv  warp 9 dV_g, S_{g+1}; warp 10 dK_g, dP_{g+1}; a unit each in turn.  P_{g+1} may take as
+//        long as warp 10's unit, dS_{g+1} as long as warp 9's.  S_{g+1} overwrites P_g, dP_{g+1}
+//        overwrites dS_g: MMAs of one warp run in order.
+//   dq   warp 9 S_{g+1}, dP_{g+1} (two buffers of dP / dS; the one that dQ_{g-1} read), warp 10
+//        dQ_g.
+// With 19 heads of 8,192 tokens the tensor pipe is busy 72 % (dkv) and 70 % (dq) of the time at
+// 1.9 GHz, 1,690 TFLOP/s of their own products; what is left are the round trips through
+// barriers and TMEM of a step's chain, and 4 us a CTA of start and end.
 //
 // Where there are fewer tiles than SMs the steps of each are cut into ranges, a CTA each, and a
 // kernel more adds up what they leave, in order.
 //
 // 12 warps: 0-7 gradient warps (thread = lane of the tile, warpgroup w = columns 64 w ..),
-// 8 TMA, 9 MMA issuer (one lane), 11 hands landed tiles on to the MMA warp and zeroes rows
-// that are not the sequence's first: they get weight 0, but 0 times what lies there (another
-// sequence, padding) may be NaN.
+// 8 TMA, 9 and 10 MMA issuers, 11 hands landed tiles on to them and zeroes rows that are not the
+// sequence's first: they get weight 0, but 0 times what lies there (another sequence, padding)
+// may be NaN.
 #pragma once
 
 #include "vsa_prompt_common.cuh"
