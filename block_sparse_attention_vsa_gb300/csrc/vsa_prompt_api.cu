@@ -160,7 +160,7 @@ vsa_status check_shape(const Shape& p) {
   return VSA_OK;
 }
 prompt::SeqArgs seq_args(const Shape& p) {
-  return prompt::SeqArgs{p.q_seq, p.k_seq, p.packed ? 1 : 0, p.B, p.Sq, p.Sk, p.causal ? 1 : 0};
+  return prompt::SeqArgs{p.q_seq, p.k_seq, p.packed ? 1 : 0, p.B, p.Sq, p.Sk, p.causal ? 1 : 0, 0};
 }
 
 // Heads that share a tile: the largest power of two, 16 at most, that divides a group.  A
@@ -193,6 +193,8 @@ int step_splits(long long items, long long steps) {
   const int a = splits(items, steps, 1, 8), b = splits(items, steps, 2, 32);
   return a > b ? a : b;
 }
+// Whether CTAs look up the order of the sequences by length (see find_tile).
+int sorted(int B, long long ctas) { return B > 1 && B <= 32 && ctas > kSms; }
 long long fwd_items(int packed, long long B, int Hq, int Hkv, long long Sq) {
   const int pack = pack_log(Hq / Hkv);
   return prompt::tile_slots(packed, B, Sq, 256 >> pack) * (Hq >> pack);
@@ -290,7 +292,6 @@ vsa_status vsa_fwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
   a.n_packs = Hq >> a.pack;
   const long long slots = prompt::tile_slots(packed, B, Sq, 256 >> a.pack);
   if (slots * a.n_packs > INT_MAX) return VSA_ERR_UNSUPPORTED;
-  a.n_slots = (int)slots;
   a.n_items = (int)(slots * a.n_packs);
   a.splits = 1;
   if (workspace != nullptr) {
@@ -309,6 +310,8 @@ vsa_status vsa_fwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
   a.scale_log2 = scale * 1.4426950408889634f;
   a.wait_ns = host_wait_ns(prompt::kWaitLimitNs);
   a.stall = host_stall();
+
+  a.seq.sort = sorted(B, (long long)a.n_items * a.splits);
 
   int dev = 0;
   st = host_device(&dev);
@@ -437,6 +440,7 @@ vsa_status vsa_bwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
     a.d0_h = wq.sh;
     a.d0_t = wq.st;
     a.splits = l.q_splits;
+    a.seq.sort = sorted(B, l.q_tiles * a.splits);
     st = launch(pb::dq::prompt_dq_kernel, dim3((unsigned)(l.q_tiles * a.splits)), pb::kThreads,
                 pb::dq::kSmemBytes, s, 0, tq, tg, tk, tv, a);
     if (st != VSA_OK) return st;
@@ -457,6 +461,7 @@ vsa_status vsa_bwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
     a.d1_h = wv.sh;
     a.d1_t = wv.st;
     a.splits = Sq > 0 ? l.k_splits : 1;
+    a.seq.sort = sorted(B, l.k_tiles * a.splits);
     st = launch(pb::dkv::prompt_dkv_kernel, dim3((unsigned)(l.k_tiles * a.splits)), pb::kThreads,
                 pb::dkv::kSmemBytes, s, 0, tq, tg, tk, tv, a);
     if (st != VSA_OK) return st;

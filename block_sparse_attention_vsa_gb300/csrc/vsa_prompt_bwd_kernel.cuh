@@ -176,16 +176,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   {
     const int slot = (int)(item / (unsigned)a.Hkv);
     k.hk = (int)(item - (unsigned)slot * (unsigned)a.Hkv);
-    // the first keys are seen by the most queries: they come first
-    if (a.seq.packed) {
-      k.b = find_slot(a.seq.k_seq, a.seq.B, a.seq.Sk, 128, slot, &k.tile);
-    } else {
-      k.tile = slot / a.seq.B;
-      k.b = slot - k.tile * a.seq.B;
-    }
-    k.s = load_seq(a.seq, k.b);
-    const int rows = a.seq.packed ? k.s.nk : a.seq.Sk;  // rows that are written
-    k.there = k.tile >= 0 && 128 * k.tile < rows;
+    const Place p = find_tile(a.seq, slot, 7, true);
+    k.s = p.s;
+    k.b = p.b;
+    k.tile = p.tile;
+    k.there = p.there;
     k.nk = clampi(k.s.nk - 128 * k.tile, 0, 128);
     int first = 0;
     if (a.seq.causal) first = clampi(128 * k.tile - (k.s.nk - k.s.nq), 0, k.s.nq);
@@ -433,15 +428,10 @@ __global__ void __launch_bounds__(256) prompt_dkv_join_kernel(const Args a) {
   const int at = (int)((blockIdx.x & 31) * 8 + (threadIdx.x >> 5)), r = at & 127;
   const int lane = (int)lane_id();
   const int slot = (int)(item / (unsigned)a.Hkv), hk = (int)(item - (unsigned)slot * a.Hkv);
-  int b, tile;
-  if (a.seq.packed) {
-    b = find_slot(a.seq.k_seq, a.seq.B, a.seq.Sk, 128, slot, &tile);
-  } else {
-    tile = slot / a.seq.B;
-    b = slot - tile * a.seq.B;
-  }
-  const Seq s = load_seq(a.seq, b);
-  if (tile < 0 || 128ll * tile + r >= (a.seq.packed ? s.nk : a.seq.Sk)) return;
+  const Place p = find_tile(a.seq, slot, 7, true);
+  const Seq& s = p.s;
+  const int tile = p.tile;
+  if (!p.there || 128ll * tile + r >= (a.seq.packed ? s.nk : a.seq.Sk)) return;
   const int T = 128 >> a.pack;
   int first = 0;
   if (a.seq.causal) first = clampi(128 * tile - (s.nk - s.nq), 0, s.nq);
@@ -543,20 +533,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
   const WaitCtx w{&ctl->abort_flag, a.status, a.wait_ns};
-  // the last tokens see the most keys: they come first
+  // (what comes before may run while the predecessor ends)
   after_predecessor();
   const unsigned item = blockIdx.x / (unsigned)a.splits, split = blockIdx.x - item * a.splits;
   const int rank = (int)(item / (unsigned)a.n_packs);
   const int hp = (int)(item - (unsigned)rank * (unsigned)a.n_packs);
-  int b, tile;
-  if (a.seq.packed) {
-    b = find_slot(a.seq.q_seq, a.seq.B, a.seq.Sq, T, a.n_tslots - 1 - rank, &tile);
-  } else {
-    tile = (a.seq.Sq + T - 1) / T - 1 - rank / a.seq.B;
-    b = rank % a.seq.B;
-  }
-  const Seq s = load_seq(a.seq, b);
-  const bool there = tile >= 0 && tile * T < (a.seq.packed ? s.nq : a.seq.Sq);
+  const Place place = find_tile(a.seq, rank, 7 - a.pack, false);
+  const Seq s = place.s;
+  const int b = place.b, tile = place.tile;
+  const bool there = place.there;
   const int off = s.nk - s.nq;
   const int tok0 = tile * T, head0 = hp << a.pack, hk = head0 / a.group;
   int keys = there && tok0 < s.nq ? s.nk : 0;
@@ -851,16 +836,11 @@ __global__ void __launch_bounds__(256) prompt_dq_join_kernel(const Args a) {
   const int T = 128 >> a.pack;
   const int rank = (int)(item / (unsigned)a.n_packs),
             hp = (int)(item - (unsigned)rank * (unsigned)a.n_packs);
-  int b, tile;
-  if (a.seq.packed) {
-    b = find_slot(a.seq.q_seq, a.seq.B, a.seq.Sq, T, a.n_tslots - 1 - rank, &tile);
-  } else {
-    tile = (a.seq.Sq + T - 1) / T - 1 - rank / a.seq.B;
-    b = rank % a.seq.B;
-  }
-  const Seq s = load_seq(a.seq, b);
+  const Place place = find_tile(a.seq, rank, 7 - a.pack, false);
+  const Seq& s = place.s;
+  const int b = place.b, tile = place.tile;
   const int tok0 = tile * T, tok = tok0 + (r & (T - 1)), head = (hp << a.pack) + (r >> (7 - a.pack));
-  if (tile < 0 || tok >= (a.seq.packed ? s.nq : a.seq.Sq)) return;
+  if (!place.there || tok >= (a.seq.packed ? s.nq : a.seq.Sq)) return;
   int keys = tok0 < s.nq ? s.nk : 0;
   if (a.seq.causal) keys = clampi((tok0 + T < s.nq ? tok0 + T : s.nq) + s.nk - s.nq, 0, keys);
   const int steps = (keys + 127) / 128;

@@ -52,7 +52,7 @@ struct FwdArgs {
   long long out_b, out_h, out_t;  // strides in elements
   unsigned int* status;
   int Hq, group, pack;  // query heads a key/value head; log2 of the heads in a tile
-  int n_packs, n_slots;  // head packs, item slots
+  int n_packs;           // head packs
   int n_items;
   int splits;       // ranges of an item's key tiles, a unit of work each
   float* part;      // [n_items * splits] partial results, if there are several
@@ -63,6 +63,7 @@ struct FwdArgs {
 
 namespace fwd {
 
+constexpr unsigned kSms = 152;
 constexpr int kThreads = 384;
 constexpr int kStages = 4;
 constexpr uint32_t kOffQ = 0;  // [2]
@@ -104,27 +105,18 @@ struct Ctl {
 };
 static_assert(sizeof(Ctl) <= 1024, "control block");
 
-// Items in the order of their size for one sequence: the last tokens first, heads inside.
 __device__ __forceinline__ bool decode_item(const FwdArgs& a, int id, Item& it) {
-  const int T = 256 >> a.pack, half = 128 >> a.pack;
+  const int half = 128 >> a.pack;
   const int slot = id / a.n_packs;
   const int hp = id - slot * a.n_packs;
-  int b, tile;
-  if (a.seq.packed) {
-    b = find_slot(a.seq.q_seq, a.seq.B, a.seq.Sq, T, a.n_slots - 1 - slot, &tile);
-  } else {
-    const int per = (a.seq.Sq + T - 1) / T;
-    tile = slot / a.seq.B;
-    b = slot - tile * a.seq.B;
-    tile = per - 1 - tile;
-  }
-  const Seq s = load_seq(a.seq, b);
+  const Place p = find_tile(a.seq, slot, 8 - a.pack, false);
+  const Seq& s = p.s;
   it.z = s.z;
   it.q0 = s.q0;
   it.nq = s.nq;
   it.k0 = s.k0;
   it.nk = s.nk;
-  it.tok = tile * T;
+  it.tok = p.tile << (8 - a.pack);
   it.head0 = hp << a.pack;
   it.kv_head = it.head0 / a.group;
   it.go = 1;
@@ -136,7 +128,7 @@ __device__ __forceinline__ bool decode_item(const FwdArgs& a, int id, Item& it) 
   };
   it.n0 = key_tiles(it.tok);
   it.n1 = key_tiles(it.tok + half);
-  return a.seq.packed ? tile >= 0 && it.tok < s.nq : true;
+  return p.there;
 }
 // A unit: an item, or a range of its key tiles -- the item of a sequence whose keys begin with
 // the range's first (a query attends keys up to its distance from the end, so nothing else
@@ -200,7 +192,9 @@ __device__ __forceinline__ void load_role(const FwdArgs& a, uint8_t* smem, Ctl* 
   uint32_t st = 0, ph = 0, fills = 0, nq0 = 0, nq1 = 0;  // ring position; loads of Q tiles
   const int half = 128 >> a.pack;
   Items items{a, ctl, w};
-  items.ask();
+  // With an SM for each CTA there is nothing to take over: a CTA not launched yet waits only for the
+  // kernel before to leave its SM.
+  if (gridDim.x > kSms) items.ask();
   Item it = ctl->own;
   bool ok = it.go || items.next(it);
   for (uint32_t i = 0; ok; ++i) {

@@ -15,9 +15,9 @@ FLUSH = 2.0 ** -126   # a weight below the least normal fp32 becomes 0: off by t
 def head(q, k, v, causal, scale, dout=None):
     """One sequence and head: (values, bounds) of out, lse, dq, dk, dv.
 
-    P is rounded to bf16 (each weight by HALF at most) for the product with v, and out to bf16;
-    the weights are normalised by what they were rounded to, so out is off by HALF * sum p |v -
-    out| before its own rounding.  dS is rounded to bf16, and carries the error of D = dout .
+    P is rounded to bf16 (each weight by HALF at most) for the product with v, and out to bf16:
+    out is off by HALF * sum p |v| before its own rounding, and by HALF * |out| more if the weights
+    were normalised by what they were rounded to.  dS is rounded to bf16, and carries the error of D = dout .
     out, which is bounded by |dout| . (out's bound)."""
     nq, nk = q.shape[0], k.shape[0]
     z = q @ k.T * scale

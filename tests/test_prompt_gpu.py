@@ -109,6 +109,46 @@ def test_lengths(nq, nk, causal):
     check_packed(nq, nk, 4, 2, causal, sum(nq) + sum(nk))
 
 
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("B,most,Hq,Hkv", [(2, 700, 32, 32), (31, 300, 6, 6), (32, 300, 12, 2),
+                                           (33, 300, 6, 6)], ids=str)
+def test_more_tiles_than_start_at_once(B, most, Hq, Hkv, causal):
+    """Sequences of unlike and of equal lengths, some of nothing, whose tiles come in turn; packed,
+    then the same padded, with 0 behind them."""
+    g = gen(B)
+    nq = torch.randint(0, most, (B,), generator=g).tolist()
+    nk = torch.randint(0, most, (B,), generator=g).tolist()
+    nq[0] = nk[0] = most
+    nq[-1], nk[-1] = nq[B // 2], nk[B // 2] = 129, most
+    if B > 2:
+        nq[3], nk[5], nq[7], nk[7] = 0, 0, 0, 0
+    aq, ak = starts(nq), starts(nk)
+    q, k, v, dout = (randn((n + 9, h, D), g)
+                     for n, h in ((aq[-1], Hq), (ak[-1], Hkv), (ak[-1], Hkv), (aq[-1], Hq)))
+    got = both(q, k, v, dout, q_seq=i32(aq), k_seq=i32(ak), causal=causal)
+    flat = {n: t if n == "lse" else t.transpose(0, 1) for n, t in got.items()}
+    want, bound = ref.attend(*(x.transpose(0, 1) for x in (q, k, v)), nq, nk, aq[:-1], ak[:-1],
+                             causal, None, dout.transpose(0, 1))
+    hold(flat, want, bound)
+
+    def pad(x, at, n):
+        y = torch.full((B, x.shape[1], most + 3, D), math.nan, dtype=x.dtype, device=DEV)
+        for b in range(B):
+            y[b, :, :n[b]] = x[at[b]:at[b] + n[b]].transpose(0, 1)
+        return y
+
+    pads = both(pad(q, aq, nq), pad(k, ak, nk), pad(v, ak, nk), pad(dout, aq, nq), q_seq=i32(nq),
+                k_seq=i32(nk), causal=causal)
+    # (not the bits of the packed call: a batch of fewer tiles than SMs is cut into more ranges)
+    for b in range(B):
+        rows = {"out": (aq, nq), "lse": (aq, nq), "dq": (aq, nq), "dk": (ak, nk), "dv": (ak, nk)}
+        at = {n: slice(a[b], a[b] + m[b]) for n, (a, m) in rows.items()}
+        hold({n: pads[n][b][:, :rows[n][1][b]] for n in rows},
+             {n: want[n][:, at[n]] for n in rows}, {n: bound[n][:, at[n]] for n in rows})
+        for n in ("out", "dq", "dk", "dv"):
+            assert (pads[n][b][:, rows[n][1][b]:] == 0).all(), (n, b)
+
+
 def test_rows_of_no_sequence_are_left_alone():
     g = gen(5)
     q, k, v, dout = (randn((300, h, D), g) for h in (4, 2, 2, 4))
