@@ -53,6 +53,7 @@ vsa_status vsa_pages_free(int32_t* table, const int32_t* lens, int B, int Hkv, i
   host_set_launches(0);
   if (B < 0 || Hkv < 0 || max_blocks < 0 || pages < 0) return VSA_ERR_INVALID_ARG;
   if (!block_ok(block)) return VSA_ERR_UNSUPPORTED;
+  if ((long long)B * Hkv > INT_MAX) return VSA_ERR_UNSUPPORTED;
   const long long entries = (long long)B * Hkv * max_blocks;
   if (entries > INT_MAX) return VSA_ERR_UNSUPPORTED;
   if (entries == 0) return VSA_OK;
@@ -79,8 +80,9 @@ vsa_status vsa_pages_reserve(int32_t* table, const int32_t* lens, const int32_t*
   host_set_launches(0);
   if (B < 0 || Hkv < 0 || max_blocks < 0 || pages < 0) return VSA_ERR_INVALID_ARG;
   if (!block_ok(block)) return VSA_ERR_UNSUPPORTED;
+  if ((long long)B * Hkv > INT_MAX) return VSA_ERR_UNSUPPORTED;
   const long long entries = (long long)B * Hkv * max_blocks;
-  if (entries > INT_MAX || (long long)B * Hkv > INT_MAX) return VSA_ERR_UNSUPPORTED;
+  if (entries > INT_MAX) return VSA_ERR_UNSUPPORTED;
   if (B == 0) return VSA_OK;
   if (!lens || !lacking || !host_aligned4(lens) || !host_aligned4(n_new) ||
       !host_aligned4(lacking))
@@ -111,10 +113,10 @@ vsa_status vsa_cache_fork(const int32_t* table, const int32_t* lens, const int32
   host_set_launches(0);
   if (B < 0 || N < 0 || Hkv < 0 || max_blocks < 0 || pages < 0) return VSA_ERR_INVALID_ARG;
   if (D != VSA_HEAD_DIM || !block_ok(block)) return VSA_ERR_UNSUPPORTED;
-  const long long rows = (long long)N * Hkv, entries = rows * max_blocks,
-                  held = (long long)B * Hkv * max_blocks;
-  if (rows > INT_MAX || entries > INT_MAX || held > INT_MAX ||
-      (long long)max_blocks * block > INT_MAX)
+  const long long rows = (long long)N * Hkv;
+  if (rows > INT_MAX || (long long)B * Hkv > INT_MAX) return VSA_ERR_UNSUPPORTED;
+  const long long entries = rows * max_blocks, held = (long long)B * Hkv * max_blocks;
+  if (entries > INT_MAX || held > INT_MAX || (long long)max_blocks * block > INT_MAX)
     return VSA_ERR_UNSUPPORTED;
   if (N == 0) return VSA_OK;
   if (!parent || !lens_out || !lacking || !host_aligned4(parent) || !host_aligned4(lens_out) ||
@@ -159,6 +161,7 @@ vsa_status vsa_cache_compact(int32_t* table, int B, int Hkv, int D, int max_bloc
   host_set_launches(0);
   if (B < 0 || Hkv < 0 || max_blocks < 0 || pages < 0) return VSA_ERR_INVALID_ARG;
   if (D != VSA_HEAD_DIM || !block_ok(block)) return VSA_ERR_UNSUPPORTED;
+  if ((long long)B * Hkv > INT_MAX) return VSA_ERR_UNSUPPORTED;
   const long long entries = (long long)B * Hkv * max_blocks;
   if (entries > INT_MAX) return VSA_ERR_UNSUPPORTED;
   if (!n_used || !host_aligned4(n_used)) return VSA_ERR_INVALID_ARG;

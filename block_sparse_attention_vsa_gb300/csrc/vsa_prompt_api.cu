@@ -61,7 +61,9 @@ bool view_ok(const View& v) {
   if (!v.p || !host_aligned16(v.p)) return false;
   for (long long s : {v.sb, v.sh, v.st})
     if (s < VSA_HEAD_DIM || s % 8 != 0 || s >= (1ll << 38)) return false;
-  return true;
+  // (beyond any address; what is left adds up in 64 bits)
+  constexpr double kMost = 1ll << 56;
+  return (double)v.nb * v.sb < kMost && (double)v.nh * v.sh < kMost && (double)v.nt * v.st < kMost;
 }
 
 // Whether the rows of a result lie apart: every stride spans what the smaller ones reach.
@@ -141,6 +143,12 @@ vsa_status prepare(Kern kern, int dev, int slot, uint32_t smem, int threads, uin
   return (long long)k.regs * threads < (long long)pool ? VSA_ERR_UNSUPPORTED : VSA_OK;
 }
 
+// (More rows than any memory holds are refused, so that counts of them fit 64 bits.)
+bool too_many(int packed, int B, int Hq, int Hkv, int Sq, int Sk) {
+  constexpr double kMost = 1ll << 40;
+  const double n = packed ? 1 : B;
+  return n * Hq * Sq > kMost || n * Hkv * Sk > kMost || (double)B * Hq > kMost;
+}
 // What both directions check: sizes, heads, types of sequence arrays.
 struct Shape {
   const int32_t *q_seq, *k_seq;
@@ -156,7 +164,8 @@ vsa_status check_shape(const Shape& p) {
   if (p.packed && p.B > 0 && (!p.q_seq || !p.k_seq)) return VSA_ERR_INVALID_ARG;
   // row coordinates, and with 128 rows behind them, stay below 2^31
   const long long most = INT_MAX - 1024;
-  if (p.Sq > most || p.Sk > most) return VSA_ERR_UNSUPPORTED;
+  if (p.Sq > most || p.Sk > most || too_many(p.packed, p.B, p.Hq, p.Hkv, p.Sq, p.Sk))
+    return VSA_ERR_UNSUPPORTED;
   return VSA_OK;
 }
 prompt::SeqArgs seq_args(const Shape& p) {
@@ -249,7 +258,9 @@ bool meets_seq(const Shape& p, const void* x, long long bytes) {
 extern "C" {
 
 size_t vsa_fwd_prompt_workspace_bytes(int packed, int B, int Hq, int Hkv, int Sq, int Sk) {
-  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Sq < 1 || Sk < 0) return 0;
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Sq < 1 || Sk < 0 ||
+      too_many(packed, B, Hq, Hkv, Sq, Sk))
+    return 0;
   const long long items = fwd_items(packed, B, Hq, Hkv, Sq);
   const int n = key_splits(items, Sk);
   return n > 1 ? (size_t)(items * n) * prompt::fwd::kPartFloats * sizeof(float) : 0;
@@ -337,7 +348,9 @@ vsa_status vsa_fwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
 }
 
 size_t vsa_bwd_prompt_workspace_bytes(int packed, int B, int Hq, int Hkv, int Sq, int Sk) {
-  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Sq < 0 || Sk < 0) return 0;
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Sq < 0 || Sk < 0 ||
+      too_many(packed, B, Hq, Hkv, Sq, Sk))
+    return 0;
   return bwd_layout(packed, B, Hq, Hkv, Sq, Sk).total;
 }
 

@@ -458,7 +458,7 @@ VSA_API vsa_status vsa_cache_evict(const float *weight, const int32_t *table,
  * lowest first, in the order of the entries (b, h, j) that ask for them, so every outcome is
  * unique.  Calls on one pool must not overlap on the GPU.  A page that several sequences name
  * is one that none of them writes: vsa_cache_fork shares full blocks only, and a write goes
- * behind those.  B * Hkv * max_blocks (and N * Hkv * max_blocks) < 2^31.
+ * behind those.  B * Hkv, B * Hkv * max_blocks (and those of N) < 2^31.
  * ------------------------------------------------------------------------------------- */
 
 /* Lets pages go: every entry of table [B, Hkv, max_blocks] from block ceil(lens[b] / block) on
@@ -535,6 +535,8 @@ VSA_API vsa_status vsa_cache_compact(int32_t *table, int B, int Hkv, int D, int 
  * slices of a fused projection's output go in as they are, and outputs may be slices of one
  * buffer.  Outputs must not share elements with inputs or with one another.  (Broadcast
  * tensors, with a stride of 0, are refused: copy them first.)
+ * Sizes.  Sq, Sk <= 2^31 - 1025; B * Hq, and the rows of all heads of a tensor, <= 2^40, and
+ * fewer than 2^31 tiles of 128 rows; more is refused.
  * ------------------------------------------------------------------------------------- */
 
 /* Forward.

@@ -75,6 +75,9 @@ def with_strides(i, values, base=rows(4) + 2 * rows(2) + rows(4)):
     (dict(ws=4 * MB + 8, n=1 << 30), INVALID), (dict(ws=64 * MB, n=1 << 30, Sk=5000), INVALID),
     (dict(ws=4 * MB, n=1 << 30, Sk=5000, lse=4 * MB + 64), INVALID),
     (dict(ws=4 * MB, n=1 << 30, Sk=5000, qs=4 * MB + 64), INVALID),
+    (dict(Sq=1 << 30, s=with_strides(0, [0, D, 1 << 37])), INVALID),  # beyond any address
+    (dict(packed=0, B=1 << 30, Hq=1 << 30, Hkv=1 << 30, Sq=1 << 30), UNSUPPORTED),
+    (dict(B=(1 << 31) - 1, Hq=1 << 30, Hkv=1 << 30), UNSUPPORTED),
 ])
 def test_fwd_prompt_checks(lib, kw, code):
     assert fwd(lib, **kw) == code
@@ -126,6 +129,12 @@ def bwd(lib, **kw):
 ])
 def test_bwd_prompt_checks(lib, kw, code):
     assert bwd(lib, **kw) == code
+
+
+def test_workspaces_of_more_rows_than_memory(lib):
+    big = (0, 1 << 30, 1 << 30, 1 << 30, 1 << 30, 1 << 30)
+    assert lib.vsa_fwd_prompt_workspace_bytes(*big) == 0
+    assert lib.vsa_bwd_prompt_workspace_bytes(*big) == 0
 
 
 def test_fwd_prompt_workspace(lib):
@@ -233,6 +242,11 @@ def compact(lib, **kw):
 ])
 def test_cache_compact_checks(lib, kw, code):
     assert compact(lib, **kw) == code
+
+
+@pytest.mark.parametrize("call", [free, reserve, fork, compact])
+def test_entries_that_pass_64_bits(lib, call):
+    assert call(lib, B=1 << 30, H=1 << 30, mb=16) == UNSUPPORTED
 
 
 @pytest.mark.parametrize("name", ["vsa_prompt_common.cuh", "vsa_prompt_fwd_kernel.cuh",
