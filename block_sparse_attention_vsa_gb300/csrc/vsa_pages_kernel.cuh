@@ -130,26 +130,36 @@ __device__ __forceinline__ int nth_free(const Pool& p, const FreeCount& f, int r
   }
   return -1;
 }
-// Consecutive free pages for a warp: 32 words of the bitmap, one a lane.
+// Consecutive free pages for a warp: those of 16 words of the bitmap, half a word a lane, written
+// out in their order, so that looking one up is a load.  (Searching the words' counts and then the
+// bits of one: 16 prompts of 50,000 tokens in 18.7 us, written out 14.7.)
+constexpr int kWindowWords = 16;
 struct FreeWindow {
   const Pool& p;
   const FreeCount& f;
-  long long w0 = 0;   // first word
-  uint32_t word = 0;
-  int base = 0, upto = 0;  // free pages before the window; before it and up to the lane's word
-  int end = 0;             // before it and in it
+  uint16_t* list;        // [32 * kWindowWords] of the warp: pages behind the window's first
+  long long w0 = 0;      // first word
+  int base = 0, end = 0; // free pages before the window; before it and in it
 
+  // (places that lanes write, or read, together lie in different banks)
+  static __device__ __forceinline__ int place(int i) { return i ^ ((i >> 6 & 7) << 1); }
   __device__ __forceinline__ void load() {
-    const long long w = w0 + (int)(threadIdx.x & 31);
-    word = w < f.words ? free_word(p, w) : 0u;
-    upto = __popc(word);
+    const int lane = (int)threadIdx.x & 31;
+    const long long w = w0 + (lane >> 1);
+    uint32_t x = w < f.words ? free_word(p, w) : 0u;
+    x = lane & 1 ? x >> 16 : x & 0xffffu;
+    int at = __popc(x);
+    const int mine = at;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, upto, o);
-      if ((int)(threadIdx.x & 31) >= o) upto += y;
+      const int y = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += y;
     }
-    upto += base;
-    end = __shfl_sync(0xffffffffu, upto, 31);
+    end = base + __shfl_sync(0xffffffffu, at, 31);
+    __syncwarp();  // (the list has been read)
+    for (at -= mine; x != 0; x &= x - 1)
+      list[place(at++)] = (uint16_t)(16 * lane + __ffs((int)x) - 1);
+    __syncwarp();
   }
   // places the window on the r-th free page's thread
   __device__ __forceinline__ void seek(int r) {
@@ -162,26 +172,18 @@ struct FreeWindow {
     load();
   }
   // The r-th free page for the lanes that want one (ranks ascend with the lane and from call
-  // to call); -1 where there are not as many.
-  __device__ __forceinline__ int get(bool want, int r) {
+  // to call; all are below `upto`); -1 where there are not as many.
+  __device__ __forceinline__ int get(bool want, int r, int upto) {
     int page = -1;
+    if (upto <= end) return want ? (int)(w0 * 32) + list[place(r - base)] : page;
     bool open = want && r < f.total;
     while (true) {
-      const bool here = open && r < end;
-      // the word that holds it: the first whose count passes r
-      int at = 0;
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1)
-        if (__shfl_sync(0xffffffffu, upto, at + s - 1) <= r) at += s;
-      at &= 31;
-      const uint32_t x = __shfl_sync(0xffffffffu, word, at);
-      const int before = __shfl_sync(0xffffffffu, upto, at) - __popc(x);
-      if (here) {
-        page = (int)((w0 + at) * 32) + nth_bit(x, r - before);
+      if (open && r < end) {
+        page = (int)(w0 * 32) + list[place(r - base)];
         open = false;
       }
-      if (!__any_sync(0xffffffffu, open) || w0 + 32 >= f.words) return page;
-      w0 += 32;
+      if (!__any_sync(0xffffffffu, open) || w0 + kWindowWords >= f.words) return page;
+      w0 += kWindowWords;
       base = end;
       load();
     }
@@ -278,6 +280,7 @@ __device__ __forceinline__ int cluster_before(PagesShared& s, int asked, int* al
 // warp takes one after another, several entries a lane under way.
 __global__ void __launch_bounds__(kPagesThreads) pages_reserve_kernel(const ReserveArgs a) {
   __shared__ PagesShared s;
+  __shared__ uint16_t s_list[kPagesThreads / 32][32 * kWindowWords];
   auto cluster = cooperative_groups::this_cluster();
   const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
   const int lane = (int)threadIdx.x & 31;
@@ -376,7 +379,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_reserve_kernel(const Rese
   at = __shfl_sync(0xffffffffu, at, 0);
   at += cluster_before(s, in_cta, &all);
   if (asked > 0) {
-    FreeWindow window{a.pool, f};
+    FreeWindow window{a.pool, f, s_list[threadIdx.x >> 5]};
     for (unsigned rb = r0; rb < r1; rb += 32) {
       if (r1 - r0 > 32) x = range(rb + lane);
       if (__all_sync(0xffffffffu, x.last - x.first <= kFew)) {
@@ -412,12 +415,14 @@ __global__ void __launch_bounds__(kPagesThreads) pages_reserve_kernel(const Rese
           for (int i = 0; i < kEntries; ++i) {
             const uint32_t votes = __ballot_sync(0xffffffffu, want[i]);
             if (votes == 0) continue;
-            const int p = window.get(want[i], at + __popc(votes & ((1u << lane) - 1u)));
+            const int r = at + __popc(votes & ((1u << lane) - 1u));
             at += __popc(votes);
+            const int p = window.get(want[i], r, at);
             if (want[i]) {
               if (p >= 0) a.pool.refs[p] = 1;
               y.row[j + 32 * i] = p;
             }
+            if (at <= f.total) continue;
             const uint32_t none = __ballot_sync(0xffffffffu, want[i] && p < 0);
             if (none && lane == 0) atomicAdd(a.lacking + y.b, __popc(none));
           }
