@@ -18,9 +18,14 @@ constexpr int kSms = 152;  // of a GB300, which host_device() asks for
 
 bool block_ok(int block) { return block == 64 || block == 128; }
 
-// CTAs that divide so many table entries among them, one cluster: one where its barriers would
-// take longer than the entries.
-int pages_ctas(long long entries) { return entries <= (1 << 17) ? 1 : kPagesCluster; }
+// CTAs that divide the rows of a table among them, one cluster: one CTA where its barriers would
+// take longer than the rows (us of one CTA and of eight: room for a token in 512 rows 6.2 and 7.6,
+// 2,048 rows 11.5 and 7.8; forks of 512 rows 8.0 and 9.8, 2,048 rows 15.8 and 14.6) or, of long
+// prompts, their entries.  How many of those are asked for only the device knows: a token in each of
+// 512 rows of 129 blocks takes 5.9 and 7.6, 8,000 tokens 49 and 13; the former come far more often.
+int pages_ctas(long long rows, long long entries) {
+  return rows <= 1024 && entries <= (1 << 17) ? 1 : kPagesCluster;
+}
 
 size_t words(int pages) { return ((size_t)pages + 31) / 32; }
 
@@ -99,7 +104,7 @@ vsa_status vsa_pages_reserve(int32_t* table, const int32_t* lens, const int32_t*
   if (st != VSA_OK) return st;
   const ReserveArgs a{{refs, free_bits, pages}, table, lens, n_new, lacking, B, Hkv, max_blocks,
                       block};
-  const int ctas = pages_ctas(entries);
+  const int ctas = pages_ctas((long long)B * Hkv, entries);
   return launch(pages_reserve_kernel, dim3(ctas), kPagesThreads, 0,
                 reinterpret_cast<cudaStream_t>(stream), ctas, a);
 }
@@ -145,7 +150,7 @@ vsa_status vsa_cache_fork(const int32_t* table, const int32_t* lens, const int32
                    table, lens, parent, table_out, lens_out, lacking, B, N, Hkv,
                    max_blocks, block};
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int ctas = pages_ctas(32 * rows);  // (a row's look-ups and its page: some 32 entries)
+  const int ctas = pages_ctas(rows, 0);
   st = launch(pages_fork_kernel, dim3(ctas), kPagesThreads, 0, s, ctas, a);
   if (st != VSA_OK || entries == 0) return st;
   st = launch(cache_fork_kernel, dim3((unsigned)rows), 256, 0, s, 0, a);

@@ -171,6 +171,40 @@ def test_fork(c, N):
         assert x is None and y is None or torch.equal(x, y)
 
 
+# divided among several CTAs: many rows, and rows of many blocks
+MANY = [(140, 8, 6, 64, 4000, 300), (17, 8, 1000, 64, 6000, 1000)]
+
+
+@pytest.mark.parametrize("c,more", [(MANY[0], "one"), (MANY[0], "some"), (MANY[0], "all"),
+                                    (MANY[1], "one"), (MANY[1], "some")], ids=str)
+def test_reserve_of_large_tables(c, more):
+    test_reserve(c, more)
+
+
+def test_reserve_of_long_prompts():
+    """Among short ones, out of a pool with holes of all sizes, whose end some do not get."""
+    B, H, mb, pages = 17, 8, 1000, 9000
+    r = random.Random(21)
+    refs = [int(r.random() < (p % 1000) / 1000) for p in range(pages)]
+    held = [p for p in range(pages) if refs[p]]
+    table = [[[-1] * mb for _ in range(H)] for _ in range(B)]
+    for p in held[:2000]:  # entries that have a page already, anywhere
+        b, h, j = r.randrange(B), r.randrange(H), r.randrange(60)
+        if table[b][h][j] < 0:
+            table[b][h][j] = p
+    lens = [r.randint(0, 2000) for _ in range(B)]
+    new = [r.choice([0, 1, 70, 300, 9000, 40_000]) for _ in range(B)]
+    pool, t = to_pool(refs), i32(table)
+    lacking = binding.vsa_pages_reserve(pool, t, i32(lens), i32(new))
+    want = ref.reserve(refs, table, lens, new, 64)
+    assert sum(want) > 0 and lacking.tolist() == want and t.tolist() == table
+    same_pool(pool, refs)
+
+
+def test_fork_of_many_rows():
+    test_fork(MANY[0], 150)
+
+
 @pytest.mark.parametrize("c", CASES, ids=str)
 @pytest.mark.parametrize("full", [False, True], ids=["holes", "full"])
 def test_compact(c, full):
