@@ -383,7 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) scores(0);
         for (int g = 0; g < k.steps && ok; ++g) {
           const bool more = g + 1 < k.steps;
-          ok = (!more || (x ? g_in(g + 1) : q_in(g + 1))) && wait_warp(ready, g & 1, w, 0x2d) &&
+          // the next scores' operands; P or dS; the gradient product's own tile, which for dK is
+          // there already (g_in(g) was waited for, and warp 11 hands Q on before dO)
+          ok = (!more || (x ? g_in(g + 1) : q_in(g + 1))) && (x || g_in(g)) &&
+               wait_warp(ready, g & 1, w, 0x2d) &&
                ((x == 0 && g == 0) || wait_warp(&ctl->turn[x], (x ? g : g - 1) & 1, w, 0x32));
           if (!ok) break;
           const uint32_t st = x ? (uint32_t)(g % kQStages) : (uint32_t)(g % kGStages);

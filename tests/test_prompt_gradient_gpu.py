@@ -1,0 +1,71 @@
+"""The gradient of the attention over whole prompts where its kernels' single parts show: one
+step a tile, what lies around a sequence, and copies that come late."""
+import math
+
+import pytest
+import torch
+
+import prompt_ref as ref
+from block_sparse_attention_vsa_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+D = 128
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def randn(shape, g, mul=1.0):
+    return (torch.randn(shape, generator=g) * mul).to(torch.bfloat16).to(DEV)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def ok():
+    torch.cuda.synchronize()
+    code, detail = binding.vsa_device_status()
+    assert code == binding.VSA_OK, hex(detail)
+
+
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 4), (16, 4)], ids=str)
+def test_sequences_of_one_step_with_anything_behind_them(Hq, Hkv, causal):
+    """Every key tile sees one query tile, whose rows behind the sequence hold NaN; dout is fetched
+    from memory each time, so that its copy lands last."""
+    g = gen(60)
+    B, S = 64, 200
+    most = 128 * Hkv // Hq  # tokens of a query tile
+    n = [1 + (b * 37) % (most - 1) for b in range(B)]
+    q, k, v, dout = (randn((B, h, S, D), g) for h in (Hq, Hkv, Hkv, Hq))
+    for b in range(B):
+        for t in (q, k, v, dout):
+            t[b, :, n[b]:] = math.nan
+    out, lse = binding.vsa_fwd_prompt(q, k, v, i32(n), causal=causal)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device=DEV)
+    first = None
+    for _ in range(20):
+        flush.zero_()
+        for t in (q, k, v):
+            t.add_(0)
+        grads = binding.vsa_bwd_prompt(q, k, v, out, dout, lse, i32(n), causal=causal)
+        first = first or grads
+        for x, y in zip(first, grads):
+            assert torch.equal(x, y)
+    ok()
+    for b in range(0, B, 9):
+        want, bound = ref.attend(q[b], k[b], v[b], [n[b]], [n[b]], [0], [0], causal, None, dout[b])
+        for x, name in zip(first, ("dq", "dk", "dv")):
+            there = slice(0, n[b])
+            err = (x[b, :, there].double() - want[name][:, there]).abs()
+            assert (err <= bound[name][:, there]).all(), (name, b)
+            assert (x[b, :, n[b]:] == 0).all(), (name, b)
