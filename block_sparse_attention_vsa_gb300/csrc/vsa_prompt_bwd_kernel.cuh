@@ -42,8 +42,8 @@
 //
 // 12 warps: 0-7 gradient warps (thread = lane of the tile, warpgroup w = columns 64 w ..),
 // 8 TMA, 9 and 10 MMA issuers, 11 hands landed tiles on to them and zeroes rows that are not the
-// sequence's first: they get weight 0, but 0 times what lies there (another sequence, padding)
-// may be NaN.
+// sequence's, and queries that attend nothing, first: they get weight 0, but 0 times what lies
+// there (another sequence, padding, a dout of anything) may be NaN.
 #pragma once
 
 #include "vsa_prompt_common.cuh"
@@ -405,14 +405,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == 11) {
       int ti = k.n_tok ? k.first + k.step0 % k.n_tok : 0;
+      const int none = a.seq.causal ? k.s.nq - k.s.nk : 0;  // first queries, that attend nothing
       for (int g = 0; g < k.steps; ++g) {
         const int qs = g % kQStages, gs = g % kGStages;
-        const int valid = k.s.nq - ti * T;  // tokens of the tile
+        const int from = none - ti * T, to = k.s.nq - ti * T;  // tokens of the tile that count
+        const bool clean = from > 0 || to < T;
         if (!wait_warp(&ctl->q_full[qs], (g / kQStages) & 1, w, 0x30)) break;
-        if (valid < T) zero_tokens(smem + kOffQ + qs * kTile, valid, T);
+        if (clean) zero_tokens(smem + kOffQ + qs * kTile, from, to, T);
         if (lane == 0) mbar_arrive(&ctl->q_ready[qs]);
         if (!wait_warp(&ctl->g_full[gs], (g / kGStages) & 1, w, 0x31)) break;
-        if (valid < T) zero_tokens(smem + kOffG + gs * kTile, valid, T);
+        if (clean) zero_tokens(smem + kOffG + gs * kTile, from, to, T);
         if (lane == 0) mbar_arrive(&ctl->g_ready[gs]);
         if (++ti == k.first + k.n_tok) ti = k.first;
       }
@@ -572,9 +574,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&ctl->x_full[warp & 3]);
       return wait_warp(&ctl->x_full[warp & 3], n, w, 0x50);
     };
+    int lim = s.nk;  // keys this row attends
+    if (a.seq.causal) lim = clampi(tok + 1 + off, 0, s.nk);
     // the row's -lse (-infinity where it attends nothing, or is none of the sequence's, so that
-    // every p of it is 0) and -D = -sum_d dout out, this warpgroup's half of the columns
-    const bool in = there && tok < s.nq;
+    // every p of it is 0) and -D = -sum_d dout out (0 there, whatever dout holds), this
+    // warpgroup's half of the columns
+    const bool in = there && tok < s.nq && lim > 0;
     float nlse = -INFINITY, part_d = 0.0f;
     if (in) {
       const int head = head0 + (r >> (7 - a.pack));
@@ -611,9 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       st[r] = nlse;
       st[128 + r] = in ? nD : 0.0f;
     }
-    int lim = s.nk;  // keys this row attends, counted from the range's first
-    if (a.seq.causal) lim = clampi(tok + 1 + off, 0, s.nk);
-    lim -= 128 * step0;
+    lim -= 128 * step0;  // counted from the range's first key
     const uint64_t c2 = f32x2(a.scale_log2, a.scale_log2), l2 = f32x2(nlse, nlse),
                    d2 = f32x2(nD, nD);
     for (int g = 0; g < steps && ok; ++g) {

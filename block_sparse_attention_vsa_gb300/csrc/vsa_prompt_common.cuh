@@ -207,14 +207,16 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int n) {
   __syncwarp();
 }
 
-// The rows of a query tile (row = head * T + token) whose token is not among the first n.
-__device__ __forceinline__ void zero_tokens(uint8_t* tile, int n, int T) {
+// The rows of a query tile (row = head * T + token) whose token is not in [from, to).
+__device__ __forceinline__ void zero_tokens(uint8_t* tile, int from, int to, int T) {
   const int lane = (int)lane_id();
-  for (int i = lane; i < 128 * 8; i += 32)
-    if (((i >> 3) & (T - 1)) >= n) {
+  for (int i = lane; i < 128 * 8; i += 32) {
+    const int t = (i >> 3) & (T - 1);
+    if (t < from || t >= to) {
       reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
       reinterpret_cast<uint4*>(tile + kTile / 2)[i] = make_uint4(0, 0, 0, 0);
     }
+  }
   fence_proxy_async_smem();
   __syncwarp();
 }

@@ -567,8 +567,10 @@ VSA_API size_t vsa_fwd_prompt_workspace_bytes(int packed, int B, int Hq, int Hkv
  * forward, D_i = dout_i . out_i and ds_ij = p_ij (dout_i . v_j - D_i):
  *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dout_i,
  * dk and dv summed over the query heads of a key/value head.  Rows that attend nothing get
- * dq = 0, keys that nothing attends dk = dv = 0; rows of no sequence as in the forward (packed:
- * not written; padded: 0).
+ * dq = 0 and reach no dk or dv, whatever q and dout hold there; keys that nothing attends get
+ * dk = dv = 0; rows of no sequence as in the forward (packed: not written; padded: 0).  Of rows
+ * that attend something, a NaN or infinity in q or dout reaches dk and dv of all keys of the key
+ * tiles that their query tile walks over.
  *   q, k, v, q_seq, k_seq, sizes, causal, scale: as given to the forward; out, lse what it
  *           returned; dout as out.
  *   strides int64 [24]: (batch, head, token) of q, k, v, out, dout, dq, dk, dv.

@@ -69,3 +69,36 @@ def test_sequences_of_one_step_with_anything_behind_them(Hq, Hkv, causal):
             err = (x[b, :, there].double() - want[name][:, there]).abs()
             assert (err <= bound[name][:, there]).all(), (name, b)
             assert (x[b, :, n[b]:] == 0).all(), (name, b)
+
+
+@pytest.mark.parametrize("nq,nk,Hq,Hkv", [
+    ([200, 130], [3, 129], 4, 2), ([300], [40], 2, 2), ([513], [257], 1, 1), ([90, 1], [0, 1], 6, 2),
+    ([1100], [90], 6, 1), ([700, 260], [330, 130], 16, 1)], ids=str)
+@pytest.mark.parametrize("bad", [math.nan, math.inf], ids=["nan", "inf"])
+def test_rows_that_attend_nothing_reach_nothing(nq, nk, Hq, Hkv, bad):
+    """More queries than keys, causal: the first queries' q and dout may hold anything."""
+    g = gen(61)
+    aq, ak = [0], [0]
+    for x, y in zip(nq, nk):
+        aq.append(aq[-1] + x)
+        ak.append(ak[-1] + y)
+    q, k, v, dout = (randn((n, h, D), g)
+                     for n, h in ((aq[-1], Hq), (ak[-1], Hkv), (ak[-1], Hkv), (aq[-1], Hq)))
+
+    def run():
+        out, lse = binding.vsa_fwd_prompt(q, k, v, i32(aq), i32(ak))
+        grads = binding.vsa_bwd_prompt(q, k, v, out, dout, lse, i32(aq), i32(ak))
+        ok()
+        return dict(out=out, lse=lse.T, dq=grads[0], dk=grads[1], dv=grads[2])
+
+    none = torch.zeros(aq[-1], dtype=torch.bool, device=DEV)
+    for a, x, y in zip(aq, nq, nk):
+        none[a:a + max(0, x - y)] = True
+    q[none], dout[none] = 0.0, 0.0
+    want = run()
+    q[none], dout[none] = bad, bad
+    dout[none, :, ::2] = -bad
+    got = run()
+    for name in want:
+        assert torch.equal(got[name], want[name]), name
+    assert (got["dq"][none] == 0).all()

@@ -31,10 +31,10 @@ DKV = {
     "grad s": "!wait_warp(&ctl->s_full, g & 1, w, 0x21)",
     "grad dp": "!wait_warp(&ctl->dp_full, g & 1, w, 0x22)",
     "clean q": "if (!wait_warp(&ctl->q_full[qs], (g / kQStages) & 1, w, 0x30)) break; "
-               "if (valid < T) zero_tokens(smem + kOffQ + qs * kTile, valid, T); "
+               "if (clean) zero_tokens(smem + kOffQ + qs * kTile, from, to, T); "
                "if (lane == 0) mbar_arrive(&ctl->q_ready[qs]);",
     "clean g": "if (!wait_warp(&ctl->g_full[gs], (g / kGStages) & 1, w, 0x31)) break; "
-               "if (valid < T) zero_tokens(smem + kOffG + gs * kTile, valid, T); "
+               "if (clean) zero_tokens(smem + kOffG + gs * kTile, from, to, T); "
                "if (lane == 0) mbar_arrive(&ctl->g_ready[gs]);",
     "load q": "!wait(&ctl->q_empty[qs], (g / kQStages + 1) & 1, w, 0x24)",
     "load g": "!wait(&ctl->g_empty[gs], (g / kGStages + 1) & 1, w, 0x25)",
