@@ -1054,7 +1054,8 @@ def fwd_prompt_workspace_bytes(packed, B, Hq, Hkv, Sq, Sk) -> int:
 def vsa_bwd_prompt(q, k, v, out, dout, lse, q_seq=None, k_seq=None, causal=True, scale=None,
                    dq=None, dk=None, dv=None, workspace=None, stream=None):
     """Gradient of vsa_fwd_prompt: dq, dk, dv for an upstream gradient dout, given the forward's
-    out and lse; the rest as given to the forward.  dq, dk, dv may be given, as slices of one
+    out and lse (of all parts, joined, where k and v are a part of the keys: dq is then the sum of
+    the parts'); the rest as given to the forward.  dq, dk, dv may be given, as slices of one
     buffer for instance.  The workspace (uint8, bwd_prompt_workspace_bytes) is allocated if
     not given."""
     if stream is None:

@@ -10,11 +10,16 @@
 //                       walks the key tiles: S = Q K^T, dP = dO V^T, dS, dQ += dS K.  It sets
 //                       out with the rows' D and leaves -lse and -D for the other kernel, in
 //                       the order of the query tiles.
-//                       out is rounded to bf16, and D with it; but a row's dS add up to 0, so
-//                       what they come to is that error: it is taken off D for the next
-//                       kernel, and here off the dS of rows of one key tile, where out is
-//                       large (elsewhere it is the mean of many v).  12 heads of up to 411
-//                       tokens: dk and dq off by 0.0024 (relative, in norm), not 0.0025.
+//                       out is rounded to bf16, and D with it; but where a row's p add up to 1
+//                       its dS add up to 0, so what they come to is that error: it is taken off
+//                       D for the next kernel, and here off the dS of rows of one key tile.
+//                       (Relative errors in norm, with and without: 12 heads of up to 411 tokens
+//                       dk and dq 0.0024 and 0.0026, sequences of 2 to 16 tokens 0.0024 and
+//                       0.0030; inputs three times as large, 400 tokens, dk 0.0023 and 0.0055.)
+//                       Where they add up to something else, lse being over more keys than this
+//                       call's, D stays as it is.  kWhole tells the two apart: a row whose other
+//                       keys weigh that little or less has D off by kWhole dout . (what out is
+//                       over these keys, less what over those), about half of the rounding's.
 //   prompt_dkv_kernel   a CTA per key tile of 128 keys and key/value head: K and V stay in
 //                       shared memory, dK and dV add up in TMEM while it walks the query
 //                       tiles that see the keys.  Per step, transposed (lanes = keys):
@@ -473,7 +478,8 @@ constexpr uint32_t kOffCtl = kOffXch + 2048;
 constexpr uint32_t kSmemBytes = kOffCtl + 1024;  // (the base is aligned)
 static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 constexpr uint32_t kColS = 0, kColDP = 128, kColDQ = 384;  // dP twice
-constexpr int kPartFloats = 128 * 128 + 128;  // of a range: dQ and the rows' sums of dS
+constexpr int kPartFloats = 128 * 128 + 128;  // of a range: dQ (and 128 that stay unused)
+constexpr float kWhole = 1.0f / 2048.0f;
 
 struct Ctl {
   uint64_t q_full;
@@ -566,13 +572,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok = tok0 + (r & (T - 1));
     float* st = a.stats + ((long long)hp * a.n_tslots + query_slot(a, b, s.q0, tile)) * 256;
     float* xch = reinterpret_cast<float*>(smem + kOffXch);  // [2][2][128]
-    uint64_t sum2 = f32x2(0.0f, 0.0f);                      // of the row's dS
-    // with the warp that has the rows' other columns, twice: -D, then the sums of dS
-    auto exchange = [&](int n, float x) {
-      xch[256 * n + 128 * wg + r] = x;
+    uint64_t sum2 = f32x2(0.0f, 0.0f), sump = sum2;         // of the row's dS, of its p
+    // with the warp that has the rows' other columns
+    auto meet = [&](uint32_t parity) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->x_full[warp & 3]);
-      return wait_warp(&ctl->x_full[warp & 3], n, w, 0x50);
+      return wait_warp(&ctl->x_full[warp & 3], parity, w, 0x50);
+    };
+    // what the row's dS come to, if that is the rounding of out in D, else 0
+    float rest = 0.0f;
+    auto find_rest = [&] {
+      float s0, s1, p0, p1;
+      split_f32x2(sum2, s0, s1);
+      split_f32x2(sump, p0, p1);
+      // (where D was, once the other warp has read it)
+      if (!wait_warp(&ctl->x_full[warp & 3], 1, w, 0x50)) return false;
+      xch[128 * wg + r] = s0 + s1;
+      xch[256 + 128 * wg + r] = p0 + p1;
+      if (!meet(0)) return false;
+      const float all = xch[256 + r] + xch[384 + r];
+      if (fabsf(all - 1.0f) <= kWhole) rest = xch[r] + xch[128 + r];
+      return true;
     };
     int lim = s.nk;  // keys this row attends
     if (a.seq.causal) lim = clampi(tok + 1 + off, 0, s.nk);
@@ -610,9 +630,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    bool ok = exchange(0, part_d);
+    xch[128 * wg + r] = part_d;
+    bool ok = meet(0);
     const float nD = -(part_d + xch[128 * (wg ^ 1) + r]);
-    if (wg == 0 && split == 0 && there) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->x_full[warp & 3]);
+    if (wg == 0 && split + 1 == (unsigned)a.splits && there) {  // (the last range has a row's last key)
       st[r] = nlse;
       st[128 + r] = in ? nD : 0.0f;
     }
@@ -667,6 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             f32x2(p[c], p[c + 1]),
             add_f32x2(f32x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), d2));
         sum2 = add_f32x2(sum2, ds);
+        sump = add_f32x2(sump, f32x2(p[c], p[c + 1]));
         float y0, y1;
         split_f32x2(ds, y0, y1);
         pk[c / 2] = pack_bf16x2(y0, y1);
@@ -674,14 +698,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         x[c + 1] = __float_as_uint(y1);
       }
       if (all_steps == 1) {
-        // the row is here as a whole: take off what its dS, which add up to 0, come to
-        float lo, hi;
-        split_f32x2(sum2, lo, hi);
-        if (!exchange(1, lo + hi)) {
+        // the row is here as a whole
+        if (!find_rest()) {
           ok = false;
           break;
         }
-        const float rest = lo + hi + xch[256 + 128 * (wg ^ 1) + r];
 #pragma unroll
         for (int c = 0; c < 64; c += 2)
           pk[c / 2] = pack_bf16x2(fmaf(-p[c], rest, __uint_as_float(x[c])),
@@ -693,20 +714,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->ds_full[g & 1]);
     }
-    if (all_steps > 1 && steps > 0 && ok) {
-      float lo, hi;
-      split_f32x2(sum2, lo, hi);
-      ok = exchange(1, lo + hi);
-    }
-    // D for the dkv kernel: sum_j p_ij (dout_i . v_j), without the rounding of out
+    // D for the dkv kernel.  (Rows whose keys are cut into ranges keep the D that they have.)
+    const bool whole = steps > 0 && steps == all_steps;
+    if (whole && all_steps > 1 && ok) ok = find_rest();
+    if (whole && ok && wg == 0 && in) st[128 + r] = nD - rest;
     float* part = a.part + (long long)blockIdx.x * kPartFloats;
-    if (steps > 0 && ok && wg == 0 && in) {
-      const float rest = xch[256 + r] + xch[384 + r];
-      if (a.splits == 1)
-        st[128 + r] = nD - rest;
-      else
-        part[128 * 128 + r] = rest;
-    }
     if (steps > 0 && ok) ok = wait_warp(&ctl->acc_full, 0, w, 0x42);
     if (ok && there) {
       tc_fence_after();
@@ -844,14 +856,12 @@ __global__ void __launch_bounds__(256) prompt_dq_join_kernel(const Args a) {
             hp = (int)(item - (unsigned)rank * (unsigned)a.n_packs);
   const Place place = find_tile(a.seq, rank, 7 - a.pack, false);
   const Seq& s = place.s;
-  const int b = place.b, tile = place.tile;
-  const int tok0 = tile * T, tok = tok0 + (r & (T - 1)), head = (hp << a.pack) + (r >> (7 - a.pack));
+  const int tok0 = place.tile * T, tok = tok0 + (r & (T - 1)), head = (hp << a.pack) + (r >> (7 - a.pack));
   if (!place.there || tok >= (a.seq.packed ? s.nq : a.seq.Sq)) return;
   int keys = tok0 < s.nq ? s.nk : 0;
   if (a.seq.causal) keys = clampi((tok0 + T < s.nq ? tok0 + T : s.nq) + s.nk - s.nq, 0, keys);
   const int steps = (keys + 127) / 128;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float rest = 0.0f;
   for (int i = 0; i < a.splits && tok < s.nq; ++i) {
     if ((long long)steps * (i + 1) / a.splits == (long long)steps * i / a.splits) continue;
     const float* part = a.part + ((long long)item * a.splits + i) * kPartFloats;
@@ -860,14 +870,11 @@ __global__ void __launch_bounds__(256) prompt_dq_join_kernel(const Args a) {
     acc.y += x.y;
     acc.z += x.z;
     acc.w += x.w;
-    rest += part[128 * 128 + r];
   }
   reinterpret_cast<uint2*>(a.d0 + s.z * a.d0_b + head * a.d0_h +
                            (long long)(s.q0 + tok) * a.d0_t)[lane] =
       make_uint2(pack_bf16x2(acc.x * a.scale, acc.y * a.scale),
                  pack_bf16x2(acc.z * a.scale, acc.w * a.scale));
-  if (lane == 0 && tok < s.nq && steps > 0)
-    a.stats[((long long)hp * a.n_tslots + query_slot(a, b, s.q0, tile)) * 256 + 128 + r] -= rest;
 }
 
 }  // namespace dq

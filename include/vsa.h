@@ -572,7 +572,10 @@ VSA_API size_t vsa_fwd_prompt_workspace_bytes(int packed, int B, int Hq, int Hkv
  * that attend something, a NaN or infinity in q or dout reaches dk and dv of all keys of the key
  * tiles that their query tile walks over.
  *   q, k, v, q_seq, k_seq, sizes, causal, scale: as given to the forward; out, lse what it
- *           returned; dout as out.
+ *           returned; dout as out.  Where k and v are a part of the keys that a row attends (a
+ *           piece of a long past, or another rank's), out and lse are those over all parts,
+ *           joined: p and D are then the whole's, dk and dv the part's, and dq adds up over the
+ *           parts.
  *   strides int64 [24]: (batch, head, token) of q, k, v, out, dout, dq, dk, dv.
  *   workspace  vsa_bwd_prompt_workspace_bytes() bytes, 16-byte aligned, no initialisation
  *           needed; calls sharing it must not overlap on the GPU.

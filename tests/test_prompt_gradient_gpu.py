@@ -102,3 +102,49 @@ def test_rows_that_attend_nothing_reach_nothing(nq, nk, Hq, Hkv, bad):
     for name in want:
         assert torch.equal(got[name], want[name]), name
     assert (got["dq"][none] == 0).all()
+
+
+def near(got, want, what, tol=0.005):
+    """Off by `tol` of its norm at most, each head for itself.  Roundings to bf16 on the way to an
+    element -- its own, that of P or dS, that of out -- are each spread over half a step, 2^-8 of a
+    value at most and 2^-8 / sqrt(3) = 0.00226 in the mean square; three, independent, make
+    0.0039."""
+    err, size = (got.double() - want).norm(dim=(-2, -1)), want.norm(dim=(-2, -1))
+    assert (err <= tol * size).all(), (what, (err / size).max().item())
+
+
+@pytest.mark.parametrize("nq,cut,nk,Hq,Hkv,causal,less", [
+    (300, 100, 300, 4, 4, False, 0), (130, 700, 1000, 8, 2, False, 0), (257, 384, 641, 2, 2, True, 0),
+    (40, 2000, 2040, 4, 1, True, 0), (513, 64, 2500, 12, 2, False, 0), (100, 64, 192, 4, 4, False, 8),
+    (100, 64, 128, 4, 4, False, 11), (300, 64, 564, 4, 2, False, 8), (300, 64, 564, 4, 2, False, 20)],
+    ids=str)
+def test_keys_in_two_parts(nq, cut, nk, Hq, Hkv, causal, less):
+    """out and lse over all keys, the gradient over a part of them at a time, against 64 bits with
+    this out and lse: dk and dv are the parts', dq adds up.  (The later keys are the causal ones;
+    the earlier ones may weigh 2^-less of what they would.)"""
+    g = gen(62)
+    q, k, v, dout = (randn((1, h, n, D), g)
+                     for n, h in ((nq, Hq), (nk, Hkv), (nk, Hkv), (nq, Hq)))
+    if less:
+        q[..., 0], k[..., 0] = 4.0, 0.0
+        k[:, :, :cut, 0] = -less * math.log(2.0) * math.sqrt(D) / 4.0
+    out, lse = binding.vsa_fwd_prompt(q, k, v, causal=causal)
+    parts = [binding.vsa_bwd_prompt(q, k[:, :, a:b], v[:, :, a:b], out, dout, lse, causal=c)
+             for a, b, c in ((0, cut, False), (cut, nk, causal))]
+    ok()
+    scale, G = 1.0 / math.sqrt(D), Hq // Hkv
+    x, y, z, d, o = (t[0].double() for t in (q, k, v, dout, out))
+    y, z = y.repeat_interleave(G, 0), z.repeat_interleave(G, 0)
+    s = x @ y.transpose(1, 2) * scale
+    if causal:
+        s = s.masked_fill(torch.ones(nq, nk, dtype=torch.bool, device=DEV).triu(nk - nq + 1),
+                          -math.inf)
+    p = torch.exp(s - lse[0].double()[..., None] * math.log(2.0))
+    ds = p * (d @ z.transpose(1, 2) - (d * o).sum(-1, keepdim=True))
+    dk = (scale * ds.transpose(1, 2) @ x).unflatten(0, (Hkv, G)).sum(1)
+    dv = (p.transpose(1, 2) @ d).unflatten(0, (Hkv, G)).sum(1)
+    for (a, b), (dq_p, dk_p, dv_p) in zip(((0, cut), (cut, nk)), parts):
+        near(dq_p[0], scale * ds[:, :, a:b] @ y[:, a:b], "dq")
+        near(dk_p[0], dk[:, a:b], "dk")
+        near(dv_p[0], dv[:, a:b], "dv")
+    near(parts[0][0][0].double() + parts[1][0][0].double(), scale * ds @ y, "dq of both", 0.0071)
