@@ -863,7 +863,9 @@ def vsa_pages_free(pool, table, lens=None, block=64, stream=None):
 def vsa_pages_reserve(pool, table, lens, n_new=None, block=64, stream=None):
     """Map pages for the tokens lens[b] .. lens[b] + n_new[b] - 1 (n_new int32 [B]; None: one
     token each) wherever table (int32 [B,Hkv,max_blocks], changed in place) names none.  Returns
-    lacking int32 [B], the pages that the pool did not have."""
+    lacking int32 [B]: the pages that the pool did not have, and the next token's where other
+    entries name it too, which a write must not touch (lens has been set back into a block that a
+    fork shares: fork the sequence and go on with the fork)."""
     if stream is None:
         r = _short("vsa_pages_reserve", "pages_reserve", pool, table, lens, n_new, block)
         if r is not None:

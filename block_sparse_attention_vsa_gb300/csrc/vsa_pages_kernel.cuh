@@ -278,6 +278,9 @@ __device__ __forceinline__ int cluster_before(PagesShared& s, int asked, int* al
 // The rows are divided among the cluster's warps in order.  A warp looks up 32 rows' ranges at a
 // time, a lane each; short ranges (a token each) stay with the lane, of long ones (a prompt) the
 // warp takes one after another, several entries a lane under way.
+// The block that the next token falls in may be there already, and shared, where a sequence's length
+// has been set back: it is not to be written, and counts as lacking.  (It is looked up beside what
+// is needed anyway, and nothing waits for it before the end.)
 __global__ void __launch_bounds__(kPagesThreads) pages_reserve_kernel(const ReserveArgs a) {
   __shared__ PagesShared s;
   __shared__ uint16_t s_list[kPagesThreads / 32][32 * kWindowWords];
@@ -298,9 +301,10 @@ __global__ void __launch_bounds__(kPagesThreads) pages_reserve_kernel(const Rese
   struct Range {
     int first, last, b;  // blocks [first, last) of the part hold tokens to come
     int32_t* row;
+    bool next;           // the first of them is the next token's
   };
   auto range = [&](unsigned part) {
-    Range x{0, 0, 0, a.table};
+    Range x{0, 0, 0, a.table, false};
     if (part >= r1) return x;
     const unsigned row = part / parts;
     x.b = (int)(row / heads);
@@ -313,11 +317,13 @@ __global__ void __launch_bounds__(kPagesThreads) pages_reserve_kernel(const Rese
     x.first = (int)(len >> shift) < a.max_blocks ? (int)(len >> shift) : a.max_blocks;
     const long long end = (len + (more > 0 ? more : 0) + a.block - 1) >> shift;
     x.last = end < a.max_blocks ? (int)end : a.max_blocks;
+    const int next = x.first;
     if (parts > 1) {
       const unsigned n = x.last - x.first, q = part - row * parts;
       x.last = x.first + (int)((unsigned long long)n * (q + 1) / parts);
       x.first += (int)((unsigned long long)n * q / parts);
     }
+    x.next = x.first == next && x.first < x.last;
     return x;
   };
   auto of_lane = [&](const Range& x, int k) {
@@ -325,6 +331,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_reserve_kernel(const Rese
     y.first = __shfl_sync(0xffffffffu, x.first, k);
     y.last = __shfl_sync(0xffffffffu, x.last, k);
     y.b = __shfl_sync(0xffffffffu, x.b, k);
+    y.next = false;
     y.row = reinterpret_cast<int32_t*>(
         __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x.row), k));
     return y;
@@ -354,10 +361,12 @@ __global__ void __launch_bounds__(kPagesThreads) pages_reserve_kernel(const Rese
     return mask;
   };
   int asked = 0;
-  Range x{0, 0, 0, a.table};
+  int next = -1, named = 0;  // the page of the lane's next token, and the entries that name it
+  Range x{0, 0, 0, a.table, false};
   uint32_t mask = 0;
   for (unsigned rb = r0; rb < r1; rb += 32) {
     x = range(rb + lane);
+    if (x.next) next = read_global(x.row + x.first);
     if (__all_sync(0xffffffffu, x.last - x.first <= kFew)) {
       mask = few(x);
       asked += (int)__reduce_add_sync(0xffffffffu, (unsigned)__popc(mask));
@@ -374,6 +383,7 @@ __global__ void __launch_bounds__(kPagesThreads) pages_reserve_kernel(const Rese
     }
   }
   const FreeCount f = count_free(a.pool, s.before, s.warp);
+  if (is_page(next, a.pool.pages)) named = read_global(a.pool.refs + next);
   int in_cta, all;
   int at = block_before(lane == 0 ? asked : 0, s.warp, &in_cta);
   at = __shfl_sync(0xffffffffu, at, 0);
@@ -429,6 +439,15 @@ __global__ void __launch_bounds__(kPagesThreads) pages_reserve_kernel(const Rese
         }
       }
     }
+  }
+  const bool again = r1 - r0 > 32;  // more rows than lanes: looked up now
+  for (unsigned rb = r0; rb < r1; rb += 32) {
+    if (again) {
+      x = range(rb + lane);
+      next = x.next ? read_global(x.row + x.first) : -1;
+      named = is_page(next, a.pool.pages) ? read_global(a.pool.refs + next) : 0;
+    }
+    if (named > 1) atomicAdd(a.lacking + x.b, 1);
   }
   if (ctas > 1)
     cluster.sync();

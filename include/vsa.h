@@ -456,9 +456,15 @@ VSA_API vsa_status vsa_cache_evict(const float *weight, const int32_t *table,
  * free_bits [ceil(pages / 32)] uint32, bit p % 32 of word p / 32 set where refs[p] is 0 (bits
  * past the pool are ignored).  An empty pool has refs 0 and all bits set.  Pages are taken
  * lowest first, in the order of the entries (b, h, j) that ask for them, so every outcome is
- * unique.  Calls on one pool must not overlap on the GPU.  A page that several sequences name
- * is one that none of them writes: vsa_cache_fork shares full blocks only, and a write goes
- * behind those.  B * Hkv, B * Hkv * max_blocks (and those of N) < 2^31.
+ * unique.  Calls on one pool must not overlap on the GPU.  B * Hkv, B * Hkv * max_blocks (and
+ * those of N) < 2^31.
+ *
+ * Shared pages.  A page that several entries name is not to be written.  vsa_cache_fork shares
+ * full blocks only, and a write goes behind those, so none is as long as lens only grows.  Where
+ * lens is set back, what lies behind it is let go first (vsa_pages_free with lens).  It may then
+ * still end inside a block that others share (drafts rejected that were there when the sequence
+ * was forked): vsa_pages_reserve counts that block as lacking.  Fork the sequence, whose
+ * part-full block is copied then, and go on with the fork in its place.
  * ------------------------------------------------------------------------------------- */
 
 /* Lets pages go: every entry of table [B, Hkv, max_blocks] from block ceil(lens[b] / block) on
@@ -473,8 +479,10 @@ VSA_API vsa_status vsa_pages_free(int32_t *table, const int32_t *lens, int B, in
 
 /* Maps pages ahead of a write: blocks lens[b] / block .. ceil((lens[b] + n_new[b]) / block) - 1
  * (n_new NULL: one token each; at most max_blocks) that have no page in the table get one.
- *   lacking [B] output: the pages that the pool could not give sequence b, all its heads
- *           together; their entries are -1 (a write drops those tokens).
+ *   lacking [B] output: what sequence b lacks for its tokens to come, all its heads together:
+ *           pages that the pool could not give (their entries are -1, and a write drops those
+ *           tokens), and the next token's block where other entries name its page too (it
+ *           stays as it is; a write would change it for the others).
  * One kernel. */
 VSA_API vsa_status vsa_pages_reserve(int32_t *table, const int32_t *lens, const int32_t *n_new,
                                      int B, int Hkv, int max_blocks, int block, int pages,
