@@ -920,7 +920,8 @@ def vsa_cache_fork(cache, pool, table, lens, parent, table_out=None, stream=None
 def vsa_cache_compact(cache, pool, table, stream=None):
     """Close the pool up: the pages in use become its first ones, and table (int32
     [B,Hkv,max_blocks]) follows.  Returns (to int32 [pages], where each page in use is now, -1
-    for free ones; n_used int32 [1])."""
+    for free ones; n_used int32 [1]).  Other tables on the pool follow by to[entry] where an entry
+    is a page: torch.where(t >= 0, to[t.clamp(min=0)], t)."""
     if stream is None:
         r = _short("vsa_cache_compact", "cache_compact", cache, pool, table)
         if r is not None:

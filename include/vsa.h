@@ -508,7 +508,7 @@ VSA_API vsa_status vsa_cache_fork(const int32_t *table, const int32_t *lens, con
 /* Closes a pool up: with U pages in use, those from U on move to the free ones below U, in
  * order, whole (codes, scales, mean, count), and the table's entries follow.
  *   to     [pages] output: where each page in use is now, -1 for free ones; entries of other
- *          tables on the pool are to be replaced by to[entry].
+ *          tables on the pool are to be replaced by to[entry] where they name a page (>= 0).
  *   n_used [1] output: U.  Pages from U on are free: the pool can be cut, or saved, there.
  * k_mean may be NULL.  Two kernels. */
 VSA_API vsa_status vsa_cache_compact(int32_t *table, int B, int Hkv, int D, int max_blocks,

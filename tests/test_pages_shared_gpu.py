@@ -138,3 +138,30 @@ def test_shared_pages_in_front_are_nobodys_matter():
         binding.vsa_pages_free(pool, kids.table)
     binding.vsa_pages_free(pool, table)
     same_pool(pool, [0] * 64)
+
+
+def test_other_tables_follow_when_a_pool_is_closed_up():
+    """Two tables on one pool, one given to the call, the other by `to`; -1 stays -1 although the
+    pool's last page is in use."""
+    kv, pool = binding.new_cache8(20), binding.new_pages(20)
+    tables = [torch.full((2, 2, 3), -1, dtype=torch.int32, device=DEV) for _ in range(2)]
+    gone = torch.full((1, 2, 3), -1, dtype=torch.int32, device=DEV)
+    for t, n in ((tables[0], [128, 64]), (gone, [150]), (tables[1], [64, 190])):
+        assert (binding.vsa_pages_reserve(pool, t, i32([0] * len(n)), i32(n)) == 0).all()
+    assert tables[1].max().item() == 19 and (tables[1] == -1).any()
+    for t in tables:
+        for b in range(2):
+            for page in t[b][t[b] >= 0].tolist():
+                kv.k[page].view(torch.uint8).fill_(page)
+    was = [t.clone() for t in tables]
+    binding.vsa_pages_free(pool, gone)
+    to, n_used = binding.vsa_cache_compact(kv, pool, tables[0])
+    t = tables[1]
+    tables[1] = torch.where(t >= 0, to[t.clamp(min=0)], t)
+    assert n_used.item() == 14
+    for t, w in zip(tables, was):
+        assert torch.equal(t >= 0, w >= 0) and t.max().item() < 14
+        for page, before in zip(t[t >= 0].tolist(), w[w >= 0].tolist()):
+            assert (kv.k[page].view(torch.uint8) == before).all()
+    named = torch.cat([t[t >= 0] for t in tables])
+    assert torch.equal(torch.bincount(named.long(), minlength=20).int(), pool.refs)
