@@ -7,6 +7,7 @@ import torch
 
 import prompt_ref as ref
 from block_sparse_attention_vsa_gb300 import binding
+from prompt_norm import NORM, off
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -104,13 +105,8 @@ def test_rows_that_attend_nothing_reach_nothing(nq, nk, Hq, Hkv, bad):
     assert (got["dq"][none] == 0).all()
 
 
-def near(got, want, what, tol=0.005):
-    """Off by `tol` of its norm at most, each head for itself.  Roundings to bf16 on the way to an
-    element -- its own, that of P or dS, that of out -- are each spread over half a step, 2^-8 of a
-    value at most and 2^-8 / sqrt(3) = 0.00226 in the mean square; three, independent, make
-    0.0039."""
-    err, size = (got.double() - want).norm(dim=(-2, -1)), want.norm(dim=(-2, -1))
-    assert (err <= tol * size).all(), (what, (err / size).max().item())
+def near(got, want, what, tol=NORM):
+    assert off(got, want) <= tol, (what, off(got, want))
 
 
 @pytest.mark.parametrize("nq,cut,nk,Hq,Hkv,causal,less", [
@@ -147,4 +143,111 @@ def test_keys_in_two_parts(nq, cut, nk, Hq, Hkv, causal, less):
         near(dq_p[0], scale * ds[:, :, a:b] @ y[:, a:b], "dq")
         near(dk_p[0], dk[:, a:b], "dk")
         near(dv_p[0], dv[:, a:b], "dv")
-    near(parts[0][0][0].double() + parts[1][0][0].double(), scale * ds @ y, "dq of both", 0.0071)
+    near(parts[0][0][0].double() + parts[1][0][0].double(), scale * ds @ y, "dq of both",
+         math.sqrt(2) * NORM)
+
+
+def plain(q, k, v, dout, nq, nk, causal):
+    """The 64-bit values of out, dq, dk, dv for packed sequences, [heads, tokens, 128], a sequence
+    and head at a time."""
+    r = {n: torch.zeros(x.shape, dtype=torch.float64, device=DEV)
+         for n, x in (("out", q), ("dq", q), ("dk", k), ("dv", v))}
+    G, scale, aq, ak = q.shape[0] // k.shape[0], 1.0 / math.sqrt(D), 0, 0
+    for n, m in zip(nq, nk):
+        for h in range(q.shape[0]):
+            rq, rk = (h, slice(aq, aq + n)), (h // G, slice(ak, ak + m))
+            x, y, z, d = q[rq].double(), k[rk].double(), v[rk].double(), dout[rq].double()
+            p = x @ y.T * scale
+            if causal:
+                p.masked_fill_(torch.ones(n, m, dtype=torch.bool, device=DEV).triu(m - n + 1), -math.inf)
+            p = torch.softmax(p, 1).nan_to_num_(0.0)  # (rows that attend nothing)
+            r["out"][rq] = out = p @ z
+            r["dv"][rk] += p.T @ d
+            ds = d @ z.T
+            ds -= (d * out).sum(1, keepdim=True)
+            ds *= p
+            r["dq"][rq] = scale * ds @ y
+            r["dk"][rk] += scale * ds.T @ x
+        aq, ak = aq + n, ak + m
+    return r
+
+
+NORMS = [  # queries, keys of packed sequences, heads, causal
+    ([300, 33, 411], [300, 33, 411], 12, 12, True), ([70], [700], 4, 2, False),
+    ([513], [513], 1, 1, False), ([200, 130], [103, 129], 4, 2, True), ([128], [128], 2, 1, True),
+    # keys, or steps, cut into ranges
+    ([70], [2500], 4, 4, False), ([300, 41], [300, 41], 24, 1, True), ([600], [600], 8, 1, True),
+    ([500, 2], [2100, 700], 16, 1, True), ([1100], [90], 6, 1, False), ([3], [2500], 2, 1, True),
+    # long walks: rings that go round many times, masks in the last tiles
+    ([5000, 3001], [5000, 3001], 2, 1, True), ([4100], [4100], 2, 2, False), ([600], [6001], 3, 1, True),
+    ([8192], [8192], 12, 2, True), ([2048], [2048], 12, 12, True),
+    # more tiles than SMs, longest first and as they come
+    ([700, 1300, 60, 900], [700, 1300, 60, 900], 32, 8, True), ([257] * 40, [257] * 40, 6, 6, True)]
+
+
+@pytest.mark.parametrize("nq,nk,Hq,Hkv,causal", NORMS, ids=str)
+def test_errors_in_norm(nq, nk, Hq, Hkv, causal):
+    g = gen(sum(nq) + Hq)
+    aq, ak = [0], [0]
+    for x, y in zip(nq, nk):
+        aq.append(aq[-1] + x)
+        ak.append(ak[-1] + y)
+    q, k, v, dout = (randn((n, h, D), g)
+                     for n, h in ((aq[-1], Hq), (ak[-1], Hkv), (ak[-1], Hkv), (aq[-1], Hq)))
+    out, lse = binding.vsa_fwd_prompt(q, k, v, i32(aq), i32(ak), causal=causal)
+    grads = binding.vsa_bwd_prompt(q, k, v, out, dout, lse, i32(aq), i32(ak), causal=causal)
+    ok()
+    want = plain(*(x.transpose(0, 1) for x in (q, k, v, dout)), nq, nk, causal)
+    for n, x in zip(("out", "dq", "dk", "dv"), (out, *grads)):
+        near(x.transpose(0, 1), want[n], n)
+
+
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+def test_differences_along_the_gradient(causal):
+    """Along the gradient itself the slope of sum(out * dout) is the gradient's norm: central
+    differences in 64 bits, which a gradient of another size, sign or direction does not meet."""
+    g = gen(63)
+    n = 180
+    q, k, v, dout = (randn((1, 2, n, D), g) for _ in range(4))
+    out, lse = binding.vsa_fwd_prompt(q, k, v, causal=causal)
+    grads = binding.vsa_bwd_prompt(q, k, v, out, dout, lse, causal=causal)
+    ok()
+    x, h = [t[0].double() for t in (q, k, v)], 1e-4
+    for i in range(3):
+        got = grads[i][0].double()
+        d = got / got.norm()
+
+        def f(t):
+            y = [a + t * d if j == i else a for j, a in enumerate(x)]
+            s = y[0] @ y[1].transpose(1, 2) / math.sqrt(D)
+            if causal:
+                s = s.masked_fill(torch.ones(n, n, dtype=torch.bool, device=DEV).triu(1), -math.inf)
+            return ((torch.softmax(s, -1) @ y[2]) * dout[0].double()).sum().item()
+
+        slope = (f(h) - f(-h)) / (2 * h)
+        # (got - true) . d is at most NORM of the norm; the differences are off by h^2 / 6 of a
+        # third derivative, 1e-8 here
+        assert slope > 1.0 and abs(got.norm().item() - slope) <= (NORM + 1e-6) * slope, i
+
+
+def test_calls_on_another_stream_do_not_wait():
+    """The current stream is held up long behind what the calls take; they end before it does."""
+    g = gen(64)
+    q, k, v, dout = (randn((500, h, D), g) for h in (4, 2, 2, 4))
+    seq = i32([0, 333, 500])
+    out, lse = binding.vsa_fwd_prompt(q, k, v, seq)
+    want = (out, lse, *binding.vsa_bwd_prompt(q, k, v, out, dout, lse, seq))
+    side = torch.cuda.Stream()
+    ok()
+    busy = torch.ones(8192, 8192, device=DEV, dtype=torch.bfloat16)
+    for _ in range(200):  # about 0.1 s
+        busy = busy @ busy
+    last = torch.cuda.Event()
+    last.record()
+    out, lse = binding.vsa_fwd_prompt(q, k, v, seq, stream=side)
+    grads = binding.vsa_bwd_prompt(q, k, v, out, dout, lse, seq, stream=side)
+    side.synchronize()
+    assert not last.query()
+    for x, y in zip(want, (out, lse, *grads)):
+        assert torch.equal(x, y)
+    ok()
