@@ -74,7 +74,6 @@ struct Args {
   long long o_b, o_h, o_t, g_b, g_h, g_t;
   unsigned int* status;
   int Hq, Hkv, group, pack, n_packs, n_tslots;  // query tiles of 128 >> pack tokens
-  int n_kslots;                                 // key tiles of 128 tokens
   float scale, scale_log2;
   unsigned long long wait_ns;
   int stall;

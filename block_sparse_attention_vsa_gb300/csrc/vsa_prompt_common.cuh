@@ -95,9 +95,10 @@ __device__ __forceinline__ int find_slot(const int32_t* seq, int B, int S, int T
 // sequences by what their tiles walk over (queries' tiles over keys, keys' over queries), longest
 // first, and inside one the last query tiles, which causal masks leave the most keys, or the first
 // key tiles, which they leave the most queries.  With more than 32 sequences, or CTAs for all tiles
-// at once, sequences come as they are: the order takes 4 prompts of up to 2,000 tokens behind 4,001
-// to 16,411 held from 1,845 us to 1,652 and a training step on 3 clips from 1,035 to 990, but 88
-// short items, which start together, from 10.1 to 11.2.
+// at once, sequences come as they are: in a tight loop the order takes 4 prompts of up to 2,000
+// tokens behind 4,001 to 16,411 held from 1,845 us to 1,652 and a training step on 3 clips from
+// 1,035 to 990 (1,780 and 1,041 as a program calls them, a pass among others), but 88 short items,
+// which start together, from 10.1 to 11.2.
 struct Place {
   Seq s;
   int b, tile;

@@ -517,7 +517,9 @@ __device__ __forceinline__ void softmax_role(const FwdArgs& a, uint8_t* smem, Ct
       a.lse[((long long)it.z * a.Hq + head) * a.seq.Sq + it.q0 + tok] =
           some ? (l > 0.0f ? m + log2f(l) : __int_as_float(0x7fffffff)) : kLseEmpty;
     // 32 columns at a time through shared memory, so that a warp's store is 8 rows of 64 bytes,
-    // not 32 of 16 (which took 6,000 cycles an item)
+    // not 32 of 16 (which took 6,000 cycles an item).  (What store_columns does, written out: with
+    // that in its place 4 prompts of up to 157 tokens take 10.4 us for 10.0, 19 heads of 8,192 390.5
+    // for 389.2.)
     uint8_t* stage = smem + kOffOut + (threadIdx.x >> 5) * 2048;
     const uint32_t lane = lane_id();
     const int r0 = (int)(threadIdx.x & 96);  // the warp's first row of the tile
