@@ -319,7 +319,9 @@ vsa_status vsa_fwd_prompt(const vsa_bf16* q, const vsa_bf16* k, const vsa_bf16* 
     a.part = static_cast<float*>(workspace);
   }
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.wait_ns = host_wait_ns(prompt::kWaitLimitNs);
+  // The softmax warps of a query tile without queries wait while its item's other tile walks over
+  // the keys, 1.7 us per 128: a second more for every 2^25 of them (0.45 s).
+  a.wait_ns = host_wait_ns(prompt::kWaitLimitNs * (1 + (Sk >> 25)));
   a.stall = host_stall();
 
   a.seq.sort = sorted(B, (long long)a.n_items * a.splits);

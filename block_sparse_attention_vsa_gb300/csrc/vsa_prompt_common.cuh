@@ -24,7 +24,7 @@
 namespace vsa {
 namespace prompt {
 
-constexpr uint64_t kWaitLimitNs = 1000000000ull;  // one second per wait
+constexpr uint64_t kWaitLimitNs = 1000000000ull;  // one second per wait (for up to 2^25 keys)
 constexpr unsigned kErrTimeout = 0x100u;          // | code of the wait that gave up
 constexpr uint32_t kSleepNs = 20000;              // a waiting thread looks up this often
 constexpr uint32_t kTile = 128 * 128 * 2;         // 128 rows of Q, K, V or dO

@@ -615,7 +615,7 @@ VSA_API int vsa_last_launch_count(void);
  *   vsa_set_wait_limit_ns(ns): the limit of every internal wait that is not a drain
  *     (a drain waits for the kernel's own copies and MMAs in flight and always keeps the
  *     full limit of about one second, so nothing is in flight when a CTA exits).
- *     0 restores the full limit.  A short limit makes waits run out on ordinary work.
+ *     0 restores the full limit (vsa_fwd_prompt: a second more for every 2^25 keys).  A short limit makes waits run out on ordinary work.
  *   vsa_set_stall_test(enable): while nonzero, the MMA warp of every CTA first waits on
  *     a barrier that nothing ever completes; that wait runs out after the limit above,
  *     records its code in the device status word (forward 0x11f, backward 0x15f), and
