@@ -545,6 +545,11 @@ VSA_API vsa_status vsa_cache_compact(int32_t *table, int B, int Hkv, int D, int 
  * tensors, with a stride of 0, are refused: copy them first.)
  * Sizes.  Sq, Sk <= 2^31 - 1025; B * Hq, and the rows of all heads of a tensor, <= 2^40, and
  * fewer than 2^31 tiles of 128 rows; more is refused.
+ * Long sums.  Products add up in fp32 in the tensor core, which drops of a term what lies some
+ * 2^25 below the sum.  Where all keys of a walk weigh alike, what their v have in common comes out
+ * too small by about 2^-28 of itself a key: 0.04 % at 2^18 keys, 0.4 % at 2^20, 1.1 % at 2^21, 10 %
+ * at 2^24 (a rounding of out is 0.2 %).  The same holds for dv over the queries, of all heads of a
+ * group, that attend a key.  Keys and queries that are cut into ranges count by the range.
  * ------------------------------------------------------------------------------------- */
 
 /* Forward.
@@ -615,7 +620,8 @@ VSA_API int vsa_last_launch_count(void);
  *   vsa_set_wait_limit_ns(ns): the limit of every internal wait that is not a drain
  *     (a drain waits for the kernel's own copies and MMAs in flight and always keeps the
  *     full limit of about one second, so nothing is in flight when a CTA exits).
- *     0 restores the full limit (vsa_fwd_prompt: a second more for every 2^25 keys).  A short limit makes waits run out on ordinary work.
+ *     0 restores the full limit (vsa_fwd_prompt: a second more for every 2^25 keys).  A short
+ *     limit makes waits run out on ordinary work.
  *   vsa_set_stall_test(enable): while nonzero, the MMA warp of every CTA first waits on
  *     a barrier that nothing ever completes; that wait runs out after the limit above,
  *     records its code in the device status word (forward 0x11f, backward 0x15f), and
