@@ -38,8 +38,8 @@
 //        overwrites dS_g: MMAs of one warp run in order.
 //   dq   warp 9 S_{g+1}, dP_{g+1} (two buffers of dP / dS; the one that dQ_{g-1} read), warp 10
 //        dQ_g.
-// With 19 heads of 8,192 tokens the tensor pipe is busy 72 % (dkv) and 70 % (dq) of the time at
-// 1.9 GHz, 1,690 TFLOP/s of their own products; what is left are the round trips through
+// With 19 heads of 8,192 tokens the tensor pipe is busy 73 % (dkv) and 70 % (dq) of the time at
+// 1.9 GHz, 1,720 and 1,625 TFLOP/s of their own products; what is left are the round trips through
 // barriers and TMEM of a step's chain, and 4 us a CTA of start and end.
 //
 // Where there are fewer tiles than SMs the steps of each are cut into ranges, a CTA each, and a
